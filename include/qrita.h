@@ -266,6 +266,159 @@ int qrita_candidates(const void* logits, int dtype, int64_t B, int64_t V, const 
                      qrita_stream_t stream);
 
 /*
+ * Losses over rows of logits, with their gradients. The candidate set and the
+ * drawn token are what reinforcement learning consumes (Qrita technical
+ * summary, "Problem statement"); these entry points score given tokens under
+ * the same logits (and, where a mask is given, over the same kept set).
+ *
+ * Row contract of the four entry points. Row r has logits x[0..V) at
+ * logits + r * ld, a token t = tokens[r], and a kept set K: the ids whose
+ * mask byte is not 0, or all of [0, V) when mask is NULL. With
+ * y_j = x_j * inv_temperature,
+ *   p_j  = exp(y_j) / sum over K of exp(y_i)  (0 outside K),
+ *   logp = log p_t,   H = - sum over K of p_j log p_j.
+ *  - t outside [0, V): the row is ignored. Its logp and H are 0, it has no
+ *    loss, its gradient is 0, and its logits are not read.
+ *  - p_t = 0 (t outside K, a logit of -inf, or K empty): logp is -inf, and the
+ *    row joins neither a loss nor a gradient of logp (H is that of K; 0 when
+ *    K is empty or holds only -inf).
+ *  - NaN or +inf in K: that row's values and its gradient in K are NaN (a
+ *    gradient of 0 where its incoming gradient is 0).
+ * Logits outside K are never used, whatever they hold; their gradient is 0.
+ *
+ * logits and out_grad have leading dimensions ld, ld_grad >= V (elements); the
+ * columns from V on are neither read nor written. out_grad has the logits'
+ * type; every gradient is computed in fp32 and rounded once. It may be the
+ * logits' own buffer (the same pointer and leading dimension: the logits are
+ * then lost); any other overlap of the two is QRITA_EINVAL. Everything else
+ * is fp32, from fp32 exponentials with sums in fp32 over at most a few
+ * thousand terms each and in fp64 beyond. Results do not depend on timing:
+ * the same call gives the same bits.
+ *
+ * Common arguments (device pointers unless said otherwise):
+ *   logits, dtype, B, V   as qrita_select; B <= 2^31-1.
+ *   ld                    leading dimension of logits, >= V.
+ *   mask                  uint8[B, V] (leading dimension V) or NULL.
+ *   tokens                int32[B].
+ *   inv_temperature       finite, > 0 (by value).
+ * Ownership, streams and errors as qrita_select; QRITA_EINVAL also for a
+ * leading dimension below V, a scalar outside its stated range, or a missing
+ * pointer that is not said to be optional. Nothing is allocated or kept.
+ */
+
+/*
+ * qrita_token_logprobs: logp (and H) of one given token per row: what a
+ * rollout stores beside its draw, and what rescoring compares.
+ *
+ *   out_logp     float[B].
+ *   out_entropy  float[B] or NULL.
+ *
+ * One kernel on stream. B == 0 launches nothing.
+ */
+int qrita_token_logprobs(const void* logits, int dtype, int64_t B, int64_t V, int64_t ld, const uint8_t* mask,
+                         const int32_t* tokens, double inv_temperature, float* out_logp, float* out_entropy,
+                         qrita_stream_t stream);
+
+/*
+ * qrita_token_logprobs_grad: its gradient,
+ *   out_grad[r, j] = grad_logp[r] d logp_r / d x_j + grad_entropy[r] d H_r / d x_j,
+ *   d logp / d x_j = inv_temperature ([j = t] - p_j),
+ *   d H / d x_j    = - inv_temperature p_j (log p_j + H).
+ *
+ *   grad_logp, grad_entropy  float[B] or NULL (not both NULL). A row whose
+ *                            given gradients are all 0 gets a gradient of 0.
+ *   out_grad                 dtype[B, V], leading dimension ld_grad.
+ *
+ * One kernel on stream. B == 0 launches nothing.
+ */
+int qrita_token_logprobs_grad(const void* logits, int dtype, int64_t B, int64_t V, int64_t ld, const uint8_t* mask,
+                              const int32_t* tokens, double inv_temperature, const float* grad_logp,
+                              const float* grad_entropy, void* out_grad, int64_t ld_grad, qrita_stream_t stream);
+
+/*
+ * qrita_policy_loss: the clipped policy loss with a KL term, and its gradient
+ * with respect to the logits, in one call. Per row, with
+ * rho = exp(logp - old_logp) and q = ref_logp - logp:
+ *   row = max(-A rho, -A clip(rho, 1 - clip_low, 1 + clip_high))
+ *         + kl_coef (exp(q) - q - 1) - entropy_coef H,
+ *   loss = sum over rows of weights[r] row_r.
+ * The first term has no gradient where the clip binds (A > 0 and
+ * rho > 1 + clip_high, or A < 0 and rho < 1 - clip_low), and
+ * d rho / d logp = rho elsewhere.
+ *
+ *   old_logp      float[B] or NULL: NULL takes logp itself as a constant
+ *                 (rho = 1, and its gradient that of logp).
+ *   ref_logp      float[B] or NULL: NULL leaves the KL term out (kl is 0).
+ *   advantages    float[B].
+ *   weights       float[B] or NULL: NULL weighs every row 1 / B.
+ *   clip_low      in [0, 1];  clip_high >= 0 (infinity: no upper clip).
+ *   kl_coef       finite, >= 0;  entropy_coef finite.
+ *   grad_loss     float[1] or NULL: the gradient of the loss itself (NULL: 1),
+ *                 which multiplies out_grad and nothing else.
+ *   out_loss      float[1].
+ *   out_row_loss  float[B]: row, before its weight.
+ *   out_logp      float[B] or NULL;  out_kl float[B] or NULL: exp(q) - q - 1;
+ *   out_entropy   float[B] or NULL.
+ *   out_grad      dtype[B, V] with leading dimension ld_grad, or NULL: the
+ *                 loss alone.
+ *
+ * Two kernels on stream. B == 0 writes a loss of 0.
+ */
+int qrita_policy_loss(const void* logits, int dtype, int64_t B, int64_t V, int64_t ld, const uint8_t* mask,
+                      const int32_t* tokens, double inv_temperature, const float* old_logp, const float* ref_logp,
+                      const float* advantages, const float* weights, double clip_low, double clip_high, double kl_coef,
+                      double entropy_coef, const float* grad_loss, float* out_loss, float* out_row_loss,
+                      float* out_logp, float* out_kl, float* out_entropy, void* out_grad, int64_t ld_grad,
+                      qrita_stream_t stream);
+
+/*
+ * qrita_preference_workspace_bytes: device bytes of workspace
+ * qrita_preference_loss needs for B rows and P pairs (a multiple of 256; the
+ * workspace starts on a 16-byte boundary). 0 for invalid sizes.
+ */
+size_t qrita_preference_workspace_bytes(int64_t B, int64_t P);
+
+/*
+ * qrita_preference_loss: the preference loss on paired log ratios, and its
+ * gradient with respect to the logits. Sequence s owns the rows
+ * [starts[s], starts[s+1]); sequence 2i is the preferred one of pair i and
+ * 2i + 1 the rejected one. With L_s the sum of its rows' logp (length_norm:
+ * their mean), over the rows that are not ignored and whose logp is above
+ * -inf (L_s = 0 when there is none):
+ *   ratio_i = (L_2i - ref_2i) - (L_2i+1 - ref_2i+1),
+ *   z_i     = beta ratio_i - margin,
+ *   pair_i  = - (1 - label_smoothing) log sigmoid(z_i) - label_smoothing log sigmoid(-z_i),
+ *   loss    = sum over pairs of weights[i] pair_i.
+ *
+ *   starts        int32[2 P + 1], not decreasing, within [0, B]. Other values
+ *                 touch nothing outside the arguments, but the results are
+ *                 then unspecified.
+ *   P             pairs, >= 0, 2 P + 1 <= 2^31-1. P == 0 writes a loss of 0.
+ *   ref_logp      float[2 P] or NULL (0): the reference's L_s.
+ *   weights       float[P] or NULL: NULL weighs every pair 1 / P.
+ *   beta          finite, > 0;  label_smoothing in [0, 1];  margin finite.
+ *   length_norm   0 or 1.
+ *   grad_loss     as qrita_policy_loss.
+ *   out_loss      float[1];  out_pair_loss float[P].
+ *   out_log_ratio float[P];  out_seq_logp float[2 P]: L_s.
+ *   out_logp      float[B] or NULL (rows of no sequence: 0).
+ *   out_grad      dtype[B, V] with leading dimension ld_grad, or NULL. Rows of
+ *                 no sequence get 0.
+ *   workspace     device buffer of at least qrita_preference_workspace_bytes,
+ *                 16-byte aligned, owned by the caller and written by the
+ *                 call; calls that may run at the same time (two captured
+ *                 graphs among them) need one each.
+ *
+ * A few kernels on stream.
+ */
+int qrita_preference_loss(const void* logits, int dtype, int64_t B, int64_t V, int64_t ld, const int32_t* tokens,
+                          double inv_temperature, const int32_t* starts, int64_t P, const float* ref_logp,
+                          const float* weights, double beta, double label_smoothing, double margin, int length_norm,
+                          const float* grad_loss, float* out_loss, float* out_pair_loss, float* out_log_ratio,
+                          float* out_seq_logp, float* out_logp, void* out_grad, int64_t ld_grad, void* workspace,
+                          size_t workspace_bytes, qrita_stream_t stream);
+
+/*
  * qrita_delta_table: copy one of the host-built truncation tables the kernel
  * receives (Qrita technical summary, "Methodology", part 1: delta comes from
  * precomputed tables of the normal quantile function keyed on k or p).

@@ -15,3 +15,4 @@ from .qrita_oracle import (  # noqa: F401
     select_row,
 )
 from .qrita_outputs import SAMPLE_BAND, candidates, sample, topk_ids  # noqa: F401
+from .qrita_losses import RowSoftmax, dentropy, dlogp, policy_row, preference, row_softmax  # noqa: F401

@@ -1,13 +1,15 @@
 """Exact top-k / top-p candidate-set selection on GB300 (Python binding).
 
 Thin wrappers over the C ABI of ``libqrita.so`` (include/qrita.h) with the
-same names. They only marshal arguments: every step of the selection runs in
-the library's CUDA kernel. PyTorch provides device memory and streams.
+same names. They only marshal arguments: every step of the selection and of
+the losses runs in the library's CUDA kernels. PyTorch provides device memory and streams.
 """
 
 from __future__ import annotations
 
+import contextlib
 import ctypes
+from collections import namedtuple
 
 import numpy as np
 
@@ -306,3 +308,224 @@ def qrita_select_host(logits, k=None, p=None, out=None, staging=None, stream=Non
     if rc != OK:
         raise QritaError(rc)
     return out
+
+
+# ---------------------------------------------------------------------------
+# Losses over rows of logits
+# ---------------------------------------------------------------------------
+PolicyLoss = namedtuple("PolicyLoss", "loss grad row_loss logp kl entropy")
+PreferenceLoss = namedtuple("PreferenceLoss", "loss grad pair_loss log_ratio seq_logp logp")
+
+
+def _ptr(t) -> ctypes.c_void_p:
+    return ctypes.c_void_p(t.data_ptr() if t is not None and t.numel() else 0)
+
+
+def _padded_rows(t, name="logits"):
+    """B, V and the leading dimension of [B, V] rows that may be padded."""
+    if t.dim() != 2:
+        raise ValueError(f"{name} must be [B, V]")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    B, V = t.shape
+    ld = t.stride(0) if B > 1 else V
+    if V < 1 or (B > 0 and ((V > 1 and t.stride(1) != 1) or ld < V)):
+        raise ValueError(f"{name} must be row-major: unit stride within a row, a leading dimension of at least V")
+    return B, V, ld
+
+
+def _keep_mask(mask, B, V, device):
+    torch = _torch()
+    if mask is not None and (mask.shape != (B, V) or mask.dtype not in (torch.bool, torch.uint8) or not mask.is_contiguous()
+                             or mask.device != device):
+        raise ValueError("mask must be a contiguous bool/uint8 [B, V] tensor on the logits' device")
+    return mask
+
+
+def _need(t, name):
+    if t is None:
+        raise ValueError(f"{name} is required")
+    return t
+
+
+def _grad_rows(out, logits, B, V):
+    """The gradient's tensor and its leading dimension."""
+    torch = _torch()
+    if out is None:
+        return torch.empty((B, V), dtype=logits.dtype, device=logits.device), V
+    if out.shape != (B, V) or out.dtype != logits.dtype or out.device != logits.device:
+        raise ValueError("the gradient must be a [B, V] tensor of the logits' type on their device")
+    return out, _padded_rows(out, "the gradient")[2]
+
+
+class _Call:
+    """The stream of one call. Tensors made for a call on another stream than
+    the current one are marked as used there (so that their memory is not
+    handed out again before that stream is done), and the launch is made with
+    the logits' device as the current one."""
+
+    def __init__(self, device, stream):
+        torch = _torch()
+        self.device = device
+        self.current = torch.cuda.current_stream(device)
+        self.stream = stream if stream is not None else self.current
+        self.ptr = ctypes.c_void_p(self.stream.cuda_stream)
+
+    def own(self, *tensors):
+        if self.stream != self.current:
+            for t in tensors:
+                if t is not None:
+                    t.record_stream(self.stream)
+
+    def guard(self):
+        torch = _torch()
+        if torch.cuda.current_device() == self.device.index:
+            return contextlib.nullcontext()
+        return torch.cuda.device(self.device)
+
+
+def _rc(rc):
+    if rc != OK:
+        raise QritaError(rc)
+
+
+def qrita_token_logprobs(logits, tokens, mask=None, inv_temperature=1.0, entropy=False, stream=None):
+    """Log-probability of one given token per row, and the row's entropy.
+
+    logits: CUDA [B, V] float32 / bfloat16 (rows may be padded: any leading
+    dimension >= V); tokens: CUDA int32 [B], a token outside [0, V) ignores
+    its row; mask: bool/uint8 [B, V] or None, the kept set the softmax runs
+    over (e.g. qrita_select's output). Returns (logp float32 [B], entropy
+    float32 [B] or None). include/qrita.h states the row contract.
+    """
+    torch = _torch()
+    B, V, ld = _padded_rows(logits)
+    dev = logits.device
+    tok = _need(_vec(tokens, B, torch.int32, "tokens", dev), "tokens")
+    mask = _keep_mask(mask, B, V, dev)
+    call = _Call(dev, stream)
+    logp = torch.empty(B, dtype=torch.float32, device=dev)
+    ent = torch.empty(B, dtype=torch.float32, device=dev) if entropy else None
+    call.own(logp, ent)
+    with call.guard():
+        _rc(lib().qrita_token_logprobs(_ptr(logits), _dtype_code(logits), B, V, ld, _ptr(mask), _ptr(tok),
+                                       float(inv_temperature), _ptr(logp), _ptr(ent), call.ptr))
+    return logp, ent
+
+
+def qrita_token_logprobs_grad(logits, tokens, grad_logp=None, grad_entropy=None, mask=None, inv_temperature=1.0,
+                              out_grad=None, stream=None):
+    """Gradient with respect to the logits of any function of
+    qrita_token_logprobs' outputs, from the gradients of those outputs
+    (float32 [B] each; one may be None). Returns the gradient, [B, V] of the
+    logits' type; ``out_grad`` gives its tensor (rows may be padded, and it
+    may be the logits themselves)."""
+    torch = _torch()
+    B, V, ld = _padded_rows(logits)
+    dev = logits.device
+    tok = _need(_vec(tokens, B, torch.int32, "tokens", dev), "tokens")
+    mask = _keep_mask(mask, B, V, dev)
+    gl = _vec(grad_logp, B, torch.float32, "grad_logp", dev)
+    ge = _vec(grad_entropy, B, torch.float32, "grad_entropy", dev)
+    if gl is None and ge is None:
+        raise ValueError("one of grad_logp and grad_entropy is required")
+    call = _Call(dev, stream)
+    grad, ldg = _grad_rows(out_grad, logits, B, V)
+    call.own(grad)
+    with call.guard():
+        _rc(lib().qrita_token_logprobs_grad(_ptr(logits), _dtype_code(logits), B, V, ld, _ptr(mask), _ptr(tok),
+                                            float(inv_temperature), _ptr(gl), _ptr(ge), _ptr(grad), ldg, call.ptr))
+    return grad
+
+
+def qrita_policy_loss(logits, tokens, old_logp, advantages, ref_logp=None, weights=None, mask=None, inv_temperature=1.0,
+                      clip_low=0.2, clip_high=0.2, kl_coef=0.0, entropy_coef=0.0, grad_loss=None, grad=True,
+                      entropy=False, out_grad=None, stream=None):
+    """The clipped policy loss with a KL term over rows of logits, and its
+    gradient with respect to them, in one call.
+
+    logits, tokens, mask, inv_temperature: as qrita_token_logprobs.
+    old_logp (None: on-policy), ref_logp (None: no KL term), advantages,
+    weights (None: 1 / B): CUDA float32 [B]. grad_loss: CUDA float32 of one
+    element that multiplies the gradient, or None. grad=False leaves the
+    gradient out; entropy=True returns the entropies even where entropy_coef
+    is 0. Returns PolicyLoss(loss [], grad [B, V] or None, row_loss [B],
+    logp [B], kl [B], entropy [B] or None).
+    """
+    torch = _torch()
+    B, V, ld = _padded_rows(logits)
+    dev = logits.device
+    f32 = torch.float32
+    tok = _need(_vec(tokens, B, torch.int32, "tokens", dev), "tokens")
+    mask = _keep_mask(mask, B, V, dev)
+    old = _vec(old_logp, B, f32, "old_logp", dev)
+    ref = _vec(ref_logp, B, f32, "ref_logp", dev)
+    adv = _need(_vec(advantages, B, f32, "advantages", dev), "advantages")
+    w = _vec(weights, B, f32, "weights", dev)
+    gl = _vec(grad_loss, 1, f32, "grad_loss", dev)
+    call = _Call(dev, stream)
+    loss = torch.empty((), dtype=f32, device=dev)
+    want_ent = entropy or entropy_coef != 0
+    small = torch.empty((4 if want_ent else 3, B), dtype=f32, device=dev)
+    row_loss, logp, kl, *ent = small.unbind()
+    ent = ent[0] if ent else None
+    g, ldg = _grad_rows(out_grad, logits, B, V) if grad else (None, 0)
+    call.own(loss, small, g)
+    with call.guard():
+        _rc(lib().qrita_policy_loss(
+            _ptr(logits), _dtype_code(logits), B, V, ld, _ptr(mask), _ptr(tok), float(inv_temperature), _ptr(old),
+            _ptr(ref), _ptr(adv), _ptr(w), float(clip_low), float(clip_high), float(kl_coef), float(entropy_coef),
+            _ptr(gl), _ptr(loss), _ptr(row_loss), _ptr(logp), _ptr(kl), _ptr(ent), _ptr(g), ldg, call.ptr))
+    return PolicyLoss(loss, g, row_loss, logp, kl, ent)
+
+
+def preference_workspace_bytes(B: int, P: int) -> int:
+    return int(lib().qrita_preference_workspace_bytes(int(B), int(P)))
+
+
+def qrita_preference_loss(logits, tokens, starts, ref_logp=None, weights=None, inv_temperature=1.0, beta=0.1,
+                          label_smoothing=0.0, margin=0.0, length_norm=False, grad_loss=None, grad=True, out_grad=None,
+                          workspace=None, stream=None):
+    """The preference loss on paired log ratios over rows of logits, and its
+    gradient with respect to them.
+
+    logits, tokens, inv_temperature: as qrita_token_logprobs, the rows of all
+    sequences one after another. starts: CUDA int32 [2 P + 1], sequence s owns
+    rows [starts[s], starts[s + 1]); sequence 2i is the preferred one of pair
+    i, 2i + 1 the rejected one. ref_logp: float32 [2 P] or None; weights:
+    float32 [P] or None (1 / P); grad_loss as qrita_policy_loss. workspace:
+    CUDA uint8 of at least preference_workspace_bytes(B, P), one for each call
+    that may run at the same time (allocated here when None). Returns
+    PreferenceLoss(loss [], grad [B, V] or None, pair_loss [P], log_ratio [P],
+    seq_logp [2 P], logp [B]).
+    """
+    torch = _torch()
+    B, V, ld = _padded_rows(logits)
+    dev = logits.device
+    f32 = torch.float32
+    tok = _need(_vec(tokens, B, torch.int32, "tokens", dev), "tokens")
+    n = _need(starts, "starts").numel()
+    if n % 2 == 0:
+        raise ValueError("starts must hold 2 P + 1 elements")
+    P = n // 2
+    at = _vec(starts, n, torch.int32, "starts", dev)
+    ref = _vec(ref_logp, 2 * P, f32, "ref_logp", dev)
+    w = _vec(weights, P, f32, "weights", dev)
+    gl = _vec(grad_loss, 1, f32, "grad_loss", dev)
+    call = _Call(dev, stream)
+    need = preference_workspace_bytes(B, P)
+    if workspace is None:
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    elif workspace.dtype != torch.uint8 or workspace.device != dev or not workspace.is_contiguous() or workspace.numel() < need:
+        raise ValueError(f"workspace must be a contiguous uint8 tensor of at least {need} bytes on {dev}")
+    small = torch.empty(1 + 4 * P + B, dtype=f32, device=dev)
+    loss, pair_loss, ratio, seq, logp = small.split([1, P, P, 2 * P, B])
+    g, ldg = _grad_rows(out_grad, logits, B, V) if grad else (None, 0)
+    call.own(small, workspace, g)
+    with call.guard():
+        _rc(lib().qrita_preference_loss(
+            _ptr(logits), _dtype_code(logits), B, V, ld, _ptr(tok), float(inv_temperature), _ptr(at), P, _ptr(ref),
+            _ptr(w), float(beta), float(label_smoothing), float(margin), int(bool(length_norm)), _ptr(gl), _ptr(loss),
+            _ptr(pair_loss), _ptr(ratio), _ptr(seq), _ptr(logp), _ptr(g), ldg, _ptr(workspace),
+            ctypes.c_size_t(workspace.numel()), call.ptr))
+    return PreferenceLoss(loss[0], g, pair_loss, ratio, seq, logp)

@@ -19,6 +19,11 @@ EXPORTED = (
     "qrita_select_host",
     "qrita_topk_ids",
     "qrita_candidates",
+    "qrita_token_logprobs",
+    "qrita_token_logprobs_grad",
+    "qrita_policy_loss",
+    "qrita_preference_workspace_bytes",
+    "qrita_preference_loss",
     "qrita_delta_table",
     "qrita_strerror",
     "qrita_version",
@@ -50,6 +55,19 @@ def lib() -> ctypes.CDLL:
     L.qrita_topk_ids.restype = i32
     L.qrita_candidates.argtypes = [vp, i32, i64, i64, vp, i32, vp, vp, vp, vp, vp, vp]
     L.qrita_candidates.restype = i32
+    f64 = ctypes.c_double
+    L.qrita_token_logprobs.argtypes = [vp, i32, i64, i64, i64, vp, vp, f64, vp, vp, vp]
+    L.qrita_token_logprobs.restype = i32
+    L.qrita_token_logprobs_grad.argtypes = [vp, i32, i64, i64, i64, vp, vp, f64, vp, vp, vp, i64, vp]
+    L.qrita_token_logprobs_grad.restype = i32
+    L.qrita_policy_loss.argtypes = [vp, i32, i64, i64, i64, vp, vp, f64, vp, vp, vp, vp, f64, f64, f64, f64, vp, vp, vp,
+                                    vp, vp, vp, vp, i64, vp]
+    L.qrita_policy_loss.restype = i32
+    L.qrita_preference_workspace_bytes.argtypes = [i64, i64]
+    L.qrita_preference_workspace_bytes.restype = sz
+    L.qrita_preference_loss.argtypes = [vp, i32, i64, i64, i64, vp, f64, vp, i64, vp, vp, f64, f64, f64, i32, vp, vp, vp,
+                                        vp, vp, vp, vp, i64, vp, sz, vp]
+    L.qrita_preference_loss.restype = i32
     L.qrita_delta_table.argtypes = [i32, vp, i32]
     L.qrita_delta_table.restype = i32
     L.qrita_strerror.argtypes = [i32]

@@ -18,7 +18,7 @@ CSRC = os.path.join(PKG_DIR, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB_PATH = os.path.join(PKG_DIR, "libqrita.so")
 
-SOURCES = ["qrita_kernel.cu", "qrita_outputs.cu", "qrita_api.cpp"]
+SOURCES = ["qrita_kernel.cu", "qrita_outputs.cu", "qrita_losses.cu", "qrita_api.cpp"]
 HEADERS = ["qrita_device.cuh", "qrita_internal.h"]
 
 GENCODE = ["-gencode", "arch=compute_103a,code=sm_103a"]

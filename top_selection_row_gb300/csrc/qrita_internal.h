@@ -84,4 +84,53 @@ int launch_candidates(const void* logits, int dtype, int64_t B, int64_t V, const
                       int32_t* out_ids, float* out_probs, int32_t* out_count, const float* u, int32_t* out_sample,
                       qrita_stream_t stream);
 
+// Losses over rows of logits (qrita_losses.cu); every launch returns a
+// cudaError_t. Null pointers are the optional arguments of the C ABI.
+struct LossParams {
+  const void* logits;
+  int64_t B, V, ld;
+  const uint8_t* mask;
+  const int32_t* tokens;
+  float c;      // log2(e) * inv_temperature: weights are 2^(x c - shift)
+  float inv_t;
+  // outputs per row
+  float* logp;
+  float* entropy;
+  float* kl;
+  float* row_loss;
+  void* grad;
+  int64_t ld_grad;
+  const float* grad_loss;
+  // qrita_token_logprobs_grad
+  const float* g_logp;
+  const float* g_entropy;
+  // qrita_policy_loss
+  const float* old_logp;
+  const float* ref_logp;
+  const float* advantages;
+  const float* weights;
+  double clip_lo, clip_hi;  // 1 - clip_low, 1 + clip_high
+  double kl_coef, entropy_coef;
+  float* loss;
+};
+
+struct PrefParams {
+  const int32_t* starts;
+  int64_t P;
+  const float* ref;
+  const float* weights;
+  double beta, smoothing, margin;
+  int length_norm;
+  float* pair_loss;
+  float* log_ratio;
+  float* seq_logp;
+  void* workspace;
+};
+
+size_t pref_workspace_bytes(int64_t B, int64_t P);
+int launch_logprobs(const LossParams& prm, int dtype, qrita_stream_t stream);
+int launch_logprobs_grad(const LossParams& prm, int dtype, qrita_stream_t stream);
+int launch_policy(const LossParams& prm, int dtype, qrita_stream_t stream);
+int launch_preference(const LossParams& prm, const PrefParams& pref, int dtype, qrita_stream_t stream);
+
 }  // namespace qrita
