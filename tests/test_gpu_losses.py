@@ -385,10 +385,11 @@ def test_padded_rows_and_misaligned_pointers(dev, dtype, keep, V, ld, ldg, shift
     left = gflat.clone()
     left[shift:shift + B * ldg].view(B, ldg)[:, :V] = 7.0
     assert (left == 7.0).all()  # padding columns, and what lies before and behind
-    g = put(dev, rng.standard_normal(B).astype(np.float32))
-    want = q.qrita_token_logprobs_grad(tight, put(dev, tokens), g, mask=put(dev, mask))
-    q.qrita_token_logprobs_grad(xd, put(dev, tokens), g, mask=put(dev, mask), out_grad=gd)
-    assert torch.equal(torch.nan_to_num(gd), torch.nan_to_num(want))
+    # (not bit for bit what tight rows give: the order of the fp32 sums follows
+    # the rows' alignment, and both are held to the oracle)
+    g = rng.standard_normal(B).astype(np.float32)
+    q.qrita_token_logprobs_grad(xd, put(dev, tokens), put(dev, g), mask=put(dev, mask), out_grad=gd)
+    near_grad(gd, dtype, softmaxes(x, dtype, mask, tokens), tokens, g, np.zeros(B), np.zeros(B), 1.0)
 
 
 @pytest.mark.parametrize("dtype,keep", FORMS)

@@ -42,14 +42,8 @@ constexpr double kLn2 = 0.69314718055994530942;
 // of such a weight with its exponent (an entropy's terms) from being 0 * inf.
 constexpr float kMinExp = -1000.0f;
 
-// What a pass computes for a row.
-enum class Op { kLogprobs, kGrad, kPolicy, kPrefStats };
-
-// Partial softmax sums of some of a row's logits: their maximum, S and T
-// relative to it (-inf and 0 before the first kept logit).
-struct Stat {
-  float m, s, t;
-};
+// What row_kernel computes for a row.
+enum Op : int { kOpLogprobs, kOpGrad, kOpPolicy, kOpPrefStats };
 
 // g_j = 2^y_j (a + h y_j), y_j = (x_j - m) c; the token's own entry is `at`.
 struct RowGrad {
@@ -63,95 +57,267 @@ struct RowStat {
   float s;  // below 0: the row joins nothing
 };
 
+// The softmax sums of some of a row's kept logits, relative to their maximum
+// m (-inf, and sums of 0, before the first): S and T as fp32 pairs.
+struct Stat {
+  float m;
+  F2 s, t;
+};
+
+// What one thread reads of a row besides its logits, before any of the row's
+// gradient is written (which may lie over the logits).
+struct RowIn {
+  int64_t token;
+  float x_t;
+  bool kept_t;
+  float old_logp, ref_logp, adv;
+  double w;         // weight in the gradient: weights[row] * grad_loss
+  float g_logp, g_entropy;
+};
+
 __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
 
+// Two fp32 operations in one instruction.
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 r;
+  asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tadd.rn.f32x2 z, x, y;\n\t"
+      "mov.b64 {%0, %1}, z;\n\t}"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return r;
+}
+
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 r;
+  asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmul.rn.f32x2 z, x, y;\n\t"
+      "mov.b64 {%0, %1}, z;\n\t}"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return r;
+}
+
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 r;
+  asm("{\n\t.reg .b64 x, y, z, w;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmov.b64 w, {%6, %7};\n\t"
+      "fma.rn.f32x2 z, x, y, w;\n\tmov.b64 {%0, %1}, z;\n\t}"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return r;
+}
+
+__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
+
+// Element access. A row is worked on in units of 16 bytes, aligned in memory:
+// `head` elements before the first unit, then the units, then a tail.
 template <int DT>
-__device__ __forceinline__ float load_logit(const void* row, int64_t j) {
-  if constexpr (DT == QRITA_DTYPE_F32) {
-    return static_cast<const float*>(row)[j];
-  } else {
+struct Elem;
+
+template <>
+struct Elem<QRITA_DTYPE_F32> {
+  static constexpr int kBytes = 4;
+  static constexpr int kUnit = 4;
+  __device__ static float load(const void* row, int64_t j) { return static_cast<const float*>(row)[j]; }
+  __device__ static void store(void* row, int64_t j, float g) { static_cast<float*>(row)[j] = g; }
+  __device__ static void unpack(uint4 v, float2 (&x)[2]) {
+    x[0] = make_float2(__uint_as_float(v.x), __uint_as_float(v.y));
+    x[1] = make_float2(__uint_as_float(v.z), __uint_as_float(v.w));
+  }
+  __device__ static uint4 pack(const float2 (&x)[2]) {
+    return make_uint4(__float_as_uint(x[0].x), __float_as_uint(x[0].y), __float_as_uint(x[1].x), __float_as_uint(x[1].y));
+  }
+};
+
+// Two fp32 values as a word of two bf16, to nearest even: the one rounding of
+// a bf16 gradient.
+__device__ __forceinline__ uint32_t bf16_pair(float2 v) {
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(v.y), "f"(v.x));
+  return r;
+}
+
+template <>
+struct Elem<QRITA_DTYPE_BF16> {
+  static constexpr int kBytes = 2;
+  static constexpr int kUnit = 8;
+  __device__ static float load(const void* row, int64_t j) {
     return __uint_as_float(static_cast<uint32_t>(static_cast<const unsigned short*>(row)[j]) << 16);
   }
-}
-
-template <int DT>
-__device__ __forceinline__ void store_grad(void* row, int64_t j, float g) {
-  if constexpr (DT == QRITA_DTYPE_F32) {
-    static_cast<float*>(row)[j] = g;
-  } else {
-    // the one rounding of a bf16 gradient, to nearest even
-    unsigned short b;
-    asm("cvt.rn.bf16.f32 %0, %1;" : "=h"(b) : "f"(g));
-    static_cast<unsigned short*>(row)[j] = b;
+  __device__ static void store(void* row, int64_t j, float g) {
+    static_cast<unsigned short*>(row)[j] = static_cast<unsigned short>(bf16_pair(make_float2(g, 0.f)));
   }
-}
-
-template <int DT>
-__device__ __forceinline__ const void* row_at(const void* base, int64_t row, int64_t ld) {
-  return static_cast<const unsigned char*>(base) + row * ld * (DT == QRITA_DTYPE_F32 ? 4 : 2);
-}
-
-template <int DT>
-__device__ __forceinline__ void* row_at(void* base, int64_t row, int64_t ld) {
-  return static_cast<unsigned char*>(base) + row * ld * (DT == QRITA_DTYPE_F32 ? 4 : 2);
-}
-
-// The sums relative to the larger of two maxima.
-template <bool ENT>
-__device__ __forceinline__ Stat stat_merge(Stat a, Stat b, float c) {
-  const float m = fmaxf(a.m, b.m);
-  // (a maximum of -inf comes with sums of 0, which any finite shift leaves 0)
-  const float da = a.m == m ? 0.f : fmaxf((a.m - m) * c, kMinExp);
-  const float db = b.m == m ? 0.f : fmaxf((b.m - m) * c, kMinExp);
-  const float fa = ex2(da), fb = ex2(db);
-  Stat o;
-  o.m = m;
-  o.s = a.s * fa + b.s * fb;
-  o.t = ENT ? (a.t + da * a.s) * fa + (b.t + db * b.s) * fb : 0.f;
-  return o;
-}
-
-// Adds logit x to the sums.
-template <bool ENT>
-__device__ __forceinline__ void stat_add(Stat& a, float x, float c) {
-  if (x > a.m) {
-    const float d = fmaxf((a.m - x) * c, kMinExp);
-    const float f = ex2(d);
-    if (ENT) a.t = (a.t + d * a.s) * f;
-    a.s *= f;
-    a.m = x;
+  __device__ static void unpack(uint4 v, float2 (&x)[4]) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x[i] = make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xFFFF0000u));
   }
-  // a maximum of -inf: every logit so far is -inf and weighs 0 (or is NaN)
-  const float y = a.m == -INFINITY ? x : (x - a.m) * c;
-  const float e = ex2(y);
-  a.s += e;
-  if (ENT) a.t = fmaf(e, y < kMinExp ? kMinExp : y, a.t);
+  __device__ static uint4 pack(const float2 (&x)[4]) {
+    return make_uint4(bf16_pair(x[0]), bf16_pair(x[1]), bf16_pair(x[2]), bf16_pair(x[3]));
+  }
+};
+
+__device__ __forceinline__ uint4 load_unit(const void* p) { return *static_cast<const uint4*>(p); }
+
+// One CTA's share of a row: units [u_lo, u_hi) of nu, and on rank 0 the head
+// and the tail too (fewer than a unit each).
+template <int DT>
+struct Share {
+  const unsigned char* x;  // the row's logits
+  const uint8_t* mask;     // its mask, or null
+  int64_t V, head, nu, u_lo, u_hi;
+  bool ends;               // this CTA has the head and the tail
+  bool mask_vec;           // a unit's mask bytes are one aligned word (or two)
+
+  __device__ Share(const LossParams& p, int64_t row, uint32_t rank, uint32_t C) {
+    constexpr int U = Elem<DT>::kUnit;
+    V = p.V;
+    x = static_cast<const unsigned char*>(p.logits) + row * p.ld * Elem<DT>::kBytes;
+    mask = p.mask != nullptr ? p.mask + row * V : nullptr;
+    head = static_cast<int64_t>((16u - (reinterpret_cast<uintptr_t>(x) & 15u)) & 15u) / Elem<DT>::kBytes;
+    if (head > V) head = V;
+    nu = (V - head) / U;
+    const int64_t per = (nu + C - 1) / C;
+    u_lo = min(nu, static_cast<int64_t>(rank) * per);
+    u_hi = min(nu, u_lo + per);
+    ends = rank == 0;
+    mask_vec = (reinterpret_cast<uintptr_t>(mask + head) & (U - 1)) == 0;
+  }
+
+  __device__ const void* unit(int64_t u) const { return x + (head * Elem<DT>::kBytes) + u * 16; }
+
+  // Bit i set: element i of unit u is kept.
+  __device__ uint32_t kept(int64_t u) const {
+    constexpr int U = Elem<DT>::kUnit;
+    const uint8_t* m = mask + head + u * U;
+    uint32_t w[U / 4];
+    if (mask_vec) {
+#pragma unroll
+      for (int i = 0; i < U / 4; ++i) w[i] = reinterpret_cast<const uint32_t*>(m)[i];
+    } else {
+#pragma unroll
+      for (int i = 0; i < U / 4; ++i)
+        w[i] = m[4 * i] | (m[4 * i + 1] << 8) | (m[4 * i + 2] << 16) | (static_cast<uint32_t>(m[4 * i + 3]) << 24);
+    }
+    uint32_t bits = 0;
+#pragma unroll
+    for (int i = 0; i < U / 4; ++i) {
+      // bit 7 of each nonzero byte, gathered into four bits by one multiply
+      const uint32_t nz = ((((w[i] & 0x7F7F7F7Fu) + 0x7F7F7F7Fu) | w[i]) >> 7) & 0x01010101u;
+      bits |= ((nz * 0x01020408u) >> 24) << (4 * i);
+    }
+    return bits;
+  }
+
+  // Index of element i of the ends (head first, then tail), or -1 past them.
+  __device__ int64_t end_index(int i) const {
+    if (i < head) return i;
+    const int64_t j = head + nu * Elem<DT>::kUnit + (i - head);
+    return j < V ? j : -1;
+  }
+  static constexpr int kEnds = 2 * (Elem<DT>::kUnit - 1);  // at most
+};
+
+// A thread's running sums, relative to the largest logit it has seen (0
+// stands for -inf in ref).
+template <bool ENT>
+struct Running {
+  float m = -INFINITY, ref = 0.f, s = 0.f, t = 0.f;
+
+  __device__ __forceinline__ void raise(float x, float c) {
+    if (x > m) {
+      // before the first finite logit the sums are 0 (or NaN), whatever the factor
+      const float d = fmaxf((m - x) * c, kMinExp);
+      const float f = ex2(d);
+      if (ENT) t = (t + d * s) * f;
+      s *= f;
+      m = ref = x;
+    }
+  }
+  __device__ __forceinline__ void add_one(float x, float c) {
+    raise(x, c);
+    const float y = (x - ref) * c;
+    const float e = ex2(y);
+    s += e;
+    if (ENT) t = fmaf(e, y < kMinExp ? kMinExp : y, t);
+  }
+  // N pairs: their own sum first, then one addition to the running one
+  template <int N>
+  __device__ __forceinline__ void add_unit(const float2 (&x)[N], float c) {
+    float top = fmaxf(x[0].x, x[0].y);
+#pragma unroll
+    for (int i = 1; i < N; ++i) top = fmaxf(top, fmaxf(x[i].x, x[i].y));
+    raise(top, c);
+    const float2 nr = both(-ref), cc = both(c);
+    float2 es[N], ts[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const float2 y = mul2(add2(x[i], nr), cc);
+      es[i] = make_float2(ex2(y.x), ex2(y.y));
+      if (ENT) ts[i] = mul2(es[i], make_float2(y.x < kMinExp ? kMinExp : y.x, y.y < kMinExp ? kMinExp : y.y));
+    }
+#pragma unroll
+    for (int o = N / 2; o > 0; o >>= 1)
+#pragma unroll
+      for (int i = 0; i < o; ++i) {
+        es[i] = add2(es[i], es[i + o]);
+        if (ENT) ts[i] = add2(ts[i], ts[i + o]);
+      }
+    s += es[0].x + es[0].y;
+    if (ENT) t += ts[0].x + ts[0].y;
+  }
+};
+
+// Sums relative to m raised to `to` (>= m).
+template <bool ENT>
+__device__ __forceinline__ void stat_shift(Stat& a, float to, float c) {
+  if (a.m == to) return;
+  const float d = fmaxf((a.m - to) * c, kMinExp);
+  const float f = ex2(d);
+  if (ENT) {
+    a.t = f2_merge(a.t, f2_prod(d, a.s.hi));
+    a.t = f2_mul(a.t, f);
+  }
+  a.s = f2_mul(a.s, f);
+  a.m = to;
 }
 
+// The block's sums from every thread's, valid in thread 0.
 template <bool ENT>
-__device__ __forceinline__ Stat stat_block(Stat v, Stat* slots, float c) {
+__device__ __forceinline__ Stat block_stat(const Running<ENT>& r, float c, Stat* slots) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  float m = r.m;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kAll, m, o));
+  Stat v;
+  v.m = r.m;
+  v.s = f2_make(r.s, 0.f);
+  v.t = f2_make(r.t, 0.f);
+  stat_shift<ENT>(v, m, c);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
-    Stat w;
-    w.m = __shfl_xor_sync(kAll, v.m, o);
-    w.s = __shfl_xor_sync(kAll, v.s, o);
-    w.t = ENT ? __shfl_xor_sync(kAll, v.t, o) : 0.f;
-    v = stat_merge<ENT>(v, w, c);
+    v.s = f2_merge(v.s, f2_make(__shfl_xor_sync(kAll, v.s.hi, o), __shfl_xor_sync(kAll, v.s.lo, o)));
+    if (ENT) v.t = f2_merge(v.t, f2_make(__shfl_xor_sync(kAll, v.t.hi, o), __shfl_xor_sync(kAll, v.t.lo, o)));
   }
-  if ((threadIdx.x & 31) == 0) slots[threadIdx.x >> 5] = v;
+  if (lane == 0) slots[warp] = v;
   __syncthreads();
-  Stat o = slots[0];
-  for (int w = 1; w < kLossWarps; ++w) o = stat_merge<ENT>(o, slots[w], c);
-  __syncthreads();
-  return o;
+  if (threadIdx.x == 0) {
+    for (int w = 1; w < kLossWarps; ++w) m = fmaxf(m, slots[w].m);
+    stat_shift<ENT>(v, m, c);
+    for (int w = 1; w < kLossWarps; ++w) {
+      Stat o = slots[w];
+      stat_shift<ENT>(o, m, c);
+      v.s = f2_merge(v.s, o.s);
+      if (ENT) v.t = f2_merge(v.t, o.t);
+    }
+  }
+  return v;
 }
 
 // A, Hc and the token's entry from the weights a, h of dlogp and dH.
-__device__ __forceinline__ RowGrad row_grad(double a, double h, double logp, double H, double ln_s, float m, float s,
+__device__ __forceinline__ RowGrad row_grad(double a, double h, double logp, double H, double ln_s, float m, double s,
                                             float inv_t) {
   RowGrad g;
   g.m = m;
@@ -166,39 +332,61 @@ __device__ __forceinline__ RowGrad row_grad(double a, double h, double logp, dou
   return g;
 }
 
-// Everything a row gives besides its gradient's entries; run by one thread.
-// kept_t: the token is in the kept set; x_t its logit.
-template <Op OP, bool ENT>
-__device__ __forceinline__ RowGrad row_scalars(const LossParams& p, RowStat* stats, int64_t row, Stat st, bool kept_t,
-                                               float x_t) {
+template <int DT>
+__device__ __forceinline__ RowIn row_in(const LossParams& p, int op, int64_t row, int64_t token) {
+  RowIn in;
+  in.token = token;
+  in.x_t = Elem<DT>::load(static_cast<const unsigned char*>(p.logits) + row * p.ld * Elem<DT>::kBytes, token);
+  in.kept_t = p.mask == nullptr || p.mask[row * p.V + token] != 0;
+  in.old_logp = in.ref_logp = in.adv = in.g_logp = in.g_entropy = 0.f;
+  in.w = 0.0;
+  if (op == kOpGrad) {
+    if (p.g_logp != nullptr) in.g_logp = p.g_logp[row];
+    if (p.g_entropy != nullptr) in.g_entropy = p.g_entropy[row];
+  } else if (op == kOpPolicy) {
+    if (p.old_logp != nullptr) in.old_logp = p.old_logp[row];
+    if (p.ref_logp != nullptr) in.ref_logp = p.ref_logp[row];
+    in.adv = p.advantages[row];
+    in.w = (p.weights != nullptr ? p.weights[row] : 1.0 / static_cast<double>(p.B)) *
+           (p.grad_loss != nullptr ? *p.grad_loss : 1.0);
+  }
+  return in;
+}
+
+// Everything a row gives besides its gradient's entries. `out`: this thread
+// writes the row's values.
+template <bool ENT>
+__device__ __forceinline__ RowGrad row_scalars(const LossParams& p, int op, RowStat* stats, int64_t row, const RowIn& in,
+                                               const Stat& st, bool out) {
   RowGrad g;
   g.m = st.m;
   g.a = g.h = g.at = 0.f;
-  const bool empty = st.s == 0.f;  // nothing kept, or only -inf
-  const double log2_s = empty ? 0.0 : log2(static_cast<double>(st.s));
+  const double S = static_cast<double>(st.s.hi) + st.s.lo;
+  const bool empty = S == 0.0;  // nothing kept, or only -inf
+  const double log2_s = empty ? 0.0 : log2(S);
   double logp = -INFINITY;
-  if (kept_t && !empty) logp = ((static_cast<double>(x_t) - st.m) * p.c - log2_s) * kLn2;
-  const double H = ENT && !empty ? (log2_s - static_cast<double>(st.t) / st.s) * kLn2 : 0.0;
+  if (in.kept_t && !empty) logp = ((static_cast<double>(in.x_t) - st.m) * p.c - log2_s) * kLn2;
+  const double H = ENT && !empty ? (log2_s - (static_cast<double>(st.t.hi) + st.t.lo) / S) * kLn2 : 0.0;
   const bool joins = logp != -INFINITY;  // (NaN joins)
-  if (p.logp != nullptr) p.logp[row] = static_cast<float>(logp);
-  if (ENT && p.entropy != nullptr) p.entropy[row] = static_cast<float>(H);
-  if constexpr (OP == Op::kGrad) {
-    const double a = joins && p.g_logp != nullptr ? p.g_logp[row] : 0.0;
-    const double h = ENT && !empty ? p.g_entropy[row] : 0.0;
-    g = row_grad(a, h, logp, H, log2_s * kLn2, st.m, st.s, p.inv_t);
+  if (out) {
+    if (p.logp != nullptr) p.logp[row] = static_cast<float>(logp);
+    if (ENT && p.entropy != nullptr) p.entropy[row] = static_cast<float>(H);
   }
-  if constexpr (OP == Op::kPolicy) {
+  if (op == kOpGrad) {
+    g = row_grad(joins ? in.g_logp : 0.0, ENT && !empty ? in.g_entropy : 0.0, logp, H, log2_s * kLn2, st.m, S, p.inv_t);
+  } else if (op == kOpPolicy) {
     double loss = 0.0, kl = 0.0;
     if (joins) {
-      const double adv = p.advantages[row];
-      const double rho = p.old_logp != nullptr ? exp(logp - p.old_logp[row]) : 1.0;
+      const double adv = in.adv;
+      const double rho = p.old_logp != nullptr ? exp(logp - in.old_logp) : 1.0;
       const double near = fmin(fmax(rho, p.clip_lo), p.clip_hi);
       loss = fmax(-adv * rho, -adv * near);
       if (rho != rho || logp != logp) loss = logp + rho;  // NaN goes through fmin and fmax unseen
       const bool bound = (adv > 0.0 && rho > p.clip_hi) || (adv < 0.0 && rho < p.clip_lo);
       double a = bound ? 0.0 : -adv * rho;
+      if (logp != logp) a = logp;
       if (p.ref_logp != nullptr) {
-        const double q = p.ref_logp[row] - logp;
+        const double q = in.ref_logp - logp;
         const double eq = expm1(q);
         kl = eq - q;
         if (p.kl_coef != 0.0) {
@@ -207,35 +395,32 @@ __device__ __forceinline__ RowGrad row_scalars(const LossParams& p, RowStat* sta
         }
       }
       if (ENT) loss -= p.entropy_coef * H;
-      if (p.grad != nullptr) {
-        const double w = (p.weights != nullptr ? p.weights[row] : 1.0 / static_cast<double>(p.B)) *
-                         (p.grad_loss != nullptr ? *p.grad_loss : 1.0);
-        g = row_grad(w * a, ENT ? -p.entropy_coef * w : 0.0, logp, H, log2_s * kLn2, st.m, st.s, p.inv_t);
-      }
+      if (p.grad != nullptr)
+        g = row_grad(in.w * a, ENT ? -p.entropy_coef * in.w : 0.0, logp, H, log2_s * kLn2, st.m, S, p.inv_t);
     }
-    p.row_loss[row] = static_cast<float>(loss);
-    if (p.kl != nullptr) p.kl[row] = static_cast<float>(kl);
-  }
-  if constexpr (OP == Op::kPrefStats) {
+    if (out) {
+      p.row_loss[row] = static_cast<float>(loss);
+      if (p.kl != nullptr) p.kl[row] = static_cast<float>(kl);
+    }
+  } else if (op == kOpPrefStats && out) {
     RowStat o;
     o.logp = logp;
     o.m = st.m;
-    o.s = joins ? st.s : -1.f;
+    o.s = joins ? static_cast<float>(S) : -1.f;
     stats[row] = o;
   }
   return g;
 }
 
 // Outputs of an ignored row, besides its gradient of 0.
-template <Op OP>
-__device__ __forceinline__ void row_ignored(const LossParams& p, RowStat* stats, int64_t row) {
+__device__ __forceinline__ void row_ignored(const LossParams& p, int op, RowStat* stats, int64_t row) {
   if (p.logp != nullptr) p.logp[row] = 0.f;
   if (p.entropy != nullptr) p.entropy[row] = 0.f;
-  if constexpr (OP == Op::kPolicy) {
+  if (op == kOpPolicy) {
     p.row_loss[row] = 0.f;
     if (p.kl != nullptr) p.kl[row] = 0.f;
   }
-  if constexpr (OP == Op::kPrefStats) {
+  if (op == kOpPrefStats) {
     RowStat o;
     o.logp = 0.0;
     o.m = 0.f;
@@ -244,54 +429,196 @@ __device__ __forceinline__ void row_ignored(const LossParams& p, RowStat* stats,
   }
 }
 
-// Writes a row's gradient; token < 0: it has none of its own entry.
-template <int DT, bool ENT>
-__device__ __forceinline__ void write_grad(const LossParams& p, const void* xrow, const uint8_t* mrow, void* grow,
-                                           RowGrad g, int64_t token) {
+template <bool ENT>
+__device__ __forceinline__ float grad_one(float x, const RowGrad& g, float c) {
+  const float y = (x - g.m) * c;
+  return ex2(y) * (ENT ? fmaf(g.h, y < kMinExp ? kMinExp : y, g.a) : g.a);
+}
+
+constexpr int kUnroll = 4;  // units a thread has in flight
+
+// Writes this CTA's share of a row's gradient. token < 0: no entry of its
+// own. Every unit is read and then written by the same thread, so the
+// gradient may lie over the logits.
+template <int DT, bool ENT, bool MASKED>
+__device__ __forceinline__ void write_grad(const LossParams& p, const Share<DT>& sh, int64_t row, const RowGrad& g,
+                                           int64_t token) {
+  using E = Elem<DT>;
+  constexpr int N = E::kUnit / 2;
+  unsigned char* grow = static_cast<unsigned char*>(p.grad) + row * p.ld_grad * E::kBytes;
+  unsigned char* gu = grow + sh.head * E::kBytes;
+  const bool vec = (reinterpret_cast<uintptr_t>(gu) & 15u) == 0;
   const bool zero = g.a == 0.f && g.h == 0.f;
-  for (int64_t j = threadIdx.x; j < p.V; j += kLossThreads) {
-    float v = 0.f;
-    if (j == token) {
-      v = g.at;
-    } else if (!zero && (mrow == nullptr || mrow[j] != 0)) {
-      const float y = (load_logit<DT>(xrow, j) - g.m) * p.c;
-      v = ex2(y) * (ENT ? fmaf(g.h, y < kMinExp ? kMinExp : y, g.a) : g.a);
+  const float2 nm = both(-g.m), cc = both(p.c), aa = both(g.a), hh = both(g.h);
+  auto put = [&](int64_t u, const float2 (&v)[N]) {
+    if (vec) {
+      *reinterpret_cast<uint4*>(gu + u * 16) = E::pack(v);
+    } else {
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        E::store(gu, u * E::kUnit + 2 * i, v[i].x);
+        E::store(gu, u * E::kUnit + 2 * i + 1, v[i].y);
+      }
     }
-    store_grad<DT>(grow, j, v);
+  };
+  if (zero) {
+    float2 v[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = both(0.f);
+    for (int64_t u = sh.u_lo + threadIdx.x; u < sh.u_hi; u += kLossThreads) put(u, v);
+  } else {
+    for (int64_t u0 = sh.u_lo + threadIdx.x; u0 < sh.u_hi; u0 += kLossThreads * kUnroll) {
+      uint4 w[kUnroll];
+      uint32_t bits[kUnroll];
+#pragma unroll
+      for (int k = 0; k < kUnroll; ++k) {
+        const int64_t u = u0 + k * kLossThreads;
+        bits[k] = u < sh.u_hi ? (MASKED ? sh.kept(u) : 1u) : 0u;
+      }
+#pragma unroll
+      for (int k = 0; k < kUnroll; ++k) {
+        w[k] = make_uint4(0u, 0u, 0u, 0u);
+        if (bits[k] != 0u) w[k] = load_unit(sh.unit(u0 + k * kLossThreads));
+      }
+#pragma unroll
+      for (int k = 0; k < kUnroll; ++k) {
+        const int64_t u = u0 + k * kLossThreads;
+        if (u >= sh.u_hi) break;
+        float2 x[N], v[N];
+        E::unpack(w[k], x);
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+          const float2 y = mul2(add2(x[i], nm), cc);
+          const float2 e = make_float2(ex2(y.x), ex2(y.y));
+          v[i] = ENT ? mul2(e, fma2(hh, make_float2(y.x < kMinExp ? kMinExp : y.x, y.y < kMinExp ? kMinExp : y.y), aa))
+                     : mul2(e, aa);
+          if (MASKED) {
+            if (!(bits[k] >> (2 * i) & 1u)) v[i].x = 0.f;
+            if (!(bits[k] >> (2 * i + 1) & 1u)) v[i].y = 0.f;
+          }
+        }
+        put(u, v);
+      }
+    }
+  }
+  if (sh.ends && threadIdx.x < Share<DT>::kEnds) {
+    const int64_t j = sh.end_index(threadIdx.x);
+    if (j >= 0) {
+      float v = 0.f;
+      if (!zero && (!MASKED || sh.mask[j] != 0)) v = grad_one<ENT>(E::load(sh.x, j), g, p.c);
+      E::store(grow, j, v);
+    }
+  }
+  // the token's own entry, by the CTA that wrote its place
+  if (token >= 0) {
+    const int64_t u = (token - sh.head) / E::kUnit;  // (token < head: 0 or below, an end)
+    const bool end = token < sh.head || u >= sh.nu;
+    if (end ? sh.ends : (u >= sh.u_lo && u < sh.u_hi)) {
+      __syncthreads();
+      if (threadIdx.x == 0) E::store(grow, token, g.at);
+    }
   }
 }
 
-// One CTA per row: the softmax sums in one pass, the row's values, and a
-// second pass for the gradient.
-template <int DT, Op OP, bool ENT>
-__global__ void __launch_bounds__(kLossThreads) row_kernel(const LossParams p, RowStat* stats) {
+// The record a CTA of a cluster gives the others.
+constexpr int kMaxRanks = 16;
+constexpr int kStatWords = 5;
+
+// A cluster of C CTAs per row: the softmax sums of every CTA's share in one
+// pass, merged through distributed shared memory; the row's values (rank 0
+// writes them); and a second pass over the share for the gradient, whose
+// reads come from L2.
+template <int DT, bool ENT, bool MASKED>
+__global__ void __launch_bounds__(kLossThreads, 4) row_kernel(const LossParams p, RowStat* stats, int op, uint32_t C) {
+  using E = Elem<DT>;
+  constexpr int N = E::kUnit / 2;
   __shared__ Stat slots[kLossWarps];
+  __shared__ float ranks[kMaxRanks][kStatWords];
   __shared__ RowGrad grad;
-  const int64_t row = blockIdx.x;
-  const void* xrow = row_at<DT>(p.logits, row, p.ld);
-  const uint8_t* mrow = p.mask != nullptr ? p.mask + row * p.V : nullptr;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const uint32_t rank = C > 1 ? cluster_rank() : 0u;
+  const int64_t row = blockIdx.x / C;
+  const Share<DT> sh(p, row, rank, C);
   const int64_t token = p.tokens[row];
-  const bool ignored = token < 0 || token >= p.V;
   RowGrad g = {0.f, 0.f, 0.f, 0.f};
-  if (ignored) {
-    if (threadIdx.x == 0) row_ignored<OP>(p, stats, row);
-  } else {
-    Stat st = {-INFINITY, 0.f, 0.f};
-    for (int64_t j = threadIdx.x; j < p.V; j += kLossThreads)
-      if (mrow == nullptr || mrow[j] != 0) stat_add<ENT>(st, load_logit<DT>(xrow, j), p.c);
-    st = stat_block<ENT>(st, slots, p.c);
-    if (threadIdx.x == 0)
-      grad = row_scalars<OP, ENT>(p, stats, row, st, mrow == nullptr || mrow[token] != 0, load_logit<DT>(xrow, token));
-    __syncthreads();
-    g = grad;
+  if (token < 0 || token >= p.V) {  // (the same in every CTA of the cluster)
+    if (threadIdx.x == 0 && rank == 0) row_ignored(p, op, stats, row);
+    if (p.grad != nullptr) write_grad<DT, ENT, MASKED>(p, sh, row, g, -1);
+    return;
   }
-  if (p.grad != nullptr)
-    write_grad<DT, ENT>(p, xrow, mrow, row_at<DT>(p.grad, row, p.ld_grad), g,
-                        ignored || (mrow != nullptr && mrow[token] == 0) ? -1 : token);
+  if (C > 1) cluster_arrive_relaxed();  // every CTA of the cluster runs before its memory is written
+  RowIn in;
+  if (threadIdx.x == 0) in = row_in<DT>(p, op, row, token);
+  Running<ENT> run;
+  for (int64_t u0 = sh.u_lo + threadIdx.x; u0 < sh.u_hi; u0 += kLossThreads * kUnroll) {
+    uint4 w[kUnroll];
+    uint32_t bits[kUnroll];
+#pragma unroll
+    for (int k = 0; k < kUnroll; ++k) {
+      const int64_t u = u0 + k * kLossThreads;
+      bits[k] = u < sh.u_hi ? (MASKED ? sh.kept(u) : 1u) : 0u;
+    }
+#pragma unroll
+    for (int k = 0; k < kUnroll; ++k)
+      if (bits[k] != 0u) w[k] = load_unit(sh.unit(u0 + k * kLossThreads));
+#pragma unroll
+    for (int k = 0; k < kUnroll; ++k) {
+      if (bits[k] == 0u) continue;
+      float2 x[N];
+      E::unpack(w[k], x);
+      if (MASKED) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+          if (!(bits[k] >> (2 * i) & 1u)) x[i].x = -INFINITY;
+          if (!(bits[k] >> (2 * i + 1) & 1u)) x[i].y = -INFINITY;
+        }
+      }
+      run.add_unit(x, p.c);
+    }
+  }
+  if (sh.ends && threadIdx.x < Share<DT>::kEnds) {
+    const int64_t j = sh.end_index(threadIdx.x);
+    if (j >= 0 && (!MASKED || sh.mask[j] != 0)) run.add_one(E::load(sh.x, j), p.c);
+  }
+  Stat st = block_stat<ENT>(run, p.c, slots);
+  if (C > 1) {
+    cluster_wait();
+    if (threadIdx.x == 0) {
+      const float rec[kStatWords] = {st.m, st.s.hi, st.s.lo, st.t.hi, st.t.lo};
+      for (uint32_t r = 0; r < C; ++r) {
+        const uint32_t at = map_rank(smem_u32(&ranks[rank][0]), r);
+#pragma unroll
+        for (int i = 0; i < (ENT ? 5 : 3); ++i) st_dsmem_u32(at + 4 * i, __float_as_uint(rec[i]));
+      }
+    }
+    cluster_sync_all();
+    if (threadIdx.x == 0) {
+      st.m = -INFINITY;
+      for (uint32_t r = 0; r < C; ++r) st.m = fmaxf(st.m, ranks[r][0]);
+      st.s = st.t = f2_make(0.f, 0.f);
+      for (uint32_t r = 0; r < C; ++r) {
+        Stat o;
+        o.m = ranks[r][0];
+        o.s = f2_make(ranks[r][1], ranks[r][2]);
+        o.t = ENT ? f2_make(ranks[r][3], ranks[r][4]) : f2_make(0.f, 0.f);
+        stat_shift<ENT>(o, st.m, p.c);
+        st.s = f2_merge(st.s, o.s);
+        if (ENT) st.t = f2_merge(st.t, o.t);
+      }
+    }
+  }
+  if (threadIdx.x == 0 && (rank == 0 || p.grad != nullptr)) grad = row_scalars<ENT>(p, op, stats, row, in, st, rank == 0);
+  if (p.grad == nullptr) return;
+  __syncthreads();
+  g = grad;
+  write_grad<DT, ENT, MASKED>(p, sh, row, g, MASKED && sh.mask[token] == 0 ? -1 : token);
 }
 
 // out = sum of w[i] v[i] in one fixed order, in fp64 (w NULL: 1 / n).
 __global__ void __launch_bounds__(1024) weighted_sum_kernel(const float* v, const float* w, int64_t n, float* out) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   __shared__ double slots[32];
   double s = 0.0;
   for (int64_t i = threadIdx.x; i < n; i += 1024) s += static_cast<double>(v[i]) * (w != nullptr ? w[i] : 1.0);
@@ -323,6 +650,8 @@ constexpr int kPairThreads = 128;
 // and the weight of dlogp of each sequence's rows.
 __global__ void __launch_bounds__(kPairThreads) pair_kernel(const LossParams p, const PrefParams q,
                                                             const RowStat* stats, double* coef) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   __shared__ double sum_slots[kPairThreads / 32];
   __shared__ int cnt_slots[kPairThreads / 32];
   const int64_t i = blockIdx.x;
@@ -387,66 +716,129 @@ __device__ __forceinline__ int64_t sequence_of(const int32_t* starts, int64_t n_
   return lo - 1;
 }
 
+// The gradient of every row, the last rows first: those are the ones the
+// sums' kernel has left in L2.
 template <int DT>
-__global__ void __launch_bounds__(kLossThreads) pref_grad_kernel(const LossParams p, const PrefParams q,
-                                                                 const RowStat* stats, const double* coef) {
-  const int64_t row = blockIdx.x;
-  const void* xrow = row_at<DT>(p.logits, row, p.ld);
-  const int64_t s = q.P > 0 ? sequence_of(q.starts, 2 * q.P + 1, row) : -1;
-  RowGrad g = {0.f, 0.f, 0.f, 0.f};
-  int64_t token = -1;
-  if (s >= 0 && s < 2 * q.P) {
-    const RowStat st = stats[row];
-    if (!(st.s < 0.f)) {
-      token = p.tokens[row];
-      g = row_grad(coef[s], 0.0, st.logp, 0.0, 0.0, st.m, st.s, p.inv_t);
+__global__ void __launch_bounds__(kLossThreads, 4) pref_grad_kernel(const LossParams p, const PrefParams q,
+                                                                    const RowStat* stats, const double* coef, uint32_t C) {
+  __shared__ RowGrad grad;
+  __shared__ int64_t grad_token;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const int64_t row = p.B - 1 - blockIdx.x / C;
+  const Share<DT> sh(p, row, blockIdx.x % C, C);
+  if (threadIdx.x == 0) {
+    const int64_t s = q.P > 0 ? sequence_of(q.starts, 2 * q.P + 1, row) : -1;
+    RowGrad g = {0.f, 0.f, 0.f, 0.f};
+    int64_t token = -1;
+    if (s >= 0 && s < 2 * q.P) {
+      const RowStat st = stats[row];
+      if (!(st.s < 0.f)) {
+        token = p.tokens[row];
+        g = row_grad(coef[s], 0.0, st.logp, 0.0, 0.0, st.m, st.s, p.inv_t);
+      }
     }
+    grad = g;
+    grad_token = token;
   }
-  write_grad<DT, false>(p, xrow, nullptr, row_at<DT>(p.grad, row, p.ld_grad), g, token);
+  __syncthreads();
+  write_grad<DT, false, false>(p, sh, row, grad, grad_token);
 }
 
 // out_logp of rows that no sequence owns is 0.
 __global__ void __launch_bounds__(kLossThreads) outside_kernel(const PrefParams q, int64_t B, float* logp) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int64_t row = static_cast<int64_t>(blockIdx.x) * kLossThreads + threadIdx.x;
   if (row >= B) return;
   const int64_t s = q.P > 0 ? sequence_of(q.starts, 2 * q.P + 1, row) : -1;
   if (s < 0 || s >= 2 * q.P) logp[row] = 0.f;
 }
 
-template <Op OP, bool ENT>
-cudaError_t launch_rows(const LossParams& p, int dtype, RowStat* stats, cudaStream_t st) {
-  const unsigned g = static_cast<unsigned>(p.B);
+// CTAs per row: as many as fill the device (a power of two), with at least a
+// unit or two for each thread; and enough that the rows in flight fit in L2
+// when a second pass follows.
+uint32_t row_ctas(const LossParams& p, int dtype, bool second_pass) {
+  const int64_t bytes = p.V * (dtype == QRITA_DTYPE_F32 ? 4 : 2);
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+    sms = 152;
+  const int64_t slots = static_cast<int64_t>(sms) * 4;
+  uint32_t C = 1;
+  while (C < kMaxRanks && bytes / (2 * C) >= 4096 && p.B * 2 * C <= slots) C *= 2;
+  if (second_pass)
+    while (C < 8 && bytes / C > 64 * 1024 && p.B * 2 * C <= INT32_MAX) C *= 2;
+  return C;
+}
+
+template <typename F, typename... Args>
+cudaError_t launch(F* fn, unsigned grid, unsigned block, unsigned cluster, cudaStream_t st, Args... args) {
+  if (cluster > 8) {
+    const cudaError_t e =
+        cudaFuncSetAttribute(reinterpret_cast<const void*>(fn), cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e != cudaSuccess) return e;
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid, 1, 1);
+  cfg.blockDim = dim3(block, 1, 1);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  // the CTAs may be scheduled while the previous kernel of the stream drains;
+  // they wait for it (griddepcontrol) before touching memory
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = cluster;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, fn, args...);
+  const cudaError_t last = cudaGetLastError();
+  return e != cudaSuccess ? e : last;
+}
+
+template <int DT, bool ENT>
+cudaError_t launch_rows_of(const LossParams& p, int op, RowStat* stats, cudaStream_t st) {
+  const uint32_t C = row_ctas(p, DT, p.grad != nullptr);
+  const unsigned grid = static_cast<unsigned>(p.B * C);
+  return p.mask != nullptr ? launch(&row_kernel<DT, ENT, true>, grid, kLossThreads, C, st, p, stats, op, C)
+                           : launch(&row_kernel<DT, ENT, false>, grid, kLossThreads, C, st, p, stats, op, C);
+}
+
+cudaError_t launch_rows(const LossParams& p, int dtype, int op, bool ent, RowStat* stats, cudaStream_t st) {
   if (dtype == QRITA_DTYPE_F32)
-    row_kernel<QRITA_DTYPE_F32, OP, ENT><<<g, kLossThreads, 0, st>>>(p, stats);
-  else
-    row_kernel<QRITA_DTYPE_BF16, OP, ENT><<<g, kLossThreads, 0, st>>>(p, stats);
-  return cudaGetLastError();
+    return ent ? launch_rows_of<QRITA_DTYPE_F32, true>(p, op, stats, st)
+               : launch_rows_of<QRITA_DTYPE_F32, false>(p, op, stats, st);
+  return ent ? launch_rows_of<QRITA_DTYPE_BF16, true>(p, op, stats, st)
+             : launch_rows_of<QRITA_DTYPE_BF16, false>(p, op, stats, st);
+}
+
+cudaError_t launch_sum(const float* v, const float* w, int64_t n, float* out, cudaStream_t st) {
+  return launch(&weighted_sum_kernel, 1u, 1024u, 1u, st, v, w, n, out);
 }
 
 }  // namespace
 
 int launch_logprobs(const LossParams& p, int dtype, qrita_stream_t stream) {
-  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  return static_cast<int>(p.entropy != nullptr ? launch_rows<Op::kLogprobs, true>(p, dtype, nullptr, st)
-                                               : launch_rows<Op::kLogprobs, false>(p, dtype, nullptr, st));
+  return static_cast<int>(
+      launch_rows(p, dtype, kOpLogprobs, p.entropy != nullptr, nullptr, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 int launch_logprobs_grad(const LossParams& p, int dtype, qrita_stream_t stream) {
-  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  return static_cast<int>(p.g_entropy != nullptr ? launch_rows<Op::kGrad, true>(p, dtype, nullptr, st)
-                                                 : launch_rows<Op::kGrad, false>(p, dtype, nullptr, st));
+  return static_cast<int>(
+      launch_rows(p, dtype, kOpGrad, p.g_entropy != nullptr, nullptr, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 int launch_policy(const LossParams& p, int dtype, qrita_stream_t stream) {
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   if (p.B > 0) {
-    const bool ent = p.entropy != nullptr || p.entropy_coef != 0.0;
-    const cudaError_t e = ent ? launch_rows<Op::kPolicy, true>(p, dtype, nullptr, st)
-                              : launch_rows<Op::kPolicy, false>(p, dtype, nullptr, st);
+    const cudaError_t e =
+        launch_rows(p, dtype, kOpPolicy, p.entropy != nullptr || p.entropy_coef != 0.0, nullptr, st);
     if (e != cudaSuccess) return static_cast<int>(e);
   }
-  weighted_sum_kernel<<<1, 1024, 0, st>>>(p.row_loss, p.weights, p.B, p.loss);
-  return static_cast<int>(cudaGetLastError());
+  return static_cast<int>(launch_sum(p.row_loss, p.weights, p.B, p.loss, st));
 }
 
 // Workspace: RowStat[B], then double[2 P].
@@ -461,24 +853,25 @@ int launch_preference(const LossParams& p, const PrefParams& q, int dtype, qrita
   double* coef = reinterpret_cast<double*>(stats + p.B);
   cudaError_t e = cudaSuccess;
   if (p.B > 0) {
-    e = launch_rows<Op::kPrefStats, false>([&] { LossParams f = p; f.grad = nullptr; return f; }(), dtype, stats, st);
-    if (e != cudaSuccess) return static_cast<int>(e);
+    LossParams f = p;
+    f.grad = nullptr;
+    if ((e = launch_rows(f, dtype, kOpPrefStats, false, stats, st)) != cudaSuccess) return static_cast<int>(e);
     if (p.logp != nullptr) {
-      outside_kernel<<<static_cast<unsigned>((p.B + kLossThreads - 1) / kLossThreads), kLossThreads, 0, st>>>(q, p.B, p.logp);
-      if ((e = cudaGetLastError()) != cudaSuccess) return static_cast<int>(e);
+      const unsigned grid = static_cast<unsigned>((p.B + kLossThreads - 1) / kLossThreads);
+      if ((e = launch(&outside_kernel, grid, kLossThreads, 1u, st, q, p.B, p.logp)) != cudaSuccess)
+        return static_cast<int>(e);
     }
   }
   if (q.P > 0) {
-    pair_kernel<<<static_cast<unsigned>(q.P), kPairThreads, 0, st>>>(p, q, stats, coef);
-    if ((e = cudaGetLastError()) != cudaSuccess) return static_cast<int>(e);
+    e = launch(&pair_kernel, static_cast<unsigned>(q.P), kPairThreads, 1u, st, p, q, static_cast<const RowStat*>(stats), coef);
+    if (e != cudaSuccess) return static_cast<int>(e);
   }
-  weighted_sum_kernel<<<1, 1024, 0, st>>>(q.pair_loss, q.weights, q.P, p.loss);
-  if ((e = cudaGetLastError()) != cudaSuccess) return static_cast<int>(e);
+  if ((e = launch_sum(q.pair_loss, q.weights, q.P, p.loss, st)) != cudaSuccess) return static_cast<int>(e);
   if (p.B > 0 && p.grad != nullptr) {
-    const unsigned g = static_cast<unsigned>(p.B);
-    if (dtype == QRITA_DTYPE_F32) pref_grad_kernel<QRITA_DTYPE_F32><<<g, kLossThreads, 0, st>>>(p, q, stats, coef);
-    else pref_grad_kernel<QRITA_DTYPE_BF16><<<g, kLossThreads, 0, st>>>(p, q, stats, coef);
-    e = cudaGetLastError();
+    const uint32_t C = row_ctas(p, dtype, true);
+    const unsigned grid = static_cast<unsigned>(p.B * C);
+    auto* fn = dtype == QRITA_DTYPE_F32 ? &pref_grad_kernel<QRITA_DTYPE_F32> : &pref_grad_kernel<QRITA_DTYPE_BF16>;
+    e = launch(fn, grid, kLossThreads, 1u, st, p, q, static_cast<const RowStat*>(stats), static_cast<const double*>(coef), C);
   }
   return static_cast<int>(e);
 }
