@@ -195,6 +195,13 @@ int select_impl(const void* logits, int dtype, int64_t B, int64_t V, const int32
   return e == 0 ? QRITA_OK : QRITA_ECUDA;
 }
 
+dev::F2 pair_of(double v) {
+  dev::F2 r;
+  r.hi = static_cast<float>(v);
+  r.lo = std::isfinite(r.hi) ? static_cast<float>(v - r.hi) : 0.f;
+  return r;
+}
+
 // Arguments every loss entry point shares; fills the row part of *out.
 int loss_args(const void* logits, int dtype, int64_t B, int64_t V, int64_t ld, const uint8_t* mask,
               const int32_t* tokens, double inv_temperature, void* grad, int64_t ld_grad, LossParams* out) {
@@ -213,7 +220,11 @@ int loss_args(const void* logits, int dtype, int64_t B, int64_t V, int64_t ld, c
   out->mask = mask;
   out->tokens = tokens;
   out->c = c;
+  const double c_ln2 = static_cast<double>(c) * 0.69314718055994530942;
+  out->c_ln2 = static_cast<float>(c_ln2);
+  out->c_ln2_lo = static_cast<float>(c_ln2 - out->c_ln2);
   out->inv_t = static_cast<float>(inv_temperature);
+  out->inv_b = B > 0 ? static_cast<float>(1.0 / static_cast<double>(B)) : 0.f;
   out->grad = grad;
   out->ld_grad = ld_grad;
   if (B == 0) return QRITA_OK;
@@ -362,17 +373,21 @@ int qrita_policy_loss(const void* logits, int dtype, int64_t B, int64_t V, int64
   const int rc = qrita::loss_args(logits, dtype, B, V, ld, mask, tokens, inv_temperature, out_grad, ld_grad, &prm);
   if (rc != QRITA_OK) return rc;
   if (!(clip_low >= 0.0 && clip_low <= 1.0) || !(clip_high >= 0.0)) return QRITA_EINVAL;
-  if (!(kl_coef >= 0.0) || !std::isfinite(kl_coef) || !std::isfinite(entropy_coef)) return QRITA_EINVAL;
+  if (!(kl_coef >= 0.0) || !std::isfinite(static_cast<float>(kl_coef)) ||
+      !std::isfinite(static_cast<float>(entropy_coef)))
+    return QRITA_EINVAL;
   if (out_loss == nullptr) return QRITA_EINVAL;
   if (B > 0 && (advantages == nullptr || out_row_loss == nullptr)) return QRITA_EINVAL;
   prm.old_logp = old_logp;
   prm.ref_logp = ref_logp;
   prm.advantages = advantages;
   prm.weights = weights;
-  prm.clip_lo = 1.0 - clip_low;
-  prm.clip_hi = 1.0 + clip_high;
-  prm.kl_coef = kl_coef;
-  prm.entropy_coef = entropy_coef;
+  prm.clip_lo = static_cast<float>(1.0 - clip_low);
+  prm.clip_hi = static_cast<float>(1.0 + clip_high);
+  prm.ln_lo = qrita::pair_of(std::log(1.0 - clip_low));
+  prm.ln_hi = qrita::pair_of(std::log1p(clip_high));
+  prm.kl_coef = static_cast<float>(kl_coef);
+  prm.entropy_coef = static_cast<float>(entropy_coef);
   prm.grad_loss = grad_loss;
   prm.loss = out_loss;
   prm.row_loss = out_row_loss;

@@ -9,6 +9,14 @@
 
 namespace qrita {
 
+namespace dev {
+// An fp32 value in two parts: hi + lo with |lo| <= ulp(hi)/2.
+struct F2 {
+  float hi, lo;
+};
+}  // namespace dev
+
+
 // delta tables (Qrita technical summary, "Methodology", part 1: precomputed
 // tables from the normal quantile function, keyed on the target k or p).
 //   lut_k[i] = Phi^-1(1 - 2^(-i/4)),  i = 0..127  (keyed on u = alpha*k/V;
@@ -91,8 +99,10 @@ struct LossParams {
   int64_t B, V, ld;
   const uint8_t* mask;
   const int32_t* tokens;
-  float c;      // log2(e) * inv_temperature: weights are 2^(x c - shift)
+  float c;      // log2(e) * inv_temperature: weights are 2^((x - m) c)
+  float c_ln2, c_ln2_lo;  // c ln2 as a pair
   float inv_t;
+  float inv_b;  // 1 / B
   // outputs per row
   float* logp;
   float* entropy;
@@ -109,8 +119,9 @@ struct LossParams {
   const float* ref_logp;
   const float* advantages;
   const float* weights;
-  double clip_lo, clip_hi;  // 1 - clip_low, 1 + clip_high
-  double kl_coef, entropy_coef;
+  float clip_lo, clip_hi;  // 1 - clip_low, 1 + clip_high
+  dev::F2 ln_lo, ln_hi;    // their logarithms as pairs (-inf, inf: no clip)
+  float kl_coef, entropy_coef;
   float* loss;
 };
 

@@ -62,7 +62,7 @@ struct RowStat {
 struct Stat {
   float m;
   F2 s, t;
-};
+};  // (five words, in this order)
 
 // What one thread reads of a row besides its logits, before any of the row's
 // gradient is written (which may lie over the logits).
@@ -71,7 +71,7 @@ struct RowIn {
   float x_t;
   bool kept_t;
   float old_logp, ref_logp, adv;
-  double w;         // weight in the gradient: weights[row] * grad_loss
+  float w;          // weight in the gradient: weights[row] * grad_loss
   float g_logp, g_entropy;
 };
 
@@ -106,6 +106,13 @@ __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
       "fma.rn.f32x2 z, x, y, w;\n\tmov.b64 {%0, %1}, z;\n\t}"
       : "=f"(r.x), "=f"(r.y)
       : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return r;
+}
+
+// The largest of three, NaNs ignored, in one instruction.
+__device__ __forceinline__ float fmax3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
   return r;
 }
 
@@ -227,17 +234,15 @@ struct Running {
   float m = -INFINITY, ref = 0.f, s = 0.f, t = 0.f;
 
   __device__ __forceinline__ void raise(float x, float c) {
-    if (x > m) {
-      // before the first finite logit the sums are 0 (or NaN), whatever the factor
-      const float d = fmaxf((m - x) * c, kMinExp);
-      const float f = ex2(d);
-      if (ENT) t = (t + d * s) * f;
-      s *= f;
-      m = ref = x;
-    }
+    // before the first finite logit the sums are 0 (or NaN), whatever the factor
+    const float d = fmaxf((m - x) * c, kMinExp);
+    const float f = ex2(d);
+    if (ENT) t = (t + d * s) * f;
+    s *= f;
+    m = ref = x;
   }
   __device__ __forceinline__ void add_one(float x, float c) {
-    raise(x, c);
+    if (x > m) raise(x, c);
     const float y = (x - ref) * c;
     const float e = ex2(y);
     s += e;
@@ -246,10 +251,10 @@ struct Running {
   // N pairs: their own sum first, then one addition to the running one
   template <int N>
   __device__ __forceinline__ void add_unit(const float2 (&x)[N], float c) {
-    float top = fmaxf(x[0].x, x[0].y);
+    float top = m;
 #pragma unroll
-    for (int i = 1; i < N; ++i) top = fmaxf(top, fmaxf(x[i].x, x[i].y));
-    raise(top, c);
+    for (int i = 0; i < N; ++i) top = fmax3(top, x[i].x, x[i].y);
+    if (top > m) raise(top, c);
     const float2 nr = both(-ref), cc = both(c);
     float2 es[N], ts[N];
 #pragma unroll
@@ -284,51 +289,102 @@ __device__ __forceinline__ void stat_shift(Stat& a, float to, float c) {
   a.m = to;
 }
 
-// The block's sums from every thread's, valid in thread 0.
-template <bool ENT>
-__device__ __forceinline__ Stat block_stat(const Running<ENT>& r, float c, Stat* slots) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  float m = r.m;
+// The sum of a Stat over the first W lanes of a warp (a power of two), in
+// every one of those lanes.
+template <bool ENT, int W>
+__device__ __forceinline__ Stat lanes_stat(Stat v, float c) {
+  float m = v.m;
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kAll, m, o));
+  for (int o = W / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kAll, m, o));
+  stat_shift<ENT>(v, m, c);
+#pragma unroll
+  for (int o = W / 2; o > 0; o >>= 1) {
+    v.s = f2_merge(v.s, f2_make(__shfl_xor_sync(kAll, v.s.hi, o), __shfl_xor_sync(kAll, v.s.lo, o)));
+    if (ENT) v.t = f2_merge(v.t, f2_make(__shfl_xor_sync(kAll, v.t.hi, o), __shfl_xor_sync(kAll, v.t.lo, o)));
+  }
+  return v;
+}
+
+constexpr int kMaxRanks = 16;
+
+// The row's sums from every thread's of its cluster of C CTAs, valid in the
+// first warp of every CTA: warps, then the CTA, then the cluster through
+// distributed shared memory (each CTA stores its record into all of them).
+template <bool ENT>
+__device__ __forceinline__ Stat row_stat(const Running<ENT>& r, float c, uint32_t rank, uint32_t C, Stat* slots,
+                                         Stat (*ranks)) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   Stat v;
   v.m = r.m;
   v.s = f2_make(r.s, 0.f);
   v.t = f2_make(r.t, 0.f);
-  stat_shift<ENT>(v, m, c);
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    v.s = f2_merge(v.s, f2_make(__shfl_xor_sync(kAll, v.s.hi, o), __shfl_xor_sync(kAll, v.s.lo, o)));
-    if (ENT) v.t = f2_merge(v.t, f2_make(__shfl_xor_sync(kAll, v.t.hi, o), __shfl_xor_sync(kAll, v.t.lo, o)));
-  }
+  v = lanes_stat<ENT, 32>(v, c);
   if (lane == 0) slots[warp] = v;
   __syncthreads();
-  if (threadIdx.x == 0) {
-    for (int w = 1; w < kLossWarps; ++w) m = fmaxf(m, slots[w].m);
-    stat_shift<ENT>(v, m, c);
-    for (int w = 1; w < kLossWarps; ++w) {
-      Stat o = slots[w];
-      stat_shift<ENT>(o, m, c);
-      v.s = f2_merge(v.s, o.s);
-      if (ENT) v.t = f2_merge(v.t, o.t);
+  if (warp == 0) v = lanes_stat<ENT, kLossWarps>(slots[lane & (kLossWarps - 1)], c);
+  if (C > 1) {
+    cluster_wait();  // (every CTA of the cluster is running)
+    if (warp == 0 && static_cast<uint32_t>(lane) < C) {
+      const uint32_t at = map_rank(smem_u32(&ranks[rank]), lane);
+      const float rec[5] = {v.m, v.s.hi, v.s.lo, v.t.hi, v.t.lo};
+#pragma unroll
+      for (int i = 0; i < (ENT ? 5 : 3); ++i) st_dsmem_u32(at + 4 * i, __float_as_uint(rec[i]));
+    }
+    cluster_sync_all();
+    if (warp == 0) {
+      v = ranks[lane & (kMaxRanks - 1)];
+      if ((lane & (kMaxRanks - 1)) >= static_cast<int>(C)) {
+        v.m = -INFINITY;
+        v.s = v.t = f2_make(0.f, 0.f);
+      }
+      v = lanes_stat<ENT, kMaxRanks>(v, c);
     }
   }
   return v;
 }
 
+// ln of a pair >= 2^-126, as a pair: off by about 2^-25 absolutely beside the
+// relative error of the pair itself. S = 2^e f with f in [0.7, 1.42):
+// e ln2 is exact in its leading part (12 bits of ln2), ln f is below 0.36.
+__device__ __forceinline__ F2 ln_pair(F2 s) {
+  const uint32_t b = __float_as_uint(s.hi);
+  int e = static_cast<int>(b >> 23) - 127;
+  float f = __uint_as_float((b & 0x007FFFFFu) | 0x3F800000u);
+  if (f > 1.41f) {
+    f *= 0.5f;
+    ++e;
+  }
+  const float n = static_cast<float>(e);
+  const float rest = logf(f) + fmaf(n, 1.42860682e-6f, s.lo / s.hi);  // ln2 - 0.693145752
+  return f2_merge(f2_make(n * 0.693145752f, 0.f), f2_make(rest, 0.f));
+}
+
+// a > b for pairs in normal form (infinities included).
+__device__ __forceinline__ bool pair_above(F2 a, F2 b) { return a.hi != b.hi ? a.hi > b.hi : a.lo > b.lo; }
+
+// e^q - 1 - q: its power series where the difference would lose digits (12
+// terms leave less than 2^-26 of it for |q| <= 1).
+__device__ __forceinline__ float exp_minus_tangent(float q) {
+  if (fabsf(q) > 1.f) return expm1f(q) - q;
+  float r = 1.f;
+#pragma unroll
+  for (int n = 13; n >= 3; --n) r = fmaf(r, q / static_cast<float>(n), 1.f);
+  return 0.5f * q * q * r;
+}
+
 // A, Hc and the token's entry from the weights a, h of dlogp and dH.
-__device__ __forceinline__ RowGrad row_grad(double a, double h, double logp, double H, double ln_s, float m, double s,
+__device__ __forceinline__ RowGrad row_grad(float a, float h, float logp, float H, float ln_s, float m, float s,
                                             float inv_t) {
   RowGrad g;
   g.m = m;
   g.a = g.h = g.at = 0.f;
-  if (a == 0.0 && h == 0.0) return g;  // (NaN weights go on)
-  const double k = -static_cast<double>(inv_t) / s;
-  g.a = static_cast<float>(k * (a + (h != 0.0 ? h * (H - ln_s) : 0.0)));
-  g.h = static_cast<float>(k * h * kLn2);
-  double at = a * -expm1(logp);
-  if (h != 0.0 && logp > -INFINITY) at -= h * exp(logp) * (logp + H);
-  g.at = static_cast<float>(inv_t * at);
+  if (a == 0.f && h == 0.f) return g;  // (NaN weights go on)
+  const float k = -inv_t / s;
+  g.a = k * (a + (h != 0.f ? h * (H - ln_s) : 0.f));
+  g.h = k * (h * static_cast<float>(kLn2));
+  float at = a * -expm1f(logp);
+  if (h != 0.f && logp > -INFINITY) at -= h * expf(logp) * (logp + H);
+  g.at = inv_t * at;
   return g;
 }
 
@@ -339,7 +395,7 @@ __device__ __forceinline__ RowIn row_in(const LossParams& p, int op, int64_t row
   in.x_t = Elem<DT>::load(static_cast<const unsigned char*>(p.logits) + row * p.ld * Elem<DT>::kBytes, token);
   in.kept_t = p.mask == nullptr || p.mask[row * p.V + token] != 0;
   in.old_logp = in.ref_logp = in.adv = in.g_logp = in.g_entropy = 0.f;
-  in.w = 0.0;
+  in.w = 0.f;
   if (op == kOpGrad) {
     if (p.g_logp != nullptr) in.g_logp = p.g_logp[row];
     if (p.g_entropy != nullptr) in.g_entropy = p.g_entropy[row];
@@ -347,66 +403,84 @@ __device__ __forceinline__ RowIn row_in(const LossParams& p, int op, int64_t row
     if (p.old_logp != nullptr) in.old_logp = p.old_logp[row];
     if (p.ref_logp != nullptr) in.ref_logp = p.ref_logp[row];
     in.adv = p.advantages[row];
-    in.w = (p.weights != nullptr ? p.weights[row] : 1.0 / static_cast<double>(p.B)) *
-           (p.grad_loss != nullptr ? *p.grad_loss : 1.0);
+    in.w = p.weights != nullptr ? p.weights[row] : p.inv_b;
+    if (p.grad_loss != nullptr) in.w *= *p.grad_loss;
   }
   return in;
 }
 
 // Everything a row gives besides its gradient's entries. `out`: this thread
-// writes the row's values.
+// writes the row's values. logp is a pair, so that ratios and their clip are
+// decided on more than fp32 has of a logp near -20; fp64 would take this one
+// thread longer than the row's whole pass (a function is hundreds of
+// dependent instructions on a narrow pipe).
 template <bool ENT>
 __device__ __forceinline__ RowGrad row_scalars(const LossParams& p, int op, RowStat* stats, int64_t row, const RowIn& in,
                                                const Stat& st, bool out) {
   RowGrad g;
   g.m = st.m;
   g.a = g.h = g.at = 0.f;
-  const double S = static_cast<double>(st.s.hi) + st.s.lo;
-  const bool empty = S == 0.0;  // nothing kept, or only -inf
-  const double log2_s = empty ? 0.0 : log2(S);
-  double logp = -INFINITY;
-  if (in.kept_t && !empty) logp = ((static_cast<double>(in.x_t) - st.m) * p.c - log2_s) * kLn2;
-  const double H = ENT && !empty ? (log2_s - (static_cast<double>(st.t.hi) + st.t.lo) / S) * kLn2 : 0.0;
-  const bool joins = logp != -INFINITY;  // (NaN joins)
+  const float S = st.s.hi;
+  const bool empty = S == 0.f;  // nothing kept, or only -inf
+  const F2 ln_s = empty ? f2_make(0.f, 0.f) : ln_pair(st.s);
+  // T / S ln2: the mean of log p_j + ln S
+  const float mean = ENT && !empty ? f2_float(st.t) / S * static_cast<float>(kLn2) : 0.f;
+  F2 logp = f2_make(-INFINITY, 0.f);
+  if (in.kept_t && !empty) {
+    F2 d;
+    two_sum(in.x_t, -st.m, d.hi, d.lo);
+    if (fabsf(d.hi) < 1e30f) {
+      F2 y = f2_mul(d, p.c_ln2);  // (x_t - m) c ln2
+      y.lo = fmaf(d.hi, p.c_ln2_lo, y.lo);
+      logp = f2_sub(y, ln_s);
+    } else {
+      logp.hi = d.hi * p.c_ln2 - ln_s.hi;  // no digit of ln S counts (or -inf, or NaN)
+    }
+  }
+  const float lp = f2_float(logp);
+  const float H = ENT && !empty ? f2_float(f2_sub(ln_s, f2_make(mean, 0.f))) : 0.f;
+  const bool joins = lp != -INFINITY;  // (NaN joins)
   if (out) {
-    if (p.logp != nullptr) p.logp[row] = static_cast<float>(logp);
-    if (ENT && p.entropy != nullptr) p.entropy[row] = static_cast<float>(H);
+    if (p.logp != nullptr) p.logp[row] = lp;
+    if (ENT && p.entropy != nullptr) p.entropy[row] = H;
   }
   if (op == kOpGrad) {
-    g = row_grad(joins ? in.g_logp : 0.0, ENT && !empty ? in.g_entropy : 0.0, logp, H, log2_s * kLn2, st.m, S, p.inv_t);
+    g = row_grad(joins ? in.g_logp : 0.f, ENT && !empty ? in.g_entropy : 0.f, lp, H, ln_s.hi, st.m, S, p.inv_t);
   } else if (op == kOpPolicy) {
-    double loss = 0.0, kl = 0.0;
+    float loss = 0.f, kl = 0.f;
     if (joins) {
-      const double adv = in.adv;
-      const double rho = p.old_logp != nullptr ? exp(logp - in.old_logp) : 1.0;
-      const double near = fmin(fmax(rho, p.clip_lo), p.clip_hi);
-      loss = fmax(-adv * rho, -adv * near);
-      if (rho != rho || logp != logp) loss = logp + rho;  // NaN goes through fmin and fmax unseen
-      const bool bound = (adv > 0.0 && rho > p.clip_hi) || (adv < 0.0 && rho < p.clip_lo);
-      double a = bound ? 0.0 : -adv * rho;
-      if (logp != logp) a = logp;
+      const float adv = in.adv;
+      F2 d = f2_make(0.f, 0.f);  // ln rho
+      if (p.old_logp != nullptr)
+        d = isinf(in.old_logp) ? f2_make(-in.old_logp, 0.f) : f2_sub(logp, f2_make(in.old_logp, 0.f));
+      const float rho = expf(d.hi) * (1.f + d.lo);
+      // rho against the clip, on the logarithms
+      const bool over = pair_above(d, p.ln_hi), under = pair_above(p.ln_lo, d);
+      const bool bound = (adv > 0.f && over) || (adv < 0.f && under);
+      loss = -adv * (bound ? (over ? p.clip_hi : p.clip_lo) : rho);
+      float a = bound ? 0.f : -adv * rho;
+      if (lp != lp) loss = a = lp;
       if (p.ref_logp != nullptr) {
-        const double q = in.ref_logp - logp;
-        const double eq = expm1(q);
-        kl = eq - q;
-        if (p.kl_coef != 0.0) {
-          loss += p.kl_coef * kl;
-          a -= p.kl_coef * eq;
+        const float q = (in.ref_logp - logp.hi) - logp.lo;
+        kl = exp_minus_tangent(q);
+        if (p.kl_coef != 0.f) {
+          loss = fmaf(p.kl_coef, kl, loss);
+          a = fmaf(-p.kl_coef, expm1f(q), a);
         }
       }
-      if (ENT) loss -= p.entropy_coef * H;
+      if (ENT) loss = fmaf(-p.entropy_coef, H, loss);
       if (p.grad != nullptr)
-        g = row_grad(in.w * a, ENT ? -p.entropy_coef * in.w : 0.0, logp, H, log2_s * kLn2, st.m, S, p.inv_t);
+        g = row_grad(in.w * a, ENT ? -p.entropy_coef * in.w : 0.f, lp, H, ln_s.hi, st.m, S, p.inv_t);
     }
     if (out) {
-      p.row_loss[row] = static_cast<float>(loss);
-      if (p.kl != nullptr) p.kl[row] = static_cast<float>(kl);
+      p.row_loss[row] = loss;
+      if (p.kl != nullptr) p.kl[row] = kl;
     }
   } else if (op == kOpPrefStats && out) {
     RowStat o;
-    o.logp = logp;
+    o.logp = static_cast<double>(logp.hi) + logp.lo;
     o.m = st.m;
-    o.s = joins ? static_cast<float>(S) : -1.f;
+    o.s = joins ? S : -1.f;
     stats[row] = o;
   }
   return g;
@@ -520,20 +594,16 @@ __device__ __forceinline__ void write_grad(const LossParams& p, const Share<DT>&
   }
 }
 
-// The record a CTA of a cluster gives the others.
-constexpr int kMaxRanks = 16;
-constexpr int kStatWords = 5;
-
-// A cluster of C CTAs per row: the softmax sums of every CTA's share in one
-// pass, merged through distributed shared memory; the row's values (rank 0
-// writes them); and a second pass over the share for the gradient, whose
-// reads come from L2.
+// A cluster of C CTAs per row, in one pass over HBM for the sums: each CTA
+// streams its share of the row, the shares merge through distributed shared
+// memory, and rank 0 writes the row's values. A gradient takes a second pass
+// over the share.
 template <int DT, bool ENT, bool MASKED>
 __global__ void __launch_bounds__(kLossThreads, 4) row_kernel(const LossParams p, RowStat* stats, int op, uint32_t C) {
   using E = Elem<DT>;
   constexpr int N = E::kUnit / 2;
   __shared__ Stat slots[kLossWarps];
-  __shared__ float ranks[kMaxRanks][kStatWords];
+  __shared__ Stat ranks[kMaxRanks];
   __shared__ RowGrad grad;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -551,68 +621,193 @@ __global__ void __launch_bounds__(kLossThreads, 4) row_kernel(const LossParams p
   RowIn in;
   if (threadIdx.x == 0) in = row_in<DT>(p, op, row, token);
   Running<ENT> run;
-  for (int64_t u0 = sh.u_lo + threadIdx.x; u0 < sh.u_hi; u0 += kLossThreads * kUnroll) {
+  auto add = [&](uint4 w, uint32_t bits) {
+    float2 x[N];
+    E::unpack(w, x);
+    if (MASKED) {
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        if (!(bits >> (2 * i) & 1u)) x[i].x = -INFINITY;
+        if (!(bits >> (2 * i + 1) & 1u)) x[i].y = -INFINITY;
+      }
+    }
+    run.add_unit(x, p.c);
+  };
+  int64_t u0 = sh.u_lo + threadIdx.x;
+  // whole steps of the block first: no unit of theirs needs a check
+  for (int64_t full = sh.u_lo + (sh.u_hi - sh.u_lo) / (kLossThreads * kUnroll) * (kLossThreads * kUnroll); u0 < full;
+       u0 += kLossThreads * kUnroll) {
     uint4 w[kUnroll];
     uint32_t bits[kUnroll];
+    if (MASKED) {
 #pragma unroll
-    for (int k = 0; k < kUnroll; ++k) {
-      const int64_t u = u0 + k * kLossThreads;
-      bits[k] = u < sh.u_hi ? (MASKED ? sh.kept(u) : 1u) : 0u;
+      for (int k = 0; k < kUnroll; ++k) bits[k] = sh.kept(u0 + k * kLossThreads);
     }
 #pragma unroll
     for (int k = 0; k < kUnroll; ++k)
-      if (bits[k] != 0u) w[k] = load_unit(sh.unit(u0 + k * kLossThreads));
+      if (!MASKED || bits[k] != 0u) w[k] = load_unit(sh.unit(u0 + k * kLossThreads));
 #pragma unroll
-    for (int k = 0; k < kUnroll; ++k) {
-      if (bits[k] == 0u) continue;
-      float2 x[N];
-      E::unpack(w[k], x);
-      if (MASKED) {
-#pragma unroll
-        for (int i = 0; i < N; ++i) {
-          if (!(bits[k] >> (2 * i) & 1u)) x[i].x = -INFINITY;
-          if (!(bits[k] >> (2 * i + 1) & 1u)) x[i].y = -INFINITY;
-        }
-      }
-      run.add_unit(x, p.c);
-    }
+    for (int k = 0; k < kUnroll; ++k)
+      if (!MASKED || bits[k] != 0u) add(w[k], bits[k]);
+  }
+  for (; u0 < sh.u_hi; u0 += kLossThreads) {
+    const uint32_t bits = MASKED ? sh.kept(u0) : 1u;
+    if (bits != 0u) add(load_unit(sh.unit(u0)), bits);
   }
   if (sh.ends && threadIdx.x < Share<DT>::kEnds) {
     const int64_t j = sh.end_index(threadIdx.x);
     if (j >= 0 && (!MASKED || sh.mask[j] != 0)) run.add_one(E::load(sh.x, j), p.c);
   }
-  Stat st = block_stat<ENT>(run, p.c, slots);
-  if (C > 1) {
-    cluster_wait();
-    if (threadIdx.x == 0) {
-      const float rec[kStatWords] = {st.m, st.s.hi, st.s.lo, st.t.hi, st.t.lo};
-      for (uint32_t r = 0; r < C; ++r) {
-        const uint32_t at = map_rank(smem_u32(&ranks[rank][0]), r);
-#pragma unroll
-        for (int i = 0; i < (ENT ? 5 : 3); ++i) st_dsmem_u32(at + 4 * i, __float_as_uint(rec[i]));
-      }
-    }
-    cluster_sync_all();
-    if (threadIdx.x == 0) {
-      st.m = -INFINITY;
-      for (uint32_t r = 0; r < C; ++r) st.m = fmaxf(st.m, ranks[r][0]);
-      st.s = st.t = f2_make(0.f, 0.f);
-      for (uint32_t r = 0; r < C; ++r) {
-        Stat o;
-        o.m = ranks[r][0];
-        o.s = f2_make(ranks[r][1], ranks[r][2]);
-        o.t = ENT ? f2_make(ranks[r][3], ranks[r][4]) : f2_make(0.f, 0.f);
-        stat_shift<ENT>(o, st.m, p.c);
-        st.s = f2_merge(st.s, o.s);
-        if (ENT) st.t = f2_merge(st.t, o.t);
-      }
-    }
-  }
+  const Stat st = row_stat<ENT>(run, p.c, rank, C, slots, ranks);
   if (threadIdx.x == 0 && (rank == 0 || p.grad != nullptr)) grad = row_scalars<ENT>(p, op, stats, row, in, st, rank == 0);
   if (p.grad == nullptr) return;
   __syncthreads();
   g = grad;
   write_grad<DT, ENT, MASKED>(p, sh, row, g, MASKED && sh.mask[token] == 0 ? -1 : token);
+}
+
+// The same with the CTA's share of the row held in shared memory from the
+// sums to the gradient, so that HBM is read once and written once. The share
+// arrives as bulk copies (TMA) of kPiece bytes, all in flight from the start,
+// and is summed as it lands; several CTAs on an SM overlap one's merge with
+// others' copies and stores.
+constexpr int kPiece = 16 * 1024;
+constexpr int kPieceUnits = kPiece / 16;
+constexpr int kMaxPieces = 14;
+constexpr uint64_t kCopyLimitNs = 200ull * 1000 * 1000;
+
+template <int DT, bool ENT>
+__global__ void __launch_bounds__(kLossThreads, 3) resident_kernel(const LossParams p, int op, uint32_t C) {
+  using E = Elem<DT>;
+  constexpr int N = E::kUnit / 2;
+  extern __shared__ __align__(128) uint4 units[];
+  __shared__ __align__(8) uint64_t bars[kMaxPieces];
+  __shared__ Stat slots[kLossWarps];
+  __shared__ Stat ranks[kMaxRanks];
+  __shared__ RowGrad grad;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const uint32_t rank = C > 1 ? cluster_rank() : 0u;
+  const int64_t row = blockIdx.x / C;
+  const Share<DT> sh(p, row, rank, C);
+  const int64_t token = p.tokens[row];
+  RowGrad g = {0.f, 0.f, 0.f, 0.f};
+  if (token < 0 || token >= p.V) {  // (the same in every CTA of the cluster)
+    if (threadIdx.x == 0 && rank == 0) row_ignored(p, op, nullptr, row);
+    write_grad<DT, ENT, false>(p, sh, row, g, -1);
+    return;
+  }
+  if (C > 1) cluster_arrive_relaxed();  // every CTA of the cluster runs before its memory is written
+  const int n = static_cast<int>(sh.u_hi - sh.u_lo);
+  const int pieces = (n + kPieceUnits - 1) / kPieceUnits;
+  const unsigned char* src = static_cast<const unsigned char*>(sh.unit(sh.u_lo));
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < pieces; ++i) mbar_init(smem_u32(&bars[i]), 1);
+    fence_mbar_init();
+    for (int i = 0; i < pieces; ++i) {
+      const uint32_t bytes = static_cast<uint32_t>(min(kPieceUnits, n - i * kPieceUnits)) * 16u;
+      mbar_expect_tx(smem_u32(&bars[i]), bytes);
+      bulk_g2s(smem_u32(units + i * kPieceUnits), src + static_cast<int64_t>(i) * kPiece, bytes, smem_u32(&bars[i]));
+    }
+  }
+  RowIn in;
+  if (threadIdx.x == 0) in = row_in<DT>(p, op, row, token);
+  float end_x = 0.f;
+  int64_t end_j = -1;
+  if (sh.ends && threadIdx.x < Share<DT>::kEnds) end_j = sh.end_index(threadIdx.x);
+  if (end_j >= 0) end_x = E::load(sh.x, end_j);
+  __syncthreads();  // the barriers are initialised
+  Running<ENT> run;
+  bool landed = true;
+  for (int i = 0; i < pieces; ++i) {
+    // a copy that never lands (not expected on a healthy device) gives a row
+    // of NaN instead of a hang
+    landed = landed && mbar_wait_bounded(smem_u32(&bars[i]), 0, kCopyLimitNs);
+    if (!landed) break;
+    const uint4* at = units + i * kPieceUnits + threadIdx.x;
+    const int left = n - i * kPieceUnits;
+    if (left >= kPieceUnits) {
+      uint4 w[kUnroll];
+#pragma unroll
+      for (int k = 0; k < kUnroll; ++k) w[k] = at[k * kLossThreads];
+#pragma unroll
+      for (int k = 0; k < kUnroll; ++k) {
+        float2 x[N];
+        E::unpack(w[k], x);
+        run.add_unit(x, p.c);
+      }
+    } else {
+      for (int u = threadIdx.x; u < left; u += kLossThreads, at += kLossThreads) {
+        float2 x[N];
+        E::unpack(*at, x);
+        run.add_unit(x, p.c);
+      }
+    }
+  }
+  if (end_j >= 0) run.add_one(end_x, p.c);
+  if (!landed) run.s = run.t = NAN;
+  const Stat st = row_stat<ENT>(run, p.c, rank, C, slots, ranks);
+  if (threadIdx.x == 0) grad = row_scalars<ENT>(p, op, nullptr, row, in, st, rank == 0);
+  __syncthreads();
+  g = grad;
+  unsigned char* grow = static_cast<unsigned char*>(p.grad) + row * p.ld_grad * E::kBytes;
+  unsigned char* gu = grow + (sh.head + sh.u_lo * E::kUnit) * E::kBytes;
+  if (!landed) {
+    // (bounded) the copies in flight end before this CTA's memory is given up
+    for (int i = 0; i < pieces; ++i) (void)mbar_wait_bounded(smem_u32(&bars[i]), 0, kCopyLimitNs);
+  }
+  const float2 nm = both(-g.m), cc = both(p.c), aa = both(g.a), hh = both(g.h);
+  const bool zero = g.a == 0.f && g.h == 0.f;
+  auto entries = [&](uint4 w, float2 (&v)[N]) {
+    float2 x[N];
+    E::unpack(w, x);
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const float2 y = mul2(add2(x[i], nm), cc);
+      const float2 e = make_float2(ex2(y.x), ex2(y.y));
+      v[i] = ENT ? mul2(e, fma2(hh, make_float2(y.x < kMinExp ? kMinExp : y.x, y.y < kMinExp ? kMinExp : y.y), aa))
+                 : mul2(e, aa);
+      if (zero) v[i] = both(0.f);
+    }
+  };
+  if ((reinterpret_cast<uintptr_t>(gu) & 15u) == 0) {
+    uint4* out = reinterpret_cast<uint4*>(gu);
+    int u = threadIdx.x;
+    for (; u + (kUnroll - 1) * kLossThreads < n; u += kUnroll * kLossThreads) {
+      uint4 w[kUnroll];
+#pragma unroll
+      for (int k = 0; k < kUnroll; ++k) w[k] = units[u + k * kLossThreads];
+#pragma unroll
+      for (int k = 0; k < kUnroll; ++k) {
+        float2 v[N];
+        entries(w[k], v);
+        out[u + k * kLossThreads] = E::pack(v);
+      }
+    }
+    for (; u < n; u += kLossThreads) {
+      float2 v[N];
+      entries(units[u], v);
+      out[u] = E::pack(v);
+    }
+  } else {
+    // gradient rows aligned otherwise than the logits': entry by entry
+    for (int u = threadIdx.x; u < n; u += kLossThreads) {
+      float2 v[N];
+      entries(units[u], v);
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        E::store(gu, static_cast<int64_t>(u) * E::kUnit + 2 * i, v[i].x);
+        E::store(gu, static_cast<int64_t>(u) * E::kUnit + 2 * i + 1, v[i].y);
+      }
+    }
+  }
+  if (end_j >= 0) E::store(grow, end_j, zero ? 0.f : grad_one<ENT>(end_x, g, p.c));
+  const int64_t u = (token - sh.head) / E::kUnit;  // (token < head: 0 or below, an end)
+  const bool end = token < sh.head || u >= sh.nu;
+  if (end ? sh.ends : (u >= sh.u_lo && u < sh.u_hi)) {
+    __syncthreads();
+    if (threadIdx.x == 0) E::store(grow, token, g.at);
+  }
 }
 
 // out = sum of w[i] v[i] in one fixed order, in fp64 (w NULL: 1 / n).
@@ -735,7 +930,7 @@ __global__ void __launch_bounds__(kLossThreads, 4) pref_grad_kernel(const LossPa
       const RowStat st = stats[row];
       if (!(st.s < 0.f)) {
         token = p.tokens[row];
-        g = row_grad(coef[s], 0.0, st.logp, 0.0, 0.0, st.m, st.s, p.inv_t);
+        g = row_grad(static_cast<float>(coef[s]), 0.f, static_cast<float>(st.logp), 0.f, 0.f, st.m, st.s, p.inv_t);
       }
     }
     grad = g;
@@ -773,7 +968,7 @@ uint32_t row_ctas(const LossParams& p, int dtype, bool second_pass) {
 }
 
 template <typename F, typename... Args>
-cudaError_t launch(F* fn, unsigned grid, unsigned block, unsigned cluster, cudaStream_t st, Args... args) {
+cudaError_t launch(F* fn, unsigned grid, unsigned block, unsigned cluster, cudaStream_t st, size_t smem, Args... args) {
   if (cluster > 8) {
     const cudaError_t e =
         cudaFuncSetAttribute(reinterpret_cast<const void*>(fn), cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
@@ -782,6 +977,7 @@ cudaError_t launch(F* fn, unsigned grid, unsigned block, unsigned cluster, cudaS
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(grid, 1, 1);
   cfg.blockDim = dim3(block, 1, 1);
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
   cudaLaunchAttribute attr[2];
   // the CTAs may be scheduled while the previous kernel of the stream drains;
@@ -799,12 +995,38 @@ cudaError_t launch(F* fn, unsigned grid, unsigned block, unsigned cluster, cudaS
   return e != cudaSuccess ? e : last;
 }
 
+// Dynamic shared memory of resident_kernel for C CTAs a row.
+size_t resident_bytes(const LossParams& p, int dtype, uint32_t C) {
+  const int64_t unit = dtype == QRITA_DTYPE_F32 ? 4 : 8;
+  return static_cast<size_t>((p.V / unit + C - 1) / C) * 16;
+}
+
+// The most shared memory a share may take: three CTAs on an SM.
+constexpr size_t kResidentMost = 72 * 1024;
+
+template <int DT, bool ENT>
+cudaError_t launch_resident(const LossParams& p, int op, uint32_t C, cudaStream_t st) {
+  const size_t smem = resident_bytes(p, DT, C);
+  auto* fn = &resident_kernel<DT, ENT>;
+  if (smem > 40 * 1024) {  // beyond what a kernel has without asking
+    const cudaError_t e = cudaFuncSetAttribute(reinterpret_cast<const void*>(fn),
+                                               cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    if (e != cudaSuccess) return e;
+  }
+  return launch(fn, static_cast<unsigned>(p.B * C), kLossThreads, C, st, smem, p, op, C);
+}
+
 template <int DT, bool ENT>
 cudaError_t launch_rows_of(const LossParams& p, int op, RowStat* stats, cudaStream_t st) {
+  if (p.grad != nullptr && p.mask == nullptr) {
+    uint32_t C = row_ctas(p, DT, false);
+    while (C < kMaxRanks && resident_bytes(p, DT, C) > kResidentMost && p.B * 2 * C <= INT32_MAX) C *= 2;
+    if (resident_bytes(p, DT, C) <= kResidentMost) return launch_resident<DT, ENT>(p, op, C, st);
+  }
   const uint32_t C = row_ctas(p, DT, p.grad != nullptr);
   const unsigned grid = static_cast<unsigned>(p.B * C);
-  return p.mask != nullptr ? launch(&row_kernel<DT, ENT, true>, grid, kLossThreads, C, st, p, stats, op, C)
-                           : launch(&row_kernel<DT, ENT, false>, grid, kLossThreads, C, st, p, stats, op, C);
+  return p.mask != nullptr ? launch(&row_kernel<DT, ENT, true>, grid, kLossThreads, C, st, size_t(0), p, stats, op, C)
+                           : launch(&row_kernel<DT, ENT, false>, grid, kLossThreads, C, st, size_t(0), p, stats, op, C);
 }
 
 cudaError_t launch_rows(const LossParams& p, int dtype, int op, bool ent, RowStat* stats, cudaStream_t st) {
@@ -816,7 +1038,7 @@ cudaError_t launch_rows(const LossParams& p, int dtype, int op, bool ent, RowSta
 }
 
 cudaError_t launch_sum(const float* v, const float* w, int64_t n, float* out, cudaStream_t st) {
-  return launch(&weighted_sum_kernel, 1u, 1024u, 1u, st, v, w, n, out);
+  return launch(&weighted_sum_kernel, 1u, 1024u, 1u, st, size_t(0), v, w, n, out);
 }
 
 }  // namespace
@@ -858,12 +1080,12 @@ int launch_preference(const LossParams& p, const PrefParams& q, int dtype, qrita
     if ((e = launch_rows(f, dtype, kOpPrefStats, false, stats, st)) != cudaSuccess) return static_cast<int>(e);
     if (p.logp != nullptr) {
       const unsigned grid = static_cast<unsigned>((p.B + kLossThreads - 1) / kLossThreads);
-      if ((e = launch(&outside_kernel, grid, kLossThreads, 1u, st, q, p.B, p.logp)) != cudaSuccess)
+      if ((e = launch(&outside_kernel, grid, kLossThreads, 1u, st, size_t(0), q, p.B, p.logp)) != cudaSuccess)
         return static_cast<int>(e);
     }
   }
   if (q.P > 0) {
-    e = launch(&pair_kernel, static_cast<unsigned>(q.P), kPairThreads, 1u, st, p, q, static_cast<const RowStat*>(stats), coef);
+    e = launch(&pair_kernel, static_cast<unsigned>(q.P), kPairThreads, 1u, st, size_t(0), p, q, static_cast<const RowStat*>(stats), coef);
     if (e != cudaSuccess) return static_cast<int>(e);
   }
   if ((e = launch_sum(q.pair_loss, q.weights, q.P, p.loss, st)) != cudaSuccess) return static_cast<int>(e);
@@ -871,7 +1093,7 @@ int launch_preference(const LossParams& p, const PrefParams& q, int dtype, qrita
     const uint32_t C = row_ctas(p, dtype, true);
     const unsigned grid = static_cast<unsigned>(p.B * C);
     auto* fn = dtype == QRITA_DTYPE_F32 ? &pref_grad_kernel<QRITA_DTYPE_F32> : &pref_grad_kernel<QRITA_DTYPE_BF16>;
-    e = launch(fn, grid, kLossThreads, 1u, st, p, q, static_cast<const RowStat*>(stats), static_cast<const double*>(coef), C);
+    e = launch(fn, grid, kLossThreads, 1u, st, size_t(0), p, q, static_cast<const RowStat*>(stats), static_cast<const double*>(coef), C);
   }
   return static_cast<int>(e);
 }
