@@ -7,7 +7,6 @@ the losses runs in the library's CUDA kernels. PyTorch provides device memory an
 
 from __future__ import annotations
 
-import contextlib
 import ctypes
 from collections import namedtuple
 
@@ -82,10 +81,16 @@ def version() -> int:
     return int(lib().qrita_version())
 
 
-def _torch():
-    import torch
+_torch_module = None
 
-    return torch
+
+def _torch():
+    global _torch_module
+    if _torch_module is None:
+        import torch
+
+        _torch_module = torch
+    return _torch_module
 
 
 def _dtype_code(t) -> int:
@@ -317,10 +322,8 @@ PolicyLoss = namedtuple("PolicyLoss", "loss grad row_loss logp kl entropy")
 PreferenceLoss = namedtuple("PreferenceLoss", "loss grad pair_loss log_ratio seq_logp logp")
 
 
-def _ptr(t) -> ctypes.c_void_p:
-    return ctypes.c_void_p(t.data_ptr() if t is not None and t.numel() else 0)
-
-
+# (These calls take 3 to 10 us on the GPU for a small batch, so what they do on
+# the host is kept short: plain integers as pointers, one test per property.)
 def _padded_rows(t, name="logits"):
     """B, V and the leading dimension of [B, V] rows that may be padded."""
     if t.dim() != 2:
@@ -328,63 +331,66 @@ def _padded_rows(t, name="logits"):
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
     B, V = t.shape
-    ld = t.stride(0) if B > 1 else V
-    if V < 1 or (B > 0 and ((V > 1 and t.stride(1) != 1) or ld < V)):
+    ld, unit = t.stride()
+    if B < 2:
+        ld = V
+    if V < 1 or (B > 0 and ((V > 1 and unit != 1) or ld < V)):
         raise ValueError(f"{name} must be row-major: unit stride within a row, a leading dimension of at least V")
     return B, V, ld
 
 
-def _keep_mask(mask, B, V, device):
-    torch = _torch()
-    if mask is not None and (mask.shape != (B, V) or mask.dtype not in (torch.bool, torch.uint8) or not mask.is_contiguous()
-                             or mask.device != device):
-        raise ValueError("mask must be a contiguous bool/uint8 [B, V] tensor on the logits' device")
-    return mask
+def _at(t, n, dtype, name, device):
+    """Address of a contiguous vector of n elements; 0 for None or an empty one."""
+    if t is None:
+        return 0
+    if not isinstance(t, _torch().Tensor) or t.dtype is not dtype or t.numel() != n or not t.is_contiguous() or t.device != device:
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of {n} elements on {device}")
+    return t.data_ptr()
 
 
-def _need(t, name):
+def _needed(t, n, dtype, name, device):
     if t is None:
         raise ValueError(f"{name} is required")
-    return t
+    return _at(t, n, dtype, name, device)
+
+
+def _mask_at(mask, B, V, device):
+    torch = _torch()
+    if mask is None:
+        return 0
+    if mask.shape != (B, V) or mask.dtype not in (torch.bool, torch.uint8) or not mask.is_contiguous() or mask.device != device:
+        raise ValueError("mask must be a contiguous bool/uint8 [B, V] tensor on the logits' device")
+    return mask.data_ptr()
 
 
 def _grad_rows(out, logits, B, V):
     """The gradient's tensor and its leading dimension."""
-    torch = _torch()
     if out is None:
-        return torch.empty((B, V), dtype=logits.dtype, device=logits.device), V
+        return _torch().empty((B, V), dtype=logits.dtype, device=logits.device), V
     if out.shape != (B, V) or out.dtype != logits.dtype or out.device != logits.device:
         raise ValueError("the gradient must be a [B, V] tensor of the logits' type on their device")
     return out, _padded_rows(out, "the gradient")[2]
 
 
-class _Call:
-    """The stream of one call. Tensors made for a call on another stream than
-    the current one are marked as used there (so that their memory is not
-    handed out again before that stream is done), and the launch is made with
-    the logits' device as the current one."""
-
-    def __init__(self, device, stream):
-        torch = _torch()
-        self.device = device
-        self.current = torch.cuda.current_stream(device)
-        self.stream = stream if stream is not None else self.current
-        self.ptr = ctypes.c_void_p(self.stream.cuda_stream)
-
-    def own(self, *tensors):
-        if self.stream != self.current:
-            for t in tensors:
+def _call(fn, device, stream, made, *args):
+    """Calls fn(*args, stream) on ``stream`` (None: the current one), with the
+    logits' device as the current one. Tensors made for a call on another
+    stream than the current one are marked as used there, so that their memory
+    is not handed out again before that stream is done."""
+    torch = _torch()
+    if stream is None:
+        raw = torch._C._cuda_getCurrentRawStream(device.index)
+    else:
+        raw = stream.cuda_stream
+        if raw != torch._C._cuda_getCurrentRawStream(device.index):
+            for t in made:
                 if t is not None:
-                    t.record_stream(self.stream)
-
-    def guard(self):
-        torch = _torch()
-        if torch.cuda.current_device() == self.device.index:
-            return contextlib.nullcontext()
-        return torch.cuda.device(self.device)
-
-
-def _rc(rc):
+                    t.record_stream(stream)
+    if torch.cuda.current_device() == device.index:
+        rc = fn(*args, raw)
+    else:
+        with torch.cuda.device(device):
+            rc = fn(*args, raw)
     if rc != OK:
         raise QritaError(rc)
 
@@ -401,15 +407,13 @@ def qrita_token_logprobs(logits, tokens, mask=None, inv_temperature=1.0, entropy
     torch = _torch()
     B, V, ld = _padded_rows(logits)
     dev = logits.device
-    tok = _need(_vec(tokens, B, torch.int32, "tokens", dev), "tokens")
-    mask = _keep_mask(mask, B, V, dev)
-    call = _Call(dev, stream)
+    dt = _dtype_code(logits)
+    tok = _needed(tokens, B, torch.int32, "tokens", dev)
+    keep = _mask_at(mask, B, V, dev)
     logp = torch.empty(B, dtype=torch.float32, device=dev)
     ent = torch.empty(B, dtype=torch.float32, device=dev) if entropy else None
-    call.own(logp, ent)
-    with call.guard():
-        _rc(lib().qrita_token_logprobs(_ptr(logits), _dtype_code(logits), B, V, ld, _ptr(mask), _ptr(tok),
-                                       float(inv_temperature), _ptr(logp), _ptr(ent), call.ptr))
+    _call(lib().qrita_token_logprobs, dev, stream, (logp, ent), logits.data_ptr(), dt, B, V, ld, keep, tok,
+          float(inv_temperature), logp.data_ptr(), ent.data_ptr() if entropy else 0)
     return logp, ent
 
 
@@ -423,18 +427,16 @@ def qrita_token_logprobs_grad(logits, tokens, grad_logp=None, grad_entropy=None,
     torch = _torch()
     B, V, ld = _padded_rows(logits)
     dev = logits.device
-    tok = _need(_vec(tokens, B, torch.int32, "tokens", dev), "tokens")
-    mask = _keep_mask(mask, B, V, dev)
-    gl = _vec(grad_logp, B, torch.float32, "grad_logp", dev)
-    ge = _vec(grad_entropy, B, torch.float32, "grad_entropy", dev)
-    if gl is None and ge is None:
+    dt = _dtype_code(logits)
+    tok = _needed(tokens, B, torch.int32, "tokens", dev)
+    keep = _mask_at(mask, B, V, dev)
+    gl = _at(grad_logp, B, torch.float32, "grad_logp", dev)
+    ge = _at(grad_entropy, B, torch.float32, "grad_entropy", dev)
+    if grad_logp is None and grad_entropy is None:
         raise ValueError("one of grad_logp and grad_entropy is required")
-    call = _Call(dev, stream)
     grad, ldg = _grad_rows(out_grad, logits, B, V)
-    call.own(grad)
-    with call.guard():
-        _rc(lib().qrita_token_logprobs_grad(_ptr(logits), _dtype_code(logits), B, V, ld, _ptr(mask), _ptr(tok),
-                                            float(inv_temperature), _ptr(gl), _ptr(ge), _ptr(grad), ldg, call.ptr))
+    _call(lib().qrita_token_logprobs_grad, dev, stream, (grad,), logits.data_ptr(), dt, B, V, ld, keep, tok,
+          float(inv_temperature), gl, ge, grad.data_ptr(), ldg)
     return grad
 
 
@@ -456,27 +458,24 @@ def qrita_policy_loss(logits, tokens, old_logp, advantages, ref_logp=None, weigh
     B, V, ld = _padded_rows(logits)
     dev = logits.device
     f32 = torch.float32
-    tok = _need(_vec(tokens, B, torch.int32, "tokens", dev), "tokens")
-    mask = _keep_mask(mask, B, V, dev)
-    old = _vec(old_logp, B, f32, "old_logp", dev)
-    ref = _vec(ref_logp, B, f32, "ref_logp", dev)
-    adv = _need(_vec(advantages, B, f32, "advantages", dev), "advantages")
-    w = _vec(weights, B, f32, "weights", dev)
-    gl = _vec(grad_loss, 1, f32, "grad_loss", dev)
-    call = _Call(dev, stream)
-    loss = torch.empty((), dtype=f32, device=dev)
+    dt = _dtype_code(logits)
+    tok = _needed(tokens, B, torch.int32, "tokens", dev)
+    keep = _mask_at(mask, B, V, dev)
+    old = _at(old_logp, B, f32, "old_logp", dev)
+    ref = _at(ref_logp, B, f32, "ref_logp", dev)
+    adv = _needed(advantages, B, f32, "advantages", dev)
+    w = _at(weights, B, f32, "weights", dev)
+    gl = _at(grad_loss, 1, f32, "grad_loss", dev)
     want_ent = entropy or entropy_coef != 0
-    small = torch.empty((4 if want_ent else 3, B), dtype=f32, device=dev)
-    row_loss, logp, kl, *ent = small.unbind()
-    ent = ent[0] if ent else None
+    loss = torch.empty((), dtype=f32, device=dev)
+    rows = torch.empty((4 if want_ent else 3, B), dtype=f32, device=dev)
     g, ldg = _grad_rows(out_grad, logits, B, V) if grad else (None, 0)
-    call.own(loss, small, g)
-    with call.guard():
-        _rc(lib().qrita_policy_loss(
-            _ptr(logits), _dtype_code(logits), B, V, ld, _ptr(mask), _ptr(tok), float(inv_temperature), _ptr(old),
-            _ptr(ref), _ptr(adv), _ptr(w), float(clip_low), float(clip_high), float(kl_coef), float(entropy_coef),
-            _ptr(gl), _ptr(loss), _ptr(row_loss), _ptr(logp), _ptr(kl), _ptr(ent), _ptr(g), ldg, call.ptr))
-    return PolicyLoss(loss, g, row_loss, logp, kl, ent)
+    at, step = rows.data_ptr(), 4 * B
+    _call(lib().qrita_policy_loss, dev, stream, (loss, rows, g), logits.data_ptr(), dt, B, V, ld, keep, tok,
+          float(inv_temperature), old, ref, adv, w, float(clip_low), float(clip_high), float(kl_coef),
+          float(entropy_coef), gl, loss.data_ptr(), at, at + step, at + 2 * step, at + 3 * step if want_ent else 0,
+          g.data_ptr() if grad else 0, ldg)
+    return PolicyLoss(loss, g, *rows.unbind()) if want_ent else PolicyLoss(loss, g, *rows.unbind(), None)
 
 
 def preference_workspace_bytes(B: int, P: int) -> int:
@@ -503,29 +502,32 @@ def qrita_preference_loss(logits, tokens, starts, ref_logp=None, weights=None, i
     B, V, ld = _padded_rows(logits)
     dev = logits.device
     f32 = torch.float32
-    tok = _need(_vec(tokens, B, torch.int32, "tokens", dev), "tokens")
-    n = _need(starts, "starts").numel()
+    dt = _dtype_code(logits)
+    tok = _needed(tokens, B, torch.int32, "tokens", dev)
+    if starts is None:
+        raise ValueError("starts is required")
+    n = starts.numel()
     if n % 2 == 0:
         raise ValueError("starts must hold 2 P + 1 elements")
     P = n // 2
-    at = _vec(starts, n, torch.int32, "starts", dev)
-    ref = _vec(ref_logp, 2 * P, f32, "ref_logp", dev)
-    w = _vec(weights, P, f32, "weights", dev)
-    gl = _vec(grad_loss, 1, f32, "grad_loss", dev)
-    call = _Call(dev, stream)
+    at = _at(starts, n, torch.int32, "starts", dev)
+    ref = _at(ref_logp, 2 * P, f32, "ref_logp", dev)
+    w = _at(weights, P, f32, "weights", dev)
+    gl = _at(grad_loss, 1, f32, "grad_loss", dev)
     need = preference_workspace_bytes(B, P)
     if workspace is None:
         workspace = torch.empty(need, dtype=torch.uint8, device=dev)
     elif workspace.dtype != torch.uint8 or workspace.device != dev or not workspace.is_contiguous() or workspace.numel() < need:
         raise ValueError(f"workspace must be a contiguous uint8 tensor of at least {need} bytes on {dev}")
-    small = torch.empty(1 + 4 * P + B, dtype=f32, device=dev)
-    loss, pair_loss, ratio, seq, logp = small.split([1, P, P, 2 * P, B])
+    loss = torch.empty((), dtype=f32, device=dev)
+    pairs = torch.empty((2, P), dtype=f32, device=dev)
+    seq = torch.empty(2 * P, dtype=f32, device=dev)
+    logp = torch.empty(B, dtype=f32, device=dev)
     g, ldg = _grad_rows(out_grad, logits, B, V) if grad else (None, 0)
-    call.own(small, workspace, g)
-    with call.guard():
-        _rc(lib().qrita_preference_loss(
-            _ptr(logits), _dtype_code(logits), B, V, ld, _ptr(tok), float(inv_temperature), _ptr(at), P, _ptr(ref),
-            _ptr(w), float(beta), float(label_smoothing), float(margin), int(bool(length_norm)), _ptr(gl), _ptr(loss),
-            _ptr(pair_loss), _ptr(ratio), _ptr(seq), _ptr(logp), _ptr(g), ldg, _ptr(workspace),
-            ctypes.c_size_t(workspace.numel()), call.ptr))
-    return PreferenceLoss(loss[0], g, pair_loss, ratio, seq, logp)
+    pair_at = pairs.data_ptr()
+    _call(lib().qrita_preference_loss, dev, stream, (loss, pairs, seq, logp, workspace, g), logits.data_ptr(), dt, B, V,
+          ld, tok, float(inv_temperature), at, P, ref, w, float(beta), float(label_smoothing), float(margin),
+          1 if length_norm else 0, gl, loss.data_ptr(), pair_at, pair_at + 4 * P, seq.data_ptr(), logp.data_ptr(),
+          g.data_ptr() if grad else 0, ldg, workspace.data_ptr(), workspace.numel())
+    pair_loss, ratio = pairs.unbind()
+    return PreferenceLoss(loss, g, pair_loss, ratio, seq, logp)

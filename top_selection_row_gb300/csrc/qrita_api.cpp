@@ -249,6 +249,9 @@ int loss_args(const void* logits, int dtype, int64_t B, int64_t V, int64_t ld, c
 size_t align256(size_t x) { return (x + 255u) & ~static_cast<size_t>(255u); }
 
 }  // namespace
+
+int device_sms() { return sm_count(); }
+
 }  // namespace qrita
 
 extern "C" {

@@ -80,6 +80,9 @@ size_t smem_bytes(int ocap);
 // Launch the selection kernel (grid B*C, cluster C). Returns a cudaError_t.
 int launch_select(const Params& prm, int dtype, size_t smem, qrita_stream_t stream);
 
+// Multiprocessors of the current device.
+int device_sms();
+
 // Largest dynamic shared memory per block on the current device.
 int max_smem_per_block();
 

@@ -810,23 +810,31 @@ __global__ void __launch_bounds__(kLossThreads, 3) resident_kernel(const LossPar
   }
 }
 
-// out = sum of w[i] v[i] in one fixed order, in fp64 (w NULL: 1 / n).
-__global__ void __launch_bounds__(1024) weighted_sum_kernel(const float* v, const float* w, int64_t n, float* out) {
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  __shared__ double slots[32];
+// *out = sum of w[i] v[i] by one block of N threads in one fixed order, in
+// fp64 (w null: 1 / n). slots: N / 32 doubles of shared memory.
+template <int N>
+__device__ __forceinline__ void weighted_sum(const float* v, const float* w, int64_t n, float* out, double* slots) {
   double s = 0.0;
-  for (int64_t i = threadIdx.x; i < n; i += 1024) s += static_cast<double>(v[i]) * (w != nullptr ? w[i] : 1.0);
+  for (int64_t i = threadIdx.x; i < n; i += N) s += static_cast<double>(v[i]) * (w != nullptr ? w[i] : 1.0);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(kAll, s, o);
   if ((threadIdx.x & 31) == 0) slots[threadIdx.x >> 5] = s;
   __syncthreads();
   if (threadIdx.x < 32) {
-    s = slots[threadIdx.x];
+    s = threadIdx.x < N / 32 ? slots[threadIdx.x] : 0.0;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(kAll, s, o);
     if (threadIdx.x == 0) *out = n == 0 ? 0.f : static_cast<float>(w != nullptr ? s : s / static_cast<double>(n));
   }
+}
+
+constexpr int kSumThreads = 512;
+
+__global__ void __launch_bounds__(kSumThreads) weighted_sum_kernel(const float* v, const float* w, int64_t n, float* out) {
+  __shared__ double slots[kSumThreads / 32];
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  weighted_sum<kSumThreads>(v, w, n, out, slots);
 }
 
 // Row [lo, hi) of sequence s, within [0, B] whatever starts holds.
@@ -850,6 +858,14 @@ __global__ void __launch_bounds__(kPairThreads) pair_kernel(const LossParams p, 
   __shared__ double sum_slots[kPairThreads / 32];
   __shared__ int cnt_slots[kPairThreads / 32];
   const int64_t i = blockIdx.x;
+  if (i == 0 && p.logp != nullptr) {
+    // rows of no sequence: those before the first and from the last's end on
+    const int64_t lo = q.P > 0 ? min(max(static_cast<int64_t>(q.starts[0]), int64_t(0)), p.B) : p.B;
+    const int64_t hi = q.P > 0 ? min(max(static_cast<int64_t>(q.starts[2 * q.P]), lo), p.B) : p.B;
+    for (int64_t row = threadIdx.x; row < lo; row += kPairThreads) p.logp[row] = 0.f;
+    for (int64_t row = hi + threadIdx.x; row < p.B; row += kPairThreads) p.logp[row] = 0.f;
+  }
+  if (i >= q.P) return;
   double seq[2], n[2];
   for (int k = 0; k < 2; ++k) {
     int64_t lo, hi;
@@ -918,8 +934,10 @@ __global__ void __launch_bounds__(kLossThreads, 4) pref_grad_kernel(const LossPa
                                                                     const RowStat* stats, const double* coef, uint32_t C) {
   __shared__ RowGrad grad;
   __shared__ int64_t grad_token;
+  __shared__ double slots[kLossThreads / 32];
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if (blockIdx.x == 0) weighted_sum<kLossThreads>(q.pair_loss, q.weights, q.P, p.loss, slots);
   const int64_t row = p.B - 1 - blockIdx.x / C;
   const Share<DT> sh(p, row, blockIdx.x % C, C);
   if (threadIdx.x == 0) {
@@ -940,25 +958,12 @@ __global__ void __launch_bounds__(kLossThreads, 4) pref_grad_kernel(const LossPa
   write_grad<DT, false, false>(p, sh, row, grad, grad_token);
 }
 
-// out_logp of rows that no sequence owns is 0.
-__global__ void __launch_bounds__(kLossThreads) outside_kernel(const PrefParams q, int64_t B, float* logp) {
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  const int64_t row = static_cast<int64_t>(blockIdx.x) * kLossThreads + threadIdx.x;
-  if (row >= B) return;
-  const int64_t s = q.P > 0 ? sequence_of(q.starts, 2 * q.P + 1, row) : -1;
-  if (s < 0 || s >= 2 * q.P) logp[row] = 0.f;
-}
-
 // CTAs per row: as many as fill the device (a power of two), with at least a
 // unit or two for each thread; and enough that the rows in flight fit in L2
 // when a second pass follows.
 uint32_t row_ctas(const LossParams& p, int dtype, bool second_pass) {
   const int64_t bytes = p.V * (dtype == QRITA_DTYPE_F32 ? 4 : 2);
-  int dev = 0, sms = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess ||
-      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-    sms = 152;
+  const int sms = device_sms();
   const int64_t slots = static_cast<int64_t>(sms) * 4;
   uint32_t C = 1;
   while (C < kMaxRanks && bytes / (2 * C) >= 4096 && p.B * 2 * C <= slots) C *= 2;
@@ -1038,7 +1043,7 @@ cudaError_t launch_rows(const LossParams& p, int dtype, int op, bool ent, RowSta
 }
 
 cudaError_t launch_sum(const float* v, const float* w, int64_t n, float* out, cudaStream_t st) {
-  return launch(&weighted_sum_kernel, 1u, 1024u, 1u, st, size_t(0), v, w, n, out);
+  return launch(&weighted_sum_kernel, 1u, kSumThreads, 1u, st, size_t(0), v, w, n, out);
 }
 
 }  // namespace
@@ -1078,18 +1083,14 @@ int launch_preference(const LossParams& p, const PrefParams& q, int dtype, qrita
     LossParams f = p;
     f.grad = nullptr;
     if ((e = launch_rows(f, dtype, kOpPrefStats, false, stats, st)) != cudaSuccess) return static_cast<int>(e);
-    if (p.logp != nullptr) {
-      const unsigned grid = static_cast<unsigned>((p.B + kLossThreads - 1) / kLossThreads);
-      if ((e = launch(&outside_kernel, grid, kLossThreads, 1u, st, size_t(0), q, p.B, p.logp)) != cudaSuccess)
-        return static_cast<int>(e);
-    }
   }
-  if (q.P > 0) {
-    e = launch(&pair_kernel, static_cast<unsigned>(q.P), kPairThreads, 1u, st, size_t(0), p, q, static_cast<const RowStat*>(stats), coef);
+  {
+    e = launch(&pair_kernel, static_cast<unsigned>(q.P > 0 ? q.P : 1), kPairThreads, 1u, st, size_t(0), p, q, static_cast<const RowStat*>(stats), coef);
     if (e != cudaSuccess) return static_cast<int>(e);
   }
-  if ((e = launch_sum(q.pair_loss, q.weights, q.P, p.loss, st)) != cudaSuccess) return static_cast<int>(e);
-  if (p.B > 0 && p.grad != nullptr) {
+  if (p.B == 0 || p.grad == nullptr) {
+    e = launch_sum(q.pair_loss, q.weights, q.P, p.loss, st);
+  } else {  // (whose first CTA sums the loss)
     const uint32_t C = row_ctas(p, dtype, true);
     const unsigned grid = static_cast<unsigned>(p.B * C);
     auto* fn = dtype == QRITA_DTYPE_F32 ? &pref_grad_kernel<QRITA_DTYPE_F32> : &pref_grad_kernel<QRITA_DTYPE_BF16>;
