@@ -35,7 +35,6 @@ namespace {
 using namespace dev;
 
 constexpr int kLossThreads = 256;
-constexpr int kLossWarps = kLossThreads / 32;
 constexpr uint32_t kAll = 0xffffffffu;
 constexpr double kLn2 = 0.69314718055994530942;
 // Exponents below this give weights of 0 in fp32; the clamp keeps products
@@ -178,15 +177,15 @@ struct Share {
   bool ends;               // this CTA has the head and the tail
   bool mask_vec;           // a unit's mask bytes are one aligned word (or two)
 
-  __device__ Share(const LossParams& p, int64_t row, uint32_t rank, uint32_t C) {
+  __device__ Share(const LossParams& p, int64_t row, uint32_t rank, int log_c) {
     constexpr int U = Elem<DT>::kUnit;
     V = p.V;
     x = static_cast<const unsigned char*>(p.logits) + row * p.ld * Elem<DT>::kBytes;
     mask = p.mask != nullptr ? p.mask + row * V : nullptr;
-    head = static_cast<int64_t>((16u - (reinterpret_cast<uintptr_t>(x) & 15u)) & 15u) / Elem<DT>::kBytes;
+    head = ((16u - (reinterpret_cast<uintptr_t>(x) & 15u)) & 15u) / Elem<DT>::kBytes;
     if (head > V) head = V;
-    nu = (V - head) / U;
-    const int64_t per = (nu + C - 1) / C;
+    nu = static_cast<int64_t>(static_cast<uint64_t>(V - head) / U);
+    const int64_t per = (nu + (1 << log_c) - 1) >> log_c;
     u_lo = min(nu, static_cast<int64_t>(rank) * per);
     u_hi = min(nu, u_lo + per);
     ends = rank == 0;
@@ -307,32 +306,62 @@ __device__ __forceinline__ Stat lanes_stat(Stat v, float c) {
 
 constexpr int kMaxRanks = 16;
 
+// Shared memory of row_stat.
+template <int THREADS>
+struct StatSlots {
+  float m[THREADS], s[THREADS], t[THREADS];
+  Stat ranks[kMaxRanks];
+};
+
 // The row's sums from every thread's of its cluster of C CTAs, valid in the
-// first warp of every CTA: warps, then the CTA, then the cluster through
-// distributed shared memory (each CTA stores its record into all of them).
-template <bool ENT>
-__device__ __forceinline__ Stat row_stat(const Running<ENT>& r, float c, uint32_t rank, uint32_t C, Stat* slots,
-                                         Stat (*ranks)) {
+// first warp of every CTA. The first warp merges its CTA's sums alone (a
+// warp's worth of pairs costs 100 instructions, as many as 25 logits a lane
+// take), then the CTAs exchange their records through distributed shared
+// memory.
+template <int THREADS, bool ENT>
+__device__ __forceinline__ Stat row_stat(const Running<ENT>& r, float c, uint32_t rank, uint32_t C,
+                                         StatSlots<THREADS>& slots) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  Stat v;
-  v.m = r.m;
-  v.s = f2_make(r.s, 0.f);
-  v.t = f2_make(r.t, 0.f);
-  v = lanes_stat<ENT, 32>(v, c);
-  if (lane == 0) slots[warp] = v;
+  slots.m[threadIdx.x] = r.m;
+  slots.s[threadIdx.x] = r.s;
+  if (ENT) slots.t[threadIdx.x] = r.t;
   __syncthreads();
-  if (warp == 0) v = lanes_stat<ENT, kLossWarps>(slots[lane & (kLossWarps - 1)], c);
+  Stat v;
+  v.m = -INFINITY;
+  v.s = v.t = f2_make(0.f, 0.f);
+  if (warp == 0) {
+    float ms[THREADS / 32];
+#pragma unroll
+    for (int i = 0; i < THREADS / 32; ++i) {
+      ms[i] = slots.m[lane + 32 * i];
+      v.m = fmaxf(v.m, ms[i]);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v.m = fmaxf(v.m, __shfl_xor_sync(kAll, v.m, o));
+#pragma unroll
+    for (int i = 0; i < THREADS / 32; ++i) {
+      const float d = ms[i] == v.m ? 0.f : fmaxf((ms[i] - v.m) * c, kMinExp);
+      const float f = ex2(d), s = slots.s[lane + 32 * i];
+      f2_add(v.s, s * f);
+      if (ENT) f2_add(v.t, fmaf(d, s, slots.t[lane + 32 * i]) * f);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      v.s = f2_merge(v.s, f2_make(__shfl_xor_sync(kAll, v.s.hi, o), __shfl_xor_sync(kAll, v.s.lo, o)));
+      if (ENT) v.t = f2_merge(v.t, f2_make(__shfl_xor_sync(kAll, v.t.hi, o), __shfl_xor_sync(kAll, v.t.lo, o)));
+    }
+  }
   if (C > 1) {
     cluster_wait();  // (every CTA of the cluster is running)
     if (warp == 0 && static_cast<uint32_t>(lane) < C) {
-      const uint32_t at = map_rank(smem_u32(&ranks[rank]), lane);
+      const uint32_t at = map_rank(smem_u32(&slots.ranks[rank]), lane);
       const float rec[5] = {v.m, v.s.hi, v.s.lo, v.t.hi, v.t.lo};
 #pragma unroll
       for (int i = 0; i < (ENT ? 5 : 3); ++i) st_dsmem_u32(at + 4 * i, __float_as_uint(rec[i]));
     }
     cluster_sync_all();
     if (warp == 0) {
-      v = ranks[lane & (kMaxRanks - 1)];
+      v = slots.ranks[lane & (kMaxRanks - 1)];
       if ((lane & (kMaxRanks - 1)) >= static_cast<int>(C)) {
         v.m = -INFINITY;
         v.s = v.t = f2_make(0.f, 0.f);
@@ -368,7 +397,7 @@ __device__ __forceinline__ float exp_minus_tangent(float q) {
   if (fabsf(q) > 1.f) return expm1f(q) - q;
   float r = 1.f;
 #pragma unroll
-  for (int n = 13; n >= 3; --n) r = fmaf(r, q / static_cast<float>(n), 1.f);
+  for (int n = 13; n >= 3; --n) r = fmaf(r, q * (1.f / static_cast<float>(n)), 1.f);
   return 0.5f * q * q * r;
 }
 
@@ -409,81 +438,97 @@ __device__ __forceinline__ RowIn row_in(const LossParams& p, int op, int64_t row
   return in;
 }
 
-// Everything a row gives besides its gradient's entries. `out`: this thread
-// writes the row's values. logp is a pair, so that ratios and their clip are
-// decided on more than fp32 has of a logp near -20; fp64 would take this one
-// thread longer than the row's whole pass (a function is hundreds of
-// dependent instructions on a narrow pipe).
+// A row's values on the way from its sums to its outputs.
+struct RowVals {
+  F2 logp;
+  float lp, H;      // as they are given out
+  float ln_s, rho, q;
+  bool joins, over, bound;  // over, bound: rho above the clip; the clip binds
+};
+
+// logp as a pair, so that ratios and their clip are decided on more than fp32
+// has of a logp near -20. (fp64 would take this one thread longer than the
+// row's whole pass: a function is hundreds of dependent instructions on a
+// narrow pipe.)
 template <bool ENT>
-__device__ __forceinline__ RowGrad row_scalars(const LossParams& p, int op, RowStat* stats, int64_t row, const RowIn& in,
-                                               const Stat& st, bool out) {
-  RowGrad g;
-  g.m = st.m;
-  g.a = g.h = g.at = 0.f;
-  const float S = st.s.hi;
-  const bool empty = S == 0.f;  // nothing kept, or only -inf
+__device__ __forceinline__ RowVals row_vals(const LossParams& p, const RowIn& in, const Stat& st) {
+  RowVals v;
+  const bool empty = st.s.hi == 0.f;  // nothing kept, or only -inf
   const F2 ln_s = empty ? f2_make(0.f, 0.f) : ln_pair(st.s);
-  // T / S ln2: the mean of log p_j + ln S
-  const float mean = ENT && !empty ? f2_float(st.t) / S * static_cast<float>(kLn2) : 0.f;
-  F2 logp = f2_make(-INFINITY, 0.f);
+  v.ln_s = ln_s.hi;
+  v.logp = f2_make(-INFINITY, 0.f);
   if (in.kept_t && !empty) {
     F2 d;
     two_sum(in.x_t, -st.m, d.hi, d.lo);
     if (fabsf(d.hi) < 1e30f) {
       F2 y = f2_mul(d, p.c_ln2);  // (x_t - m) c ln2
       y.lo = fmaf(d.hi, p.c_ln2_lo, y.lo);
-      logp = f2_sub(y, ln_s);
+      v.logp = f2_sub(y, ln_s);
     } else {
-      logp.hi = d.hi * p.c_ln2 - ln_s.hi;  // no digit of ln S counts (or -inf, or NaN)
+      v.logp.hi = d.hi * p.c_ln2 - ln_s.hi;  // no digit of ln S counts (or -inf, or NaN)
     }
   }
-  const float lp = f2_float(logp);
-  const float H = ENT && !empty ? f2_float(f2_sub(ln_s, f2_make(mean, 0.f))) : 0.f;
-  const bool joins = lp != -INFINITY;  // (NaN joins)
-  if (out) {
-    if (p.logp != nullptr) p.logp[row] = lp;
-    if (ENT && p.entropy != nullptr) p.entropy[row] = H;
-  }
+  v.lp = f2_float(v.logp);
+  // ln S less the mean of y_j ln2
+  v.H = ENT && !empty ? f2_float(f2_sub(ln_s, f2_make(f2_float(st.t) / st.s.hi * static_cast<float>(kLn2), 0.f))) : 0.f;
+  v.joins = v.lp != -INFINITY;  // (NaN joins)
+  v.rho = v.q = 0.f;
+  v.over = v.bound = false;
+  return v;
+}
+
+// The weights of a row's gradient.
+template <bool ENT>
+__device__ __forceinline__ RowGrad row_weights(const LossParams& p, int op, const RowIn& in, const Stat& st, RowVals& v) {
+  float a = 0.f, h = 0.f;
   if (op == kOpGrad) {
-    g = row_grad(joins ? in.g_logp : 0.f, ENT && !empty ? in.g_entropy : 0.f, lp, H, ln_s.hi, st.m, S, p.inv_t);
-  } else if (op == kOpPolicy) {
+    if (v.joins) a = in.g_logp;
+    if (ENT && st.s.hi != 0.f) h = in.g_entropy;
+  } else if (op == kOpPolicy && v.joins) {
+    F2 d = f2_make(0.f, 0.f);  // ln rho
+    if (p.old_logp != nullptr)
+      d = isinf(in.old_logp) ? f2_make(-in.old_logp, 0.f) : f2_sub(v.logp, f2_make(in.old_logp, 0.f));
+    v.rho = expf(d.hi) * (1.f + d.lo);
+    // rho against the clip, on the logarithms
+    v.over = pair_above(d, p.ln_hi);
+    v.bound = (in.adv > 0.f && v.over) || (in.adv < 0.f && pair_above(p.ln_lo, d));
+    a = v.bound ? 0.f : -in.adv * v.rho;
+    if (v.lp != v.lp) a = v.lp;
+    if (p.ref_logp != nullptr) {
+      v.q = (in.ref_logp - v.logp.hi) - v.logp.lo;
+      if (p.kl_coef != 0.f) a = fmaf(-p.kl_coef, expm1f(v.q), a);
+    }
+    a *= in.w;
+    if (ENT) h = -p.entropy_coef * in.w;
+  }
+  return row_grad(a, h, v.lp, v.H, v.ln_s, st.m, st.s.hi, p.inv_t);
+}
+
+// Writes a row's values (after row_weights where the operator has them).
+template <bool ENT>
+__device__ __forceinline__ void row_out(const LossParams& p, int op, RowStat* stats, int64_t row, const RowIn& in,
+                                        const Stat& st, const RowVals& v) {
+  if (p.logp != nullptr) p.logp[row] = v.lp;
+  if (ENT && p.entropy != nullptr) p.entropy[row] = v.H;
+  if (op == kOpPolicy) {
     float loss = 0.f, kl = 0.f;
-    if (joins) {
-      const float adv = in.adv;
-      F2 d = f2_make(0.f, 0.f);  // ln rho
-      if (p.old_logp != nullptr)
-        d = isinf(in.old_logp) ? f2_make(-in.old_logp, 0.f) : f2_sub(logp, f2_make(in.old_logp, 0.f));
-      const float rho = expf(d.hi) * (1.f + d.lo);
-      // rho against the clip, on the logarithms
-      const bool over = pair_above(d, p.ln_hi), under = pair_above(p.ln_lo, d);
-      const bool bound = (adv > 0.f && over) || (adv < 0.f && under);
-      loss = -adv * (bound ? (over ? p.clip_hi : p.clip_lo) : rho);
-      float a = bound ? 0.f : -adv * rho;
-      if (lp != lp) loss = a = lp;
+    if (v.joins) {
+      loss = v.lp != v.lp ? v.lp : -in.adv * (v.bound ? (v.over ? p.clip_hi : p.clip_lo) : v.rho);
       if (p.ref_logp != nullptr) {
-        const float q = (in.ref_logp - logp.hi) - logp.lo;
-        kl = exp_minus_tangent(q);
-        if (p.kl_coef != 0.f) {
-          loss = fmaf(p.kl_coef, kl, loss);
-          a = fmaf(-p.kl_coef, expm1f(q), a);
-        }
+        kl = exp_minus_tangent(v.q);
+        if (p.kl_coef != 0.f) loss = fmaf(p.kl_coef, kl, loss);
       }
-      if (ENT) loss = fmaf(-p.entropy_coef, H, loss);
-      if (p.grad != nullptr)
-        g = row_grad(in.w * a, ENT ? -p.entropy_coef * in.w : 0.f, lp, H, ln_s.hi, st.m, S, p.inv_t);
+      if (ENT) loss = fmaf(-p.entropy_coef, v.H, loss);
     }
-    if (out) {
-      p.row_loss[row] = loss;
-      if (p.kl != nullptr) p.kl[row] = kl;
-    }
-  } else if (op == kOpPrefStats && out) {
+    p.row_loss[row] = loss;
+    if (p.kl != nullptr) p.kl[row] = kl;
+  } else if (op == kOpPrefStats) {
     RowStat o;
-    o.logp = static_cast<double>(logp.hi) + logp.lo;
+    o.logp = static_cast<double>(v.logp.hi) + v.logp.lo;
     o.m = st.m;
-    o.s = joins ? S : -1.f;
+    o.s = v.joins ? st.s.hi : -1.f;
     stats[row] = o;
   }
-  return g;
 }
 
 // Outputs of an ignored row, besides its gradient of 0.
@@ -514,7 +559,7 @@ constexpr int kUnroll = 4;  // units a thread has in flight
 // Writes this CTA's share of a row's gradient. token < 0: no entry of its
 // own. Every unit is read and then written by the same thread, so the
 // gradient may lie over the logits.
-template <int DT, bool ENT, bool MASKED>
+template <int THREADS, int DT, bool ENT, bool MASKED>
 __device__ __forceinline__ void write_grad(const LossParams& p, const Share<DT>& sh, int64_t row, const RowGrad& g,
                                            int64_t token) {
   using E = Elem<DT>;
@@ -539,24 +584,24 @@ __device__ __forceinline__ void write_grad(const LossParams& p, const Share<DT>&
     float2 v[N];
 #pragma unroll
     for (int i = 0; i < N; ++i) v[i] = both(0.f);
-    for (int64_t u = sh.u_lo + threadIdx.x; u < sh.u_hi; u += kLossThreads) put(u, v);
+    for (int64_t u = sh.u_lo + threadIdx.x; u < sh.u_hi; u += THREADS) put(u, v);
   } else {
-    for (int64_t u0 = sh.u_lo + threadIdx.x; u0 < sh.u_hi; u0 += kLossThreads * kUnroll) {
+    for (int64_t u0 = sh.u_lo + threadIdx.x; u0 < sh.u_hi; u0 += THREADS * kUnroll) {
       uint4 w[kUnroll];
       uint32_t bits[kUnroll];
 #pragma unroll
       for (int k = 0; k < kUnroll; ++k) {
-        const int64_t u = u0 + k * kLossThreads;
+        const int64_t u = u0 + k * THREADS;
         bits[k] = u < sh.u_hi ? (MASKED ? sh.kept(u) : 1u) : 0u;
       }
 #pragma unroll
       for (int k = 0; k < kUnroll; ++k) {
         w[k] = make_uint4(0u, 0u, 0u, 0u);
-        if (bits[k] != 0u) w[k] = load_unit(sh.unit(u0 + k * kLossThreads));
+        if (bits[k] != 0u) w[k] = load_unit(sh.unit(u0 + k * THREADS));
       }
 #pragma unroll
       for (int k = 0; k < kUnroll; ++k) {
-        const int64_t u = u0 + k * kLossThreads;
+        const int64_t u = u0 + k * THREADS;
         if (u >= sh.u_hi) break;
         float2 x[N], v[N];
         E::unpack(w[k], x);
@@ -599,27 +644,27 @@ __device__ __forceinline__ void write_grad(const LossParams& p, const Share<DT>&
 // memory, and rank 0 writes the row's values. A gradient takes a second pass
 // over the share.
 template <int DT, bool ENT, bool MASKED>
-__global__ void __launch_bounds__(kLossThreads, 4) row_kernel(const LossParams p, RowStat* stats, int op, uint32_t C) {
+__global__ void __launch_bounds__(kLossThreads, 4) row_kernel(const LossParams p, RowStat* stats, int op, int log_c) {
   using E = Elem<DT>;
   constexpr int N = E::kUnit / 2;
-  __shared__ Stat slots[kLossWarps];
-  __shared__ Stat ranks[kMaxRanks];
+  __shared__ StatSlots<kLossThreads> slots;
   __shared__ RowGrad grad;
+  __shared__ RowIn in;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  const uint32_t rank = C > 1 ? cluster_rank() : 0u;
-  const int64_t row = blockIdx.x / C;
-  const Share<DT> sh(p, row, rank, C);
+  const uint32_t C = 1u << log_c;
+  const int64_t row = blockIdx.x >> log_c;
   const int64_t token = p.tokens[row];
+  const uint32_t rank = C > 1 ? cluster_rank() : 0u;
+  const Share<DT> sh(p, row, rank, log_c);
   RowGrad g = {0.f, 0.f, 0.f, 0.f};
   if (token < 0 || token >= p.V) {  // (the same in every CTA of the cluster)
     if (threadIdx.x == 0 && rank == 0) row_ignored(p, op, stats, row);
-    if (p.grad != nullptr) write_grad<DT, ENT, MASKED>(p, sh, row, g, -1);
+    if (p.grad != nullptr) write_grad<kLossThreads, DT, ENT, MASKED>(p, sh, row, g, -1);
     return;
   }
   if (C > 1) cluster_arrive_relaxed();  // every CTA of the cluster runs before its memory is written
-  RowIn in;
-  if (threadIdx.x == 0) in = row_in<DT>(p, op, row, token);
+  if (threadIdx.x == 32) in = row_in<DT>(p, op, row, token);  // (read after the sums' barrier)
   Running<ENT> run;
   auto add = [&](uint4 w, uint32_t bits) {
     float2 x[N];
@@ -658,12 +703,18 @@ __global__ void __launch_bounds__(kLossThreads, 4) row_kernel(const LossParams p
     const int64_t j = sh.end_index(threadIdx.x);
     if (j >= 0 && (!MASKED || sh.mask[j] != 0)) run.add_one(E::load(sh.x, j), p.c);
   }
-  const Stat st = row_stat<ENT>(run, p.c, rank, C, slots, ranks);
-  if (threadIdx.x == 0 && (rank == 0 || p.grad != nullptr)) grad = row_scalars<ENT>(p, op, stats, row, in, st, rank == 0);
+  const Stat st = row_stat(run, p.c, rank, C, slots);
+  RowVals v;
+  if (threadIdx.x == 0 && (rank == 0 || p.grad != nullptr)) {
+    v = row_vals<ENT>(p, in, st);
+    if (p.grad != nullptr || op == kOpPolicy) grad = row_weights<ENT>(p, op, in, st, v);
+    if (p.grad == nullptr) row_out<ENT>(p, op, stats, row, in, st, v);
+  }
   if (p.grad == nullptr) return;
   __syncthreads();
+  if (threadIdx.x == 0 && rank == 0) row_out<ENT>(p, op, stats, row, in, st, v);
   g = grad;
-  write_grad<DT, ENT, MASKED>(p, sh, row, g, MASKED && sh.mask[token] == 0 ? -1 : token);
+  write_grad<kLossThreads, DT, ENT, MASKED>(p, sh, row, g, MASKED && sh.mask[token] == 0 ? -1 : token);
 }
 
 // The same with the CTA's share of the row held in shared memory from the
@@ -671,52 +722,62 @@ __global__ void __launch_bounds__(kLossThreads, 4) row_kernel(const LossParams p
 // arrives as bulk copies (TMA) of kPiece bytes, all in flight from the start,
 // and is summed as it lands; several CTAs on an SM overlap one's merge with
 // others' copies and stores.
-constexpr int kPiece = 16 * 1024;
+#ifndef KT
+#define KT 256
+#define KB 3
+#define KRES 72
+#define KPIECE 16
+#endif
+constexpr int kResThreads = KT;
+constexpr int kResBlocks = KB;
+constexpr int kPiece = KPIECE * 1024;
 constexpr int kPieceUnits = kPiece / 16;
 constexpr int kMaxPieces = 14;
 constexpr uint64_t kCopyLimitNs = 200ull * 1000 * 1000;
 
 template <int DT, bool ENT>
-__global__ void __launch_bounds__(kLossThreads, 3) resident_kernel(const LossParams p, int op, uint32_t C) {
+__global__ void __launch_bounds__(kResThreads, kResBlocks) resident_kernel(const LossParams p, int op, int log_c) {
   using E = Elem<DT>;
   constexpr int N = E::kUnit / 2;
   extern __shared__ __align__(128) uint4 units[];
   __shared__ __align__(8) uint64_t bars[kMaxPieces];
-  __shared__ Stat slots[kLossWarps];
-  __shared__ Stat ranks[kMaxRanks];
+  __shared__ StatSlots<kResThreads> slots;
   __shared__ RowGrad grad;
+  __shared__ RowIn in;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  const uint32_t rank = C > 1 ? cluster_rank() : 0u;
-  const int64_t row = blockIdx.x / C;
-  const Share<DT> sh(p, row, rank, C);
+  const uint32_t C = 1u << log_c;
+  const int64_t row = blockIdx.x >> log_c;
   const int64_t token = p.tokens[row];
-  RowGrad g = {0.f, 0.f, 0.f, 0.f};
-  if (token < 0 || token >= p.V) {  // (the same in every CTA of the cluster)
-    if (threadIdx.x == 0 && rank == 0) row_ignored(p, op, nullptr, row);
-    write_grad<DT, ENT, false>(p, sh, row, g, -1);
-    return;
-  }
-  if (C > 1) cluster_arrive_relaxed();  // every CTA of the cluster runs before its memory is written
+  const uint32_t rank = C > 1 ? cluster_rank() : 0u;
+  const Share<DT> sh(p, row, rank, log_c);
   const int n = static_cast<int>(sh.u_hi - sh.u_lo);
   const int pieces = (n + kPieceUnits - 1) / kPieceUnits;
-  const unsigned char* src = static_cast<const unsigned char*>(sh.unit(sh.u_lo));
   if (threadIdx.x == 0) {
     for (int i = 0; i < pieces; ++i) mbar_init(smem_u32(&bars[i]), 1);
     fence_mbar_init();
+  }
+  RowGrad g = {0.f, 0.f, 0.f, 0.f};
+  if (token < 0 || token >= p.V) {  // (the same in every CTA of the cluster)
+    if (threadIdx.x == 0 && rank == 0) row_ignored(p, op, nullptr, row);
+    write_grad<kResThreads, DT, ENT, false>(p, sh, row, g, -1);
+    return;
+  }
+  if (C > 1) cluster_arrive_relaxed();  // every CTA of the cluster runs before its memory is written
+  if (threadIdx.x == 0) {
+    const unsigned char* src = static_cast<const unsigned char*>(sh.unit(sh.u_lo));
     for (int i = 0; i < pieces; ++i) {
       const uint32_t bytes = static_cast<uint32_t>(min(kPieceUnits, n - i * kPieceUnits)) * 16u;
       mbar_expect_tx(smem_u32(&bars[i]), bytes);
       bulk_g2s(smem_u32(units + i * kPieceUnits), src + static_cast<int64_t>(i) * kPiece, bytes, smem_u32(&bars[i]));
     }
   }
-  RowIn in;
-  if (threadIdx.x == 0) in = row_in<DT>(p, op, row, token);
+  __syncthreads();  // the barriers are initialised
+  if (threadIdx.x == 32) in = row_in<DT>(p, op, row, token);  // (read after the sums' barrier)
   float end_x = 0.f;
   int64_t end_j = -1;
   if (sh.ends && threadIdx.x < Share<DT>::kEnds) end_j = sh.end_index(threadIdx.x);
   if (end_j >= 0) end_x = E::load(sh.x, end_j);
-  __syncthreads();  // the barriers are initialised
   Running<ENT> run;
   bool landed = true;
   for (int i = 0; i < pieces; ++i) {
@@ -725,30 +786,35 @@ __global__ void __launch_bounds__(kLossThreads, 3) resident_kernel(const LossPar
     landed = landed && mbar_wait_bounded(smem_u32(&bars[i]), 0, kCopyLimitNs);
     if (!landed) break;
     const uint4* at = units + i * kPieceUnits + threadIdx.x;
-    const int left = n - i * kPieceUnits;
-    if (left >= kPieceUnits) {
+    const int left = min(n - i * kPieceUnits, kPieceUnits);
+    int u = threadIdx.x;
+    for (; u + (kUnroll - 1) * kResThreads < left; u += kUnroll * kResThreads, at += kUnroll * kResThreads) {
       uint4 w[kUnroll];
 #pragma unroll
-      for (int k = 0; k < kUnroll; ++k) w[k] = at[k * kLossThreads];
+      for (int k = 0; k < kUnroll; ++k) w[k] = at[k * kResThreads];
 #pragma unroll
       for (int k = 0; k < kUnroll; ++k) {
         float2 x[N];
         E::unpack(w[k], x);
         run.add_unit(x, p.c);
       }
-    } else {
-      for (int u = threadIdx.x; u < left; u += kLossThreads, at += kLossThreads) {
-        float2 x[N];
-        E::unpack(*at, x);
-        run.add_unit(x, p.c);
-      }
+    }
+    for (; u < left; u += kResThreads, at += kResThreads) {
+      float2 x[N];
+      E::unpack(*at, x);
+      run.add_unit(x, p.c);
     }
   }
   if (end_j >= 0) run.add_one(end_x, p.c);
   if (!landed) run.s = run.t = NAN;
-  const Stat st = row_stat<ENT>(run, p.c, rank, C, slots, ranks);
-  if (threadIdx.x == 0) grad = row_scalars<ENT>(p, op, nullptr, row, in, st, rank == 0);
+  const Stat st = row_stat(run, p.c, rank, C, slots);
+  RowVals v;
+  if (threadIdx.x == 0) {
+    v = row_vals<ENT>(p, in, st);
+    grad = row_weights<ENT>(p, op, in, st, v);
+  }
   __syncthreads();
+  if (threadIdx.x == 0 && rank == 0) row_out<ENT>(p, op, nullptr, row, in, st, v);
   g = grad;
   unsigned char* grow = static_cast<unsigned char*>(p.grad) + row * p.ld_grad * E::kBytes;
   unsigned char* gu = grow + (sh.head + sh.u_lo * E::kUnit) * E::kBytes;
@@ -767,31 +833,34 @@ __global__ void __launch_bounds__(kLossThreads, 3) resident_kernel(const LossPar
       const float2 e = make_float2(ex2(y.x), ex2(y.y));
       v[i] = ENT ? mul2(e, fma2(hh, make_float2(y.x < kMinExp ? kMinExp : y.x, y.y < kMinExp ? kMinExp : y.y), aa))
                  : mul2(e, aa);
-      if (zero) v[i] = both(0.f);
     }
   };
+  if (zero) {
+    write_grad<kResThreads, DT, ENT, false>(p, sh, row, g, token);
+    return;
+  }
   if ((reinterpret_cast<uintptr_t>(gu) & 15u) == 0) {
     uint4* out = reinterpret_cast<uint4*>(gu);
     int u = threadIdx.x;
-    for (; u + (kUnroll - 1) * kLossThreads < n; u += kUnroll * kLossThreads) {
+    for (; u + (kUnroll - 1) * kResThreads < n; u += kUnroll * kResThreads) {
       uint4 w[kUnroll];
 #pragma unroll
-      for (int k = 0; k < kUnroll; ++k) w[k] = units[u + k * kLossThreads];
+      for (int k = 0; k < kUnroll; ++k) w[k] = units[u + k * kResThreads];
 #pragma unroll
       for (int k = 0; k < kUnroll; ++k) {
         float2 v[N];
         entries(w[k], v);
-        out[u + k * kLossThreads] = E::pack(v);
+        out[u + k * kResThreads] = E::pack(v);
       }
     }
-    for (; u < n; u += kLossThreads) {
+    for (; u < n; u += kResThreads) {
       float2 v[N];
       entries(units[u], v);
       out[u] = E::pack(v);
     }
   } else {
     // gradient rows aligned otherwise than the logits': entry by entry
-    for (int u = threadIdx.x; u < n; u += kLossThreads) {
+    for (int u = threadIdx.x; u < n; u += kResThreads) {
       float2 v[N];
       entries(units[u], v);
 #pragma unroll
@@ -801,7 +870,7 @@ __global__ void __launch_bounds__(kLossThreads, 3) resident_kernel(const LossPar
       }
     }
   }
-  if (end_j >= 0) E::store(grow, end_j, zero ? 0.f : grad_one<ENT>(end_x, g, p.c));
+  if (end_j >= 0) E::store(grow, end_j, grad_one<ENT>(end_x, g, p.c));
   const int64_t u = (token - sh.head) / E::kUnit;  // (token < head: 0 or below, an end)
   const bool end = token < sh.head || u >= sh.nu;
   if (end ? sh.ends : (u >= sh.u_lo && u < sh.u_hi)) {
@@ -931,15 +1000,15 @@ __device__ __forceinline__ int64_t sequence_of(const int32_t* starts, int64_t n_
 // sums' kernel has left in L2.
 template <int DT>
 __global__ void __launch_bounds__(kLossThreads, 4) pref_grad_kernel(const LossParams p, const PrefParams q,
-                                                                    const RowStat* stats, const double* coef, uint32_t C) {
+                                                                    const RowStat* stats, const double* coef, int log_c) {
   __shared__ RowGrad grad;
   __shared__ int64_t grad_token;
   __shared__ double slots[kLossThreads / 32];
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (blockIdx.x == 0) weighted_sum<kLossThreads>(q.pair_loss, q.weights, q.P, p.loss, slots);
-  const int64_t row = p.B - 1 - blockIdx.x / C;
-  const Share<DT> sh(p, row, blockIdx.x % C, C);
+  const int64_t row = p.B - 1 - (blockIdx.x >> log_c);
+  const Share<DT> sh(p, row, blockIdx.x & ((1u << log_c) - 1u), log_c);
   if (threadIdx.x == 0) {
     const int64_t s = q.P > 0 ? sequence_of(q.starts, 2 * q.P + 1, row) : -1;
     RowGrad g = {0.f, 0.f, 0.f, 0.f};
@@ -955,21 +1024,27 @@ __global__ void __launch_bounds__(kLossThreads, 4) pref_grad_kernel(const LossPa
     grad_token = token;
   }
   __syncthreads();
-  write_grad<DT, false, false>(p, sh, row, grad, grad_token);
+  write_grad<kLossThreads, DT, false, false>(p, sh, row, grad, grad_token);
 }
 
 // CTAs per row: as many as fill the device (a power of two), with at least a
 // unit or two for each thread; and enough that the rows in flight fit in L2
 // when a second pass follows.
-uint32_t row_ctas(const LossParams& p, int dtype, bool second_pass) {
+uint32_t row_ctas(const LossParams& p, int dtype, bool second_pass, int per_sm) {
   const int64_t bytes = p.V * (dtype == QRITA_DTYPE_F32 ? 4 : 2);
   const int sms = device_sms();
-  const int64_t slots = static_cast<int64_t>(sms) * 4;
+  const int64_t slots = static_cast<int64_t>(sms) * per_sm;
   uint32_t C = 1;
   while (C < kMaxRanks && bytes / (2 * C) >= 4096 && p.B * 2 * C <= slots) C *= 2;
   if (second_pass)
     while (C < 8 && bytes / C > 64 * 1024 && p.B * 2 * C <= INT32_MAX) C *= 2;
   return C;
+}
+
+int log2_of(uint32_t c) {
+  int n = 0;
+  while ((1u << n) < c) ++n;
+  return n;
 }
 
 template <typename F, typename... Args>
@@ -1007,7 +1082,7 @@ size_t resident_bytes(const LossParams& p, int dtype, uint32_t C) {
 }
 
 // The most shared memory a share may take: three CTAs on an SM.
-constexpr size_t kResidentMost = 72 * 1024;
+constexpr size_t kResidentMost = KRES * 1024;
 
 template <int DT, bool ENT>
 cudaError_t launch_resident(const LossParams& p, int op, uint32_t C, cudaStream_t st) {
@@ -1018,20 +1093,20 @@ cudaError_t launch_resident(const LossParams& p, int op, uint32_t C, cudaStream_
                                                cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
     if (e != cudaSuccess) return e;
   }
-  return launch(fn, static_cast<unsigned>(p.B * C), kLossThreads, C, st, smem, p, op, C);
+  return launch(fn, static_cast<unsigned>(p.B * C), kResThreads, C, st, smem, p, op, log2_of(C));
 }
 
 template <int DT, bool ENT>
 cudaError_t launch_rows_of(const LossParams& p, int op, RowStat* stats, cudaStream_t st) {
   if (p.grad != nullptr && p.mask == nullptr) {
-    uint32_t C = row_ctas(p, DT, false);
+    uint32_t C = row_ctas(p, DT, false, kResBlocks);
     while (C < kMaxRanks && resident_bytes(p, DT, C) > kResidentMost && p.B * 2 * C <= INT32_MAX) C *= 2;
     if (resident_bytes(p, DT, C) <= kResidentMost) return launch_resident<DT, ENT>(p, op, C, st);
   }
-  const uint32_t C = row_ctas(p, DT, p.grad != nullptr);
+  const uint32_t C = row_ctas(p, DT, p.grad != nullptr, 4);
   const unsigned grid = static_cast<unsigned>(p.B * C);
-  return p.mask != nullptr ? launch(&row_kernel<DT, ENT, true>, grid, kLossThreads, C, st, size_t(0), p, stats, op, C)
-                           : launch(&row_kernel<DT, ENT, false>, grid, kLossThreads, C, st, size_t(0), p, stats, op, C);
+  return p.mask != nullptr ? launch(&row_kernel<DT, ENT, true>, grid, kLossThreads, C, st, size_t(0), p, stats, op, log2_of(C))
+                           : launch(&row_kernel<DT, ENT, false>, grid, kLossThreads, C, st, size_t(0), p, stats, op, log2_of(C));
 }
 
 cudaError_t launch_rows(const LossParams& p, int dtype, int op, bool ent, RowStat* stats, cudaStream_t st) {
@@ -1091,10 +1166,10 @@ int launch_preference(const LossParams& p, const PrefParams& q, int dtype, qrita
   if (p.B == 0 || p.grad == nullptr) {
     e = launch_sum(q.pair_loss, q.weights, q.P, p.loss, st);
   } else {  // (whose first CTA sums the loss)
-    const uint32_t C = row_ctas(p, dtype, true);
+    const uint32_t C = row_ctas(p, dtype, true, 4);
     const unsigned grid = static_cast<unsigned>(p.B * C);
     auto* fn = dtype == QRITA_DTYPE_F32 ? &pref_grad_kernel<QRITA_DTYPE_F32> : &pref_grad_kernel<QRITA_DTYPE_BF16>;
-    e = launch(fn, grid, kLossThreads, 1u, st, size_t(0), p, q, static_cast<const RowStat*>(stats), static_cast<const double*>(coef), C);
+    e = launch(fn, grid, kLossThreads, 1u, st, size_t(0), p, q, static_cast<const RowStat*>(stats), static_cast<const double*>(coef), log2_of(C));
   }
   return static_cast<int>(e);
 }
