@@ -413,7 +413,7 @@ def qrita_token_logprobs(logits, tokens, mask=None, inv_temperature=1.0, entropy
     logp = torch.empty(B, dtype=torch.float32, device=dev)
     ent = torch.empty(B, dtype=torch.float32, device=dev) if entropy else None
     _call(lib().qrita_token_logprobs, dev, stream, (logp, ent), logits.data_ptr(), dt, B, V, ld, keep, tok,
-          float(inv_temperature), logp.data_ptr(), ent.data_ptr() if entropy else 0)
+          inv_temperature, logp.data_ptr(), ent.data_ptr() if entropy else 0)
     return logp, ent
 
 
@@ -436,7 +436,7 @@ def qrita_token_logprobs_grad(logits, tokens, grad_logp=None, grad_entropy=None,
         raise ValueError("one of grad_logp and grad_entropy is required")
     grad, ldg = _grad_rows(out_grad, logits, B, V)
     _call(lib().qrita_token_logprobs_grad, dev, stream, (grad,), logits.data_ptr(), dt, B, V, ld, keep, tok,
-          float(inv_temperature), gl, ge, grad.data_ptr(), ldg)
+          inv_temperature, gl, ge, grad.data_ptr(), ldg)
     return grad
 
 
@@ -467,15 +467,18 @@ def qrita_policy_loss(logits, tokens, old_logp, advantages, ref_logp=None, weigh
     w = _at(weights, B, f32, "weights", dev)
     gl = _at(grad_loss, 1, f32, "grad_loss", dev)
     want_ent = entropy or entropy_coef != 0
+    # (a tensor each: a view of a shared one takes longer to make and free)
     loss = torch.empty((), dtype=f32, device=dev)
-    rows = torch.empty((4 if want_ent else 3, B), dtype=f32, device=dev)
+    row_loss = torch.empty_like(advantages)
+    logp = torch.empty_like(advantages)
+    kl = torch.empty_like(advantages)
+    ent = torch.empty_like(advantages) if want_ent else None
     g, ldg = _grad_rows(out_grad, logits, B, V) if grad else (None, 0)
-    at, step = rows.data_ptr(), 4 * B
-    _call(lib().qrita_policy_loss, dev, stream, (loss, rows, g), logits.data_ptr(), dt, B, V, ld, keep, tok,
-          float(inv_temperature), old, ref, adv, w, float(clip_low), float(clip_high), float(kl_coef),
-          float(entropy_coef), gl, loss.data_ptr(), at, at + step, at + 2 * step, at + 3 * step if want_ent else 0,
+    _call(lib().qrita_policy_loss, dev, stream, (loss, row_loss, logp, kl, ent, g), logits.data_ptr(), dt, B, V, ld, keep,
+          tok, inv_temperature, old, ref, adv, w, clip_low, clip_high, kl_coef, entropy_coef, gl, loss.data_ptr(),
+          row_loss.data_ptr(), logp.data_ptr(), kl.data_ptr(), ent.data_ptr() if want_ent else 0,
           g.data_ptr() if grad else 0, ldg)
-    return PolicyLoss(loss, g, *rows.unbind()) if want_ent else PolicyLoss(loss, g, *rows.unbind(), None)
+    return PolicyLoss(loss, g, row_loss, logp, kl, ent)
 
 
 def preference_workspace_bytes(B: int, P: int) -> int:
@@ -520,14 +523,13 @@ def qrita_preference_loss(logits, tokens, starts, ref_logp=None, weights=None, i
     elif workspace.dtype != torch.uint8 or workspace.device != dev or not workspace.is_contiguous() or workspace.numel() < need:
         raise ValueError(f"workspace must be a contiguous uint8 tensor of at least {need} bytes on {dev}")
     loss = torch.empty((), dtype=f32, device=dev)
-    pairs = torch.empty((2, P), dtype=f32, device=dev)
+    pair_loss = torch.empty(P, dtype=f32, device=dev)
+    ratio = torch.empty_like(pair_loss)
     seq = torch.empty(2 * P, dtype=f32, device=dev)
     logp = torch.empty(B, dtype=f32, device=dev)
     g, ldg = _grad_rows(out_grad, logits, B, V) if grad else (None, 0)
-    pair_at = pairs.data_ptr()
-    _call(lib().qrita_preference_loss, dev, stream, (loss, pairs, seq, logp, workspace, g), logits.data_ptr(), dt, B, V,
-          ld, tok, float(inv_temperature), at, P, ref, w, float(beta), float(label_smoothing), float(margin),
-          1 if length_norm else 0, gl, loss.data_ptr(), pair_at, pair_at + 4 * P, seq.data_ptr(), logp.data_ptr(),
+    _call(lib().qrita_preference_loss, dev, stream, (loss, pair_loss, ratio, seq, logp, workspace, g), logits.data_ptr(),
+          dt, B, V, ld, tok, inv_temperature, at, P, ref, w, beta, label_smoothing, margin, 1 if length_norm else 0, gl,
+          loss.data_ptr(), pair_loss.data_ptr(), ratio.data_ptr(), seq.data_ptr(), logp.data_ptr(),
           g.data_ptr() if grad else 0, ldg, workspace.data_ptr(), workspace.numel())
-    pair_loss, ratio = pairs.unbind()
     return PreferenceLoss(loss, g, pair_loss, ratio, seq, logp)

@@ -106,6 +106,8 @@ struct LossParams {
   float c_ln2, c_ln2_lo;  // c ln2 as a pair
   float inv_t;
   float inv_b;  // 1 / B
+  uint32_t C;   // CTAs per row, and the 16-byte units of it each of them takes
+  int64_t per;
   // outputs per row
   float* logp;
   float* entropy;

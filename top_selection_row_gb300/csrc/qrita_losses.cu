@@ -41,6 +41,13 @@ constexpr double kLn2 = 0.69314718055994530942;
 // of such a weight with its exponent (an entropy's terms) from being 0 * inf.
 constexpr float kMinExp = -1000.0f;
 
+// The hardware's base-2 exponential is exact at 0 and lies low by 5.0e-8 of
+// its value on average over (-32, 0) (measured over 2^20 arguments, the same
+// to 1e-9 in every octave from -1 down; root mean square 5.8e-8). S takes the
+// mean back for the logits below the maximum, and again for every sum that
+// was shifted by an exponential: logp is then off by 4e-8 instead of 1.2e-7.
+constexpr float kExLow = 5.0e-8f;
+
 // What row_kernel computes for a row.
 enum Op : int { kOpLogprobs, kOpGrad, kOpPolicy, kOpPrefStats };
 
@@ -78,6 +85,13 @@ __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
+}
+
+// This CTA's cluster (a CTA alone is a cluster of one).
+__device__ __forceinline__ uint32_t cluster_id() {
+  uint32_t r;
+  asm("mov.u32 %0, %%clusterid.x;" : "=r"(r));
+  return r;
 }
 
 // Two fp32 operations in one instruction.
@@ -177,7 +191,7 @@ struct Share {
   bool ends;               // this CTA has the head and the tail
   bool mask_vec;           // a unit's mask bytes are one aligned word (or two)
 
-  __device__ Share(const LossParams& p, int64_t row, uint32_t rank, int log_c) {
+  __device__ Share(const LossParams& p, int64_t row, uint32_t rank) {
     constexpr int U = Elem<DT>::kUnit;
     V = p.V;
     x = static_cast<const unsigned char*>(p.logits) + row * p.ld * Elem<DT>::kBytes;
@@ -185,9 +199,8 @@ struct Share {
     head = ((16u - (reinterpret_cast<uintptr_t>(x) & 15u)) & 15u) / Elem<DT>::kBytes;
     if (head > V) head = V;
     nu = static_cast<int64_t>(static_cast<uint64_t>(V - head) / U);
-    const int64_t per = (nu + (1 << log_c) - 1) >> log_c;
-    u_lo = min(nu, static_cast<int64_t>(rank) * per);
-    u_hi = min(nu, u_lo + per);
+    u_lo = min(nu, static_cast<int64_t>(rank) * p.per);
+    u_hi = min(nu, u_lo + p.per);
     ends = rank == 0;
     mask_vec = (reinterpret_cast<uintptr_t>(mask + head) & (U - 1)) == 0;
   }
@@ -247,7 +260,9 @@ struct Running {
     s += e;
     if (ENT) t = fmaf(e, y < kMinExp ? kMinExp : y, t);
   }
-  // N pairs: their own sum first, then one addition to the running one
+  // N pairs (a power of two): their own sum first, then one addition to the
+  // running one. The more pairs, the more independent exponentials follow
+  // one test of the maximum.
   template <int N>
   __device__ __forceinline__ void add_unit(const float2 (&x)[N], float c) {
     float top = m;
@@ -285,6 +300,7 @@ __device__ __forceinline__ void stat_shift(Stat& a, float to, float c) {
     a.t = f2_mul(a.t, f);
   }
   a.s = f2_mul(a.s, f);
+  a.s.lo = fmaf(a.s.hi, kExLow, a.s.lo);
   a.m = to;
 }
 
@@ -313,61 +329,84 @@ struct StatSlots {
   Stat ranks[kMaxRanks];
 };
 
-// The row's sums from every thread's of its cluster of C CTAs, valid in the
-// first warp of every CTA. The first warp merges its CTA's sums alone (a
-// warp's worth of pairs costs 100 instructions, as many as 25 logits a lane
-// take), then the CTAs exchange their records through distributed shared
-// memory.
+// The CTA's sums from every thread's, in the first warp after a barrier over
+// the THREADS threads: that warp merges them alone (a warp's worth of pairs
+// costs 100 instructions, as many as 25 logits a lane take).
 template <int THREADS, bool ENT>
-__device__ __forceinline__ Stat row_stat(const Running<ENT>& r, float c, uint32_t rank, uint32_t C,
-                                         StatSlots<THREADS>& slots) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+__device__ __forceinline__ void put_stat(const Running<ENT>& r, StatSlots<THREADS>& slots) {
   slots.m[threadIdx.x] = r.m;
   slots.s[threadIdx.x] = r.s;
   if (ENT) slots.t[threadIdx.x] = r.t;
-  __syncthreads();
+}
+
+template <int THREADS, bool ENT>
+__device__ __forceinline__ Stat warp_stat(float c, const StatSlots<THREADS>& slots) {
+  const int lane = threadIdx.x & 31;
   Stat v;
   v.m = -INFINITY;
   v.s = v.t = f2_make(0.f, 0.f);
-  if (warp == 0) {
-    float ms[THREADS / 32];
+  float ms[THREADS / 32];
 #pragma unroll
-    for (int i = 0; i < THREADS / 32; ++i) {
-      ms[i] = slots.m[lane + 32 * i];
-      v.m = fmaxf(v.m, ms[i]);
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v.m = fmaxf(v.m, __shfl_xor_sync(kAll, v.m, o));
-#pragma unroll
-    for (int i = 0; i < THREADS / 32; ++i) {
-      const float d = ms[i] == v.m ? 0.f : fmaxf((ms[i] - v.m) * c, kMinExp);
-      const float f = ex2(d), s = slots.s[lane + 32 * i];
-      f2_add(v.s, s * f);
-      if (ENT) f2_add(v.t, fmaf(d, s, slots.t[lane + 32 * i]) * f);
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      v.s = f2_merge(v.s, f2_make(__shfl_xor_sync(kAll, v.s.hi, o), __shfl_xor_sync(kAll, v.s.lo, o)));
-      if (ENT) v.t = f2_merge(v.t, f2_make(__shfl_xor_sync(kAll, v.t.hi, o), __shfl_xor_sync(kAll, v.t.lo, o)));
-    }
+  for (int i = 0; i < THREADS / 32; ++i) {
+    ms[i] = slots.m[lane + 32 * i];
+    v.m = fmaxf(v.m, ms[i]);
   }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v.m = fmaxf(v.m, __shfl_xor_sync(kAll, v.m, o));
+#pragma unroll
+  for (int i = 0; i < THREADS / 32; ++i) {
+    const float d = ms[i] == v.m ? 0.f : fmaxf((ms[i] - v.m) * c, kMinExp);
+    const float f = ex2(d), s = slots.s[lane + 32 * i] * f;
+    f2_add(v.s, s);
+    if (d != 0.f) v.s.lo = fmaf(s, kExLow, v.s.lo);
+    if (ENT) f2_add(v.t, fmaf(d, s, slots.t[lane + 32 * i] * f));
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    v.s = f2_merge(v.s, f2_make(__shfl_xor_sync(kAll, v.s.hi, o), __shfl_xor_sync(kAll, v.s.lo, o)));
+    if (ENT) v.t = f2_merge(v.t, f2_make(__shfl_xor_sync(kAll, v.t.hi, o), __shfl_xor_sync(kAll, v.t.lo, o)));
+  }
+  return v;
+}
+
+// Stores a CTA's record (the same in every lane of its first warp) in all C
+// CTAs of the cluster, a lane each.
+template <bool ENT>
+__device__ __forceinline__ void send_stat(const Stat& v, uint32_t rank, uint32_t C, Stat* ranks) {
+  const uint32_t lane = threadIdx.x & 31;
+  if (lane < C) {
+    const uint32_t at = map_rank(smem_u32(&ranks[rank]), lane);
+    const float rec[5] = {v.m, v.s.hi, v.s.lo, v.t.hi, v.t.lo};
+#pragma unroll
+    for (int i = 0; i < (ENT ? 5 : 3); ++i) st_dsmem_u32(at + 4 * i, __float_as_uint(rec[i]));
+  }
+}
+
+template <bool ENT>
+__device__ __forceinline__ Stat merge_ranks(uint32_t C, float c, const Stat* ranks) {
+  const int lane = threadIdx.x & (kMaxRanks - 1);
+  Stat v = ranks[lane];
+  if (lane >= static_cast<int>(C)) {
+    v.m = -INFINITY;
+    v.s = v.t = f2_make(0.f, 0.f);
+  }
+  return lanes_stat<ENT, kMaxRanks>(v, c);
+}
+
+// The row's sums from every thread's of its cluster of C CTAs, valid in the
+// first warp of every CTA.
+template <int THREADS, bool ENT>
+__device__ __forceinline__ Stat row_stat(const Running<ENT>& r, float c, uint32_t rank, uint32_t C,
+                                         StatSlots<THREADS>& slots) {
+  put_stat(r, slots);
+  __syncthreads();
+  Stat v;
+  if (threadIdx.x < 32) v = warp_stat<THREADS, ENT>(c, slots);
   if (C > 1) {
     cluster_wait();  // (every CTA of the cluster is running)
-    if (warp == 0 && static_cast<uint32_t>(lane) < C) {
-      const uint32_t at = map_rank(smem_u32(&slots.ranks[rank]), lane);
-      const float rec[5] = {v.m, v.s.hi, v.s.lo, v.t.hi, v.t.lo};
-#pragma unroll
-      for (int i = 0; i < (ENT ? 5 : 3); ++i) st_dsmem_u32(at + 4 * i, __float_as_uint(rec[i]));
-    }
+    if (threadIdx.x < 32) send_stat<ENT>(v, rank, C, slots.ranks);
     cluster_sync_all();
-    if (warp == 0) {
-      v = slots.ranks[lane & (kMaxRanks - 1)];
-      if ((lane & (kMaxRanks - 1)) >= static_cast<int>(C)) {
-        v.m = -INFINITY;
-        v.s = v.t = f2_make(0.f, 0.f);
-      }
-      v = lanes_stat<ENT, kMaxRanks>(v, c);
-    }
+    if (threadIdx.x < 32) v = merge_ranks<ENT>(C, c, slots.ranks);
   }
   return v;
 }
@@ -454,7 +493,7 @@ template <bool ENT>
 __device__ __forceinline__ RowVals row_vals(const LossParams& p, const RowIn& in, const Stat& st) {
   RowVals v;
   const bool empty = st.s.hi == 0.f;  // nothing kept, or only -inf
-  const F2 ln_s = empty ? f2_make(0.f, 0.f) : ln_pair(st.s);
+  const F2 ln_s = empty ? f2_make(0.f, 0.f) : ln_pair(f2_merge(st.s, f2_make((st.s.hi - 1.f) * kExLow, 0.f)));
   v.ln_s = ln_s.hi;
   v.logp = f2_make(-INFINITY, 0.f);
   if (in.kept_t && !empty) {
@@ -644,7 +683,7 @@ __device__ __forceinline__ void write_grad(const LossParams& p, const Share<DT>&
 // memory, and rank 0 writes the row's values. A gradient takes a second pass
 // over the share.
 template <int DT, bool ENT, bool MASKED>
-__global__ void __launch_bounds__(kLossThreads, 4) row_kernel(const LossParams p, RowStat* stats, int op, int log_c) {
+__global__ void __launch_bounds__(kLossThreads, 4) row_kernel(const LossParams p, RowStat* stats, int op) {
   using E = Elem<DT>;
   constexpr int N = E::kUnit / 2;
   __shared__ StatSlots<kLossThreads> slots;
@@ -652,11 +691,11 @@ __global__ void __launch_bounds__(kLossThreads, 4) row_kernel(const LossParams p
   __shared__ RowIn in;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  const uint32_t C = 1u << log_c;
-  const int64_t row = blockIdx.x >> log_c;
+  const uint32_t C = p.C;
+  const int64_t row = cluster_id();
   const int64_t token = p.tokens[row];
   const uint32_t rank = C > 1 ? cluster_rank() : 0u;
-  const Share<DT> sh(p, row, rank, log_c);
+  const Share<DT> sh(p, row, rank);
   RowGrad g = {0.f, 0.f, 0.f, 0.f};
   if (token < 0 || token >= p.V) {  // (the same in every CTA of the cluster)
     if (threadIdx.x == 0 && rank == 0) row_ignored(p, op, stats, row);
@@ -717,165 +756,241 @@ __global__ void __launch_bounds__(kLossThreads, 4) row_kernel(const LossParams p
   write_grad<kLossThreads, DT, ENT, MASKED>(p, sh, row, g, MASKED && sh.mask[token] == 0 ? -1 : token);
 }
 
-// The same with the CTA's share of the row held in shared memory from the
-// sums to the gradient, so that HBM is read once and written once. The share
-// arrives as bulk copies (TMA) of kPiece bytes, all in flight from the start,
-// and is summed as it lands; several CTAs on an SM overlap one's merge with
-// others' copies and stores.
-#ifndef KT
-#define KT 256
-#define KB 3
-#define KRES 72
-#define KPIECE 16
-#endif
-constexpr int kResThreads = KT;
-constexpr int kResBlocks = KB;
-constexpr int kPiece = KPIECE * 1024;
-constexpr int kPieceUnits = kPiece / 16;
-constexpr int kMaxPieces = 14;
+// ---------------------------------------------------------------------------
+// Tensor memory as plain storage: 256 KB an SM that only tensor-core products
+// use otherwise. A thread keeps 32-bit words in its own lane of it: a warp
+// reaches the 32 lanes of its number mod 4, so warps that share a quarter take
+// different columns. All of these are warp-wide.
+// ---------------------------------------------------------------------------
+__device__ __forceinline__ void tmem_alloc(uint32_t dst_smem, uint32_t columns) {
+  asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(dst_smem), "r"(columns)
+               : "memory");
+}
+
+__device__ __forceinline__ void tmem_waive() {  // this CTA allocates no (more) of it
+  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+}
+
+__device__ __forceinline__ void tmem_free(uint32_t addr, uint32_t columns) {
+  asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(addr), "r"(columns) : "memory");
+}
+
+// 16 words of every lane to and from 16 columns.
+__device__ __forceinline__ void tmem_put(uint32_t addr, const uint4 (&w)[4]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16};" ::"r"(addr),
+      "r"(w[0].x), "r"(w[0].y), "r"(w[0].z), "r"(w[0].w), "r"(w[1].x), "r"(w[1].y), "r"(w[1].z), "r"(w[1].w),
+      "r"(w[2].x), "r"(w[2].y), "r"(w[2].z), "r"(w[2].w), "r"(w[3].x), "r"(w[3].y), "r"(w[3].z), "r"(w[3].w)
+      : "memory");
+}
+
+__device__ __forceinline__ void tmem_put_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+__device__ __forceinline__ void tmem_get(uint32_t addr, uint4 (&w)[4]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, "
+      "[%16];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(w[0].x), "=r"(w[0].y), "=r"(w[0].z), "=r"(w[0].w), "=r"(w[1].x), "=r"(w[1].y), "=r"(w[1].z), "=r"(w[1].w),
+        "=r"(w[2].x), "=r"(w[2].y), "=r"(w[2].z), "=r"(w[2].w), "=r"(w[3].x), "=r"(w[3].y), "=r"(w[3].z), "=r"(w[3].w)
+      : "r"(addr)
+      : "memory");
+}
+
+// ---------------------------------------------------------------------------
+// Sums and gradient with the CTA's share of the row held on the SM in between,
+// so that HBM is read once and written once. The share arrives by bulk copies
+// (TMA) of kPiece bytes into kSlots slots of shared memory. The last kSlots
+// pieces stay there; the ones before them move on to tensor memory as they are
+// summed, which frees their slots for the later copies. Three CTAs on an SM
+// hold up to 384 KB of rows that way, against 216 KB in shared memory alone:
+// while some wait for their cluster's sums, the others' copies and stores keep
+// HBM busy.
+// ---------------------------------------------------------------------------
+constexpr int kResThreads = 128;
+constexpr int kResBlocks = 8;
+constexpr int kPieceUnits = kResThreads * kUnroll;
+constexpr int kPiece = kPieceUnits * 16;
+constexpr int kSlots = 3;
+constexpr int kMoved = 4;  // pieces in tensor memory, at most
+constexpr int kTmemColumns = kMoved * 16 * (kResThreads / 128);
 constexpr uint64_t kCopyLimitNs = 200ull * 1000 * 1000;
 
-template <int DT, bool ENT>
-__global__ void __launch_bounds__(kResThreads, kResBlocks) resident_kernel(const LossParams p, int op, int log_c) {
+// MOVED: the share has more than kSlots pieces. Tensor memory is taken first
+// of all: an SM starts no further block of a kernel that may take some before
+// the last one has given up its right to (measured: without that, blocks of
+// this kernel ran one after another on an SM, 2.5 times the time).
+template <int DT, bool ENT, bool MOVED>
+__global__ void __launch_bounds__(kResThreads, kResBlocks) resident_kernel(const LossParams p, int op) {
   using E = Elem<DT>;
   constexpr int N = E::kUnit / 2;
   extern __shared__ __align__(128) uint4 units[];
-  __shared__ __align__(8) uint64_t bars[kMaxPieces];
+  __shared__ __align__(8) uint64_t bars[kSlots];
   __shared__ StatSlots<kResThreads> slots;
   __shared__ RowGrad grad;
   __shared__ RowIn in;
+  __shared__ uint32_t tmem_at;
+  const int tid = threadIdx.x, warp = tid >> 5;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  const uint32_t C = 1u << log_c;
-  const int64_t row = blockIdx.x >> log_c;
+  const uint32_t C = p.C;
+  const int64_t row = cluster_id();
   const int64_t token = p.tokens[row];
   const uint32_t rank = C > 1 ? cluster_rank() : 0u;
-  const Share<DT> sh(p, row, rank, log_c);
+  const Share<DT> sh(p, row, rank);
   const int n = static_cast<int>(sh.u_hi - sh.u_lo);
   const int pieces = (n + kPieceUnits - 1) / kPieceUnits;
-  if (threadIdx.x == 0) {
-    for (int i = 0; i < pieces; ++i) mbar_init(smem_u32(&bars[i]), 1);
+  const int moved = MOVED ? max(0, pieces - kSlots) : 0;
+  if (tid == 0) {
+    for (int i = 0; i < kSlots; ++i) mbar_init(smem_u32(&bars[i]), 1);
     fence_mbar_init();
   }
   RowGrad g = {0.f, 0.f, 0.f, 0.f};
   if (token < 0 || token >= p.V) {  // (the same in every CTA of the cluster)
-    if (threadIdx.x == 0 && rank == 0) row_ignored(p, op, nullptr, row);
+    if (MOVED && warp == 1) tmem_waive();
+    if (tid == 0 && rank == 0) row_ignored(p, op, nullptr, row);
     write_grad<kResThreads, DT, ENT, false>(p, sh, row, g, -1);
     return;
   }
   if (C > 1) cluster_arrive_relaxed();  // every CTA of the cluster runs before its memory is written
-  if (threadIdx.x == 0) {
-    const unsigned char* src = static_cast<const unsigned char*>(sh.unit(sh.u_lo));
-    for (int i = 0; i < pieces; ++i) {
-      const uint32_t bytes = static_cast<uint32_t>(min(kPieceUnits, n - i * kPieceUnits)) * 16u;
-      mbar_expect_tx(smem_u32(&bars[i]), bytes);
-      bulk_g2s(smem_u32(units + i * kPieceUnits), src + static_cast<int64_t>(i) * kPiece, bytes, smem_u32(&bars[i]));
-    }
+  const unsigned char* src = static_cast<const unsigned char*>(sh.unit(sh.u_lo));
+  auto fill = [&](int i) {
+    const uint32_t bytes = static_cast<uint32_t>(min(kPieceUnits, n - i * kPieceUnits)) * 16u;
+    const uint32_t bar = smem_u32(&bars[i % kSlots]);
+    mbar_expect_tx(bar, bytes);
+    bulk_g2s(smem_u32(units + (i % kSlots) * kPieceUnits), src + static_cast<int64_t>(i) * kPiece, bytes, bar);
+  };
+  if (tid == 0)
+    for (int i = 0; i < min(pieces, kSlots); ++i) fill(i);
+  if (MOVED && warp == 1) {
+    tmem_alloc(smem_u32(&tmem_at), kTmemColumns);
+    tmem_waive();
   }
-  __syncthreads();  // the barriers are initialised
-  if (threadIdx.x == 32) in = row_in<DT>(p, op, row, token);  // (read after the sums' barrier)
+  __syncthreads();  // the barriers are initialised, tensor memory is there
+  const uint32_t tmem =
+      MOVED ? tmem_at + (static_cast<uint32_t>(warp & 3) << 21) + static_cast<uint32_t>(warp >> 2) * (kMoved * 16) : 0u;
+  if (tid == 32) in = row_in<DT>(p, op, row, token);  // (read after the sums' barrier)
   float end_x = 0.f;
   int64_t end_j = -1;
-  if (sh.ends && threadIdx.x < Share<DT>::kEnds) end_j = sh.end_index(threadIdx.x);
+  if (sh.ends && tid < Share<DT>::kEnds) end_j = sh.end_index(tid);
   if (end_j >= 0) end_x = E::load(sh.x, end_j);
   Running<ENT> run;
   bool landed = true;
   for (int i = 0; i < pieces; ++i) {
     // a copy that never lands (not expected on a healthy device) gives a row
     // of NaN instead of a hang
-    landed = landed && mbar_wait_bounded(smem_u32(&bars[i]), 0, kCopyLimitNs);
-    if (!landed) break;
-    const uint4* at = units + i * kPieceUnits + threadIdx.x;
-    const int left = min(n - i * kPieceUnits, kPieceUnits);
-    int u = threadIdx.x;
-    for (; u + (kUnroll - 1) * kResThreads < left; u += kUnroll * kResThreads, at += kUnroll * kResThreads) {
+    landed = landed && mbar_wait_bounded(smem_u32(&bars[i % kSlots]), (i / kSlots) & 1, kCopyLimitNs);
+    landed = __all_sync(kAll, landed);
+    const uint4* at = units + (i % kSlots) * kPieceUnits + tid;
+    const int left = n - i * kPieceUnits;
+    if (left >= kPieceUnits) {
       uint4 w[kUnroll];
+      float2 x[kUnroll * N];
 #pragma unroll
       for (int k = 0; k < kUnroll; ++k) w[k] = at[k * kResThreads];
+      if (MOVED && i < moved) {
+        tmem_put(tmem + i * 16, w);
+        __syncthreads();  // the slot is read
+        if (tid == 0 && landed) {
+          fence_proxy_async_smem();
+          fill(i + kSlots);
+        }
+      }
 #pragma unroll
-      for (int k = 0; k < kUnroll; ++k) {
+      for (int k = 0; k < kUnroll; ++k) E::unpack(w[k], reinterpret_cast<float2(&)[N]>(x[k * N]));
+      run.add_unit(x, p.c);
+    } else {
+      for (int u = tid; u < left; u += kResThreads, at += kResThreads) {
         float2 x[N];
-        E::unpack(w[k], x);
+        E::unpack(*at, x);
         run.add_unit(x, p.c);
       }
-    }
-    for (; u < left; u += kResThreads, at += kResThreads) {
-      float2 x[N];
-      E::unpack(*at, x);
-      run.add_unit(x, p.c);
     }
   }
   if (end_j >= 0) run.add_one(end_x, p.c);
   if (!landed) run.s = run.t = NAN;
+  if (MOVED) tmem_put_wait();
   const Stat st = row_stat(run, p.c, rank, C, slots);
   RowVals v;
-  if (threadIdx.x == 0) {
+  if (tid == 0) {
     v = row_vals<ENT>(p, in, st);
     grad = row_weights<ENT>(p, op, in, st, v);
   }
   __syncthreads();
-  if (threadIdx.x == 0 && rank == 0) row_out<ENT>(p, op, nullptr, row, in, st, v);
+  if (tid == 0 && rank == 0) row_out<ENT>(p, op, nullptr, row, in, st, v);
+  __syncwarp();
   g = grad;
   unsigned char* grow = static_cast<unsigned char*>(p.grad) + row * p.ld_grad * E::kBytes;
   unsigned char* gu = grow + (sh.head + sh.u_lo * E::kUnit) * E::kBytes;
-  if (!landed) {
-    // (bounded) the copies in flight end before this CTA's memory is given up
-    for (int i = 0; i < pieces; ++i) (void)mbar_wait_bounded(smem_u32(&bars[i]), 0, kCopyLimitNs);
-  }
-  const float2 nm = both(-g.m), cc = both(p.c), aa = both(g.a), hh = both(g.h);
-  const bool zero = g.a == 0.f && g.h == 0.f;
-  auto entries = [&](uint4 w, float2 (&v)[N]) {
-    float2 x[N];
-    E::unpack(w, x);
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-      const float2 y = mul2(add2(x[i], nm), cc);
-      const float2 e = make_float2(ex2(y.x), ex2(y.y));
-      v[i] = ENT ? mul2(e, fma2(hh, make_float2(y.x < kMinExp ? kMinExp : y.x, y.y < kMinExp ? kMinExp : y.y), aa))
-                 : mul2(e, aa);
-    }
-  };
-  if (zero) {
+  if (g.a == 0.f && g.h == 0.f) {
     write_grad<kResThreads, DT, ENT, false>(p, sh, row, g, token);
-    return;
-  }
-  if ((reinterpret_cast<uintptr_t>(gu) & 15u) == 0) {
-    uint4* out = reinterpret_cast<uint4*>(gu);
-    int u = threadIdx.x;
-    for (; u + (kUnroll - 1) * kResThreads < n; u += kUnroll * kResThreads) {
-      uint4 w[kUnroll];
-#pragma unroll
-      for (int k = 0; k < kUnroll; ++k) w[k] = units[u + k * kResThreads];
-#pragma unroll
-      for (int k = 0; k < kUnroll; ++k) {
-        float2 v[N];
-        entries(w[k], v);
-        out[u + k * kResThreads] = E::pack(v);
-      }
-    }
-    for (; u < n; u += kResThreads) {
-      float2 v[N];
-      entries(units[u], v);
-      out[u] = E::pack(v);
-    }
   } else {
-    // gradient rows aligned otherwise than the logits': entry by entry
-    for (int u = threadIdx.x; u < n; u += kResThreads) {
-      float2 v[N];
-      entries(units[u], v);
+    const float2 nm = both(-g.m), cc = both(p.c), aa = both(g.a), hh = both(g.h);
+    auto entries = [&](uint4 w, float2 (&e)[N]) {
+      float2 x[N];
+      E::unpack(w, x);
 #pragma unroll
       for (int i = 0; i < N; ++i) {
-        E::store(gu, static_cast<int64_t>(u) * E::kUnit + 2 * i, v[i].x);
-        E::store(gu, static_cast<int64_t>(u) * E::kUnit + 2 * i + 1, v[i].y);
+        const float2 y = mul2(add2(x[i], nm), cc);
+        const float2 w2 = make_float2(ex2(y.x), ex2(y.y));
+        e[i] = ENT ? mul2(w2, fma2(hh, make_float2(y.x < kMinExp ? kMinExp : y.x, y.y < kMinExp ? kMinExp : y.y), aa))
+                   : mul2(w2, aa);
+      }
+    };
+    const bool vec = (reinterpret_cast<uintptr_t>(gu) & 15u) == 0;
+    auto put = [&](int u, const float2 (&e)[N]) {
+      if (vec) {
+        reinterpret_cast<uint4*>(gu)[u] = E::pack(e);
+      } else {  // gradient rows aligned otherwise than the logits': entry by entry
+#pragma unroll
+        for (int k = 0; k < N; ++k) {
+          E::store(gu, static_cast<int64_t>(u) * E::kUnit + 2 * k, e[k].x);
+          E::store(gu, static_cast<int64_t>(u) * E::kUnit + 2 * k + 1, e[k].y);
+        }
+      }
+    };
+    for (int i = 0; i < pieces; ++i) {
+      const uint4* at = units + (i % kSlots) * kPieceUnits + tid;
+      const int u0 = i * kPieceUnits + tid;
+      if (n - i * kPieceUnits >= kPieceUnits) {
+        uint4 w[kUnroll];
+        if (MOVED && i < moved) {
+          tmem_get(tmem + i * 16, w);
+        } else {
+#pragma unroll
+          for (int k = 0; k < kUnroll; ++k) w[k] = at[k * kResThreads];
+        }
+#pragma unroll
+        for (int k = 0; k < kUnroll; ++k) {
+          float2 e[N];
+          entries(w[k], e);
+          put(u0 + k * kResThreads, e);
+        }
+      } else {
+        for (int u = u0; u < n; u += kResThreads, at += kResThreads) {
+          float2 e[N];
+          entries(*at, e);
+          put(u, e);
+        }
       }
     }
+    if (end_j >= 0) E::store(grow, end_j, grad_one<ENT>(end_x, g, p.c));
+    const int64_t u = (token - sh.head) / E::kUnit;  // (token < head: 0 or below, an end)
+    const bool end = token < sh.head || u >= sh.nu;
+    if (end ? sh.ends : (u >= sh.u_lo && u < sh.u_hi)) {
+      __syncthreads();
+      if (tid == 0) E::store(grow, token, g.at);
+    }
   }
-  if (end_j >= 0) E::store(grow, end_j, grad_one<ENT>(end_x, g, p.c));
-  const int64_t u = (token - sh.head) / E::kUnit;  // (token < head: 0 or below, an end)
-  const bool end = token < sh.head || u >= sh.nu;
-  if (end ? sh.ends : (u >= sh.u_lo && u < sh.u_hi)) {
-    __syncthreads();
-    if (threadIdx.x == 0) E::store(grow, token, g.at);
+  if (MOVED) {
+    __syncthreads();  // every warp has read its words
+    if (warp == 1) tmem_free(tmem_at, kTmemColumns);
+  }
+  if (!landed) {
+    // (bounded) copies in flight end before this CTA's memory is given up
+    const uint64_t t0 = globaltimer_ns();
+    while (globaltimer_ns() - t0 < kCopyLimitNs) __nanosleep(1000);
   }
 }
 
@@ -1000,15 +1115,15 @@ __device__ __forceinline__ int64_t sequence_of(const int32_t* starts, int64_t n_
 // sums' kernel has left in L2.
 template <int DT>
 __global__ void __launch_bounds__(kLossThreads, 4) pref_grad_kernel(const LossParams p, const PrefParams q,
-                                                                    const RowStat* stats, const double* coef, int log_c) {
+                                                                    const RowStat* stats, const double* coef) {
   __shared__ RowGrad grad;
   __shared__ int64_t grad_token;
   __shared__ double slots[kLossThreads / 32];
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (blockIdx.x == 0) weighted_sum<kLossThreads>(q.pair_loss, q.weights, q.P, p.loss, slots);
-  const int64_t row = p.B - 1 - (blockIdx.x >> log_c);
-  const Share<DT> sh(p, row, blockIdx.x & ((1u << log_c) - 1u), log_c);
+  const int64_t row = p.B - 1 - blockIdx.x / p.C;
+  const Share<DT> sh(p, row, blockIdx.x % p.C);
   if (threadIdx.x == 0) {
     const int64_t s = q.P > 0 ? sequence_of(q.starts, 2 * q.P + 1, row) : -1;
     RowGrad g = {0.f, 0.f, 0.f, 0.f};
@@ -1041,12 +1156,6 @@ uint32_t row_ctas(const LossParams& p, int dtype, bool second_pass, int per_sm) 
   return C;
 }
 
-int log2_of(uint32_t c) {
-  int n = 0;
-  while ((1u << n) < c) ++n;
-  return n;
-}
-
 template <typename F, typename... Args>
 cudaError_t launch(F* fn, unsigned grid, unsigned block, unsigned cluster, cudaStream_t st, size_t smem, Args... args) {
   if (cluster > 8) {
@@ -1075,38 +1184,54 @@ cudaError_t launch(F* fn, unsigned grid, unsigned block, unsigned cluster, cudaS
   return e != cudaSuccess ? e : last;
 }
 
-// Dynamic shared memory of resident_kernel for C CTAs a row.
-size_t resident_bytes(const LossParams& p, int dtype, uint32_t C) {
-  const int64_t unit = dtype == QRITA_DTYPE_F32 ? 4 : 8;
-  return static_cast<size_t>((p.V / unit + C - 1) / C) * 16;
+// p for C CTAs a row.
+LossParams with_ctas(const LossParams& p, int dtype, uint32_t C) {
+  LossParams q = p;
+  const int64_t units = p.V / (dtype == QRITA_DTYPE_F32 ? 4 : 8);
+  q.C = C;
+  q.per = (units + C - 1) / C;
+  return q;
 }
 
-// The most shared memory a share may take: three CTAs on an SM.
-constexpr size_t kResidentMost = KRES * 1024;
+constexpr int64_t kResidentUnits = static_cast<int64_t>(kSlots + kMoved) * kPieceUnits;  // a share's, at most
+
+// CTAs per row for resident_kernel (0: a row does not fit in a cluster): as
+// few as hold the row, and more where the batch leaves SMs idle.
+uint32_t resident_ctas(const LossParams& p, int dtype) {
+  const int64_t units = p.V / (dtype == QRITA_DTYPE_F32 ? 4 : 8);
+  const int64_t least = units > 0 ? (units + kResidentUnits - 1) / kResidentUnits : 1;
+  if (least > kMaxRanks || p.B * least > INT32_MAX) return 0;
+  int64_t C = static_cast<int64_t>(device_sms()) * kResBlocks / p.B;
+  if (C > units / 256) C = units / 256;
+  if (C > kMaxRanks) C = kMaxRanks;
+  return static_cast<uint32_t>(C > least ? C : least);
+}
 
 template <int DT, bool ENT>
 cudaError_t launch_resident(const LossParams& p, int op, uint32_t C, cudaStream_t st) {
-  const size_t smem = resident_bytes(p, DT, C);
-  auto* fn = &resident_kernel<DT, ENT>;
+  const LossParams q = with_ctas(p, DT, C);
+  if (q.per > kResidentUnits) return cudaErrorInvalidValue;  // (a share past its storage)
+  const int64_t pieces = (q.per + kPieceUnits - 1) / kPieceUnits;
+  const size_t smem = static_cast<size_t>(pieces < kSlots ? pieces : kSlots) * kPiece;
+  auto* fn = pieces > kSlots ? &resident_kernel<DT, ENT, true> : &resident_kernel<DT, ENT, false>;
   if (smem > 40 * 1024) {  // beyond what a kernel has without asking
     const cudaError_t e = cudaFuncSetAttribute(reinterpret_cast<const void*>(fn),
                                                cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
     if (e != cudaSuccess) return e;
   }
-  return launch(fn, static_cast<unsigned>(p.B * C), kResThreads, C, st, smem, p, op, log2_of(C));
+  return launch(fn, static_cast<unsigned>(p.B * C), kResThreads, C, st, smem, q, op);
 }
 
 template <int DT, bool ENT>
 cudaError_t launch_rows_of(const LossParams& p, int op, RowStat* stats, cudaStream_t st) {
   if (p.grad != nullptr && p.mask == nullptr) {
-    uint32_t C = row_ctas(p, DT, false, kResBlocks);
-    while (C < kMaxRanks && resident_bytes(p, DT, C) > kResidentMost && p.B * 2 * C <= INT32_MAX) C *= 2;
-    if (resident_bytes(p, DT, C) <= kResidentMost) return launch_resident<DT, ENT>(p, op, C, st);
+    uint32_t C = resident_ctas(p, DT);
+    if (C > 0) return launch_resident<DT, ENT>(p, op, C, st);
   }
   const uint32_t C = row_ctas(p, DT, p.grad != nullptr, 4);
   const unsigned grid = static_cast<unsigned>(p.B * C);
-  return p.mask != nullptr ? launch(&row_kernel<DT, ENT, true>, grid, kLossThreads, C, st, size_t(0), p, stats, op, log2_of(C))
-                           : launch(&row_kernel<DT, ENT, false>, grid, kLossThreads, C, st, size_t(0), p, stats, op, log2_of(C));
+  return p.mask != nullptr ? launch(&row_kernel<DT, ENT, true>, grid, kLossThreads, C, st, size_t(0), with_ctas(p, DT, C), stats, op)
+                           : launch(&row_kernel<DT, ENT, false>, grid, kLossThreads, C, st, size_t(0), with_ctas(p, DT, C), stats, op);
 }
 
 cudaError_t launch_rows(const LossParams& p, int dtype, int op, bool ent, RowStat* stats, cudaStream_t st) {
@@ -1169,7 +1294,8 @@ int launch_preference(const LossParams& p, const PrefParams& q, int dtype, qrita
     const uint32_t C = row_ctas(p, dtype, true, 4);
     const unsigned grid = static_cast<unsigned>(p.B * C);
     auto* fn = dtype == QRITA_DTYPE_F32 ? &pref_grad_kernel<QRITA_DTYPE_F32> : &pref_grad_kernel<QRITA_DTYPE_BF16>;
-    e = launch(fn, grid, kLossThreads, 1u, st, size_t(0), p, q, static_cast<const RowStat*>(stats), static_cast<const double*>(coef), log2_of(C));
+    e = launch(fn, grid, kLossThreads, 1u, st, size_t(0), with_ctas(p, dtype, C), q, static_cast<const RowStat*>(stats),
+               static_cast<const double*>(coef));
   }
   return static_cast<int>(e);
 }
