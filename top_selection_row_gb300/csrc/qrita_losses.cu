@@ -35,6 +35,7 @@ namespace {
 using namespace dev;
 
 constexpr int kLossThreads = 256;
+constexpr int kLossBlocks = 4;  // of row_kernel on an SM
 constexpr uint32_t kAll = 0xffffffffu;
 constexpr double kLn2 = 0.69314718055994530942;
 // Exponents below this give weights of 0 in fp32; the clamp keeps products
@@ -683,7 +684,7 @@ __device__ __forceinline__ void write_grad(const LossParams& p, const Share<DT>&
 // memory, and rank 0 writes the row's values. A gradient takes a second pass
 // over the share.
 template <int DT, bool ENT, bool MASKED>
-__global__ void __launch_bounds__(kLossThreads, 4) row_kernel(const LossParams p, RowStat* stats, int op) {
+__global__ void __launch_bounds__(kLossThreads, kLossBlocks) row_kernel(const LossParams p, RowStat* stats, int op) {
   using E = Elem<DT>;
   constexpr int N = E::kUnit / 2;
   __shared__ StatSlots<kLossThreads> slots;
@@ -730,9 +731,16 @@ __global__ void __launch_bounds__(kLossThreads, 4) row_kernel(const LossParams p
 #pragma unroll
     for (int k = 0; k < kUnroll; ++k)
       if (!MASKED || bits[k] != 0u) w[k] = load_unit(sh.unit(u0 + k * kLossThreads));
+    if (MASKED) {
 #pragma unroll
-    for (int k = 0; k < kUnroll; ++k)
-      if (!MASKED || bits[k] != 0u) add(w[k], bits[k]);
+      for (int k = 0; k < kUnroll; ++k)
+        if (bits[k] != 0u) add(w[k], bits[k]);
+    } else {
+      float2 x[kUnroll * N];
+#pragma unroll
+      for (int k = 0; k < kUnroll; ++k) E::unpack(w[k], reinterpret_cast<float2(&)[N]>(x[k * N]));
+      run.add_unit(x, p.c);
+    }
   }
   for (; u0 < sh.u_hi; u0 += kLossThreads) {
     const uint32_t bits = MASKED ? sh.kept(u0) : 1u;
@@ -1228,7 +1236,7 @@ cudaError_t launch_rows_of(const LossParams& p, int op, RowStat* stats, cudaStre
     uint32_t C = resident_ctas(p, DT);
     if (C > 0) return launch_resident<DT, ENT>(p, op, C, st);
   }
-  const uint32_t C = row_ctas(p, DT, p.grad != nullptr, 4);
+  const uint32_t C = row_ctas(p, DT, p.grad != nullptr, kLossBlocks);
   const unsigned grid = static_cast<unsigned>(p.B * C);
   return p.mask != nullptr ? launch(&row_kernel<DT, ENT, true>, grid, kLossThreads, C, st, size_t(0), with_ctas(p, DT, C), stats, op)
                            : launch(&row_kernel<DT, ENT, false>, grid, kLossThreads, C, st, size_t(0), with_ctas(p, DT, C), stats, op);
