@@ -173,6 +173,9 @@ def policy_case(dev, rng, x, dtype, tokens, mask, inv_t=1.0, kl=0.1, ent=0.0, ol
     soft = softmaxes(x, dtype, mask, tokens, inv_t)
     base = np.array([s.logp if s.joins and np.isfinite(s.logp) else -1.0 for s in soft])
     old_v = (base + 0.3 * rng.standard_normal(B)).astype(np.float32) if old else None
+    if old:  # draws keep away from the clip's corners, where the slope is not defined
+        for corner in (0.8, 1 + hi):
+            old_v[np.abs(np.exp(base - old_v) - corner) < 1e-3] += np.float32(0.01)
     ref_v = (base + 0.5 * rng.standard_normal(B)).astype(np.float32) if ref else None
     adv = rng.standard_normal(B).astype(np.float32)
     w = rng.uniform(0.1, 1, B).astype(np.float32) if weights else None
@@ -193,7 +196,6 @@ def policy_case(dev, rng, x, dtype, tokens, mask, inv_t=1.0, kl=0.1, ent=0.0, ol
         kl_tol[r] = ABS * (1 + eq)
         row_tol[r] = ABS * slope + 2 * ABS * abs(ent)
         loss[r] = (1.0 / B if w is None else float(w[r])) * rows[r]
-        # the draws keep away from the clip's corners, where the slope is not defined
         if old_v is not None and s.joins and np.isfinite(rho):
             assert min(abs(rho - 0.8), abs(rho - 1 - hi)) > 1e-4
     near_rows(got.logp.cpu().numpy(), [s.logp for s in soft], "logp")
@@ -213,6 +215,20 @@ def policy_case(dev, rng, x, dtype, tokens, mask, inv_t=1.0, kl=0.1, ent=0.0, ol
 def test_policy_loss(dev, B, V, dtype, keep):
     rng, x, tokens, mask = make_rows(100 + V + B, B, V, dtype, keep)
     policy_case(dev, rng, x, dtype, tokens, mask, inv_t=1.0 if V % 2 else 1.25, ent=0.0 if B % 2 else 0.02)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("B,V,density", [(2, 262144, 0.5), (3, 100003, 1.0), (700, 2500, 0.9), (1, 32767, 0.99)])
+def test_wide_kept_sets(dev, dtype, B, V, density):
+    """Masks that keep far more ids than a sampler's, up to all of them."""
+    rng = np.random.default_rng(B + V)
+    x = (rng.standard_normal((B, V)) * 2).astype(np.float32)
+    tokens = rng.integers(0, V, B).astype(np.int32)
+    mask = (rng.random((B, V)) < density).astype(np.uint8)
+    mask[np.arange(B), tokens] = 1
+    if dtype == "bf16":
+        x = f32_to_bf16_bits(x)
+    policy_case(dev, rng, x, dtype, tokens, mask, ent=0.02)
 
 
 @pytest.mark.parametrize("kw", [dict(old=False), dict(ref=False), dict(weights=False), dict(kl=0.0), dict(gl=-3.0),

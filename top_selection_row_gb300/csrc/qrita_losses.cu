@@ -187,49 +187,22 @@ __device__ __forceinline__ uint4 load_unit(const void* p) { return *static_cast<
 template <int DT>
 struct Share {
   const unsigned char* x;  // the row's logits
-  const uint8_t* mask;     // its mask, or null
   int64_t V, head, nu, u_lo, u_hi;
   bool ends;               // this CTA has the head and the tail
-  bool mask_vec;           // a unit's mask bytes are one aligned word (or two)
 
   __device__ Share(const LossParams& p, int64_t row, uint32_t rank) {
     constexpr int U = Elem<DT>::kUnit;
     V = p.V;
     x = static_cast<const unsigned char*>(p.logits) + row * p.ld * Elem<DT>::kBytes;
-    mask = p.mask != nullptr ? p.mask + row * V : nullptr;
     head = ((16u - (reinterpret_cast<uintptr_t>(x) & 15u)) & 15u) / Elem<DT>::kBytes;
     if (head > V) head = V;
     nu = static_cast<int64_t>(static_cast<uint64_t>(V - head) / U);
     u_lo = min(nu, static_cast<int64_t>(rank) * p.per);
     u_hi = min(nu, u_lo + p.per);
     ends = rank == 0;
-    mask_vec = (reinterpret_cast<uintptr_t>(mask + head) & (U - 1)) == 0;
   }
 
   __device__ const void* unit(int64_t u) const { return x + (head * Elem<DT>::kBytes) + u * 16; }
-
-  // Bit i set: element i of unit u is kept.
-  __device__ uint32_t kept(int64_t u) const {
-    constexpr int U = Elem<DT>::kUnit;
-    const uint8_t* m = mask + head + u * U;
-    uint32_t w[U / 4];
-    if (mask_vec) {
-#pragma unroll
-      for (int i = 0; i < U / 4; ++i) w[i] = reinterpret_cast<const uint32_t*>(m)[i];
-    } else {
-#pragma unroll
-      for (int i = 0; i < U / 4; ++i)
-        w[i] = m[4 * i] | (m[4 * i + 1] << 8) | (m[4 * i + 2] << 16) | (static_cast<uint32_t>(m[4 * i + 3]) << 24);
-    }
-    uint32_t bits = 0;
-#pragma unroll
-    for (int i = 0; i < U / 4; ++i) {
-      // bit 7 of each nonzero byte, gathered into four bits by one multiply
-      const uint32_t nz = ((((w[i] & 0x7F7F7F7Fu) + 0x7F7F7F7Fu) | w[i]) >> 7) & 0x01010101u;
-      bits |= ((nz * 0x01020408u) >> 24) << (4 * i);
-    }
-    return bits;
-  }
 
   // Index of element i of the ends (head first, then tail), or -1 past them.
   __device__ int64_t end_index(int i) const {
@@ -394,6 +367,16 @@ __device__ __forceinline__ Stat merge_ranks(uint32_t C, float c, const Stat* ran
   return lanes_stat<ENT, kMaxRanks>(v, c);
 }
 
+// The cluster's sums from those the first warp of every CTA has, in that warp.
+// (Every CTA of the cluster is running by now.)
+template <bool ENT>
+__device__ __forceinline__ void cluster_stat(Stat& v, float c, uint32_t rank, uint32_t C, Stat* ranks) {
+  if (C == 1) return;
+  if (threadIdx.x < 32) send_stat<ENT>(v, rank, C, ranks);
+  cluster_sync_all();
+  if (threadIdx.x < 32) v = merge_ranks<ENT>(C, c, ranks);
+}
+
 // The row's sums from every thread's of its cluster of C CTAs, valid in the
 // first warp of every CTA.
 template <int THREADS, bool ENT>
@@ -403,12 +386,8 @@ __device__ __forceinline__ Stat row_stat(const Running<ENT>& r, float c, uint32_
   __syncthreads();
   Stat v;
   if (threadIdx.x < 32) v = warp_stat<THREADS, ENT>(c, slots);
-  if (C > 1) {
-    cluster_wait();  // (every CTA of the cluster is running)
-    if (threadIdx.x < 32) send_stat<ENT>(v, rank, C, slots.ranks);
-    cluster_sync_all();
-    if (threadIdx.x < 32) v = merge_ranks<ENT>(C, c, slots.ranks);
-  }
+  if (C > 1) cluster_wait();
+  cluster_stat<ENT>(v, c, rank, C, slots.ranks);
   return v;
 }
 
@@ -599,7 +578,7 @@ constexpr int kUnroll = 4;  // units a thread has in flight
 // Writes this CTA's share of a row's gradient. token < 0: no entry of its
 // own. Every unit is read and then written by the same thread, so the
 // gradient may lie over the logits.
-template <int THREADS, int DT, bool ENT, bool MASKED>
+template <int THREADS, int DT, bool ENT>
 __device__ __forceinline__ void write_grad(const LossParams& p, const Share<DT>& sh, int64_t row, const RowGrad& g,
                                            int64_t token) {
   using E = Elem<DT>;
@@ -628,17 +607,9 @@ __device__ __forceinline__ void write_grad(const LossParams& p, const Share<DT>&
   } else {
     for (int64_t u0 = sh.u_lo + threadIdx.x; u0 < sh.u_hi; u0 += THREADS * kUnroll) {
       uint4 w[kUnroll];
-      uint32_t bits[kUnroll];
 #pragma unroll
-      for (int k = 0; k < kUnroll; ++k) {
-        const int64_t u = u0 + k * THREADS;
-        bits[k] = u < sh.u_hi ? (MASKED ? sh.kept(u) : 1u) : 0u;
-      }
-#pragma unroll
-      for (int k = 0; k < kUnroll; ++k) {
-        w[k] = make_uint4(0u, 0u, 0u, 0u);
-        if (bits[k] != 0u) w[k] = load_unit(sh.unit(u0 + k * THREADS));
-      }
+      for (int k = 0; k < kUnroll; ++k)
+        if (u0 + k * THREADS < sh.u_hi) w[k] = load_unit(sh.unit(u0 + k * THREADS));
 #pragma unroll
       for (int k = 0; k < kUnroll; ++k) {
         const int64_t u = u0 + k * THREADS;
@@ -651,10 +622,6 @@ __device__ __forceinline__ void write_grad(const LossParams& p, const Share<DT>&
           const float2 e = make_float2(ex2(y.x), ex2(y.y));
           v[i] = ENT ? mul2(e, fma2(hh, make_float2(y.x < kMinExp ? kMinExp : y.x, y.y < kMinExp ? kMinExp : y.y), aa))
                      : mul2(e, aa);
-          if (MASKED) {
-            if (!(bits[k] >> (2 * i) & 1u)) v[i].x = 0.f;
-            if (!(bits[k] >> (2 * i + 1) & 1u)) v[i].y = 0.f;
-          }
         }
         put(u, v);
       }
@@ -664,7 +631,7 @@ __device__ __forceinline__ void write_grad(const LossParams& p, const Share<DT>&
     const int64_t j = sh.end_index(threadIdx.x);
     if (j >= 0) {
       float v = 0.f;
-      if (!zero && (!MASKED || sh.mask[j] != 0)) v = grad_one<ENT>(E::load(sh.x, j), g, p.c);
+      if (!zero) v = grad_one<ENT>(E::load(sh.x, j), g, p.c);
       E::store(grow, j, v);
     }
   }
@@ -683,7 +650,7 @@ __device__ __forceinline__ void write_grad(const LossParams& p, const Share<DT>&
 // streams its share of the row, the shares merge through distributed shared
 // memory, and rank 0 writes the row's values. A gradient takes a second pass
 // over the share.
-template <int DT, bool ENT, bool MASKED>
+template <int DT, bool ENT>
 __global__ void __launch_bounds__(kLossThreads, kLossBlocks) row_kernel(const LossParams p, RowStat* stats, int op) {
   using E = Elem<DT>;
   constexpr int N = E::kUnit / 2;
@@ -700,55 +667,32 @@ __global__ void __launch_bounds__(kLossThreads, kLossBlocks) row_kernel(const Lo
   RowGrad g = {0.f, 0.f, 0.f, 0.f};
   if (token < 0 || token >= p.V) {  // (the same in every CTA of the cluster)
     if (threadIdx.x == 0 && rank == 0) row_ignored(p, op, stats, row);
-    if (p.grad != nullptr) write_grad<kLossThreads, DT, ENT, MASKED>(p, sh, row, g, -1);
+    if (p.grad != nullptr) write_grad<kLossThreads, DT, ENT>(p, sh, row, g, -1);
     return;
   }
   if (C > 1) cluster_arrive_relaxed();  // every CTA of the cluster runs before its memory is written
   if (threadIdx.x == 32) in = row_in<DT>(p, op, row, token);  // (read after the sums' barrier)
   Running<ENT> run;
-  auto add = [&](uint4 w, uint32_t bits) {
-    float2 x[N];
-    E::unpack(w, x);
-    if (MASKED) {
-#pragma unroll
-      for (int i = 0; i < N; ++i) {
-        if (!(bits >> (2 * i) & 1u)) x[i].x = -INFINITY;
-        if (!(bits >> (2 * i + 1) & 1u)) x[i].y = -INFINITY;
-      }
-    }
-    run.add_unit(x, p.c);
-  };
   int64_t u0 = sh.u_lo + threadIdx.x;
   // whole steps of the block first: no unit of theirs needs a check
   for (int64_t full = sh.u_lo + (sh.u_hi - sh.u_lo) / (kLossThreads * kUnroll) * (kLossThreads * kUnroll); u0 < full;
        u0 += kLossThreads * kUnroll) {
     uint4 w[kUnroll];
-    uint32_t bits[kUnroll];
-    if (MASKED) {
+    float2 x[kUnroll * N];
 #pragma unroll
-      for (int k = 0; k < kUnroll; ++k) bits[k] = sh.kept(u0 + k * kLossThreads);
-    }
+    for (int k = 0; k < kUnroll; ++k) w[k] = load_unit(sh.unit(u0 + k * kLossThreads));
 #pragma unroll
-    for (int k = 0; k < kUnroll; ++k)
-      if (!MASKED || bits[k] != 0u) w[k] = load_unit(sh.unit(u0 + k * kLossThreads));
-    if (MASKED) {
-#pragma unroll
-      for (int k = 0; k < kUnroll; ++k)
-        if (bits[k] != 0u) add(w[k], bits[k]);
-    } else {
-      float2 x[kUnroll * N];
-#pragma unroll
-      for (int k = 0; k < kUnroll; ++k) E::unpack(w[k], reinterpret_cast<float2(&)[N]>(x[k * N]));
-      run.add_unit(x, p.c);
-    }
+    for (int k = 0; k < kUnroll; ++k) E::unpack(w[k], reinterpret_cast<float2(&)[N]>(x[k * N]));
+    run.add_unit(x, p.c);
   }
   for (; u0 < sh.u_hi; u0 += kLossThreads) {
-    const uint32_t bits = MASKED ? sh.kept(u0) : 1u;
-    if (bits != 0u) add(load_unit(sh.unit(u0)), bits);
+    float2 x[N];
+    E::unpack(load_unit(sh.unit(u0)), x);
+    run.add_unit(x, p.c);
   }
   if (sh.ends && threadIdx.x < Share<DT>::kEnds) {
     const int64_t j = sh.end_index(threadIdx.x);
-    if (j >= 0 && (!MASKED || sh.mask[j] != 0)) run.add_one(E::load(sh.x, j), p.c);
+    if (j >= 0) run.add_one(E::load(sh.x, j), p.c);
   }
   const Stat st = row_stat(run, p.c, rank, C, slots);
   RowVals v;
@@ -761,7 +705,257 @@ __global__ void __launch_bounds__(kLossThreads, kLossBlocks) row_kernel(const Lo
   __syncthreads();
   if (threadIdx.x == 0 && rank == 0) row_out<ENT>(p, op, stats, row, in, st, v);
   g = grad;
-  write_grad<kLossThreads, DT, ENT, MASKED>(p, sh, row, g, MASKED && sh.mask[token] == 0 ? -1 : token);
+  write_grad<kLossThreads, DT, ENT>(p, sh, row, g, token);
+}
+
+// ---------------------------------------------------------------------------
+// The same over a kept set. Masks keep tens to thousands of a row's ids, so the
+// mask is what is read whole, 16 ids to a load, and the kept ids go on a list in
+// shared memory; then all their logits are loaded at once (a load for each as
+// it is found would put one memory latency after another). The gradient is a
+// row of zeros, stored while the sums are taken, with the listed entries put
+// over them. The list's order is that of the atomics on its length: its sums
+// are taken in 64-bit fixed point, which no order changes. Rows that keep more
+// than a CTA's list holds are walked unit by unit instead, twice.
+// ---------------------------------------------------------------------------
+constexpr int kKeptUnit = 16;
+constexpr int kKeptList = 2048;  // entries of a CTA's list
+// A listed logit weighs at most 1 and a CTA lists at most 2^11: sums stay
+// below 2^63 at this scale, and a weight is rounded by 2^-48 of the largest.
+constexpr float kKeptScale = 0x1p47f;
+
+__device__ __forceinline__ F2 kept_pair(unsigned long long v) {
+  const F2 a = f2_from_u64(v);
+  return f2_make(a.hi * 0x1p-47f, a.lo * 0x1p-47f);
+}
+
+// Kept bits of 16 mask bytes: bit 7 of each nonzero byte, gathered into four
+// bits a word by one multiply.
+__device__ __forceinline__ uint32_t kept_bits(const uint4 m) {
+  if ((m.x | m.y | m.z | m.w) == 0u) return 0u;
+  const uint32_t w[4] = {m.x, m.y, m.z, m.w};
+  uint32_t bits = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t nz = ((((w[i] & 0x7F7F7F7Fu) + 0x7F7F7F7Fu) | w[i]) >> 7) & 0x01010101u;
+    bits |= ((nz * 0x01020408u) >> 24) << (4 * i);
+  }
+  return bits;
+}
+
+// Zeros to elements [lo, hi) of a row, by the whole block.
+template <int DT>
+__device__ __forceinline__ void zero_range(unsigned char* grow, int64_t lo, int64_t hi) {
+  using E = Elem<DT>;
+  const uintptr_t a = reinterpret_cast<uintptr_t>(grow + lo * E::kBytes), b = reinterpret_cast<uintptr_t>(grow + hi * E::kBytes);
+  uintptr_t va = (a + 15u) & ~static_cast<uintptr_t>(15u), vb = b & ~static_cast<uintptr_t>(15u);
+  if (va > vb) va = vb = b;  // no whole unit: all of it is the head
+  for (uintptr_t q = va + 16u * threadIdx.x; q < vb; q += 16u * kLossThreads)
+    *reinterpret_cast<uint4*>(q) = make_uint4(0u, 0u, 0u, 0u);
+  const int64_t head = static_cast<int64_t>(va - a) / E::kBytes, tail = static_cast<int64_t>(b - vb) / E::kBytes;
+  if (threadIdx.x < head) E::store(grow, lo + threadIdx.x, 0.f);
+  if (threadIdx.x < tail) E::store(grow, hi - tail + threadIdx.x, 0.f);
+}
+
+template <int DT, bool ENT>
+__global__ void __launch_bounds__(kLossThreads, kLossBlocks) kept_kernel(const LossParams p, int op) {
+  using E = Elem<DT>;
+  __shared__ StatSlots<kLossThreads> slots;
+  __shared__ RowGrad grad;
+  __shared__ RowIn in;
+  __shared__ int count;
+  __shared__ unsigned long long sums[2];
+  __shared__ int2 list[kKeptList];  // id within the CTA's range, logit
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const int tid = threadIdx.x;
+  const uint32_t C = p.C;
+  const int64_t row = cluster_id();
+  const uint32_t rank = C > 1 ? cluster_rank() : 0u;
+  const int64_t token = p.tokens[row];
+  const int64_t V = p.V;
+  const unsigned char* xrow = static_cast<const unsigned char*>(p.logits) + row * p.ld * E::kBytes;
+  const uint8_t* mrow = p.mask + row * V;
+  unsigned char* grow = p.grad != nullptr ? static_cast<unsigned char*>(p.grad) + row * p.ld_grad * E::kBytes : nullptr;
+  // units of 16 ids on the mask's 16-byte boundaries; the ids before the first
+  // unit are rank 0's, those behind the last one the last rank's
+  const int64_t head = min(V, static_cast<int64_t>((16u - (reinterpret_cast<uintptr_t>(mrow) & 15u)) & 15u));
+  const int64_t nu = static_cast<int64_t>(static_cast<uint64_t>(V - head) / kKeptUnit);
+  const int64_t u_lo = min(nu, static_cast<int64_t>(rank) * p.per), u_hi = rank == C - 1 ? nu : min(nu, u_lo + p.per);
+  const int64_t lo = rank == 0 ? 0 : head + u_lo * kKeptUnit, hi = rank == C - 1 ? V : head + u_hi * kKeptUnit;
+  if (token < 0 || token >= V) {  // (the same in every CTA of the cluster)
+    if (tid == 0 && rank == 0) row_ignored(p, op, nullptr, row);
+    if (grow != nullptr) zero_range<DT>(grow, lo, hi);
+    return;
+  }
+  if (C > 1) cluster_arrive_relaxed();  // every CTA of the cluster runs before its memory is written
+  if (tid == 0) {
+    count = 0;
+    sums[0] = sums[1] = 0ull;
+  }
+  if (tid == 32) in = row_in<DT>(p, op, row, token);  // (read after the sums' barrier)
+  __syncthreads();
+  for (int64_t u0 = u_lo + tid; u0 < u_hi; u0 += kLossThreads * kUnroll) {
+    if (*reinterpret_cast<volatile int*>(&count) > kKeptList) break;  // no list for this row
+    uint4 m[kUnroll];
+#pragma unroll
+    for (int k = 0; k < kUnroll; ++k) {
+      const int64_t u = u0 + k * kLossThreads;
+      m[k] = u < u_hi ? load_unit(mrow + head + u * kKeptUnit) : make_uint4(0u, 0u, 0u, 0u);
+    }
+#pragma unroll
+    for (int k = 0; k < kUnroll; ++k) {
+      uint32_t bits = kept_bits(m[k]);
+      if (bits == 0u || *reinterpret_cast<volatile int*>(&count) > kKeptList) continue;
+      int at = atomicAdd(&count, __popc(bits));
+      const int j = static_cast<int>(head + (u0 + k * kLossThreads) * kKeptUnit - lo);
+      for (; bits != 0u && at < kKeptList; ++at, bits &= bits - 1u) list[at].x = j + __ffs(bits) - 1;
+    }
+  }
+  int64_t end_j = -1;  // this thread's id before the first unit or behind the last
+  if (rank == 0 && tid < head) end_j = tid;
+  const int64_t tail = head + nu * kKeptUnit;
+  if (rank == C - 1 && tid >= 32 && tail + tid - 32 < V) end_j = tail + tid - 32;
+  if (end_j >= 0 && mrow[end_j] != 0) {
+    const int at = atomicAdd(&count, 1);
+    if (at < kKeptList) list[at].x = static_cast<int>(end_j - lo);
+  }
+  __syncthreads();
+  const bool listed = count <= kKeptList;
+  const bool over_logits = p.grad == p.logits;
+  const bool vec = (reinterpret_cast<uintptr_t>(xrow + head * E::kBytes) & 15u) == 0;
+  // A row walked unit by unit takes 16 bytes of logits at a time: U of them
+  // with their U mask bytes (aligned: the units of 16 ids are).
+  constexpr int U = E::kUnit, N = U / 2;
+  const int64_t e_lo = head + u_lo * kKeptUnit, n_u = (u_hi - u_lo) * (kKeptUnit / U);
+  auto bits_of = [&](int64_t u) {
+    uint4 m = make_uint4(0u, 0u, 0u, 0u);
+    const uint32_t* w = reinterpret_cast<const uint32_t*>(mrow + e_lo + u * U);
+    m.x = w[0];
+    if (U == 8) m.y = w[1];
+    return kept_bits(m);
+  };
+  // logits of unit u, -inf where they are not kept
+  auto unit = [&](int64_t u, uint32_t bits, float2 (&x)[N]) {
+    const int64_t j = e_lo + u * U;
+    if (vec) E::unpack(load_unit(xrow + j * E::kBytes), x);
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const bool a = bits >> (2 * i) & 1u, b = bits >> (2 * i + 1) & 1u;
+      x[i].x = !a ? -INFINITY : vec ? x[i].x : E::load(xrow, j + 2 * i);
+      x[i].y = !b ? -INFINITY : vec ? x[i].y : E::load(xrow, j + 2 * i + 1);
+    }
+  };
+  Stat st;
+  if (listed) {
+    float m = -INFINITY;
+    bool bad = false;  // NaN has no fixed point
+    for (int i = tid; i < count; i += kLossThreads) {
+      const float x = E::load(xrow, lo + list[i].x);
+      list[i].y = __float_as_int(x);
+      m = fmaxf(m, x);
+      bad = bad || x != x || x == INFINITY;
+    }
+    if (grow != nullptr && !over_logits) zero_range<DT>(grow, lo, hi);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kAll, m, o));
+    if ((tid & 31) == 0) slots.m[tid >> 5] = m;
+    bad = __syncthreads_or(bad);
+    for (int w = 0; w < kLossThreads / 32; ++w) m = fmaxf(m, slots.m[w]);
+    unsigned long long s = 0ull, t = 0ull;
+    for (int i = tid; i < count; i += kLossThreads) {
+      const float x = __int_as_float(list[i].y);
+      const float y = x == -INFINITY ? kMinExp : fmaxf((x - m) * p.c, kMinExp);
+      const float e = bad ? 0.f : ex2(y);
+      s += round_u64(e * kKeptScale);
+      if (ENT) t += round_u64(e * -y * kKeptScale);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      s += __shfl_xor_sync(kAll, s, o);
+      if (ENT) t += __shfl_xor_sync(kAll, t, o);
+    }
+    if ((tid & 31) == 0) {
+      atomicAdd(&sums[0], s);
+      if (ENT) atomicAdd(&sums[1], t);
+    }
+    __syncthreads();
+    st.m = m;
+    st.s = bad ? f2_make(NAN, NAN) : kept_pair(sums[0]);
+    st.t = bad ? f2_make(NAN, NAN) : kept_pair(sums[1]);
+    st.t = f2_make(-st.t.hi, -st.t.lo);
+  } else {
+    Running<ENT> run;
+    int64_t u = tid;
+    for (; u + (kUnroll - 1) * kLossThreads < n_u; u += kUnroll * kLossThreads) {
+      uint32_t bits[kUnroll];
+      float2 x[kUnroll * N];
+#pragma unroll
+      for (int k = 0; k < kUnroll; ++k) bits[k] = bits_of(u + k * kLossThreads);
+#pragma unroll
+      for (int k = 0; k < kUnroll; ++k) unit(u + k * kLossThreads, bits[k], reinterpret_cast<float2(&)[N]>(x[k * N]));
+      run.add_unit(x, p.c);
+    }
+    for (; u < n_u; u += kLossThreads) {
+      float2 x[N];
+      unit(u, bits_of(u), x);
+      run.add_unit(x, p.c);
+    }
+    if (end_j >= 0 && mrow[end_j] != 0) run.add_one(E::load(xrow, end_j), p.c);
+    put_stat(run, slots);
+    __syncthreads();
+    if (tid < 32) st = warp_stat<kLossThreads, ENT>(p.c, slots);
+  }
+  if (C > 1) cluster_wait();
+  cluster_stat<ENT>(st, p.c, rank, C, slots.ranks);
+  RowVals v;
+  if (tid == 0 && (rank == 0 || grow != nullptr)) {
+    v = row_vals<ENT>(p, in, st);
+    if (grow != nullptr || op == kOpPolicy) grad = row_weights<ENT>(p, op, in, st, v);
+    if (grow == nullptr) row_out<ENT>(p, op, nullptr, row, in, st, v);
+  }
+  if (grow == nullptr) return;
+  __syncthreads();
+  if (tid == 0 && rank == 0) row_out<ENT>(p, op, nullptr, row, in, st, v);
+  const RowGrad g = grad;
+  const bool zero = g.a == 0.f && g.h == 0.f;
+  if (listed) {
+    if (over_logits) {  // (the other CTAs have read the token's logit by now)
+      zero_range<DT>(grow, lo, hi);
+      __syncthreads();
+    }
+    if (!zero)
+      for (int i = tid; i < count; i += kLossThreads)
+        E::store(grow, lo + list[i].x, grad_one<ENT>(__int_as_float(list[i].y), g, p.c));
+  } else {
+    const bool gvec = (reinterpret_cast<uintptr_t>(grow + head * E::kBytes) & 15u) == 0;
+    for (int64_t u = tid; u < n_u; u += kLossThreads) {
+      const uint32_t bits = zero ? 0u : bits_of(u);
+      const int64_t j = e_lo + u * U;
+      float2 x[N];
+      if (bits != 0u) unit(u, bits, x);
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        x[i].x = bits >> (2 * i) & 1u ? grad_one<ENT>(x[i].x, g, p.c) : 0.f;
+        x[i].y = bits >> (2 * i + 1) & 1u ? grad_one<ENT>(x[i].y, g, p.c) : 0.f;
+      }
+      if (gvec) {
+        *reinterpret_cast<uint4*>(grow + j * E::kBytes) = E::pack(x);
+      } else {
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+          E::store(grow, j + 2 * i, x[i].x);
+          E::store(grow, j + 2 * i + 1, x[i].y);
+        }
+      }
+    }
+    if (end_j >= 0)
+      E::store(grow, end_j, !zero && mrow[end_j] != 0 ? grad_one<ENT>(E::load(xrow, end_j), g, p.c) : 0.f);
+  }
+  if (in.kept_t && token >= lo && token < hi) {
+    __syncthreads();
+    if (tid == 0) E::store(grow, token, g.at);
+  }
 }
 
 // ---------------------------------------------------------------------------
@@ -858,7 +1052,7 @@ __global__ void __launch_bounds__(kResThreads, kResBlocks) resident_kernel(const
   if (token < 0 || token >= p.V) {  // (the same in every CTA of the cluster)
     if (MOVED && warp == 1) tmem_waive();
     if (tid == 0 && rank == 0) row_ignored(p, op, nullptr, row);
-    write_grad<kResThreads, DT, ENT, false>(p, sh, row, g, -1);
+    write_grad<kResThreads, DT, ENT>(p, sh, row, g, -1);
     return;
   }
   if (C > 1) cluster_arrive_relaxed();  // every CTA of the cluster runs before its memory is written
@@ -932,7 +1126,7 @@ __global__ void __launch_bounds__(kResThreads, kResBlocks) resident_kernel(const
   unsigned char* grow = static_cast<unsigned char*>(p.grad) + row * p.ld_grad * E::kBytes;
   unsigned char* gu = grow + (sh.head + sh.u_lo * E::kUnit) * E::kBytes;
   if (g.a == 0.f && g.h == 0.f) {
-    write_grad<kResThreads, DT, ENT, false>(p, sh, row, g, token);
+    write_grad<kResThreads, DT, ENT>(p, sh, row, g, token);
   } else {
     const float2 nm = both(-g.m), cc = both(p.c), aa = both(g.a), hh = both(g.h);
     auto entries = [&](uint4 w, float2 (&e)[N]) {
@@ -1147,14 +1341,13 @@ __global__ void __launch_bounds__(kLossThreads, 4) pref_grad_kernel(const LossPa
     grad_token = token;
   }
   __syncthreads();
-  write_grad<kLossThreads, DT, false, false>(p, sh, row, grad, grad_token);
+  write_grad<kLossThreads, DT, false>(p, sh, row, grad, grad_token);
 }
 
 // CTAs per row: as many as fill the device (a power of two), with at least a
 // unit or two for each thread; and enough that the rows in flight fit in L2
 // when a second pass follows.
-uint32_t row_ctas(const LossParams& p, int dtype, bool second_pass, int per_sm) {
-  const int64_t bytes = p.V * (dtype == QRITA_DTYPE_F32 ? 4 : 2);
+uint32_t row_ctas(const LossParams& p, int64_t bytes, bool second_pass, int per_sm) {
   const int sms = device_sms();
   const int64_t slots = static_cast<int64_t>(sms) * per_sm;
   uint32_t C = 1;
@@ -1192,10 +1385,10 @@ cudaError_t launch(F* fn, unsigned grid, unsigned block, unsigned cluster, cudaS
   return e != cudaSuccess ? e : last;
 }
 
-// p for C CTAs a row.
-LossParams with_ctas(const LossParams& p, int dtype, uint32_t C) {
+// p for C CTAs a row, which share its units of so many elements.
+LossParams with_ctas(const LossParams& p, int64_t unit, uint32_t C) {
   LossParams q = p;
-  const int64_t units = p.V / (dtype == QRITA_DTYPE_F32 ? 4 : 8);
+  const int64_t units = p.V / unit;
   q.C = C;
   q.per = (units + C - 1) / C;
   return q;
@@ -1217,7 +1410,7 @@ uint32_t resident_ctas(const LossParams& p, int dtype) {
 
 template <int DT, bool ENT>
 cudaError_t launch_resident(const LossParams& p, int op, uint32_t C, cudaStream_t st) {
-  const LossParams q = with_ctas(p, DT, C);
+  const LossParams q = with_ctas(p, Elem<DT>::kUnit, C);
   if (q.per > kResidentUnits) return cudaErrorInvalidValue;  // (a share past its storage)
   const int64_t pieces = (q.per + kPieceUnits - 1) / kPieceUnits;
   const size_t smem = static_cast<size_t>(pieces < kSlots ? pieces : kSlots) * kPiece;
@@ -1232,14 +1425,18 @@ cudaError_t launch_resident(const LossParams& p, int op, uint32_t C, cudaStream_
 
 template <int DT, bool ENT>
 cudaError_t launch_rows_of(const LossParams& p, int op, RowStat* stats, cudaStream_t st) {
-  if (p.grad != nullptr && p.mask == nullptr) {
-    uint32_t C = resident_ctas(p, DT);
+  if (p.mask != nullptr) {
+    const uint32_t C = row_ctas(p, p.V, false, kLossBlocks);
+    return launch(&kept_kernel<DT, ENT>, static_cast<unsigned>(p.B * C), kLossThreads, C, st, size_t(0),
+                  with_ctas(p, kKeptUnit, C), op);
+  }
+  if (p.grad != nullptr) {
+    const uint32_t C = resident_ctas(p, DT);
     if (C > 0) return launch_resident<DT, ENT>(p, op, C, st);
   }
-  const uint32_t C = row_ctas(p, DT, p.grad != nullptr, kLossBlocks);
-  const unsigned grid = static_cast<unsigned>(p.B * C);
-  return p.mask != nullptr ? launch(&row_kernel<DT, ENT, true>, grid, kLossThreads, C, st, size_t(0), with_ctas(p, DT, C), stats, op)
-                           : launch(&row_kernel<DT, ENT, false>, grid, kLossThreads, C, st, size_t(0), with_ctas(p, DT, C), stats, op);
+  const uint32_t C = row_ctas(p, p.V * Elem<DT>::kBytes, p.grad != nullptr, kLossBlocks);
+  return launch(&row_kernel<DT, ENT>, static_cast<unsigned>(p.B * C), kLossThreads, C, st, size_t(0),
+                with_ctas(p, Elem<DT>::kUnit, C), stats, op);
 }
 
 cudaError_t launch_rows(const LossParams& p, int dtype, int op, bool ent, RowStat* stats, cudaStream_t st) {
@@ -1299,10 +1496,11 @@ int launch_preference(const LossParams& p, const PrefParams& q, int dtype, qrita
   if (p.B == 0 || p.grad == nullptr) {
     e = launch_sum(q.pair_loss, q.weights, q.P, p.loss, st);
   } else {  // (whose first CTA sums the loss)
-    const uint32_t C = row_ctas(p, dtype, true, 4);
+    const int bytes = dtype == QRITA_DTYPE_F32 ? 4 : 2;
+    const uint32_t C = row_ctas(p, p.V * bytes, true, 4);
     const unsigned grid = static_cast<unsigned>(p.B * C);
     auto* fn = dtype == QRITA_DTYPE_F32 ? &pref_grad_kernel<QRITA_DTYPE_F32> : &pref_grad_kernel<QRITA_DTYPE_BF16>;
-    e = launch(fn, grid, kLossThreads, 1u, st, size_t(0), with_ctas(p, dtype, C), q, static_cast<const RowStat*>(stats),
+    e = launch(fn, grid, kLossThreads, 1u, st, size_t(0), with_ctas(p, 16 / bytes, C), q, static_cast<const RowStat*>(stats),
                static_cast<const double*>(coef));
   }
   return static_cast<int>(e);
