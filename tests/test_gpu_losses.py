@@ -311,6 +311,73 @@ def test_preference_options(dev, kw):
     pref_case(dev, 21, [4, 6, 2, 9], 777, "bf16", **kw)
 
 
+@pytest.mark.parametrize("dtype,lens,V,kw", [
+    ("bf16", [700, 800], 2003, {}),                    # a pair of more rows than wait for its end
+    ("f32", [2, 3, 480, 300, 1, 1], 8000, dict(before=2, behind=1)),
+    ("bf16", [40, 60, 55, 33, 47, 52, 61, 39], 5000, dict(norm=True)),
+])
+def test_preference_over_many_rows(dev, dtype, lens, V, kw):
+    pref_case(dev, sum(lens), lens, V, dtype, **kw)
+
+
+# rows past what a cluster holds on chip (16 x 56 KB)
+@pytest.mark.parametrize("dtype,V", [("bf16", 600001), ("f32", 300007)])
+def test_rows_longer_than_a_cluster_holds(dev, dtype, V):
+    import torch
+
+    import top_selection_row_gb300 as q
+
+    rng, x, tokens, _ = make_rows(V, 5, V, dtype)
+    policy_case(dev, rng, x, dtype, tokens, None, ent=0.02)
+    a = rng.standard_normal(5).astype(np.float32)
+    xd = to_device(x, dtype, dev)
+    soft = softmaxes(x, dtype, None, tokens)
+    got = q.qrita_token_logprobs_grad(xd, put(dev, tokens), put(dev, a), out_grad=xd.clone())
+    near_grad(got, dtype, soft, tokens, a, np.zeros(5), np.zeros(5), 1.0)
+    over = q.qrita_token_logprobs_grad(xd, put(dev, tokens), put(dev, a), out_grad=xd)
+    assert torch.equal(over, got)
+    pref_case(dev, V + 1, [2, 2], V, dtype)
+
+
+def test_preference_with_bad_starts_touches_nothing_else(dev):
+    """Starts out of order or out of range leave everything outside the
+    arguments as it was, and a later call is right."""
+    import torch
+
+    import top_selection_row_gb300 as q
+
+    rng, x, tokens, _ = make_rows(5, 9, 301, "f32")
+    xd, td = to_device(x, "f32", dev), put(dev, tokens)
+    flat = torch.full((11, 301), 7.0, device=dev)
+    for bad in ([-5, 3, 2, 7, 99], [9, 0, 9, 0, 9], [2**31 - 1, -(2**31), 4, 4, 4]):
+        q.qrita_preference_loss(xd, td, put(dev, np.array(bad, np.int32)), out_grad=flat[1:10])
+        assert (flat[0] == 7).all() and (flat[10] == 7).all()
+    pref_case(dev, 5, [2, 3, 1, 3], 301, "f32")
+
+
+def test_preference_calls_at_the_same_time(dev):
+    """Two calls on two streams, each with pairs that could fill the device:
+    rows that wait for their pair may find its rest not running."""
+    import torch
+
+    import top_selection_row_gb300 as q
+
+    rng = np.random.default_rng(2)
+    B, V = 900, 32000
+    xs = [torch.from_numpy((rng.standard_normal((B, V)) * 2).astype(np.float32)).to(dev).bfloat16() for _ in range(2)]
+    t = put(dev, rng.integers(0, V, B).astype(np.int32))
+    starts = put(dev, np.array([0, 200, 420, 700, 900], np.int32))
+    want = [q.qrita_preference_loss(x, t, starts) for x in xs]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for _ in range(4):
+        got = [q.qrita_preference_loss(x, t, starts, stream=s) for x, s in zip(xs, streams)]
+        torch.cuda.synchronize()
+        for a, b in zip(got, want):
+            for u, v in zip(a, b):
+                assert torch.equal(u, v)
+
+
 def test_preference_without_pairs_or_rows(dev):
     got = pref_case(dev, 3, [], 40, "f32", before=2, behind=3)
     assert float(got.loss) == 0.0 and not got.grad.any()

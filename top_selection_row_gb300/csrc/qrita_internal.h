@@ -137,6 +137,7 @@ struct PrefParams {
   const float* weights;
   double beta, smoothing, margin;
   int length_norm;
+  float inv_p;  // 1 / P
   float* pair_loss;
   float* log_ratio;
   float* seq_logp;

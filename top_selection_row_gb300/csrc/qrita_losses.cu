@@ -53,7 +53,7 @@ constexpr float kExLow = 5.0e-8f;
 enum Op : int { kOpLogprobs, kOpGrad, kOpPolicy, kOpPrefStats };
 
 // g_j = 2^y_j (a + h y_j), y_j = (x_j - m) c; the token's own entry is `at`.
-struct RowGrad {
+struct alignas(16) RowGrad {
   float m, a, h, at;
 };
 
@@ -590,7 +590,7 @@ __device__ __forceinline__ void write_grad(const LossParams& p, const Share<DT>&
   const float2 nm = both(-g.m), cc = both(p.c), aa = both(g.a), hh = both(g.h);
   auto put = [&](int64_t u, const float2 (&v)[N]) {
     if (vec) {
-      *reinterpret_cast<uint4*>(gu + u * 16) = E::pack(v);
+      __stcs(reinterpret_cast<uint4*>(gu + u * 16), E::pack(v));
     } else {
 #pragma unroll
       for (int i = 0; i < N; ++i) {
@@ -609,7 +609,7 @@ __device__ __forceinline__ void write_grad(const LossParams& p, const Share<DT>&
       uint4 w[kUnroll];
 #pragma unroll
       for (int k = 0; k < kUnroll; ++k)
-        if (u0 + k * THREADS < sh.u_hi) w[k] = load_unit(sh.unit(u0 + k * THREADS));
+        if (u0 + k * THREADS < sh.u_hi) w[k] = __ldcs(static_cast<const uint4*>(sh.unit(u0 + k * THREADS)));
 #pragma unroll
       for (int k = 0; k < kUnroll; ++k) {
         const int64_t u = u0 + k * THREADS;
@@ -1223,125 +1223,125 @@ __global__ void __launch_bounds__(kSumThreads) weighted_sum_kernel(const float* 
   weighted_sum<kSumThreads>(v, w, n, out, slots);
 }
 
-// Row [lo, hi) of sequence s, within [0, B] whatever starts holds.
-__device__ __forceinline__ void sequence_rows(const int32_t* starts, int64_t s, int64_t B, int64_t& lo, int64_t& hi) {
-  lo = min(max(static_cast<int64_t>(starts[s]), int64_t(0)), B);
-  hi = min(max(static_cast<int64_t>(starts[s + 1]), lo), B);
+// ---------------------------------------------------------------------------
+// Preference loss: the rows' sums, the pairs, the rows' gradient, a kernel
+// each. The gradient needs the sums of both sequences of its pair, so logits are
+// read twice. (Measured and not kept: one persistent kernel that takes a pair's
+// gradient right after its sums, for its second reads to hit L2, 1.6 to 2 times
+// the time, as every share then ends in a fence and an atomic; rows that wait on
+// the SM for their pair and write without a second read, 1.3 to 1.5 times, as
+// reads and writes then take turns, and writes alone run at 4.0 TB/s here.)
+// ---------------------------------------------------------------------------
+
+// log(1 + e^x), x = hi + lo, and the sigmoid.
+__device__ __forceinline__ float softplus(float hi, float lo) {
+  return fmaxf(hi, 0.f) + (hi > 0.f ? lo : 0.f) + log1pf(expf(-fabsf(hi)) * (1.f - copysignf(1.f, hi) * lo));
+}
+__device__ __forceinline__ float sigmoid(float x) { return 1.f / (1.f + expf(-x)); }
+
+constexpr int kPairThreads = 256;
+
+// The sum of one value per thread over the block in a fixed order, in every thread.
+__device__ __forceinline__ double pair_sum(double v, double* slots) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(kAll, v, o);
+  __syncthreads();
+  if ((threadIdx.x & 31) == 0) slots[threadIdx.x >> 5] = v;
+  __syncthreads();
+  v = 0.0;
+  for (int k = 0; k < kPairThreads / 32; ++k) v += slots[k];
+  return v;
 }
 
-// softplus(x) = log(1 + e^x) without overflow
-__device__ __forceinline__ double softplus(double x) { return fmax(x, 0.0) + log1p(exp(-fabs(x))); }
-__device__ __forceinline__ double sigmoid(double x) { return 1.0 / (1.0 + exp(-x)); }
-
-constexpr int kPairThreads = 128;
-
-// One CTA per pair: the two sequences' sums in a fixed order, the pair's loss
-// and the weight of dlogp of each sequence's rows.
+// One CTA per pair, and one more: the two sequences' sums in a fixed order, the
+// pair's loss, and the gradient weights of its rows; the last CTA has the rows
+// that no sequence owns.
 __global__ void __launch_bounds__(kPairThreads) pair_kernel(const LossParams p, const PrefParams q,
-                                                            const RowStat* stats, double* coef) {
+                                                            const RowStat* stats, RowGrad* grads) {
+  __shared__ double slots[kPairThreads / 32];
+  __shared__ float slope[2];
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  __shared__ double sum_slots[kPairThreads / 32];
-  __shared__ int cnt_slots[kPairThreads / 32];
   const int64_t i = blockIdx.x;
-  if (i == 0 && p.logp != nullptr) {
-    // rows of no sequence: those before the first and from the last's end on
-    const int64_t lo = q.P > 0 ? min(max(static_cast<int64_t>(q.starts[0]), int64_t(0)), p.B) : p.B;
-    const int64_t hi = q.P > 0 ? min(max(static_cast<int64_t>(q.starts[2 * q.P]), lo), p.B) : p.B;
-    for (int64_t row = threadIdx.x; row < lo; row += kPairThreads) p.logp[row] = 0.f;
-    for (int64_t row = hi + threadIdx.x; row < p.B; row += kPairThreads) p.logp[row] = 0.f;
+  const int tid = threadIdx.x;
+  const int32_t B = static_cast<int32_t>(p.B);
+  // within [0, B] and in order within the pair, whatever starts holds
+  int32_t at[3] = {0, 0, 0};
+  for (int k = 0; k < 3; ++k)
+    if (2 * i + k <= 2 * q.P && q.P > 0) at[k] = min(max(q.starts[2 * i + k], k > 0 ? at[k - 1] : 0), B);
+  auto outside = [&](int64_t row) {
+    if (p.logp != nullptr) p.logp[row] = 0.f;
+    if (p.grad != nullptr) grads[row] = RowGrad{0.f, 0.f, 0.f, 0.f};
+  };
+  if (i >= q.P) {
+    const int32_t lo = q.P > 0 ? min(max(q.starts[0], 0), B) : B;
+    for (int64_t row = tid; row < lo; row += kPairThreads) outside(row);
+    for (int64_t row = max(at[0], lo) + tid; row < p.B; row += kPairThreads) outside(row);
+    return;
   }
-  if (i >= q.P) return;
-  double seq[2], n[2];
+  double sum[2];
+  int rows[2];
   for (int k = 0; k < 2; ++k) {
-    int64_t lo, hi;
-    sequence_rows(q.starts, 2 * i + k, p.B, lo, hi);
-    double s = 0.0;
-    int cnt = 0;
-    for (int64_t row = lo + threadIdx.x; row < hi; row += kPairThreads) {
+    double s = 0.0, n = 0.0;
+    for (int64_t row = at[k] + tid; row < at[k + 1]; row += kPairThreads) {
       const RowStat st = stats[row];
       if (!(st.s < 0.f)) {
         s += st.logp;
-        ++cnt;
+        n += 1.0;
       }
     }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      s += __shfl_xor_sync(kAll, s, o);
-      cnt += __shfl_xor_sync(kAll, cnt, o);
-    }
-    if ((threadIdx.x & 31) == 0) {
-      sum_slots[threadIdx.x >> 5] = s;
-      cnt_slots[threadIdx.x >> 5] = cnt;
-    }
-    __syncthreads();
-    s = 0.0;
-    cnt = 0;
-    for (int w = 0; w < kPairThreads / 32; ++w) {
-      s += sum_slots[w];
-      cnt += cnt_slots[w];
-    }
-    __syncthreads();
-    n[k] = q.length_norm && cnt > 0 ? 1.0 / cnt : 1.0;
-    seq[k] = s * n[k];
+    sum[k] = pair_sum(s, slots);
+    rows[k] = static_cast<int>(pair_sum(n, slots));
   }
-  if (threadIdx.x != 0) return;
-  double rel[2];
-  for (int k = 0; k < 2; ++k) {
-    q.seq_logp[2 * i + k] = static_cast<float>(seq[k]);
-    rel[k] = seq[k] - (q.ref != nullptr ? q.ref[2 * i + k] : 0.0);
+  if (tid == 0) {
+    double rel[2];
+    float scale[2];
+    for (int k = 0; k < 2; ++k) {
+      const double n = q.length_norm && rows[k] > 0 ? 1.0 / rows[k] : 1.0;
+      const double seq = sum[k] * n;
+      scale[k] = static_cast<float>(n);
+      q.seq_logp[2 * i + k] = static_cast<float>(seq);
+      rel[k] = seq - (q.ref != nullptr ? q.ref[2 * i + k] : 0.f);
+    }
+    const double ratio = rel[0] - rel[1], z = q.beta * ratio - q.margin;
+    const float zh = static_cast<float>(z), zl = isfinite(zh) ? static_cast<float>(z - zh) : 0.f;
+    const float ls = static_cast<float>(q.smoothing), keep = static_cast<float>(1.0 - q.smoothing);
+    const float wt = (q.weights != nullptr ? q.weights[i] : q.inv_p) * (p.grad_loss != nullptr ? *p.grad_loss : 1.f);
+    float d = -keep * sigmoid(-zh);
+    if (ls != 0.f) d = fmaf(ls, sigmoid(zh), d);
+    d *= wt * static_cast<float>(q.beta);
+    slope[0] = d * scale[0];
+    slope[1] = -d * scale[1];
+    q.log_ratio[i] = static_cast<float>(ratio);
+    float loss = keep != 0.f ? keep * softplus(-zh, -zl) : 0.f;
+    if (ls != 0.f) loss = fmaf(ls, softplus(zh, zl), loss);
+    q.pair_loss[i] = z != z ? zh : loss;
   }
-  const double ratio = rel[0] - rel[1];
-  const double z = q.beta * ratio - q.margin;
-  q.log_ratio[i] = static_cast<float>(ratio);
-  q.pair_loss[i] = static_cast<float>((1.0 - q.smoothing) * softplus(-z) + (q.smoothing != 0.0 ? q.smoothing * softplus(z) : 0.0));
-  const double w = (q.weights != nullptr ? q.weights[i] : 1.0 / static_cast<double>(q.P)) *
-                   (p.grad_loss != nullptr ? *p.grad_loss : 1.0);
-  const double d = w * q.beta * (q.smoothing * sigmoid(z) - (1.0 - q.smoothing) * sigmoid(-z));
-  coef[2 * i] = d * n[0];
-  coef[2 * i + 1] = -d * n[1];
+  if (p.grad == nullptr) return;
+  __syncthreads();
+  for (int64_t row = at[0] + tid; row < at[2]; row += kPairThreads) {
+    const RowStat st = stats[row];
+    RowGrad g = {0.f, 0.f, 0.f, 0.f};
+    if (!(st.s < 0.f))
+      g = row_grad(slope[row < at[1] ? 0 : 1], 0.f, static_cast<float>(st.logp), 0.f, 0.f, st.m, st.s, p.inv_t);
+    grads[row] = g;
+  }
 }
 
-// The last sequence that starts at or before row, -1 before the first.
-__device__ __forceinline__ int64_t sequence_of(const int32_t* starts, int64_t n_starts, int64_t row) {
-  int64_t lo = 0, hi = n_starts;
-  while (lo < hi) {
-    const int64_t mid = (lo + hi) >> 1;
-    if (starts[mid] <= row) lo = mid + 1;
-    else hi = mid;
-  }
-  return lo - 1;
-}
-
-// The gradient of every row, the last rows first: those are the ones the
-// sums' kernel has left in L2.
+// The gradient of every row, the last rows first: those are the ones the sums'
+// kernel has left in L2. The first CTA adds up the loss.
 template <int DT>
-__global__ void __launch_bounds__(kLossThreads, 4) pref_grad_kernel(const LossParams p, const PrefParams q,
-                                                                    const RowStat* stats, const double* coef) {
-  __shared__ RowGrad grad;
-  __shared__ int64_t grad_token;
+__global__ void __launch_bounds__(kLossThreads, kLossBlocks) pref_grad_kernel(const LossParams p, const PrefParams q,
+                                                                              const RowGrad* grads) {
   __shared__ double slots[kLossThreads / 32];
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  if (blockIdx.x == 0) weighted_sum<kLossThreads>(q.pair_loss, q.weights, q.P, p.loss, slots);
   const int64_t row = p.B - 1 - blockIdx.x / p.C;
+  const RowGrad g = grads[row];
+  const int64_t token = p.tokens[row];
+  if (blockIdx.x == 0) weighted_sum<kLossThreads>(q.pair_loss, q.weights, q.P, p.loss, slots);
   const Share<DT> sh(p, row, blockIdx.x % p.C);
-  if (threadIdx.x == 0) {
-    const int64_t s = q.P > 0 ? sequence_of(q.starts, 2 * q.P + 1, row) : -1;
-    RowGrad g = {0.f, 0.f, 0.f, 0.f};
-    int64_t token = -1;
-    if (s >= 0 && s < 2 * q.P) {
-      const RowStat st = stats[row];
-      if (!(st.s < 0.f)) {
-        token = p.tokens[row];
-        g = row_grad(static_cast<float>(coef[s]), 0.f, static_cast<float>(st.logp), 0.f, 0.f, st.m, st.s, p.inv_t);
-      }
-    }
-    grad = g;
-    grad_token = token;
-  }
-  __syncthreads();
-  write_grad<kLossThreads, DT, false>(p, sh, row, grad, grad_token);
+  write_grad<kLossThreads, DT, false>(p, sh, row, g, token < p.V ? token : -1);
 }
 
 // CTAs per row: as many as fill the device (a power of two), with at least a
@@ -1473,37 +1473,34 @@ int launch_policy(const LossParams& p, int dtype, qrita_stream_t stream) {
   return static_cast<int>(launch_sum(p.row_loss, p.weights, p.B, p.loss, st));
 }
 
-// Workspace: RowStat[B], then double[2 P].
+// Workspace: RowStat[B], then RowGrad[B].
 size_t pref_workspace_bytes(int64_t B, int64_t P) {
-  const size_t n = static_cast<size_t>(B) * sizeof(RowStat) + static_cast<size_t>(P) * 2 * sizeof(double);
+  (void)P;
+  const size_t n = static_cast<size_t>(B) * (sizeof(RowStat) + sizeof(RowGrad));
   return n < 256 ? 256 : (n + 255) / 256 * 256;
 }
 
 int launch_preference(const LossParams& p, const PrefParams& q, int dtype, qrita_stream_t stream) {
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   RowStat* stats = static_cast<RowStat*>(q.workspace);
-  double* coef = reinterpret_cast<double*>(stats + p.B);
+  RowGrad* grads = reinterpret_cast<RowGrad*>(stats + p.B);
+  PrefParams f = q;
+  f.inv_p = q.P > 0 ? static_cast<float>(1.0 / static_cast<double>(q.P)) : 0.f;
   cudaError_t e = cudaSuccess;
   if (p.B > 0) {
-    LossParams f = p;
-    f.grad = nullptr;
-    if ((e = launch_rows(f, dtype, kOpPrefStats, false, stats, st)) != cudaSuccess) return static_cast<int>(e);
+    LossParams sums = p;
+    sums.grad = nullptr;
+    if ((e = launch_rows(sums, dtype, kOpPrefStats, false, stats, st)) != cudaSuccess) return static_cast<int>(e);
   }
-  {
-    e = launch(&pair_kernel, static_cast<unsigned>(q.P > 0 ? q.P : 1), kPairThreads, 1u, st, size_t(0), p, q, static_cast<const RowStat*>(stats), coef);
-    if (e != cudaSuccess) return static_cast<int>(e);
-  }
-  if (p.B == 0 || p.grad == nullptr) {
-    e = launch_sum(q.pair_loss, q.weights, q.P, p.loss, st);
-  } else {  // (whose first CTA sums the loss)
-    const int bytes = dtype == QRITA_DTYPE_F32 ? 4 : 2;
-    const uint32_t C = row_ctas(p, p.V * bytes, true, 4);
-    const unsigned grid = static_cast<unsigned>(p.B * C);
-    auto* fn = dtype == QRITA_DTYPE_F32 ? &pref_grad_kernel<QRITA_DTYPE_F32> : &pref_grad_kernel<QRITA_DTYPE_BF16>;
-    e = launch(fn, grid, kLossThreads, 1u, st, size_t(0), with_ctas(p, 16 / bytes, C), q, static_cast<const RowStat*>(stats),
-               static_cast<const double*>(coef));
-  }
-  return static_cast<int>(e);
+  e = launch(&pair_kernel, static_cast<unsigned>(q.P + 1), kPairThreads, 1u, st, size_t(0), p, f,
+             static_cast<const RowStat*>(stats), grads);
+  if (e != cudaSuccess) return static_cast<int>(e);
+  if (p.B == 0 || p.grad == nullptr) return static_cast<int>(launch_sum(q.pair_loss, q.weights, q.P, p.loss, st));
+  const int bytes = dtype == QRITA_DTYPE_F32 ? 4 : 2;
+  const uint32_t C = row_ctas(p, p.V * bytes, true, kLossBlocks);
+  auto* fn = dtype == QRITA_DTYPE_F32 ? &pref_grad_kernel<QRITA_DTYPE_F32> : &pref_grad_kernel<QRITA_DTYPE_BF16>;
+  return static_cast<int>(launch(fn, static_cast<unsigned>(p.B * C), kLossThreads, 1u, st, size_t(0),
+                                 with_ctas(p, 16 / bytes, C), f, static_cast<const RowGrad*>(grads)));
 }
 
 }  // namespace qrita
