@@ -35,7 +35,7 @@ namespace {
 using namespace dev;
 
 constexpr int kLossThreads = 256;
-constexpr int kLossBlocks = 4;  // of row_kernel on an SM
+constexpr int kLossBlocks = 4;  // on an SM
 constexpr uint32_t kAll = 0xffffffffu;
 constexpr double kLn2 = 0.69314718055994530942;
 // Exponents below this give weights of 0 in fp32; the clamp keeps products
@@ -303,9 +303,6 @@ struct StatSlots {
   Stat ranks[kMaxRanks];
 };
 
-// The CTA's sums from every thread's, in the first warp after a barrier over
-// the THREADS threads: that warp merges them alone (a warp's worth of pairs
-// costs 100 instructions, as many as 25 logits a lane take).
 template <int THREADS, bool ENT>
 __device__ __forceinline__ void put_stat(const Running<ENT>& r, StatSlots<THREADS>& slots) {
   slots.m[threadIdx.x] = r.m;
@@ -313,6 +310,9 @@ __device__ __forceinline__ void put_stat(const Running<ENT>& r, StatSlots<THREAD
   if (ENT) slots.t[threadIdx.x] = r.t;
 }
 
+// The CTA's sums from what every thread has put, by one warp after a barrier:
+// merging pairs in every warp first would cost each of them 100 instructions,
+// as many as 25 logits a lane take.
 template <int THREADS, bool ENT>
 __device__ __forceinline__ Stat warp_stat(float c, const StatSlots<THREADS>& slots) {
   const int lane = threadIdx.x & 31;
@@ -1241,24 +1241,12 @@ __device__ __forceinline__ float sigmoid(float x) { return 1.f / (1.f + expf(-x)
 
 constexpr int kPairThreads = 256;
 
-// The sum of one value per thread over the block in a fixed order, in every thread.
-__device__ __forceinline__ double pair_sum(double v, double* slots) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(kAll, v, o);
-  __syncthreads();
-  if ((threadIdx.x & 31) == 0) slots[threadIdx.x >> 5] = v;
-  __syncthreads();
-  v = 0.0;
-  for (int k = 0; k < kPairThreads / 32; ++k) v += slots[k];
-  return v;
-}
-
 // One CTA per pair, and one more: the two sequences' sums in a fixed order, the
 // pair's loss, and the gradient weights of its rows; the last CTA has the rows
 // that no sequence owns.
 __global__ void __launch_bounds__(kPairThreads) pair_kernel(const LossParams p, const PrefParams q,
                                                             const RowStat* stats, RowGrad* grads) {
-  __shared__ double slots[kPairThreads / 32];
+  __shared__ double slots[kPairThreads / 32][4];
   __shared__ float slope[2];
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -1279,34 +1267,50 @@ __global__ void __launch_bounds__(kPairThreads) pair_kernel(const LossParams p, 
     for (int64_t row = max(at[0], lo) + tid; row < p.B; row += kPairThreads) outside(row);
     return;
   }
-  double sum[2];
-  int rows[2];
-  for (int k = 0; k < 2; ++k) {
-    double s = 0.0, n = 0.0;
-    for (int64_t row = at[k] + tid; row < at[k + 1]; row += kPairThreads) {
-      const RowStat st = stats[row];
-      if (!(st.s < 0.f)) {
-        s += st.logp;
-        n += 1.0;
-      }
-    }
-    sum[k] = pair_sum(s, slots);
-    rows[k] = static_cast<int>(pair_sum(n, slots));
+  // sums of logp and numbers of rows of both sequences at once
+  double v[4] = {0.0, 0.0, 0.0, 0.0};
+  RowStat mine = {0.0, 0.f, -1.f};  // this thread's first row
+  for (int64_t row = at[0] + tid; row < at[2]; row += kPairThreads) {
+    const RowStat st = stats[row];
+    if (row < at[0] + kPairThreads) mine = st;
+    if (st.s < 0.f) continue;
+    const int k = row < at[1] ? 0 : 2;
+    v[k] += st.logp;
+    v[k + 1] += 1.0;
   }
+  float ref[2] = {0.f, 0.f}, wt = q.inv_p;
   if (tid == 0) {
-    double rel[2];
+    if (q.ref != nullptr) {
+      ref[0] = q.ref[2 * i];
+      ref[1] = q.ref[2 * i + 1];
+    }
+    if (q.weights != nullptr) wt = q.weights[i];
+    if (p.grad_loss != nullptr) wt *= *p.grad_loss;
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1)
+#pragma unroll
+    for (int k = 0; k < 4; ++k) v[k] += __shfl_xor_sync(kAll, v[k], o);
+  if ((tid & 31) < 4) slots[tid >> 5][tid & 31] = v[tid & 3];
+  __syncthreads();
+  if (tid == 0) {
+    double ratio = 0.0;
     float scale[2];
     for (int k = 0; k < 2; ++k) {
-      const double n = q.length_norm && rows[k] > 0 ? 1.0 / rows[k] : 1.0;
-      const double seq = sum[k] * n;
-      scale[k] = static_cast<float>(n);
-      q.seq_logp[2 * i + k] = static_cast<float>(seq);
-      rel[k] = seq - (q.ref != nullptr ? q.ref[2 * i + k] : 0.f);
+      double sum = 0.0, n = 0.0;
+      for (int x = 0; x < kPairThreads / 32; ++x) {
+        sum += slots[x][2 * k];
+        n += slots[x][2 * k + 1];
+      }
+      const double one = q.length_norm && n > 0.0 ? 1.0 / n : 1.0;
+      sum *= one;
+      scale[k] = static_cast<float>(one);
+      q.seq_logp[2 * i + k] = static_cast<float>(sum);
+      ratio += k == 0 ? sum - ref[0] : ref[1] - sum;
     }
-    const double ratio = rel[0] - rel[1], z = q.beta * ratio - q.margin;
+    const double z = q.beta * ratio - q.margin;
     const float zh = static_cast<float>(z), zl = isfinite(zh) ? static_cast<float>(z - zh) : 0.f;
     const float ls = static_cast<float>(q.smoothing), keep = static_cast<float>(1.0 - q.smoothing);
-    const float wt = (q.weights != nullptr ? q.weights[i] : q.inv_p) * (p.grad_loss != nullptr ? *p.grad_loss : 1.f);
     float d = -keep * sigmoid(-zh);
     if (ls != 0.f) d = fmaf(ls, sigmoid(zh), d);
     d *= wt * static_cast<float>(q.beta);
@@ -1320,7 +1324,7 @@ __global__ void __launch_bounds__(kPairThreads) pair_kernel(const LossParams p, 
   if (p.grad == nullptr) return;
   __syncthreads();
   for (int64_t row = at[0] + tid; row < at[2]; row += kPairThreads) {
-    const RowStat st = stats[row];
+    const RowStat st = row < at[0] + kPairThreads ? mine : stats[row];
     RowGrad g = {0.f, 0.f, 0.f, 0.f};
     if (!(st.s < 0.f))
       g = row_grad(slope[row < at[1] ? 0 : 1], 0.f, static_cast<float>(st.logp), 0.f, 0.f, st.m, st.s, p.inv_t);
