@@ -290,10 +290,11 @@ int qrita_candidates(const void* logits, int dtype, int64_t B, int64_t V, const 
  * columns from V on are neither read nor written. out_grad has the logits'
  * type; every gradient is computed in fp32 and rounded once. It may be the
  * logits' own buffer (the same pointer and leading dimension: the logits are
- * then lost); any other overlap of the two is QRITA_EINVAL. Everything else
- * is fp32, from fp32 exponentials with sums in fp32 over at most a few
- * thousand terms each and in fp64 beyond. Results do not depend on timing:
- * the same call gives the same bits.
+ * then lost); any other overlap of the two is QRITA_EINVAL. The other outputs
+ * overlap nothing. Values are fp32, from fp32 exponentials; the sums of a
+ * thread's share of a row are fp32, all sums beyond are pairs of fp32 or fp64
+ * (logp is within about 1e-7 of its definition before it is rounded). Results
+ * do not depend on timing: the same call gives the same bits.
  *
  * Common arguments (device pointers unless said otherwise):
  *   logits, dtype, B, V   as qrita_select; B <= 2^31-1.
@@ -409,7 +410,7 @@ size_t qrita_preference_workspace_bytes(int64_t B, int64_t P);
  *                 call; calls that may run at the same time (two captured
  *                 graphs among them) need one each.
  *
- * A few kernels on stream.
+ * Three kernels on stream.
  */
 int qrita_preference_loss(const void* logits, int dtype, int64_t B, int64_t V, int64_t ld, const int32_t* tokens,
                           double inv_temperature, const int32_t* starts, int64_t P, const float* ref_logp,

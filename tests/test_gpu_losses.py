@@ -339,6 +339,36 @@ def test_rows_longer_than_a_cluster_holds(dev, dtype, V):
     pref_case(dev, V + 1, [2, 2], V, dtype)
 
 
+@pytest.mark.parametrize("masked", [False, True])
+def test_offsets_past_32_bits(dev, masked):
+    """More than 2^31 logits in a batch: first, middle and last rows."""
+    import torch
+
+    import top_selection_row_gb300 as q
+
+    B, V = 70000, 32000
+    g = torch.Generator(device=dev).manual_seed(4)
+    x = torch.empty(B, V, dtype=torch.bfloat16, device=dev)
+    for a in range(0, B, 10000):
+        x[a:a + 10000] = torch.randn(10000, V, generator=g, device=dev)
+    t = torch.randint(0, V, (B,), generator=g, device=dev, dtype=torch.int32)
+    adv = torch.randn(B, generator=g, device=dev)
+    mask = None
+    if masked:
+        mask = torch.zeros(B, V, dtype=torch.bool, device=dev)
+        mask[:, ::1000] = True
+        mask[torch.arange(B, device=dev), t.long()] = True
+    w = torch.ones(B, device=dev)
+    got = q.qrita_policy_loss(x, t, None, adv, weights=w, mask=mask)
+    rows = [0, 1, B // 2, 67108, 67109, B - 1]  # 67108 * 32000 < 2^31 < 67109 * 32000
+    xs = x[rows].float().cpu().numpy()
+    ts, avs = t[rows].cpu().numpy(), adv[rows].cpu().numpy()
+    ms = None if mask is None else mask[rows].cpu().numpy()
+    soft = softmaxes(xs, "f32", ms, ts)
+    near_rows(got.logp[rows].cpu().numpy(), [s.logp for s in soft], "logp")
+    near_grad(got.grad[rows], "bf16", soft, ts, -avs, np.zeros(len(rows)), np.abs(avs) * ABS, 1.0)
+
+
 def test_preference_with_bad_starts_touches_nothing_else(dev):
     """Starts out of order or out of range leave everything outside the
     arguments as it was, and a later call is right."""

@@ -18,8 +18,8 @@ CSRC = os.path.join(PKG_DIR, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB_PATH = os.path.join(PKG_DIR, "libqrita.so")
 
-SOURCES = ["qrita_kernel.cu", "qrita_outputs.cu", "qrita_losses.cu", "qrita_api.cpp"]
-HEADERS = ["qrita_device.cuh", "qrita_internal.h"]
+SOURCES = ["qrita_kernel.cu", "qrita_outputs.cu", "qrita_losses.cu", "qrita_api.cpp", "qrita_losses_api.cpp"]
+HEADERS = ["qrita_device.cuh", "qrita_internal.h", "qrita_losses.h"]
 
 GENCODE = ["-gencode", "arch=compute_103a,code=sm_103a"]
 

@@ -6,8 +6,6 @@
 #include <cstdint>
 #include <cuda_runtime.h>
 
-#include "qrita_internal.h"
-
 namespace qrita {
 namespace dev {
 
@@ -94,6 +92,10 @@ __device__ __forceinline__ uint32_t bf16_ceil_bits(float t) {
 // Compensated fp32 sums: a value is hi + lo with |lo| <= ulp(hi)/2.
 // two_sum is Knuth's error-free addition (6 flops, no ordering condition).
 // ---------------------------------------------------------------------------
+struct F2 {
+  float hi, lo;
+};
+
 __device__ __forceinline__ void two_sum(float a, float b, float& s, float& e) {
   s = a + b;
   float bb = s - a;

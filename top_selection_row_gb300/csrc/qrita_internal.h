@@ -9,14 +9,6 @@
 
 namespace qrita {
 
-namespace dev {
-// An fp32 value in two parts: hi + lo with |lo| <= ulp(hi)/2.
-struct F2 {
-  float hi, lo;
-};
-}  // namespace dev
-
-
 // delta tables (Qrita technical summary, "Methodology", part 1: precomputed
 // tables from the normal quantile function, keyed on the target k or p).
 //   lut_k[i] = Phi^-1(1 - 2^(-i/4)),  i = 0..127  (keyed on u = alpha*k/V;
@@ -80,9 +72,6 @@ size_t smem_bytes(int ocap);
 // Launch the selection kernel (grid B*C, cluster C). Returns a cudaError_t.
 int launch_select(const Params& prm, int dtype, size_t smem, qrita_stream_t stream);
 
-// Multiprocessors of the current device.
-int device_sms();
-
 // Largest dynamic shared memory per block on the current device.
 int max_smem_per_block();
 
@@ -94,60 +83,5 @@ int launch_ids(const void* logits, int dtype, int64_t B, int64_t V, const int32_
 int launch_candidates(const void* logits, int dtype, int64_t B, int64_t V, const uint8_t* mask, int32_t cap,
                       int32_t* out_ids, float* out_probs, int32_t* out_count, const float* u, int32_t* out_sample,
                       qrita_stream_t stream);
-
-// Losses over rows of logits (qrita_losses.cu); every launch returns a
-// cudaError_t. Null pointers are the optional arguments of the C ABI.
-struct LossParams {
-  const void* logits;
-  int64_t B, V, ld;
-  const uint8_t* mask;
-  const int32_t* tokens;
-  float c;      // log2(e) * inv_temperature: weights are 2^((x - m) c)
-  float c_ln2, c_ln2_lo;  // c ln2 as a pair
-  float inv_t;
-  float inv_b;  // 1 / B
-  uint32_t C;   // CTAs per row, and the 16-byte units of it each of them takes
-  int64_t per;
-  // outputs per row
-  float* logp;
-  float* entropy;
-  float* kl;
-  float* row_loss;
-  void* grad;
-  int64_t ld_grad;
-  const float* grad_loss;
-  // qrita_token_logprobs_grad
-  const float* g_logp;
-  const float* g_entropy;
-  // qrita_policy_loss
-  const float* old_logp;
-  const float* ref_logp;
-  const float* advantages;
-  const float* weights;
-  float clip_lo, clip_hi;  // 1 - clip_low, 1 + clip_high
-  dev::F2 ln_lo, ln_hi;    // their logarithms as pairs (-inf, inf: no clip)
-  float kl_coef, entropy_coef;
-  float* loss;
-};
-
-struct PrefParams {
-  const int32_t* starts;
-  int64_t P;
-  const float* ref;
-  const float* weights;
-  double beta, smoothing, margin;
-  int length_norm;
-  float inv_p;  // 1 / P
-  float* pair_loss;
-  float* log_ratio;
-  float* seq_logp;
-  void* workspace;
-};
-
-size_t pref_workspace_bytes(int64_t B, int64_t P);
-int launch_logprobs(const LossParams& prm, int dtype, qrita_stream_t stream);
-int launch_logprobs_grad(const LossParams& prm, int dtype, qrita_stream_t stream);
-int launch_policy(const LossParams& prm, int dtype, qrita_stream_t stream);
-int launch_preference(const LossParams& prm, const PrefParams& pref, int dtype, qrita_stream_t stream);
 
 }  // namespace qrita

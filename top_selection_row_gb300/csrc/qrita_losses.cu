@@ -22,12 +22,13 @@
 // digits when p_t is near 1.
 
 #include <cstddef>
+#include <atomic>
 #include <cstdint>
 
 #include <cuda_runtime.h>
 
 #include "qrita_device.cuh"
-#include "qrita_internal.h"
+#include "qrita_losses.h"
 
 namespace qrita {
 namespace {
@@ -408,7 +409,8 @@ __device__ __forceinline__ F2 ln_pair(F2 s) {
 }
 
 // a > b for pairs in normal form (infinities included).
-__device__ __forceinline__ bool pair_above(F2 a, F2 b) { return a.hi != b.hi ? a.hi > b.hi : a.lo > b.lo; }
+template <typename A, typename B>
+__device__ __forceinline__ bool pair_above(A a, B b) { return a.hi != b.hi ? a.hi > b.hi : a.lo > b.lo; }
 
 // e^q - 1 - q: its power series where the difference would lose digits (12
 // terms leave less than 2^-26 of it for |q| <= 1).
@@ -1348,6 +1350,17 @@ __global__ void __launch_bounds__(kLossThreads, kLossBlocks) pref_grad_kernel(co
   write_grad<kLossThreads, DT, false>(p, sh, row, g, token < p.V ? token : -1);
 }
 
+// Multiprocessors of the current device.
+int device_sms() {
+  static std::atomic<int> known[64];
+  int dev = 0, n = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return 1;
+  if (dev >= 0 && dev < 64 && (n = known[dev].load(std::memory_order_relaxed)) > 0) return n;
+  if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n < 1) return 1;
+  if (dev >= 0 && dev < 64) known[dev].store(n, std::memory_order_relaxed);
+  return n;
+}
+
 // CTAs per row: as many as fill the device (a power of two), with at least a
 // unit or two for each thread; and enough that the rows in flight fit in L2
 // when a second pass follows.
@@ -1478,8 +1491,7 @@ int launch_policy(const LossParams& p, int dtype, qrita_stream_t stream) {
 }
 
 // Workspace: RowStat[B], then RowGrad[B].
-size_t pref_workspace_bytes(int64_t B, int64_t P) {
-  (void)P;
+size_t pref_workspace_bytes(int64_t B) {
   const size_t n = static_cast<size_t>(B) * (sizeof(RowStat) + sizeof(RowGrad));
   return n < 256 ? 256 : (n + 255) / 256 * 256;
 }
