@@ -290,8 +290,9 @@ int qrita_candidates(const void* logits, int dtype, int64_t B, int64_t V, const 
  * columns from V on are neither read nor written. out_grad has the logits'
  * type; every gradient is computed in fp32 and rounded once. It may be the
  * logits' own buffer (the same pointer and leading dimension: the logits are
- * then lost); any other overlap of the two is QRITA_EINVAL. The other outputs
- * overlap nothing. Values are fp32, from fp32 exponentials; the sums of a
+ * then lost), or share wider rows with them (the same leading dimension, no
+ * element in common); two buffers whose addresses overlap otherwise are
+ * QRITA_EINVAL. The other outputs overlap nothing. Values are fp32, from fp32 exponentials; the sums of a
  * thread's share of a row are fp32, all sums beyond are pairs of fp32 or fp64
  * (logp is within about 1e-7 of its definition before it is rounded). Results
  * do not depend on timing: the same call gives the same bits.

@@ -83,6 +83,12 @@ def test_bad_gradients(L, call, bad):
     assert call(L, **bad) == EINVAL
 
 
+@pytest.mark.parametrize("shift", [1, 99, 157, 256 + 99, 256 + 157])
+def test_gradients_beside_the_logits_that_share_elements(L, shift):
+    # V = 100 in rows of 256: a gradient that starts 100 .. 156 elements on shares none
+    assert policy(L, ld=256, ld_grad=256, out_grad=VP(0x100000 + 2 * shift)) == EINVAL
+
+
 def test_missing_pointers(L):
     assert logprobs(L, out_logp=NULL) == EINVAL
     assert logprobs_grad(L, out_grad=NULL) == EINVAL

@@ -531,6 +531,23 @@ def test_gradient_over_the_logits_themselves(dev, dtype, keep, V):
         assert torch.equal(want.grad, b) and torch.equal(want.loss, got.loss)
 
 
+def test_gradient_beside_the_logits(dev):
+    """Logits and gradient as two halves of the same wider rows."""
+    import torch
+
+    import top_selection_row_gb300 as q
+
+    V = 1003
+    rng, x, tokens, _ = make_rows(19, 5, V, "bf16")
+    buf = torch.zeros(5, 2 * V + 3, dtype=torch.bfloat16, device=dev)
+    buf[:, :V] = to_device(x, "bf16", dev)
+    got = policy_case(dev, rng, x, "bf16", tokens, None, xd=buf[:, :V], out_grad=buf[:, V + 1:2 * V + 1])
+    assert torch.equal(buf[:, :V], to_device(x, "bf16", dev)) and not buf[:, V].any() and not buf[:, 2 * V + 1:].any()
+    assert got.grad.data_ptr() == buf[:, V + 1:].data_ptr()
+    with pytest.raises(q.QritaError):
+        q.qrita_token_logprobs_grad(buf[:, :V], put(dev, tokens), got.logp, out_grad=buf[:, V - 1:2 * V - 1])
+
+
 def test_binding_refusals(dev):
     import torch
 

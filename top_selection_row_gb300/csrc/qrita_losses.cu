@@ -1232,7 +1232,7 @@ __global__ void __launch_bounds__(kSumThreads) weighted_sum_kernel(const float* 
 // gradient right after its sums, for its second reads to hit L2, 1.6 to 2 times
 // the time, as every share then ends in a fence and an atomic; rows that wait on
 // the SM for their pair and write without a second read, 1.3 to 1.5 times, as
-// reads and writes then take turns, and writes alone run at 4.0 TB/s here.)
+// every row then ends in a fence and an atomic and the SMs idle at a pair's end.)
 // ---------------------------------------------------------------------------
 
 // log(1 + e^x), x = hi + lo, and the sigmoid.

@@ -58,7 +58,13 @@ int loss_args(const void* logits, int dtype, int64_t B, int64_t V, int64_t ld, c
     const uint64_t xn = (rows * static_cast<uint64_t>(ld) + static_cast<uint64_t>(V)) * eb;
     const uint64_t gn = (rows * static_cast<uint64_t>(ld_grad) + static_cast<uint64_t>(V)) * eb;
     const bool same = x0 == g0 && (ld == ld_grad || B == 1);
-    if (!same && x0 < g0 + gn && g0 < x0 + xn) return QRITA_EINVAL;
+    // rows side by side in wider ones: apart by [V, ld - V] modulo ld
+    bool apart = false;
+    if (ld == ld_grad && x0 % eb == g0 % eb) {
+      const uint64_t d = (x0 < g0 ? g0 - x0 : x0 - g0) / eb % static_cast<uint64_t>(ld);
+      apart = d >= static_cast<uint64_t>(V) && d <= static_cast<uint64_t>(ld - V);
+    }
+    if (!same && !apart && x0 < g0 + gn && g0 < x0 + xn) return QRITA_EINVAL;
   }
   return QRITA_OK;
 }
