@@ -531,6 +531,34 @@ def test_gradient_over_the_logits_themselves(dev, dtype, keep, V):
         assert torch.equal(want.grad, b) and torch.equal(want.loss, got.loss)
 
 
+def test_outputs_are_reused(dev):
+    """out=: the tensors of an earlier call are filled again, others refused."""
+    import torch
+
+    import top_selection_row_gb300 as q
+
+    rng, x, tokens, _ = make_rows(23, 6, 1201, "bf16")
+    xd, td = to_device(x, "bf16", dev), put(dev, tokens)
+    adv = put(dev, rng.standard_normal(6).astype(np.float32))
+    starts = put(dev, np.array([0, 2, 6], np.int32))
+    calls = [lambda **k: q.qrita_token_logprobs(xd, td, entropy=True, **k),
+             lambda **k: q.qrita_policy_loss(xd, td, None, adv, entropy_coef=0.1, **k),
+             lambda **k: q.qrita_preference_loss(xd, td, starts, **k)]
+    for f in calls:
+        want = f()
+        held = type(want)(*[torch.full_like(t, 7) for t in want]) if hasattr(want, "_fields") else tuple(torch.full_like(t, 7) for t in want)
+        got = f(out=held)
+        for a, b, c in zip(got, want, held):
+            assert a.data_ptr() == c.data_ptr() and torch.equal(a, b)
+        for i in range(len(held)):
+            for wrong in (held[i].double(), held[i].reshape(-1)[:0], None):
+                if wrong is None and hasattr(want, "grad") and i == 1:
+                    continue  # (no tensor for the gradient: one is made)
+                bad = tuple(wrong if j == i else t for j, t in enumerate(held))
+                with pytest.raises(ValueError):
+                    f(out=bad)
+
+
 def test_gradient_beside_the_logits(dev):
     """Logits and gradient as two halves of the same wider rows."""
     import torch

@@ -395,14 +395,15 @@ def _call(fn, device, stream, made, *args):
         raise QritaError(rc)
 
 
-def qrita_token_logprobs(logits, tokens, mask=None, inv_temperature=1.0, entropy=False, stream=None):
+def qrita_token_logprobs(logits, tokens, mask=None, inv_temperature=1.0, entropy=False, stream=None, out=None):
     """Log-probability of one given token per row, and the row's entropy.
 
     logits: CUDA [B, V] float32 / bfloat16 (rows may be padded: any leading
     dimension >= V); tokens: CUDA int32 [B], a token outside [0, V) ignores
     its row; mask: bool/uint8 [B, V] or None, the kept set the softmax runs
     over (e.g. qrita_select's output). Returns (logp float32 [B], entropy
-    float32 [B] or None). include/qrita.h states the row contract.
+    float32 [B] or None); ``out`` = such a pair reuses the caller's buffers.
+    include/qrita.h states the row contract.
     """
     torch = _torch()
     B, V, ld = _padded_rows(logits)
@@ -410,11 +411,17 @@ def qrita_token_logprobs(logits, tokens, mask=None, inv_temperature=1.0, entropy
     dt = _dtype_code(logits)
     tok = _needed(tokens, B, torch.int32, "tokens", dev)
     keep = _mask_at(mask, B, V, dev)
-    logp = torch.empty(B, dtype=torch.float32, device=dev)
-    ent = torch.empty(B, dtype=torch.float32, device=dev) if entropy else None
+    if out is None:
+        logp = torch.empty(B, dtype=torch.float32, device=dev)
+        ent = torch.empty(B, dtype=torch.float32, device=dev) if entropy else None
+    else:
+        logp, ent = out
+        _needed(logp, B, torch.float32, "out logp", dev)
+        if entropy:
+            _needed(ent, B, torch.float32, "out entropy", dev)
     _call(lib().qrita_token_logprobs, dev, stream, (logp, ent), logits.data_ptr(), dt, B, V, ld, keep, tok,
           inv_temperature, logp.data_ptr(), ent.data_ptr() if entropy else 0)
-    return logp, ent
+    return logp, ent if entropy else None
 
 
 def qrita_token_logprobs_grad(logits, tokens, grad_logp=None, grad_entropy=None, mask=None, inv_temperature=1.0,
@@ -442,7 +449,7 @@ def qrita_token_logprobs_grad(logits, tokens, grad_logp=None, grad_entropy=None,
 
 def qrita_policy_loss(logits, tokens, old_logp, advantages, ref_logp=None, weights=None, mask=None, inv_temperature=1.0,
                       clip_low=0.2, clip_high=0.2, kl_coef=0.0, entropy_coef=0.0, grad_loss=None, grad=True,
-                      entropy=False, out_grad=None, stream=None):
+                      entropy=False, out_grad=None, stream=None, out=None):
     """The clipped policy loss with a KL term over rows of logits, and its
     gradient with respect to them, in one call.
 
@@ -452,7 +459,8 @@ def qrita_policy_loss(logits, tokens, old_logp, advantages, ref_logp=None, weigh
     element that multiplies the gradient, or None. grad=False leaves the
     gradient out; entropy=True returns the entropies even where entropy_coef
     is 0. Returns PolicyLoss(loss [], grad [B, V] or None, row_loss [B],
-    logp [B], kl [B], entropy [B] or None).
+    logp [B], kl [B], entropy [B] or None); ``out`` = such a tuple, as an
+    earlier call returned it, reuses its tensors.
     """
     torch = _torch()
     B, V, ld = _padded_rows(logits)
@@ -467,12 +475,21 @@ def qrita_policy_loss(logits, tokens, old_logp, advantages, ref_logp=None, weigh
     w = _at(weights, B, f32, "weights", dev)
     gl = _at(grad_loss, 1, f32, "grad_loss", dev)
     want_ent = entropy or entropy_coef != 0
-    # (a tensor each: a view of a shared one takes longer to make and free)
-    loss = torch.empty((), dtype=f32, device=dev)
-    row_loss = torch.empty_like(advantages)
-    logp = torch.empty_like(advantages)
-    kl = torch.empty_like(advantages)
-    ent = torch.empty_like(advantages) if want_ent else None
+    if out is None:
+        # (a tensor each: a view of a shared one takes longer to make and free)
+        loss = torch.empty((), dtype=f32, device=dev)
+        row_loss = torch.empty_like(advantages)
+        logp = torch.empty_like(advantages)
+        kl = torch.empty_like(advantages)
+        ent = torch.empty_like(advantages) if want_ent else None
+    else:
+        loss, given, row_loss, logp, kl, ent = out
+        _needed(loss, 1, f32, "out loss", dev)
+        for name, t in (("row_loss", row_loss), ("logp", logp), ("kl", kl), ("entropy", ent)):
+            if name != "entropy" or want_ent:
+                _needed(t, B, f32, "out " + name, dev)
+        out_grad = given if out_grad is None else out_grad
+        ent = ent if want_ent else None
     g, ldg = _grad_rows(out_grad, logits, B, V) if grad else (None, 0)
     _call(lib().qrita_policy_loss, dev, stream, (loss, row_loss, logp, kl, ent, g), logits.data_ptr(), dt, B, V, ld, keep,
           tok, inv_temperature, old, ref, adv, w, clip_low, clip_high, kl_coef, entropy_coef, gl, loss.data_ptr(),
@@ -487,7 +504,7 @@ def preference_workspace_bytes(B: int, P: int) -> int:
 
 def qrita_preference_loss(logits, tokens, starts, ref_logp=None, weights=None, inv_temperature=1.0, beta=0.1,
                           label_smoothing=0.0, margin=0.0, length_norm=False, grad_loss=None, grad=True, out_grad=None,
-                          workspace=None, stream=None):
+                          workspace=None, stream=None, out=None):
     """The preference loss on paired log ratios over rows of logits, and its
     gradient with respect to them.
 
@@ -499,7 +516,7 @@ def qrita_preference_loss(logits, tokens, starts, ref_logp=None, weights=None, i
     CUDA uint8 of at least preference_workspace_bytes(B, P), one for each call
     that may run at the same time (allocated here when None). Returns
     PreferenceLoss(loss [], grad [B, V] or None, pair_loss [P], log_ratio [P],
-    seq_logp [2 P], logp [B]).
+    seq_logp [2 P], logp [B]); ``out`` as qrita_policy_loss.
     """
     torch = _torch()
     B, V, ld = _padded_rows(logits)
@@ -522,11 +539,18 @@ def qrita_preference_loss(logits, tokens, starts, ref_logp=None, weights=None, i
         workspace = torch.empty(need, dtype=torch.uint8, device=dev)
     elif workspace.dtype != torch.uint8 or workspace.device != dev or not workspace.is_contiguous() or workspace.numel() < need:
         raise ValueError(f"workspace must be a contiguous uint8 tensor of at least {need} bytes on {dev}")
-    loss = torch.empty((), dtype=f32, device=dev)
-    pair_loss = torch.empty(P, dtype=f32, device=dev)
-    ratio = torch.empty_like(pair_loss)
-    seq = torch.empty(2 * P, dtype=f32, device=dev)
-    logp = torch.empty(B, dtype=f32, device=dev)
+    if out is None:
+        loss = torch.empty((), dtype=f32, device=dev)
+        pair_loss = torch.empty(P, dtype=f32, device=dev)
+        ratio = torch.empty_like(pair_loss)
+        seq = torch.empty(2 * P, dtype=f32, device=dev)
+        logp = torch.empty(B, dtype=f32, device=dev)
+    else:
+        loss, given, pair_loss, ratio, seq, logp = out
+        for name, t, n in (("loss", loss, 1), ("pair_loss", pair_loss, P), ("log_ratio", ratio, P), ("seq_logp", seq, 2 * P),
+                           ("logp", logp, B)):
+            _needed(t, n, f32, "out " + name, dev)
+        out_grad = given if out_grad is None else out_grad
     g, ldg = _grad_rows(out_grad, logits, B, V) if grad else (None, 0)
     _call(lib().qrita_preference_loss, dev, stream, (loss, pair_loss, ratio, seq, logp, workspace, g), logits.data_ptr(),
           dt, B, V, ld, tok, inv_temperature, at, P, ref, w, beta, label_smoothing, margin, 1 if length_norm else 0, gl,
