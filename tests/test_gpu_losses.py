@@ -722,6 +722,39 @@ def test_side_stream_repeat_and_captured_graph(dev):
     assert same(held, want2)
 
 
+def test_temporaries_of_a_call_on_another_stream(dev):
+    """Inputs that are dropped as soon as the call returns, on a stream that is
+    behind: their memory is not handed out again before the kernels have run."""
+    import torch
+
+    import top_selection_row_gb300 as q
+
+    rng, x, tokens, _ = make_rows(3, 8, 32000, "bf16")
+    xd, td = to_device(x, "bf16", dev), put(dev, tokens)
+    adv = put(dev, rng.standard_normal(8).astype(np.float32))
+    starts = put(dev, np.array([0, 4, 8], np.int32))
+    want = [q.qrita_token_logprobs(xd, td)[0], q.qrita_token_logprobs_grad(xd, td, adv),
+            q.qrita_policy_loss(xd, td, None, adv).grad, q.qrita_preference_loss(xd, td, starts).grad]
+    side, work = torch.cuda.Stream(), torch.randn(4096, 4096, device=dev)
+    calls = [lambda v, t, a: q.qrita_token_logprobs(v, t, stream=side)[0],
+             lambda v, t, a: q.qrita_token_logprobs_grad(v, t, a, stream=side),
+             lambda v, t, a: q.qrita_policy_loss(v, t, None, a, stream=side).grad,
+             lambda v, t, a: q.qrita_preference_loss(v, t, starts.clone(), stream=side).grad]
+    torch.cuda.synchronize()
+    for f, w in zip(calls, want):
+        v, t, a = xd.clone(), td.clone(), adv.clone()
+        torch.cuda.synchronize()
+        with torch.cuda.stream(side):
+            for _ in range(20):
+                work @ work  # the side stream is busy for a few milliseconds
+        got = f(v, t, a)
+        del v, t, a
+        for _ in range(8):  # would land in their memory, were it free
+            torch.full_like(xd, 9), torch.full_like(td, 9), torch.full_like(adv, 9)
+        torch.cuda.synchronize()
+        assert torch.equal(got, w)
+
+
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 def test_gradients_against_differences(dev, dtype):
     """The gradient of the loss against differences of the loss itself along

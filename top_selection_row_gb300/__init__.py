@@ -372,18 +372,18 @@ def _grad_rows(out, logits, B, V):
     return out, _padded_rows(out, "the gradient")[2]
 
 
-def _call(fn, device, stream, made, *args):
+def _call(fn, device, stream, tensors, *args):
     """Calls fn(*args, stream) on ``stream`` (None: the current one), with the
-    logits' device as the current one. Tensors made for a call on another
-    stream than the current one are marked as used there, so that their memory
-    is not handed out again before that stream is done."""
+    logits' device as the current one. The tensors of a call on another stream
+    than the current one are marked as used there, so that their memory is not
+    handed out again before that stream is done with it."""
     torch = _torch()
     if stream is None:
         raw = torch._C._cuda_getCurrentRawStream(device.index)
     else:
         raw = stream.cuda_stream
         if raw != torch._C._cuda_getCurrentRawStream(device.index):
-            for t in made:
+            for t in tensors:
                 if t is not None:
                     t.record_stream(stream)
     if torch.cuda.current_device() == device.index:
@@ -419,8 +419,8 @@ def qrita_token_logprobs(logits, tokens, mask=None, inv_temperature=1.0, entropy
         _needed(logp, B, torch.float32, "out logp", dev)
         if entropy:
             _needed(ent, B, torch.float32, "out entropy", dev)
-    _call(lib().qrita_token_logprobs, dev, stream, (logp, ent), logits.data_ptr(), dt, B, V, ld, keep, tok,
-          inv_temperature, logp.data_ptr(), ent.data_ptr() if entropy else 0)
+    _call(lib().qrita_token_logprobs, dev, stream, (logp, ent, logits, tokens, mask), logits.data_ptr(), dt, B, V, ld,
+          keep, tok, inv_temperature, logp.data_ptr(), ent.data_ptr() if entropy else 0)
     return logp, ent if entropy else None
 
 
@@ -442,8 +442,8 @@ def qrita_token_logprobs_grad(logits, tokens, grad_logp=None, grad_entropy=None,
     if grad_logp is None and grad_entropy is None:
         raise ValueError("one of grad_logp and grad_entropy is required")
     grad, ldg = _grad_rows(out_grad, logits, B, V)
-    _call(lib().qrita_token_logprobs_grad, dev, stream, (grad,), logits.data_ptr(), dt, B, V, ld, keep, tok,
-          inv_temperature, gl, ge, grad.data_ptr(), ldg)
+    _call(lib().qrita_token_logprobs_grad, dev, stream, (grad, logits, tokens, mask, grad_logp, grad_entropy),
+          logits.data_ptr(), dt, B, V, ld, keep, tok, inv_temperature, gl, ge, grad.data_ptr(), ldg)
     return grad
 
 
@@ -491,8 +491,9 @@ def qrita_policy_loss(logits, tokens, old_logp, advantages, ref_logp=None, weigh
         out_grad = given if out_grad is None else out_grad
         ent = ent if want_ent else None
     g, ldg = _grad_rows(out_grad, logits, B, V) if grad else (None, 0)
-    _call(lib().qrita_policy_loss, dev, stream, (loss, row_loss, logp, kl, ent, g), logits.data_ptr(), dt, B, V, ld, keep,
-          tok, inv_temperature, old, ref, adv, w, clip_low, clip_high, kl_coef, entropy_coef, gl, loss.data_ptr(),
+    used = (loss, row_loss, logp, kl, ent, g, logits, tokens, mask, old_logp, ref_logp, advantages, weights, grad_loss)
+    _call(lib().qrita_policy_loss, dev, stream, used, logits.data_ptr(), dt, B, V, ld, keep, tok, inv_temperature,
+          old, ref, adv, w, clip_low, clip_high, kl_coef, entropy_coef, gl, loss.data_ptr(),
           row_loss.data_ptr(), logp.data_ptr(), kl.data_ptr(), ent.data_ptr() if want_ent else 0,
           g.data_ptr() if grad else 0, ldg)
     return PolicyLoss(loss, g, row_loss, logp, kl, ent)
@@ -552,8 +553,9 @@ def qrita_preference_loss(logits, tokens, starts, ref_logp=None, weights=None, i
             _needed(t, n, f32, "out " + name, dev)
         out_grad = given if out_grad is None else out_grad
     g, ldg = _grad_rows(out_grad, logits, B, V) if grad else (None, 0)
-    _call(lib().qrita_preference_loss, dev, stream, (loss, pair_loss, ratio, seq, logp, workspace, g), logits.data_ptr(),
-          dt, B, V, ld, tok, inv_temperature, at, P, ref, w, beta, label_smoothing, margin, 1 if length_norm else 0, gl,
+    used = (loss, pair_loss, ratio, seq, logp, workspace, g, logits, tokens, starts, ref_logp, weights, grad_loss)
+    _call(lib().qrita_preference_loss, dev, stream, used, logits.data_ptr(), dt, B, V, ld, tok, inv_temperature,
+          at, P, ref, w, beta, label_smoothing, margin, 1 if length_norm else 0, gl,
           loss.data_ptr(), pair_loss.data_ptr(), ratio.data_ptr(), seq.data_ptr(), logp.data_ptr(),
           g.data_ptr() if grad else 0, ldg, workspace.data_ptr(), workspace.numel())
     return PreferenceLoss(loss, g, pair_loss, ratio, seq, logp)
