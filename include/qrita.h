@@ -283,7 +283,8 @@ int qrita_candidates(const void* logits, int dtype, int64_t B, int64_t V, const 
  *    row joins neither a loss nor a gradient of logp (H is that of K; 0 when
  *    K is empty or holds only -inf).
  *  - NaN or +inf in K: that row's values and its gradient in K are NaN (a
- *    gradient of 0 where its incoming gradient is 0).
+ *    gradient of 0 where its incoming gradient is 0). A weight of 0 does not
+ *    hide such a row from a loss; a token outside [0, V) does.
  * Logits outside K are never used, whatever they hold; their gradient is 0.
  *
  * logits and out_grad have leading dimensions ld, ld_grad >= V (elements); the
@@ -292,9 +293,9 @@ int qrita_candidates(const void* logits, int dtype, int64_t B, int64_t V, const 
  * logits' own buffer (the same pointer and leading dimension: the logits are
  * then lost), or share wider rows with them (the same leading dimension, no
  * element in common); two buffers whose addresses overlap otherwise are
- * QRITA_EINVAL. The other outputs overlap nothing. Values are fp32, from fp32 exponentials; the sums of a
- * thread's share of a row are fp32, all sums beyond are pairs of fp32 or fp64
- * (logp is within about 1e-7 of its definition before it is rounded). Results
+ * QRITA_EINVAL. The other outputs overlap nothing. Values are fp32, from fp32
+ * exponentials; the sums of a thread's share of a row are fp32, all sums beyond
+ * are pairs of fp32 or fp64 (logp is within about 1e-7 of its definition before it is rounded). Results
  * do not depend on timing: the same call gives the same bits.
  *
  * Common arguments (device pointers unless said otherwise):

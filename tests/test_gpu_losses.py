@@ -755,6 +755,31 @@ def test_temporaries_of_a_call_on_another_stream(dev):
         assert torch.equal(got, w)
 
 
+def test_beside_matrix_products_of_another_stream(dev):
+    """Rows held in tensor memory while another stream's products take theirs."""
+    import torch
+
+    import top_selection_row_gb300 as q
+
+    rng, x, tokens, _ = make_rows(5, 64, 200000, "bf16")
+    xd, td = to_device(x, "bf16", dev), put(dev, tokens)
+    adv = put(dev, rng.standard_normal(64).astype(np.float32))
+    want = q.qrita_policy_loss(xd, td, None, adv)
+    a = torch.randn(4096, 4096, device=dev, dtype=torch.bfloat16)
+    product = a @ a
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    got = []
+    for _ in range(20):
+        with torch.cuda.stream(side):
+            b = a @ a
+        got.append(q.qrita_policy_loss(xd, td, None, adv))
+    torch.cuda.synchronize()
+    assert torch.equal(b, product)
+    for g in got:
+        assert torch.equal(g.loss, want.loss) and torch.equal(g.grad, want.grad)
+
+
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 def test_gradients_against_differences(dev, dtype):
     """The gradient of the loss against differences of the loss itself along

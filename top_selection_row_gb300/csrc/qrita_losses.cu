@@ -984,6 +984,12 @@ __device__ __forceinline__ void tmem_free(uint32_t addr, uint32_t columns) {
   asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(addr), "r"(columns) : "memory");
 }
 
+// Counts this thread at another CTA's barrier, and orders nothing (in release
+// form it is a fence: policy loss of 1024 x 262144 bf16 179 us against 170).
+__device__ __forceinline__ void arrive_remote(uint32_t bar) {
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+
 // 16 words of every lane to and from 16 columns.
 __device__ __forceinline__ void tmem_put(uint32_t addr, const uint4 (&w)[4]) {
   asm volatile(
@@ -1017,7 +1023,7 @@ __device__ __forceinline__ void tmem_get(uint32_t addr, uint4 (&w)[4]) {
 // against 216 KB in shared memory alone: while some wait for their cluster's
 // sums, the others' copies and stores keep HBM busy.
 //
-// HBM bounds it: policy loss of 1024 x 262144 bf16 169 us, 6.4 TB/s of reads and
+// HBM bounds it: policy loss of 1024 x 262144 bf16 170 us, 6.3 TB/s of reads and
 // writes (shared memory alone, three CTAs of 64 KB: 201 us; shares of 64 KB, six
 // CTAs: 174; three CTAs of 256 threads and 128 KB: 179). A single wave of blocks
 // reads, merges and writes one after another: 255 x 50021 fp32 20 us for 102 MB.
@@ -1030,6 +1036,13 @@ constexpr int kSlots = 3;
 constexpr int kMoved = 4;  // pieces in tensor memory, at most
 constexpr int kTmemColumns = kMoved * 16 * (kResThreads / 128);
 constexpr uint64_t kCopyLimitNs = 200ull * 1000 * 1000;
+// A CTA keeps its tensor memory this long while its cluster's sums are not all
+// there, some 50 times what a share takes. Allocation blocks, so a CTA of the
+// cluster can be waiting for columns that another kernel holds, whose own other
+// CTAs can be waiting for this CTA's columns. Then the pieces in them are given
+// up, and read again for the gradient: no CTA waits for ever with columns held.
+// (The watch costs 1 us of 170; with every CTA giving its columns up, 215 us.)
+constexpr uint64_t kHoldLimitNs = 1000ull * 1000;
 
 // MOVED: the share has more than kSlots pieces. Tensor memory is taken first
 // of all: an SM starts no further block of a kernel that may take some before
@@ -1045,6 +1058,8 @@ __global__ void __launch_bounds__(kResThreads, kResBlocks) resident_kernel(const
   __shared__ RowGrad grad;
   __shared__ RowIn in;
   __shared__ uint32_t tmem_at;
+  __shared__ bool given_up;               // this CTA's tensor memory
+  __shared__ __align__(8) uint64_t sent;  // the cluster's CTAs, as they send their sums
   const int tid = threadIdx.x, warp = tid >> 5;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -1058,6 +1073,10 @@ __global__ void __launch_bounds__(kResThreads, kResBlocks) resident_kernel(const
   const int moved = MOVED ? max(0, pieces - kSlots) : 0;
   if (tid == 0) {
     for (int i = 0; i < kSlots; ++i) mbar_init(smem_u32(&bars[i]), 1);
+    if (MOVED) {
+      mbar_init(smem_u32(&sent), C);
+      given_up = false;
+    }
     fence_mbar_init();
   }
   RowGrad g = {0.f, 0.f, 0.f, 0.f};
@@ -1125,7 +1144,24 @@ __global__ void __launch_bounds__(kResThreads, kResBlocks) resident_kernel(const
   if (end_j >= 0) run.add_one(end_x, p.c);
   if (!landed) run.s = run.t = NAN;
   if (MOVED) tmem_put_wait();
-  const Stat st = row_stat(run, p.c, rank, C, slots);
+  put_stat(run, slots);
+  __syncthreads();
+  Stat st;
+  if (warp == 0) st = warp_stat<kResThreads, ENT>(p.c, slots);
+  if (C > 1) {
+    cluster_wait();
+    if (warp == 0) {
+      send_stat<ENT>(st, rank, C, slots.ranks);
+      if (MOVED && tid < C) arrive_remote(map_rank(smem_u32(&sent), tid));
+    }
+    cluster_arrive();
+    if (MOVED && warp == 1 && !__all_sync(kAll, mbar_wait_bounded(smem_u32(&sent), 0, kHoldLimitNs))) {
+      given_up = true;  // (read after a barrier)
+      tmem_free(tmem_at, kTmemColumns);
+    }
+    cluster_wait();
+    if (warp == 0) st = merge_ranks<ENT>(C, p.c, slots.ranks);
+  }
   RowVals v;
   if (tid == 0) {
     v = row_vals<ENT>(p, in, st);
@@ -1170,7 +1206,12 @@ __global__ void __launch_bounds__(kResThreads, kResBlocks) resident_kernel(const
       if (n - i * kPieceUnits >= kPieceUnits) {
         uint4 w[kUnroll];
         if (MOVED && i < moved) {
-          tmem_get(tmem + i * 16, w);
+          if (!given_up) {
+            tmem_get(tmem + i * 16, w);
+          } else {
+#pragma unroll
+            for (int k = 0; k < kUnroll; ++k) w[k] = __ldcs(reinterpret_cast<const uint4*>(src) + u0 + k * kResThreads);
+          }
         } else {
 #pragma unroll
           for (int k = 0; k < kUnroll; ++k) w[k] = at[k * kResThreads];
@@ -1199,7 +1240,7 @@ __global__ void __launch_bounds__(kResThreads, kResBlocks) resident_kernel(const
   }
   if (MOVED) {
     __syncthreads();  // every warp has read its words
-    if (warp == 1) tmem_free(tmem_at, kTmemColumns);
+    if (warp == 1 && !given_up) tmem_free(tmem_at, kTmemColumns);
   }
   if (!landed) {
     // (bounded) copies in flight end before this CTA's memory is given up
