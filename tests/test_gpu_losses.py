@@ -231,6 +231,43 @@ def test_wide_kept_sets(dev, dtype, B, V, density):
     policy_case(dev, rng, x, dtype, tokens, mask, ent=0.02)
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("B,V,counts", [
+    (400, 20000, (0, 1, 2047, 2048, 2049, 20000)),       # one CTA a row, a short one's list
+    (400, 40007, (1, 4095, 4096, 4097, 9000)),           # one CTA a row, a longer one's list; odd rows
+    (320, 131072, (4096, 4097, 131072)),                 # the whole of a CTA's map
+    (320, 131073, (8000, 8300, 131073)),                 # just beyond it: two CTAs a row
+    (1, 16 * 131072 + 4099, (300,)), (1, 16 * 131072 + 4099, (900000,)),  # shares beyond the map
+])
+def test_kept_counts_around_the_limits(dev, dtype, B, V, counts):
+    """Rows that keep as many ids as a list or a map holds, and one more; the
+    rows between them are ignored. In place gives the same bits."""
+    import torch
+
+    rng = np.random.default_rng(V + len(counts))
+    n = len(counts)
+    at = np.linspace(0, B - 1, n).astype(np.int64)
+    x = np.zeros((B, V), np.float32)
+    mask = np.zeros((B, V), np.uint8)
+    tokens = np.full(B, -1, np.int32)
+    for r, c in zip(at, counts):
+        x[r] = rng.standard_normal(V) * 2
+        ids = rng.permutation(V)[:c]
+        mask[r, ids] = rng.integers(1, 256, c)
+        tokens[r] = ids[-1] if c else 5
+    if dtype == "bf16":
+        x = f32_to_bf16_bits(x)
+    got = policy_case(dev, rng, x, dtype, tokens, mask, ent=0.02)
+    rng = np.random.default_rng(9)
+    args = dict(old=False, ref=False, kl=0.0, ent=0.02)
+    apart = policy_case(dev, rng, x, dtype, tokens, mask, **args)
+    rng, xd = np.random.default_rng(9), to_device(x, dtype, dev)
+    onto = policy_case(dev, rng, x, dtype, tokens, mask, xd=xd, out_grad=xd, **args)
+    assert onto.grad.data_ptr() == xd.data_ptr()
+    assert torch.equal(onto.grad, apart.grad) and torch.equal(onto.row_loss, apart.row_loss)
+    assert torch.equal(got.logp, apart.logp)
+
+
 @pytest.mark.parametrize("kw", [dict(old=False), dict(ref=False), dict(weights=False), dict(kl=0.0), dict(gl=-3.0),
                                 dict(ent=-0.05, entropy=True), dict(entropy=True), dict(grad=False), dict(hi=np.inf)],
                          ids=str)

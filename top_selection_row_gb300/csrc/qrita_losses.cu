@@ -50,6 +50,13 @@ constexpr float kMinExp = -1000.0f;
 // was shifted by an exponential: logp is then off by 4e-8 instead of 1.2e-7.
 constexpr float kExLow = 5.0e-8f;
 
+// Rows this short (bytes that their sums read) take blocks of half the threads
+// where a block has one whole: more of them on an SM cover the chain of steps
+// that every row goes through. Log-probabilities of 4000 rows of 2000, 8000 and
+// 16000 bf16: 9.9, 17.3 and 25.9 us against 14.9, 25.2 and 32.5; of 32000
+// (64 KB), 11.6 us against 10.2 for 700 rows.
+constexpr int64_t kShortRow = 32 * 1024;
+
 // What row_kernel computes for a row.
 enum Op : int { kOpLogprobs, kOpGrad, kOpPolicy, kOpPrefStats };
 
@@ -711,23 +718,35 @@ __global__ void __launch_bounds__(THREADS, kLossThreads * kLossBlocks / THREADS)
 }
 
 // ---------------------------------------------------------------------------
-// The same over a kept set. Masks keep tens to thousands of a row's ids, so the
-// mask is what is read whole, 16 ids to a load, and the kept ids go on a list in
-// shared memory; then all their logits are loaded at once (a load for each as
-// it is found would put one memory latency after another). The gradient is a
-// row of zeros, stored while the sums are taken, with the listed entries put
-// over them. The list's order is that of the atomics on its length: its sums
-// are taken in 64-bit fixed point, which no order changes. Rows that keep more
-// than a CTA's list holds are walked unit by unit instead, twice.
+// The same over a kept set. The mask is read once, 16 ids to a load: its bits go
+// to a map in shared memory, the kept ids to a list. Where the list holds them
+// (top-k sets, most top-p sets), all their logits are then loaded at once (a load
+// for each as it is found would put one memory latency after another), and the
+// gradient is a row of zeros, stored while the sums are taken, with the listed
+// entries put over them. The list's order is that of the atomics on its length:
+// its sums are taken in 64-bit fixed point, which no order changes. Rows that
+// keep more are walked by the map, 16 bytes of logits at a time and only where a
+// bit is set, once for the sums and once for the gradient.
 //
-// Log-probabilities over 64 kept ids of 1024 x 262144: 47 us, the mask at
-// 5.7 TB/s (78 us when a unit of mask bytes led to its logits at once). With a
-// gradient, 128 x 151936 fp32: 24 us for 97 MB of mask and zeros; scan, merge
-// and stores of one wave of blocks follow one another.
+// Log-probabilities over 64 kept ids of 1024 x 262144 bf16: 53 us, the mask at
+// 5.0 TB/s (78 us when a unit of mask bytes led to its logits at once); half of
+// all ids kept, 144 us for 805 MB. Policy loss over the kept sets of a mixed top-k
+// and top-p batch of that size (a fifth of the rows keep 16 thousand ids or more)
+// 188 us; with a list of half the length and no map (rows beyond it read the mask
+// again before each load, and again for the gradient) 373. 128 x 151936 fp32 with
+// 64 kept: 24 us for 97 MB of mask and zeros; scan, merge and stores of one wave
+// of blocks follow one another. Four mask units in flight instead of eight cost
+// 4 %; a list in id order by prefix sums over the map, two barriers more, 12 % of
+// the log-probabilities of 64 x 128256.
 // ---------------------------------------------------------------------------
 constexpr int kKeptUnit = 16;
-constexpr int kKeptList = 2048;  // entries of a CTA's list
-// A listed logit weighs at most 1 and a CTA lists at most 2^11: sums stay
+constexpr int kMaskUnroll = 8;  // units of the mask, or kept logits, a thread has in flight
+// Ids of a CTA's bit map, and the entries of its list.
+template <int THREADS>
+constexpr int kKeptMap = THREADS == kLossThreads ? 128 * 1024 : kShortRow;
+template <int THREADS>
+constexpr int kKeptList = 16 * THREADS;
+// A listed logit weighs at most 1 and a CTA lists at most 2^12: sums stay
 // below 2^63 at this scale, and a weight is rounded by 2^-48 of the largest.
 constexpr float kKeptScale = 0x1p47f;
 
@@ -770,9 +789,14 @@ __global__ void __launch_bounds__(THREADS, kLossThreads * kLossBlocks / THREADS)
   __shared__ StatSlots<THREADS> slots;
   __shared__ RowGrad grad;
   __shared__ RowIn in;
-  __shared__ int count;
+  __shared__ int count;  // kept ids, up to where the list overflows
   __shared__ unsigned long long sums[2];
-  __shared__ int2 list[kKeptList];  // id within the CTA's range, logit
+  __shared__ int list[kKeptList<THREADS>];  // ids within the CTA's range
+  // the kept bits of each unit; where there is a list, its logits take their place
+  constexpr int kMapBytes = kKeptMap<THREADS> / 8, kLogitBytes = 4 * kKeptList<THREADS>;
+  __shared__ uint4 shared_units[(kMapBytes > kLogitBytes ? kMapBytes : kLogitBytes) / 16];
+  unsigned short* map = reinterpret_cast<unsigned short*>(shared_units);
+  float* list_x = reinterpret_cast<float*>(shared_units);
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int tid = threadIdx.x;
@@ -790,6 +814,16 @@ __global__ void __launch_bounds__(THREADS, kLossThreads * kLossBlocks / THREADS)
   const int64_t nu = static_cast<int64_t>(static_cast<uint64_t>(V - head) / kKeptUnit);
   const int64_t u_lo = min(nu, static_cast<int64_t>(rank) * p.per), u_hi = rank == C - 1 ? nu : min(nu, u_lo + p.per);
   const int64_t lo = rank == 0 ? 0 : head + u_lo * kKeptUnit, hi = rank == C - 1 ? V : head + u_hi * kKeptUnit;
+  const int n_map = static_cast<int>(min(u_hi - u_lo, static_cast<int64_t>(INT32_MAX)));
+  const bool mapped = n_map <= kKeptMap<THREADS> / kKeptUnit;
+  const uint8_t* mu = mrow + head + u_lo * kKeptUnit;
+  uint4 m_in[kMaskUnroll];
+  auto fetch = [&](int u0) {
+#pragma unroll
+    for (int k = 0; k < kMaskUnroll; ++k)
+      if (u0 + k * THREADS < n_map) m_in[k] = load_unit(mu + static_cast<int64_t>(u0 + k * THREADS) * kKeptUnit);
+  };
+  if (mapped) fetch(tid);  // (on its way while the token is)
   if (token < 0 || token >= V) {  // (the same in every CTA of the cluster)
     if (tid == 0 && rank == 0) row_ignored(p, op, nullptr, row);
     if (grow != nullptr) zero_range<THREADS, DT>(grow, lo, hi);
@@ -797,71 +831,92 @@ __global__ void __launch_bounds__(THREADS, kLossThreads * kLossBlocks / THREADS)
   }
   if (C > 1) cluster_arrive_relaxed();  // every CTA of the cluster runs before its memory is written
   if (tid == 0) {
-    count = 0;
+    count = mapped ? 0 : INT32_MAX;
     sums[0] = sums[1] = 0ull;
   }
   if (tid == 32) in = row_in<DT>(p, op, row, token);  // (read after the sums' barrier)
-  __syncthreads();
-  for (int64_t u0 = u_lo + tid; u0 < u_hi; u0 += THREADS * kUnroll) {
-    if (*reinterpret_cast<volatile int*>(&count) > kKeptList) break;  // no list for this row
-    uint4 m[kUnroll];
-#pragma unroll
-    for (int k = 0; k < kUnroll; ++k) {
-      const int64_t u = u0 + k * THREADS;
-      m[k] = u < u_hi ? load_unit(mrow + head + u * kKeptUnit) : make_uint4(0u, 0u, 0u, 0u);
-    }
-#pragma unroll
-    for (int k = 0; k < kUnroll; ++k) {
-      uint32_t bits = kept_bits(m[k]);
-      if (bits == 0u || *reinterpret_cast<volatile int*>(&count) > kKeptList) continue;
-      int at = atomicAdd(&count, __popc(bits));
-      const int j = static_cast<int>(head + (u0 + k * THREADS) * kKeptUnit - lo);
-      for (; bits != 0u && at < kKeptList; ++at, bits &= bits - 1u) list[at].x = j + __ffs(bits) - 1;
-    }
-  }
   int64_t end_j = -1;  // this thread's id before the first unit or behind the last
   if (rank == 0 && tid < head) end_j = tid;
   const int64_t tail = head + nu * kKeptUnit;
   if (rank == C - 1 && tid >= 32 && tail + tid - 32 < V) end_j = tail + tid - 32;
-  if (end_j >= 0 && mrow[end_j] != 0) {
-    const int at = atomicAdd(&count, 1);
-    if (at < kKeptList) list[at].x = static_cast<int>(end_j - lo);
+  const bool end_kept = end_j >= 0 && mrow[end_j] != 0;
+  __syncthreads();
+  if (mapped) {
+    const int j0 = static_cast<int>(head + u_lo * kKeptUnit - lo);
+    for (int u0 = tid; u0 < n_map; u0 += THREADS * kMaskUnroll) {
+      if (u0 != tid) fetch(u0);
+#pragma unroll
+      for (int k = 0; k < kMaskUnroll; ++k) {
+        const int u = u0 + k * THREADS;
+        if (u >= n_map) break;
+        uint32_t bits = kept_bits(m_in[k]);
+        map[u] = static_cast<unsigned short>(bits);
+        if (bits == 0u || *reinterpret_cast<volatile int*>(&count) > kKeptList<THREADS>) continue;
+        int at = atomicAdd(&count, __popc(bits));
+        for (; bits != 0u && at < kKeptList<THREADS>; ++at, bits &= bits - 1u) list[at] = j0 + u * kKeptUnit + __ffs(bits) - 1;
+      }
+    }
+    if (end_kept) {
+      const int at = atomicAdd(&count, 1);
+      if (at < kKeptList<THREADS>) list[at] = static_cast<int>(end_j - lo);
+    }
   }
   __syncthreads();
-  const bool listed = count <= kKeptList;
+  const bool listed = count <= kKeptList<THREADS>;
   const bool over_logits = p.grad == p.logits;
   const bool vec = (reinterpret_cast<uintptr_t>(xrow + head * E::kBytes) & 15u) == 0;
-  // A row walked unit by unit takes 16 bytes of logits at a time: U of them
-  // with their U mask bytes (aligned: the units of 16 ids are).
+  // Walked units: 16 bytes of logits, U of them. Their bits are in the map, or
+  // (shares beyond the map's length, rows of millions) in U aligned mask bytes.
   constexpr int U = E::kUnit, N = U / 2;
   const int64_t e_lo = head + u_lo * kKeptUnit, n_u = (u_hi - u_lo) * (kKeptUnit / U);
   auto bits_of = [&](int64_t u) {
+    if (mapped) {
+      const unsigned char* at = reinterpret_cast<const unsigned char*>(map);
+      return U == 8 ? static_cast<uint32_t>(at[u]) : at[u >> 1] >> (4 * (u & 1)) & 15u;
+    }
     uint4 m = make_uint4(0u, 0u, 0u, 0u);
     const uint32_t* w = reinterpret_cast<const uint32_t*>(mrow + e_lo + u * U);
     m.x = w[0];
     if (U == 8) m.y = w[1];
     return kept_bits(m);
   };
-  // logits of unit u, -inf where they are not kept
-  auto unit = [&](int64_t u, uint32_t bits, float2 (&x)[N]) {
+  // the kept logits of unit u (anything where none is kept)
+  auto load = [&](int64_t u, uint32_t bits) {
     const int64_t j = e_lo + u * U;
-    if (vec) E::unpack(load_unit(xrow + j * E::kBytes), x);
+    if (bits == 0u) return make_uint4(0u, 0u, 0u, 0u);
+    if (vec) return load_unit(xrow + j * E::kBytes);
+    float2 x[N];
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      const bool a = bits >> (2 * i) & 1u, b = bits >> (2 * i + 1) & 1u;
-      x[i].x = !a ? -INFINITY : vec ? x[i].x : E::load(xrow, j + 2 * i);
-      x[i].y = !b ? -INFINITY : vec ? x[i].y : E::load(xrow, j + 2 * i + 1);
+      x[i].x = bits >> (2 * i) & 1u ? E::load(xrow, j + 2 * i) : 0.f;
+      x[i].y = bits >> (2 * i + 1) & 1u ? E::load(xrow, j + 2 * i + 1) : 0.f;
+    }
+    return E::pack(x);
+  };
+  // -inf where they are not kept
+  auto expand = [&](uint4 w, uint32_t bits, float2 (&x)[N]) {
+    E::unpack(w, x);
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      if (!(bits >> (2 * i) & 1u)) x[i].x = -INFINITY;
+      if (!(bits >> (2 * i + 1) & 1u)) x[i].y = -INFINITY;
     }
   };
   Stat st;
   if (listed) {
     float m = -INFINITY;
     bool bad = false;  // NaN has no fixed point
-    for (int i = tid; i < count; i += THREADS) {
-      const float x = E::load(xrow, lo + list[i].x);
-      list[i].y = __float_as_int(x);
-      m = fmaxf(m, x);
-      bad = bad || x != x || x == INFINITY;
+    for (int i0 = tid; i0 < count; i0 += THREADS * kMaskUnroll) {
+      float x[kMaskUnroll];
+#pragma unroll
+      for (int k = 0; k < kMaskUnroll; ++k)
+        x[k] = i0 + k * THREADS < count ? E::load(xrow, lo + list[i0 + k * THREADS]) : -INFINITY;
+#pragma unroll
+      for (int k = 0; k < kMaskUnroll; ++k) {
+        if (i0 + k * THREADS < count) list_x[i0 + k * THREADS] = x[k];
+        m = fmaxf(m, x[k]);
+        bad = bad || x[k] != x[k] || x[k] == INFINITY;
+      }
     }
     if (grow != nullptr && !over_logits) zero_range<THREADS, DT>(grow, lo, hi);
 #pragma unroll
@@ -871,7 +926,7 @@ __global__ void __launch_bounds__(THREADS, kLossThreads * kLossBlocks / THREADS)
     for (int w = 0; w < THREADS / 32; ++w) m = fmaxf(m, slots.m[w]);
     unsigned long long s = 0ull, t = 0ull;
     for (int i = tid; i < count; i += THREADS) {
-      const float x = __int_as_float(list[i].y);
+      const float x = list_x[i];
       const float y = x == -INFINITY ? kMinExp : fmaxf((x - m) * p.c, kMinExp);
       const float e = bad ? 0.f : ex2(y);
       s += round_u64(e * kKeptScale);
@@ -896,19 +951,23 @@ __global__ void __launch_bounds__(THREADS, kLossThreads * kLossBlocks / THREADS)
     int64_t u = tid;
     for (; u + (kUnroll - 1) * THREADS < n_u; u += kUnroll * THREADS) {
       uint32_t bits[kUnroll];
+      uint4 w[kUnroll];
       float2 x[kUnroll * N];
 #pragma unroll
       for (int k = 0; k < kUnroll; ++k) bits[k] = bits_of(u + k * THREADS);
 #pragma unroll
-      for (int k = 0; k < kUnroll; ++k) unit(u + k * THREADS, bits[k], reinterpret_cast<float2(&)[N]>(x[k * N]));
+      for (int k = 0; k < kUnroll; ++k) w[k] = load(u + k * THREADS, bits[k]);
+#pragma unroll
+      for (int k = 0; k < kUnroll; ++k) expand(w[k], bits[k], reinterpret_cast<float2(&)[N]>(x[k * N]));
       run.add_unit(x, p.c);
     }
     for (; u < n_u; u += THREADS) {
       float2 x[N];
-      unit(u, bits_of(u), x);
+      const uint32_t bits = bits_of(u);
+      expand(load(u, bits), bits, x);
       run.add_unit(x, p.c);
     }
-    if (end_j >= 0 && mrow[end_j] != 0) run.add_one(E::load(xrow, end_j), p.c);
+    if (end_kept) run.add_one(E::load(xrow, end_j), p.c);
     put_stat(run, slots);
     __syncthreads();
     if (tid < 32) st = warp_stat<THREADS, ENT>(p.c, slots);
@@ -933,31 +992,40 @@ __global__ void __launch_bounds__(THREADS, kLossThreads * kLossBlocks / THREADS)
     }
     if (!zero)
       for (int i = tid; i < count; i += THREADS)
-        E::store(grow, lo + list[i].x, grad_one<ENT>(__int_as_float(list[i].y), g, p.c));
+        E::store(grow, lo + list[i], grad_one<ENT>(list_x[i], g, p.c));
   } else {
     const bool gvec = (reinterpret_cast<uintptr_t>(grow + head * E::kBytes) & 15u) == 0;
-    for (int64_t u = tid; u < n_u; u += THREADS) {
-      const uint32_t bits = zero ? 0u : bits_of(u);
-      const int64_t j = e_lo + u * U;
-      float2 x[N];
-      if (bits != 0u) unit(u, bits, x);
+    for (int64_t u0 = tid; u0 < n_u; u0 += THREADS * kUnroll) {
+      uint32_t bits[kUnroll];
+      uint4 w[kUnroll];
 #pragma unroll
-      for (int i = 0; i < N; ++i) {
-        x[i].x = bits >> (2 * i) & 1u ? grad_one<ENT>(x[i].x, g, p.c) : 0.f;
-        x[i].y = bits >> (2 * i + 1) & 1u ? grad_one<ENT>(x[i].y, g, p.c) : 0.f;
-      }
-      if (gvec) {
-        *reinterpret_cast<uint4*>(grow + j * E::kBytes) = E::pack(x);
-      } else {
+      for (int k = 0; k < kUnroll; ++k) bits[k] = zero || u0 + k * THREADS >= n_u ? 0u : bits_of(u0 + k * THREADS);
+#pragma unroll
+      for (int k = 0; k < kUnroll; ++k) w[k] = load(u0 + k * THREADS, bits[k]);
+#pragma unroll
+      for (int k = 0; k < kUnroll; ++k) {
+        if (u0 + k * THREADS >= n_u) break;
+        const int64_t j = e_lo + (u0 + k * THREADS) * U;
+        float2 x[N];
+        E::unpack(w[k], x);
 #pragma unroll
         for (int i = 0; i < N; ++i) {
-          E::store(grow, j + 2 * i, x[i].x);
-          E::store(grow, j + 2 * i + 1, x[i].y);
+          x[i].x = bits[k] >> (2 * i) & 1u ? grad_one<ENT>(x[i].x, g, p.c) : 0.f;
+          x[i].y = bits[k] >> (2 * i + 1) & 1u ? grad_one<ENT>(x[i].y, g, p.c) : 0.f;
+        }
+        if (gvec) {
+          *reinterpret_cast<uint4*>(grow + j * E::kBytes) = E::pack(x);
+        } else {
+#pragma unroll
+          for (int i = 0; i < N; ++i) {
+            E::store(grow, j + 2 * i, x[i].x);
+            E::store(grow, j + 2 * i + 1, x[i].y);
+          }
         }
       }
     }
     if (end_j >= 0)
-      E::store(grow, end_j, !zero && mrow[end_j] != 0 ? grad_one<ENT>(E::load(xrow, end_j), g, p.c) : 0.f);
+      E::store(grow, end_j, !zero && end_kept ? grad_one<ENT>(E::load(xrow, end_j), g, p.c) : 0.f);
   }
   if (in.kept_t && token >= lo && token < hi) {
     __syncthreads();
@@ -1488,26 +1556,19 @@ cudaError_t launch_resident(const LossParams& p, int op, uint32_t C, cudaStream_
   if (q.per > kResidentUnits) return cudaErrorInvalidValue;  // (a share past its storage)
   const int64_t pieces = (q.per + kPieceUnits - 1) / kPieceUnits;
   const size_t smem = static_cast<size_t>(pieces < kSlots ? pieces : kSlots) * kPiece;
+  static_assert(kSlots * kPiece <= 40 * 1024, "a kernel that does not ask has 48 KB, static memory included");
   auto* fn = pieces > kSlots ? &resident_kernel<DT, ENT, true> : &resident_kernel<DT, ENT, false>;
-  if (smem > 40 * 1024) {  // beyond what a kernel has without asking
-    const cudaError_t e = cudaFuncSetAttribute(reinterpret_cast<const void*>(fn),
-                                               cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
-    if (e != cudaSuccess) return e;
-  }
   return launch(fn, static_cast<unsigned>(p.B * C), kResThreads, C, st, smem, q, op);
 }
-
-// Rows this short (bytes that their sums read) take blocks of half the threads
-// where a block has one whole: more of them on an SM cover the chain of steps
-// that every row goes through. Log-probabilities of 4000 rows of 2000, 8000 and
-// 16000 bf16: 9.9, 17.3 and 25.9 us against 14.9, 25.2 and 32.5; of 32000
-// (64 KB), 11.6 us against 10.2 for 700 rows.
-constexpr int64_t kShortRow = 32 * 1024;
 
 template <int DT, bool ENT>
 cudaError_t launch_rows_of(const LossParams& p, int op, RowStat* stats, cudaStream_t st) {
   if (p.mask != nullptr) {
-    const uint32_t C = row_ctas(p, p.V, false, kLossBlocks);
+    // a share's bits fit in the map: with one CTA a row instead of two, the rows
+    // of 262144 that keep many leave a tail (the mixed batch above: 313 us), where
+    // the sets of 64 alone are faster (47 us against 53)
+    uint32_t C = row_ctas(p, p.V, false, kLossBlocks);
+    while (C < kMaxRanks && p.V / C > kKeptMap<kLossThreads> && p.B * 2 * C <= INT32_MAX) C *= 2;
     const unsigned grid = static_cast<unsigned>(p.B * C);
     if (C == 1 && p.V <= kShortRow)
       return launch(&kept_kernel<kLossThreads / 2, DT, ENT>, grid, kLossThreads / 2, C, st, size_t(0),
