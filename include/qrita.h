@@ -294,9 +294,10 @@ int qrita_candidates(const void* logits, int dtype, int64_t B, int64_t V, const 
  * then lost), or share wider rows with them (the same leading dimension, no
  * element in common); two buffers whose addresses overlap otherwise are
  * QRITA_EINVAL. The other outputs overlap nothing. Values are fp32, from fp32
- * exponentials; the sums of a thread's share of a row are fp32, all sums beyond
- * are pairs of fp32 or fp64 (logp is within about 1e-7 of its definition before it is rounded). Results
- * do not depend on timing: the same call gives the same bits.
+ * exponentials; a thread's share of a row is summed in compensated fp32 (its
+ * entropy terms in fp32), all sums beyond are pairs of fp32 or fp64 (logp is
+ * within about 1e-7 of its definition before it is rounded). Results do not
+ * depend on timing: the same call gives the same bits.
  *
  * Common arguments (device pointers unless said otherwise):
  *   logits, dtype, B, V   as qrita_select; B <= 2^31-1.

@@ -221,10 +221,15 @@ struct Share {
 };
 
 // A thread's running sums, relative to the largest logit it has seen (0
-// stands for -inf in ref).
+// stands for -inf in ref). S is compensated: where one token holds most of a
+// row, every other group of its thread's share rounds at that token's weight
+// (logp of 700 x 128256 fp32, 157 groups a thread: root mean square error 5.5e-8,
+// 1.4e-7 without, for 0.5 % of the time). Taking that token's weight out of its
+// own group's sum as well would leave 3.6e-8, for 3 to 7 % of the time.
 template <bool ENT>
 struct Running {
   float m = -INFINITY, ref = 0.f, s = 0.f, t = 0.f;
+  float lo = 0.f;  // to be added to s
 
   __device__ __forceinline__ void raise(float x, float c) {
     // before the first finite logit the sums are 0 (or NaN), whatever the factor
@@ -232,13 +237,19 @@ struct Running {
     const float f = ex2(d);
     if (ENT) t = (t + d * s) * f;
     s *= f;
+    lo *= f;
     m = ref = x;
+  }
+  __device__ __forceinline__ void add(float e) {
+    const float d = e + lo, sum = s + d;
+    lo = d - (sum - s);
+    s = sum;
   }
   __device__ __forceinline__ void add_one(float x, float c) {
     if (x > m) raise(x, c);
     const float y = (x - ref) * c;
     const float e = ex2(y);
-    s += e;
+    add(e);
     if (ENT) t = fmaf(e, y < kMinExp ? kMinExp : y, t);
   }
   // N pairs (a power of two): their own sum first, then one addition to the
@@ -265,7 +276,7 @@ struct Running {
         es[i] = add2(es[i], es[i + o]);
         if (ENT) ts[i] = add2(ts[i], ts[i + o]);
       }
-    s += es[0].x + es[0].y;
+    add(es[0].x + es[0].y);
     if (ENT) t += ts[0].x + ts[0].y;
   }
 };
@@ -306,7 +317,7 @@ constexpr int kMaxRanks = 16;
 // Shared memory of row_stat.
 template <int THREADS>
 struct StatSlots {
-  float m[THREADS], s[THREADS], t[THREADS];
+  float m[THREADS], s[THREADS], lo[THREADS], t[THREADS];
   Stat ranks[kMaxRanks];
 };
 
@@ -314,6 +325,7 @@ template <int THREADS, bool ENT>
 __device__ __forceinline__ void put_stat(const Running<ENT>& r, StatSlots<THREADS>& slots) {
   slots.m[threadIdx.x] = r.m;
   slots.s[threadIdx.x] = r.s;
+  slots.lo[threadIdx.x] = r.lo;
   if (ENT) slots.t[threadIdx.x] = r.t;
 }
 
@@ -339,7 +351,7 @@ __device__ __forceinline__ Stat warp_stat(float c, const StatSlots<THREADS>& slo
     const float d = ms[i] == v.m ? 0.f : fmaxf((ms[i] - v.m) * c, kMinExp);
     const float f = ex2(d), s = slots.s[lane + 32 * i] * f;
     f2_add(v.s, s);
-    if (d != 0.f) v.s.lo = fmaf(s, kExLow, v.s.lo);
+    v.s.lo += slots.lo[lane + 32 * i] * f + (d != 0.f ? s * kExLow : 0.f);
     if (ENT) f2_add(v.t, fmaf(d, s, slots.t[lane + 32 * i] * f));
   }
 #pragma unroll
