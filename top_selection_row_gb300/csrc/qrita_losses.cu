@@ -480,7 +480,7 @@ __device__ __forceinline__ RowIn row_in(const LossParams& p, int op, int64_t row
 struct RowVals {
   F2 logp;
   float lp, H;      // as they are given out
-  float ln_s, rho, q;
+  float ln_s, step, q;      // step: -advantage * rho
   bool joins, over, bound;  // over, bound: rho above the clip; the clip binds
 };
 
@@ -510,7 +510,7 @@ __device__ __forceinline__ RowVals row_vals(const LossParams& p, const RowIn& in
   // ln S less the mean of y_j ln2
   v.H = ENT && !empty ? f2_float(f2_sub(ln_s, f2_make(f2_float(st.t) / st.s.hi * static_cast<float>(kLn2), 0.f))) : 0.f;
   v.joins = v.lp != -INFINITY;  // (NaN joins)
-  v.rho = v.q = 0.f;
+  v.step = v.q = 0.f;
   v.over = v.bound = false;
   return v;
 }
@@ -526,11 +526,14 @@ __device__ __forceinline__ RowGrad row_weights(const LossParams& p, int op, cons
     F2 d = f2_make(0.f, 0.f);  // ln rho
     if (p.old_logp != nullptr)
       d = isinf(in.old_logp) ? f2_make(-in.old_logp, 0.f) : f2_sub(v.logp, f2_make(in.old_logp, 0.f));
-    v.rho = expf(d.hi) * (1.f + d.lo);
+    // rho = 1 + (e^d - 1): near 1 one rounding of the product is what it costs
+    float more = expm1f(d.hi);
+    if (fabsf(d.hi) < 80.f) more = fmaf(d.lo, more + 1.f, more);
+    v.step = more > -0.5f ? fmaf(-in.adv, more, -in.adv) : -in.adv * (expf(d.hi) * (1.f + d.lo));
     // rho against the clip, on the logarithms
     v.over = pair_above(d, p.ln_hi);
     v.bound = (in.adv > 0.f && v.over) || (in.adv < 0.f && pair_above(p.ln_lo, d));
-    a = v.bound ? 0.f : -in.adv * v.rho;
+    a = v.bound ? 0.f : v.step;
     if (v.lp != v.lp) a = v.lp;
     if (p.ref_logp != nullptr) {
       v.q = (in.ref_logp - v.logp.hi) - v.logp.lo;
@@ -551,7 +554,7 @@ __device__ __forceinline__ void row_out(const LossParams& p, int op, RowStat* st
   if (op == kOpPolicy) {
     float loss = 0.f, kl = 0.f;
     if (v.joins) {
-      loss = v.lp != v.lp ? v.lp : -in.adv * (v.bound ? (v.over ? p.clip_hi : p.clip_lo) : v.rho);
+      loss = v.lp != v.lp ? v.lp : v.bound ? -in.adv * (v.over ? p.clip_hi : p.clip_lo) : v.step;
       if (p.ref_logp != nullptr) {
         kl = exp_minus_tangent(v.q);
         if (p.kl_coef != 0.f) loss = fmaf(p.kl_coef, kl, loss);
