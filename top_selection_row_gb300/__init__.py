@@ -322,6 +322,10 @@ PolicyLoss = namedtuple("PolicyLoss", "loss grad row_loss logp kl entropy")
 PreferenceLoss = namedtuple("PreferenceLoss", "loss grad pair_loss log_ratio seq_logp logp")
 
 
+# stream= runs a call on another stream than the current one. The caller sees to
+# it that its inputs are ready there, and waits for it before the results are used
+# elsewhere; both may be dropped at any time.
+#
 # (These calls take 3 to 10 us on the GPU for a small batch, so what they do on
 # the host is kept short: plain integers as pointers, one test per property.)
 def _padded_rows(t, name="logits"):
@@ -337,6 +341,36 @@ def _padded_rows(t, name="logits"):
     if V < 1 or (B > 0 and ((V > 1 and unit != 1) or ld < V)):
         raise ValueError(f"{name} must be row-major: unit stride within a row, a leading dimension of at least V")
     return B, V, ld
+
+
+def _tensors(values):
+    """The CUDA tensors among values and the tuples they hold."""
+    for v in values:
+        if isinstance(v, (tuple, list)):
+            yield from _tensors(v)
+        elif isinstance(v, _torch().Tensor) and v.is_cuda:
+            yield v
+
+
+def _on_stream(stream, fn, *args):
+    """fn(*args) with ``stream`` as the current one: what the call allocates
+    comes from that stream's memory, whose last use is ordered before the
+    call's kernels (a block of another stream may still be read or written
+    there). The arguments are marked as used on ``stream`` and the results as
+    used on the caller's, so that neither's memory is handed out again before
+    that stream is done with it."""
+    torch = _torch()
+    if any(t.device != stream.device for t in _tensors(args)):
+        raise ValueError(f"stream must be one of the tensors' device, not of {stream.device}")
+    caller = torch.cuda.current_stream(stream.device)
+    with torch.cuda.stream(stream):
+        got = fn(*args)
+    if stream != caller:
+        for t in _tensors(args):
+            t.record_stream(stream)
+        for t in _tensors((got,)):
+            t.record_stream(caller)
+    return got
 
 
 def _at(t, n, dtype, name, device):
@@ -372,20 +406,11 @@ def _grad_rows(out, logits, B, V):
     return out, _padded_rows(out, "the gradient")[2]
 
 
-def _call(fn, device, stream, tensors, *args):
-    """Calls fn(*args, stream) on ``stream`` (None: the current one), with the
-    logits' device as the current one. The tensors of a call on another stream
-    than the current one are marked as used there, so that their memory is not
-    handed out again before that stream is done with it."""
+def _call(fn, device, *args):
+    """Calls fn(*args, stream) on the current stream, with the logits' device
+    as the current one."""
     torch = _torch()
-    if stream is None:
-        raw = torch._C._cuda_getCurrentRawStream(device.index)
-    else:
-        raw = stream.cuda_stream
-        if raw != torch._C._cuda_getCurrentRawStream(device.index):
-            for t in tensors:
-                if t is not None:
-                    t.record_stream(stream)
+    raw = torch._C._cuda_getCurrentRawStream(device.index)
     if torch.cuda.current_device() == device.index:
         rc = fn(*args, raw)
     else:
@@ -405,6 +430,8 @@ def qrita_token_logprobs(logits, tokens, mask=None, inv_temperature=1.0, entropy
     float32 [B] or None); ``out`` = such a pair reuses the caller's buffers.
     include/qrita.h states the row contract.
     """
+    if stream is not None:
+        return _on_stream(stream, qrita_token_logprobs, logits, tokens, mask, inv_temperature, entropy, None, out)
     torch = _torch()
     B, V, ld = _padded_rows(logits)
     dev = logits.device
@@ -419,8 +446,8 @@ def qrita_token_logprobs(logits, tokens, mask=None, inv_temperature=1.0, entropy
         _needed(logp, B, torch.float32, "out logp", dev)
         if entropy:
             _needed(ent, B, torch.float32, "out entropy", dev)
-    _call(lib().qrita_token_logprobs, dev, stream, (logp, ent, logits, tokens, mask), logits.data_ptr(), dt, B, V, ld,
-          keep, tok, inv_temperature, logp.data_ptr(), ent.data_ptr() if entropy else 0)
+    _call(lib().qrita_token_logprobs, dev, logits.data_ptr(), dt, B, V, ld, keep, tok,
+          inv_temperature, logp.data_ptr(), ent.data_ptr() if entropy else 0)
     return logp, ent if entropy else None
 
 
@@ -431,6 +458,9 @@ def qrita_token_logprobs_grad(logits, tokens, grad_logp=None, grad_entropy=None,
     (float32 [B] each; one may be None). Returns the gradient, [B, V] of the
     logits' type; ``out_grad`` gives its tensor (rows may be padded, and it
     may be the logits themselves)."""
+    if stream is not None:
+        return _on_stream(stream, qrita_token_logprobs_grad, logits, tokens, grad_logp, grad_entropy, mask,
+                          inv_temperature, out_grad)
     torch = _torch()
     B, V, ld = _padded_rows(logits)
     dev = logits.device
@@ -442,8 +472,8 @@ def qrita_token_logprobs_grad(logits, tokens, grad_logp=None, grad_entropy=None,
     if grad_logp is None and grad_entropy is None:
         raise ValueError("one of grad_logp and grad_entropy is required")
     grad, ldg = _grad_rows(out_grad, logits, B, V)
-    _call(lib().qrita_token_logprobs_grad, dev, stream, (grad, logits, tokens, mask, grad_logp, grad_entropy),
-          logits.data_ptr(), dt, B, V, ld, keep, tok, inv_temperature, gl, ge, grad.data_ptr(), ldg)
+    _call(lib().qrita_token_logprobs_grad, dev, logits.data_ptr(), dt, B, V, ld, keep, tok, inv_temperature, gl, ge,
+          grad.data_ptr(), ldg)
     return grad
 
 
@@ -462,6 +492,10 @@ def qrita_policy_loss(logits, tokens, old_logp, advantages, ref_logp=None, weigh
     logp [B], kl [B], entropy [B] or None); ``out`` = such a tuple, as an
     earlier call returned it, reuses its tensors.
     """
+    if stream is not None:
+        return _on_stream(stream, qrita_policy_loss, logits, tokens, old_logp, advantages, ref_logp, weights, mask,
+                          inv_temperature, clip_low, clip_high, kl_coef, entropy_coef, grad_loss, grad, entropy,
+                          out_grad, None, out)
     torch = _torch()
     B, V, ld = _padded_rows(logits)
     dev = logits.device
@@ -491,9 +525,8 @@ def qrita_policy_loss(logits, tokens, old_logp, advantages, ref_logp=None, weigh
         out_grad = given if out_grad is None else out_grad
         ent = ent if want_ent else None
     g, ldg = _grad_rows(out_grad, logits, B, V) if grad else (None, 0)
-    used = (loss, row_loss, logp, kl, ent, g, logits, tokens, mask, old_logp, ref_logp, advantages, weights, grad_loss)
-    _call(lib().qrita_policy_loss, dev, stream, used, logits.data_ptr(), dt, B, V, ld, keep, tok, inv_temperature,
-          old, ref, adv, w, clip_low, clip_high, kl_coef, entropy_coef, gl, loss.data_ptr(),
+    _call(lib().qrita_policy_loss, dev, logits.data_ptr(), dt, B, V, ld, keep, tok, inv_temperature, old,
+          ref, adv, w, clip_low, clip_high, kl_coef, entropy_coef, gl, loss.data_ptr(),
           row_loss.data_ptr(), logp.data_ptr(), kl.data_ptr(), ent.data_ptr() if want_ent else 0,
           g.data_ptr() if grad else 0, ldg)
     return PolicyLoss(loss, g, row_loss, logp, kl, ent)
@@ -519,6 +552,9 @@ def qrita_preference_loss(logits, tokens, starts, ref_logp=None, weights=None, i
     PreferenceLoss(loss [], grad [B, V] or None, pair_loss [P], log_ratio [P],
     seq_logp [2 P], logp [B]); ``out`` as qrita_policy_loss.
     """
+    if stream is not None:
+        return _on_stream(stream, qrita_preference_loss, logits, tokens, starts, ref_logp, weights, inv_temperature, beta,
+                          label_smoothing, margin, length_norm, grad_loss, grad, out_grad, workspace, None, out)
     torch = _torch()
     B, V, ld = _padded_rows(logits)
     dev = logits.device
@@ -553,9 +589,8 @@ def qrita_preference_loss(logits, tokens, starts, ref_logp=None, weights=None, i
             _needed(t, n, f32, "out " + name, dev)
         out_grad = given if out_grad is None else out_grad
     g, ldg = _grad_rows(out_grad, logits, B, V) if grad else (None, 0)
-    used = (loss, pair_loss, ratio, seq, logp, workspace, g, logits, tokens, starts, ref_logp, weights, grad_loss)
-    _call(lib().qrita_preference_loss, dev, stream, used, logits.data_ptr(), dt, B, V, ld, tok, inv_temperature,
-          at, P, ref, w, beta, label_smoothing, margin, 1 if length_norm else 0, gl,
+    _call(lib().qrita_preference_loss, dev, logits.data_ptr(), dt, B, V, ld, tok, inv_temperature, at,
+          P, ref, w, beta, label_smoothing, margin, 1 if length_norm else 0, gl,
           loss.data_ptr(), pair_loss.data_ptr(), ratio.data_ptr(), seq.data_ptr(), logp.data_ptr(),
           g.data_ptr() if grad else 0, ldg, workspace.data_ptr(), workspace.numel())
     return PreferenceLoss(loss, g, pair_loss, ratio, seq, logp)
