@@ -124,10 +124,38 @@ def _vec(t, n, dtype, name, device):
     return t
 
 
-def _stream_ptr(device, stream):
+def _tensors(values):
+    """The CUDA tensors among values and the tuples they hold."""
+    for v in values:
+        if isinstance(v, (tuple, list)):
+            yield from _tensors(v)
+        elif isinstance(v, _torch().Tensor) and v.is_cuda:
+            yield v
+
+
+def _on_stream(stream, fn, *args):
+    """fn(*args) with ``stream`` as the current one: what the call allocates
+    comes from that stream's memory, whose last use is ordered before the
+    call's kernels (a block of another stream may still be read or written
+    there). The arguments are marked as used on ``stream`` and the results as
+    used on the caller's, so that neither's memory is handed out again before
+    that stream is done with it."""
     torch = _torch()
-    s = stream if stream is not None else torch.cuda.current_stream(device)
-    return ctypes.c_void_p(s.cuda_stream)
+    if any(t.device != stream.device for t in _tensors(args)):
+        raise ValueError(f"stream must be one of the tensors' device, not of {stream.device}")
+    caller = torch.cuda.current_stream(stream.device)
+    with torch.cuda.stream(stream):
+        got = fn(*args)
+    if stream != caller:
+        for t in _tensors(args):
+            t.record_stream(stream)
+        for t in _tensors((got,)):
+            t.record_stream(caller)
+    return got
+
+
+def _stream_ptr(device):
+    return ctypes.c_void_p(_torch().cuda.current_stream(device).cuda_stream)
 
 
 def qrita_select(logits, k=None, p=None, out=None, stream=None):
@@ -136,7 +164,8 @@ def qrita_select(logits, k=None, p=None, out=None, stream=None):
     logits: CUDA tensor [B, V], float32 or bfloat16, row-major.
     k: CUDA int32 [B] or None (top-k off); p: CUDA float32 [B] or None.
     out: optional CUDA bool/uint8 tensor [B, V]. Returns the mask (bool).
-    The kernel is enqueued on ``stream`` (default: the current stream).
+    The kernel is enqueued on ``stream`` (default: the current stream), where
+    the caller sees to it that the inputs are ready.
     """
     return qrita_select_ex(logits, k, p, out=out, stream=stream)[0]
 
@@ -149,6 +178,8 @@ def qrita_select_ex(logits, k=None, p=None, out=None, stream=None, flags=0,
     [B] tensor, ``info`` a CUDA uint8 [B, 64] tensor holding
     qrita_row_info_t records (decode with :func:`decode_row_info`).
     """
+    if stream is not None:
+        return _on_stream(stream, qrita_select_ex, logits, k, p, out, None, flags, row_status, row_info)
     torch = _torch()
     B, V = _check_rows(logits)
     dev = logits.device
@@ -169,7 +200,7 @@ def qrita_select_ex(logits, k=None, p=None, out=None, stream=None, flags=0,
         ctypes.c_void_p(kk.data_ptr() if kk is not None else 0),
         ctypes.c_void_p(pp.data_ptr() if pp is not None else 0),
         ctypes.c_void_p(out.data_ptr() if B else 0),
-        _stream_ptr(dev, stream),
+        _stream_ptr(dev),
         ctypes.c_uint32(flags),
         ctypes.c_void_p(st.data_ptr() if st is not None else 0),
         ctypes.c_void_p(info.data_ptr() if info is not None else 0),
@@ -192,6 +223,8 @@ def qrita_topk_ids(logits, k, kmax, out_mask=None, out_ids=None, stream=None):
     logits: CUDA [B, V] float32 / bfloat16; k: CUDA int32 [B]; kmax: 1..8192.
     Returns (ids int32 [B, kmax], padded with -1; mask bool [B, V]).
     """
+    if stream is not None:
+        return _on_stream(stream, qrita_topk_ids, logits, k, kmax, out_mask, out_ids)
     torch = _torch()
     B, V = _check_rows(logits)
     dev = logits.device
@@ -207,7 +240,7 @@ def qrita_topk_ids(logits, k, kmax, out_mask=None, out_ids=None, stream=None):
     rc = lib().qrita_topk_ids(
         ctypes.c_void_p(logits.data_ptr() if B else 0), _dtype_code(logits), B, V,
         ctypes.c_void_p(kk.data_ptr()), int(kmax), ctypes.c_void_p(out_mask.data_ptr() if B else 0),
-        ctypes.c_void_p(out_ids.data_ptr() if B else 0), _stream_ptr(dev, stream))
+        ctypes.c_void_p(out_ids.data_ptr() if B else 0), _stream_ptr(dev))
     if rc != OK:
         raise QritaError(rc)
     return out_ids, out_mask
@@ -222,6 +255,8 @@ def qrita_candidates(logits, mask, cap, u=None, stream=None, out=None):
     (contiguous int32 [B, cap], float32 [B, cap], int32 [B], int32 [B] or
     None exactly when u is), whose entries past a row's count are left as
     they were."""
+    if stream is not None:
+        return _on_stream(stream, qrita_candidates, logits, mask, cap, u, None, out)
     torch = _torch()
     B, V = _check_rows(logits)
     dev = logits.device
@@ -249,7 +284,7 @@ def qrita_candidates(logits, mask, cap, u=None, stream=None, out=None):
         ctypes.c_void_p(mask.data_ptr() if B else 0), int(cap), ctypes.c_void_p(ids.data_ptr() if B else 0),
         ctypes.c_void_p(probs.data_ptr() if B else 0), ctypes.c_void_p(count.data_ptr() if B else 0),
         ctypes.c_void_p(uu.data_ptr() if uu is not None else 0),
-        ctypes.c_void_p(sample.data_ptr() if sample is not None else 0), _stream_ptr(dev, stream))
+        ctypes.c_void_p(sample.data_ptr() if sample is not None else 0), _stream_ptr(dev))
     if rc != OK:
         raise QritaError(rc)
     return ids, probs, count, sample
@@ -280,6 +315,8 @@ def qrita_select_host(logits, k=None, p=None, out=None, staging=None, stream=Non
     host_staging_bytes(...) bytes (allocated here when None). Returns ``out``
     after the stream has finished.
     """
+    if stream is not None:
+        return _on_stream(stream, qrita_select_host, logits, k, p, out, staging)
     torch = _torch()
     if logits.dim() != 2 or logits.is_cuda:
         raise ValueError("logits must be a host [B, V] tensor")
@@ -308,7 +345,7 @@ def qrita_select_host(logits, k=None, p=None, out=None, staging=None, stream=Non
         ctypes.c_void_p(out.data_ptr() if B else 0),
         ctypes.c_void_p(staging.data_ptr()),
         ctypes.c_size_t(staging.numel()),
-        _stream_ptr(staging.device, stream),
+        _stream_ptr(staging.device),
     )
     if rc != OK:
         raise QritaError(rc)
@@ -341,36 +378,6 @@ def _padded_rows(t, name="logits"):
     if V < 1 or (B > 0 and ((V > 1 and unit != 1) or ld < V)):
         raise ValueError(f"{name} must be row-major: unit stride within a row, a leading dimension of at least V")
     return B, V, ld
-
-
-def _tensors(values):
-    """The CUDA tensors among values and the tuples they hold."""
-    for v in values:
-        if isinstance(v, (tuple, list)):
-            yield from _tensors(v)
-        elif isinstance(v, _torch().Tensor) and v.is_cuda:
-            yield v
-
-
-def _on_stream(stream, fn, *args):
-    """fn(*args) with ``stream`` as the current one: what the call allocates
-    comes from that stream's memory, whose last use is ordered before the
-    call's kernels (a block of another stream may still be read or written
-    there). The arguments are marked as used on ``stream`` and the results as
-    used on the caller's, so that neither's memory is handed out again before
-    that stream is done with it."""
-    torch = _torch()
-    if any(t.device != stream.device for t in _tensors(args)):
-        raise ValueError(f"stream must be one of the tensors' device, not of {stream.device}")
-    caller = torch.cuda.current_stream(stream.device)
-    with torch.cuda.stream(stream):
-        got = fn(*args)
-    if stream != caller:
-        for t in _tensors(args):
-            t.record_stream(stream)
-        for t in _tensors((got,)):
-            t.record_stream(caller)
-    return got
 
 
 def _at(t, n, dtype, name, device):
