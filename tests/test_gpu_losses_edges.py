@@ -1,0 +1,108 @@
+"""Losses at the edges of their definitions: ratios and KL terms far from 1,
+rows that a weight hides, values that are not finite beside tokens that are not
+kept. Against the fp64 oracle; the tolerances are test_gpu_losses' own (ABS of
+logp, so ABS of an exponential of it relatively)."""
+
+import numpy as np
+import pytest
+
+from oracle import dentropy, dlogp, policy_row
+from parity_helpers import to_device
+from test_gpu_losses import ABS, F32_ROUND, dev, make_rows, near, near_grad, near_rows, put, softmaxes  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+
+FORMS = [("f32", 0, 300), ("bf16", 0, 300), ("f32", 12, 300), ("bf16", 0, 40000), ("f32", 12, 40000)]
+
+
+def policy(dev, x, dtype, tokens, mask, old, ref, adv, w, kl=0.0, ent=0.0, lo=0.2, hi=0.3, gl=None):
+    """qrita_policy_loss against the oracle; returns the call's result."""
+    import top_selection_row_gb300 as q
+
+    f = np.float32
+    B = len(tokens)
+    old, adv, w = (np.asarray(v, f) for v in (old, adv, w))
+    ref = None if ref is None else np.asarray(ref, f)
+    got = q.qrita_policy_loss(to_device(x, dtype, dev), put(dev, tokens), put(dev, old), put(dev, adv), ref_logp=put(dev, ref),
+                              weights=put(dev, w), mask=put(dev, mask), clip_low=lo, clip_high=hi, kl_coef=kl, entropy_coef=ent,
+                              grad_loss=None if gl is None else put(dev, [gl], f))
+    soft = softmaxes(x, dtype, mask, tokens)
+    rows, kls, a, h, size = (np.zeros(B) for _ in range(5))
+    for r, s in enumerate(soft):
+        rows[r], kls[r], da, dh = policy_row(s, float(old[r]), None if ref is None else float(ref[r]), float(adv[r]), lo, hi, kl, ent)
+        if s.joins:
+            wr = float(w[r]) * (1.0 if gl is None else gl)
+            a[r], h[r] = wr * da, wr * dh
+            eq = 0.0 if ref is None else kl * float(np.exp(float(ref[r]) - s.logp))
+            size[r] = abs(float(adv[r])) * float(np.exp(s.logp - float(old[r]))) + eq + kl + abs(ent)
+    with np.errstate(over="ignore"):
+        rows32, kl32 = rows.astype(f), kls.astype(f)  # (a value beyond fp32 is an infinity)
+    near(got.row_loss.cpu().numpy(), np.where(np.isinf(rows32), rows32, rows), 2 * ABS * size + 2 * F32_ROUND * np.abs(rows), "row loss")
+    kl_size = np.array([1 + (0.0 if ref is None or not s.joins else np.exp(float(ref[r]) - s.logp)) for r, s in enumerate(soft)])
+    # (the output's own rounding: half a step of 699 is 3e-5)
+    near(got.kl.cpu().numpy(), np.where(np.isinf(kl32), kl32, kls), 2 * ABS * kl_size + 2 * F32_ROUND * np.abs(np.where(np.isinf(kl32), 0, kls)), "kl")
+    used = w != 0
+    loss = float((w[used].astype(np.float64) * rows[used]).sum())
+    near(float(got.loss), loss, float((np.abs(w[used]) * 2 * ABS * (size + np.abs(rows))[used]).sum()) + 2 * F32_ROUND * abs(loss), "loss")
+    near_grad(got.grad, dtype, soft, tokens, a, h, np.abs(w * (1.0 if gl is None else gl)) * 2 * ABS * size, 1.0)
+    return got
+
+
+def rows_of(seed, B, V, dtype, keep):
+    rng, x, tokens, mask = make_rows(seed, B, V, dtype, keep)
+    if mask is not None:
+        mask[1, tokens[1]] = 1  # (make_rows leaves these two without their token)
+        mask[2, tokens[2]] = 1
+    tokens[:] = np.where((tokens < 0) | (tokens >= V), 1, tokens)
+    if mask is not None:
+        mask[np.arange(B), tokens] = 1
+    base = np.array([s.logp for s in softmaxes(x, dtype, mask, tokens)])
+    return rng, x, tokens, mask, base
+
+
+@pytest.mark.parametrize("dtype,keep,V", FORMS)
+def test_an_advantage_of_zero_takes_nothing_from_any_ratio(dev, dtype, keep, V):
+    """rho = e^d leaves fp32 above d = 88.7; 0 times it is 0, not NaN."""
+    _, x, tokens, mask, base = rows_of(11, 9, V, dtype, keep)
+    far = np.array([0.0, 79.0, 81.0, 88.5, 89.0, 120.0, 180.0, 360.0, 650.0])
+    adv = np.zeros(9)
+    adv[0] = 1.0
+    got = policy(dev, x, dtype, tokens, mask, base - far, None, adv, np.ones(9), ent=0.01)
+    assert np.isfinite(float(got.loss))
+    assert not policy(dev, x, dtype, tokens, mask, base - far, None, adv, np.ones(9)).grad[1:].any()
+
+
+@pytest.mark.parametrize("dtype,keep,V", FORMS)
+def test_large_ratios_times_small_advantages(dev, dtype, keep, V):
+    """-A rho is within fp32 where rho alone is not; so is its gradient, and
+    the one that a weight brings back."""
+    _, x, tokens, mask, base = rows_of(12, 8, V, dtype, keep)
+    far = np.array([70.0, 81.0, 85.0, 90.0, 100.0, 110.0, 95.0, 88.0])
+    adv = -np.array([1e-3, 1e-3, 1e-2, 1e-10, 1e-20, 1e-25, 1e-30, 1.0])
+    w = np.array([1.0, 0.5, 1e-3, 1e-3, 1.0, 1e-4, 1e-6, 1e-6])
+    policy(dev, x, dtype, tokens, mask, base - far, None, adv, w)
+
+
+@pytest.mark.parametrize("dtype,keep,V", FORMS)
+def test_large_kl_terms(dev, dtype, keep, V):
+    """kl_coef e^q is within fp32 where e^q alone is not."""
+    _, x, tokens, mask, base = rows_of(13, 8, V, dtype, keep)
+    q = np.array([-700.0, -90.0, 0.0, 79.0, 81.0, 88.0, 90.0, 93.0])
+    policy(dev, x, dtype, tokens, mask, base, base + q, np.ones(8), np.full(8, 0.01), kl=1e-4)
+
+
+@pytest.mark.parametrize("dtype,keep,V", FORMS)
+def test_gradients_of_rows_with_a_weight_of_zero(dev, dtype, keep, V):
+    """A padded batch: rows of weight 0 whose tokens and reference values are
+    fillers, so that their ratios and KL terms leave fp32, have no gradient."""
+    import top_selection_row_gb300 as q
+
+    rng, x, tokens, mask, base = rows_of(14, 8, V, dtype, keep)
+    f = np.float32
+    old, ref, w = base.copy(), base.copy(), np.ones(8)
+    w[3:] = 0.0
+    old[3:], ref[3:] = base[3:] - 150.0, base[3:] + 150.0
+    adv = rng.standard_normal(8)
+    got = q.qrita_policy_loss(to_device(x, dtype, dev), put(dev, tokens), put(dev, old, f), put(dev, adv, f), ref_logp=put(dev, ref, f),
+                              weights=put(dev, w, f), mask=put(dev, mask), kl_coef=0.1)
+    assert not got.grad[3:].any() and got.grad[[0, 2]].any(dim=1).all()  # (row 1 keeps its token alone: 0)

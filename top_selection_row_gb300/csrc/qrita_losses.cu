@@ -440,6 +440,15 @@ __device__ __forceinline__ float exp_minus_tangent(float q) {
   return 0.5f * q * q * r;
 }
 
+// v e^d where e^d alone may leave fp32 (d above kFarExp): by two factors of
+// e^(d/2), which reach every product that fp32 holds of a normal v. 0 stays 0.
+constexpr float kFarExp = 80.f;
+__device__ __forceinline__ float times_far_exp(float v, F2 d) {
+  if (v == 0.f && d.hi < INFINITY) return 0.f;
+  const float h = expf(0.5f * d.hi) * (1.f + 0.5f * d.lo);
+  return v * h * h;
+}
+
 // A, Hc and the token's entry from the weights a, h of dlogp and dH.
 __device__ __forceinline__ RowGrad row_grad(float a, float h, float logp, float H, float ln_s, float m, float s,
                                             float inv_t) {
@@ -527,19 +536,32 @@ __device__ __forceinline__ RowGrad row_weights(const LossParams& p, int op, cons
     if (p.old_logp != nullptr)
       d = isinf(in.old_logp) ? f2_make(-in.old_logp, 0.f) : f2_sub(v.logp, f2_make(in.old_logp, 0.f));
     // rho = 1 + (e^d - 1): near 1 one rounding of the product is what it costs
-    float more = expm1f(d.hi);
-    if (fabsf(d.hi) < 80.f) more = fmaf(d.lo, more + 1.f, more);
-    v.step = more > -0.5f ? fmaf(-in.adv, more, -in.adv) : -in.adv * (expf(d.hi) * (1.f + d.lo));
+    const float adv_w = in.adv * in.w;
+    if (d.hi > kFarExp) {
+      v.step = times_far_exp(-in.adv, d);
+      a = times_far_exp(-adv_w, d);
+    } else {
+      float more = expm1f(d.hi);
+      if (d.hi > -kFarExp) more = fmaf(d.lo, more + 1.f, more);
+      if (more > -0.5f) {
+        v.step = fmaf(-in.adv, more, -in.adv);
+        a = fmaf(-adv_w, more, -adv_w);
+      } else {
+        const float rho = expf(d.hi) * (1.f + d.lo);
+        v.step = -in.adv * rho;
+        a = -adv_w * rho;
+      }
+    }
     // rho against the clip, on the logarithms
     v.over = pair_above(d, p.ln_hi);
     v.bound = (in.adv > 0.f && v.over) || (in.adv < 0.f && pair_above(p.ln_lo, d));
-    a = v.bound ? 0.f : v.step;
-    if (v.lp != v.lp) a = v.lp;
+    if (v.bound) a = 0.f;
     if (p.ref_logp != nullptr) {
       v.q = (in.ref_logp - v.logp.hi) - v.logp.lo;
-      if (p.kl_coef != 0.f) a = fmaf(-p.kl_coef, expm1f(v.q), a);
+      const float kl_w = p.kl_coef * in.w;
+      if (p.kl_coef != 0.f) a = v.q > kFarExp ? a - times_far_exp(kl_w, f2_make(v.q, 0.f)) : fmaf(-kl_w, expm1f(v.q), a);
     }
-    a *= in.w;
+    if (v.lp != v.lp) a = v.lp;
     if (ENT) h = -p.entropy_coef * in.w;
   }
   return row_grad(a, h, v.lp, v.H, v.ln_s, st.m, st.s.hi, p.inv_t);
@@ -557,7 +579,8 @@ __device__ __forceinline__ void row_out(const LossParams& p, int op, RowStat* st
       loss = v.lp != v.lp ? v.lp : v.bound ? -in.adv * (v.over ? p.clip_hi : p.clip_lo) : v.step;
       if (p.ref_logp != nullptr) {
         kl = exp_minus_tangent(v.q);
-        if (p.kl_coef != 0.f) loss = fmaf(p.kl_coef, kl, loss);
+        if (p.kl_coef != 0.f)
+          loss = v.q > kFarExp ? loss + times_far_exp(p.kl_coef, f2_make(v.q, 0.f)) : fmaf(p.kl_coef, kl, loss);
       }
       if (ENT) loss = fmaf(-p.entropy_coef, v.H, loss);
     }
