@@ -354,7 +354,9 @@ int qrita_token_logprobs_grad(const void* logits, int dtype, int64_t B, int64_t 
  *                 (rho = 1, and its gradient that of logp).
  *   ref_logp      float[B] or NULL: NULL leaves the KL term out (kl is 0).
  *   advantages    float[B].
- *   weights       float[B] or NULL: NULL weighs every row 1 / B.
+ *   weights       float[B] or NULL: NULL weighs every row 1 / B. A row of
+ *                 weight 0 adds nothing to the loss or the gradient, however
+ *                 large its value (NaN rows apart).
  *   clip_low      in [0, 1];  clip_high >= 0 (infinity: no upper clip).
  *   kl_coef       finite, >= 0;  entropy_coef finite.
  *   grad_loss     float[1] or NULL: the gradient of the loss itself (NULL: 1),

@@ -106,3 +106,41 @@ def test_gradients_of_rows_with_a_weight_of_zero(dev, dtype, keep, V):
     got = q.qrita_policy_loss(to_device(x, dtype, dev), put(dev, tokens), put(dev, old, f), put(dev, adv, f), ref_logp=put(dev, ref, f),
                               weights=put(dev, w, f), mask=put(dev, mask), kl_coef=0.1)
     assert not got.grad[3:].any() and got.grad[[0, 2]].any(dim=1).all()  # (row 1 keeps its token alone: 0)
+
+
+@pytest.mark.parametrize("dtype,keep,V", FORMS)
+def test_losses_of_rows_with_a_weight_of_zero(dev, dtype, keep, V):
+    """The same batch's loss is that of the rows that count; with a NaN among the
+    kept logits of a row of weight 0 it is NaN, as the row contract says."""
+    rng, x, tokens, mask, base = rows_of(15, 8, V, dtype, keep)
+    old, ref, w = base - 0.1, base + 0.2, np.ones(8)
+    w[3:] = 0.0
+    old[3:], ref[3:] = base[3:] - 150.0, base[3:] + 150.0
+    adv = rng.standard_normal(8)
+    adv[4] = -1.0  # (no clip: its row loss is beyond fp32 by its ratio too)
+    got = policy(dev, x, dtype, tokens, mask, old, ref, adv, w, kl=0.1)
+    assert np.isinf(got.row_loss[3:].cpu().numpy()).all() and np.isfinite(float(got.loss))
+    x[5, tokens[5]] = 0x7FC0 if dtype == "bf16" else np.nan
+    import top_selection_row_gb300 as q
+
+    f = np.float32
+    got = q.qrita_policy_loss(to_device(x, dtype, dev), put(dev, tokens), put(dev, old, f), put(dev, adv, f), ref_logp=put(dev, ref, f),
+                              weights=put(dev, w, f), mask=put(dev, mask), kl_coef=0.1)
+    assert np.isnan(float(got.loss)) and got.grad[5].isnan().any()
+
+
+def test_preference_pairs_with_a_weight_of_zero(dev):
+    """A pair whose loss leaves fp32 and has no weight adds nothing."""
+    import torch
+
+    import top_selection_row_gb300 as q
+
+    _, x, tokens, _, _ = rows_of(16, 4, 300, "f32", 0)
+    xd, td, starts = put(dev, x), put(dev, tokens), put(dev, np.arange(5, dtype=np.int32))
+    far = np.zeros(4, np.float32)
+    far[2], far[3] = 3e38, -3e38
+    kw = dict(ref_logp=put(dev, far), beta=10.0)
+    got = q.qrita_preference_loss(xd, td, starts, weights=put(dev, np.array([1, 0], np.float32)), **kw)
+    one = q.qrita_preference_loss(xd[:2], td[:2], starts[:3], ref_logp=kw["ref_logp"][:2], weights=put(dev, np.ones(1, np.float32)), beta=10.0)
+    assert np.isinf(float(got.pair_loss[1])) and torch.equal(got.loss, one.loss)
+    assert torch.equal(got.grad[:2], one.grad) and not got.grad[2:].any()

@@ -1356,11 +1356,15 @@ __global__ void __launch_bounds__(kResThreads, kResBlocks) resident_kernel(const
 }
 
 // *out = sum of w[i] v[i] by one block of N threads in one fixed order, in
-// fp64 (w null: 1 / n). slots: N / 32 doubles of shared memory.
+// fp64 (w null: 1 / n). A weight of 0 takes nothing of a value that has left
+// fp32 (0, not 0 * inf); NaN stays. slots: N / 32 doubles of shared memory.
 template <int N>
 __device__ __forceinline__ void weighted_sum(const float* v, const float* w, int64_t n, float* out, double* slots) {
   double s = 0.0;
-  for (int64_t i = threadIdx.x; i < n; i += N) s += static_cast<double>(v[i]) * (w != nullptr ? w[i] : 1.0);
+  for (int64_t i = threadIdx.x; i < n; i += N) {
+    const float x = v[i], weight = w != nullptr ? w[i] : 1.f;
+    s += weight == 0.f && isinf(x) ? 0.0 : static_cast<double>(x) * weight;
+  }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(kAll, s, o);
   if ((threadIdx.x & 31) == 0) slots[threadIdx.x >> 5] = s;
