@@ -144,3 +144,45 @@ def test_preference_pairs_with_a_weight_of_zero(dev):
     one = q.qrita_preference_loss(xd[:2], td[:2], starts[:3], ref_logp=kw["ref_logp"][:2], weights=put(dev, np.ones(1, np.float32)), beta=10.0)
     assert np.isinf(float(got.pair_loss[1])) and torch.equal(got.loss, one.loss)
     assert torch.equal(got.grad[:2], one.grad) and not got.grad[2:].any()
+
+
+@pytest.mark.parametrize("bad", [np.nan, np.inf])
+@pytest.mark.parametrize("dtype,V,keep", [("f32", 9, 4), ("bf16", 1003, 40), ("f32", 40000, 300), ("bf16", 40000, 20000)])
+def test_nan_or_infinity_beside_a_token_of_no_probability(dev, bad, dtype, V, keep):
+    """NaN or +inf among the kept logits makes the row NaN wherever its token
+    is: kept, not kept, or at -inf. Row 3 holds it outside the kept set."""
+    import top_selection_row_gb300 as q
+
+    rng = np.random.default_rng(V)
+    x = (rng.standard_normal((5, V)) * 2).astype(np.float32)
+    mask = np.zeros((5, V), np.uint8)
+    tokens = np.zeros(5, np.int32)
+    for r in range(5):
+        ids = rng.permutation(V)[:keep]
+        mask[r, ids] = 1
+        tokens[r] = ids[0]
+        if r < 3:
+            x[r, ids[1]] = bad
+    mask[0, tokens[0]] = 0
+    x[2, tokens[2]] = -np.inf
+    mask[3, tokens[3] - 1] = 0
+    x[3, tokens[3] - 1] = bad
+    mask[4, tokens[4]] = 0
+    if dtype == "bf16":
+        from workloads import f32_to_bf16_bits
+
+        x = f32_to_bf16_bits(x)
+    soft = softmaxes(x, dtype, mask, tokens)
+    assert np.isnan([s.logp for s in soft[:3]]).all() and np.isfinite(soft[3].logp) and soft[4].logp == -np.inf
+    xd, td, md = to_device(x, dtype, dev), put(dev, tokens), put(dev, mask)
+    logp, ent = q.qrita_token_logprobs(xd, td, mask=md, entropy=True)
+    near_rows(logp.cpu().numpy(), [s.logp for s in soft], "logp")
+    near_rows(ent.cpu().numpy(), [s.entropy for s in soft], "entropy", extra=ABS)
+    near_rows(q.qrita_token_logprobs(xd, td, mask=md)[0].cpu().numpy(), [s.logp for s in soft], "logp alone")
+    a, h = rng.standard_normal(5).astype(np.float32), rng.standard_normal(5).astype(np.float32)
+    got = q.qrita_token_logprobs_grad(xd, td, put(dev, a), put(dev, h), mask=md)
+    near_grad(got, dtype, soft, tokens, a, h, np.zeros(5), 1.0)
+    step = q.qrita_policy_loss(xd, td, None, put(dev, a), mask=md)
+    rows = step.row_loss.cpu().numpy()
+    assert np.isnan(rows[:3]).all() and np.isfinite(rows[3:]).all() and np.isnan(float(step.loss))
+    near_grad(step.grad, dtype, soft, tokens, -a / 5, np.zeros(5), np.zeros(5), 1.0)

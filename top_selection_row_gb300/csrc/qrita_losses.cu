@@ -503,7 +503,8 @@ __device__ __forceinline__ RowVals row_vals(const LossParams& p, const RowIn& in
   const bool empty = st.s.hi == 0.f;  // nothing kept, or only -inf
   const F2 ln_s = empty ? f2_make(0.f, 0.f) : ln_pair(f2_merge(st.s, f2_make((st.s.hi - 1.f) * kExLow, 0.f)));
   v.ln_s = ln_s.hi;
-  v.logp = f2_make(-INFINITY, 0.f);
+  // (a token that is not kept has probability 0 unless the row's sums are NaN)
+  v.logp = f2_make(st.s.hi == st.s.hi ? -INFINITY : st.s.hi, 0.f);
   if (in.kept_t && !empty) {
     F2 d;
     two_sum(in.x_t, -st.m, d.hi, d.lo);
