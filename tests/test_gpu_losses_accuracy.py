@@ -1,0 +1,96 @@
+"""How far logp and H are from their definitions, at the accuracy include/qrita.h
+states, which is finer than fp32 holds of a logp near -20.
+
+A ratio and a KL term see logp before its rounding to fp32. With a reference
+that lies q = 2^-6 above the exact logp, kl = e^q - 1 - q gives q, and so logp,
+back to 2^-23 of kl, which is q 2^-24 = 1e-9: that is how logp is read here.
+
+Bounds, from the arithmetic: a weight is off by at most 2^-22 (the instruction)
+and 2^-24 times its exponent's logarithm (one rounding of the exponent); a
+thread's compensated sum of groups, a group's tree of at most 5 additions and
+the merges by at most 6 * 2^-24: log S, and so logp, is off by no more than
+  BOUND(E) = 2^-22 + 2^-24 (6 + E),  E the mean of |log p_j / p_max| under p.
+These errors are spread over many weights with either sign and their mean is
+taken back: the root mean square over rows, and the mean, stay below RMS = 1e-7.
+H = log S + E exactly, E a quotient of two such sums: twice the bound, and
+RMS (1 + E).
+"""
+
+import numpy as np
+import pytest
+
+from test_gpu_losses import dev  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+
+RMS = 1e-7
+HALF = 2.0 ** -24
+
+
+def bound(E):
+    return 2.0 ** -22 + HALF * (6 + E)
+
+
+def exact(x, tokens, inv_t, mask=None):
+    """(logp, H, E) of every row in fp64."""
+    import torch
+
+    logp, H, E = [], [], []
+    for a in range(0, x.shape[0], 32):
+        u = x[a:a + 32].double() * inv_t
+        if mask is not None:
+            u = u.masked_fill(~mask[a:a + 32], -np.inf)
+        y = u - u.amax(dim=1, keepdim=True)
+        e = y.exp()
+        S = e.sum(dim=1)
+        mean = -(e * y.clamp(min=-1e6)).sum(dim=1) / S
+        logp.append(y.gather(1, tokens[a:a + 32, None].long())[:, 0] - S.log())
+        H.append(S.log() + mean)
+        E.append(mean)
+    return [torch.cat(v).cpu().numpy() for v in (logp, H, E)]
+
+
+def check(x, tokens, inv_t=1.0, mask=None):
+    import torch
+
+    import top_selection_row_gb300 as q
+
+    want, H, E = exact(x, tokens, inv_t, mask)
+    ref = torch.from_numpy((want + 2.0 ** -6).astype(np.float32)).to(x.device)
+    zero = torch.zeros_like(ref)
+    for form in (dict(grad=False), dict(), dict(grad=False, entropy=True)):  # each of the kernels' sums
+        got = q.qrita_policy_loss(x, tokens, ref, zero, ref_logp=ref, mask=mask, inv_temperature=inv_t, **form)
+        kl = got.kl.cpu().numpy().astype(np.float64)
+        d = np.full_like(kl, 2.0 ** -6)
+        for _ in range(6):  # e^d - 1 - d = kl, by Newton
+            d -= (np.expm1(d) - d - kl) / np.expm1(d)
+        err = ref.cpu().numpy().astype(np.float64) - d - want
+        assert (np.abs(err) <= bound(E) + 2e-9).all(), (form, np.abs(err).max(), bound(E).max())
+        assert np.sqrt((err ** 2).mean()) <= RMS and abs(err.mean()) <= RMS, (form, np.sqrt((err ** 2).mean()), err.mean())
+        # the fp32 value given out is that, rounded
+        out = got.logp.cpu().numpy().astype(np.float64)
+        assert (np.abs(out - want) <= bound(E) + HALF * np.abs(want) * 1.01).all()
+
+
+def logits(dev, seed, B, V, dtype, scale=2.0):
+    import torch
+
+    g = torch.Generator(device=dev).manual_seed(seed)
+    x = torch.randn(B, V, generator=g, device=dev) * scale
+    where = torch.randint(0, V, (B, 8), generator=g, device=dev)
+    x.scatter_add_(1, where, 5 + 2 * torch.randn(B, 8, generator=g, device=dev))
+    x = x.to(torch.float32 if dtype == "f32" else torch.bfloat16)
+    return g, x
+
+
+DTYPES = pytest.mark.parametrize("dtype", ["f32", "bf16"])
+
+
+@DTYPES
+@pytest.mark.parametrize("inv_t", [1.0, 0.71875, 0.75, 1.25, 1.4375])
+@pytest.mark.parametrize("B,V", [(256, 3001), (128, 50021), (40, 128256)])
+def test_rare_tokens_at_any_temperature(dev, dtype, inv_t, B, V):
+    """The least likely token of each row: what the temperature's own rounding
+    would move the most."""
+    _, x = logits(dev, V, B, V, dtype)
+    check(x, x.float().argmin(dim=1).int(), inv_t)

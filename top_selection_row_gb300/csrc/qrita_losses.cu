@@ -139,6 +139,22 @@ __device__ __forceinline__ float fmax3(float a, float b, float c) {
 
 __device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
 
+// d c for the sums' exponents. c in fp32 is off by up to 6e-8 of itself, the same
+// way for every logit of a row, and leaves logp off by that of the token's
+// distance from the row's mean exponent (1.1e-6 at a distance of 20). Sums
+// without an entropy take c as hi + lo, rounded once (lo is above 0, so that a
+// difference of -inf stays -inf); with one, log S is put right by the mean
+// exponent that the entropy's sum gives (one more instruction a pair there: 91.1
+// us against 87.0 for 1024 x 262144 bf16).
+template <bool ENT>
+__device__ __forceinline__ float scaled(float d, const Scale& c) {
+  return ENT ? d * c.near : fmaf(d, c.hi, d * c.lo);
+}
+template <bool ENT>
+__device__ __forceinline__ float2 scaled2(float2 d, const Scale& c) {
+  return ENT ? mul2(d, both(c.near)) : fma2(d, both(c.hi), mul2(d, both(c.lo)));
+}
+
 // Element access. A row is worked on in units of 16 bytes, aligned in memory:
 // `head` elements before the first unit, then the units, then a tail.
 template <int DT>
@@ -231,9 +247,9 @@ struct Running {
   float m = -INFINITY, ref = 0.f, s = 0.f, t = 0.f;
   float lo = 0.f;  // to be added to s
 
-  __device__ __forceinline__ void raise(float x, float c) {
+  __device__ __forceinline__ void raise(float x, const Scale& c) {
     // before the first finite logit the sums are 0 (or NaN), whatever the factor
-    const float d = fmaxf((m - x) * c, kMinExp);
+    const float d = fmaxf(scaled<ENT>(m - x, c), kMinExp);
     const float f = ex2(d);
     if (ENT) t = (t + d * s) * f;
     s *= f;
@@ -245,9 +261,9 @@ struct Running {
     lo = d - (sum - s);
     s = sum;
   }
-  __device__ __forceinline__ void add_one(float x, float c) {
+  __device__ __forceinline__ void add_one(float x, const Scale& c) {
     if (x > m) raise(x, c);
-    const float y = (x - ref) * c;
+    const float y = scaled<ENT>(x - ref, c);
     const float e = ex2(y);
     add(e);
     if (ENT) t = fmaf(e, y < kMinExp ? kMinExp : y, t);
@@ -256,16 +272,16 @@ struct Running {
   // running one. The more pairs, the more independent exponentials follow
   // one test of the maximum.
   template <int N>
-  __device__ __forceinline__ void add_unit(const float2 (&x)[N], float c) {
+  __device__ __forceinline__ void add_unit(const float2 (&x)[N], const Scale& c) {
     float top = m;
 #pragma unroll
     for (int i = 0; i < N; ++i) top = fmax3(top, x[i].x, x[i].y);
     if (top > m) raise(top, c);
-    const float2 nr = both(-ref), cc = both(c);
+    const float2 nr = both(-ref);
     float2 es[N], ts[N];
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      const float2 y = mul2(add2(x[i], nr), cc);
+      const float2 y = scaled2<ENT>(add2(x[i], nr), c);
       es[i] = make_float2(ex2(y.x), ex2(y.y));
       if (ENT) ts[i] = mul2(es[i], make_float2(y.x < kMinExp ? kMinExp : y.x, y.y < kMinExp ? kMinExp : y.y));
     }
@@ -283,9 +299,9 @@ struct Running {
 
 // Sums relative to m raised to `to` (>= m).
 template <bool ENT>
-__device__ __forceinline__ void stat_shift(Stat& a, float to, float c) {
+__device__ __forceinline__ void stat_shift(Stat& a, float to, const Scale& c) {
   if (a.m == to) return;
-  const float d = fmaxf((a.m - to) * c, kMinExp);
+  const float d = fmaxf(scaled<ENT>(a.m - to, c), kMinExp);
   const float f = ex2(d);
   if (ENT) {
     a.t = f2_merge(a.t, f2_prod(d, a.s.hi));
@@ -299,7 +315,7 @@ __device__ __forceinline__ void stat_shift(Stat& a, float to, float c) {
 // The sum of a Stat over the first W lanes of a warp (a power of two), in
 // every one of those lanes.
 template <bool ENT, int W>
-__device__ __forceinline__ Stat lanes_stat(Stat v, float c) {
+__device__ __forceinline__ Stat lanes_stat(Stat v, const Scale& c) {
   float m = v.m;
 #pragma unroll
   for (int o = W / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kAll, m, o));
@@ -333,7 +349,7 @@ __device__ __forceinline__ void put_stat(const Running<ENT>& r, StatSlots<THREAD
 // merging pairs in every warp first would cost each of them 100 instructions,
 // as many as 25 logits a lane take.
 template <int THREADS, bool ENT>
-__device__ __forceinline__ Stat warp_stat(float c, const StatSlots<THREADS>& slots) {
+__device__ __forceinline__ Stat warp_stat(const Scale& c, const StatSlots<THREADS>& slots) {
   const int lane = threadIdx.x & 31;
   Stat v;
   v.m = -INFINITY;
@@ -348,7 +364,7 @@ __device__ __forceinline__ Stat warp_stat(float c, const StatSlots<THREADS>& slo
   for (int o = 16; o > 0; o >>= 1) v.m = fmaxf(v.m, __shfl_xor_sync(kAll, v.m, o));
 #pragma unroll
   for (int i = 0; i < THREADS / 32; ++i) {
-    const float d = ms[i] == v.m ? 0.f : fmaxf((ms[i] - v.m) * c, kMinExp);
+    const float d = ms[i] == v.m ? 0.f : fmaxf(scaled<ENT>(ms[i] - v.m, c), kMinExp);
     const float f = ex2(d), s = slots.s[lane + 32 * i] * f;
     f2_add(v.s, s);
     v.s.lo += slots.lo[lane + 32 * i] * f + (d != 0.f ? s * kExLow : 0.f);
@@ -376,7 +392,7 @@ __device__ __forceinline__ void send_stat(const Stat& v, uint32_t rank, uint32_t
 }
 
 template <bool ENT>
-__device__ __forceinline__ Stat merge_ranks(uint32_t C, float c, const Stat* ranks) {
+__device__ __forceinline__ Stat merge_ranks(uint32_t C, const Scale& c, const Stat* ranks) {
   const int lane = threadIdx.x & (kMaxRanks - 1);
   Stat v = ranks[lane];
   if (lane >= static_cast<int>(C)) {
@@ -389,7 +405,7 @@ __device__ __forceinline__ Stat merge_ranks(uint32_t C, float c, const Stat* ran
 // The cluster's sums from those the first warp of every CTA has, in that warp.
 // (Every CTA of the cluster is running by now.)
 template <bool ENT>
-__device__ __forceinline__ void cluster_stat(Stat& v, float c, uint32_t rank, uint32_t C, Stat* ranks) {
+__device__ __forceinline__ void cluster_stat(Stat& v, const Scale& c, uint32_t rank, uint32_t C, Stat* ranks) {
   if (C == 1) return;
   if (threadIdx.x < 32) send_stat<ENT>(v, rank, C, ranks);
   cluster_sync_all();
@@ -399,7 +415,7 @@ __device__ __forceinline__ void cluster_stat(Stat& v, float c, uint32_t rank, ui
 // The row's sums from every thread's of its cluster of C CTAs, valid in the
 // first warp of every CTA.
 template <int THREADS, bool ENT>
-__device__ __forceinline__ Stat row_stat(const Running<ENT>& r, float c, uint32_t rank, uint32_t C,
+__device__ __forceinline__ Stat row_stat(const Running<ENT>& r, const Scale& c, uint32_t rank, uint32_t C,
                                          StatSlots<THREADS>& slots) {
   put_stat(r, slots);
   __syncthreads();
@@ -503,22 +519,25 @@ __device__ __forceinline__ RowVals row_vals(const LossParams& p, const RowIn& in
   const bool empty = st.s.hi == 0.f;  // nothing kept, or only -inf
   const F2 ln_s = empty ? f2_make(0.f, 0.f) : ln_pair(f2_merge(st.s, f2_make((st.s.hi - 1.f) * kExLow, 0.f)));
   v.ln_s = ln_s.hi;
+  // of y_j ln2 under p
+  const float mean = ENT && !empty ? f2_float(st.t) / st.s.hi * static_cast<float>(kLn2) : 0.f;
   // (a token that is not kept has probability 0 unless the row's sums are NaN)
   v.logp = f2_make(st.s.hi == st.s.hi ? -INFINITY : st.s.hi, 0.f);
   if (in.kept_t && !empty) {
+    // d ln S / d ln c is that mean: from c.near back to c
+    const F2 ln_sc = ENT ? f2_merge(ln_s, f2_make(-mean * p.c.near_off, 0.f)) : ln_s;
     F2 d;
     two_sum(in.x_t, -st.m, d.hi, d.lo);
     if (fabsf(d.hi) < 1e30f) {
-      F2 y = f2_mul(d, p.c_ln2);  // (x_t - m) c ln2
-      y.lo = fmaf(d.hi, p.c_ln2_lo, y.lo);
-      v.logp = f2_sub(y, ln_s);
+      F2 y = f2_mul(d, p.inv_t);  // (x_t - m) inv_t
+      y.lo = fmaf(d.hi, p.inv_t_lo, y.lo);
+      v.logp = f2_sub(y, ln_sc);
     } else {
-      v.logp.hi = d.hi * p.c_ln2 - ln_s.hi;  // no digit of ln S counts (or -inf, or NaN)
+      v.logp.hi = d.hi * p.inv_t - ln_s.hi;  // no digit of ln S counts (or -inf, or NaN)
     }
   }
   v.lp = f2_float(v.logp);
-  // ln S less the mean of y_j ln2
-  v.H = ENT && !empty ? f2_float(f2_sub(ln_s, f2_make(f2_float(st.t) / st.s.hi * static_cast<float>(kLn2), 0.f))) : 0.f;
+  v.H = ENT && !empty ? f2_float(f2_sub(ln_s, f2_make(mean, 0.f))) : 0.f;
   v.joins = v.lp != -INFINITY;  // (NaN joins)
   v.step = v.q = 0.f;
   v.over = v.bound = false;
@@ -633,7 +652,7 @@ __device__ __forceinline__ void write_grad(const LossParams& p, const Share<DT>&
   unsigned char* gu = grow + sh.head * E::kBytes;
   const bool vec = (reinterpret_cast<uintptr_t>(gu) & 15u) == 0;
   const bool zero = g.a == 0.f && g.h == 0.f;
-  const float2 nm = both(-g.m), cc = both(p.c), aa = both(g.a), hh = both(g.h);
+  const float2 nm = both(-g.m), cc = both(p.c.near), aa = both(g.a), hh = both(g.h);
   auto put = [&](int64_t u, const float2 (&v)[N]) {
     if (vec) {
       __stcs(reinterpret_cast<uint4*>(gu + u * 16), E::pack(v));
@@ -677,7 +696,7 @@ __device__ __forceinline__ void write_grad(const LossParams& p, const Share<DT>&
     const int64_t j = sh.end_index(threadIdx.x);
     if (j >= 0) {
       float v = 0.f;
-      if (!zero) v = grad_one<ENT>(E::load(sh.x, j), g, p.c);
+      if (!zero) v = grad_one<ENT>(E::load(sh.x, j), g, p.c.near);
       E::store(grow, j, v);
     }
   }
@@ -966,7 +985,7 @@ __global__ void __launch_bounds__(THREADS, kLossThreads * kLossBlocks / THREADS)
     unsigned long long s = 0ull, t = 0ull;
     for (int i = tid; i < count; i += THREADS) {
       const float x = list_x[i];
-      const float y = x == -INFINITY ? kMinExp : fmaxf((x - m) * p.c, kMinExp);
+      const float y = x == -INFINITY ? kMinExp : fmaxf(scaled<ENT>(x - m, p.c), kMinExp);
       const float e = bad ? 0.f : ex2(y);
       s += round_u64(e * kKeptScale);
       if (ENT) t += round_u64(e * -y * kKeptScale);
@@ -1031,7 +1050,7 @@ __global__ void __launch_bounds__(THREADS, kLossThreads * kLossBlocks / THREADS)
     }
     if (!zero)
       for (int i = tid; i < count; i += THREADS)
-        E::store(grow, lo + list[i], grad_one<ENT>(list_x[i], g, p.c));
+        E::store(grow, lo + list[i], grad_one<ENT>(list_x[i], g, p.c.near));
   } else {
     const bool gvec = (reinterpret_cast<uintptr_t>(grow + head * E::kBytes) & 15u) == 0;
     for (int64_t u0 = tid; u0 < n_u; u0 += THREADS * kUnroll) {
@@ -1049,8 +1068,8 @@ __global__ void __launch_bounds__(THREADS, kLossThreads * kLossBlocks / THREADS)
         E::unpack(w[k], x);
 #pragma unroll
         for (int i = 0; i < N; ++i) {
-          x[i].x = bits[k] >> (2 * i) & 1u ? grad_one<ENT>(x[i].x, g, p.c) : 0.f;
-          x[i].y = bits[k] >> (2 * i + 1) & 1u ? grad_one<ENT>(x[i].y, g, p.c) : 0.f;
+          x[i].x = bits[k] >> (2 * i) & 1u ? grad_one<ENT>(x[i].x, g, p.c.near) : 0.f;
+          x[i].y = bits[k] >> (2 * i + 1) & 1u ? grad_one<ENT>(x[i].y, g, p.c.near) : 0.f;
         }
         if (gvec) {
           *reinterpret_cast<uint4*>(grow + j * E::kBytes) = E::pack(x);
@@ -1064,7 +1083,7 @@ __global__ void __launch_bounds__(THREADS, kLossThreads * kLossBlocks / THREADS)
       }
     }
     if (end_j >= 0)
-      E::store(grow, end_j, !zero && end_kept ? grad_one<ENT>(E::load(xrow, end_j), g, p.c) : 0.f);
+      E::store(grow, end_j, !zero && end_kept ? grad_one<ENT>(E::load(xrow, end_j), g, p.c.near) : 0.f);
   }
   if (in.kept_t && token >= lo && token < hi) {
     __syncthreads();
@@ -1283,7 +1302,7 @@ __global__ void __launch_bounds__(kResThreads, kResBlocks) resident_kernel(const
   if (g.a == 0.f && g.h == 0.f) {
     write_grad<kResThreads, DT, ENT>(p, sh, row, g, token);
   } else {
-    const float2 nm = both(-g.m), cc = both(p.c), aa = both(g.a), hh = both(g.h);
+    const float2 nm = both(-g.m), cc = both(p.c.near), aa = both(g.a), hh = both(g.h);
     auto entries = [&](uint4 w, float2 (&e)[N]) {
       float2 x[N];
       E::unpack(w, x);
@@ -1337,7 +1356,7 @@ __global__ void __launch_bounds__(kResThreads, kResBlocks) resident_kernel(const
         }
       }
     }
-    if (end_j >= 0) E::store(grow, end_j, grad_one<ENT>(end_x, g, p.c));
+    if (end_j >= 0) E::store(grow, end_j, grad_one<ENT>(end_x, g, p.c.near));
     const int64_t u = (token - sh.head) / E::kUnit;  // (token < head: 0 or below, an end)
     const bool end = token < sh.head || u >= sh.nu;
     if (end ? sh.ends : (u >= sh.u_lo && u < sh.u_hi)) {

@@ -14,6 +14,12 @@ struct LossPair {
   float hi, lo;
 };
 
+// c = log2(e) * inv_temperature (weights are 2^((x - m) c)) as hi + lo with
+// lo > 0, and to nearest, which is off by near_off of c.
+struct Scale {
+  float hi, lo, near, near_off;
+};
+
 // Arguments of the loss kernels; null pointers are the optional arguments of
 // the C ABI.
 struct LossParams {
@@ -21,9 +27,8 @@ struct LossParams {
   int64_t B, V, ld;
   const uint8_t* mask;
   const int32_t* tokens;
-  float c;      // log2(e) * inv_temperature: weights are 2^((x - m) c)
-  float c_ln2, c_ln2_lo;  // c ln2 as a pair
-  float inv_t;
+  Scale c;
+  float inv_t, inv_t_lo;  // inv_temperature as a pair
   float inv_b;  // 1 / B
   uint32_t C;   // CTAs per row, and the units of it each of them takes
   int64_t per;

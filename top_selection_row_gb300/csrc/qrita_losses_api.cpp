@@ -26,8 +26,9 @@ int loss_args(const void* logits, int dtype, int64_t B, int64_t V, int64_t ld, c
   constexpr int64_t kMax = std::numeric_limits<int32_t>::max();
   if (B < 0 || B > kMax || V < 1 || V > kMax || ld < V) return QRITA_EINVAL;
   if (!(inv_temperature > 0.0) || !std::isfinite(inv_temperature)) return QRITA_EINVAL;
-  const float c = static_cast<float>(1.4426950408889634074 * inv_temperature);
-  if (!std::isfinite(c) || !std::isnormal(c)) return QRITA_EINVAL;
+  const double c = 1.4426950408889634074 * inv_temperature;
+  const float near = static_cast<float>(c);
+  if (!std::isfinite(near) || !std::isnormal(near)) return QRITA_EINVAL;
   if (grad != nullptr && ld_grad < V) return QRITA_EINVAL;
   std::memset(out, 0, sizeof(*out));
   out->logits = logits;
@@ -36,11 +37,13 @@ int loss_args(const void* logits, int dtype, int64_t B, int64_t V, int64_t ld, c
   out->ld = ld;
   out->mask = mask;
   out->tokens = tokens;
-  out->c = c;
-  const double c_ln2 = static_cast<double>(c) * 0.69314718055994530942;
-  out->c_ln2 = static_cast<float>(c_ln2);
-  out->c_ln2_lo = static_cast<float>(c_ln2 - out->c_ln2);
+  out->c.near = near;
+  out->c.near_off = static_cast<float>(near / c - 1.0);
+  out->c.hi = near < c ? near : std::nextafterf(near, 0.f);
+  out->c.lo = static_cast<float>(c - out->c.hi);
+  if (!(out->c.lo > 0.f)) out->c.lo = std::numeric_limits<float>::denorm_min();
   out->inv_t = static_cast<float>(inv_temperature);
+  out->inv_t_lo = static_cast<float>(inv_temperature - out->inv_t);
   out->inv_b = B > 0 ? static_cast<float>(1.0 / static_cast<double>(B)) : 0.f;
   out->grad = grad;
   out->ld_grad = ld_grad;
