@@ -94,3 +94,16 @@ def test_rare_tokens_at_any_temperature(dev, dtype, inv_t, B, V):
     would move the most."""
     _, x = logits(dev, V, B, V, dtype)
     check(x, x.float().argmin(dim=1).int(), inv_t)
+
+
+@DTYPES
+@pytest.mark.parametrize("span", [0.25, 1.0, 4.0, 20.0])
+@pytest.mark.parametrize("B,V", [(160, 50021), (320, 128256)])
+def test_rows_that_rise_slowly(dev, dtype, span, B, V):
+    """Ascending logits over a range of `span`: a thread meets a new maximum at
+    nearly each of its groups."""
+    import torch
+
+    x = (torch.arange(V, device=dev, dtype=torch.float64) * (span / V)).expand(B, V)
+    x = (x + torch.linspace(0, 0.3, B, device=dev, dtype=torch.float64)[:, None]).to(torch.float32 if dtype == "f32" else torch.bfloat16)
+    check(x.contiguous(), torch.arange(B, device=dev, dtype=torch.int32) * (V // B))

@@ -44,11 +44,15 @@ constexpr double kLn2 = 0.69314718055994530942;
 constexpr float kMinExp = -1000.0f;
 
 // The hardware's base-2 exponential is exact at 0 and lies low by 5.0e-8 of
-// its value on average over (-32, 0) (measured over 2^20 arguments, the same
+// its value on average over (-32, -1) (measured over 2^20 arguments, the same
 // to 1e-9 in every octave from -1 down; root mean square 5.8e-8). S takes the
 // mean back for the logits below the maximum, and again for every sum that
 // was shifted by an exponential: logp is then off by 4e-8 instead of 1.2e-7.
+// (Above -1 the instruction lies low by 2.3e-8, and above 0 by nothing: rows whose
+// weight is all near their maximum come out up to 5e-8 low in logp.)
 constexpr float kExLow = 5.0e-8f;
+// The same of a factor 2^d that shifts a sum (d <= 0): 2.3e-8 above -1.
+__device__ __forceinline__ float shift_low(float d) { return d > -1.f ? 2.3e-8f : kExLow; }
 
 // Rows this short (bytes that their sums read) take blocks of half the threads
 // where a block has one whole: more of them on an SM cover the chain of steps
@@ -236,25 +240,39 @@ struct Share {
   static constexpr int kEnds = 2 * (Elem<DT>::kUnit - 1);  // at most
 };
 
-// A thread's running sums, relative to the largest logit it has seen (0
-// stands for -inf in ref). S is compensated: where one token holds most of a
-// row, every other group of its thread's share rounds at that token's weight
-// (logp of 700 x 128256 fp32, 157 groups a thread: root mean square error 5.5e-8,
+// A thread's running sums, relative to a reference: the first finite logit, and
+// each one that lies more than an octave of weight (a factor of 2) above the last
+// reference. So the sums are shifted, by an exponential that is off by its own
+// error, at most once an octave, and what such errors make of the older sums
+// halves each time. (With every new maximum as the reference, a row that rises
+// slowly is shifted at each of its groups: logp of 128256 ascending logits over
+// ranges of 0.25 to 4 off by 1.9e-7 to 4.8e-7 root mean square, and by more when
+// each of those shifts is put right by the mean; below 1e-7 this way, for 0.3 to
+// 0.9 % of the time.) A reference's own weight is exactly 1, so a token that holds
+// most of a row keeps the digits of log p: it is a reference, or there is a
+// logit with more than half its weight.
+//
+// S is compensated: where one token holds most of a row, every other group of its
+// thread's share rounds at that token's weight (logp of 700 x 128256 fp32, one
+// CTA a row, 31 groups and 2 single units a thread: root mean square error 5.5e-8,
 // 1.4e-7 without, for 0.5 % of the time). Taking that token's weight out of its
 // own group's sum as well would leave 3.6e-8, for 3 to 7 % of the time.
 template <bool ENT>
 struct Running {
-  float m = -INFINITY, ref = 0.f, s = 0.f, t = 0.f;
-  float lo = 0.f;  // to be added to s
+  float ref = 0.f, s = 0.f, t = 0.f;
+  float lo = 0.f;           // to be added to s
+  float limit = -INFINITY;  // an octave above ref; -inf before the first finite logit
 
+  __device__ __forceinline__ float m() const { return limit == -INFINITY ? -INFINITY : ref; }
   __device__ __forceinline__ void raise(float x, const Scale& c) {
-    // before the first finite logit the sums are 0 (or NaN), whatever the factor
-    const float d = fmaxf(scaled<ENT>(m - x, c), kMinExp);
+    // (the first time the sums are 0, or NaN, whatever the factor)
+    const float d = fminf(fmaxf(scaled<ENT>(ref - x, c), kMinExp), 0.f);
     const float f = ex2(d);
     if (ENT) t = (t + d * s) * f;
     s *= f;
-    lo *= f;
-    m = ref = x;
+    lo = fmaf(lo, f, s * kExLow);
+    ref = x;
+    limit = x + c.octave;
   }
   __device__ __forceinline__ void add(float e) {
     const float d = e + lo, sum = s + d;
@@ -262,7 +280,7 @@ struct Running {
     s = sum;
   }
   __device__ __forceinline__ void add_one(float x, const Scale& c) {
-    if (x > m) raise(x, c);
+    if (x > limit) raise(x, c);
     const float y = scaled<ENT>(x - ref, c);
     const float e = ex2(y);
     add(e);
@@ -273,10 +291,10 @@ struct Running {
   // one test of the maximum.
   template <int N>
   __device__ __forceinline__ void add_unit(const float2 (&x)[N], const Scale& c) {
-    float top = m;
+    float top = limit;
 #pragma unroll
     for (int i = 0; i < N; ++i) top = fmax3(top, x[i].x, x[i].y);
-    if (top > m) raise(top, c);
+    if (top > limit) raise(top, c);
     const float2 nr = both(-ref);
     float2 es[N], ts[N];
 #pragma unroll
@@ -308,7 +326,7 @@ __device__ __forceinline__ void stat_shift(Stat& a, float to, const Scale& c) {
     a.t = f2_mul(a.t, f);
   }
   a.s = f2_mul(a.s, f);
-  a.s.lo = fmaf(a.s.hi, kExLow, a.s.lo);
+  a.s.lo = fmaf(a.s.hi, shift_low(d), a.s.lo);
   a.m = to;
 }
 
@@ -339,7 +357,7 @@ struct StatSlots {
 
 template <int THREADS, bool ENT>
 __device__ __forceinline__ void put_stat(const Running<ENT>& r, StatSlots<THREADS>& slots) {
-  slots.m[threadIdx.x] = r.m;
+  slots.m[threadIdx.x] = r.m();
   slots.s[threadIdx.x] = r.s;
   slots.lo[threadIdx.x] = r.lo;
   if (ENT) slots.t[threadIdx.x] = r.t;
@@ -367,7 +385,7 @@ __device__ __forceinline__ Stat warp_stat(const Scale& c, const StatSlots<THREAD
     const float d = ms[i] == v.m ? 0.f : fmaxf(scaled<ENT>(ms[i] - v.m, c), kMinExp);
     const float f = ex2(d), s = slots.s[lane + 32 * i] * f;
     f2_add(v.s, s);
-    v.s.lo += slots.lo[lane + 32 * i] * f + (d != 0.f ? s * kExLow : 0.f);
+    v.s.lo += slots.lo[lane + 32 * i] * f + (d != 0.f ? s * shift_low(d) : 0.f);
     if (ENT) f2_add(v.t, fmaf(d, s, slots.t[lane + 32 * i] * f));
   }
 #pragma unroll

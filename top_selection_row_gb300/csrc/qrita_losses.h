@@ -15,9 +15,10 @@ struct LossPair {
 };
 
 // c = log2(e) * inv_temperature (weights are 2^((x - m) c)) as hi + lo with
-// lo > 0, and to nearest, which is off by near_off of c.
+// lo > 0, and to nearest, which is off by near_off of c. Logits an octave
+// (1 / c) apart differ by a factor of 2 in weight.
 struct Scale {
-  float hi, lo, near, near_off;
+  float hi, lo, near, near_off, octave;
 };
 
 // Arguments of the loss kernels; null pointers are the optional arguments of

@@ -38,6 +38,7 @@ int loss_args(const void* logits, int dtype, int64_t B, int64_t V, int64_t ld, c
   out->mask = mask;
   out->tokens = tokens;
   out->c.near = near;
+  out->c.octave = static_cast<float>(1.0 / c);
   out->c.near_off = static_cast<float>(near / c - 1.0);
   out->c.hi = near < c ? near : std::nextafterf(near, 0.f);
   out->c.lo = static_cast<float>(c - out->c.hi);
