@@ -148,8 +148,10 @@ __device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
 // distance from the row's mean exponent (1.1e-6 at a distance of 20). Sums
 // without an entropy take c as hi + lo, rounded once (lo is above 0, so that a
 // difference of -inf stays -inf); with one, log S is put right by the mean
-// exponent that the entropy's sum gives (one more instruction a pair there: 91.1
-// us against 87.0 for 1024 x 262144 bf16).
+// exponent that the entropy's sum gives, and H is left off by c's error times the
+// variance of log p, as is usual for its temperature in fp32 (1.3e-8 of it at
+// temperature 1; hi + lo there would take 91.1 us against 87.0 for 1024 x 262144
+// bf16).
 template <bool ENT>
 __device__ __forceinline__ float scaled(float d, const Scale& c) {
   return ENT ? d * c.near : fmaf(d, c.hi, d * c.lo);
@@ -268,7 +270,10 @@ struct Running {
     // (the first time the sums are 0, or NaN, whatever the factor)
     const float d = fminf(fmaxf(scaled<ENT>(ref - x, c), kMinExp), 0.f);
     const float f = ex2(d);
-    if (ENT) t = (t + d * s) * f;
+    if (ENT) {
+      t = (t + d * s) * f;
+      t = fmaf(t, kExLow, t);
+    }
     s *= f;
     lo = fmaf(lo, f, s * kExLow);
     ref = x;
@@ -324,6 +329,7 @@ __device__ __forceinline__ void stat_shift(Stat& a, float to, const Scale& c) {
   if (ENT) {
     a.t = f2_merge(a.t, f2_prod(d, a.s.hi));
     a.t = f2_mul(a.t, f);
+    a.t.lo = fmaf(a.t.hi, shift_low(d), a.t.lo);
   }
   a.s = f2_mul(a.s, f);
   a.s.lo = fmaf(a.s.hi, shift_low(d), a.s.lo);
@@ -386,7 +392,11 @@ __device__ __forceinline__ Stat warp_stat(const Scale& c, const StatSlots<THREAD
     const float f = ex2(d), s = slots.s[lane + 32 * i] * f;
     f2_add(v.s, s);
     v.s.lo += slots.lo[lane + 32 * i] * f + (d != 0.f ? s * shift_low(d) : 0.f);
-    if (ENT) f2_add(v.t, fmaf(d, s, slots.t[lane + 32 * i] * f));
+    if (ENT) {
+      const float t = fmaf(d, s, slots.t[lane + 32 * i] * f);
+      f2_add(v.t, t);
+      v.t.lo += d != 0.f ? t * shift_low(d) : 0.f;
+    }
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
@@ -458,6 +468,16 @@ __device__ __forceinline__ F2 ln_pair(F2 s) {
   const float n = static_cast<float>(e);
   const float rest = logf(f) + fmaf(n, 1.42860682e-6f, s.lo / s.hi);  // ln2 - 0.693145752
   return f2_merge(f2_make(n * 0.693145752f, 0.f), f2_make(rest, 0.f));
+}
+
+// ln2 T / S as a pair. T's mean error is taken back here, as S's has been.
+__device__ __forceinline__ F2 mean_exponent(F2 s, F2 t) {
+  t.lo = fmaf(t.hi, kExLow, t.lo);
+  const float q = f2_float(t) / s.hi;
+  const float rest = (fmaf(-q, s.hi, t.hi) + fmaf(-q, s.lo, t.lo)) / s.hi;
+  F2 r = f2_mul(f2_make(q, rest), static_cast<float>(kLn2));
+  r.lo = fmaf(q, static_cast<float>(kLn2 - static_cast<float>(kLn2)), r.lo);
+  return r;
 }
 
 // a > b for pairs in normal form (infinities included).
@@ -535,15 +555,16 @@ template <bool ENT>
 __device__ __forceinline__ RowVals row_vals(const LossParams& p, const RowIn& in, const Stat& st) {
   RowVals v;
   const bool empty = st.s.hi == 0.f;  // nothing kept, or only -inf
-  const F2 ln_s = empty ? f2_make(0.f, 0.f) : ln_pair(f2_merge(st.s, f2_make((st.s.hi - 1.f) * kExLow, 0.f)));
+  const F2 S = f2_merge(st.s, f2_make((st.s.hi - 1.f) * kExLow, 0.f));
+  const F2 ln_s = empty ? f2_make(0.f, 0.f) : ln_pair(S);
   v.ln_s = ln_s.hi;
-  // of y_j ln2 under p
-  const float mean = ENT && !empty ? f2_float(st.t) / st.s.hi * static_cast<float>(kLn2) : 0.f;
+  // the mean of y_j ln2 under p
+  const F2 mean = ENT && !empty ? mean_exponent(S, st.t) : f2_make(0.f, 0.f);
   // (a token that is not kept has probability 0 unless the row's sums are NaN)
   v.logp = f2_make(st.s.hi == st.s.hi ? -INFINITY : st.s.hi, 0.f);
   if (in.kept_t && !empty) {
     // d ln S / d ln c is that mean: from c.near back to c
-    const F2 ln_sc = ENT ? f2_merge(ln_s, f2_make(-mean * p.c.near_off, 0.f)) : ln_s;
+    const F2 ln_sc = ENT ? f2_merge(ln_s, f2_make(-mean.hi * p.c.near_off, 0.f)) : ln_s;
     F2 d;
     two_sum(in.x_t, -st.m, d.hi, d.lo);
     if (fabsf(d.hi) < 1e30f) {
@@ -555,7 +576,7 @@ __device__ __forceinline__ RowVals row_vals(const LossParams& p, const RowIn& in
     }
   }
   v.lp = f2_float(v.logp);
-  v.H = ENT && !empty ? f2_float(f2_sub(ln_s, f2_make(mean, 0.f))) : 0.f;
+  v.H = ENT && !empty ? f2_float(f2_sub(ln_s, mean)) : 0.f;
   v.joins = v.lp != -INFINITY;  // (NaN joins)
   v.step = v.q = 0.f;
   v.over = v.bound = false;
