@@ -150,3 +150,36 @@ def check_entropies(x, inv_t=1.0, mask=None):
 def test_entropies(dev, dtype, B, V, scale, inv_t):
     _, x = logits(dev, V + B, B, V, dtype, scale)
     check_entropies(x, inv_t)
+
+
+@DTYPES
+@pytest.mark.parametrize("far", [-60.0, -7.0, 3.0, 23.0, 61.0, 79.0, 84.0])
+def test_ratios_and_kl_terms_far_from_one(dev, dtype, far):
+    """e^d of a d that fp32 holds to |d| 2^-24 only: the ratio, the KL term, their
+    sum and the gradient's entry of the token (p_t is near 0) see d as a pair. Off by
+    logp's own bound, an exponential's rounding of 2^-22 and a product's and the
+    output's 2^-23, relative to the terms."""
+    import torch
+
+    import top_selection_row_gb300 as q
+
+    B, V = 200, 5003
+    g, x = logits(dev, 71, B, V, "f32")
+    t = torch.randint(0, V, (B,), generator=g, device=dev, dtype=torch.int32)
+    x[torch.arange(B, device=dev), t.long()] = torch.linspace(-25, -22, B, device=dev)
+    x = x.to(torch.float32 if dtype == "f32" else torch.bfloat16)
+    want, _, E = exact(x, t, 1.0)
+    near = torch.from_numpy((want - far).astype(np.float32)).to(dev)
+    there = torch.from_numpy((want + far).astype(np.float32)).to(dev)
+    d, k = want - near.cpu().numpy().astype(np.float64), there.cpu().numpy().astype(np.float64) - want
+    one = torch.full((B,), -1.0, device=dev)
+    coef = float(np.float32(1e-3))
+    tol = bound(E) + 2.0 ** -21
+    got = q.qrita_policy_loss(x, t, near, one, ref_logp=there, clip_low=1.0, weights=-one, kl_coef=coef, out_grad=torch.empty_like(x))
+    rho, kl = np.exp(d), np.expm1(k) - k
+    assert (np.abs(got.kl.cpu().numpy() - kl) <= tol * (np.exp(k) + np.abs(k) + 1)).all()
+    row = rho + coef * kl
+    assert (np.abs(got.row_loss.cpu().numpy() - row) <= tol * (rho + coef * (np.exp(k) + np.abs(k) + 1))).all()
+    at = got.grad[torch.arange(B, device=dev), t.long()].double().cpu().numpy()
+    slope = (rho - coef * np.expm1(k)) * -np.expm1(want)
+    assert (np.abs(at - slope) <= tol * (rho + coef * (np.exp(k) + 1)) + (2.0 ** -8 * np.abs(slope) if dtype == "bf16" else 0)).all()

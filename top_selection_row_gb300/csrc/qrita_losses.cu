@@ -466,7 +466,7 @@ __device__ __forceinline__ F2 ln_pair(F2 s) {
     ++e;
   }
   const float n = static_cast<float>(e);
-  const float rest = logf(f) + fmaf(n, 1.42860682e-6f, s.lo / s.hi);  // ln2 - 0.693145752
+  const float rest = logf(f) + fmaf(n, 1.42860682e-6f, __fdividef(s.lo, s.hi));  // ln2 - 0.693145752
   return f2_merge(f2_make(n * 0.693145752f, 0.f), f2_make(rest, 0.f));
 }
 
@@ -474,7 +474,7 @@ __device__ __forceinline__ F2 ln_pair(F2 s) {
 __device__ __forceinline__ F2 mean_exponent(F2 s, F2 t) {
   t.lo = fmaf(t.hi, kExLow, t.lo);
   const float q = f2_float(t) / s.hi;
-  const float rest = (fmaf(-q, s.hi, t.hi) + fmaf(-q, s.lo, t.lo)) / s.hi;
+  const float rest = __fdividef(fmaf(-q, s.hi, t.hi) + fmaf(-q, s.lo, t.lo), s.hi);  // (of 2^-24 of q)
   F2 r = f2_mul(f2_make(q, rest), static_cast<float>(kLn2));
   r.lo = fmaf(q, static_cast<float>(kLn2 - static_cast<float>(kLn2)), r.lo);
   return r;
@@ -484,16 +484,6 @@ __device__ __forceinline__ F2 mean_exponent(F2 s, F2 t) {
 template <typename A, typename B>
 __device__ __forceinline__ bool pair_above(A a, B b) { return a.hi != b.hi ? a.hi > b.hi : a.lo > b.lo; }
 
-// e^q - 1 - q: its power series where the difference would lose digits (12
-// terms leave less than 2^-26 of it for |q| <= 1).
-__device__ __forceinline__ float exp_minus_tangent(float q) {
-  if (fabsf(q) > 1.f) return expm1f(q) - q;
-  float r = 1.f;
-#pragma unroll
-  for (int n = 13; n >= 3; --n) r = fmaf(r, q * (1.f / static_cast<float>(n)), 1.f);
-  return 0.5f * q * q * r;
-}
-
 // v e^d where e^d alone may leave fp32 (d above kFarExp): by two factors of
 // e^(d/2), which reach every product that fp32 holds of a normal v. 0 stays 0.
 constexpr float kFarExp = 80.f;
@@ -501,6 +491,24 @@ __device__ __forceinline__ float times_far_exp(float v, F2 d) {
   if (v == 0.f && d.hi < INFINITY) return 0.f;
   const float h = expf(0.5f * d.hi) * (1.f + 0.5f * d.lo);
   return v * h * h;
+}
+
+// e^d - 1 of a pair. (Below -kFarExp, as an infinity's, d's low part is nothing.)
+__device__ __forceinline__ float expm1_pair(F2 d) {
+  const float more = expm1f(d.hi);
+  return fabsf(d.hi) <= kFarExp ? fmaf(d.lo, more + 1.f, more) : more;
+}
+
+// e^q - 1 - q: its power series where the difference would lose digits (12
+// terms leave less than 2^-26 of it for |q| <= 1).
+__device__ __forceinline__ float exp_minus_tangent(F2 d) {
+  const float q = d.hi;
+  if (q > kFarExp) return times_far_exp(1.f, d);  // (1 + q is nothing beside it)
+  if (fabsf(q) > 1.f) return expm1_pair(d) - q;
+  float r = 1.f;
+#pragma unroll
+  for (int n = 13; n >= 3; --n) r = fmaf(r, q * (1.f / static_cast<float>(n)), 1.f);
+  return fmaf(0.5f * q * q, r, d.lo * q);  // (q for its slope e^q - 1: d.lo q^2 is nothing)
 }
 
 // A, Hc and the token's entry from the weights a, h of dlogp and dH.
@@ -543,7 +551,8 @@ __device__ __forceinline__ RowIn row_in(const LossParams& p, int op, int64_t row
 struct RowVals {
   F2 logp;
   float lp, H;      // as they are given out
-  float ln_s, step, q;      // step: -advantage * rho
+  float ln_s, step;         // step: -advantage * rho
+  F2 q;                     // reference less logp
   bool joins, over, bound;  // over, bound: rho above the clip; the clip binds
 };
 
@@ -578,7 +587,8 @@ __device__ __forceinline__ RowVals row_vals(const LossParams& p, const RowIn& in
   v.lp = f2_float(v.logp);
   v.H = ENT && !empty ? f2_float(f2_sub(ln_s, mean)) : 0.f;
   v.joins = v.lp != -INFINITY;  // (NaN joins)
-  v.step = v.q = 0.f;
+  v.step = 0.f;
+  v.q = f2_make(0.f, 0.f);
   v.over = v.bound = false;
   return v;
 }
@@ -600,8 +610,7 @@ __device__ __forceinline__ RowGrad row_weights(const LossParams& p, int op, cons
       v.step = times_far_exp(-in.adv, d);
       a = times_far_exp(-adv_w, d);
     } else {
-      float more = expm1f(d.hi);
-      if (d.hi > -kFarExp) more = fmaf(d.lo, more + 1.f, more);
+      const float more = expm1_pair(d);
       if (more > -0.5f) {
         v.step = fmaf(-in.adv, more, -in.adv);
         a = fmaf(-adv_w, more, -adv_w);
@@ -616,9 +625,9 @@ __device__ __forceinline__ RowGrad row_weights(const LossParams& p, int op, cons
     v.bound = (in.adv > 0.f && v.over) || (in.adv < 0.f && pair_above(p.ln_lo, d));
     if (v.bound) a = 0.f;
     if (p.ref_logp != nullptr) {
-      v.q = (in.ref_logp - v.logp.hi) - v.logp.lo;
+      v.q = isinf(in.ref_logp) ? f2_make(in.ref_logp, 0.f) : f2_sub(f2_make(in.ref_logp, 0.f), v.logp);
       const float kl_w = p.kl_coef * in.w;
-      if (p.kl_coef != 0.f) a = v.q > kFarExp ? a - times_far_exp(kl_w, f2_make(v.q, 0.f)) : fmaf(-kl_w, expm1f(v.q), a);
+      if (p.kl_coef != 0.f) a = v.q.hi > kFarExp ? a - times_far_exp(kl_w, v.q) : fmaf(-kl_w, expm1_pair(v.q), a);
     }
     if (v.lp != v.lp) a = v.lp;
     if (ENT) h = -p.entropy_coef * in.w;
@@ -639,7 +648,7 @@ __device__ __forceinline__ void row_out(const LossParams& p, int op, RowStat* st
       if (p.ref_logp != nullptr) {
         kl = exp_minus_tangent(v.q);
         if (p.kl_coef != 0.f)
-          loss = v.q > kFarExp ? loss + times_far_exp(p.kl_coef, f2_make(v.q, 0.f)) : fmaf(p.kl_coef, kl, loss);
+          loss = v.q.hi > kFarExp ? loss + times_far_exp(p.kl_coef, v.q) : fmaf(p.kl_coef, kl, loss);
       }
       if (ENT) loss = fmaf(-p.entropy_coef, v.H, loss);
     }
