@@ -183,3 +183,45 @@ def test_ratios_and_kl_terms_far_from_one(dev, dtype, far):
     at = got.grad[torch.arange(B, device=dev), t.long()].double().cpu().numpy()
     slope = (rho - coef * np.expm1(k)) * -np.expm1(want)
     assert (np.abs(at - slope) <= tol * (rho + coef * (np.exp(k) + 1)) + (2.0 ** -8 * np.abs(slope) if dtype == "bf16" else 0)).all()
+
+
+@pytest.mark.parametrize("z", [-80.0, -9.0, 0.5, 9.0, 30.0, 80.0])
+def test_slopes_of_distant_pairs(dev, z):
+    """Pairs far apart: the sigmoid's slope, of a z that fp32 holds to |z| 2^-24
+    only, in the gradient's entry of a token whose probability is near 0."""
+    import torch
+
+    import top_selection_row_gb300 as q
+
+    P, V = 64, 3001
+    g, x = logits(dev, 5, 2 * P, V, "f32")
+    t = torch.randint(0, V, (2 * P,), generator=g, device=dev, dtype=torch.int32)
+    x[torch.arange(2 * P, device=dev), t.long()] = -22.0
+    want, _, E = exact(x, t, 1.0)
+    ref = np.zeros(2 * P)
+    ref[0::2] = want[0::2] - want[1::2] - np.linspace(z, z * 1.01, P)
+    ref = torch.from_numpy(ref.astype(np.float32)).to(dev)
+    got = q.qrita_preference_loss(x, t, torch.arange(2 * P + 1, device=dev, dtype=torch.int32), ref_logp=ref, beta=1.0,
+                                  weights=torch.ones(P, device=dev))
+    r = ref.cpu().numpy().astype(np.float64)
+    zz = (want[0::2] - r[0::2]) - (want[1::2] - r[1::2])
+    slope = -1 / (1 + np.exp(zz)) * -np.expm1(want[0::2])
+    at = got.grad[torch.arange(0, 2 * P, 2, device=dev), t[0::2].long()].double().cpu().numpy()
+    assert (np.abs(at / slope - 1) <= 2 * bound(E).max() + 2.0 ** -21).all(), np.abs(at / slope - 1).max()
+
+
+def test_a_beta_beyond_fp32(dev):
+    """Slopes of pairs under a beta of 1e39: 0 where z saturates, beta's own value
+    times a small weight where it does not."""
+    import torch
+
+    import top_selection_row_gb300 as q
+
+    x = torch.zeros(4, 100, device=dev)
+    x[2, 5] = 3.0
+    t = torch.full((4,), 5, dtype=torch.int32, device=dev)
+    w = torch.tensor([1e-4, 1.0], device=dev)
+    got = q.qrita_preference_loss(x, t, torch.arange(5, device=dev, dtype=torch.int32), weights=w, beta=1e39)
+    assert abs(float(got.grad[0, 5]) / (-0.5 * 1e35 * 0.99) - 1) < 1e-5  # (z = 0)
+    assert abs(float(got.pair_loss[0]) - np.log(2)) < 1e-6 and float(got.pair_loss[1]) == 0
+    assert not got.grad[2:].any()

@@ -1468,7 +1468,10 @@ __global__ void __launch_bounds__(kSumThreads) weighted_sum_kernel(const float* 
 __device__ __forceinline__ float softplus(float hi, float lo) {
   return fmaxf(hi, 0.f) + (hi > 0.f ? lo : 0.f) + log1pf(expf(-fabsf(hi)) * (1.f - copysignf(1.f, hi) * lo));
 }
-__device__ __forceinline__ float sigmoid(float x) { return 1.f / (1.f + expf(-x)); }
+__device__ __forceinline__ float sigmoid(float hi, float lo) {
+  const float e = expf(-hi), r = 1.f / (1.f + e);
+  return e < INFINITY ? fmaf(lo * r, e * r, r) : expf(hi) * (1.f + lo);  // its slope is r (1 - r)
+}
 
 constexpr int kPairThreads = 256;
 
@@ -1542,11 +1545,11 @@ __global__ void __launch_bounds__(kPairThreads) pair_kernel(const LossParams p, 
     const double z = q.beta * ratio - q.margin;
     const float zh = static_cast<float>(z), zl = isfinite(zh) ? static_cast<float>(z - zh) : 0.f;
     const float ls = static_cast<float>(q.smoothing), keep = static_cast<float>(1.0 - q.smoothing);
-    float d = -keep * sigmoid(-zh);
-    if (ls != 0.f) d = fmaf(ls, sigmoid(zh), d);
-    d *= wt * static_cast<float>(q.beta);
-    slope[0] = d * scale[0];
-    slope[1] = -d * scale[1];
+    float d = -keep * sigmoid(-zh, -zl);
+    if (ls != 0.f) d = fmaf(ls, sigmoid(zh, zl), d);
+    const double by = wt * q.beta;  // (beta alone may be beyond fp32)
+    slope[0] = static_cast<float>(d * by * scale[0]);
+    slope[1] = static_cast<float>(-d * by * scale[1]);
     q.log_ratio[i] = static_cast<float>(ratio);
     float loss = keep != 0.f ? keep * softplus(-zh, -zl) : 0.f;
     if (ls != 0.f) loss = fmaf(ls, softplus(zh, zl), loss);
