@@ -186,3 +186,28 @@ def test_nan_or_infinity_beside_a_token_of_no_probability(dev, bad, dtype, V, ke
     rows = step.row_loss.cpu().numpy()
     assert np.isnan(rows[:3]).all() and np.isfinite(rows[3:]).all() and np.isnan(float(step.loss))
     near_grad(step.grad, dtype, soft, tokens, -a / 5, np.zeros(5), np.zeros(5), 1.0)
+
+
+@pytest.mark.parametrize("shape", [(6,), (3, 2), (1, 6), (6, 1)])
+def test_outputs_have_their_own_shape(dev, shape):
+    """[B], whatever the shape of the B values given."""
+    import torch
+
+    import top_selection_row_gb300 as q
+
+    rng, x, tokens, _ = make_rows(33, 6, 300, "f32")
+    v = put(dev, rng.standard_normal(6).astype(np.float32))
+    xd, td = put(dev, x), put(dev, tokens)
+    want = q.qrita_policy_loss(xd, td, v, v, ref_logp=v, weights=v, entropy=True)
+    w = v.view(shape)
+    got = q.qrita_policy_loss(xd, td.view(shape), w, w, ref_logp=w, weights=w, entropy=True)
+    for a, b in zip(got, want):
+        assert a.shape == b.shape and torch.equal(a, b)
+    assert [tuple(t.shape) for t in got] == [(), (6, 300), (6,), (6,), (6,), (6,)]
+    logp, ent = q.qrita_token_logprobs(xd, td.view(shape), entropy=True)
+    assert logp.shape == ent.shape == (6,)
+    starts = torch.arange(0, 7, 3, device=dev, dtype=torch.int32)
+    got = q.qrita_preference_loss(xd, td.view(shape), starts.view(3, 1), ref_logp=v[:2].view(1, 2), weights=v[:1].view(1, 1))
+    assert [tuple(t.shape) for t in got] == [(), (6, 300), (1,), (1,), (2,), (6,)]
+    one = q.qrita_policy_loss(xd[:1], td[0], v[0], v[0])  # (values without a dimension are B = 1)
+    assert [tuple(t.shape) for t in one[2:5]] == [(1,), (1,), (1,)]

@@ -519,10 +519,10 @@ def qrita_policy_loss(logits, tokens, old_logp, advantages, ref_logp=None, weigh
     if out is None:
         # (a tensor each: a view of a shared one takes longer to make and free)
         loss = torch.empty((), dtype=f32, device=dev)
-        row_loss = torch.empty_like(advantages)
-        logp = torch.empty_like(advantages)
-        kl = torch.empty_like(advantages)
-        ent = torch.empty_like(advantages) if want_ent else None
+        row_loss = torch.empty(B, dtype=f32, device=dev)
+        logp = torch.empty_like(row_loss)
+        kl = torch.empty_like(row_loss)
+        ent = torch.empty_like(row_loss) if want_ent else None
     else:
         loss, given, row_loss, logp, kl, ent = out
         _needed(loss, 1, f32, "out loss", dev)
