@@ -154,6 +154,15 @@ def _on_stream(stream, fn, *args):
     return got
 
 
+def _wrote(*tensors):
+    """Raises the versions of tensors that the caller gave and a call has written
+    through their addresses, as an in-place operation does: autograd then refuses
+    a backward pass that has saved one of them, instead of reading what is there
+    now."""
+    torch = _torch()
+    torch.autograd.graph.increment_version([t for t in tensors if t is not None and not t.is_inference()])
+
+
 def _stream_ptr(device):
     return ctypes.c_void_p(_torch().cuda.current_stream(device).cuda_stream)
 
@@ -186,6 +195,7 @@ def qrita_select_ex(logits, k=None, p=None, out=None, stream=None, flags=0,
     dt = _dtype_code(logits)
     kk = _vec(k, B, torch.int32, "k", dev)
     pp = _vec(p, B, torch.float32, "p", dev)
+    given = out
     if out is None:
         out = torch.empty((B, V), dtype=torch.bool, device=dev)
     elif out.shape != (B, V) or out.dtype not in (torch.bool, torch.uint8) or out.device != dev or not out.is_contiguous():
@@ -207,6 +217,8 @@ def qrita_select_ex(logits, k=None, p=None, out=None, stream=None, flags=0,
     )
     if rc != OK:
         raise QritaError(rc)
+    if given is not None:
+        _wrote(given)
     return out, st, info
 
 
@@ -231,6 +243,7 @@ def qrita_topk_ids(logits, k, kmax, out_mask=None, out_ids=None, stream=None):
     kk = _vec(k, B, torch.int32, "k", dev)
     if kk is None:
         raise ValueError("k is required")
+    given = out_ids, out_mask
     if out_mask is None:
         out_mask = torch.empty((B, V), dtype=torch.bool, device=dev)
     if out_ids is None:
@@ -243,6 +256,7 @@ def qrita_topk_ids(logits, k, kmax, out_mask=None, out_ids=None, stream=None):
         ctypes.c_void_p(out_ids.data_ptr() if B else 0), _stream_ptr(dev))
     if rc != OK:
         raise QritaError(rc)
+    _wrote(*given)
     return out_ids, out_mask
 
 
@@ -287,6 +301,8 @@ def qrita_candidates(logits, mask, cap, u=None, stream=None, out=None):
         ctypes.c_void_p(sample.data_ptr() if sample is not None else 0), _stream_ptr(dev))
     if rc != OK:
         raise QritaError(rc)
+    if out is not None:
+        _wrote(ids, probs, count, sample)
     return ids, probs, count, sample
 
 
@@ -327,6 +343,7 @@ def qrita_select_host(logits, k=None, p=None, out=None, staging=None, stream=Non
     cpu = torch.device("cpu")
     kk = _vec(k, B, torch.int32, "k", cpu)
     pp = _vec(p, B, torch.float32, "p", cpu)
+    given = out
     if out is None:
         out = torch.empty((B, V), dtype=torch.bool, pin_memory=logits.is_pinned())
     need = host_staging_bytes(dt, B, V)
@@ -349,6 +366,8 @@ def qrita_select_host(logits, k=None, p=None, out=None, staging=None, stream=Non
     )
     if rc != OK:
         raise QritaError(rc)
+    if given is not None:
+        _wrote(given)
     return out
 
 
@@ -455,7 +474,10 @@ def qrita_token_logprobs(logits, tokens, mask=None, inv_temperature=1.0, entropy
             _needed(ent, B, torch.float32, "out entropy", dev)
     _call(lib().qrita_token_logprobs, dev, logits.data_ptr(), dt, B, V, ld, keep, tok,
           inv_temperature, logp.data_ptr(), ent.data_ptr() if entropy else 0)
-    return logp, ent if entropy else None
+    ent = ent if entropy else None
+    if out is not None:
+        _wrote(logp, ent)
+    return logp, ent
 
 
 def qrita_token_logprobs_grad(logits, tokens, grad_logp=None, grad_entropy=None, mask=None, inv_temperature=1.0,
@@ -481,6 +503,8 @@ def qrita_token_logprobs_grad(logits, tokens, grad_logp=None, grad_entropy=None,
     grad, ldg = _grad_rows(out_grad, logits, B, V)
     _call(lib().qrita_token_logprobs_grad, dev, logits.data_ptr(), dt, B, V, ld, keep, tok, inv_temperature, gl, ge,
           grad.data_ptr(), ldg)
+    if out_grad is not None:
+        _wrote(grad)
     return grad
 
 
@@ -536,6 +560,10 @@ def qrita_policy_loss(logits, tokens, old_logp, advantages, ref_logp=None, weigh
           ref, adv, w, clip_low, clip_high, kl_coef, entropy_coef, gl, loss.data_ptr(),
           row_loss.data_ptr(), logp.data_ptr(), kl.data_ptr(), ent.data_ptr() if want_ent else 0,
           g.data_ptr() if grad else 0, ldg)
+    if out is not None:
+        _wrote(loss, row_loss, logp, kl, ent, g)
+    elif out_grad is not None:
+        _wrote(g)
     return PolicyLoss(loss, g, row_loss, logp, kl, ent)
 
 
@@ -600,4 +628,8 @@ def qrita_preference_loss(logits, tokens, starts, ref_logp=None, weights=None, i
           P, ref, w, beta, label_smoothing, margin, 1 if length_norm else 0, gl,
           loss.data_ptr(), pair_loss.data_ptr(), ratio.data_ptr(), seq.data_ptr(), logp.data_ptr(),
           g.data_ptr() if grad else 0, ldg, workspace.data_ptr(), workspace.numel())
+    if out is not None:
+        _wrote(loss, pair_loss, ratio, seq, logp, g)
+    elif out_grad is not None:
+        _wrote(g)
     return PreferenceLoss(loss, g, pair_loss, ratio, seq, logp)
