@@ -377,6 +377,20 @@ int qrita_policy_loss(const void* logits, int dtype, int64_t B, int64_t V, int64
                       float* out_logp, float* out_kl, float* out_entropy, void* out_grad, int64_t ld_grad,
                       qrita_stream_t stream);
 
+/* Flags of qrita_policy_loss_ex. Results do not depend on them. */
+#define QRITA_LOSS_FLAG_TEST_GIVE_BACK 0x1u /* tests only: CTAs that keep part of a row in
+                                               tensor memory give it back before their
+                                               cluster's sums are there, as they do when
+                                               those are late, and read that part again */
+
+/* qrita_policy_loss with flags (QRITA_EINVAL for unknown ones). */
+int qrita_policy_loss_ex(const void* logits, int dtype, int64_t B, int64_t V, int64_t ld, const uint8_t* mask,
+                         const int32_t* tokens, double inv_temperature, const float* old_logp, const float* ref_logp,
+                         const float* advantages, const float* weights, double clip_low, double clip_high,
+                         double kl_coef, double entropy_coef, const float* grad_loss, float* out_loss,
+                         float* out_row_loss, float* out_logp, float* out_kl, float* out_entropy, void* out_grad,
+                         int64_t ld_grad, uint32_t flags, qrita_stream_t stream);
+
 /*
  * qrita_preference_workspace_bytes: device bytes of workspace
  * qrita_preference_loss needs for B rows and P pairs (a multiple of 256; the

@@ -1,0 +1,26 @@
+"""qrita_policy_loss_ex: the same refusals as without flags, and unknown flags (no
+GPU here; pointers are never dereferenced)."""
+
+import ctypes
+
+import pytest
+
+from test_abi_losses import BAD_ROWS, EINVAL, F, GRAD, L, NULL, ROWS, _rows  # noqa: F401
+
+
+def policy_ex(L, flags=0, **kw):
+    a = {**ROWS, **GRAD, "adv": F, "loss": F, "row_loss": F, **kw}
+    return L.qrita_policy_loss_ex(*_rows(a), NULL, NULL, a["adv"], NULL, 0.2, 0.2, 0.0, 0.0, NULL, a["loss"], a["row_loss"],
+                                  NULL, NULL, NULL, a["out_grad"], a["ld_grad"], ctypes.c_uint32(flags), NULL)
+
+
+@pytest.mark.parametrize("bad", BAD_ROWS + [dict(adv=NULL), dict(loss=NULL), dict(row_loss=NULL), dict(ld_grad=99)],
+                         ids=lambda b: " ".join(f"{k}={v}" for k, v in b.items()))
+@pytest.mark.parametrize("flags", [0, 1])
+def test_bad_arguments(L, bad, flags):
+    assert policy_ex(L, flags, **bad) == EINVAL
+
+
+@pytest.mark.parametrize("flags", [2, 3, 0x1000, 0x80000000])
+def test_unknown_flags(L, flags):
+    assert policy_ex(L, flags) == EINVAL

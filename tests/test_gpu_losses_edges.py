@@ -211,3 +211,58 @@ def test_outputs_have_their_own_shape(dev, shape):
     assert [tuple(t.shape) for t in got] == [(), (6, 300), (1,), (1,), (2,), (6,)]
     one = q.qrita_policy_loss(xd[:1], td[0], v[0], v[0])  # (values without a dimension are B = 1)
     assert [tuple(t.shape) for t in one[2:5]] == [(1,), (1,), (1,)]
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("ent", [0.0, 0.05])
+@pytest.mark.parametrize("B,V,ld", [(64, 200000, 200000), (150, 262144, 262144), (40, 262141, 262149), (20, 1000, 1000)])
+def test_tensor_memory_given_back_early(dev, dtype, ent, B, V, ld):
+    """A CTA whose cluster's sums are late gives its tensor memory back and reads
+    that part of its row again for the gradient: the same bits, beside the logits,
+    over them, and while another call does the same on another stream. (Rows of one
+    CTA, and of shares that shared memory holds, have nothing to give back.)"""
+    import torch
+
+    import top_selection_row_gb300 as q
+
+    if dtype == "f32":
+        V, ld = V // 2, ld // 2 + 1
+    g = torch.Generator(device=dev).manual_seed(B)
+    dt = torch.float32 if dtype == "f32" else torch.bfloat16
+    wide = torch.randn(B, ld, generator=g, device=dev).to(dt)
+    x = wide[:, :V]
+    t = torch.randint(0, V, (B,), generator=g, device=dev, dtype=torch.int32)
+    t[3] = -1
+    adv = torch.randn(B, generator=g, device=dev)
+    flag = dict(flags=q.LOSS_FLAG_TEST_GIVE_BACK)
+
+    def call(v, **k):
+        return q.qrita_policy_loss(v, t, None, adv, entropy_coef=ent, entropy=True, **k)
+
+    want = call(x)
+    got = call(x, **flag)
+    assert all(torch.equal(u, v) for u, v in zip(got, want))
+    over = wide.clone()
+    got = call(over[:, :V], out_grad=over[:, :V], **flag)
+    assert torch.equal(over[:, :V], want.grad) and torch.equal(over[:, V:], wide[:, V:]) and torch.equal(got.loss, want.loss)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    for _ in range(3):
+        here, there = call(x, **flag), call(x, stream=side, **flag)
+        also = call(x)
+        torch.cuda.synchronize()
+        for got in (here, there, also):
+            assert torch.equal(got.grad, want.grad) and torch.equal(got.loss, want.loss)
+    soft = softmaxes(x[:2].float().cpu().numpy(), "f32", None, t[:2].cpu().numpy())
+    near_grad(got.grad[:2], dtype, soft, t[:2].cpu().numpy(), -adv[:2].cpu().numpy() / B, np.full(2, -ent / B), np.zeros(2), 1.0)
+
+
+def test_unknown_flags_are_refused(dev):
+    import torch
+
+    import top_selection_row_gb300 as q
+
+    x, t, f = torch.zeros(3, 10, device=dev), torch.zeros(3, dtype=torch.int32, device=dev), torch.zeros(3, device=dev)
+    with pytest.raises(q.QritaError) as err:
+        q.qrita_policy_loss(x, t, f, f, flags=2)
+    assert err.value.code == q.EINVAL

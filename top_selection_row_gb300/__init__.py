@@ -30,6 +30,7 @@ FLAG_TEST_GIVE_UP = 0x1000
 FLAG_NO_KEY_HIST = 0x2000
 FLAG_SEARCH_QUATERNARY = 0x4000
 FLAG_SEARCH_BINARY = 0x8000
+LOSS_FLAG_TEST_GIVE_BACK = 0x1
 
 
 def flag_cluster(n_ctas: int) -> int:
@@ -510,7 +511,7 @@ def qrita_token_logprobs_grad(logits, tokens, grad_logp=None, grad_entropy=None,
 
 def qrita_policy_loss(logits, tokens, old_logp, advantages, ref_logp=None, weights=None, mask=None, inv_temperature=1.0,
                       clip_low=0.2, clip_high=0.2, kl_coef=0.0, entropy_coef=0.0, grad_loss=None, grad=True,
-                      entropy=False, out_grad=None, stream=None, out=None):
+                      entropy=False, out_grad=None, stream=None, out=None, flags=0):
     """The clipped policy loss with a KL term over rows of logits, and its
     gradient with respect to them, in one call.
 
@@ -521,12 +522,12 @@ def qrita_policy_loss(logits, tokens, old_logp, advantages, ref_logp=None, weigh
     gradient out; entropy=True returns the entropies even where entropy_coef
     is 0. Returns PolicyLoss(loss [], grad [B, V] or None, row_loss [B],
     logp [B], kl [B], entropy [B] or None); ``out`` = such a tuple, as an
-    earlier call returned it, reuses its tensors.
+    earlier call returned it, reuses its tensors. flags: qrita_policy_loss_ex's.
     """
     if stream is not None:
         return _on_stream(stream, qrita_policy_loss, logits, tokens, old_logp, advantages, ref_logp, weights, mask,
                           inv_temperature, clip_low, clip_high, kl_coef, entropy_coef, grad_loss, grad, entropy,
-                          out_grad, None, out)
+                          out_grad, None, out, flags)
     torch = _torch()
     B, V, ld = _padded_rows(logits)
     dev = logits.device
@@ -556,10 +557,11 @@ def qrita_policy_loss(logits, tokens, old_logp, advantages, ref_logp=None, weigh
         out_grad = given if out_grad is None else out_grad
         ent = ent if want_ent else None
     g, ldg = _grad_rows(out_grad, logits, B, V) if grad else (None, 0)
-    _call(lib().qrita_policy_loss, dev, logits.data_ptr(), dt, B, V, ld, keep, tok, inv_temperature, old,
+    fn, more = (lib().qrita_policy_loss, ()) if flags == 0 else (lib().qrita_policy_loss_ex, (flags,))
+    _call(fn, dev, logits.data_ptr(), dt, B, V, ld, keep, tok, inv_temperature, old,
           ref, adv, w, clip_low, clip_high, kl_coef, entropy_coef, gl, loss.data_ptr(),
           row_loss.data_ptr(), logp.data_ptr(), kl.data_ptr(), ent.data_ptr() if want_ent else 0,
-          g.data_ptr() if grad else 0, ldg)
+          g.data_ptr() if grad else 0, ldg, *more)
     if out is not None:
         _wrote(loss, row_loss, logp, kl, ent, g)
     elif out_grad is not None:

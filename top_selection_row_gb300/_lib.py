@@ -22,6 +22,7 @@ EXPORTED = (
     "qrita_token_logprobs",
     "qrita_token_logprobs_grad",
     "qrita_policy_loss",
+    "qrita_policy_loss_ex",
     "qrita_preference_workspace_bytes",
     "qrita_preference_loss",
     "qrita_delta_table",
@@ -63,6 +64,8 @@ def lib() -> ctypes.CDLL:
     L.qrita_policy_loss.argtypes = [vp, i32, i64, i64, i64, vp, vp, f64, vp, vp, vp, vp, f64, f64, f64, f64, vp, vp, vp,
                                     vp, vp, vp, vp, i64, vp]
     L.qrita_policy_loss.restype = i32
+    L.qrita_policy_loss_ex.argtypes = [*L.qrita_policy_loss.argtypes[:-1], u32, vp]
+    L.qrita_policy_loss_ex.restype = i32
     L.qrita_preference_workspace_bytes.argtypes = [i64, i64]
     L.qrita_preference_workspace_bytes.restype = sz
     L.qrita_preference_loss.argtypes = [vp, i32, i64, i64, i64, vp, f64, vp, i64, vp, vp, f64, f64, f64, i32, vp, vp, vp,

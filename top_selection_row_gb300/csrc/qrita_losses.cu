@@ -1329,7 +1329,8 @@ __global__ void __launch_bounds__(kResThreads, kResBlocks) resident_kernel(const
       if (MOVED && tid < C) arrive_remote(map_rank(smem_u32(&sent), tid));
     }
     cluster_arrive();
-    if (MOVED && warp == 1 && !__all_sync(kAll, mbar_wait_bounded(smem_u32(&sent), 0, kHoldLimitNs))) {
+    if (MOVED && warp == 1 &&
+        (p.give_back || !__all_sync(kAll, mbar_wait_bounded(smem_u32(&sent), 0, kHoldLimitNs)))) {
       given_up = true;  // (read after a barrier)
       tmem_free(tmem_at, kTmemColumns);
     }

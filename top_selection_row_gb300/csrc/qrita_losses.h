@@ -53,6 +53,7 @@ struct LossParams {
   LossPair ln_lo, ln_hi;   // their logarithms as pairs (-inf, inf: no clip)
   float kl_coef, entropy_coef;
   float* loss;
+  bool give_back;  // tensor memory, without waiting for the cluster (tests)
 };
 
 struct PrefParams {

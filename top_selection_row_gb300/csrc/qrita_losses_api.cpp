@@ -108,6 +108,18 @@ int qrita_policy_loss(const void* logits, int dtype, int64_t B, int64_t V, int64
                       double entropy_coef, const float* grad_loss, float* out_loss, float* out_row_loss,
                       float* out_logp, float* out_kl, float* out_entropy, void* out_grad, int64_t ld_grad,
                       qrita_stream_t stream) {
+  return qrita_policy_loss_ex(logits, dtype, B, V, ld, mask, tokens, inv_temperature, old_logp, ref_logp, advantages,
+                              weights, clip_low, clip_high, kl_coef, entropy_coef, grad_loss, out_loss, out_row_loss,
+                              out_logp, out_kl, out_entropy, out_grad, ld_grad, 0u, stream);
+}
+
+int qrita_policy_loss_ex(const void* logits, int dtype, int64_t B, int64_t V, int64_t ld, const uint8_t* mask,
+                         const int32_t* tokens, double inv_temperature, const float* old_logp, const float* ref_logp,
+                         const float* advantages, const float* weights, double clip_low, double clip_high,
+                         double kl_coef, double entropy_coef, const float* grad_loss, float* out_loss,
+                         float* out_row_loss, float* out_logp, float* out_kl, float* out_entropy, void* out_grad,
+                         int64_t ld_grad, uint32_t flags, qrita_stream_t stream) {
+  if ((flags & ~QRITA_LOSS_FLAG_TEST_GIVE_BACK) != 0u) return QRITA_EINVAL;
   qrita::LossParams prm;
   const int rc = qrita::loss_args(logits, dtype, B, V, ld, mask, tokens, inv_temperature, out_grad, ld_grad, &prm);
   if (rc != QRITA_OK) return rc;
@@ -133,6 +145,7 @@ int qrita_policy_loss(const void* logits, int dtype, int64_t B, int64_t V, int64
   prm.logp = out_logp;
   prm.kl = out_kl;
   prm.entropy = out_entropy;
+  prm.give_back = (flags & QRITA_LOSS_FLAG_TEST_GIVE_BACK) != 0u;
   return qrita::launch_policy(prm, dtype, stream) == 0 ? QRITA_OK : QRITA_ECUDA;
 }
 
