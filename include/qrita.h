@@ -304,7 +304,7 @@ int qrita_candidates(const void* logits, int dtype, int64_t B, int64_t V, const 
  *   ld                    leading dimension of logits, >= V.
  *   mask                  uint8[B, V] (leading dimension V) or NULL.
  *   tokens                int32[B].
- *   inv_temperature       finite, > 0 (by value).
+ *   inv_temperature       from 1e-30 to 1e30 (by value).
  * Ownership, streams and errors as qrita_select; QRITA_EINVAL also for a
  * leading dimension below V, a scalar outside its stated range, or a missing
  * pointer that is not said to be optional. Nothing is allocated or kept.

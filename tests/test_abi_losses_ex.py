@@ -24,3 +24,9 @@ def test_bad_arguments(L, bad, flags):
 @pytest.mark.parametrize("flags", [2, 3, 0x1000, 0x80000000])
 def test_unknown_flags(L, flags):
     assert policy_ex(L, flags) == EINVAL
+
+
+@pytest.mark.parametrize("inv_t", [9e-31, 1.1e30, 1e-38, 1e38])
+def test_temperatures_outside_the_stated_range(L, inv_t):
+    assert policy_ex(L, inv_t=inv_t) == EINVAL
+    assert L.qrita_token_logprobs(*_rows({**ROWS, "inv_t": inv_t}), F, NULL, NULL) == EINVAL

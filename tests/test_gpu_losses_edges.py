@@ -266,3 +266,34 @@ def test_unknown_flags_are_refused(dev):
     with pytest.raises(q.QritaError) as err:
         q.qrita_policy_loss(x, t, f, f, flags=2)
     assert err.value.code == q.EINVAL
+
+
+@pytest.mark.parametrize("inv_t", [1e-30, 1e-10, 1e4, 1e10, 1e30])
+@pytest.mark.parametrize("dtype,V", [("f32", 300), ("bf16", 300), ("f32", 40000)])
+def test_extreme_temperatures(dev, dtype, V, inv_t):
+    """Weights all equal, or one token's alone, over rows with masked places of
+    -1e9, -1e29 and -inf among them; tokens on such places too."""
+    import top_selection_row_gb300 as q
+
+    rng = np.random.default_rng(3)
+    x = rng.standard_normal((6, V)).astype(np.float32)
+    for r, low in ((1, -1e9), (2, -1e29), (3, -np.inf), (4, -1e9), (5, -1e29)):
+        x[r, 50:] = low
+    tokens = np.array([3, 2, 1, 4, 70, 80], np.int32)
+    if dtype == "bf16":
+        from workloads import f32_to_bf16_bits
+
+        x = f32_to_bf16_bits(x)
+    soft = softmaxes(x, dtype, None, tokens, inv_t)
+    xd, td = to_device(x, dtype, dev), put(dev, tokens)
+    with np.errstate(over="ignore"):
+        want = np.array([s.logp for s in soft]).astype(np.float32)
+    for ent in (False, True):
+        logp, H = q.qrita_token_logprobs(xd, td, inv_temperature=inv_t, entropy=ent)
+        near_rows(logp.cpu().numpy(), want, "logp")
+    near_rows(H.cpu().numpy(), [s.entropy for s in soft], "entropy", extra=ABS)
+    a = rng.standard_normal(6).astype(np.float32) * np.float32(1e-2)
+    got = q.qrita_token_logprobs_grad(xd, td, put(dev, a), inv_temperature=inv_t)
+    keep = [0, 1, 2, 3]  # (a logp beyond fp32 is -inf, and its row then has no gradient)
+    near_grad(got[keep], dtype, [soft[r] for r in keep], tokens[keep], a[keep], np.zeros(4), np.zeros(4), inv_t)
+    assert np.isfinite(got.float().cpu().numpy()).all()

@@ -576,7 +576,7 @@ __device__ __forceinline__ RowVals row_vals(const LossParams& p, const RowIn& in
     const F2 ln_sc = ENT ? f2_merge(ln_s, f2_make(-mean.hi * p.c.near_off, 0.f)) : ln_s;
     F2 d;
     two_sum(in.x_t, -st.m, d.hi, d.lo);
-    if (fabsf(d.hi) < 1e30f) {
+    if (fabsf(d.hi) < 1e30f && fabsf(d.hi * p.inv_t) < 1e30f) {
       F2 y = f2_mul(d, p.inv_t);  // (x_t - m) inv_t
       y.lo = fmaf(d.hi, p.inv_t_lo, y.lo);
       v.logp = f2_sub(y, ln_sc);
