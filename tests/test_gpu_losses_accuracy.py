@@ -225,3 +225,60 @@ def test_a_beta_beyond_fp32(dev):
     assert abs(float(got.grad[0, 5]) / (-0.5 * 1e35 * 0.99) - 1) < 1e-5  # (z = 0)
     assert abs(float(got.pair_loss[0]) - np.log(2)) < 1e-6 and float(got.pair_loss[1]) == 0
     assert not got.grad[2:].any()
+
+
+@DTYPES
+@pytest.mark.parametrize("B,V", [(700, 128256), (64, 262144), (1000, 3001), (16, 32000)])
+def test_ordinary_tokens(dev, dtype, B, V):
+    import torch
+
+    g, x = logits(dev, V + 1, B, V, dtype)
+    noise = torch.rand(B, V, generator=g, device=dev).clamp_(min=1e-30).log_().neg_().log_().neg_()
+    check(x, (x.float() + noise).argmax(dim=1).int(), 1.0 if V % 2 else 0.75)
+
+
+@DTYPES
+@pytest.mark.parametrize("lead", [10.0, 14.0])
+@pytest.mark.parametrize("B,V", [(700, 128256), (100, 50021)])
+def test_a_token_that_outweighs_its_row(dev, dtype, lead, B, V):
+    """Most of a row's weight in one token (p from 0.15 to 0.9): every other group
+    of its thread's share is added to a sum near that token's weight."""
+    import torch
+
+    g, x = logits(dev, V + 2, B, V, "f32", 0.5)
+    t = torch.randint(0, V, (B,), generator=g, device=dev, dtype=torch.int32)
+    x = torch.randn(B, V, generator=g, device=dev) * 0.5
+    x[torch.arange(B, device=dev), t.long()] = lead
+    check(x.to(torch.float32 if dtype == "f32" else torch.bfloat16), t)
+
+
+@DTYPES
+def test_rows_of_few_values(dev, dtype):
+    """Uniform rows, and one token above rows of one other value: every weight has
+    the same error, so only the bound holds of these."""
+    import torch
+
+    import top_selection_row_gb300 as q
+
+    B, V = 64, 50021
+    x = torch.full((B, V), 3.0, device=dev)
+    t = torch.arange(B, device=dev, dtype=torch.int32) * 700
+    x[torch.arange(B, device=dev), t.long()] += torch.arange(B, device=dev) * 0.25
+    x = x.to(torch.float32 if dtype == "f32" else torch.bfloat16)
+    want, _, E = exact(x, t, 1.0)
+    for ent in (False, True):
+        got = q.qrita_token_logprobs(x, t, entropy=ent)[0].cpu().numpy().astype(np.float64)
+        assert (np.abs(got - want) <= bound(E) + HALF * np.abs(want) * 1.01).all()
+
+
+@DTYPES
+@pytest.mark.parametrize("B,V,density", [(128, 50021, 0.001), (128, 50021, 0.5), (500, 30000, 0.03), (24, 262144, 0.3)])
+def test_kept_sets(dev, dtype, B, V, density):
+    import torch
+
+    g, x = logits(dev, V + 3, B, V, dtype)
+    mask = torch.rand(B, V, generator=g, device=dev) < density
+    t = torch.where(mask, torch.rand(B, V, generator=g, device=dev), -1.0).argmax(dim=1)
+    for inv_t in (1.0, 1.4375):
+        check(x, t.int(), inv_t, mask)
+    check_entropies(x, 1.0, mask)

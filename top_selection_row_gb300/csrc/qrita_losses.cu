@@ -320,19 +320,26 @@ struct Running {
   }
 };
 
-// Sums relative to m raised to `to` (>= m).
+// Sums relative to m raised to `to` (>= m). One factor here holds a CTA's whole
+// share of a row, so what its exponent loses to rounding (2^-25 of it and of the
+// difference) is put back: with one token far above the rest, logp of 400 x 50021
+// fp32 in shares of a sixth is off by 1.0e-7 root mean square without.
 template <bool ENT>
 __device__ __forceinline__ void stat_shift(Stat& a, float to, const Scale& c) {
   if (a.m == to) return;
-  const float d = fmaxf(scaled<ENT>(a.m - to, c), kMinExp);
-  const float f = ex2(d);
+  float dh, dl;
+  two_sum(a.m, -to, dh, dl);
+  const float by = ENT ? c.near : c.hi;
+  const float y = dh * by, d = fmaxf(y, kMinExp);
+  const float lost = y > kMinExp ? fmaf(dh, by, -y) + fmaf(dl, by, ENT ? 0.f : dh * c.lo) : 0.f;
+  const float f = ex2(d), more = fmaf(lost, static_cast<float>(kLn2), shift_low(d));
   if (ENT) {
     a.t = f2_merge(a.t, f2_prod(d, a.s.hi));
     a.t = f2_mul(a.t, f);
-    a.t.lo = fmaf(a.t.hi, shift_low(d), a.t.lo);
+    a.t.lo = fmaf(a.t.hi, more, a.t.lo);
   }
   a.s = f2_mul(a.s, f);
-  a.s.lo = fmaf(a.s.hi, shift_low(d), a.s.lo);
+  a.s.lo = fmaf(a.s.hi, more, a.s.lo);
   a.m = to;
 }
 
