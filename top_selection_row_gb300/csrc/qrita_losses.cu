@@ -1555,9 +1555,9 @@ __global__ void __launch_bounds__(kPairThreads) pair_kernel(const LossParams p, 
     const float ls = static_cast<float>(q.smoothing), keep = static_cast<float>(1.0 - q.smoothing);
     float d = -keep * sigmoid(-zh, -zl);
     if (ls != 0.f) d = fmaf(ls, sigmoid(zh, zl), d);
-    const double by = wt * q.beta;  // (beta alone may be beyond fp32)
-    slope[0] = static_cast<float>(d * by * scale[0]);
-    slope[1] = static_cast<float>(-d * by * scale[1]);
+    d = d * wt * q.beta_parts[0] * q.beta_parts[1];
+    slope[0] = d * scale[0];
+    slope[1] = -d * scale[1];
     q.log_ratio[i] = static_cast<float>(ratio);
     float loss = keep != 0.f ? keep * softplus(-zh, -zl) : 0.f;
     if (ls != 0.f) loss = fmaf(ls, softplus(zh, zl), loss);

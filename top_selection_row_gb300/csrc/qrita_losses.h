@@ -62,6 +62,7 @@ struct PrefParams {
   const float* ref;
   const float* weights;
   double beta, smoothing, margin;
+  float beta_parts[2];  // their product is beta, also beyond fp32 (up to 2^253)
   int length_norm;
   float inv_p;  // 1 / P
   float* pair_loss;

@@ -181,6 +181,8 @@ int qrita_preference_loss(const void* logits, int dtype, int64_t B, int64_t V, i
   pref.ref = ref_logp;
   pref.weights = weights;
   pref.beta = beta;
+  pref.beta_parts[1] = beta > 0x1p126 ? 0x1p126f : 1.f;
+  pref.beta_parts[0] = static_cast<float>(std::fmin(beta / pref.beta_parts[1], 0x1p127));
   pref.smoothing = label_smoothing;
   pref.margin = margin;
   pref.length_norm = length_norm;
