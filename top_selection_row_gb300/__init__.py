@@ -142,15 +142,26 @@ def _on_stream(stream, fn, *args):
     used on the caller's, so that neither's memory is handed out again before
     that stream is done with it."""
     torch = _torch()
-    if any(t.device != stream.device for t in _tensors(args)):
-        raise ValueError(f"stream must be one of the tensors' device, not of {stream.device}")
-    caller = torch.cuda.current_stream(stream.device)
-    with torch.cuda.stream(stream):
-        got = fn(*args)
-    if stream != caller:
-        for t in _tensors(args):
-            t.record_stream(stream)
-        for t in _tensors((got,)):
+    dev = stream.device
+    if args[0].is_cuda and args[0].device != dev:
+        raise ValueError(f"stream must be one of the logits' device, not of {dev}")
+    if stream.cuda_stream == torch._C._cuda_getCurrentRawStream(dev.index):
+        return fn(*args)
+    caller = torch.cuda.current_stream(dev)
+    if torch.cuda.current_device() == dev.index:
+        torch.cuda.set_stream(stream)  # (as the context below, some 6 us sooner)
+        try:
+            got = fn(*args)
+        finally:
+            torch.cuda.set_stream(caller)
+    else:
+        with torch.cuda.stream(stream):
+            got = fn(*args)
+    given = list(_tensors(args))
+    for t in given:
+        t.record_stream(stream)
+    for t in _tensors((got,)):
+        if not any(t is g for g in given):
             t.record_stream(caller)
     return got
 
@@ -165,7 +176,7 @@ def _wrote(*tensors):
 
 
 def _stream_ptr(device):
-    return ctypes.c_void_p(_torch().cuda.current_stream(device).cuda_stream)
+    return ctypes.c_void_p(_torch()._C._cuda_getCurrentRawStream(device.index))
 
 
 def qrita_select(logits, k=None, p=None, out=None, stream=None):
