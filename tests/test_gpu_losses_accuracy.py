@@ -282,3 +282,37 @@ def test_kept_sets(dev, dtype, B, V, density):
     for inv_t in (1.0, 1.4375):
         check(x, t.int(), inv_t, mask)
     check_entropies(x, 1.0, mask)
+
+
+@pytest.mark.parametrize("ref", [False, True])
+@pytest.mark.parametrize("ent", [0.0, 0.01])
+def test_row_losses_are_rounded_once(dev, ref, ent):
+    """Rows of one token (logp is exactly 0): a row's loss is within half a step of
+    the formula's, an exponential's error (a step of e^d - 1) and the KL term's
+    three roundings apart."""
+    import torch
+
+    import top_selection_row_gb300 as q
+
+    B = 5000
+    g = torch.Generator(device=dev).manual_seed(9)
+    adv = torch.randn(B, generator=g, device=dev)
+    old = torch.randn(B, generator=g, device=dev) * 0.3
+    there = torch.randn(B, generator=g, device=dev) * 0.5 if ref else None
+    got = q.qrita_policy_loss(torch.zeros(B, 1, device=dev), torch.zeros(B, dtype=torch.int32, device=dev), old, adv, ref_logp=there,
+                              clip_low=0.2, clip_high=0.28, kl_coef=0.05, entropy_coef=ent, grad=False)
+    a, d = adv.double().cpu().numpy(), -old.double().cpu().numpy()
+    rho = np.exp(d)
+    surrogate = np.maximum(-a * rho, -a * np.clip(rho, 1 - 0.2, 1 + 0.28))
+    kl = 0.0
+    if ref:
+        k = there.double().cpu().numpy()
+        kl = 0.05 * (np.expm1(k) - k)
+    row = surrogate + kl
+    err = np.abs(got.row_loss.double().cpu().numpy() - row)
+    edge = np.minimum(np.abs(rho - 0.8), np.abs(rho - 1.28)) < 1e-6
+    tol = HALF * np.abs(row) * 1.01 + 2.0 ** -23 * np.abs(a) * np.abs(np.expm1(d)) + 3 * 2.0 ** -23 * np.abs(kl)
+    # (below rho = 1/2 the exponential itself is taken, off by two steps)
+    tol = tol + np.where(rho < 0.51, 2.0 ** -22 * np.abs(a) * rho, 0.0)
+    assert (err <= tol)[~edge].all(), ((err - tol)[~edge].max(), np.argmax(np.where(edge, 0, err - tol)))
+    assert abs(float(got.loss) - row.mean()) <= HALF * (abs(row.mean()) + np.abs(row).mean())

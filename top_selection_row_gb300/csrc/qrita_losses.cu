@@ -558,7 +558,8 @@ __device__ __forceinline__ RowIn row_in(const LossParams& p, int op, int64_t row
 struct RowVals {
   F2 logp;
   float lp, H;      // as they are given out
-  float ln_s, step;         // step: -advantage * rho
+  float ln_s;
+  F2 step;                  // -advantage * rho
   F2 q;                     // reference less logp
   bool joins, over, bound;  // over, bound: rho above the clip; the clip binds
 };
@@ -594,8 +595,7 @@ __device__ __forceinline__ RowVals row_vals(const LossParams& p, const RowIn& in
   v.lp = f2_float(v.logp);
   v.H = ENT && !empty ? f2_float(f2_sub(ln_s, mean)) : 0.f;
   v.joins = v.lp != -INFINITY;  // (NaN joins)
-  v.step = 0.f;
-  v.q = f2_make(0.f, 0.f);
+  v.step = v.q = f2_make(0.f, 0.f);
   v.over = v.bound = false;
   return v;
 }
@@ -614,16 +614,17 @@ __device__ __forceinline__ RowGrad row_weights(const LossParams& p, int op, cons
     // rho = 1 + (e^d - 1): near 1 one rounding of the product is what it costs
     const float adv_w = in.adv * in.w;
     if (d.hi > kFarExp) {
-      v.step = times_far_exp(-in.adv, d);
+      v.step.hi = times_far_exp(-in.adv, d);
       a = times_far_exp(-adv_w, d);
     } else {
       const float more = expm1_pair(d);
       if (more > -0.5f) {
-        v.step = fmaf(-in.adv, more, -in.adv);
+        v.step = f2_prod(-in.adv, more);
+        f2_add(v.step, -in.adv);
         a = fmaf(-adv_w, more, -adv_w);
       } else {
         const float rho = expf(d.hi) * (1.f + d.lo);
-        v.step = -in.adv * rho;
+        v.step.hi = -in.adv * rho;
         a = -adv_w * rho;
       }
     }
@@ -651,13 +652,15 @@ __device__ __forceinline__ void row_out(const LossParams& p, int op, RowStat* st
   if (op == kOpPolicy) {
     float loss = 0.f, kl = 0.f;
     if (v.joins) {
-      loss = v.lp != v.lp ? v.lp : v.bound ? -in.adv * (v.over ? p.clip_hi : p.clip_lo) : v.step;
+      const LossPair clip = v.over ? p.clip_hi : p.clip_lo;
+      F2 term = v.bound ? f2_mul(f2_make(clip.hi, clip.lo), -in.adv) : v.step;  // rounded once, with its terms
+      if (isinf(term.hi)) term.lo = 0.f;
       if (p.ref_logp != nullptr) {
         kl = exp_minus_tangent(v.q);
-        if (p.kl_coef != 0.f)
-          loss = v.q.hi > kFarExp ? loss + times_far_exp(p.kl_coef, v.q) : fmaf(p.kl_coef, kl, loss);
+        if (p.kl_coef != 0.f) term.lo += v.q.hi > kFarExp ? times_far_exp(p.kl_coef, v.q) : p.kl_coef * kl;
       }
-      if (ENT) loss = fmaf(-p.entropy_coef, v.H, loss);
+      if (ENT) term.lo = fmaf(-p.entropy_coef, v.H, term.lo);
+      loss = v.lp != v.lp ? v.lp : f2_float(term);
     }
     p.row_loss[row] = loss;
     if (p.kl != nullptr) p.kl[row] = kl;

@@ -49,8 +49,8 @@ struct LossParams {
   const float* ref_logp;
   const float* advantages;
   const float* weights;
-  float clip_lo, clip_hi;  // 1 - clip_low, 1 + clip_high
-  LossPair ln_lo, ln_hi;   // their logarithms as pairs (-inf, inf: no clip)
+  LossPair clip_lo, clip_hi;  // 1 - clip_low, 1 + clip_high
+  LossPair ln_lo, ln_hi;      // their logarithms (-inf, inf: no clip)
   float kl_coef, entropy_coef;
   float* loss;
   bool give_back;  // tensor memory, without waiting for the cluster (tests)

@@ -132,8 +132,8 @@ int qrita_policy_loss_ex(const void* logits, int dtype, int64_t B, int64_t V, in
   prm.ref_logp = ref_logp;
   prm.advantages = advantages;
   prm.weights = weights;
-  prm.clip_lo = static_cast<float>(1.0 - clip_low);
-  prm.clip_hi = static_cast<float>(1.0 + clip_high);
+  prm.clip_lo = qrita::pair_of(1.0 - clip_low);
+  prm.clip_hi = qrita::pair_of(1.0 + clip_high);
   prm.ln_lo = qrita::pair_of(std::log(1.0 - clip_low));
   prm.ln_hi = qrita::pair_of(std::log1p(clip_high));
   prm.kl_coef = static_cast<float>(kl_coef);
