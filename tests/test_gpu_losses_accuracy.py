@@ -110,12 +110,10 @@ def test_rows_that_rise_slowly(dev, dtype, span, B, V):
 
 
 def check_entropies(x, inv_t=1.0, mask=None):
-    """H against its definition. Sums with an entropy take c = log2(e) inv_t in
-    fp32; where that is off by `off` of itself, H is by -off times the variance of
-    log p (d H / d inv_t = - inv_t Var x). Beside that, and the roundings of the values given out (half a step of
-    either sign: three times their mean's standard error), no bias is left above
-    5e-8 in log S and 2.7e-8 of E (what the exponential's mean error differs by
-    within an octave of the maximum)."""
+    """H against its definition: beside the roundings of the values given out (half
+    a step of either sign: three times their mean's standard error), no bias is left
+    above 5e-8 in log S and 2.7e-8 of E (what the exponential's mean error differs
+    by within an octave of the maximum)."""
     import torch
 
     import top_selection_row_gb300 as q
@@ -123,25 +121,13 @@ def check_entropies(x, inv_t=1.0, mask=None):
     B = x.shape[0]
     t = x.float().masked_fill(~mask, -np.inf).argmax(dim=1) if mask is not None else x.float().argmax(dim=1)
     _, H, E = exact(x, t, inv_t, mask)
-    var = []
-    for a in range(0, B, 32):
-        u = x[a:a + 32].double() * inv_t
-        if mask is not None:
-            u = u.masked_fill(~mask[a:a + 32], -np.inf)
-        l = torch.log_softmax(u, dim=1)
-        p, l = l.exp(), l.clamp(min=-1e6)
-        var.append((p * l * l).sum(dim=1) - (p * l).sum(dim=1) ** 2)
-    var = torch.cat(var).cpu().numpy()
-    c = np.log2(np.e) * inv_t
-    off = float(np.float32(c)) / c - 1
     outs = [q.qrita_token_logprobs(x, t.int(), mask=mask, inv_temperature=inv_t, entropy=True)[1],
             q.qrita_policy_loss(x, t.int(), None, torch.zeros(B, device=x.device), mask=mask, inv_temperature=inv_t, entropy=True).entropy]
     for got in outs:
         err = got.cpu().numpy().astype(np.float64) - H
-        assert (np.abs(err) <= 2 * bound(E) + abs(off) * var + HALF * H * 1.01).all(), np.abs(err).max()
+        assert (np.abs(err) <= 2 * bound(E) + HALF * H * 1.01).all(), np.abs(err).max()
         noise = 3 * HALF * np.sqrt((H ** 2).mean() / 3 / B)
-        bias = (err + off * var).mean()
-        assert abs(bias) <= 5e-8 + 2.7e-8 * E.mean() + noise, (bias, err.mean(), E.mean(), var.mean(), off)
+        assert abs(err.mean()) <= 5e-8 + 2.7e-8 * E.mean() + noise, (err.mean(), E.mean())
 
 
 @DTYPES

@@ -144,22 +144,16 @@ __device__ __forceinline__ float fmax3(float a, float b, float c) {
 __device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
 
 // d c for the sums' exponents. c in fp32 is off by up to 6e-8 of itself, the same
-// way for every logit of a row, and leaves logp off by that of the token's
-// distance from the row's mean exponent (1.1e-6 at a distance of 20). Sums
-// without an entropy take c as hi + lo, rounded once (lo is above 0, so that a
-// difference of -inf stays -inf); with one, log S is put right by the mean
-// exponent that the entropy's sum gives, and H is left off by c's error times the
-// variance of log p, as is usual for its temperature in fp32 (1.3e-8 of it at
-// temperature 1; hi + lo there would take 91.1 us against 87.0 for 1024 x 262144
-// bf16).
-template <bool ENT>
-__device__ __forceinline__ float scaled(float d, const Scale& c) {
-  return ENT ? d * c.near : fmaf(d, c.hi, d * c.lo);
-}
-template <bool ENT>
-__device__ __forceinline__ float2 scaled2(float2 d, const Scale& c) {
-  return ENT ? mul2(d, both(c.near)) : fma2(d, both(c.hi), mul2(d, both(c.lo)));
-}
+// way for every logit of a row, and alone would leave logp off by that of the
+// token's distance from the row's mean exponent (1.1e-6 at a distance of 20), and H
+// by that of the variance of log p. A single difference takes c as a pair. A group
+// of logits takes the low part's product of its largest one, as the addend of its
+// multiplications: what is left is the low part's of the distances within a group,
+// where a thirty-second of the weight goes three below its top. (The low part of
+// each difference by itself, one more instruction a pair, takes 102 us against 89
+// for the sums of 1222 x 201088 bf16.) The bound keeps a difference of -inf at -inf.
+constexpr float kFarthest = -1e30f;
+__device__ __forceinline__ float scaled(float d, const Scale& c) { return fmaf(d, c.hi, fmaxf(d, kFarthest) * c.lo); }
 
 // Element access. A row is worked on in units of 16 bytes, aligned in memory:
 // `head` elements before the first unit, then the units, then a tail.
@@ -268,7 +262,7 @@ struct Running {
   __device__ __forceinline__ float m() const { return limit == -INFINITY ? -INFINITY : ref; }
   __device__ __forceinline__ void raise(float x, const Scale& c) {
     // (the first time the sums are 0, or NaN, whatever the factor)
-    const float d = fminf(fmaxf(scaled<ENT>(ref - x, c), kMinExp), 0.f);
+    const float d = fminf(fmaxf(scaled(ref - x, c), kMinExp), 0.f);
     const float f = ex2(d);
     if (ENT) {
       t = (t + d * s) * f;
@@ -286,7 +280,7 @@ struct Running {
   }
   __device__ __forceinline__ void add_one(float x, const Scale& c) {
     if (x > limit) raise(x, c);
-    const float y = scaled<ENT>(x - ref, c);
+    const float y = scaled(x - ref, c);
     const float e = ex2(y);
     add(e);
     if (ENT) t = fmaf(e, y < kMinExp ? kMinExp : y, t);
@@ -296,15 +290,15 @@ struct Running {
   // one test of the maximum.
   template <int N>
   __device__ __forceinline__ void add_unit(const float2 (&x)[N], const Scale& c) {
-    float top = limit;
+    float top = fmaxf(x[0].x, x[0].y);
 #pragma unroll
-    for (int i = 0; i < N; ++i) top = fmax3(top, x[i].x, x[i].y);
+    for (int i = 1; i < N; ++i) top = fmax3(top, x[i].x, x[i].y);
     if (top > limit) raise(top, c);
-    const float2 nr = both(-ref);
+    const float2 nr = both(-ref), by = both(c.hi), low = both(fmaxf(top - ref, kFarthest) * c.lo);
     float2 es[N], ts[N];
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      const float2 y = scaled2<ENT>(add2(x[i], nr), c);
+      const float2 y = fma2(add2(x[i], nr), by, low);
       es[i] = make_float2(ex2(y.x), ex2(y.y));
       if (ENT) ts[i] = mul2(es[i], make_float2(y.x < kMinExp ? kMinExp : y.x, y.y < kMinExp ? kMinExp : y.y));
     }
@@ -329,9 +323,8 @@ __device__ __forceinline__ void stat_shift(Stat& a, float to, const Scale& c) {
   if (a.m == to) return;
   float dh, dl;
   two_sum(a.m, -to, dh, dl);
-  const float by = ENT ? c.near : c.hi;
-  const float y = dh * by, d = fmaxf(y, kMinExp);
-  const float lost = y > kMinExp ? fmaf(dh, by, -y) + fmaf(dl, by, ENT ? 0.f : dh * c.lo) : 0.f;
+  const float y = dh * c.hi, d = fmaxf(y, kMinExp);
+  const float lost = y > kMinExp ? fmaf(dh, c.hi, -y) + fmaf(dl, c.hi, dh * c.lo) : 0.f;
   const float f = ex2(d), more = fmaf(lost, static_cast<float>(kLn2), shift_low(d));
   if (ENT) {
     a.t = f2_merge(a.t, f2_prod(d, a.s.hi));
@@ -395,7 +388,7 @@ __device__ __forceinline__ Stat warp_stat(const Scale& c, const StatSlots<THREAD
   for (int o = 16; o > 0; o >>= 1) v.m = fmaxf(v.m, __shfl_xor_sync(kAll, v.m, o));
 #pragma unroll
   for (int i = 0; i < THREADS / 32; ++i) {
-    const float d = ms[i] == v.m ? 0.f : fmaxf(scaled<ENT>(ms[i] - v.m, c), kMinExp);
+    const float d = ms[i] == v.m ? 0.f : fmaxf(scaled(ms[i] - v.m, c), kMinExp);
     const float f = ex2(d), s = slots.s[lane + 32 * i] * f;
     f2_add(v.s, s);
     v.s.lo += slots.lo[lane + 32 * i] * f + (d != 0.f ? s * shift_low(d) : 0.f);
@@ -580,14 +573,12 @@ __device__ __forceinline__ RowVals row_vals(const LossParams& p, const RowIn& in
   // (a token that is not kept has probability 0 unless the row's sums are NaN)
   v.logp = f2_make(st.s.hi == st.s.hi ? -INFINITY : st.s.hi, 0.f);
   if (in.kept_t && !empty) {
-    // d ln S / d ln c is that mean: from c.near back to c
-    const F2 ln_sc = ENT ? f2_merge(ln_s, f2_make(-mean.hi * p.c.near_off, 0.f)) : ln_s;
     F2 d;
     two_sum(in.x_t, -st.m, d.hi, d.lo);
     if (fabsf(d.hi) < 1e30f && fabsf(d.hi * p.inv_t) < 1e30f) {
       F2 y = f2_mul(d, p.inv_t);  // (x_t - m) inv_t
       y.lo = fmaf(d.hi, p.inv_t_lo, y.lo);
-      v.logp = f2_sub(y, ln_sc);
+      v.logp = f2_sub(y, ln_s);
     } else {
       v.logp.hi = d.hi * p.inv_t - ln_s.hi;  // no digit of ln S counts (or -inf, or NaN)
     }
@@ -710,7 +701,7 @@ __device__ __forceinline__ void write_grad(const LossParams& p, const Share<DT>&
   unsigned char* gu = grow + sh.head * E::kBytes;
   const bool vec = (reinterpret_cast<uintptr_t>(gu) & 15u) == 0;
   const bool zero = g.a == 0.f && g.h == 0.f;
-  const float2 nm = both(-g.m), cc = both(p.c.near), aa = both(g.a), hh = both(g.h);
+  const float2 nm = both(-g.m), cc = both(p.c.hi), aa = both(g.a), hh = both(g.h);
   auto put = [&](int64_t u, const float2 (&v)[N]) {
     if (vec) {
       __stcs(reinterpret_cast<uint4*>(gu + u * 16), E::pack(v));
@@ -754,7 +745,7 @@ __device__ __forceinline__ void write_grad(const LossParams& p, const Share<DT>&
     const int64_t j = sh.end_index(threadIdx.x);
     if (j >= 0) {
       float v = 0.f;
-      if (!zero) v = grad_one<ENT>(E::load(sh.x, j), g, p.c.near);
+      if (!zero) v = grad_one<ENT>(E::load(sh.x, j), g, p.c.hi);
       E::store(grow, j, v);
     }
   }
@@ -769,6 +760,11 @@ __device__ __forceinline__ void write_grad(const LossParams& p, const Share<DT>&
   }
 }
 
+// Blocks of row_kernel on an SM: five where 48 registers a thread are enough
+// (1500 x 262144 bf16 112 us, with four 124; 700 x 32000 7.9 and 9.9).
+template <int DT, bool ENT>
+constexpr int kRowBlocks = DT == QRITA_DTYPE_BF16 && !ENT ? 5 : kLossBlocks;
+
 // A cluster of C CTAs per row, in one pass over HBM for the sums: each CTA
 // streams its share of the row, the shares merge through distributed shared
 // memory, and rank 0 writes the row's values. A gradient (here only of rows too
@@ -776,7 +772,8 @@ __device__ __forceinline__ void write_grad(const LossParams& p, const Share<DT>&
 // log-probabilities of 1500 x 262144 bf16 112 us (7.0 TB/s), of 1024 rows 84 us
 // (6.4 TB/s: 1.7 waves of blocks); with entropies 1024 rows 87 us.
 template <int THREADS, int DT, bool ENT>
-__global__ void __launch_bounds__(THREADS, kLossThreads * kLossBlocks / THREADS) row_kernel(const LossParams p, RowStat* stats, int op) {
+__global__ void __launch_bounds__(THREADS, kLossThreads * kRowBlocks<DT, ENT> / THREADS)
+row_kernel(const LossParams p, RowStat* stats, int op) {
   using E = Elem<DT>;
   constexpr int N = E::kUnit / 2;
   __shared__ StatSlots<THREADS> slots;
@@ -1043,7 +1040,7 @@ __global__ void __launch_bounds__(THREADS, kLossThreads * kLossBlocks / THREADS)
     unsigned long long s = 0ull, t = 0ull;
     for (int i = tid; i < count; i += THREADS) {
       const float x = list_x[i];
-      const float y = x == -INFINITY ? kMinExp : fmaxf(scaled<ENT>(x - m, p.c), kMinExp);
+      const float y = x == -INFINITY ? kMinExp : fmaxf(scaled(x - m, p.c), kMinExp);
       const float e = bad ? 0.f : ex2(y);
       s += round_u64(e * kKeptScale);
       if (ENT) t += round_u64(e * -y * kKeptScale);
@@ -1108,7 +1105,7 @@ __global__ void __launch_bounds__(THREADS, kLossThreads * kLossBlocks / THREADS)
     }
     if (!zero)
       for (int i = tid; i < count; i += THREADS)
-        E::store(grow, lo + list[i], grad_one<ENT>(list_x[i], g, p.c.near));
+        E::store(grow, lo + list[i], grad_one<ENT>(list_x[i], g, p.c.hi));
   } else {
     const bool gvec = (reinterpret_cast<uintptr_t>(grow + head * E::kBytes) & 15u) == 0;
     for (int64_t u0 = tid; u0 < n_u; u0 += THREADS * kUnroll) {
@@ -1126,8 +1123,8 @@ __global__ void __launch_bounds__(THREADS, kLossThreads * kLossBlocks / THREADS)
         E::unpack(w[k], x);
 #pragma unroll
         for (int i = 0; i < N; ++i) {
-          x[i].x = bits[k] >> (2 * i) & 1u ? grad_one<ENT>(x[i].x, g, p.c.near) : 0.f;
-          x[i].y = bits[k] >> (2 * i + 1) & 1u ? grad_one<ENT>(x[i].y, g, p.c.near) : 0.f;
+          x[i].x = bits[k] >> (2 * i) & 1u ? grad_one<ENT>(x[i].x, g, p.c.hi) : 0.f;
+          x[i].y = bits[k] >> (2 * i + 1) & 1u ? grad_one<ENT>(x[i].y, g, p.c.hi) : 0.f;
         }
         if (gvec) {
           *reinterpret_cast<uint4*>(grow + j * E::kBytes) = E::pack(x);
@@ -1141,7 +1138,7 @@ __global__ void __launch_bounds__(THREADS, kLossThreads * kLossBlocks / THREADS)
       }
     }
     if (end_j >= 0)
-      E::store(grow, end_j, !zero && end_kept ? grad_one<ENT>(E::load(xrow, end_j), g, p.c.near) : 0.f);
+      E::store(grow, end_j, !zero && end_kept ? grad_one<ENT>(E::load(xrow, end_j), g, p.c.hi) : 0.f);
   }
   if (in.kept_t && token >= lo && token < hi) {
     __syncthreads();
@@ -1361,7 +1358,7 @@ __global__ void __launch_bounds__(kResThreads, kResBlocks) resident_kernel(const
   if (g.a == 0.f && g.h == 0.f) {
     write_grad<kResThreads, DT, ENT>(p, sh, row, g, token);
   } else {
-    const float2 nm = both(-g.m), cc = both(p.c.near), aa = both(g.a), hh = both(g.h);
+    const float2 nm = both(-g.m), cc = both(p.c.hi), aa = both(g.a), hh = both(g.h);
     auto entries = [&](uint4 w, float2 (&e)[N]) {
       float2 x[N];
       E::unpack(w, x);
@@ -1415,7 +1412,7 @@ __global__ void __launch_bounds__(kResThreads, kResBlocks) resident_kernel(const
         }
       }
     }
-    if (end_j >= 0) E::store(grow, end_j, grad_one<ENT>(end_x, g, p.c.near));
+    if (end_j >= 0) E::store(grow, end_j, grad_one<ENT>(end_x, g, p.c.hi));
     const int64_t u = (token - sh.head) / E::kUnit;  // (token < head: 0 or below, an end)
     const bool end = token < sh.head || u >= sh.nu;
     if (end ? sh.ends : (u >= sh.u_lo && u < sh.u_hi)) {

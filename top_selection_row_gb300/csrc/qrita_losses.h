@@ -14,11 +14,10 @@ struct LossPair {
   float hi, lo;
 };
 
-// c = log2(e) * inv_temperature (weights are 2^((x - m) c)) as hi + lo with
-// lo > 0, and to nearest, which is off by near_off of c. Logits an octave
-// (1 / c) apart differ by a factor of 2 in weight.
+// c = log2(e) * inv_temperature, hi + lo: weights are 2^((x - m) c). Logits an
+// octave (1 / c) apart differ by a factor of 2 in weight.
 struct Scale {
-  float hi, lo, near, near_off, octave;
+  float hi, lo, octave;
 };
 
 // Arguments of the loss kernels; null pointers are the optional arguments of

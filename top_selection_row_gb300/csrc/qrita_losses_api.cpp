@@ -27,7 +27,6 @@ int loss_args(const void* logits, int dtype, int64_t B, int64_t V, int64_t ld, c
   if (B < 0 || B > kMax || V < 1 || V > kMax || ld < V) return QRITA_EINVAL;
   if (!(inv_temperature >= 1e-30 && inv_temperature <= 1e30)) return QRITA_EINVAL;
   const double c = 1.4426950408889634074 * inv_temperature;
-  const float near = static_cast<float>(c);
   if (grad != nullptr && ld_grad < V) return QRITA_EINVAL;
   std::memset(out, 0, sizeof(*out));
   out->logits = logits;
@@ -36,12 +35,9 @@ int loss_args(const void* logits, int dtype, int64_t B, int64_t V, int64_t ld, c
   out->ld = ld;
   out->mask = mask;
   out->tokens = tokens;
-  out->c.near = near;
-  out->c.octave = static_cast<float>(1.0 / c);
-  out->c.near_off = static_cast<float>(near / c - 1.0);
-  out->c.hi = near < c ? near : std::nextafterf(near, 0.f);
+  out->c.hi = static_cast<float>(c);
   out->c.lo = static_cast<float>(c - out->c.hi);
-  if (!(out->c.lo > 0.f)) out->c.lo = std::numeric_limits<float>::denorm_min();  // (near is c itself)
+  out->c.octave = static_cast<float>(1.0 / c);
   out->inv_t = static_cast<float>(inv_temperature);
   out->inv_t_lo = static_cast<float>(inv_temperature - out->inv_t);
   out->inv_b = B > 0 ? static_cast<float>(1.0 / static_cast<double>(B)) : 0.f;
