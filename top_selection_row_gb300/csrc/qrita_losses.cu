@@ -151,9 +151,9 @@ __device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
 // multiplications: what is left is the low part's of the distances within a group,
 // where a thirty-second of the weight goes three below its top. (The low part of
 // each difference by itself, one more instruction a pair, takes 102 us against 89
-// for the sums of 1222 x 201088 bf16.) The bound keeps a difference of -inf at -inf.
-constexpr float kFarthest = -1e30f;
-__device__ __forceinline__ float scaled(float d, const Scale& c) { return fmaf(d, c.hi, fmaxf(d, kFarthest) * c.lo); }
+// for the sums of 1222 x 201088 bf16.) The bound, at a weight of 0, keeps what is
+// added below 2^-14: an exponent of -inf stays so.
+__device__ __forceinline__ float scaled(float d, const Scale& c) { return fmaf(d, c.hi, fmaxf(d, c.bottom) * c.lo); }
 
 // Element access. A row is worked on in units of 16 bytes, aligned in memory:
 // `head` elements before the first unit, then the units, then a tail.
@@ -294,7 +294,7 @@ struct Running {
 #pragma unroll
     for (int i = 1; i < N; ++i) top = fmax3(top, x[i].x, x[i].y);
     if (top > limit) raise(top, c);
-    const float2 nr = both(-ref), by = both(c.hi), low = both(fmaxf(top - ref, kFarthest) * c.lo);
+    const float2 nr = both(-ref), by = both(c.hi), low = both(fmaxf(top - ref, c.bottom) * c.lo);
     float2 es[N], ts[N];
 #pragma unroll
     for (int i = 0; i < N; ++i) {

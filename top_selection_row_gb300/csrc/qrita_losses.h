@@ -15,9 +15,10 @@ struct LossPair {
 };
 
 // c = log2(e) * inv_temperature, hi + lo: weights are 2^((x - m) c). Logits an
-// octave (1 / c) apart differ by a factor of 2 in weight.
+// octave (1 / c) apart differ by a factor of 2 in weight, and one a thousand
+// octaves below another (bottom, < 0) has none beside it.
 struct Scale {
-  float hi, lo, octave;
+  float hi, lo, octave, bottom;
 };
 
 // Arguments of the loss kernels; null pointers are the optional arguments of

@@ -38,6 +38,7 @@ int loss_args(const void* logits, int dtype, int64_t B, int64_t V, int64_t ld, c
   out->c.hi = static_cast<float>(c);
   out->c.lo = static_cast<float>(c - out->c.hi);
   out->c.octave = static_cast<float>(1.0 / c);
+  out->c.bottom = static_cast<float>(-1000.0 / c);
   out->inv_t = static_cast<float>(inv_temperature);
   out->inv_t_lo = static_cast<float>(inv_temperature - out->inv_t);
   out->inv_b = B > 0 ? static_cast<float>(1.0 / static_cast<double>(B)) : 0.f;
