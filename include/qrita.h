@@ -295,9 +295,14 @@ int qrita_candidates(const void* logits, int dtype, int64_t B, int64_t V, const 
  * element in common); two buffers whose addresses overlap otherwise are
  * QRITA_EINVAL. The other outputs overlap nothing. Values are fp32, from fp32
  * exponentials; a thread's share of a row is summed in compensated fp32 (its
- * entropy terms in fp32), all sums beyond are pairs of fp32 or fp64 (logp is
- * within about 1e-7 of its definition before it is rounded). Results do not
- * depend on timing: the same call gives the same bits.
+ * entropy terms in fp32), all sums beyond are pairs of fp32 or fp64. Before it
+ * is rounded, logp is off by at most 2^-22 + 2^-24 (10 + E), E the mean of
+ * |log(p_j / max p)| under p, and by less than 1e-7 as a root mean square over
+ * rows; ratios, KL terms and sums over rows see it so. H is off by at most twice
+ * as much. A row's loss is rounded once, and a loss is the fp64 sum of the
+ * rounded rows or pairs: where those cancel, it is off by as much as they are,
+ * not by 2^-24 of itself. Results do not depend on timing: the same call gives
+ * the same bits.
  *
  * Common arguments (device pointers unless said otherwise):
  *   logits, dtype, B, V   as qrita_select; B <= 2^31-1.
@@ -416,7 +421,7 @@ size_t qrita_preference_workspace_bytes(int64_t B, int64_t P);
  *   P             pairs, >= 0, 2 P + 1 <= 2^31-1. P == 0 writes a loss of 0.
  *   ref_logp      float[2 P] or NULL (0): the reference's L_s.
  *   weights       float[P] or NULL: NULL weighs every pair 1 / P.
- *   beta          finite, > 0;  label_smoothing in [0, 1];  margin finite.
+ *   beta          finite, > 0 (beyond fp32 too);  label_smoothing in [0, 1];  margin finite.
  *   length_norm   0 or 1.
  *   grad_loss     as qrita_policy_loss.
  *   out_loss      float[1];  out_pair_loss float[P].

@@ -394,7 +394,7 @@ PreferenceLoss = namedtuple("PreferenceLoss", "loss grad pair_loss log_ratio seq
 # it that its inputs are ready there, and waits for it before the results are used
 # elsewhere; both may be dropped at any time.
 #
-# (These calls take 3 to 10 us on the GPU for a small batch, so what they do on
+# (These calls take 3 to 13 us on the GPU for a small batch, so what they do on
 # the host is kept short: plain integers as pointers, one test per property.)
 def _padded_rows(t, name="logits"):
     """B, V and the leading dimension of [B, V] rows that may be padded."""

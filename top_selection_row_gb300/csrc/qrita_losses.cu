@@ -57,8 +57,8 @@ __device__ __forceinline__ float shift_low(float d) { return d > -1.f ? 2.3e-8f 
 // Rows this short (bytes that their sums read) take blocks of half the threads
 // where a block has one whole: more of them on an SM cover the chain of steps
 // that every row goes through. Log-probabilities of 4000 rows of 2000, 8000 and
-// 16000 bf16: 9.9, 17.3 and 25.9 us against 14.9, 25.2 and 32.5; of 32000
-// (64 KB), 11.6 us against 10.2 for 700 rows.
+// 16000 bf16: 8.6, 13.7 and 26.1 us against 13.2, 18.8 and 32.6; of 700 rows of
+// 32000 (64 KB), from HBM, 18.4 us against 16.4.
 constexpr int64_t kShortRow = 32 * 1024;
 
 // What row_kernel computes for a row.
@@ -150,8 +150,9 @@ __device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
 // of logits takes the low part's product of its largest one, as the addend of its
 // multiplications: what is left is the low part's of the distances within a group,
 // where a thirty-second of the weight goes three below its top. (The low part of
-// each difference by itself, one more instruction a pair, takes 102 us against 89
-// for the sums of 1222 x 201088 bf16.) The bound, at a weight of 0, keeps what is
+// each difference by itself, one more instruction a pair: log-probabilities of 4000
+// x 8000 bf16 15.7 us against 14.1, of 1024 x 262144 with entropies 91 against 88.)
+// The bound, at a weight of 0, keeps what is
 // added below 2^-14: an exponent of -inf stays so.
 __device__ __forceinline__ float scaled(float d, const Scale& c) { return fmaf(d, c.hi, fmaxf(d, c.bottom) * c.lo); }
 
@@ -761,7 +762,8 @@ __device__ __forceinline__ void write_grad(const LossParams& p, const Share<DT>&
 }
 
 // Blocks of row_kernel on an SM: five where 48 registers a thread are enough
-// (1500 x 262144 bf16 112 us, with four 124; 700 x 32000 7.9 and 9.9).
+// (log-probabilities of 1500 x 262144 bf16 113 us, with four 124; of 700 x 32000 8.4
+// and 9.9; of 1024 x 262144, whose last wave is fuller with four, 91 and 85).
 template <int DT, bool ENT>
 constexpr int kRowBlocks = DT == QRITA_DTYPE_BF16 && !ENT ? 5 : kLossBlocks;
 
@@ -769,8 +771,8 @@ constexpr int kRowBlocks = DT == QRITA_DTYPE_BF16 && !ENT ? 5 : kLossBlocks;
 // streams its share of the row, the shares merge through distributed shared
 // memory, and rank 0 writes the row's values. A gradient (here only of rows too
 // long for resident_kernel) takes a second pass over the share. HBM bounds it:
-// log-probabilities of 1500 x 262144 bf16 112 us (7.0 TB/s), of 1024 rows 84 us
-// (6.4 TB/s: 1.7 waves of blocks); with entropies 1024 rows 87 us.
+// log-probabilities of 1500 x 262144 bf16 113 us (7.0 TB/s), of 1024 rows 91 us
+// (5.9 TB/s: 1.3 waves of blocks); with entropies 1024 rows 89 us (1.7 waves).
 template <int THREADS, int DT, bool ENT>
 __global__ void __launch_bounds__(THREADS, kLossThreads * kRowBlocks<DT, ENT> / THREADS)
 row_kernel(const LossParams p, RowStat* stats, int op) {
@@ -843,11 +845,11 @@ row_kernel(const LossParams p, RowStat* stats, int op) {
 //
 // Log-probabilities over 64 kept ids of 1024 x 262144 bf16: 53 us, the mask at
 // 5.0 TB/s (78 us when a unit of mask bytes led to its logits at once); half of
-// all ids kept, 144 us for 805 MB. Policy loss over the kept sets of a mixed top-k
+// all ids kept, 148 us for 805 MB. Policy loss over the kept sets of a mixed top-k
 // and top-p batch of that size (a fifth of the rows keep 16 thousand ids or more)
 // 188 us; with a list of half the length and no map (rows beyond it read the mask
 // again before each load, and again for the gradient) 373. 128 x 151936 fp32 with
-// 64 kept: 24 us for 97 MB of mask and zeros; scan, merge and stores of one wave
+// 64 kept: 22 us for 97 MB of mask and zeros; scan, merge and stores of one wave
 // of blocks follow one another. Four mask units in flight instead of eight cost
 // 4 %; a list in id order by prefix sums over the map, two barriers more, 12 % of
 // the log-probabilities of 64 x 128256.
@@ -1204,10 +1206,10 @@ __device__ __forceinline__ void tmem_get(uint32_t addr, uint4 (&w)[4]) {
 // against 216 KB in shared memory alone: while some wait for their cluster's
 // sums, the others' copies and stores keep HBM busy.
 //
-// HBM bounds it: policy loss of 1024 x 262144 bf16 170 us, 6.3 TB/s of reads and
-// writes (shared memory alone, three CTAs of 64 KB: 201 us; shares of 64 KB, six
+// HBM bounds it: policy loss of 1024 x 262144 bf16 171 us, 6.3 TB/s of reads and
+// writes (when it took 170: shared memory alone, three CTAs of 64 KB: 201 us; shares of 64 KB, six
 // CTAs: 174; three CTAs of 256 threads and 128 KB: 179). A single wave of blocks
-// reads, merges and writes one after another: 255 x 50021 fp32 20 us for 102 MB.
+// reads, merges and writes one after another: 255 x 50021 fp32 19 us for 102 MB.
 // ---------------------------------------------------------------------------
 constexpr int kResThreads = 128;
 constexpr int kResBlocks = 8;
@@ -1222,7 +1224,7 @@ constexpr uint64_t kCopyLimitNs = 200ull * 1000 * 1000;
 // cluster can be waiting for columns that another kernel holds, whose own other
 // CTAs can be waiting for this CTA's columns. Then the pieces in them are given
 // up, and read again for the gradient: no CTA waits for ever with columns held.
-// (The watch costs 1 us of 170; with every CTA giving its columns up, 215 us.)
+// (The watch costs 1 us of 171; with every CTA giving its columns up, 184 us.)
 constexpr uint64_t kHoldLimitNs = 1000ull * 1000;
 
 // MOVED: the share has more than kSlots pieces. Tensor memory is taken first
@@ -1432,7 +1434,8 @@ __global__ void __launch_bounds__(kResThreads, kResBlocks) resident_kernel(const
 }
 
 // *out = sum of w[i] v[i] by one block of N threads in one fixed order, in
-// fp64 (w null: 1 / n). A weight of 0 takes nothing of a value that has left
+// fp64 (w null: 1 / n). v are the values as they are given out, rounded to fp32
+// (their own errors are as large as that: 3e-8 of a row of a policy loss). A weight of 0 takes nothing of a value that has left
 // fp32 (0, not 0 * inf); NaN stays. slots: N / 32 doubles of shared memory.
 template <int N>
 __device__ __forceinline__ void weighted_sum(const float* v, const float* w, int64_t n, float* out, double* slots) {
@@ -1576,8 +1579,8 @@ __global__ void __launch_bounds__(kPairThreads) pair_kernel(const LossParams p, 
 
 // The gradient of every row, the last rows first: those are the ones the sums'
 // kernel has left in L2 (of 300 x 128256 bf16, 77 MB, 56 MB are still there). The
-// first CTA adds up the loss. HBM bounds it: 1222 x 201088 bf16 in 150 us is
-// 6.5 TB/s of reads and writes.
+// first CTA adds up the loss. HBM bounds it: 1222 x 201088 bf16 in 146 us is
+// 6.7 TB/s of reads and writes.
 template <int DT>
 __global__ void __launch_bounds__(kLossThreads, kLossBlocks) pref_grad_kernel(const LossParams p, const PrefParams q,
                                                                               const RowGrad* grads) {
@@ -1605,8 +1608,8 @@ int device_sms() {
 
 // CTAs per row: as many as fill the device (a power of two), with at least a
 // unit or two for each thread. Fewer leave SMs idle (log-probabilities of 64 x
-// 128256 bf16: 8 CTAs 7.4 us, 2 CTAs 10.5), more than fill it only add merges
-// (300 x 128256 fp32: 1 or 2 CTAs 26.6 us, 4 CTAs 36.4). When a second pass
+// 128256 bf16 from HBM: 8 CTAs 12.3 us, 2 CTAs 16.4, 1 CTA 20.5), more than fill
+// it only add merges (300 x 128256 fp32: 2 CTAs 26.9 us, 1 CTA 31.1, 4 CTAs 37.7). When a second pass
 // follows, shares of 64 KB at most, so that the rows in flight fit in L2.
 uint32_t row_ctas(const LossParams& p, int64_t bytes, bool second_pass, int per_sm) {
   const int sms = device_sms();
@@ -1659,8 +1662,9 @@ constexpr int64_t kResidentUnits = static_cast<int64_t>(kSlots + kMoved) * kPiec
 
 // CTAs per row for resident_kernel (0: a row does not fit in a cluster): as
 // few as hold the row, and more where the batch leaves SMs idle. More than that
-// cost merges (policy loss of 1024 x 262144 bf16: 10 CTAs 169 us, 12 CTAs 177, 16
-// CTAs 196; gradients of 1000 x 16000 bf16: 1 CTA 14.0 us, 2 CTAs 16.9).
+// cost merges (policy loss of 1024 x 262144 bf16: 10 CTAs 171 us, 12 CTAs 181, 16
+// CTAs 202; gradients of 1000 x 16000 bf16 from HBM: 1 CTA 20.5 us, 2 CTAs 22.5, 4
+// CTAs 28.7).
 uint32_t resident_ctas(const LossParams& p, int dtype) {
   const int64_t units = p.V / (dtype == QRITA_DTYPE_F32 ? 4 : 8);
   const int64_t least = units > 0 ? (units + kResidentUnits - 1) / kResidentUnits : 1;
