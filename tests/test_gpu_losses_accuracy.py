@@ -50,7 +50,7 @@ def exact(x, tokens, inv_t, mask=None):
     return [torch.cat(v).cpu().numpy() for v in (logp, H, E)]
 
 
-def check(x, tokens, inv_t=1.0, mask=None):
+def check(x, tokens, inv_t=1.0, mask=None, mean=RMS):
     import torch
 
     import top_selection_row_gb300 as q
@@ -66,7 +66,7 @@ def check(x, tokens, inv_t=1.0, mask=None):
             d -= (np.expm1(d) - d - kl) / np.expm1(d)
         err = ref.cpu().numpy().astype(np.float64) - d - want
         assert (np.abs(err) <= bound(E) + 2e-9).all(), (form, np.abs(err).max(), bound(E).max())
-        assert np.sqrt((err ** 2).mean()) <= RMS and abs(err.mean()) <= RMS, (form, np.sqrt((err ** 2).mean()), err.mean())
+        assert np.sqrt((err ** 2).mean()) <= RMS and abs(err.mean()) <= mean, (form, np.sqrt((err ** 2).mean()), err.mean())
         # the fp32 value given out is that, rounded
         out = got.logp.cpu().numpy().astype(np.float64)
         assert (np.abs(out - want) <= bound(E) + HALF * np.abs(want) * 1.01).all()
@@ -214,13 +214,22 @@ def test_a_beta_beyond_fp32(dev):
 
 
 @DTYPES
+@pytest.mark.parametrize("warm", [True, False])
 @pytest.mark.parametrize("B,V", [(700, 128256), (64, 262144), (1000, 3001), (16, 32000)])
-def test_ordinary_tokens(dev, dtype, B, V):
+def test_ordinary_tokens(dev, dtype, B, V, warm):
+    """The mean over rows adds up in a sequence's sum. The instruction's own is 0
+    to 5e-8 from octave to octave, and 2.5e-8 of it are taken back; a group of 32
+    logits takes the low part of c = log2(e) inv_t by its largest, which leaves c's
+    error in fp32 times their mean distance below it under p: at most 1.83 (that of
+    31 logits 3 below one)."""
     import torch
 
     g, x = logits(dev, V + 1, B, V, dtype)
     noise = torch.rand(B, V, generator=g, device=dev).clamp_(min=1e-30).log_().neg_().log_().neg_()
-    check(x, (x.float() + noise).argmax(dim=1).int(), 1.0 if V % 2 else 0.75)
+    inv_t = 1.25 if not warm else 1.0 if V % 2 else 0.75
+    c = np.log2(np.e) * inv_t
+    off = abs(float(np.float32(c)) / c - 1)  # (3e-9 at 1.25)
+    check(x, (x.float() + noise).argmax(dim=1).int(), inv_t, mean=2.5e-8 + 1.83 * off + 3 * 5e-8 / np.sqrt(B))
 
 
 @DTYPES
@@ -302,3 +311,17 @@ def test_row_losses_are_rounded_once(dev, ref, ent):
     tol = tol + np.where(rho < 0.51, 2.0 ** -22 * np.abs(a) * rho, 0.0)
     assert (err <= tol)[~edge].all(), ((err - tol)[~edge].max(), np.argmax(np.where(edge, 0, err - tol)))
     assert abs(float(got.loss) - row.mean()) <= HALF * (abs(row.mean()) + np.abs(row).mean())
+
+
+@DTYPES
+@pytest.mark.parametrize("scale", [0.25, 0.5, 1.0])
+@pytest.mark.parametrize("B,V", [(3000, 3001), (1000, 20011)])
+def test_broad_rows_have_no_bias(dev, dtype, scale, B, V):
+    """Rows whose weight is spread over logits near their maximum, at a temperature
+    that fp32 holds to 3e-9: the bounds of test_ordinary_tokens."""
+    import torch
+
+    g = torch.Generator(device=dev).manual_seed(V)
+    x = (torch.randn(B, V, generator=g, device=dev) * scale).to(torch.float32 if dtype == "f32" else torch.bfloat16)
+    t = torch.randint(0, V, (B,), generator=g, device=dev, dtype=torch.int32)
+    check(x, t, 1.25, mean=2.5e-8 + 1.83 * 3.2e-9 + 3 * 5e-8 / np.sqrt(B))
