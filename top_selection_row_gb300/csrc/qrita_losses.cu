@@ -7,8 +7,9 @@
 // learning; these kernels score the drawn tokens under the same logits (and
 // the same keep-mask).
 //
-// Everything is in base 2. With c = log2(e) * inv_temperature and m the
-// largest kept logit, a kept logit weighs e_j = 2^y_j, y_j = (x_j - m) c, and
+// Everything is in base 2. With c = log2(e) * inv_temperature and m a kept logit
+// within an octave of weight (1 / c) of the largest, a kept logit weighs
+// e_j = 2^y_j, y_j = (x_j - m) c, and
 //   S = sum e_j,  T = sum e_j y_j,
 //   logp_t = ln2 (y_t - log2 S),  H = ln2 (log2 S - T / S),  p_j = e_j / S.
 // The difference x_j - m comes before the product, so rows of the type's
@@ -79,8 +80,9 @@ struct RowStat {
   float s;  // below 0: the row joins nothing
 };
 
-// The softmax sums of some of a row's kept logits, relative to their maximum
-// m (-inf, and sums of 0, before the first): S and T as fp32 pairs.
+// The softmax sums of some of a row's kept logits, relative to one of them, m,
+// within an octave of the largest (-inf, and sums of 0, before the first): S and
+// T as fp32 pairs.
 struct Stat {
   float m;
   F2 s, t;
