@@ -420,7 +420,8 @@ size_t qrita_preference_workspace_bytes(int64_t B, int64_t P);
  *                 then unspecified.
  *   P             pairs, >= 0, 2 P + 1 <= 2^31-1. P == 0 writes a loss of 0.
  *   ref_logp      float[2 P] or NULL (0): the reference's L_s.
- *   weights       float[P] or NULL: NULL weighs every pair 1 / P.
+ *   weights       float[P] or NULL: NULL weighs every pair 1 / P. A pair of
+ *                 weight 0 adds nothing (NaN pairs apart).
  *   beta          finite, > 0 (beyond fp32 too);  label_smoothing in [0, 1];  margin finite.
  *   length_norm   0 or 1.
  *   grad_loss     as qrita_policy_loss.
