@@ -445,6 +445,57 @@ int qrita_preference_loss(const void* logits, int dtype, int64_t B, int64_t V, i
                           size_t workspace_bytes, qrita_stream_t stream);
 
 /*
+ * qrita_token_scores: log-probabilities of M given tokens a row, the first one's
+ * rank, the row's entropy and its N top alternatives, in one read of the logits:
+ * what a sampler reports beside its draw, and what a teacher gives a student.
+ * Rows, kept sets, probabilities and accuracy are those of the losses above, but
+ * a token outside [0, V) is padding of its own place alone.
+ *
+ *   tokens       int32[B, M]; M from 0 to 8192 (NULL where M is 0).
+ *   N            0 to 128.
+ *   out_logp     float[B, M]: log p of each token; 0 for padding, -inf where p
+ *                is 0 (not kept, or a logit of -inf).
+ *   out_rank     int32[B] or NULL (NULL where M is 0): how many kept tokens
+ *                precede tokens[r, 0] in the stable descending order of the row
+ *                (0: it is the first); -1 where it is padding or its p is 0.
+ *   out_entropy  float[B] or NULL.
+ *   out_top_ids  int32[B, N]: the first N kept tokens of that order, then -1 where
+ *                fewer have a logit above -inf.
+ *   out_top_logp float[B, N]: their log p, then -inf.
+ *   A row with NaN or +inf in K: its logp (padding apart), entropy and top logp
+ *   are NaN, its rank and top ids -1.
+ *
+ * One kernel on stream; a row whose largest logits are many equal ones, or lie
+ * apart by a multiple of the kernel's step, takes longer. At least one of M, N and
+ * out_entropy is given. B == 0 launches nothing.
+ */
+int qrita_token_scores(const void* logits, int dtype, int64_t B, int64_t V, int64_t ld, const uint8_t* mask,
+                       const int32_t* tokens, int32_t M, int32_t N, double inv_temperature, float* out_logp,
+                       int32_t* out_rank, float* out_entropy, int32_t* out_top_ids, float* out_top_logp,
+                       qrita_stream_t stream);
+
+/*
+ * qrita_token_scores_grad: its gradient,
+ *   out_grad[r, j] = sum over i of grad_logp[r, i] d logp(ids[r, i]) / d x_j
+ *                    + grad_entropy[r] d H_r / d x_j,
+ * the derivatives as in qrita_token_logprobs_grad. The ids are given tokens, top
+ * ids, or both in one row; one that is listed twice counts twice, padding and
+ * tokens of probability 0 count for nothing.
+ *
+ *   ids                      int32[B, K]; K from 1 to 256.
+ *   grad_logp                float[B, K], grad_entropy float[B]; either may be
+ *                            NULL. A row whose given gradients are all 0 gets a
+ *                            gradient of 0.
+ *   out_grad                 dtype[B, V], leading dimension ld_grad; may be the
+ *                            logits' own buffer, as for the losses.
+ *
+ * One kernel on stream. B == 0 launches nothing.
+ */
+int qrita_token_scores_grad(const void* logits, int dtype, int64_t B, int64_t V, int64_t ld, const uint8_t* mask,
+                            const int32_t* ids, int32_t K, double inv_temperature, const float* grad_logp,
+                            const float* grad_entropy, void* out_grad, int64_t ld_grad, qrita_stream_t stream);
+
+/*
  * qrita_delta_table: copy one of the host-built truncation tables the kernel
  * receives (Qrita technical summary, "Methodology", part 1: delta comes from
  * precomputed tables of the normal quantile function keyed on k or p).

@@ -16,3 +16,4 @@ from .qrita_oracle import (  # noqa: F401
 )
 from .qrita_outputs import SAMPLE_BAND, candidates, sample, topk_ids  # noqa: F401
 from .qrita_losses import RowSoftmax, dentropy, dlogp, policy_row, preference, row_softmax  # noqa: F401
+from .qrita_scores import cache_weights, kept_order, scores_grad_row, scores_row  # noqa: F401

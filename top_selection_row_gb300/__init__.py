@@ -646,3 +646,90 @@ def qrita_preference_loss(logits, tokens, starts, ref_logp=None, weights=None, i
     elif out_grad is not None:
         _wrote(g)
     return PreferenceLoss(loss, g, pair_loss, ratio, seq, logp)
+
+
+# ---------------------------------------------------------------------------
+# Scores of given tokens and top alternatives
+# ---------------------------------------------------------------------------
+TokenScores = namedtuple("TokenScores", "logp rank entropy top_ids top_logp")
+
+
+def qrita_token_scores(logits, tokens=None, top=0, mask=None, inv_temperature=1.0, entropy=False, rank=False, stream=None,
+                       out=None):
+    """Log-probabilities of given tokens, the first one's rank, the row's entropy
+    and its top alternatives, in one read of the logits.
+
+    logits, mask, inv_temperature: as qrita_token_logprobs. tokens: CUDA int32
+    [B, M] or None, a token outside [0, V) is padding; top: 0 to 128
+    alternatives. Returns TokenScores(logp float32 [B, M] or None, rank int32 [B]
+    or None, entropy float32 [B] or None, top_ids int32 [B, top] or None,
+    top_logp float32 [B, top] or None); ``out`` = such a tuple, as an earlier call
+    returned it, reuses its tensors. include/qrita.h states what padded, unkept and
+    NaN places hold.
+    """
+    if stream is not None:
+        return _on_stream(stream, qrita_token_scores, logits, tokens, top, mask, inv_temperature, entropy, rank, None, out)
+    torch = _torch()
+    B, V, ld = _padded_rows(logits)
+    dev = logits.device
+    dt = _dtype_code(logits)
+    keep = _mask_at(mask, B, V, dev)
+    M = 0
+    if tokens is not None:
+        if tokens.dim() != 2 or tokens.shape[0] != B:
+            raise ValueError("tokens must be [B, M]")
+        M = tokens.shape[1]
+    tok = _at(tokens, B * M, torch.int32, "tokens", dev)
+    top = int(top)
+    shapes = (((B, M) if tokens is not None else None, torch.float32), ((B,) if rank else None, torch.int32),
+              ((B,) if entropy else None, torch.float32), ((B, top) if top else None, torch.int32),
+              ((B, top) if top else None, torch.float32))
+    if not 0 <= top <= 128:
+        raise ValueError("top must be from 0 to 128")
+    if out is None:
+        got = [None if s is None else torch.empty(s, dtype=d, device=dev) for s, d in shapes]
+    else:
+        got = []
+        for name, t, (s, d) in zip(TokenScores._fields, out, shapes):
+            if s is not None and (t is None or t.shape != s):
+                raise ValueError(f"out {name} must be {list(s)}")
+            got.append(None if s is None else t)
+            _at(got[-1], 0 if s is None else t.numel(), d, "out " + name, dev)
+    _call(lib().qrita_token_scores, dev, logits.data_ptr(), dt, B, V, ld, keep, tok, M, top, inv_temperature,
+          *(0 if t is None else t.data_ptr() for t in got))
+    if out is not None:
+        _wrote(*got)
+    return TokenScores(*got)
+
+
+def qrita_token_scores_grad(logits, ids, grad_logp=None, grad_entropy=None, mask=None, inv_temperature=1.0, out_grad=None,
+                            stream=None):
+    """Gradient with respect to the logits of any function of qrita_token_scores'
+    outputs: ids int32 [B, K] (given tokens, top ids, or both; K up to 256) with
+    the gradients of their log-probabilities (float32 [B, K]), and those of the
+    entropies (float32 [B]); one may be None. Returns the gradient, [B, V] of the
+    logits' type; ``out_grad`` as qrita_token_logprobs_grad."""
+    if stream is not None:
+        return _on_stream(stream, qrita_token_scores_grad, logits, ids, grad_logp, grad_entropy, mask, inv_temperature,
+                          out_grad)
+    torch = _torch()
+    B, V, ld = _padded_rows(logits)
+    dev = logits.device
+    dt = _dtype_code(logits)
+    keep = _mask_at(mask, B, V, dev)
+    if ids is None or ids.dim() != 2 or ids.shape[0] != B:
+        raise ValueError("ids must be [B, K]")
+    K = ids.shape[1]
+    at = _at(ids, B * K, torch.int32, "ids", dev)
+    if grad_logp is None and grad_entropy is None:
+        raise ValueError("one of grad_logp and grad_entropy is required")
+    if grad_logp is not None and grad_logp.shape != ids.shape:
+        raise ValueError("grad_logp must be [B, K], as the ids")
+    gl = _at(grad_logp, B * K, torch.float32, "grad_logp", dev)
+    ge = _at(grad_entropy, B, torch.float32, "grad_entropy", dev)
+    grad, ldg = _grad_rows(out_grad, logits, B, V)
+    _call(lib().qrita_token_scores_grad, dev, logits.data_ptr(), dt, B, V, ld, keep, at, K, inv_temperature, gl, ge,
+          grad.data_ptr(), ldg)
+    if out_grad is not None:
+        _wrote(grad)
+    return grad

@@ -25,6 +25,8 @@ EXPORTED = (
     "qrita_policy_loss_ex",
     "qrita_preference_workspace_bytes",
     "qrita_preference_loss",
+    "qrita_token_scores",
+    "qrita_token_scores_grad",
     "qrita_delta_table",
     "qrita_strerror",
     "qrita_version",
@@ -71,6 +73,10 @@ def lib() -> ctypes.CDLL:
     L.qrita_preference_loss.argtypes = [vp, i32, i64, i64, i64, vp, f64, vp, i64, vp, vp, f64, f64, f64, i32, vp, vp, vp,
                                         vp, vp, vp, vp, i64, vp, sz, vp]
     L.qrita_preference_loss.restype = i32
+    L.qrita_token_scores.argtypes = [vp, i32, i64, i64, i64, vp, vp, i32, i32, f64, vp, vp, vp, vp, vp, vp]
+    L.qrita_token_scores.restype = i32
+    L.qrita_token_scores_grad.argtypes = [vp, i32, i64, i64, i64, vp, vp, i32, f64, vp, vp, vp, i64, vp]
+    L.qrita_token_scores_grad.restype = i32
     L.qrita_delta_table.argtypes = [i32, vp, i32]
     L.qrita_delta_table.restype = i32
     L.qrita_strerror.argtypes = [i32]

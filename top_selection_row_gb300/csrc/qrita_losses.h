@@ -27,7 +27,8 @@ struct LossParams {
   const void* logits;
   int64_t B, V, ld;
   const uint8_t* mask;
-  const int32_t* tokens;
+  const int32_t* tokens;  // [B], or [B, K]
+  int K;                  // qrita_token_scores_grad's ids of a row
   Scale c;
   float inv_t, inv_t_lo;  // inv_temperature as a pair
   float inv_b;  // 1 / B
@@ -41,7 +42,7 @@ struct LossParams {
   void* grad;
   int64_t ld_grad;
   const float* grad_loss;
-  // qrita_token_logprobs_grad
+  // qrita_token_logprobs_grad, qrita_token_scores_grad
   const float* g_logp;
   const float* g_entropy;
   // qrita_policy_loss
@@ -55,6 +56,8 @@ struct LossParams {
   float* loss;
   bool give_back;  // tensor memory, without waiting for the cluster (tests)
 };
+
+constexpr int kMaxGradIds = 256;  // K, at most
 
 struct PrefParams {
   const int32_t* starts;
@@ -73,9 +76,15 @@ struct PrefParams {
 
 size_t pref_workspace_bytes(int64_t B);
 
+// Checks of the arguments that every entry point over rows shares (a QRITA_* code),
+// and the row part of *out.
+int row_args(const void* logits, int dtype, int64_t B, int64_t V, int64_t ld, const uint8_t* mask,
+             const int32_t* tokens, double inv_temperature, void* grad, int64_t ld_grad, LossParams* out);
+
 // Every launch returns a cudaError_t.
 int launch_logprobs(const LossParams& prm, int dtype, qrita_stream_t stream);
 int launch_logprobs_grad(const LossParams& prm, int dtype, qrita_stream_t stream);
+int launch_scores_grad(const LossParams& prm, int dtype, qrita_stream_t stream);
 int launch_policy(const LossParams& prm, int dtype, qrita_stream_t stream);
 int launch_preference(const LossParams& prm, const PrefParams& pref, int dtype, qrita_stream_t stream);
 

@@ -19,9 +19,10 @@ LossPair pair_of(double v) {
   return r;
 }
 
-// Arguments every loss entry point shares; fills the row part of *out.
-int loss_args(const void* logits, int dtype, int64_t B, int64_t V, int64_t ld, const uint8_t* mask,
-              const int32_t* tokens, double inv_temperature, void* grad, int64_t ld_grad, LossParams* out) {
+}  // namespace
+
+int row_args(const void* logits, int dtype, int64_t B, int64_t V, int64_t ld, const uint8_t* mask,
+             const int32_t* tokens, double inv_temperature, void* grad, int64_t ld_grad, LossParams* out) {
   if (dtype != QRITA_DTYPE_F32 && dtype != QRITA_DTYPE_BF16) return QRITA_EINVAL;
   constexpr int64_t kMax = std::numeric_limits<int32_t>::max();
   if (B < 0 || B > kMax || V < 1 || V > kMax || ld < V) return QRITA_EINVAL;
@@ -45,7 +46,7 @@ int loss_args(const void* logits, int dtype, int64_t B, int64_t V, int64_t ld, c
   out->grad = grad;
   out->ld_grad = ld_grad;
   if (B == 0) return QRITA_OK;
-  if (logits == nullptr || tokens == nullptr) return QRITA_EINVAL;
+  if (logits == nullptr) return QRITA_EINVAL;
   const uint64_t eb = static_cast<uint64_t>(dtype == QRITA_DTYPE_F32 ? 4 : 2);
   const uint64_t x0 = reinterpret_cast<uintptr_t>(logits), g0 = reinterpret_cast<uintptr_t>(grad);
   if (x0 % eb != 0 || g0 % eb != 0) return QRITA_EINVAL;
@@ -67,6 +68,15 @@ int loss_args(const void* logits, int dtype, int64_t B, int64_t V, int64_t ld, c
     if (!same && !apart && x0 < g0 + gn && g0 < x0 + xn) return QRITA_EINVAL;
   }
   return QRITA_OK;
+}
+
+namespace {
+
+// The same, and a token for every row.
+int loss_args(const void* logits, int dtype, int64_t B, int64_t V, int64_t ld, const uint8_t* mask,
+              const int32_t* tokens, double inv_temperature, void* grad, int64_t ld_grad, LossParams* out) {
+  const int rc = row_args(logits, dtype, B, V, ld, mask, tokens, inv_temperature, grad, ld_grad, out);
+  return rc == QRITA_OK && B > 0 && tokens == nullptr ? QRITA_EINVAL : rc;
 }
 
 }  // namespace

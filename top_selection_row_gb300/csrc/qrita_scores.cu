@@ -1,0 +1,539 @@
+// Scores of given tokens over rows of logits: their log-probabilities, the first
+// one's rank, the row's entropy and its top alternatives, in one pass.
+//
+// Qrita technical summary (gist.science, paper 2602.01518), "Problem
+// statement": the candidate set beside the drawn token; what a sampler reports of
+// both. The sums are those of the losses (qrita_rows.cuh).
+//
+// The top N of a row, in the stable descending order, without a second pass: a
+// thread keeps the largest logit of each group of units it has summed. The N-th
+// largest of the threads' own maxima bounds the N-th largest logit from below (N
+// threads have one as large), and only groups whose maximum reaches that bound are
+// read again: about N of them, 32 logits each, from L2. What reaches the bound is
+// listed as 64-bit keys (logit, then lower id) and put in order by counting, a CTA's
+// list by itself, the lists of a cluster by searches in one another. Where ties or
+// an unlucky order list more than fits, the groups are walked again in steps, and
+// the list is cut to its first N whenever it fills: right for every row, and slower.
+//
+// The rank counts logits above the token's while they are summed: before the
+// token's own unit those above its next lower value (equal ones precede it there),
+// behind it those above it; bf16 words two at a time.
+
+#include <cstddef>
+#include <cstdint>
+
+#include "qrita_rows.cuh"
+#include "qrita_scores.h"
+
+namespace qrita {
+namespace {
+
+constexpr int kScoreThreads = kLossThreads;
+constexpr int kGroups = 32;     // of a thread, at most
+constexpr int kListCap = 1024;  // candidates of a CTA
+
+// Elements of the kernel's units, and the units a thread sums in one step.
+template <int DT, bool MASKED>
+constexpr int kUnitOf = MASKED ? 16 : Elem<DT>::kUnit;
+template <int DT, bool MASKED>
+constexpr int kStep = MASKED ? 8 : kUnroll;
+
+// One CTA's units [u_lo, u_hi) of a row, with its head and tail on rank 0. Without
+// a mask units are 16 bytes of logits, aligned; under one they are 16 ids, aligned
+// in the mask, whose logits may lie anywhere.
+template <int DT, bool MASKED>
+struct Span {
+  using E = Elem<DT>;
+  static constexpr int U = kUnitOf<DT, MASKED>;
+  static constexpr int kEnds = 2 * (U - 1);  // at most
+  const unsigned char* x;
+  const uint8_t* keep;
+  int64_t V, head, nu, u_lo, u_hi;
+  bool ends, vec;
+
+  __device__ Span(const ScoreParams& p, int64_t row, uint32_t rank) {
+    V = p.V;
+    x = static_cast<const unsigned char*>(p.logits) + row * p.ld * E::kBytes;
+    keep = MASKED ? p.mask + row * V : nullptr;
+    const uintptr_t at = reinterpret_cast<uintptr_t>(MASKED ? keep : x);
+    head = min(V, static_cast<int64_t>(((16u - (at & 15u)) & 15u) / (MASKED ? 1 : E::kBytes)));
+    nu = static_cast<int64_t>(static_cast<uint64_t>(V - head) / U);
+    u_lo = min(nu, static_cast<int64_t>(rank) * p.per);
+    u_hi = min(nu, u_lo + p.per);
+    ends = rank == 0;
+    vec = (reinterpret_cast<uintptr_t>(x + head * E::kBytes) & 15u) == 0;
+  }
+
+  __device__ int64_t id(int64_t u) const { return head + u * U; }
+  __device__ int64_t end_index(int i) const {
+    if (i < head) return i;
+    const int64_t j = head + nu * U + (i - head);
+    return j < V ? j : -1;
+  }
+  __device__ bool kept(int64_t j) const { return !MASKED || keep[j] != 0; }
+  __device__ float value(int64_t j) const { return kept(j) ? E::load(x, j) : -INFINITY; }
+
+  // The kept bits of a unit (all of an unmasked one).
+  __device__ uint32_t bits(int64_t u) const { return MASKED ? kept_bits(load_unit(keep + id(u))) : 0xFFFFu; }
+  // The words of a unit's logits; nothing is read where no bit is set.
+  static constexpr int W = U * E::kBytes / 16;
+  __device__ void words(int64_t u, uint32_t b, uint4 (&w)[W]) const {
+    const int64_t j = id(u);
+    if (MASKED && b == 0u) {
+#pragma unroll
+      for (int i = 0; i < W; ++i) w[i] = make_uint4(0u, 0u, 0u, 0u);
+    } else if (!MASKED || vec) {
+#pragma unroll
+      for (int i = 0; i < W; ++i) w[i] = load_unit(x + j * E::kBytes + 16 * i);
+    } else {
+      float2 v[U / 2];
+#pragma unroll
+      for (int i = 0; i < U / 2; ++i) {
+        v[i].x = b >> (2 * i) & 1u ? E::load(x, j + 2 * i) : 0.f;
+        v[i].y = b >> (2 * i + 1) & 1u ? E::load(x, j + 2 * i + 1) : 0.f;
+      }
+#pragma unroll
+      for (int i = 0; i < W; ++i) w[i] = E::pack(reinterpret_cast<const float2(&)[E::kUnit / 2]>(v[i * E::kUnit / 2]));
+    }
+  }
+  // Their values, -inf where they are not kept.
+  __device__ static void expand(const uint4 (&w)[W], uint32_t b, float2* v) {
+#pragma unroll
+    for (int i = 0; i < W; ++i) E::unpack(w[i], reinterpret_cast<float2(&)[E::kUnit / 2]>(v[i * E::kUnit / 2]));
+    if (MASKED) {
+#pragma unroll
+      for (int i = 0; i < U / 2; ++i) {
+        if (!(b >> (2 * i) & 1u)) v[i].x = -INFINITY;
+        if (!(b >> (2 * i + 1) & 1u)) v[i].y = -INFINITY;
+      }
+    }
+  }
+};
+
+// Larger for logits that come first in the stable descending order.
+__device__ __forceinline__ unsigned long long order_key(float x, int64_t id) {
+  return static_cast<unsigned long long>(f2key(x)) << 32 | (0xFFFFFFFFu - static_cast<uint32_t>(id));
+}
+
+// What counts the logits that precede the first token: those above `at`, and above
+// `below` in units before its own. (bf16: both values twice in a word.)
+struct Above {
+  float at, below;
+  uint32_t at2, below2;
+  int64_t unit;  // the token's
+};
+
+template <int DT>
+__device__ __forceinline__ Above above_of(float x) {
+  Above a;
+  a.at = x;
+  // the next lower value of the type (x is finite; below +-0 the largest negative one)
+  uint32_t b = __float_as_uint(x);
+  if (DT == QRITA_DTYPE_BF16) b >>= 16;
+  const uint32_t sign = DT == QRITA_DTYPE_BF16 ? 0x8000u : 0x80000000u;
+  if ((b & ~sign) == 0u)
+    b = sign | 1u;
+  else
+    b = (b & sign) != 0u ? b + 1u : b - 1u;
+  a.below = __uint_as_float(DT == QRITA_DTYPE_BF16 ? b << 16 : b);
+  a.at2 = (__float_as_uint(a.at) >> 16) * 0x10001u;
+  a.below2 = (__float_as_uint(a.below) >> 16) * 0x10001u;
+  return a;
+}
+
+// The first n of the c listed keys, largest first, to `first`; the block is in step.
+template <int THREADS>
+__device__ __forceinline__ void first_of(const unsigned long long* list, int c, int n, unsigned long long* first) {
+  for (int i = threadIdx.x; i < c; i += THREADS) {
+    const unsigned long long k = list[i];
+    int r = 0;
+    for (int j = 0; j < c; ++j) r += list[j] > k;
+    if (r < n) first[r] = k;
+  }
+}
+
+// HBM bounds it where rows fill the device.
+template <int THREADS, int DT, bool ENT, bool MASKED>
+__global__ void __launch_bounds__(THREADS, kLossThreads * kLossBlocks / THREADS) score_kernel(const ScoreParams p) {
+  using Sp = Span<DT, MASKED>;
+  constexpr int U = Sp::U, K = kStep<DT, MASKED>, W = Sp::W;
+  __shared__ StatSlots<THREADS> slots;
+  __shared__ float tops[THREADS];
+  __shared__ unsigned long long list[kListCap];
+  __shared__ unsigned long long first[kMaxTop];
+  __shared__ int count;
+  __shared__ unsigned long long ranked;
+  __shared__ float bound;
+  __shared__ float row_of[6];  // m, S (its sign and NaN), ln S as a pair, H
+  extern __shared__ __align__(16) unsigned char dynamic[];
+  float* gmax = reinterpret_cast<float*>(dynamic);  // [groups][THREADS]
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const int tid = threadIdx.x;
+  const uint32_t C = p.C;
+  const int64_t row = cluster_id();
+  const uint32_t rank = C > 1 ? cluster_rank() : 0u;
+  const Sp sp(p, row, rank);
+  const int N = p.N;
+  if (C > 1) cluster_arrive_relaxed();  // every CTA of the cluster runs before its memory is written
+  if (tid == 0) {
+    count = 0;
+    ranked = 0ull;
+  }
+  // the first token's logit, for its rank; this thread's own token
+  int64_t t0 = -1;
+  bool counts = false;
+  Above ab = {};
+  if (p.rank != nullptr) {
+    t0 = p.tokens[row * p.M];
+    if (t0 >= 0 && t0 < p.V) {
+      const float x = sp.value(t0);
+      counts = x > -INFINITY && x < INFINITY;
+      if (counts) {
+        ab = above_of<DT>(x);
+        ab.unit = t0 < sp.head ? -1 : (t0 - sp.head) / U;
+      }
+    }
+  }
+  Running<ENT> run;
+  float top = -INFINITY, group = -INFINITY;
+  unsigned long long before = 0ull;  // logits that precede the token
+  const int64_t n = sp.u_hi - sp.u_lo;
+  const int64_t steps = (n + static_cast<int64_t>(THREADS) * K - 1) / (static_cast<int64_t>(THREADS) * K);
+  int64_t in_group = 0;
+  int g = 0;
+  for (int64_t s = 0; s < steps; ++s) {
+    const int64_t u0 = sp.u_lo + s * (THREADS * K) + tid;
+    if constexpr (MASKED) {
+      // the masks of all units first; logits only where a bit is set
+      uint4 mw[K];
+#pragma unroll
+      for (int k = 0; k < K; ++k)
+        mw[k] = u0 + k * THREADS < sp.u_hi ? load_unit(sp.keep + sp.id(u0 + k * THREADS)) : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+      for (int k = 0; k < K; ++k) {
+        const uint32_t b = kept_bits(mw[k]);
+        if (b == 0u) continue;
+        const int64_t u = u0 + k * THREADS;
+        uint4 w[W];
+        float2 x[U / 2];
+        sp.words(u, b, w);
+        Sp::expand(w, b, x);
+        if (counts) {
+          const float at = u < ab.unit ? ab.below : ab.at;
+          int a = 0;
+#pragma unroll
+          for (int i = 0; i < U / 2; ++i) a += (x[i].x > at) + (x[i].y > at);
+          before += a;
+        }
+        group = fmaxf(group, run.add_unit(x, p.c));
+      }
+    } else {
+      uint4 w[K][W];
+      float2 x[K * U / 2];
+      const bool full = (s + 1) * (THREADS * K) <= n;
+      if (full) {
+#pragma unroll
+        for (int k = 0; k < K; ++k) sp.words(u0 + k * THREADS, 0u, w[k]);
+#pragma unroll
+        for (int k = 0; k < K; ++k) Sp::expand(w[k], 0u, x + k * (U / 2));
+      } else {
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+          w[k][0] = make_uint4(0u, 0u, 0u, 0u);
+          if (u0 + k * THREADS < sp.u_hi) {
+            sp.words(u0 + k * THREADS, 0u, w[k]);
+            Sp::expand(w[k], 0u, x + k * (U / 2));
+          } else {
+#pragma unroll
+            for (int i = 0; i < U / 2; ++i) x[k * (U / 2) + i] = both(-INFINITY);
+          }
+        }
+      }
+      if (counts) {
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+          const int64_t u = u0 + k * THREADS;
+          if (DT == QRITA_DTYPE_BF16) {
+            const uint32_t at = u < ab.unit ? ab.below2 : ab.at2;
+            // (0xFFFF for each half above: what is taken off is -low and (low - high) 2^16)
+            uint32_t a = 0u;
+            const uint32_t q[4] = {w[k][0].x, w[k][0].y, w[k][0].z, w[k][0].w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) a -= bf2_gt_mask(q[i], at);
+            const uint32_t lo = a & 0xFFFFu;
+            if (full || u < sp.u_hi) before += lo + (((a >> 16) + lo) & 0xFFFFu);
+          } else {
+            const float at = u < ab.unit ? ab.below : ab.at;
+            int a = 0;
+#pragma unroll
+            for (int i = 0; i < U / 2; ++i) a += (x[k * (U / 2) + i].x > at) + (x[k * (U / 2) + i].y > at);
+            before += a;
+          }
+        }
+      }
+      group = fmaxf(group, run.add_unit(x, p.c));
+    }
+    if (N > 0 && (++in_group == p.group_steps || s + 1 == steps)) {
+      gmax[g * THREADS + tid] = group;
+      top = fmaxf(top, group);
+      group = -INFINITY;
+      in_group = 0;
+      ++g;
+    }
+  }
+  const int groups = g;
+  // the row's head and tail
+  int64_t end_j = -1;
+  float end_x = -INFINITY;
+  if (sp.ends && tid < Sp::kEnds) end_j = sp.end_index(tid);
+  if (end_j >= 0) {
+    end_x = sp.value(end_j);
+    run.add_one(end_x, p.c);
+    top = fmaxf(top, end_x);
+    if (counts) before += end_x > ab.at || (end_x == ab.at && end_j < t0);
+  }
+  // equal logits before the token in its own unit
+  if (counts && tid == THREADS - 1 && ab.unit >= sp.u_lo && ab.unit < sp.u_hi)
+    for (int64_t j = sp.id(ab.unit); j < t0; ++j) before += sp.value(j) == ab.at;
+  put_stat(run, slots);
+  tops[tid] = top;
+  if (p.rank != nullptr) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) before += __shfl_xor_sync(kAll, before, o);
+  }
+  __syncthreads();
+  if (p.rank != nullptr && (tid & 31) == 0 && before != 0ull) atomicAdd(&ranked, before);
+  Stat st;
+  if (tid < 32) st = warp_stat<THREADS, ENT>(p.c, slots);
+  if (C > 1) {
+    cluster_wait();
+    if (tid < 32) send_stat<ENT>(st, rank, C, slots.ranks);
+  }
+  int c = 0;
+  if (N > 0) {
+    // the N-th largest of the threads' maxima
+    int r = 0;
+    for (int j = 0; j < THREADS; ++j) r += tops[j] > top || (tops[j] == top && j < tid);
+    if (r == N - 1) bound = top;
+    __syncthreads();
+    const float least = bound;
+    auto push = [&](float x, int64_t id) {
+      if (x >= least && x > -INFINITY) {
+        const int at = atomicAdd(&count, 1);
+        if (at < kListCap) list[at] = order_key(x, id);
+      }
+    };
+    if (end_j >= 0) push(end_x, end_j);
+    for (int i = 0; i < groups; ++i) {
+      const float m = gmax[i * THREADS + tid];
+      if (!(m >= least) || m == -INFINITY) continue;
+      const int64_t s0 = i * p.group_steps, s1 = min(s0 + p.group_steps, steps);
+      for (int64_t s = s0; s < s1; ++s)
+        for (int k = 0; k < K; ++k) {
+          const int64_t u = sp.u_lo + s * (THREADS * K) + k * THREADS + tid;
+          if (u >= sp.u_hi) break;
+          uint4 w[W];
+          float2 x[U / 2];
+          const uint32_t b = sp.bits(u);
+          sp.words(u, b, w);
+          Sp::expand(w, b, x);
+#pragma unroll
+          for (int j = 0; j < U / 2; ++j) {
+            push(x[j].x, sp.id(u) + 2 * j);
+            push(x[j].y, sp.id(u) + 2 * j + 1);
+          }
+        }
+    }
+    __syncthreads();
+    c = count;
+    if (c > kListCap) {
+      // more than fits: again, two logits of a thread at a time, the list cut to its
+      // first N whenever the next step might not fit
+      __syncthreads();
+      if (tid == 0) count = 0;
+      unsigned long long above = (static_cast<unsigned long long>(f2key(least)) << 32) - 1ull;  // keys beyond it count
+      __syncthreads();
+      auto put = [&](float x, int64_t id) {
+        const unsigned long long key = order_key(x, id);
+        if (x > -INFINITY && key > above) list[atomicAdd(&count, 1)] = key;
+      };
+      auto cut = [&](int room) {
+        __syncthreads();
+        const int have = count;
+        __syncthreads();  // (the next entries change it)
+        if (have <= room) return;
+        first_of<THREADS>(list, have, N, first);
+        __syncthreads();
+        for (int i = tid; i < min(have, N); i += THREADS) list[i] = first[i];
+        if (tid == 0) count = min(have, N);
+        if (have >= N) above = first[N - 1];
+        __syncthreads();
+      };
+      constexpr int kRoom = kListCap - 2 * THREADS;
+      if (end_j >= 0) put(end_x, end_j);
+      for (int i = 0; i < groups; ++i) {
+        const int64_t s0 = i * p.group_steps, s1 = min(s0 + p.group_steps, steps);
+        const float m = gmax[i * THREADS + tid];
+        const bool some = m > -INFINITY && order_key(m, sp.id(sp.u_lo + s0 * (THREADS * K) + tid)) > above;
+        if (!__syncthreads_or(some)) continue;
+        for (int64_t s = s0; s < s1; ++s)
+          for (int k = 0; k < K; ++k) {
+            const int64_t u = sp.u_lo + s * (THREADS * K) + k * THREADS + tid;
+            const bool mine = some && u < sp.u_hi;
+            for (int j = 0; j < U; j += 2) {
+              cut(kRoom);
+              if (mine) {
+                put(sp.value(sp.id(u) + j), sp.id(u) + j);
+                put(sp.value(sp.id(u) + j + 1), sp.id(u) + j + 1);
+              }
+            }
+          }
+      }
+      __syncthreads();
+      c = count;
+    }
+    if (tid < N) first[tid] = 0ull;
+    __syncthreads();
+    first_of<THREADS>(list, c, N, first);
+  }
+  __syncthreads();
+  if (C > 1) {
+    cluster_sync_all();  // every CTA's sums, list and count are there
+    if (rank != 0) {  // rank 0 reads this CTA's memory until the next barrier
+      cluster_arrive_relaxed();
+      cluster_wait();
+      return;
+    }
+    if (tid < 32) st = merge_ranks<ENT>(C, p.c, slots.ranks);
+    if (p.rank != nullptr && tid > 0 && tid < static_cast<int>(C)) {
+      const uint32_t at = map_rank(smem_u32(&ranked), tid);
+      const unsigned long long more = static_cast<unsigned long long>(ld_dsmem_u32(at + 4)) << 32 | ld_dsmem_u32(at);
+      if (more != 0ull) atomicAdd(&ranked, more);
+    }
+  }
+  if (tid == 0) {
+    const bool empty = st.s.hi == 0.f;
+    const F2 S = sum_of(st);
+    const F2 ln_s = empty ? f2_make(0.f, 0.f) : ln_pair(S);
+    row_of[0] = st.m;
+    row_of[1] = st.s.hi;
+    row_of[2] = ln_s.hi;
+    row_of[3] = ln_s.lo;
+    row_of[4] = ENT && !empty ? f2_float(f2_sub(ln_s, mean_exponent(S, st.t))) : 0.f;
+  }
+  // the cluster's lists, one after another in the groups' place
+  unsigned long long* lists = reinterpret_cast<unsigned long long*>(dynamic);
+  if (N > 0 && C > 1) {
+    for (int i = tid; i < static_cast<int>(C) * N; i += THREADS) {
+      const uint32_t at = map_rank(smem_u32(&first[i % N]), i / N);
+      lists[i] = static_cast<unsigned long long>(ld_dsmem_u32(at + 4)) << 32 | ld_dsmem_u32(at);
+    }
+  }
+  __syncthreads();
+  if (C > 1) cluster_arrive();  // (the other CTAs may end)
+  const float m = row_of[0], total = row_of[1];
+  const F2 ln_s = f2_make(row_of[2], row_of[3]);
+  const bool nan = total != total;
+  auto score = [&](float x) {  // of a kept token
+    if (nan) return total;
+    return total == 0.f || x == -INFINITY ? -INFINITY : f2_float(logp_of(x, m, ln_s, p.inv_t, p.inv_t_lo));
+  };
+  float lp0 = 0.f;
+  for (int i = tid; i < p.M; i += THREADS) {
+    const int64_t t = p.tokens[row * p.M + i];
+    float lp = 0.f;
+    if (t >= 0 && t < p.V) lp = score(sp.value(t));
+    p.logp[row * p.M + i] = lp;
+    if (i == 0) lp0 = lp;
+  }
+  if (tid == 0) {
+    if (p.rank != nullptr)
+      p.rank[row] = counts && !nan && lp0 > -INFINITY ? static_cast<int32_t>(ranked) : -1;
+    if (ENT) p.entropy[row] = nan ? total : row_of[4];
+  }
+  if (N > 0) {
+    auto put = [&](int at, unsigned long long key) {
+      const float x = key2f(static_cast<uint32_t>(key >> 32));
+      p.top_ids[row * N + at] = key == 0ull || nan ? -1 : static_cast<int32_t>(0xFFFFFFFFu - static_cast<uint32_t>(key));
+      p.top_logp[row * N + at] = nan ? total : key == 0ull ? -INFINITY : score(x);
+    };
+    if (C == 1) {
+      if (tid < N) put(tid, first[tid]);
+    } else {
+      int have = 0;
+      for (int i = tid; i < static_cast<int>(C) * N; i += THREADS) {
+        const unsigned long long key = lists[i];
+        if (key == 0ull) continue;
+        int at = i % N;
+        for (int l = 0; l < static_cast<int>(C); ++l) {
+          if (l == i / N) continue;
+          // keys of list l above this one (its first `lo`)
+          int lo = 0, hi = N;
+          while (lo < hi) {
+            const int mid = (lo + hi) / 2;
+            if (lists[l * N + mid] > key)
+              lo = mid + 1;
+            else
+              hi = mid;
+          }
+          at += lo;
+        }
+        if (at < N) {
+          put(at, key);
+          have = max(have, at + 1);
+        }
+      }
+      // what the row has too few logits for
+      if (tid == 0) count = 0;
+      __syncthreads();
+      if (have > 0) atomicMax(&count, have);
+      __syncthreads();
+      for (int i = count + tid; i < N; i += THREADS) put(i, 0ull);
+    }
+  }
+  if (C > 1) cluster_wait();
+}
+
+template <int DT, bool ENT, bool MASKED>
+cudaError_t launch_scores_of(const ScoreParams& p, cudaStream_t st) {
+  constexpr int U = kUnitOf<DT, MASKED>, K = kStep<DT, MASKED>;
+  const int64_t bytes = p.V * (MASKED ? 1 : Elem<DT>::kBytes);
+  const uint32_t C = row_ctas(p.B, bytes, false, kLossBlocks);
+  const bool small = C == 1 && bytes <= kShortRow;
+  const int threads = small ? kScoreThreads / 2 : kScoreThreads;
+  ScoreParams q = p;
+  q.C = C;
+  const int64_t units = p.V / U;
+  q.per = (units + C - 1) / C;
+  const int64_t steps = (q.per + threads * K - 1) / (threads * K);
+  q.group_steps = steps <= kGroups ? 1 : (steps + kGroups - 1) / kGroups;
+  size_t smem = 0;
+  if (p.N > 0) {
+    smem = static_cast<size_t>((steps + q.group_steps - 1) / q.group_steps) * threads * sizeof(float);
+    const size_t lists = static_cast<size_t>(C) * p.N * 8u;
+    if (C > 1 && lists > smem) smem = lists;
+  }
+  static_assert(kGroups * kScoreThreads * 4 + 15 * 1024 <= 48 * 1024, "a kernel that does not ask has 48 KB");
+  static_assert(kMaxRanks * kMaxTop * 8 <= kGroups * kScoreThreads * 4, "the lists fit in the groups' place");
+  const unsigned grid = static_cast<unsigned>(p.B * C);
+  if (small) return launch(&score_kernel<kScoreThreads / 2, DT, ENT, MASKED>, grid, threads, C, st, smem, q);
+  return launch(&score_kernel<kScoreThreads, DT, ENT, MASKED>, grid, threads, C, st, smem, q);
+}
+
+template <int DT>
+cudaError_t launch_scores_type(const ScoreParams& p, cudaStream_t st) {
+  if (p.mask != nullptr)
+    return p.entropy != nullptr ? launch_scores_of<DT, true, true>(p, st) : launch_scores_of<DT, false, true>(p, st);
+  return p.entropy != nullptr ? launch_scores_of<DT, true, false>(p, st) : launch_scores_of<DT, false, false>(p, st);
+}
+
+}  // namespace
+
+int launch_scores(const ScoreParams& p, int dtype, qrita_stream_t stream) {
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  return static_cast<int>(dtype == QRITA_DTYPE_F32 ? launch_scores_type<QRITA_DTYPE_F32>(p, st)
+                                                   : launch_scores_type<QRITA_DTYPE_BF16>(p, st));
+}
+
+}  // namespace qrita
