@@ -496,6 +496,113 @@ int qrita_token_scores_grad(const void* logits, int dtype, int64_t B, int64_t V,
                             const float* grad_entropy, void* out_grad, int64_t ld_grad, qrita_stream_t stream);
 
 /*
+ * The slots of a key-value cache. A sequence's tokens have a slot each in every kv
+ * head, [B, H, S]; attention does not depend on the slots' order, so a full cache
+ * puts its next token over the slot that it can miss best. These entry points
+ * gather each slot's attention weight, keep the slots that a budget allows, and put
+ * one token into a full cache. What is kept is the top of a row of weights in the
+ * library's stable order (Qrita technical summary, "Problem statement": the exact
+ * result of a stable sort), which is exact and does not depend on timing.
+ *
+ * Order of the slots of one sequence and head, first to last: protected slots
+ * before others; then larger weights first (-0 == +0, NaN last); then lower slots.
+ * A slot is protected when its position is below `sink` or one of the `recent` last
+ * ones seen, positions >= seen - recent. (Protected slots beyond a budget go by
+ * the rest of the order.)
+ *
+ * Common arguments (device pointers unless said otherwise):
+ *   B, H, S      sequences, kv heads and slots; S up to 2^31-1, B H up to 2^27.
+ *   lengths      int32[B]: slots [0, lengths[b]) hold tokens, in every head (more
+ *                than there are slots counts as that many). The slots behind them
+ *                are not read. A sequence of negative length is idle.
+ *   weights      float[B, H, S].
+ *   positions    int32[B, H, S]: the position of each slot's token in its sequence,
+ *                not negative; seen int32[B]: positions [0, seen[b]) have been put.
+ *                Both NULL: slot s has position s, and seen is the length.
+ *   strides      host int64 arrays, not negative; a slot's key or value is
+ *                contiguous. Rows of inputs may share memory (an expanded head);
+ *                rows that are written share none, and outputs overlap nothing.
+ * Ownership, streams and errors as qrita_select; QRITA_EINVAL also for sizes,
+ * strides or scalars outside their stated range. Nothing is allocated or kept.
+ * B == 0 launches nothing.
+ */
+
+/*
+ * qrita_cache_weights: what T queries a sequence see, added to their slots' weights.
+ *   weights[b, h, s] = decay weights[b, h, s]
+ *     + sum over t in [0, T), g in [0, G) of softmax over visible s of
+ *       scale query[b, t, h G + g] . keys[b, h, s],
+ * for s < lengths[b]; the others are left as they were. The queries are the last T
+ * tokens seen: query t is at position seen - T + t, and sees the slots of positions
+ * up to its own (all slots, for one query of the newest token). A query that sees no
+ * slot, or only scores of -inf, adds nothing; one whose visible scores hold NaN or
+ * +inf adds NaN to all the slots that it sees. What keys hold elsewhere changes
+ * nothing.
+ *
+ *   query         dtype[B, T, H G, D], strides in elements of the batch, the token
+ *                 and the head; T G up to 8192.
+ *   dtype         QRITA_DTYPE_F32 or QRITA_DTYPE_BF16, of queries and keys.
+ *   keys          dtype[B, H, S, D], strides in elements of the batch, head and
+ *                 slot; D from 1 to 1024.
+ *   scale         finite in fp32 (by value), 1 / sqrt(D) as a rule.
+ *   decay         in [0, 1]; 0 does not read the weights.
+ *
+ * Scores are fp32 sums of exact products, softmax sums fp32. bf16 heads of 32, 64,
+ * 96, 128, 192 or 256 dimensions whose rows are aligned to 16 bytes run on the
+ * tensor cores. One kernel on stream. Idle sequences are left as they were.
+ */
+int qrita_cache_weights(int64_t B, int64_t H, int64_t S, const void* query, int dtype, int32_t T, int32_t G, int32_t D,
+                        const int64_t* query_strides, const void* keys, const int64_t* key_strides, double scale,
+                        double decay, const int32_t* lengths, const int32_t* positions, const int32_t* seen,
+                        float* weights, qrita_stream_t stream);
+
+/*
+ * qrita_cache_evict: the first min(length, budget) slots in order of each sequence
+ * and head, packed into another cache in increasing slot order: a prompt's cache cut
+ * to a budget.
+ *
+ *   budget        >= 1;  sink, recent >= 0.
+ *   keys, values  rows of key_bytes and value_bytes bytes (1 to 2^20, any type) a
+ *                 slot, strides in bytes of the batch, head and slot.
+ *   out_keys, out_values  the same, for slots [0, budget), strides in bytes. They lie
+ *                 apart from keys and values (QRITA_EINVAL where addresses overlap).
+ *   out_S         slots of out_weights and out_positions, >= budget.
+ *   out_weights   float[B, H, out_S];  out_positions int32[B, H, out_S].
+ *   out_slots     int32[B, H, budget]: the kept slots.
+ *   out_lengths   int32[B]: min(length, budget) (0 for an idle sequence).
+ *
+ * Slots from out_lengths[b] up to the budget get rows and weights of 0 and -1 for
+ * position and slot; slots from the budget on are left as they were. Two kernels on
+ * stream.
+ */
+int qrita_cache_evict(int64_t B, int64_t H, int64_t S, const int32_t* lengths, const float* weights,
+                      const int32_t* positions, const int32_t* seen, int32_t budget, int32_t sink, int32_t recent,
+                      const void* keys, int64_t key_bytes, const int64_t* key_strides, const void* values,
+                      int64_t value_bytes, const int64_t* value_strides, void* out_keys, const int64_t* out_key_strides,
+                      void* out_values, const int64_t* out_value_strides, int64_t out_S, float* out_weights,
+                      int32_t* out_positions, int32_t* out_slots, int32_t* out_lengths, qrita_stream_t stream);
+
+/*
+ * qrita_cache_insert: one token a sequence, in place. While a sequence holds fewer
+ * than budget tokens its slot is lengths[b]; then, in each head, the slot that is
+ * last in order. The slot gets the token's key and value, a weight of 0 and the
+ * position seen[b]; then lengths[b] becomes min(lengths[b] + 1, budget) and seen[b]
+ * goes up by one. Idle sequences are left as they were (their out_slots are -1).
+ *
+ *   budget        1 to S;  sink, recent >= 0. positions and seen are required.
+ *   keys, values, key_bytes, value_bytes, strides  as qrita_cache_evict.
+ *   new_keys, new_values  [B, H] rows, strides in bytes of the batch and head.
+ *   out_slots     int32[B, H].
+ *
+ * One kernel on stream.
+ */
+int qrita_cache_insert(int64_t B, int64_t H, int64_t S, int32_t* lengths, int32_t* seen, float* weights,
+                       int32_t* positions, int32_t budget, int32_t sink, int32_t recent, void* keys, int64_t key_bytes,
+                       const int64_t* key_strides, void* values, int64_t value_bytes, const int64_t* value_strides,
+                       const void* new_keys, const int64_t* new_key_strides, const void* new_values,
+                       const int64_t* new_value_strides, int32_t* out_slots, qrita_stream_t stream);
+
+/*
  * qrita_delta_table: copy one of the host-built truncation tables the kernel
  * receives (Qrita technical summary, "Methodology", part 1: delta comes from
  * precomputed tables of the normal quantile function keyed on k or p).

@@ -733,3 +733,176 @@ def qrita_token_scores_grad(logits, ids, grad_logp=None, grad_entropy=None, mask
     if out_grad is not None:
         _wrote(grad)
     return grad
+
+
+# ---------------------------------------------------------------------------
+# The slots of a key-value cache
+# ---------------------------------------------------------------------------
+EvictedCache = namedtuple("EvictedCache", "keys values weights positions slots lengths")
+
+_Strides = ctypes.c_int64 * 3
+
+
+def _cache(t, name, device=None, shape=None):
+    """Strides in bytes and the bytes of a row of a [B, H, S, D] (or [B, H, D])
+    tensor whose rows are contiguous; any type."""
+    if t.dim() not in (3, 4) or not t.is_cuda or (device is not None and t.device != device):
+        raise ValueError(f"{name} must be a CUDA [B, H, S, D] tensor" + (f" on {device}" if device is not None else ""))
+    if shape is not None and t.shape != shape:
+        raise ValueError(f"{name} must be {list(shape)}")
+    e, strides = t.element_size(), t.stride()
+    if t.shape[-1] < 1 or (t.shape[-1] > 1 and strides[-1] != 1):
+        raise ValueError(f"{name}: a row must be contiguous")
+    if t.dim() == 4 and t.shape[2] < 2:
+        strides = (*strides[:2], t.shape[-1], 1)
+    return _Strides(*(v * e for v in strides[:-1])), t.shape[-1] * e
+
+
+def _written(t, name):
+    """Refuses tensors that are written where rows share memory (expanded ones)."""
+    if any(n > 1 and s == 0 for n, s in zip(t.shape, t.stride())):
+        raise ValueError(f"{name} is written: its rows must not share memory")
+
+
+def _order(weights, lengths, positions, seen, B, H, S, device):
+    torch = _torch()
+    if weights is None or weights.shape != (B, H, S):
+        raise ValueError(f"weights must be [{B}, {H}, {S}]")
+    if positions is not None and positions.shape != (B, H, S):
+        raise ValueError(f"positions must be [{B}, {H}, {S}]")
+    if (positions is None) != (seen is None):
+        raise ValueError("positions and seen are given together")
+    return (_at(weights, B * H * S, torch.float32, "weights", device), _needed(lengths, B, torch.int32, "lengths", device),
+            _at(positions, B * H * S, torch.int32, "positions", device), _at(seen, B, torch.int32, "seen", device))
+
+
+def qrita_cache_weights(query, keys, weights, lengths, positions=None, seen=None, scale=None, decay=1.0, stream=None):
+    """Adds what the last T queries of each sequence see to their slots' weights.
+
+    query: CUDA [B, T, H G, D]; keys: [B, H, S, D], float32 or bfloat16 both, any
+    strides with contiguous rows; weights: float32 [B, H, S], written in place
+    (slots below a sequence's length: decay times what they held plus the sum of
+    the softmax weights over the T queries and G heads that share a kv head);
+    lengths: int32 [B], a negative one leaves its sequence alone; positions int32
+    [B, H, S] and seen int32 [B], or neither (slot s holds position s); scale:
+    1 / sqrt(D) where None. Returns weights. include/qrita.h states which slots a
+    query sees.
+    """
+    if stream is not None:
+        return _on_stream(stream, qrita_cache_weights, query, keys, weights, lengths, positions, seen, scale, decay)
+    if query.dim() != 4 or keys.dim() != 4:
+        raise ValueError("query must be [B, T, H G, D] and keys [B, H, S, D]")
+    B, H, S, D = keys.shape
+    T, heads = query.shape[1:3]
+    if query.shape != (B, T, heads, D) or H < 1 or heads < 1 or heads % H or T < 1:
+        raise ValueError("query must be [B, T, H G, D] for keys of [B, H, S, D]")
+    if query.dtype != keys.dtype:
+        raise TypeError("query and keys must have one type")
+    dev = keys.device
+    _cache(keys, "keys")
+    _cache(query, "query", dev)
+    dt = _dtype_code(keys)
+    w, n, at, se = _order(weights, lengths, positions, seen, B, H, S, dev)
+    _call(lib().qrita_cache_weights, dev, B, H, S, query.data_ptr(), dt, T, heads // H, D, _Strides(*query.stride()[:3]),
+          keys.data_ptr(), _Strides(*keys.stride()[:3]), D ** -0.5 if scale is None else scale, decay, n, at, se, w)
+    _wrote(weights)
+    return weights
+
+
+def qrita_cache_evict(keys, values, weights, lengths, budget, sink=0, recent=0, positions=None, seen=None, stream=None,
+                      out=None):
+    """The budget slots of each sequence and head that are first in order, packed
+    into another cache in slot order.
+
+    keys [B, H, S, Dk], values [B, H, S, Dv]: CUDA, any type, contiguous rows;
+    weights float32 [B, H, S]; lengths int32 [B]; positions and seen as
+    qrita_cache_weights. Positions below sink and the `recent` last ones are kept
+    before all others. Returns EvictedCache(keys [B, H, budget, Dk], values, weights
+    [B, H, budget], positions int32 [B, H, budget], slots int32 [B, H, budget],
+    lengths int32 [B]); behind a sequence's length rows and weights are 0, positions
+    and slots -1. ``out`` = such a tuple writes into its tensors, whose caches may
+    have more slots (left as they were).
+    """
+    if stream is not None:
+        return _on_stream(stream, qrita_cache_evict, keys, values, weights, lengths, budget, sink, recent, positions, seen,
+                          None, out)
+    torch = _torch()
+    if keys.dim() != 4:
+        raise ValueError("keys must be [B, H, S, D]")
+    B, H, S, _ = keys.shape
+    dev = keys.device
+    ks, kb = _cache(keys, "keys")
+    vs, vb = _cache(values, "values", dev, (B, H, S, values.shape[-1]))
+    w, n, at, se = _order(weights, lengths, positions, seen, B, H, S, dev)
+    budget = int(budget)
+    if budget < 1 or H < 1 or S < 1:
+        raise ValueError("a cache has heads and slots, and a budget of at least one")
+    if out is None:
+        i32 = torch.int32
+        got = EvictedCache(torch.empty((B, H, budget, keys.shape[3]), dtype=keys.dtype, device=dev),
+                           torch.empty((B, H, budget, values.shape[3]), dtype=values.dtype, device=dev),
+                           torch.empty((B, H, budget), dtype=torch.float32, device=dev),
+                           torch.empty((B, H, budget), dtype=i32, device=dev),
+                           torch.empty((B, H, budget), dtype=i32, device=dev), torch.empty(B, dtype=i32, device=dev))
+    else:
+        got = EvictedCache(*out)
+        if got.keys.dtype != keys.dtype or got.values.dtype != values.dtype:
+            raise TypeError("out keys and values must have the types of keys and values")
+        more = got.keys.shape[2] if got.keys.dim() == 4 else 0
+        if more < budget:
+            raise ValueError(f"out must have at least {budget} slots")
+        _needed(got.weights, B * H * more, torch.float32, "out weights", dev)
+        _needed(got.positions, B * H * more, torch.int32, "out positions", dev)
+        _needed(got.slots, B * H * budget, torch.int32, "out slots", dev)
+        _needed(got.lengths, B, torch.int32, "out lengths", dev)
+        _written(got.keys, "out keys")
+        _written(got.values, "out values")
+    more = got.keys.shape[2]
+    oks, _ = _cache(got.keys, "out keys", dev, (B, H, more, keys.shape[3]))
+    ovs, _ = _cache(got.values, "out values", dev, (B, H, more, values.shape[3]))
+    _call(lib().qrita_cache_evict, dev, B, H, S, n, w, at, se, budget, sink, recent, keys.data_ptr(), kb, ks,
+          values.data_ptr(), vb, vs, got.keys.data_ptr(), oks, got.values.data_ptr(), ovs, more, got.weights.data_ptr(),
+          got.positions.data_ptr(), got.slots.data_ptr(), got.lengths.data_ptr())
+    if out is not None:
+        _wrote(*got)
+    return got
+
+
+def qrita_cache_insert(keys, values, weights, positions, lengths, seen, new_keys, new_values, budget, sink=0, recent=0,
+                       stream=None, out=None):
+    """Puts one token a sequence into a cache, in place: behind its last slot, or,
+    where it holds budget tokens, over each head's slot that is last in order.
+
+    keys [B, H, S, Dk], values [B, H, S, Dv], weights float32 [B, H, S], positions
+    int32 [B, H, S], lengths and seen int32 [B] are all written; new_keys [B, H, Dk],
+    new_values [B, H, Dv]; budget: 1 to S. A sequence of negative length is left
+    alone. Returns the slots, int32 [B, H] (-1 there); ``out`` gives their tensor.
+    """
+    if stream is not None:
+        return _on_stream(stream, qrita_cache_insert, keys, values, weights, positions, lengths, seen, new_keys, new_values,
+                          budget, sink, recent, None, out)
+    torch = _torch()
+    if keys.dim() != 4:
+        raise ValueError("keys must be [B, H, S, D]")
+    B, H, S, _ = keys.shape
+    dev = keys.device
+    ks, kb = _cache(keys, "keys")
+    vs, vb = _cache(values, "values", dev, (B, H, S, values.shape[-1]))
+    _written(keys, "keys")
+    _written(values, "values")
+    if positions is None or seen is None:
+        raise ValueError("positions and seen are required")
+    w, n, at, se = _order(weights, lengths, positions, seen, B, H, S, dev)
+    if new_keys.dtype != keys.dtype or new_values.dtype != values.dtype:
+        raise TypeError("new_keys and new_values must have the types of keys and values")
+    nks, _ = _cache(new_keys, "new_keys", dev, (B, H, keys.shape[3]))
+    nvs, _ = _cache(new_values, "new_values", dev, (B, H, values.shape[3]))
+    if out is None:
+        slots = torch.empty((B, H), dtype=torch.int32, device=dev)
+    else:
+        slots = out
+        _needed(slots, B * H, torch.int32, "out", dev)
+    _call(lib().qrita_cache_insert, dev, B, H, S, n, se, w, at, int(budget), sink, recent, keys.data_ptr(), kb, ks,
+          values.data_ptr(), vb, vs, new_keys.data_ptr(), nks, new_values.data_ptr(), nvs, slots.data_ptr())
+    _wrote(keys, values, weights, positions, lengths, seen, out)
+    return slots

@@ -27,6 +27,9 @@ EXPORTED = (
     "qrita_preference_loss",
     "qrita_token_scores",
     "qrita_token_scores_grad",
+    "qrita_cache_weights",
+    "qrita_cache_evict",
+    "qrita_cache_insert",
     "qrita_delta_table",
     "qrita_strerror",
     "qrita_version",
@@ -77,6 +80,14 @@ def lib() -> ctypes.CDLL:
     L.qrita_token_scores.restype = i32
     L.qrita_token_scores_grad.argtypes = [vp, i32, i64, i64, i64, vp, vp, i32, f64, vp, vp, vp, i64, vp]
     L.qrita_token_scores_grad.restype = i32
+    L.qrita_cache_weights.argtypes = [i64, i64, i64, vp, i32, i32, i32, i32, vp, vp, vp, f64, f64, vp, vp, vp, vp, vp]
+    L.qrita_cache_weights.restype = i32
+    L.qrita_cache_evict.argtypes = [i64, i64, i64, vp, vp, vp, vp, i32, i32, i32, vp, i64, vp, vp, i64, vp, vp, vp, vp, vp,
+                                    i64, vp, vp, vp, vp, vp]
+    L.qrita_cache_evict.restype = i32
+    L.qrita_cache_insert.argtypes = [i64, i64, i64, vp, vp, vp, vp, i32, i32, i32, vp, i64, vp, vp, i64, vp, vp, vp, vp,
+                                     vp, vp, vp]
+    L.qrita_cache_insert.restype = i32
     L.qrita_delta_table.argtypes = [i32, vp, i32]
     L.qrita_delta_table.restype = i32
     L.qrita_strerror.argtypes = [i32]

@@ -1,0 +1,757 @@
+// The slots of a key-value cache that a budget keeps: attention weights gathered
+// for each slot, the selection of the slots to keep with their rows packed, and a
+// full cache's next token put over the slot that is last.
+//
+// The order of slots is the library's stable descending one (Qrita technical
+// summary, gist.science, paper 2602.01518, "Problem statement": the exact result of
+// a stable sort), of the weights, with protected slots before all others: the
+// kept set is exact, equal weights go to the lower slot.
+
+#include <cstddef>
+#include <cstdint>
+
+#include "qrita_cache.h"
+#include "qrita_rows.cuh"
+
+namespace qrita {
+namespace {
+
+constexpr float kLog2e = 1.44269504088896340736f;
+
+// Larger for weights that are kept longer: the order of the numbers, NaN below all
+// of them (0; -inf's is 0x007FFFFF).
+__device__ __forceinline__ uint32_t weight_key(float w) { return w != w ? 0u : f2key(w); }
+
+struct Guard {
+  int32_t sink;
+  int64_t from;  // positions from here on are the last ones seen
+
+  __device__ Guard(const CacheOrder& c, int64_t b, int32_t length) {
+    sink = c.sink;
+    from = static_cast<int64_t>(c.seen != nullptr ? c.seen[b] : length) - c.recent;
+  }
+  __device__ bool holds(int32_t position) const { return position < sink || position >= from; }
+};
+
+__device__ __forceinline__ int32_t length_of(const CacheOrder& c, int64_t b, int64_t most) {
+  return static_cast<int32_t>(min(static_cast<int64_t>(max(c.lengths[b], 0)), most));
+}
+
+// ---------------------------------------------------------------------------
+// Attention weights.
+//
+// For one kv head, x_ri = scale q_r . k_i over the rows r (queries, G heads each)
+// and visible slots i, and w_i = decay w_i + sum_r exp(x_ri - m_r) / sum_j exp(x_rj - m_r).
+// A cluster of CTAs takes a (sequence, kv head), a share of the slots each. First
+// every CTA works out its scores and each row's maximum and sum; these merge through
+// distributed shared memory; then a slot's weight is the sum over its scores, which
+// wait in shared memory where they fit, so that keys are read once, and are worked
+// out again from keys that are in L2 where they do not.
+// ---------------------------------------------------------------------------
+constexpr int kWThreads = 512;
+constexpr int kWWarps = kWThreads / 32;
+constexpr int kMaxRowsAtOnce = 32;
+
+struct RowSum {
+  float m, s;
+};
+
+__device__ __forceinline__ void sum_add(RowSum& a, RowSum b) {
+  const float m = fmaxf(a.m, b.m);
+  if (m == -INFINITY) {  // (sums of 0, or NaN)
+    a.s += b.s;
+    return;
+  }
+  a.s = a.s * ex2((a.m - m) * kLog2e) + b.s * ex2((b.m - m) * kLog2e);
+  a.m = m;
+}
+
+__device__ __forceinline__ void mma_bf16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, "
+      "%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// Scores of a warp's tile of slots against kRows query rows. Each thread has kKeys
+// slots and kQ rows: key(i) within the tile, row(j) within the rows.
+//
+// On the tensor cores (bf16, D a multiple of 32): 16 slots are the rows of a product,
+// 8 query rows its columns. The order of the dimensions within a dot product is
+// free: a thread's 16 bytes of a slot's key serve two products as they are, and the
+// same 16 bytes of a query are its share of the other operand.
+template <int NT, int CHUNKS>
+struct MmaScores {
+  static constexpr int kTile = 16, kRows = 8 * NT, kKeys = 2, kQ = 2 * NT;
+  static constexpr int kD = 32 * CHUNKS;
+  static constexpr int kPitch = kD * 2 + 64;  // bytes of a query row in shared memory
+  uint4 k[2][CHUNKS];
+
+  __device__ static size_t smem_bytes(int) { return kRows * kPitch; }
+  __device__ __forceinline__ static int key(int i) { return ((threadIdx.x & 31) >> 2) + 8 * i; }
+  __device__ __forceinline__ static int row(int j) { return (j >> 1) * 8 + 2 * (threadIdx.x & 3) + (j & 1); }
+  // lanes that share a row's columns differ in their upper three bits
+  static constexpr int kFirstLane = 4;
+
+  __device__ static void put_rows(const WeightParams& p, const unsigned char* q, int r0, int n, unsigned char* smem) {
+    for (int i = threadIdx.x; i < kRows * (kD / 8); i += kWThreads) {
+      const int r = i / (kD / 8), c = i % (kD / 8);
+      uint4 v = make_uint4(0u, 0u, 0u, 0u);
+      if (r < n) {
+        const int64_t t = (r0 + r) / p.G, g = (r0 + r) % p.G;
+        v = load_unit(q + (t * p.q_token + g * p.q_head) * 2 + c * 16);
+      }
+      *reinterpret_cast<uint4*>(smem + r * kPitch + c * 16) = v;
+    }
+  }
+  __device__ __forceinline__ void load(const WeightParams& p, const unsigned char* keys, int64_t first, int64_t end) {
+    const int t = threadIdx.x & 3;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int64_t s = first + key(i);
+      const unsigned char* at = keys + s * p.k_slot * 2 + t * 16;
+#pragma unroll
+      for (int c = 0; c < CHUNKS; ++c)
+        k[i][c] = s < end ? __ldcs(reinterpret_cast<const uint4*>(at + c * 64)) : make_uint4(0u, 0u, 0u, 0u);
+    }
+  }
+  __device__ __forceinline__ void scores(const WeightParams&, const unsigned char* smem, float (&x)[kKeys][kQ]) const {
+    const unsigned char* at = smem + ((threadIdx.x & 31) >> 2) * kPitch + (threadIdx.x & 3) * 16;
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      float c[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int i = 0; i < CHUNKS; ++i) {
+        const uint4 b = *reinterpret_cast<const uint4*>(at + n * 8 * kPitch + i * 64);
+        const uint32_t a0[4] = {k[0][i].x, k[1][i].x, k[0][i].y, k[1][i].y};
+        const uint32_t a1[4] = {k[0][i].z, k[1][i].z, k[0][i].w, k[1][i].w};
+        mma_bf16(c, a0, b.x, b.y);
+        mma_bf16(c, a1, b.z, b.w);
+      }
+      x[0][2 * n] = c[0];
+      x[0][2 * n + 1] = c[1];
+      x[1][2 * n] = c[2];
+      x[1][2 * n + 1] = c[3];
+    }
+  }
+};
+
+// In fp32, of any type and size: a slot a lane, 8 query rows that the warp reads
+// together.
+template <int DT>
+struct FmaScores {
+  static constexpr int kTile = 32, kRows = 8, kKeys = 1, kQ = 8;
+  static constexpr int kFirstLane = 1;
+  const unsigned char* at;
+  bool live;
+
+  __device__ __forceinline__ static int key(int) { return threadIdx.x & 31; }
+  __device__ __forceinline__ static int row(int j) { return j; }
+
+  __device__ static void put_rows(const WeightParams& p, const unsigned char* q, int r0, int n, unsigned char* smem) {
+    float* to = reinterpret_cast<float*>(smem);  // [D][kRows]
+    for (int i = threadIdx.x; i < kRows * p.D; i += kWThreads) {
+      const int r = i % kRows, d = i / kRows;
+      const int64_t t = (r0 + r) / p.G, g = (r0 + r) % p.G;
+      to[i] = r < n ? Elem<DT>::load(q, t * p.q_token + g * p.q_head + d) : 0.f;
+    }
+  }
+  __device__ __forceinline__ void load(const WeightParams& p, const unsigned char* keys, int64_t first, int64_t end) {
+    const int64_t s = first + key(0);
+    live = s < end;
+    at = keys + s * p.k_slot * Elem<DT>::kBytes;
+  }
+  __device__ __forceinline__ void scores(const WeightParams& p, const unsigned char* smem, float (&x)[kKeys][kQ]) const {
+#pragma unroll
+    for (int j = 0; j < kQ; ++j) x[0][j] = 0.f;
+    if (!live) return;
+    const float4* q = reinterpret_cast<const float4*>(smem);
+    constexpr int U = Elem<DT>::kUnit;
+    int d = 0;
+    if ((reinterpret_cast<uintptr_t>(at) & 15u) == 0)
+      for (; d + U <= p.D; d += U) {
+        float2 v[U / 2];
+        Elem<DT>::unpack(load_unit(at + d * Elem<DT>::kBytes), v);
+#pragma unroll
+        for (int i = 0; i < U / 2; ++i) {
+          step(v[i].x, q + 2 * (d + 2 * i), x[0]);
+          step(v[i].y, q + 2 * (d + 2 * i + 1), x[0]);
+        }
+      }
+    for (; d < p.D; ++d) step(Elem<DT>::load(at, d), q + 2 * d, x[0]);
+  }
+  __device__ __forceinline__ static void step(float k, const float4* q, float (&x)[kQ]) {
+    const float4 a = q[0], b = q[1];
+    x[0] = fmaf(k, a.x, x[0]);
+    x[1] = fmaf(k, a.y, x[1]);
+    x[2] = fmaf(k, a.z, x[2]);
+    x[3] = fmaf(k, a.w, x[3]);
+    x[4] = fmaf(k, b.x, x[4]);
+    x[5] = fmaf(k, b.y, x[5]);
+    x[6] = fmaf(k, b.z, x[6]);
+    x[7] = fmaf(k, b.w, x[7]);
+  }
+};
+
+// Scores are kept in natural units, and exponents are formed of their differences.
+template <typename SC, int BYTES>
+__global__ void __launch_bounds__(kWThreads, 1) weights_kernel(const WeightParams p) {
+  extern __shared__ __align__(16) unsigned char dynamic[];
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const uint32_t rank = cluster_rank(), C = p.c.B * p.c.H == 0 ? 1u : gridDim.x / static_cast<uint32_t>(p.c.B * p.c.H);
+  const int64_t bh = cluster_id(), b = bh / p.c.H, h = bh % p.c.H;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int R = p.G * p.T, chunks = (R + p.rows - 1) / p.rows;
+  // dynamic: sums of a chunk's rows by warp, sums of all rows, query rows, scores
+  RowSum* by_warp = reinterpret_cast<RowSum*>(dynamic);
+  RowSum* sums = by_warp + kWWarps * kMaxRowsAtOnce;
+  unsigned char* rows = reinterpret_cast<unsigned char*>(sums + 2 * ((R + 1) / 2));
+  cluster_arrive_relaxed();
+  const bool idle = p.c.lengths[b] < 0;
+  const int32_t n = length_of(p.c, b, p.c.S);
+  const int64_t last = static_cast<int64_t>(p.c.seen != nullptr ? p.c.seen[b] : n) - p.T;  // the first query's position
+  const int64_t per = (static_cast<int64_t>(n) + C - 1) / C;
+  const int64_t share = (per + SC::kTile - 1) / SC::kTile * SC::kTile;
+  const int64_t lo = min(static_cast<int64_t>(n), rank * share), hi = min(static_cast<int64_t>(n), lo + share);
+  const unsigned char* q = static_cast<const unsigned char*>(p.query) + (b * p.q_batch + h * p.G * p.q_head) * BYTES;
+  const unsigned char* keys = static_cast<const unsigned char*>(p.keys) + (b * p.k_batch + h * p.k_head) * BYTES;
+  float* weights = p.c.weights + bh * p.c.S;
+  const int32_t* positions = p.c.positions != nullptr ? p.c.positions + bh * p.c.S : nullptr;
+  const bool stashed = p.stash > 0;
+  float* stash = reinterpret_cast<float*>(rows + p.rows * (sizeof(float) * (p.D + 16)));
+  auto last_of = [&](int r) { return last + r / p.G; };
+  auto position = [&](int64_t s) { return static_cast<int64_t>(positions != nullptr ? positions[s] : s); };
+
+  for (int c = 0; c < chunks; ++c) {
+    const int r0 = c * p.rows, nr = min(p.rows, R - r0);
+    __syncthreads();
+    SC::put_rows(p, q, r0, nr, rows);
+    __syncthreads();
+    RowSum run[SC::kQ];
+#pragma unroll
+    for (int j = 0; j < SC::kQ; ++j) run[j] = {-INFINITY, 0.f};
+    for (int64_t s0 = lo + warp * SC::kTile; s0 < hi; s0 += kWWarps * SC::kTile) {
+      SC sc;
+      float x[SC::kKeys][SC::kQ];
+      sc.load(p, keys, s0, hi);
+      int64_t at[SC::kKeys];
+#pragma unroll
+      for (int i = 0; i < SC::kKeys; ++i) at[i] = s0 + SC::key(i) < hi ? position(s0 + SC::key(i)) : INT64_MAX;
+      sc.scores(p, rows, x);
+#pragma unroll
+      for (int j = 0; j < SC::kQ; ++j) {
+        const int r = SC::row(j);
+        const int64_t see = r < nr ? last_of(r0 + r) : INT64_MIN;
+        float top = run[j].m;
+#pragma unroll
+        for (int i = 0; i < SC::kKeys; ++i) {
+          x[i][j] = at[i] <= see ? x[i][j] * p.scale : -INFINITY;
+          top = fmaxf(top, x[i][j]);
+          if (stashed && r < nr && s0 + SC::key(i) < hi) stash[r * p.stash + static_cast<int>(s0 + SC::key(i) - lo)] = x[i][j];
+        }
+        if (top > run[j].m) {
+          run[j].s *= ex2((run[j].m - top) * kLog2e);
+          run[j].m = top;
+        }
+#pragma unroll
+        for (int i = 0; i < SC::kKeys; ++i)  // (a visible NaN, or one of +inf, makes the sum NaN)
+          if (x[i][j] != -INFINITY) run[j].s += ex2((x[i][j] - run[j].m) * kLog2e);
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < SC::kQ; ++j)
+#pragma unroll
+      for (int o = 16; o >= SC::kFirstLane; o >>= 1) {
+        RowSum other;
+        other.m = __shfl_xor_sync(kAll, run[j].m, o);
+        other.s = __shfl_xor_sync(kAll, run[j].s, o);
+        sum_add(run[j], other);
+      }
+    if (lane < SC::kFirstLane) {
+#pragma unroll
+      for (int j = 0; j < SC::kQ; ++j) by_warp[warp * kMaxRowsAtOnce + SC::row(j)] = run[j];
+    }
+    __syncthreads();
+    if (tid < nr) {
+      RowSum all = by_warp[tid];
+      for (int w = 1; w < kWWarps; ++w) sum_add(all, by_warp[w * kMaxRowsAtOnce + tid]);
+      sums[r0 + tid] = all;
+    }
+  }
+  // the rows' sums over the cluster, in place after everyone has read them
+  cluster_wait();
+  cluster_sync_all();
+  for (int r0 = 0; r0 < R; r0 += kWThreads) {
+    const int r = r0 + tid;
+    RowSum all = {-INFINITY, 0.f};
+    if (r < R)
+      for (uint32_t c = 0; c < C; ++c) {
+        const uint32_t from = map_rank(smem_u32(&sums[r]), c);
+        RowSum other;
+        other.m = ld_dsmem_f32(from);
+        other.s = ld_dsmem_f32(from + 4);
+        sum_add(all, other);
+      }
+    cluster_sync_all();
+    // (only this chunk's entries change, which everyone has read)
+    // (a row that sees nothing, or logits of -inf alone, adds 0)
+    if (r < R) sums[r] = {all.s == 0.f ? 0.f : all.m, all.s == 0.f ? 0.f : 1.f / all.s};
+  }
+  __syncthreads();
+  if (idle) return;
+  if (stashed) {
+    for (int64_t s = lo + tid; s < hi; s += kWThreads) {
+      const int64_t at = position(s);
+      float w = 0.f;
+      for (int r = 0; r < R; ++r)
+        if (at <= last_of(r)) w += ex2((stash[r * p.stash + static_cast<int>(s - lo)] - sums[r].m) * kLog2e) * sums[r].s;
+      weights[s] = p.decay != 0.f ? fmaf(p.decay, weights[s], w) : w;
+    }
+    return;
+  }
+  for (int c = 0; c < chunks; ++c) {
+    const int r0 = c * p.rows, nr = min(p.rows, R - r0);
+    __syncthreads();
+    SC::put_rows(p, q, r0, nr, rows);
+    __syncthreads();
+    for (int64_t s0 = lo + warp * SC::kTile; s0 < hi; s0 += kWWarps * SC::kTile) {
+      SC sc;
+      float x[SC::kKeys][SC::kQ];
+      sc.load(p, keys, s0, hi);
+      sc.scores(p, rows, x);
+#pragma unroll
+      for (int i = 0; i < SC::kKeys; ++i) {
+        const int64_t s = s0 + SC::key(i);
+        const int64_t at = s < hi ? position(s) : INT64_MAX;
+        float w = 0.f;
+#pragma unroll
+        for (int j = 0; j < SC::kQ; ++j) {
+          const int r = SC::row(j);
+          if (r < nr && at <= last_of(r0 + r)) w += ex2((x[i][j] * p.scale - sums[r0 + r].m) * kLog2e) * sums[r0 + r].s;
+        }
+#pragma unroll
+        for (int o = 1; o < SC::kFirstLane; o <<= 1) w += __shfl_xor_sync(kAll, w, o);
+        const float keep = c == 0 ? p.decay : 1.f;
+        if ((lane & (SC::kFirstLane - 1)) == 0 && s < hi) weights[s] = keep != 0.f ? fmaf(keep, weights[s], w) : w;
+      }
+    }
+  }
+}
+
+template <typename SC, int BYTES>
+cudaError_t launch_weights_of(const WeightParams& p, cudaStream_t st) {
+  WeightParams q = p;
+  q.rows = SC::kRows;
+  const int64_t R = static_cast<int64_t>(p.G) * p.T, pairs = p.c.B * p.c.H;
+  const size_t fixed = sizeof(RowSum) * (kWWarps * kMaxRowsAtOnce + 2 * ((R + 1) / 2)) + q.rows * (sizeof(float) * (p.D + 16));
+  constexpr size_t kMost = 200 * 1024;
+  if (fixed > kMost) return cudaErrorInvalidValue;
+  // shares of the slots: enough for the device, and of no more scores than fit
+  uint32_t C = 1;
+  auto floats = [&](uint32_t c) {
+    const int64_t per = (p.c.S + c - 1) / c, share = (per + SC::kTile - 1) / SC::kTile * SC::kTile;
+    return share + (4 - share % 16 + 16) % 16;  // (4 modulo 16: a tile's stores meet no bank twice)
+  };
+  auto fits = [&](uint32_t c) { return R <= q.rows && fixed + static_cast<size_t>(floats(c) * R) * 4 <= kMost; };
+  while (C < kMaxRanks && pairs * 2 * C <= INT32_MAX && p.c.S / (2 * C) >= kWWarps * SC::kTile / 2 &&
+         (pairs * 2 * C <= 2 * device_sms() || (R <= q.rows && !fits(C))))
+    C *= 2;
+  q.stash = fits(C) ? static_cast<int32_t>(floats(C)) : 0;
+  const size_t smem = fixed + static_cast<size_t>(q.stash * R) * 4;
+  auto* fn = &weights_kernel<SC, BYTES>;
+  const cudaError_t e = cudaFuncSetAttribute(reinterpret_cast<const void*>(fn), cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             static_cast<int>(kMost));
+  if (e != cudaSuccess) return e;
+  return launch(fn, static_cast<unsigned>(pairs * C), kWThreads, C, st, smem, q);
+}
+
+template <int CHUNKS>
+cudaError_t launch_weights_mma(const WeightParams& p, cudaStream_t st) {
+  const int64_t R = static_cast<int64_t>(p.G) * p.T;
+  if (R <= 8) return launch_weights_of<MmaScores<1, CHUNKS>, 2>(p, st);
+  if (R <= 16) return launch_weights_of<MmaScores<2, CHUNKS>, 2>(p, st);
+  return launch_weights_of<MmaScores<4, CHUNKS>, 2>(p, st);
+}
+
+// ---------------------------------------------------------------------------
+// Eviction: the kept slots of each (sequence, kv head), then their rows.
+// ---------------------------------------------------------------------------
+constexpr int kSelThreads = 512;
+constexpr int kSelWarps = kSelThreads / 32;
+constexpr int kBins = 256;
+constexpr int kMaxShare = 48 * 1024;  // keys a CTA keeps in shared memory
+
+// Selection of the first `keep` slots in order: the keep-th largest key by four
+// histograms of 8 bits (integers: any order of the atomics gives the same), then the
+// slots above it and the first of those equal to it, in slot order.
+__global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictParams p) {
+  extern __shared__ __align__(16) unsigned char dynamic[];
+  uint32_t* own = reinterpret_cast<uint32_t*>(dynamic);
+  __shared__ uint32_t hist[kBins];
+  __shared__ uint32_t all[kBins];
+  __shared__ uint32_t counts[2];           // this CTA's protected slots; chosen bin
+  __shared__ uint32_t above_of, digit_of;
+  __shared__ uint32_t warp_more[kSelWarps], warp_same[kSelWarps];
+  __shared__ uint32_t tally[2];            // this CTA's slots above the boundary, and equal to it
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const uint32_t rank = cluster_rank(), C = gridDim.x / static_cast<uint32_t>(p.c.B * p.c.H);
+  const int64_t bh = cluster_id(), b = bh / p.c.H;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int32_t n = length_of(p.c, b, p.c.S);
+  const int32_t keep = min(n, p.c.budget);
+  const Guard guard(p.c, b, n);
+  const float* weights = p.c.weights + bh * p.c.S;
+  const int32_t* positions = p.c.positions != nullptr ? p.c.positions + bh * p.c.S : nullptr;
+  const int64_t row = bh * p.out_slots_of;
+  int32_t* slots = p.out_slots + bh * p.c.budget;
+  auto write = [&](int32_t at, int32_t s) {
+    slots[at] = s;
+    p.out_weights[row + at] = weights[s];
+    p.out_positions[row + at] = positions != nullptr ? positions[s] : s;
+  };
+  if (rank == 0) {
+    if (bh % p.c.H == 0 && tid == 0) p.out_lengths[b] = keep;
+    for (int32_t i = keep + tid; i < p.c.budget; i += kSelThreads) {
+      slots[i] = -1;
+      p.out_weights[row + i] = 0.f;
+      p.out_positions[row + i] = -1;
+    }
+  }
+  if (n <= p.c.budget) {  // (the same in every CTA of the cluster)
+    for (int32_t i = rank * kSelThreads + tid; i < n; i += C * kSelThreads) write(i, i);
+    return;
+  }
+  cluster_arrive_relaxed();  // every CTA of the cluster runs before its memory is read
+  const int32_t share = (n + static_cast<int32_t>(C) - 1) / static_cast<int32_t>(C);
+  const int32_t lo = min(n, static_cast<int32_t>(rank) * share), hi = min(n, lo + share);
+  const bool kept_here = share <= p.share;
+  auto raw = [&](int32_t s, bool& held) {
+    held = guard.holds(positions != nullptr ? positions[s] : s);
+    return weight_key(weights[s]);
+  };
+  if (tid == 0) counts[0] = 0u;
+  __syncthreads();
+  // protected slots: they are kept, or (more than the budget) the choice is theirs
+  uint32_t mine = 0;
+  for (int32_t s = lo + tid; s < hi; s += kSelThreads) {
+    bool held;
+    const uint32_t k = raw(s, held);
+    if (kept_here) own[s - lo] = held ? 0xFFFFFFFFu : k;
+    mine += held;
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(kAll, mine, o);
+  if (lane == 0 && mine != 0u) atomicAdd(&counts[0], mine);
+  cluster_wait();
+  cluster_sync_all();
+  uint32_t held_all = 0;
+  for (uint32_t c = 0; c < C; ++c) held_all += ld_dsmem_u32(map_rank(smem_u32(&counts[0]), c));
+  const bool crowded = held_all > static_cast<uint32_t>(keep);
+  // the key of slot s: of protected ones above all others, or all others below them
+  auto key = [&](int32_t s) {
+    if (!crowded && kept_here) return own[s - lo];
+    bool held;
+    const uint32_t k = raw(s, held);
+    return crowded ? (held ? max(k, 1u) : 0u) : (held ? 0xFFFFFFFFu : k);
+  };
+  uint32_t prefix = 0, left = static_cast<uint32_t>(keep);  // the boundary's digits so far; its rank among those that share them
+  for (int shift = 24; shift >= 0; shift -= 8) {
+    for (int i = tid; i < kBins; i += kSelThreads) hist[i] = 0u;
+    __syncthreads();
+    for (int32_t s = lo + tid; s < hi; s += kSelThreads) {
+      const uint32_t k = key(s);
+      if (shift == 24 || (k >> (shift + 8)) == prefix) atomicAdd(&hist[(k >> shift) & 255u], 1u);
+    }
+    cluster_sync_all();
+    for (int i = tid; i < kBins; i += kSelThreads) {
+      uint32_t v = 0;
+      for (uint32_t c = 0; c < C; ++c) v += ld_dsmem_u32(map_rank(smem_u32(&hist[i]), c));
+      all[i] = v;
+    }
+    __syncthreads();
+    if (warp == 0) {
+      // 8 bins a lane, the largest first
+      uint32_t v[8], sum = 0;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) sum += v[i] = all[255 - (lane * 8 + i)];
+      uint32_t before = sum;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t up = __shfl_up_sync(kAll, before, o);
+        if (lane >= o) before += up;
+      }
+      before -= sum;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        if (before < left && left <= before + v[i]) {
+          digit_of = 255u - static_cast<uint32_t>(lane * 8 + i);
+          above_of = before;
+        }
+        before += v[i];
+      }
+    }
+    __syncthreads();
+    prefix = prefix << 8 | digit_of;
+    left -= above_of;
+    cluster_sync_all();  // (the histograms have been read)
+  }
+  // slots above the boundary and equal to it: counts by warp, each with its own range
+  const int32_t span = ((hi - lo + kSelWarps - 1) / kSelWarps + 31) / 32 * 32;
+  const int32_t w_lo = min(hi, lo + warp * span), w_hi = min(hi, w_lo + span);
+  uint32_t more = 0, same = 0;
+  for (int32_t s0 = w_lo; s0 < w_hi; s0 += 32) {
+    const int32_t s = s0 + lane;
+    const uint32_t k = s < w_hi ? key(s) : 0u;
+    more += __popc(__ballot_sync(kAll, s < w_hi && k > prefix));
+    same += __popc(__ballot_sync(kAll, s < w_hi && k == prefix));
+  }
+  if (lane == 0) {
+    warp_more[warp] = more;
+    warp_same[warp] = same;
+  }
+  __syncthreads();
+  if (tid == 0) {
+    uint32_t m = 0, e = 0;
+    for (int w = 0; w < kSelWarps; ++w) {
+      m += warp_more[w];
+      e += warp_same[w];
+    }
+    tally[0] = m;
+    tally[1] = e;
+  }
+  cluster_sync_all();
+  uint32_t m0 = 0, e0 = 0;
+  for (uint32_t c = 0; c < rank; ++c) {
+    m0 += ld_dsmem_u32(map_rank(smem_u32(&tally[0]), c));
+    e0 += ld_dsmem_u32(map_rank(smem_u32(&tally[1]), c));
+  }
+  cluster_arrive();
+  for (int w = 0; w < warp; ++w) {
+    m0 += warp_more[w];
+    e0 += warp_same[w];
+  }
+  for (int32_t s0 = w_lo; s0 < w_hi; s0 += 32) {
+    const int32_t s = s0 + lane;
+    const uint32_t k = s < w_hi ? key(s) : 0u;
+    const uint32_t gt = __ballot_sync(kAll, s < w_hi && k > prefix), eq = __ballot_sync(kAll, s < w_hi && k == prefix);
+    const uint32_t below = (1u << lane) - 1u;
+    const uint32_t e = e0 + __popc(eq & below);  // equal ones before this slot
+    const bool kept = (gt >> lane & 1u) != 0u || ((eq >> lane & 1u) != 0u && e < left);
+    if (kept) write(static_cast<int32_t>(m0 + __popc(gt & below) + min(e, left)), s);
+    m0 += __popc(gt);
+    e0 += __popc(eq);
+  }
+  cluster_wait();
+}
+
+// Copies a row of bytes by N threads, in units of 16, 4 or 1 bytes as both ends
+// allow; from null writes zeros.
+template <int UNIT>
+struct UnitOf {
+  using T = uint4;
+};
+template <>
+struct UnitOf<4> {
+  using T = uint32_t;
+};
+template <>
+struct UnitOf<1> {
+  using T = unsigned char;
+};
+
+constexpr int kGatherThreads = 256;
+
+// The kept rows: threads take units of rows in turn, several loads in flight.
+template <int UNIT>
+__device__ __forceinline__ void gather_rows(const CacheRows& from, const CacheRows& to, const EvictParams& p, int64_t bh,
+                                            int64_t first, int64_t count) {
+  using T = typename UnitOf<UNIT>::T;
+  constexpr int kFlight = 4;
+  const int64_t b = bh / p.c.H, h = bh % p.c.H;
+  const uint32_t units = static_cast<uint32_t>(from.bytes / UNIT), total = static_cast<uint32_t>(count) * units;
+  const unsigned char* src = static_cast<const unsigned char*>(from.at) + b * from.batch + h * from.head;
+  unsigned char* dst = static_cast<unsigned char*>(to.at) + b * to.batch + h * to.head;
+  const int32_t* slots = p.out_slots + bh * p.c.budget;
+  for (uint32_t i0 = threadIdx.x; i0 < total; i0 += kFlight * kGatherThreads) {
+    T v[kFlight];
+#pragma unroll
+    for (int k = 0; k < kFlight; ++k) {
+      const uint32_t i = i0 + k * kGatherThreads;
+      v[k] = T{};
+      const int32_t s = i < total ? slots[first + i / units] : -1;
+      if (s >= 0) v[k] = __ldcs(reinterpret_cast<const T*>(src + s * from.slot + static_cast<int64_t>(i % units) * UNIT));
+    }
+#pragma unroll
+    for (int k = 0; k < kFlight; ++k) {
+      const uint32_t i = i0 + k * kGatherThreads;
+      if (i < total) *reinterpret_cast<T*>(dst + (first + i / units) * to.slot + static_cast<int64_t>(i % units) * UNIT) = v[k];
+    }
+  }
+}
+
+__device__ __forceinline__ uint64_t alignment_of(const CacheRows& r) {
+  return static_cast<uint64_t>(reinterpret_cast<uintptr_t>(r.at)) | static_cast<uint64_t>(r.bytes | r.batch | r.head | r.slot);
+}
+
+constexpr int kGatherRows = 64;
+
+__global__ void __launch_bounds__(kGatherThreads) evict_gather_kernel(const EvictParams p) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const int64_t parts = (p.c.budget + kGatherRows - 1) / kGatherRows;
+  const int64_t bh = blockIdx.x / parts, first = blockIdx.x % parts * kGatherRows;
+  const int64_t count = min(static_cast<int64_t>(kGatherRows), p.c.budget - first);
+  const CacheRows& from = blockIdx.y == 0 ? p.key : p.value;
+  const CacheRows& to = blockIdx.y == 0 ? p.out_key : p.out_value;
+  const uint64_t a = alignment_of(from) | alignment_of(to);
+  if ((a & 15u) == 0u)
+    gather_rows<16>(from, to, p, bh, first, count);
+  else if ((a & 3u) == 0u)
+    gather_rows<4>(from, to, p, bh, first, count);
+  else
+    gather_rows<1>(from, to, p, bh, first, count);
+}
+
+// ---------------------------------------------------------------------------
+// One token a sequence: behind the last slot, or over the one that is last in order.
+// ---------------------------------------------------------------------------
+constexpr int kInsThreads = 256;
+
+template <int UNIT>
+__device__ __forceinline__ void copy_row(const unsigned char* from, unsigned char* to, int64_t bytes) {
+  using T = typename UnitOf<UNIT>::T;
+  for (int64_t i = threadIdx.x; i < bytes / UNIT; i += kInsThreads)
+    reinterpret_cast<T*>(to)[i] = reinterpret_cast<const T*>(from)[i];
+}
+
+__device__ __forceinline__ void put_row(const CacheRows& from, const CacheRows& to, int64_t b, int64_t h, int64_t slot) {
+  const unsigned char* src = static_cast<const unsigned char*>(from.at) + b * from.batch + h * from.head;
+  unsigned char* dst = static_cast<unsigned char*>(to.at) + b * to.batch + h * to.head + slot * to.slot;
+  const uint64_t a = reinterpret_cast<uintptr_t>(src) | reinterpret_cast<uintptr_t>(dst) | static_cast<uint64_t>(from.bytes);
+  if ((a & 15u) == 0u)
+    copy_row<16>(src, dst, from.bytes);
+  else if ((a & 3u) == 0u)
+    copy_row<4>(src, dst, from.bytes);
+  else
+    copy_row<1>(src, dst, from.bytes);
+}
+
+// A cluster takes a sequence, its heads in turn; the sequence's length goes up
+// when every CTA has read it.
+__global__ void __launch_bounds__(kInsThreads) insert_kernel(const InsertParams p) {
+  __shared__ unsigned long long least[kInsThreads / 32];
+  __shared__ int32_t chosen;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const uint32_t rank = cluster_rank(), C = gridDim.x / static_cast<uint32_t>(p.c.B);
+  const int64_t b = cluster_id();
+  const int tid = threadIdx.x;
+  const int32_t given = p.c.lengths[b], seen = p.c.seen[b];
+  if (given < 0) {  // (the same in every CTA of the cluster)
+    for (int64_t h = static_cast<int64_t>(rank) * kInsThreads + tid; h < p.c.H; h += static_cast<int64_t>(C) * kInsThreads)
+      p.out_slots[b * p.c.H + h] = -1;
+    return;
+  }
+  const int32_t n = length_of(p.c, b, p.c.budget);
+  const Guard guard(p.c, b, n);
+  for (int64_t h = rank; h < p.c.H; h += C) {
+    const int64_t row = (b * p.c.H + h) * p.c.S;
+    if (n < p.c.budget) {
+      if (tid == 0) chosen = n;
+    } else {
+      unsigned long long low = ~0ull;
+      for (int32_t s = tid; s < n; s += kInsThreads) {
+        const unsigned long long held = guard.holds(p.c.positions[row + s]);
+        const unsigned long long k = held << 63 | static_cast<unsigned long long>(weight_key(p.c.weights[row + s])) << 31 |
+                                     static_cast<unsigned long long>(0x7FFFFFFF - s);
+        low = min(low, k);
+      }
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) low = min(low, __shfl_xor_sync(kAll, low, o));
+      if ((tid & 31) == 0) least[tid >> 5] = low;
+      __syncthreads();
+      if (tid == 0) {
+        for (int w = 1; w < kInsThreads / 32; ++w) low = min(low, least[w]);
+        chosen = 0x7FFFFFFF - static_cast<int32_t>(low & 0x7FFFFFFFull);
+      }
+    }
+    __syncthreads();
+    const int32_t s = chosen;
+    put_row(p.new_key, p.key, b, h, s);
+    put_row(p.new_value, p.value, b, h, s);
+    if (tid == 0) {
+      p.c.weights[row + s] = 0.f;
+      p.c.positions[row + s] = seen;
+      p.out_slots[b * p.c.H + h] = s;
+    }
+    __syncthreads();  // (the next head's slot)
+  }
+  if (C > 1) cluster_sync_all();
+  if (rank == 0 && tid == 0) {
+    p.c.lengths[b] = min(n + 1, p.c.budget);
+    p.c.seen[b] = seen + 1;
+  }
+}
+
+}  // namespace
+
+int launch_cache_weights(const WeightParams& p, int dtype, qrita_stream_t stream) {
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  if (dtype == QRITA_DTYPE_F32) return static_cast<int>(launch_weights_of<FmaScores<QRITA_DTYPE_F32>, 4>(p, st));
+  // rows of 16-byte units on their boundaries, 32 dimensions at a time: the tensor cores
+  const uint64_t a = static_cast<uint64_t>(reinterpret_cast<uintptr_t>(p.query) | reinterpret_cast<uintptr_t>(p.keys)) |
+                     2u * static_cast<uint64_t>(p.q_batch | p.q_token | p.q_head | p.k_batch | p.k_head | p.k_slot);
+  if ((a & 15u) == 0u) {
+    switch (p.D) {
+      case 32: return static_cast<int>(launch_weights_mma<1>(p, st));
+      case 64: return static_cast<int>(launch_weights_mma<2>(p, st));
+      case 96: return static_cast<int>(launch_weights_mma<3>(p, st));
+      case 128: return static_cast<int>(launch_weights_mma<4>(p, st));
+      case 192: return static_cast<int>(launch_weights_mma<6>(p, st));
+      case 256: return static_cast<int>(launch_weights_mma<8>(p, st));
+      default: break;
+    }
+  }
+  return static_cast<int>(launch_weights_of<FmaScores<QRITA_DTYPE_BF16>, 2>(p, st));
+}
+
+int launch_cache_evict(const EvictParams& p, qrita_stream_t stream) {
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  const int64_t pairs = p.c.B * p.c.H;
+  uint32_t C = 1;
+  while (C < kMaxRanks && pairs * 2 * C <= 2 * device_sms() && p.c.S / (2 * C) >= 2 * kSelThreads) C *= 2;
+  EvictParams q = p;
+  const int64_t share = (p.c.S + C - 1) / C;
+  q.share = share <= kMaxShare ? static_cast<int32_t>(share) : 0;
+  const size_t smem = static_cast<size_t>(q.share) * 4;
+  cudaError_t e = cudaFuncSetAttribute(reinterpret_cast<const void*>(&evict_select_kernel),
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxShare * 4);
+  if (e != cudaSuccess) return static_cast<int>(e);
+  e = launch(&evict_select_kernel, static_cast<unsigned>(pairs * C), kSelThreads, C, st, smem, q);
+  if (e != cudaSuccess) return static_cast<int>(e);
+  const int64_t parts = (p.c.budget + kGatherRows - 1) / kGatherRows;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(pairs * parts), 2, 1);
+  cfg.blockDim = dim3(kGatherThreads, 1, 1);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  e = cudaLaunchKernelEx(&cfg, &evict_gather_kernel, q);
+  const cudaError_t last = cudaGetLastError();
+  return static_cast<int>(e != cudaSuccess ? e : last);
+}
+
+int launch_cache_insert(const InsertParams& p, qrita_stream_t stream) {
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  uint32_t C = 1;
+  while (C < 8 && 2 * C <= p.c.H) C *= 2;
+  return static_cast<int>(launch(&insert_kernel, static_cast<unsigned>(p.c.B * C), kInsThreads, C, st, size_t(0), p));
+}
+
+}  // namespace qrita
