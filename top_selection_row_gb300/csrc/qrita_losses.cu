@@ -259,8 +259,9 @@ __device__ __forceinline__ float grad_one(float x, const RowGrad& g, float c) {
 // the sum of g_i over the ids of probability above 0, a logit's own entry is
 //   inv_t (G_j - p_j (a + h (log p_j + H))),  G_j the sum of g_i over i with id j,
 // taken as G_j (1 - p_j) - p_j (a - G_j + ...), 1 - p_j by expm1. A thread keeps the
-// logits of its ids (read before a gradient is written over them); sums of g_i are
-// fp64, in one order.
+// logits of its ids (read before a gradient is written over them), on their way while
+// the row is summed; ids and gradients are read again where they are used, and wait
+// for the last step in the sums' shared memory. Sums of g_i are fp64, in one order.
 struct ManyRow {
   F2 ln_s;
   float m, H, a, h;
@@ -270,43 +271,80 @@ template <int THREADS>
 struct Many {
   static constexpr int kEach = kMaxGradIds / THREADS;
   float x[kEach];  // -inf: its probability is 0, or there is no such id
-  const int32_t* ids;
-  const float* g;
-  int K;
 
-  // Whether any incoming gradient of the row is not 0 (by the whole block); the
-  // warps' sums of g.
-  __device__ __forceinline__ bool load(const LossParams& p, int64_t row, const unsigned char* xrow, int dt, double* sums) {
-    K = p.K;
-    ids = p.tokens + row * K;
-    g = p.g_logp != nullptr ? p.g_logp + row * K : nullptr;
+  // Whether any incoming gradient of the row is not 0 (by the whole block).
+  // `logit` gives the logit of an id in this CTA's share (-inf of one that is not
+  // kept, or lies in another CTA's).
+  template <typename F>
+  __device__ __forceinline__ bool load(const LossParams& p, int64_t row, F logit) {
     bool any = threadIdx.x == 0 && p.g_entropy != nullptr && p.g_entropy[row] != 0.f;
-    double sum = 0.0;
+    int id[kEach];
 #pragma unroll
     for (int i = 0; i < kEach; ++i) {
       const int k = threadIdx.x + i * THREADS;
+      id[i] = -1;
       x[i] = -INFINITY;
-      if (k >= K || g == nullptr) continue;
-      const int64_t id = ids[k];
-      if (id < 0 || id >= p.V) continue;
-      const float gk = g[k];
-      any = any || gk != 0.f;
-      if (p.mask == nullptr || p.mask[row * p.V + id] != 0)
-        x[i] = dt == QRITA_DTYPE_F32 ? Elem<QRITA_DTYPE_F32>::load(xrow, id) : Elem<QRITA_DTYPE_BF16>::load(xrow, id);
-      if (x[i] != -INFINITY) sum += gk;
+      if (k < p.K && p.g_logp != nullptr) {
+        const float g = p.g_logp[row * p.K + k];
+        id[i] = p.tokens[row * p.K + k];
+        if (id[i] >= p.V) id[i] = -1;
+        any = any || (id[i] >= 0 && g != 0.f);
+      }
     }
+    any = __syncthreads_or(any);
+    if (any) {
+#pragma unroll
+      for (int i = 0; i < kEach; ++i)
+        if (id[i] >= 0) x[i] = logit(i, static_cast<int64_t>(id[i]));
+    }
+    return any;
+  }
+
+  // The warps' sums of the gradients of this CTA's ids that have a probability.
+  __device__ __forceinline__ void add_up(const LossParams& p, int64_t row, double* sums) const {
+    double sum = 0.0;
+#pragma unroll
+    for (int i = 0; i < kEach; ++i)
+      if (x[i] != -INFINITY) sum += p.g_logp[row * p.K + threadIdx.x + i * THREADS];
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(kAll, sum, o);
     if ((threadIdx.x & 31) == 0) sums[threadIdx.x >> 5] = sum;
-    return __syncthreads_or(any);
+  }
+
+  // The CTA's own to every CTA of the cluster, before its barrier, by one warp and
+  // after one of the block; every warp's sum is there.
+  __device__ __forceinline__ static void send(const double* sums, uint32_t rank, uint32_t C, double* ranks) {
+    double a = 0.0;
+    for (int i = 0; i < THREADS / 32; ++i) a += sums[i];
+    const uint32_t lane = threadIdx.x & 31;
+    if (lane < C) {
+      const uint32_t at = map_rank(smem_u32(&ranks[rank]), lane);
+      st_dsmem_u32(at, static_cast<uint32_t>(__double2loint(a)));
+      st_dsmem_u32(at + 4, static_cast<uint32_t>(__double2hiint(a)));
+    }
+  }
+
+  // Ids and gradients to shared memory that the sums have left.
+  __device__ __forceinline__ static void keep(const LossParams& p, int64_t row, StatSlots<THREADS>& slots) {
+    static_assert(4 * THREADS >= 2 * kMaxGradIds, "ids and gradients fit in the sums' place");
+    int* ids = reinterpret_cast<int*>(slots.m);
+    float* g = reinterpret_cast<float*>(ids + kMaxGradIds);
+    if (p.g_logp == nullptr) return;
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+      const int k = threadIdx.x + i * THREADS;
+      if (k >= kMaxGradIds) break;
+      ids[k] = k < p.K ? p.tokens[row * p.K + k] : -1;
+      g[k] = k < p.K ? p.g_logp[row * p.K + k] : 0.f;
+    }
   }
 
   // One thread's: the row's gradient weights from its sums.
   template <bool ENT>
   __device__ __forceinline__ static RowGrad weights(const LossParams& p, int64_t row, const Stat& st, const RowVals& v,
-                                                    const double* sums, ManyRow& r) {
+                                                    const double* ranks, ManyRow& r) {
     double a = 0.0;
-    for (int i = 0; i < THREADS / 32; ++i) a += sums[i];
+    for (uint32_t i = 0; i < p.C; ++i) a += ranks[i];
     r.a = static_cast<float>(a);
     r.h = ENT && st.s.hi != 0.f ? p.g_entropy[row] : 0.f;
     r.H = v.H;
@@ -316,24 +354,30 @@ struct Many {
     return row_grad(r.a, r.h, -INFINITY, v.H, v.ln_s, st.m, st.s.hi, p.inv_t);
   }
 
-  // The ids' own entries, of those that `mine` says are this CTA's, over what a
-  // barrier before this has seen written.
-  template <int DT, typename F>
-  __device__ __forceinline__ void write(const LossParams& p, const ManyRow& r, unsigned char* grow, F mine) const {
+  // The entries of this CTA's ids, over what a barrier before this has seen written.
+  template <int DT>
+  __device__ __forceinline__ void write(const LossParams& p, const ManyRow& r, const StatSlots<THREADS>& slots,
+                                        unsigned char* grow) const {
+    const int* ids = reinterpret_cast<const int*>(slots.m);
+    const float* g = reinterpret_cast<const float*>(ids + kMaxGradIds);
 #pragma unroll
     for (int i = 0; i < kEach; ++i) {
-      if (x[i] == -INFINITY) continue;
       const int k = threadIdx.x + i * THREADS;
+      if (x[i] == -INFINITY) continue;
       const int id = ids[k];
-      if (!mine(static_cast<int64_t>(id))) continue;
       float G = 0.f;
-      bool first = true;
-      for (int j = 0; j < K; ++j)
-        if (ids[j] == id) {
-          first = first && j >= k;
-          G += g[j];
-        }
-      if (!first) continue;
+      int first = k;
+      for (int j = 0; j < p.K; j += 4) {  // (behind the last id are ids of -1)
+        const int4 v = *reinterpret_cast<const int4*>(ids + j);
+        const int same[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int n = 0; n < 4; ++n)
+          if (same[n] == id) {
+            first = min(first, j + n);
+            G += g[j + n];
+          }
+      }
+      if (first != k) continue;
       const float lp = f2_float(logp_of(x[i], r.m, r.ln_s, p.inv_t, p.inv_t_lo)), prob = expf(lp);
       float rest = r.a - G;
       if (r.h != 0.f) rest = fmaf(r.h, lp + r.H, rest);
@@ -438,11 +482,11 @@ row_kernel(const LossParams p, RowStat* stats, int op) {
   const Share<DT> sh(p, row, rank);
   RowGrad g = {0.f, 0.f, 0.f, 0.f};
   Many<THREADS> many;
-  __shared__ double many_sums[MANY ? THREADS / 32 : 1];
+  __shared__ double many_sums[MANY ? THREADS / 32 : 1], many_ranks[MANY ? kMaxRanks : 1];
   __shared__ ManyRow many_row;
   bool ignored = false;
   if constexpr (MANY)
-    ignored = !many.load(p, row, sh.x, DT, many_sums);
+    ignored = !many.load(p, row, [&](int, int64_t id) { return sh.owns(id) ? E::load(sh.x, id) : -INFINITY; });
   else
     ignored = token < 0 || token >= p.V;
   if (ignored) {  // (the same in every CTA of the cluster)
@@ -474,12 +518,15 @@ row_kernel(const LossParams p, RowStat* stats, int op) {
     const int64_t j = sh.end_index(threadIdx.x);
     if (j >= 0) run.add_one(E::load(sh.x, j), p.c);
   }
-  const Stat st = row_stat(run, p.c, rank, C, slots);
+  if constexpr (MANY) many.add_up(p, row, many_sums);
+  const Stat st = row_stat(run, p.c, rank, C, slots, [&]() {
+    if constexpr (MANY) Many<THREADS>::send(many_sums, rank, C, many_ranks);
+  });
   RowVals v;
   if (threadIdx.x == 0 && (rank == 0 || p.grad != nullptr)) {
     if constexpr (MANY) {
       v = row_vals<ENT>(p, RowIn{}, st);
-      grad = Many<THREADS>::template weights<ENT>(p, row, st, v, many_sums, many_row);
+      grad = Many<THREADS>::template weights<ENT>(p, row, st, v, many_ranks, many_row);
     } else {
       v = row_vals<ENT>(p, in, st);
       if (p.grad != nullptr || op == kOpPolicy) grad = row_weights<ENT>(p, op, in, st, v);
@@ -489,12 +536,12 @@ row_kernel(const LossParams p, RowStat* stats, int op) {
   if (p.grad == nullptr) return;
   __syncthreads();
   if (!MANY && threadIdx.x == 0 && rank == 0) row_out<ENT>(p, op, stats, row, in, st, v);
+  if constexpr (MANY) many.keep(p, row, slots);
   g = grad;
   write_grad<THREADS, DT, ENT>(p, sh, row, g, token);
   if constexpr (MANY) {
     __syncthreads();
-    many.template write<DT>(p, many_row, static_cast<unsigned char*>(p.grad) + row * p.ld_grad * E::kBytes,
-                            [&](int64_t id) { return sh.owns(id); });
+    many.template write<DT>(p, many_row, slots, static_cast<unsigned char*>(p.grad) + row * p.ld_grad * E::kBytes);
   }
 }
 
@@ -592,11 +639,13 @@ __global__ void __launch_bounds__(THREADS, kLossThreads * kLossBlocks / THREADS)
   };
   if (mapped) fetch(tid);  // (on its way while the token is)
   Many<THREADS> many;
-  __shared__ double many_sums[MANY ? THREADS / 32 : 1];
+  __shared__ double many_sums[MANY ? THREADS / 32 : 1], many_ranks[MANY ? kMaxRanks : 1];
   __shared__ ManyRow many_row;
   bool ignored = false;
   if constexpr (MANY)
-    ignored = !many.load(p, row, xrow, DT, many_sums);
+    ignored = !many.load(p, row, [&](int, int64_t id) {
+      return id >= lo && id < hi && mrow[id] != 0 ? E::load(xrow, id) : -INFINITY;
+    });
   else
     ignored = token < 0 || token >= V;
   if (ignored) {  // (the same in every CTA of the cluster)
@@ -677,6 +726,7 @@ __global__ void __launch_bounds__(THREADS, kLossThreads * kLossBlocks / THREADS)
       if (!(bits >> (2 * i + 1) & 1u)) x[i].y = -INFINITY;
     }
   };
+  if constexpr (MANY) many.add_up(p, row, many_sums);  // (barriers follow)
   Stat st;
   if (listed) {
     float m = -INFINITY;
@@ -748,12 +798,15 @@ __global__ void __launch_bounds__(THREADS, kLossThreads * kLossBlocks / THREADS)
     if (tid < 32) st = warp_stat<THREADS, ENT>(p.c, slots);
   }
   if (C > 1) cluster_wait();
+  if constexpr (MANY) {
+    if (tid < 32) Many<THREADS>::send(many_sums, rank, C, many_ranks);
+  }
   cluster_stat<ENT>(st, p.c, rank, C, slots.ranks);
   RowVals v;
   if (tid == 0 && (rank == 0 || grow != nullptr)) {
     if constexpr (MANY) {
       v = row_vals<ENT>(p, RowIn{}, st);
-      grad = Many<THREADS>::template weights<ENT>(p, row, st, v, many_sums, many_row);
+      grad = Many<THREADS>::template weights<ENT>(p, row, st, v, many_ranks, many_row);
     } else {
       v = row_vals<ENT>(p, in, st);
       if (grow != nullptr || op == kOpPolicy) grad = row_weights<ENT>(p, op, in, st, v);
@@ -763,6 +816,7 @@ __global__ void __launch_bounds__(THREADS, kLossThreads * kLossBlocks / THREADS)
   if (grow == nullptr) return;
   __syncthreads();
   if (!MANY && tid == 0 && rank == 0) row_out<ENT>(p, op, nullptr, row, in, st, v);
+  if constexpr (MANY) many.keep(p, row, slots);
   const RowGrad g = grad;
   const bool zero = g.a == 0.f && g.h == 0.f;
   if (listed) {
@@ -809,7 +863,7 @@ __global__ void __launch_bounds__(THREADS, kLossThreads * kLossBlocks / THREADS)
   }
   if constexpr (MANY) {
     __syncthreads();
-    many.template write<DT>(p, many_row, grow, [&](int64_t id) { return id >= lo && id < hi; });
+    many.template write<DT>(p, many_row, slots, grow);
   } else if (in.kept_t && token >= lo && token < hi) {
     __syncthreads();
     if (tid == 0) E::store(grow, token, g.at);
@@ -932,11 +986,22 @@ __global__ void __launch_bounds__(kResThreads, kResBlocks) resident_kernel(const
   }
   RowGrad g = {0.f, 0.f, 0.f, 0.f};
   Many<kResThreads> many;
-  __shared__ double many_sums[MANY ? kResThreads / 32 : 1];
+  // where this thread's ids lie in the share, in bytes: they are read as their pieces
+  // land (from HBM, 64 of them a row of 512 x 151936 cost 12 us of 61)
+  int many_at[Many<kResThreads>::kEach];
+#pragma unroll
+  for (int i = 0; i < Many<kResThreads>::kEach; ++i) many_at[i] = -1;
+  __shared__ double many_sums[MANY ? kResThreads / 32 : 1], many_ranks[MANY ? kMaxRanks : 1];
   __shared__ ManyRow many_row;
   bool ignored = false;
   if constexpr (MANY)
-    ignored = !many.load(p, row, sh.x, DT, many_sums);
+    ignored = !many.load(p, row, [&](int i, int64_t id) {
+      if (!sh.owns(id)) return -INFINITY;
+      const int64_t u = id - sh.head - sh.u_lo * E::kUnit;
+      if (id < sh.head || id >= sh.head + sh.nu * E::kUnit) return E::load(sh.x, id);
+      many_at[i] = static_cast<int>(u) * E::kBytes;
+      return -INFINITY;
+    });
   else
     ignored = token < 0 || token >= p.V;
   if (ignored) {  // (the same in every CTA of the cluster)
@@ -976,6 +1041,12 @@ __global__ void __launch_bounds__(kResThreads, kResBlocks) resident_kernel(const
     landed = __all_sync(kAll, landed);
     const uint4* at = units + (i % kSlots) * kPieceUnits + tid;
     const int left = n - i * kPieceUnits;
+    if constexpr (MANY) {
+#pragma unroll
+      for (int j = 0; j < Many<kResThreads>::kEach; ++j)
+        if (many_at[j] >= 0 && many_at[j] / kPiece == i)
+          many.x[j] = E::load(units + (i % kSlots) * kPieceUnits, many_at[j] % kPiece / E::kBytes);
+    }
     if (left >= kPieceUnits) {
       uint4 w[kUnroll];
       float2 x[kUnroll * N];
@@ -1002,6 +1073,7 @@ __global__ void __launch_bounds__(kResThreads, kResBlocks) resident_kernel(const
   }
   if (end_j >= 0) run.add_one(end_x, p.c);
   if (!landed) run.s = run.t = NAN;
+  if constexpr (MANY) many.add_up(p, row, many_sums);
   if (MOVED) tmem_put_wait();
   put_stat(run, slots);
   __syncthreads();
@@ -1011,6 +1083,7 @@ __global__ void __launch_bounds__(kResThreads, kResBlocks) resident_kernel(const
     cluster_wait();
     if (warp == 0) {
       send_stat<ENT>(st, rank, C, slots.ranks);
+      if constexpr (MANY) Many<kResThreads>::send(many_sums, rank, C, many_ranks);
       if (MOVED && tid < C) arrive_remote(map_rank(smem_u32(&sent), tid));
     }
     cluster_arrive();
@@ -1021,12 +1094,15 @@ __global__ void __launch_bounds__(kResThreads, kResBlocks) resident_kernel(const
     }
     cluster_wait();
     if (warp == 0) st = merge_ranks<ENT>(C, p.c, slots.ranks);
+  } else if constexpr (MANY) {
+    if (warp == 0) Many<kResThreads>::send(many_sums, 0u, 1u, many_ranks);
+    __syncwarp();
   }
   RowVals v;
   if (tid == 0) {
     if constexpr (MANY) {
       v = row_vals<ENT>(p, RowIn{}, st);
-      grad = Many<kResThreads>::template weights<ENT>(p, row, st, v, many_sums, many_row);
+      grad = Many<kResThreads>::template weights<ENT>(p, row, st, v, many_ranks, many_row);
     } else {
       v = row_vals<ENT>(p, in, st);
       grad = row_weights<ENT>(p, op, in, st, v);
@@ -1034,6 +1110,7 @@ __global__ void __launch_bounds__(kResThreads, kResBlocks) resident_kernel(const
   }
   __syncthreads();
   if (!MANY && tid == 0 && rank == 0) row_out<ENT>(p, op, nullptr, row, in, st, v);
+  if constexpr (MANY) many.keep(p, row, slots);
   __syncwarp();
   g = grad;
   unsigned char* grow = static_cast<unsigned char*>(p.grad) + row * p.ld_grad * E::kBytes;
@@ -1103,7 +1180,7 @@ __global__ void __launch_bounds__(kResThreads, kResBlocks) resident_kernel(const
   }
   if constexpr (MANY) {
     __syncthreads();
-    many.template write<DT>(p, many_row, grow, [&](int64_t id) { return sh.owns(id); });
+    many.template write<DT>(p, many_row, slots, grow);
   }
   if (MOVED) {
     __syncthreads();  // every warp has read its words

@@ -233,6 +233,8 @@ struct Running {
   float lo = 0.f;           // to be added to s
   float limit = -INFINITY;  // an octave above ref; -inf before the first finite logit
 
+  bool lost = false;        // add_unit's
+
   __device__ __forceinline__ float m() const { return limit == -INFINITY ? -INFINITY : ref; }
   __device__ __forceinline__ void raise(float x, const Scale& c) {
     // (the first time the sums are 0, or NaN, whatever the factor)
@@ -257,12 +259,27 @@ struct Running {
     const float y = scaled(x - ref, c);
     const float e = ex2(y);
     add(e);
-    if (ENT) t = fmaf(e, y < kMinExp ? kMinExp : y, t);
+    if (ENT) t = fmaf(e, fmaxf(y, kMinExp), t);
+  }
+  // The part of T of pairs that add_unit has summed last.
+  template <int N>
+  __device__ __forceinline__ void add_exponents(const float2 (&x)[N], const Scale& c) {
+    float sum = 0.f;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const float y0 = scaled(x[i].x - ref, c), y1 = scaled(x[i].y - ref, c);
+      sum = fmaf(ex2(y0), fmaxf(y0, kMinExp), sum);
+      sum = fmaf(ex2(y1), fmaxf(y1, kMinExp), sum);
+    }
+    t += sum;
   }
   // N pairs (a power of two): their own sum first, then one addition to the
   // running one. The more pairs, the more independent exponentials follow
-  // one test of the maximum, which is returned (NaNs ignored).
-  template <int N>
+  // one test of the maximum, which is returned (NaNs ignored). FUSED: their part of
+  // T in two chains of multiply-adds, with no exponent held above the lowest; where a
+  // logit of -inf makes that NaN it is left out, `lost` says so, and the caller
+  // gives add_exponents the same pairs.
+  template <bool FUSED = false, int N>
   __device__ __forceinline__ float add_unit(const float2 (&x)[N], const Scale& c) {
     float top = fmaxf(x[0].x, x[0].y);
 #pragma unroll
@@ -274,17 +291,23 @@ struct Running {
     for (int i = 0; i < N; ++i) {
       const float2 y = fma2(add2(x[i], nr), by, low);
       es[i] = make_float2(ex2(y.x), ex2(y.y));
-      if (ENT) ts[i] = mul2(es[i], make_float2(y.x < kMinExp ? kMinExp : y.x, y.y < kMinExp ? kMinExp : y.y));
+      if (ENT && !FUSED) ts[i] = mul2(es[i], make_float2(fmaxf(y.x, kMinExp), fmaxf(y.y, kMinExp)));  // (NaN by the weight)
+      if (ENT && FUSED) ts[i & 1] = i < 2 ? mul2(es[i], y) : fma2(es[i], y, ts[i & 1]);
+    }
+    if (ENT && FUSED) {
+      const float sum = (ts[0].x + ts[0].y) + (ts[1].x + ts[1].y);
+      lost = sum != sum;
+      if (!lost) t += sum;
     }
 #pragma unroll
     for (int o = N / 2; o > 0; o >>= 1)
 #pragma unroll
       for (int i = 0; i < o; ++i) {
         es[i] = add2(es[i], es[i + o]);
-        if (ENT) ts[i] = add2(ts[i], ts[i + o]);
+        if (ENT && !FUSED) ts[i] = add2(ts[i], ts[i + o]);
       }
     add(es[0].x + es[0].y);
-    if (ENT) t += ts[0].x + ts[0].y;
+    if (ENT && !FUSED) t += ts[0].x + ts[0].y;
     return top;
   }
 };
@@ -331,7 +354,7 @@ constexpr int kMaxRanks = 16;
 
 // Shared memory of row_stat.
 template <int THREADS>
-struct StatSlots {
+struct alignas(16) StatSlots {
   float m[THREADS], s[THREADS], lo[THREADS], t[THREADS];
   Stat ranks[kMaxRanks];
 };
@@ -416,15 +439,17 @@ __device__ __forceinline__ void cluster_stat(Stat& v, const Scale& c, uint32_t r
 }
 
 // The row's sums from every thread's of its cluster of C CTAs, valid in the
-// first warp of every CTA.
-template <int THREADS, bool ENT>
+// first warp of every CTA, which calls `send` before the cluster's barrier.
+template <int THREADS, bool ENT, typename F>
 __device__ __forceinline__ Stat row_stat(const Running<ENT>& r, const Scale& c, uint32_t rank, uint32_t C,
-                                         StatSlots<THREADS>& slots) {
+                                         StatSlots<THREADS>& slots, F send) {
   put_stat(r, slots);
   __syncthreads();
   Stat v;
   if (threadIdx.x < 32) v = warp_stat<THREADS, ENT>(c, slots);
   if (C > 1) cluster_wait();
+  if (threadIdx.x < 32) send();
+  __syncwarp();
   cluster_stat<ENT>(v, c, rank, C, slots.ranks);
   return v;
 }

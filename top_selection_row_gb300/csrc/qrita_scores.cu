@@ -31,6 +31,7 @@ namespace {
 constexpr int kScoreThreads = kLossThreads;
 constexpr int kGroups = 32;     // of a thread, at most
 constexpr int kListCap = 1024;  // candidates of a CTA
+constexpr int kHits = 512;      // groups read again
 
 // Elements of the kernel's units, and the units a thread sums in one step.
 template <int DT, bool MASKED>
@@ -115,12 +116,25 @@ __device__ __forceinline__ unsigned long long order_key(float x, int64_t id) {
   return static_cast<unsigned long long>(f2key(x)) << 32 | (0xFFFFFFFFu - static_cast<uint32_t>(id));
 }
 
+// 1.0 in each half where a > b, and the sum of two such words.
+__device__ __forceinline__ uint32_t bf2_gt(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("set.gt.bf16x2.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+
+__device__ __forceinline__ uint32_t bf2_add(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("add.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+
 // What counts the logits that precede the first token: those above `at`, and above
 // `below` in units before its own. (bf16: both values twice in a word.)
 struct Above {
   float at, below;
   uint32_t at2, below2;
-  int64_t unit;  // the token's
+  int unit;  // the token's, of this CTA's: -1 before its first, the number of them behind its last
 };
 
 template <int DT>
@@ -141,15 +155,27 @@ __device__ __forceinline__ Above above_of(float x) {
   return a;
 }
 
-// The first n of the c listed keys, largest first, to `first`; the block is in step.
+// The first n of the c listed keys, largest first, to `first`, by counting the keys
+// above each: a few lanes a key while there are few of them. The block is in step.
 template <int THREADS>
 __device__ __forceinline__ void first_of(const unsigned long long* list, int c, int n, unsigned long long* first) {
-  for (int i = threadIdx.x; i < c; i += THREADS) {
-    const unsigned long long k = list[i];
+  const int parts = c <= THREADS / 8 ? 8 : c <= THREADS / 4 ? 4 : 1;
+  const int part = threadIdx.x & (parts - 1);
+  for (int i0 = 0; i0 < c; i0 += THREADS / parts) {
+    const int i = i0 + threadIdx.x / parts;
+    const unsigned long long k = i < c ? list[i] : ~0ull;
     int r = 0;
-    for (int j = 0; j < c; ++j) r += list[j] > k;
-    if (r < n) first[r] = k;
+#pragma unroll 4
+    for (int j = part; j < c; j += parts) r += list[j] > k;
+    for (int o = 1; o < parts; o <<= 1) r += __shfl_xor_sync(kAll, r, o);
+    if (i < c && part == 0 && r < n) first[r] = k;
   }
+}
+
+__device__ __forceinline__ unsigned long long ld_dsmem_u64(uint32_t addr) {
+  unsigned long long v;
+  asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(v) : "r"(addr) : "memory");
+  return v;
 }
 
 // HBM bounds it where rows fill the device.
@@ -158,12 +184,13 @@ __global__ void __launch_bounds__(THREADS, kLossThreads * kLossBlocks / THREADS)
   using Sp = Span<DT, MASKED>;
   constexpr int U = Sp::U, K = kStep<DT, MASKED>, W = Sp::W;
   __shared__ StatSlots<THREADS> slots;
-  __shared__ float tops[THREADS];
+  __shared__ __align__(16) float tops[THREADS], quads[THREADS / 4];
   __shared__ unsigned long long list[kListCap];
   __shared__ unsigned long long first[kMaxTop];
-  __shared__ int count;
+  __shared__ unsigned short hits[kHits];
+  __shared__ int count, found;
   __shared__ unsigned long long ranked;
-  __shared__ float bound;
+  __shared__ uint32_t bound;   // key of what the N-th largest logit is at least
   __shared__ float row_of[6];  // m, S (its sign and NaN), ln S as a pair, H
   extern __shared__ __align__(16) unsigned char dynamic[];
   float* gmax = reinterpret_cast<float*>(dynamic);  // [groups][THREADS]
@@ -177,10 +204,17 @@ __global__ void __launch_bounds__(THREADS, kLossThreads * kLossBlocks / THREADS)
   const int N = p.N;
   if (C > 1) cluster_arrive_relaxed();  // every CTA of the cluster runs before its memory is written
   if (tid == 0) {
-    count = 0;
+    count = found = 0;
     ranked = 0ull;
+    bound = 0xFFFFFFFFu;
   }
-  // the first token's logit, for its rank; this thread's own token
+  const int n = static_cast<int>(sp.u_hi - sp.u_lo);  // (a row has fewer than 2^31 logits)
+  // what the first step reads, on its way while the token's logit is looked up
+  if constexpr (!MASKED) {
+#pragma unroll
+    for (int k = 0; k < K; ++k)
+      if (tid + k * THREADS < n) asm volatile("prefetch.global.L2 [%0];" ::"l"(sp.x + sp.id(sp.u_lo + tid + k * THREADS) * Elem<DT>::kBytes));
+  }
   int64_t t0 = -1;
   bool counts = false;
   Above ab = {};
@@ -189,104 +223,124 @@ __global__ void __launch_bounds__(THREADS, kLossThreads * kLossBlocks / THREADS)
     if (t0 >= 0 && t0 < p.V) {
       const float x = sp.value(t0);
       counts = x > -INFINITY && x < INFINITY;
-      if (counts) {
-        ab = above_of<DT>(x);
-        ab.unit = t0 < sp.head ? -1 : (t0 - sp.head) / U;
-      }
+      if (counts) ab = above_of<DT>(x);
+      const int64_t u = t0 < sp.head ? -1 : (t0 - sp.head) / U - sp.u_lo;
+      ab.unit = static_cast<int>(min(max(u, static_cast<int64_t>(-1)), static_cast<int64_t>(n)));
     }
+  }
+  // this thread's given token, whose score waits for the sums
+  float mine = -INFINITY;
+  int32_t my_token = -1;
+  if (rank == 0 && tid < p.M) {
+    my_token = p.tokens[row * p.M + tid];
+    if (my_token >= 0 && my_token < p.V) mine = sp.value(my_token);
   }
   Running<ENT> run;
   float top = -INFINITY, group = -INFINITY;
-  unsigned long long before = 0ull;  // logits that precede the token
-  const int64_t n = sp.u_hi - sp.u_lo;
-  const int64_t steps = (n + static_cast<int64_t>(THREADS) * K - 1) / (static_cast<int64_t>(THREADS) * K);
-  int64_t in_group = 0;
-  int g = 0;
-  for (int64_t s = 0; s < steps; ++s) {
-    const int64_t u0 = sp.u_lo + s * (THREADS * K) + tid;
-    if constexpr (MASKED) {
-      // the masks of all units first; logits only where a bit is set
-      uint4 mw[K];
-#pragma unroll
-      for (int k = 0; k < K; ++k)
-        mw[k] = u0 + k * THREADS < sp.u_hi ? load_unit(sp.keep + sp.id(u0 + k * THREADS)) : make_uint4(0u, 0u, 0u, 0u);
-#pragma unroll
-      for (int k = 0; k < K; ++k) {
-        const uint32_t b = kept_bits(mw[k]);
-        if (b == 0u) continue;
-        const int64_t u = u0 + k * THREADS;
-        uint4 w[W];
-        float2 x[U / 2];
-        sp.words(u, b, w);
-        Sp::expand(w, b, x);
-        if (counts) {
-          const float at = u < ab.unit ? ab.below : ab.at;
-          int a = 0;
-#pragma unroll
-          for (int i = 0; i < U / 2; ++i) a += (x[i].x > at) + (x[i].y > at);
-          before += a;
-        }
-        group = fmaxf(group, run.add_unit(x, p.c));
-      }
-    } else {
-      uint4 w[K][W];
-      float2 x[K * U / 2];
-      const bool full = (s + 1) * (THREADS * K) <= n;
-      if (full) {
-#pragma unroll
-        for (int k = 0; k < K; ++k) sp.words(u0 + k * THREADS, 0u, w[k]);
-#pragma unroll
-        for (int k = 0; k < K; ++k) Sp::expand(w[k], 0u, x + k * (U / 2));
-      } else {
-#pragma unroll
-        for (int k = 0; k < K; ++k) {
-          w[k][0] = make_uint4(0u, 0u, 0u, 0u);
-          if (u0 + k * THREADS < sp.u_hi) {
-            sp.words(u0 + k * THREADS, 0u, w[k]);
-            Sp::expand(w[k], 0u, x + k * (U / 2));
-          } else {
-#pragma unroll
-            for (int i = 0; i < U / 2; ++i) x[k * (U / 2) + i] = both(-INFINITY);
-          }
-        }
-      }
-      if (counts) {
-#pragma unroll
-        for (int k = 0; k < K; ++k) {
-          const int64_t u = u0 + k * THREADS;
-          if (DT == QRITA_DTYPE_BF16) {
-            const uint32_t at = u < ab.unit ? ab.below2 : ab.at2;
-            // (0xFFFF for each half above: what is taken off is -low and (low - high) 2^16)
-            uint32_t a = 0u;
-            const uint32_t q[4] = {w[k][0].x, w[k][0].y, w[k][0].z, w[k][0].w};
-#pragma unroll
-            for (int i = 0; i < 4; ++i) a -= bf2_gt_mask(q[i], at);
-            const uint32_t lo = a & 0xFFFFu;
-            if (full || u < sp.u_hi) before += lo + (((a >> 16) + lo) & 0xFFFFu);
-          } else {
-            const float at = u < ab.unit ? ab.below : ab.at;
-            int a = 0;
-#pragma unroll
-            for (int i = 0; i < U / 2; ++i) a += (x[k * (U / 2) + i].x > at) + (x[k * (U / 2) + i].y > at);
-            before += a;
-          }
-        }
-      }
-      group = fmaxf(group, run.add_unit(x, p.c));
-    }
-    if (N > 0 && (++in_group == p.group_steps || s + 1 == steps)) {
+  uint32_t before = 0u;  // logits that precede the token
+  const int steps = (n + THREADS * K - 1) / (THREADS * K);
+  int in_group = 0, g = 0;
+  auto summed = [&](float t, bool end) {
+    group = fmaxf(group, t);
+    if (N > 0 && (++in_group == p.group_steps || end)) {
       gmax[g * THREADS + tid] = group;
       top = fmaxf(top, group);
       group = -INFINITY;
       in_group = 0;
       ++g;
     }
+  };
+  uint32_t above2 = 0u;
+  auto count_up = [&]() {
+    if (!MASKED && DT == QRITA_DTYPE_BF16) {
+      before += static_cast<uint32_t>(__uint_as_float(above2 << 16)) + static_cast<uint32_t>(__uint_as_float(above2 & 0xFFFF0000u));
+      above2 = 0u;
+    }
+  };
+  auto count_above = [&](const uint4& w, const float2* x, int u) {
+    if (!MASKED && DT == QRITA_DTYPE_BF16) {
+      const uint32_t at = u < ab.unit ? ab.below2 : ab.at2;
+      // (1.0 for each half above, added up in bf16: exact up to 256)
+      const uint32_t a = bf2_add(bf2_add(bf2_gt(w.x, at), bf2_gt(w.y, at)), bf2_add(bf2_gt(w.z, at), bf2_gt(w.w, at)));
+      above2 = bf2_add(above2, a);
+    } else {
+      const float at = u < ab.unit ? ab.below : ab.at;
+#pragma unroll
+      for (int i = 0; i < U / 2; ++i) before += (x[i].x > at) + (x[i].y > at);
+    }
+  };
+  if constexpr (MASKED) {
+    const uint8_t* keep = sp.keep + sp.id(sp.u_lo);
+    for (int s = 0; s < steps; ++s) {
+      // the masks of all units first; logits only where a bit is set
+      const int u0 = s * (THREADS * K) + tid;
+      uint4 mw[K];
+#pragma unroll
+      for (int k = 0; k < K; ++k)
+        mw[k] = u0 + k * THREADS < n ? __ldcs(reinterpret_cast<const uint4*>(keep) + u0 + k * THREADS) : make_uint4(0u, 0u, 0u, 0u);
+      float t = -INFINITY;
+#pragma unroll
+      for (int k = 0; k < K; ++k) {
+        const uint32_t b = kept_bits(mw[k]);
+        if (b == 0u) continue;
+        const int u = u0 + k * THREADS;
+        uint4 w[W];
+        float2 x[U / 2];
+        sp.words(sp.u_lo + u, b, w);
+        Sp::expand(w, b, x);
+        if (counts) count_above(w[0], x, u);
+        t = fmaxf(t, run.add_unit(x, p.c));
+      }
+      summed(t, s + 1 == steps);
+    }
+  } else {
+    const uint4* units = reinterpret_cast<const uint4*>(sp.x + sp.id(sp.u_lo) * Elem<DT>::kBytes) + tid;
+    const int full = n / (THREADS * K);
+    auto again = [&](const uint4* at) {
+      float2 x[U / 2];
+      const uint4 w = load_unit(at);
+      Sp::expand(reinterpret_cast<const uint4(&)[1]>(w), 0u, x);
+      run.add_exponents(x, p.c);
+    };
+    for (int s = 0; s < full; ++s, units += THREADS * K) {
+      uint4 w[K];
+      float2 x[K * U / 2];
+#pragma unroll
+      for (int k = 0; k < K; ++k) w[k] = load_unit(units + k * THREADS);
+#pragma unroll
+      for (int k = 0; k < K; ++k) Sp::expand(reinterpret_cast<const uint4(&)[1]>(w[k]), 0u, x + k * (U / 2));
+      if (counts) {
+#pragma unroll
+        for (int k = 0; k < K; ++k) count_above(w[k], x + k * (U / 2), s * (THREADS * K) + k * THREADS + tid);
+        count_up();
+      }
+      summed(run.template add_unit<true>(x, p.c), s + 1 == steps);
+      if (ENT && run.lost) {  // (logits of -inf)
+#pragma unroll 1
+        for (int k = 0; k < K; ++k) again(units + k * THREADS);
+        run.lost = false;
+      }
+    }
+    if (full < steps) {  // the rest of the units, one at a time
+      float t = -INFINITY;
+      for (int u = full * (THREADS * K) + tid; u < n; u += THREADS, units += THREADS) {
+        float2 x[U / 2];
+        const uint4 w = load_unit(units);
+        Sp::expand(reinterpret_cast<const uint4(&)[1]>(w), 0u, x);
+        if (counts) count_above(w, x, u);
+        t = fmaxf(t, run.template add_unit<true>(x, p.c));
+        if (ENT && run.lost) again(units);
+        run.lost = false;
+      }
+      count_up();
+      summed(t, true);
+    }
   }
   const int groups = g;
   // the row's head and tail
   int64_t end_j = -1;
   float end_x = -INFINITY;
-  if (sp.ends && tid < Sp::kEnds) end_j = sp.end_index(tid);
+  if (sp.ends && THREADS - 1 - tid < Sp::kEnds) end_j = sp.end_index(THREADS - 1 - tid);
   if (end_j >= 0) {
     end_x = sp.value(end_j);
     run.add_one(end_x, p.c);
@@ -294,65 +348,113 @@ __global__ void __launch_bounds__(THREADS, kLossThreads * kLossBlocks / THREADS)
     if (counts) before += end_x > ab.at || (end_x == ab.at && end_j < t0);
   }
   // equal logits before the token in its own unit
-  if (counts && tid == THREADS - 1 && ab.unit >= sp.u_lo && ab.unit < sp.u_hi)
-    for (int64_t j = sp.id(ab.unit); j < t0; ++j) before += sp.value(j) == ab.at;
+  if (counts && tid == THREADS - 1 && ab.unit >= 0 && ab.unit < n)
+    for (int64_t j = sp.id(sp.u_lo + ab.unit); j < t0; ++j) before += sp.value(j) == ab.at;
   put_stat(run, slots);
-  tops[tid] = top;
-  if (p.rank != nullptr) {
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) before += __shfl_xor_sync(kAll, before, o);
+  // maxima of threads, or (few alternatives) of four threads
+  const int maxima = N <= THREADS / 8 ? THREADS / 4 : THREADS;
+  if (N > 0) {
+    tops[tid] = top;
+    if (maxima < THREADS) {
+      float t = fmaxf(top, __shfl_xor_sync(kAll, top, 1));
+      t = fmaxf(t, __shfl_xor_sync(kAll, t, 2));
+      if ((tid & 3) == 0) quads[tid >> 2] = t;
+    }
   }
+  if (p.rank != nullptr) before = __reduce_add_sync(kAll, before);
   __syncthreads();
-  if (p.rank != nullptr && (tid & 31) == 0 && before != 0ull) atomicAdd(&ranked, before);
-  Stat st;
-  if (tid < 32) st = warp_stat<THREADS, ENT>(p.c, slots);
-  if (C > 1) {
-    cluster_wait();
-    if (tid < 32) send_stat<ENT>(st, rank, C, slots.ranks);
+  if (p.rank != nullptr && (tid & 31) == 0 && before != 0u) atomicAdd(&ranked, static_cast<unsigned long long>(before));
+  // the first warp merges the sums while the others look for the alternatives
+  Stat st = {};
+  auto row_values = [&]() {
+    const bool empty = st.s.hi == 0.f;
+    const F2 S = sum_of(st);
+    const F2 ln_s = empty ? f2_make(0.f, 0.f) : ln_pair(S);
+    row_of[0] = st.m;
+    row_of[1] = st.s.hi;
+    row_of[2] = ln_s.hi;
+    row_of[3] = ln_s.lo;
+    row_of[4] = ENT && !empty ? f2_float(f2_sub(ln_s, mean_exponent(S, st.t))) : 0.f;
+  };
+  if (tid < 32) {
+    st = warp_stat<THREADS, ENT>(p.c, slots);
+    if (C > 1) {
+      cluster_wait();
+      send_stat<ENT>(st, rank, C, slots.ranks);
+    } else if (tid == 0) {
+      row_values();
+    }
+  } else {
+    if (C > 1) cluster_wait();
+  }
+  float least = 0.f;
+  auto push = [&](float x, int64_t id) {
+    if (x >= least && x > -INFINITY) {
+      const int at = atomicAdd(&count, 1);
+      if (at < kListCap) list[at] = order_key(x, id);
+    }
+  };
+  if (N > 0 && tid >= 32) {
+    constexpr int kOthers = THREADS - 32;
+    const int wt = tid - 32;
+    auto others_sync = [&]() { asm volatile("bar.sync 1, %0;" ::"n"(kOthers) : "memory"); };
+    // the N-th largest of the maxima: the least of those with fewer than N above
+    const float* of = maxima < THREADS ? quads : tops;
+    uint32_t low = 0xFFFFFFFFu;
+    for (int i = wt; i < maxima; i += kOthers) {
+      const float mine = of[i];
+      int r = 0;
+#pragma unroll 4
+      for (int j = 0; j < maxima; j += 4) {
+        const float4 v = *reinterpret_cast<const float4*>(of + j);
+        r += (v.x > mine) + (v.y > mine) + (v.z > mine) + (v.w > mine);
+      }
+      if (r < N) low = min(low, f2key(mine));
+    }
+    low = __reduce_min_sync(kAll, low);
+    if ((tid & 31) == 0 && low != 0xFFFFFFFFu) atomicMin(&bound, low);
+    others_sync();
+    least = key2f(bound);
+    if (end_j >= 0) push(end_x, end_j);
+    // the groups that reach it, then their units, each by a thread
+    for (int i = wt; i < groups * (THREADS / 4); i += kOthers) {
+      const float4 v = reinterpret_cast<const float4*>(gmax)[i];
+      const float m[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (m[j] >= least && m[j] > -INFINITY) {
+          const int at = atomicAdd(&found, 1);
+          if (at < kHits) hits[at] = static_cast<unsigned short>(4 * i + j);
+        }
+    }
+    others_sync();
+    const int each = p.group_steps * K, tasks = min(found, kHits) * each;
+    for (int i = wt; i < tasks; i += kOthers) {
+      const int hit = hits[i / each];
+      const int u = ((hit / THREADS) * each + i % each) * THREADS + hit % THREADS;
+      if (u >= n) continue;
+      uint4 w[W];
+      float2 x[U / 2];
+      const uint32_t b = sp.bits(sp.u_lo + u);
+      sp.words(sp.u_lo + u, b, w);
+      Sp::expand(w, b, x);
+#pragma unroll
+      for (int j = 0; j < U / 2; ++j) {
+        push(x[j].x, sp.id(sp.u_lo + u) + 2 * j);
+        push(x[j].y, sp.id(sp.u_lo + u) + 2 * j + 1);
+      }
+    }
   }
   int c = 0;
   if (N > 0) {
-    // the N-th largest of the threads' maxima
-    int r = 0;
-    for (int j = 0; j < THREADS; ++j) r += tops[j] > top || (tops[j] == top && j < tid);
-    if (r == N - 1) bound = top;
-    __syncthreads();
-    const float least = bound;
-    auto push = [&](float x, int64_t id) {
-      if (x >= least && x > -INFINITY) {
-        const int at = atomicAdd(&count, 1);
-        if (at < kListCap) list[at] = order_key(x, id);
-      }
-    };
-    if (end_j >= 0) push(end_x, end_j);
-    for (int i = 0; i < groups; ++i) {
-      const float m = gmax[i * THREADS + tid];
-      if (!(m >= least) || m == -INFINITY) continue;
-      const int64_t s0 = i * p.group_steps, s1 = min(s0 + p.group_steps, steps);
-      for (int64_t s = s0; s < s1; ++s)
-        for (int k = 0; k < K; ++k) {
-          const int64_t u = sp.u_lo + s * (THREADS * K) + k * THREADS + tid;
-          if (u >= sp.u_hi) break;
-          uint4 w[W];
-          float2 x[U / 2];
-          const uint32_t b = sp.bits(u);
-          sp.words(u, b, w);
-          Sp::expand(w, b, x);
-#pragma unroll
-          for (int j = 0; j < U / 2; ++j) {
-            push(x[j].x, sp.id(u) + 2 * j);
-            push(x[j].y, sp.id(u) + 2 * j + 1);
-          }
-        }
-    }
     __syncthreads();
     c = count;
-    if (c > kListCap) {
+    if (c > kListCap || found > kHits) {
       // more than fits: again, two logits of a thread at a time, the list cut to its
       // first N whenever the next step might not fit
       __syncthreads();
       if (tid == 0) count = 0;
-      unsigned long long above = (static_cast<unsigned long long>(f2key(least)) << 32) - 1ull;  // keys beyond it count
+      unsigned long long above = (static_cast<unsigned long long>(bound) << 32) - 1ull;  // keys beyond it count
       __syncthreads();
       auto put = [&](float x, int64_t id) {
         const unsigned long long key = order_key(x, id);
@@ -373,11 +475,11 @@ __global__ void __launch_bounds__(THREADS, kLossThreads * kLossBlocks / THREADS)
       constexpr int kRoom = kListCap - 2 * THREADS;
       if (end_j >= 0) put(end_x, end_j);
       for (int i = 0; i < groups; ++i) {
-        const int64_t s0 = i * p.group_steps, s1 = min(s0 + p.group_steps, steps);
+        const int s0 = i * p.group_steps, s1 = min(s0 + p.group_steps, steps);
         const float m = gmax[i * THREADS + tid];
         const bool some = m > -INFINITY && order_key(m, sp.id(sp.u_lo + s0 * (THREADS * K) + tid)) > above;
         if (!__syncthreads_or(some)) continue;
-        for (int64_t s = s0; s < s1; ++s)
+        for (int s = s0; s < s1; ++s)
           for (int k = 0; k < K; ++k) {
             const int64_t u = sp.u_lo + s * (THREADS * K) + k * THREADS + tid;
             const bool mine = some && u < sp.u_hi;
@@ -412,26 +514,33 @@ __global__ void __launch_bounds__(THREADS, kLossThreads * kLossBlocks / THREADS)
       if (more != 0ull) atomicAdd(&ranked, more);
     }
   }
-  if (tid == 0) {
-    const bool empty = st.s.hi == 0.f;
-    const F2 S = sum_of(st);
-    const F2 ln_s = empty ? f2_make(0.f, 0.f) : ln_pair(S);
-    row_of[0] = st.m;
-    row_of[1] = st.s.hi;
-    row_of[2] = ln_s.hi;
-    row_of[3] = ln_s.lo;
-    row_of[4] = ENT && !empty ? f2_float(f2_sub(ln_s, mean_exponent(S, st.t))) : 0.f;
-  }
-  // the cluster's lists, one after another in the groups' place
+  if (C > 1 && tid == 0) row_values();
+  // The cluster's lists, one after another in the groups' place. With q the smallest
+  // number of each list's first entries that makes N together, the least of the q-th
+  // entries has N at or above it; what is above is put in order by counting.
   unsigned long long* lists = reinterpret_cast<unsigned long long*>(dynamic);
   if (N > 0 && C > 1) {
-    for (int i = tid; i < static_cast<int>(C) * N; i += THREADS) {
-      const uint32_t at = map_rank(smem_u32(&first[i % N]), i / N);
-      lists[i] = static_cast<unsigned long long>(ld_dsmem_u32(at + 4)) << 32 | ld_dsmem_u32(at);
-    }
+    const int all = static_cast<int>(C) * N;
+    if (tid >= 32)
+      for (int i = tid - 32; i < all; i += THREADS - 32) lists[i] = ld_dsmem_u64(map_rank(smem_u32(&first[i % N]), i / N));
+    if (tid == 0) count = 0;
+    __syncthreads();
+    cluster_arrive();  // (the other CTAs may end)
+    const int q = (N + static_cast<int>(C) - 1) / static_cast<int>(C), l = tid & 31;
+    unsigned long long low = l < static_cast<int>(C) ? lists[l * N + q - 1] : ~0ull;
+#pragma unroll
+    for (int o = kMaxRanks / 2; o > 0; o >>= 1) low = min(low, __shfl_xor_sync(kAll, low, o));
+    low = max(__shfl_sync(kAll, low, 0), 1ull);
+    unsigned long long* merged = lists + all;
+    for (int i = tid; i < all; i += THREADS)
+      if (lists[i] >= low) merged[atomicAdd(&count, 1)] = lists[i];
+    if (tid < N) first[tid] = 0ull;  // (read by nobody else any more)
+    __syncthreads();
+    first_of<THREADS>(merged, count, N, first);
+  } else if (C > 1) {
+    cluster_arrive();
   }
   __syncthreads();
-  if (C > 1) cluster_arrive();  // (the other CTAs may end)
   const float m = row_of[0], total = row_of[1];
   const F2 ln_s = f2_make(row_of[2], row_of[3]);
   const bool nan = total != total;
@@ -441,9 +550,9 @@ __global__ void __launch_bounds__(THREADS, kLossThreads * kLossBlocks / THREADS)
   };
   float lp0 = 0.f;
   for (int i = tid; i < p.M; i += THREADS) {
-    const int64_t t = p.tokens[row * p.M + i];
+    const int32_t t = i == tid ? my_token : p.tokens[row * p.M + i];
     float lp = 0.f;
-    if (t >= 0 && t < p.V) lp = score(sp.value(t));
+    if (t >= 0 && t < p.V) lp = score(i == tid ? mine : sp.value(t));
     p.logp[row * p.M + i] = lp;
     if (i == 0) lp0 = lp;
   }
@@ -458,39 +567,7 @@ __global__ void __launch_bounds__(THREADS, kLossThreads * kLossBlocks / THREADS)
       p.top_ids[row * N + at] = key == 0ull || nan ? -1 : static_cast<int32_t>(0xFFFFFFFFu - static_cast<uint32_t>(key));
       p.top_logp[row * N + at] = nan ? total : key == 0ull ? -INFINITY : score(x);
     };
-    if (C == 1) {
-      if (tid < N) put(tid, first[tid]);
-    } else {
-      int have = 0;
-      for (int i = tid; i < static_cast<int>(C) * N; i += THREADS) {
-        const unsigned long long key = lists[i];
-        if (key == 0ull) continue;
-        int at = i % N;
-        for (int l = 0; l < static_cast<int>(C); ++l) {
-          if (l == i / N) continue;
-          // keys of list l above this one (its first `lo`)
-          int lo = 0, hi = N;
-          while (lo < hi) {
-            const int mid = (lo + hi) / 2;
-            if (lists[l * N + mid] > key)
-              lo = mid + 1;
-            else
-              hi = mid;
-          }
-          at += lo;
-        }
-        if (at < N) {
-          put(at, key);
-          have = max(have, at + 1);
-        }
-      }
-      // what the row has too few logits for
-      if (tid == 0) count = 0;
-      __syncthreads();
-      if (have > 0) atomicMax(&count, have);
-      __syncthreads();
-      for (int i = count + tid; i < N; i += THREADS) put(i, 0ull);
-    }
+    if (tid < N) put(tid, first[tid]);
   }
   if (C > 1) cluster_wait();
 }
@@ -499,23 +576,37 @@ template <int DT, bool ENT, bool MASKED>
 cudaError_t launch_scores_of(const ScoreParams& p, cudaStream_t st) {
   constexpr int U = kUnitOf<DT, MASKED>, K = kStep<DT, MASKED>;
   const int64_t bytes = p.V * (MASKED ? 1 : Elem<DT>::kBytes);
-  const uint32_t C = row_ctas(p.B, bytes, false, kLossBlocks);
-  const bool small = C == 1 && bytes <= kShortRow;
+  const int64_t sms = device_sms();
+  uint32_t C = 1;
+  if (p.N == 0) {
+    C = row_ctas(p.B, bytes, false, kLossBlocks);
+  } else {
+    // Lists to merge cost more than sums: two CTAs an SM with shares of 20 KB (4 KB of a
+    // mask), four with 100 KB. (4 x 32000 fp32, 20 alternatives: 4 CTAs a row 9.1 us, 16
+    // CTAs 10.3, 2 CTAs 10.0; 64 x 128256 bf16: 4 CTAs 13.0, 8 CTAs 14.9, 2 CTAs 14.6.)
+    while (C < kMaxRanks && p.B * 2 * C <= sms * kLossBlocks &&
+           bytes / (2 * C) >= (p.B * 2 * C > sms * 2 ? 100000 : MASKED ? 4000 : 20000))
+      C *= 2;
+  }
+  // Blocks of half the threads where rows are short, and where one row a block takes
+  // more than a wave: twice as many are on an SM, and a wave ends in the steps of its
+  // blocks that read nothing.
+  const bool small = C == 1 && (bytes <= kShortRow || (p.N > 0 && p.B > sms * kLossBlocks)) && p.N <= kScoreThreads / 8;
   const int threads = small ? kScoreThreads / 2 : kScoreThreads;
   ScoreParams q = p;
   q.C = C;
   const int64_t units = p.V / U;
   q.per = (units + C - 1) / C;
   const int64_t steps = (q.per + threads * K - 1) / (threads * K);
-  q.group_steps = steps <= kGroups ? 1 : (steps + kGroups - 1) / kGroups;
+  q.group_steps = steps <= kGroups ? 1 : static_cast<int>((steps + kGroups - 1) / kGroups);
   size_t smem = 0;
   if (p.N > 0) {
     smem = static_cast<size_t>((steps + q.group_steps - 1) / q.group_steps) * threads * sizeof(float);
-    const size_t lists = static_cast<size_t>(C) * p.N * 8u;
+    const size_t lists = static_cast<size_t>(C) * p.N * 16u;
     if (C > 1 && lists > smem) smem = lists;
   }
-  static_assert(kGroups * kScoreThreads * 4 + 15 * 1024 <= 48 * 1024, "a kernel that does not ask has 48 KB");
-  static_assert(kMaxRanks * kMaxTop * 8 <= kGroups * kScoreThreads * 4, "the lists fit in the groups' place");
+  static_assert(kGroups * kScoreThreads * 4 + 16 * 1024 <= 48 * 1024, "a kernel that does not ask has 48 KB");
+  static_assert(kMaxRanks * kMaxTop * 16 <= kGroups * kScoreThreads * 4, "the lists fit in the groups' place");
   const unsigned grid = static_cast<unsigned>(p.B * C);
   if (small) return launch(&score_kernel<kScoreThreads / 2, DT, ENT, MASKED>, grid, threads, C, st, smem, q);
   return launch(&score_kernel<kScoreThreads, DT, ENT, MASKED>, grid, threads, C, st, smem, q);

@@ -23,7 +23,7 @@ struct ScoreParams {
   float inv_t, inv_t_lo;  // inv_temperature as a pair
   uint32_t C;             // CTAs per row, and the units of it each of them takes
   int64_t per;
-  int64_t group_steps;    // steps of a thread whose largest logit is kept as one
+  int group_steps;        // steps of a thread whose largest logit is kept as one
   float* logp;            // [B, M]
   int32_t* rank;
   float* entropy;
