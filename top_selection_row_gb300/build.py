@@ -18,7 +18,7 @@ CSRC = os.path.join(PKG_DIR, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB_PATH = os.path.join(PKG_DIR, "libqrita.so")
 
-SOURCES = ["qrita_kernel.cu", "qrita_outputs.cu", "qrita_losses.cu", "qrita_scores.cu", "qrita_cache.cu",
+SOURCES = ["qrita_kernel.cu", "qrita_outputs.cu", "qrita_losses.cu", "qrita_scores.cu", "qrita_cache.cu", "qrita_cache_window.cu",
            "qrita_api.cpp", "qrita_losses_api.cpp", "qrita_scores_api.cpp", "qrita_cache_api.cpp"]
 HEADERS = ["qrita_device.cuh", "qrita_internal.h", "qrita_losses.h", "qrita_rows.cuh", "qrita_scores.h",
            "qrita_cache.h"]

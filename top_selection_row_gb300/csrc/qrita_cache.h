@@ -56,6 +56,11 @@ struct InsertParams {
   int32_t* out_slots;  // [B, H]
 };
 
+// Whether qrita_cache_window.cu takes a call (bf16 rows of 16-byte units on their
+// boundaries), and its launches.
+bool window_fits(const WeightParams& prm);
+int launch_cache_window(const WeightParams& prm, qrita_stream_t stream);
+
 // Every launch returns a cudaError_t.
 int launch_cache_weights(const WeightParams& prm, int dtype, qrita_stream_t stream);
 int launch_cache_evict(const EvictParams& prm, qrita_stream_t stream);

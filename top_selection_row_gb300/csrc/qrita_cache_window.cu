@@ -1,0 +1,416 @@
+// Attention weights of a window of queries: more than 32 rows (queries times the
+// heads that share a kv head) at once, on the fifth-generation tensor cores.
+//
+// The formulas are those of qrita_cache.cu's weights_kernel. A cluster of CTAs takes
+// a (sequence, kv head), a share of the slots each, in tiles of 128 slots. Scores are
+// worked out twice, with the operands' roles changed, so that no sum crosses lanes:
+//   first   Q K^T, a query row a lane of tensor memory: its thread keeps the row's
+//           running maximum and sum over the slots;
+//   second  K Q^T, a slot a lane: its thread adds up the slot's weights over the rows,
+//           w = sum_r 2^(c x_r - c m_r) / S_r, c = scale log2 e.
+// Between them the rows' sums merge through distributed shared memory. Both products
+// read the same tiles of shared memory (dimensions contiguous, swizzled over 128
+// bytes). Keys are read again for the second product: a share of a thousand slots is
+// small enough that they come from L2.
+//
+// Warps 0 to 3 are the lanes' threads, warp 4 issues the products, warps 5 and 6 copy.
+// Two accumulators of 128 columns and two stages of keys; CTAs ask for so much shared
+// memory that two at most are on an SM, whose tensor memory holds both: no CTA of
+// these kernels waits for columns that another one holds.
+
+#include <cfloat>
+#include <cstddef>
+#include <cstdint>
+
+#include "qrita_cache.h"
+#include "qrita_rows.cuh"
+
+namespace qrita {
+namespace {
+
+constexpr float kLog2e = 1.44269504088896340736f;
+constexpr int kLanes = 128;              // threads of the epilogues, slots of a tile, rows at most
+constexpr int kWindowThreads = kLanes + 32 + 64;
+constexpr int kCopyThreads = 64;
+constexpr int kColumns = 2 * kLanes;     // of tensor memory: two accumulators
+constexpr int kHalf = kLanes * 128;      // bytes of a tile's 64 dimensions
+constexpr int kStages = 2;
+constexpr uint64_t kWindowLimitNs = 10ull * 1000 * 1000 * 1000;
+
+// Shared-memory operand: rows of 128 bytes, swizzled, eight rows 1024 bytes.
+__device__ __forceinline__ uint64_t operand(uint32_t addr) {
+  return static_cast<uint64_t>((addr & 0x3FFFFu) >> 4) | static_cast<uint64_t>(1) << 16 |
+         static_cast<uint64_t>(1024 >> 4) << 32 | static_cast<uint64_t>(1) << 46 | static_cast<uint64_t>(2) << 61;
+}
+
+// bf16 operands with contiguous dimensions, fp32 accumulators, 128 rows, n columns.
+__device__ __forceinline__ uint32_t product_shape(int n) {
+  return 1u << 4 | 1u << 7 | 1u << 10 | static_cast<uint32_t>(n >> 3) << 17 | static_cast<uint32_t>(kLanes >> 4) << 24;
+}
+
+__device__ __forceinline__ void product(uint32_t d, uint64_t a, uint64_t b, uint32_t shape, bool add) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(shape), "r"(add ? 1u : 0u)
+      : "memory");
+}
+
+// Arrives at bar when every product issued so far is done.
+__device__ __forceinline__ void products_done(uint32_t bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+}
+
+__device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+
+__device__ __forceinline__ void arrive(uint32_t bar) {
+  asm volatile("mbarrier.arrive.release.cta.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+
+// 16 bytes to shared memory, zeros where `some` is false (nothing is read then).
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool some) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(some ? 16u : 0u) : "memory");
+}
+
+// 32 columns of this lane.
+__device__ __forceinline__ void columns32(uint32_t addr, float (&v)[32]) {
+  uint32_t r[32];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(addr)
+      : "memory");
+#pragma unroll
+  for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+}
+
+// Whether `yes` holds in all of the epilogues' threads.
+__device__ __forceinline__ bool lanes_all(bool yes) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbarrier.cta.red.and.pred q, 1, %2, p;\n\tselp.u32 %0, 1, 0, "
+      "q;\n\t}"
+      : "=r"(r)
+      : "r"(yes ? 1u : 0u), "n"(kLanes)
+      : "memory");
+  return r != 0u;
+}
+
+// A row's largest exponent c x and its sum of 2^(c x - top).
+struct WindowSum {
+  float top, s;
+};
+
+struct WindowParams {
+  WeightParams w;
+  int32_t rows, first;  // this launch's rows, and its first query
+};
+
+template <int HALVES>
+__global__ void __launch_bounds__(kWindowThreads, HALVES <= 2 ? 2 : 1) window_kernel(const WindowParams wp) {
+  const WeightParams& p = wp.w;
+  extern __shared__ unsigned char raw[];
+  __shared__ __align__(8) uint64_t full[kStages], empty[kStages], made[2], taken[2];
+  __shared__ WindowSum sums[kLanes];
+  __shared__ float4 row_pairs[kLanes / 2];  // -top of two rows, 1 / S of the two
+  __shared__ int tile_positions[2][kLanes];
+  __shared__ uint32_t tmem_at;
+  __shared__ volatile int failed;  // a bounded wait gave up
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const uint32_t rank = cluster_rank(), C = gridDim.x / static_cast<uint32_t>(p.c.B * p.c.H);
+  const int64_t bh = cluster_id(), b = bh / p.c.H, h = bh % p.c.H;
+  const uint32_t base = (smem_u32(raw) + 1023u) & ~1023u;
+  const uint32_t q_at = base, k_at = base + HALVES * kHalf;
+  const int32_t given = p.c.lengths[b];
+  const int32_t n = static_cast<int32_t>(min(static_cast<int64_t>(max(given, 0)), p.c.S));
+  // (the position of this launch's first query)
+  const int64_t first = static_cast<int64_t>(p.c.seen != nullptr ? p.c.seen[b] : n) - p.T + wp.first;
+  const int64_t per = (static_cast<int64_t>(n) + C - 1) / C;
+  const int64_t share = (per + kLanes - 1) / kLanes * kLanes;
+  const int64_t lo = min(static_cast<int64_t>(n), rank * share), hi = min(static_cast<int64_t>(n), lo + share);
+  const int tiles = static_cast<int>((hi - lo + kLanes - 1) / kLanes);
+  const int R = wp.rows, columns = (R + 15) / 16 * 16;
+  // (above 0, so that what is not seen stays -inf)
+  const float scale = fminf(fmaxf(fabsf(p.scale) * kLog2e, 1e-37f), FLT_MAX);
+  if (tid == 0) {
+    for (int i = 0; i < kStages; ++i) {
+      mbar_init(smem_u32(&full[i]), kCopyThreads);
+      mbar_init(smem_u32(&empty[i]), 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(smem_u32(&made[i]), 1);
+      mbar_init(smem_u32(&taken[i]), kLanes);
+    }
+    fence_mbar_init();
+    failed = 0;
+  }
+  if (warp == 4) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&tmem_at)),
+                 "r"(static_cast<uint32_t>(kColumns))
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    fence_before();
+  }
+  __syncthreads();
+  fence_after();
+  const uint32_t tmem = tmem_at;
+  cluster_sync_all();  // every CTA of the cluster runs before its memory is read
+  auto wait = [&](uint64_t& bar, int use) {  // for the use-th completion (0, 1, ...)
+    if (failed != 0 || !mbar_wait_bounded(smem_u32(&bar), static_cast<uint32_t>(use) & 1u, kWindowLimitNs)) {
+      failed = 1;
+      return false;
+    }
+    return true;
+  };
+
+  if (warp > 4) {
+    // copies: Q once, then the tiles of keys, all of them twice
+    cluster_arrive();
+    const int ct = tid - (kLanes + 32);
+    const unsigned char* q = static_cast<const unsigned char*>(p.query) + (b * p.q_batch + h * p.G * p.q_head) * 2;
+    const unsigned char* keys = static_cast<const unsigned char*>(p.keys) + (b * p.k_batch + h * p.k_head) * 2;
+    constexpr int kChunks = HALVES * 8;
+    for (int i = ct; i < kLanes * kChunks; i += kCopyThreads) {
+      const int r = i / kChunks, c = i % kChunks;
+      const bool some = r < R && c * 8 < p.D;
+      const int64_t t = wp.first + r / p.G, g = r % p.G;
+      copy16(q_at + (c >> 3) * kHalf + r * 128 + (((c & 7) ^ (r & 7)) << 4),
+             some ? q + (t * p.q_token + g * p.q_head) * 2 + c * 16 : q, some);
+    }
+    int told = 0;  // tiles that the products know of
+    auto tell = [&]() {
+      fence_proxy_async_smem();
+      arrive(smem_u32(&full[told % kStages]));
+      ++told;
+    };
+    for (int it = 0; it < 2 * tiles; ++it) {
+      const int stage = it % kStages;
+      if (it >= kStages && !mbar_try_wait(smem_u32(&empty[stage]), static_cast<uint32_t>(it / kStages - 1) & 1u)) {
+        // the products still read this stage: meanwhile they may have the last tile
+        if (told < it) {
+          asm volatile("cp.async.wait_all;" ::: "memory");
+          tell();
+        }
+        if (!wait(empty[stage], it / kStages - 1)) break;
+      }
+      const int64_t s0 = lo + static_cast<int64_t>(it < tiles ? it : it - tiles) * kLanes;
+      const uint32_t to = k_at + stage * (HALVES * kHalf);
+      const unsigned char* from = keys + s0 * p.k_slot * 2;
+#pragma unroll 8
+      for (int i = ct; i < kLanes * kChunks; i += kCopyThreads) {
+        const int r = i / kChunks, c = i % kChunks;
+        const bool some = s0 + r < hi && c * 8 < p.D;
+        copy16(to + (c >> 3) * kHalf + r * 128 + (((c & 7) ^ (r & 7)) << 4), some ? from + r * p.k_slot * 2 + c * 16 : keys, some);
+      }
+      asm volatile("cp.async.commit_group;" ::: "memory");
+      if (told < it) {
+        asm volatile("cp.async.wait_group 1;" ::: "memory");
+        tell();
+      }
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    if (told < 2 * tiles && failed == 0) tell();
+    cluster_wait();
+    cluster_arrive();
+  } else if (warp == 4) {
+    cluster_arrive();
+    // scores of a negative scale are those of -Q
+    const uint32_t minus = p.scale < 0.f ? 1u : 0u;
+    for (int it = 0; it < 2 * tiles; ++it) {
+      const int stage = it % kStages, buf = it & 1;
+      bool ok = wait(full[stage], it / kStages);
+      if (it >= 2) ok = ok && wait(taken[buf], it / 2 - 1);
+      if (!__all_sync(kAll, ok)) break;
+      fence_after();
+      if (lane == 0) {
+        const uint32_t k = k_at + stage * (HALVES * kHalf), d = tmem + buf * kLanes;
+        const bool rows_first = it < tiles;
+        const uint32_t shape = product_shape(rows_first ? kLanes : columns) | minus << (rows_first ? 13 : 14);
+#pragma unroll
+        for (int i = 0; i < HALVES * 4; ++i) {
+          const uint32_t off = (i >> 2) * kHalf + (i & 3) * 32;
+          const uint64_t qd = operand(q_at + off), kd = operand(k + off);
+          product(d, rows_first ? qd : kd, rows_first ? kd : qd, shape, i > 0);
+        }
+        products_done(smem_u32(&empty[stage]));
+        products_done(smem_u32(&made[buf]));
+      }
+      __syncwarp();
+    }
+    cluster_wait();
+    cluster_arrive();
+  } else {
+    const uint32_t mine = tmem + (static_cast<uint32_t>(warp) << 21);  // this warp's lanes
+    const int32_t* positions = p.c.positions != nullptr ? p.c.positions + bh * p.c.S : nullptr;
+    float* weights = p.c.weights + bh * p.c.S;
+    auto position = [&](int64_t s) {  // of a slot; one behind the share is seen by no query
+      return s >= hi ? INT32_MAX : positions != nullptr ? positions[s] : static_cast<int32_t>(s);
+    };
+    // (A wait that has given up ends no loop here: all lanes meet at every barrier, and
+    // the weights are NaN at the end.)
+    // The rows' sums.
+    const int64_t see = first + tid / p.G;  // the last position this thread's row sees
+    float m = -FLT_MAX, top = -FLT_MAX;     // the largest score, and its exponent
+    float2 s2 = both(0.f);
+    int32_t at = position(lo + tid);
+    int it = 0;
+    for (; it < tiles; ++it) {
+      const int64_t s0 = lo + static_cast<int64_t>(it) * kLanes;
+      tile_positions[it & 1][tid] = at;
+      const bool all = lanes_all(at <= first);
+      at = it + 1 < tiles ? position(s0 + kLanes + tid) : 0;
+      wait(made[it & 1], it / 2);
+      __syncwarp();
+      fence_after();
+#pragma unroll 1
+      for (int c = 0; c < kLanes; c += 32) {
+        float x[32];
+        columns32(mine + (it & 1) * kLanes + c, x);
+        if (!all) {
+          // (no exponential of what is not seen: its place is that of a logit of -inf)
+#pragma unroll
+          for (int i = 0; i < 32; ++i)
+            if (tile_positions[it & 1][c + i] > see) x[i] = -INFINITY;
+        }
+        float most = x[0];
+#pragma unroll
+        for (int i = 1; i < 31; i += 2) most = fmax3(most, x[i], x[i + 1]);
+        most = fmaxf(most, x[31]);
+        if (most > m) {
+          m = most;
+          const float next = fmaxf(m * scale, -FLT_MAX), f = ex2(top - next);
+          s2.x *= f;
+          s2.y *= f;
+          top = next;
+        }
+        const float2 cc = both(scale), nt = both(-top);
+        float2 part = both(0.f);
+#pragma unroll
+        for (int i = 0; i < 32; i += 2) {
+          const float2 y = fma2(make_float2(x[i], x[i + 1]), cc, nt);
+          part = add2(part, make_float2(ex2(y.x), ex2(y.y)));
+        }
+        s2 = add2(s2, part);
+      }
+      fence_before();
+      arrive(smem_u32(&taken[it & 1]));
+    }
+    sums[tid] = {top, s2.x + s2.y};
+    cluster_arrive();
+    cluster_wait();
+    WindowSum all = {-FLT_MAX, 0.f};
+    for (uint32_t c = 0; c < C; ++c) {
+      const uint32_t from = map_rank(smem_u32(&sums[tid]), c);
+      const float t = ld_dsmem_f32(from), s = ld_dsmem_f32(from + 4);
+      const float most = fmaxf(all.top, t);
+      all.s = all.s * ex2(all.top - most) + s * ex2(t - most);
+      all.top = most;
+    }
+    cluster_arrive();  // (the other CTAs may end)
+    {
+      // rows that see nothing, or scores of -inf alone, add 0; so do those past the last
+      float* to = reinterpret_cast<float*>(&row_pairs[tid >> 1]) + (tid & 1);
+      const bool none = all.s == 0.f || tid >= R;
+      to[0] = none ? 0.f : -all.top;
+      to[2] = none ? 0.f : 1.f / all.s;
+    }
+    lanes_all(true);
+    // The slots' weights.
+    at = position(lo + tid);
+    for (; it < 2 * tiles; ++it) {
+      const int64_t s = lo + static_cast<int64_t>(it - tiles) * kLanes + tid;
+      // rows from here on see this slot
+      const int64_t after = at == INT32_MAX ? INT64_MAX : at - first;
+      const int least = after <= 0 ? 0 : after >= R ? R : static_cast<int>(min(after * p.G, static_cast<int64_t>(R)));
+      at = it + 1 < 2 * tiles ? position(s + kLanes) : 0;
+      wait(made[it & 1], it / 2);
+      __syncwarp();
+      fence_after();
+      const bool all_rows = __all_sync(kAll, least == 0);
+      float2 w = both(0.f);
+#pragma unroll 1
+      for (int c = 0; c < columns; c += 32) {
+        float x[32];
+        columns32(mine + (it & 1) * kLanes + c, x);
+        const float2 cc = both(scale);
+        if (all_rows && c + 32 <= R) {
+#pragma unroll
+          for (int i = 0; i < 32; i += 2) {
+            const float4 row = row_pairs[(c + i) >> 1];
+            const float2 y = fma2(make_float2(x[i], x[i + 1]), cc, make_float2(row.x, row.y));
+            w = fma2(make_float2(ex2(y.x), ex2(y.y)), make_float2(row.z, row.w), w);
+          }
+        } else {  // (columns past the last row hold anything)
+#pragma unroll
+          for (int i = 0; i < 32; i += 2) {
+            const float4 row = row_pairs[(c + i) >> 1];
+            const float2 y = fma2(make_float2(x[i], x[i + 1]), cc, make_float2(row.x, row.y));
+            if (c + i >= least && c + i < R) w.x = fmaf(ex2(y.x), row.z, w.x);
+            if (c + i + 1 >= least && c + i + 1 < R) w.y = fmaf(ex2(y.y), row.w, w.y);
+          }
+        }
+      }
+      fence_before();
+      arrive(smem_u32(&taken[it & 1]));
+      if (s < hi) weights[s] = p.decay != 0.f ? fmaf(p.decay, weights[s], w.x + w.y) : w.x + w.y;
+    }
+    if (failed != 0)
+      for (int64_t s = lo + tid; s < hi; s += kLanes) weights[s] = NAN;
+  }
+  __syncthreads();
+  if (warp == 4) {
+    fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(static_cast<uint32_t>(kColumns))
+                 : "memory");
+  }
+  cluster_wait();
+}
+
+template <int HALVES>
+cudaError_t launch_window_of(const WeightParams& p, cudaStream_t st) {
+  const int64_t pairs = p.c.B * p.c.H;
+  // (80 KB and more, so that two are on an SM at most)
+  constexpr size_t smem = (1 + kStages) * HALVES * kHalf + 1024 < 80 * 1024 ? 80 * 1024 : (1 + kStages) * HALVES * kHalf + 1024;
+  auto* fn = &window_kernel<HALVES>;
+  cudaError_t e = cudaFuncSetAttribute(reinterpret_cast<const void*>(fn), cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       static_cast<int>(smem));
+  if (e != cudaSuccess) return e;
+  // shares of a thousand slots, so that what all CTAs read again is in L2
+  uint32_t C = 1;
+  while (C < kMaxRanks && pairs * 2 * C <= INT32_MAX &&
+         (p.c.S > 1024 * static_cast<int64_t>(C) ||
+          (pairs * 2 * C <= 2 * device_sms() && p.c.S >= kLanes * 2 * static_cast<int64_t>(C))))
+    C *= 2;
+  // as many whole queries at a time as there are lanes for
+  const int each = kLanes / p.G;
+  for (int t = 0; t < p.T; t += each) {
+    WindowParams q;
+    q.w = p;
+    q.first = t;
+    q.rows = (p.T - t < each ? p.T - t : each) * p.G;
+    if (t > 0) q.w.decay = 1.f;
+    e = launch(fn, static_cast<unsigned>(pairs * C), kWindowThreads, C, st, smem, q);
+    if (e != cudaSuccess) return e;
+  }
+  return cudaSuccess;
+}
+
+}  // namespace
+
+bool window_fits(const WeightParams& p) { return p.G <= kLanes && p.D <= 256 && p.D % 8 == 0; }
+
+int launch_cache_window(const WeightParams& p, qrita_stream_t stream) {
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  if (p.D <= 64) return static_cast<int>(launch_window_of<1>(p, st));
+  return static_cast<int>(p.D <= 128 ? launch_window_of<2>(p, st) : launch_window_of<4>(p, st));
+}
+
+}  // namespace qrita
