@@ -91,7 +91,7 @@ def check_weights(dev, seed, B, H, G, T, S, D, dtype, evicted=False, decay=0.9, 
                 want[:m] = want[:m] * decay + add
                 fin = np.nan_to_num(k64[b, h, :m], nan=0.0, posinf=0.0, neginf=0.0)
                 A = np.abs(fin) @ np.abs(q64[b, :, h * G:(h + 1) * G]).reshape(T * G, D).T if m else np.zeros((1, 1))
-                A = A.max() * sc
+                A = A.max() * abs(sc)
                 d = 2 * (D * 2.0**-22 * A + 2.0**-23 * A)
                 tol = 2 * (d + 2.0**-21 + S * 2.0**-24) * np.abs(np.r_[np.nan_to_num(add), np.zeros(S - m)]) + 2.0**-22 * np.abs(np.nan_to_num(want))
                 tol[m:] = 0
@@ -134,6 +134,14 @@ def test_weights_of_long_caches(dev):
     check_weights(dev, 5, 1, 1, 2, 1, 70001, 64, "bf16")
     check_weights(dev, 6, 1, 1, 8, 5, 33000, 64, "bf16", evicted=True)
     check_weights(dev, 7, 20, 9, 1, 2, 500, 32, "bf16")
+
+
+def test_weights_of_windows_over_several_tiles(dev):
+    """One CTA a kv head (many of them), and shares of several tiles."""
+    check_weights(dev, 11, 160, 2, 1, 40, 700, 64, "bf16", evicted=True)
+    check_weights(dev, 12, 1, 2, 8, 40, 5000, 72, "bf16", scale=-0.1)
+    check_weights(dev, 13, 2, 1, 4, 9, 3000, 200, "bf16", evicted=True, scale=0.0)
+    check_weights(dev, 14, 4, 2, 40, 5, 600, 128, "bf16", special=True)
 
 
 def test_weights_decay_zero_reads_nothing(dev):

@@ -22,6 +22,15 @@ constexpr float kLog2e = 1.44269504088896340736f;
 // of them (0; -inf's is 0x007FFFFF).
 __device__ __forceinline__ uint32_t weight_key(float w) { return w != w ? 0u : f2key(w); }
 
+// Every thread of a row's C CTAs. (Without a cluster its barrier is none to rely on:
+// threads that arrived at it ahead of others were held there.)
+__device__ __forceinline__ void row_sync(uint32_t C) {
+  if (C > 1)
+    cluster_sync_all();
+  else
+    __syncthreads();
+}
+
 struct Guard {
   int32_t sink;
   int64_t from;  // positions from here on are the last ones seen
@@ -208,7 +217,7 @@ __global__ void __launch_bounds__(kWThreads, 1) weights_kernel(const WeightParam
   RowSum* by_warp = reinterpret_cast<RowSum*>(dynamic);
   RowSum* sums = by_warp + kWWarps * kMaxRowsAtOnce;
   unsigned char* rows = reinterpret_cast<unsigned char*>(sums + 2 * ((R + 1) / 2));
-  cluster_arrive_relaxed();
+  if (C > 1) cluster_arrive_relaxed();
   const bool idle = p.c.lengths[b] < 0;
   const int32_t n = length_of(p.c, b, p.c.S);
   const int64_t last = static_cast<int64_t>(p.c.seen != nullptr ? p.c.seen[b] : n) - p.T;  // the first query's position
@@ -281,8 +290,8 @@ __global__ void __launch_bounds__(kWThreads, 1) weights_kernel(const WeightParam
     }
   }
   // the rows' sums over the cluster, in place after everyone has read them
-  cluster_wait();
-  cluster_sync_all();
+  if (C > 1) cluster_wait();
+  row_sync(C);
   for (int r0 = 0; r0 < R; r0 += kWThreads) {
     const int r = r0 + tid;
     RowSum all = {-INFINITY, 0.f};
@@ -294,7 +303,7 @@ __global__ void __launch_bounds__(kWThreads, 1) weights_kernel(const WeightParam
         other.s = ld_dsmem_f32(from + 4);
         sum_add(all, other);
       }
-    cluster_sync_all();
+    row_sync(C);
     // (only this chunk's entries change, which everyone has read)
     // (a row that sees nothing, or logits of -inf alone, adds 0)
     if (r < R) sums[r] = {all.s == 0.f ? 0.f : all.m, all.s == 0.f ? 0.f : 1.f / all.s};
@@ -424,7 +433,7 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictPa
     for (int32_t i = rank * kSelThreads + tid; i < n; i += C * kSelThreads) write(i, i);
     return;
   }
-  cluster_arrive_relaxed();  // every CTA of the cluster runs before its memory is read
+  if (C > 1) cluster_arrive_relaxed();  // every CTA of the cluster runs before its memory is read
   const int32_t share = (n + static_cast<int32_t>(C) - 1) / static_cast<int32_t>(C);
   const int32_t lo = min(n, static_cast<int32_t>(rank) * share), hi = min(n, lo + share);
   const bool kept_here = share <= p.share;
@@ -445,8 +454,8 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictPa
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(kAll, mine, o);
   if (lane == 0 && mine != 0u) atomicAdd(&counts[0], mine);
-  cluster_wait();
-  cluster_sync_all();
+  if (C > 1) cluster_wait();
+  row_sync(C);
   uint32_t held_all = 0;
   for (uint32_t c = 0; c < C; ++c) held_all += ld_dsmem_u32(map_rank(smem_u32(&counts[0]), c));
   const bool crowded = held_all > static_cast<uint32_t>(keep);
@@ -465,7 +474,7 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictPa
       const uint32_t k = key(s);
       if (shift == 24 || (k >> (shift + 8)) == prefix) atomicAdd(&hist[(k >> shift) & 255u], 1u);
     }
-    cluster_sync_all();
+    row_sync(C);
     for (int i = tid; i < kBins; i += kSelThreads) {
       uint32_t v = 0;
       for (uint32_t c = 0; c < C; ++c) v += ld_dsmem_u32(map_rank(smem_u32(&hist[i]), c));
@@ -496,7 +505,7 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictPa
     __syncthreads();
     prefix = prefix << 8 | digit_of;
     left -= above_of;
-    cluster_sync_all();  // (the histograms have been read)
+    row_sync(C);  // (the histograms have been read)
   }
   // slots above the boundary and equal to it: counts by warp, each with its own range
   const int32_t span = ((hi - lo + kSelWarps - 1) / kSelWarps + 31) / 32 * 32;
@@ -522,13 +531,13 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictPa
     tally[0] = m;
     tally[1] = e;
   }
-  cluster_sync_all();
+  row_sync(C);
   uint32_t m0 = 0, e0 = 0;
   for (uint32_t c = 0; c < rank; ++c) {
     m0 += ld_dsmem_u32(map_rank(smem_u32(&tally[0]), c));
     e0 += ld_dsmem_u32(map_rank(smem_u32(&tally[1]), c));
   }
-  cluster_arrive();
+  if (C > 1) cluster_arrive();
   for (int w = 0; w < warp; ++w) {
     m0 += warp_more[w];
     e0 += warp_same[w];
@@ -544,7 +553,7 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictPa
     m0 += __popc(gt);
     e0 += __popc(eq);
   }
-  cluster_wait();
+  if (C > 1) cluster_wait();
 }
 
 // Copies a row of bytes by N threads, in units of 16, 4 or 1 bytes as both ends

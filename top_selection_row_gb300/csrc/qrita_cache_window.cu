@@ -73,21 +73,24 @@ __device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool some)
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(some ? 16u : 0u) : "memory");
 }
 
-// 32 columns of this lane.
-__device__ __forceinline__ void columns32(uint32_t addr, float (&v)[32]) {
-  uint32_t r[32];
+// 32 columns of this lane, there after columns_wait.
+__device__ __forceinline__ void columns32(uint32_t addr, uint32_t (&r)[32]) {
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
-      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];\n\t"
-      "tcgen05.wait::ld.sync.aligned;"
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
       : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
         "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
         "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
         "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
       : "r"(addr)
       : "memory");
+}
+
+// (The words pass through, so that no use of them moves before the wait.)
+__device__ __forceinline__ void columns_wait(uint32_t (&r)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 #pragma unroll
-  for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+  for (int i = 0; i < 32; ++i) asm volatile("" : "+r"(r[i]));
 }
 
 // Whether `yes` holds in all of the epilogues' threads.
@@ -162,7 +165,9 @@ __global__ void __launch_bounds__(kWindowThreads, HALVES <= 2 ? 2 : 1) window_ke
   __syncthreads();
   fence_after();
   const uint32_t tmem = tmem_at;
-  cluster_sync_all();  // every CTA of the cluster runs before its memory is read
+  // every CTA of the cluster runs before its memory is read (in a launch without
+  // clusters, threads that arrive at the cluster's barrier ahead of others are held)
+  if (C > 1) cluster_sync_all();
   auto wait = [&](uint64_t& bar, int use) {  // for the use-th completion (0, 1, ...)
     if (failed != 0 || !mbar_wait_bounded(smem_u32(&bar), static_cast<uint32_t>(use) & 1u, kWindowLimitNs)) {
       failed = 1;
@@ -172,8 +177,9 @@ __global__ void __launch_bounds__(kWindowThreads, HALVES <= 2 ? 2 : 1) window_ke
   };
 
   if (warp > 4) {
-    // copies: Q once, then the tiles of keys, all of them twice
-    cluster_arrive();
+    // copies: Q once, then the tiles of keys, all of them twice; the second time last ones
+    // first, which are the ones that L2 has
+    if (C > 1) cluster_arrive();
     const int ct = tid - (kLanes + 32);
     const unsigned char* q = static_cast<const unsigned char*>(p.query) + (b * p.q_batch + h * p.G * p.q_head) * 2;
     const unsigned char* keys = static_cast<const unsigned char*>(p.keys) + (b * p.k_batch + h * p.k_head) * 2;
@@ -185,6 +191,9 @@ __global__ void __launch_bounds__(kWindowThreads, HALVES <= 2 ? 2 : 1) window_ke
       copy16(q_at + (c >> 3) * kHalf + r * 128 + (((c & 7) ^ (r & 7)) << 4),
              some ? q + (t * p.q_token + g * p.q_head) * 2 + c * 16 : q, some);
     }
+    // this thread's 16 bytes of a row, and its rows
+    constexpr int kPass = kCopyThreads / kChunks;
+    const int c0 = ct % kChunks, r0 = ct / kChunks;
     int told = 0;  // tiles that the products know of
     auto tell = [&]() {
       fence_proxy_async_smem();
@@ -201,15 +210,13 @@ __global__ void __launch_bounds__(kWindowThreads, HALVES <= 2 ? 2 : 1) window_ke
         }
         if (!wait(empty[stage], it / kStages - 1)) break;
       }
-      const int64_t s0 = lo + static_cast<int64_t>(it < tiles ? it : it - tiles) * kLanes;
-      const uint32_t to = k_at + stage * (HALVES * kHalf);
-      const unsigned char* from = keys + s0 * p.k_slot * 2;
+      const int64_t s0 = lo + static_cast<int64_t>(it < tiles ? it : 2 * tiles - 1 - it) * kLanes;
+      const uint32_t to = k_at + stage * (HALVES * kHalf) + (c0 >> 3) * kHalf;
+      const int some = c0 * 8 < p.D ? static_cast<int>(min(hi - s0, static_cast<int64_t>(kLanes))) : 0;  // slots there are
+      const unsigned char* from = keys + (s0 + r0) * p.k_slot * 2 + c0 * 16;
 #pragma unroll 8
-      for (int i = ct; i < kLanes * kChunks; i += kCopyThreads) {
-        const int r = i / kChunks, c = i % kChunks;
-        const bool some = s0 + r < hi && c * 8 < p.D;
-        copy16(to + (c >> 3) * kHalf + r * 128 + (((c & 7) ^ (r & 7)) << 4), some ? from + r * p.k_slot * 2 + c * 16 : keys, some);
-      }
+      for (int r = r0; r < kLanes; r += kPass, from += kPass * p.k_slot * 2)
+        copy16(to + r * 128 + (((c0 ^ r) & 7) << 4), r < some ? from : keys, r < some);
       asm volatile("cp.async.commit_group;" ::: "memory");
       if (told < it) {
         asm volatile("cp.async.wait_group 1;" ::: "memory");
@@ -218,16 +225,18 @@ __global__ void __launch_bounds__(kWindowThreads, HALVES <= 2 ? 2 : 1) window_ke
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
     if (told < 2 * tiles && failed == 0) tell();
-    cluster_wait();
-    cluster_arrive();
+    if (C > 1) {
+      cluster_wait();
+      cluster_arrive();
+    }
   } else if (warp == 4) {
-    cluster_arrive();
+    if (C > 1) cluster_arrive();
     // scores of a negative scale are those of -Q
     const uint32_t minus = p.scale < 0.f ? 1u : 0u;
     for (int it = 0; it < 2 * tiles; ++it) {
       const int stage = it % kStages, buf = it & 1;
-      bool ok = wait(full[stage], it / kStages);
-      if (it >= 2) ok = ok && wait(taken[buf], it / 2 - 1);
+      bool ok = true;
+      if (lane == 0) ok = wait(full[stage], it / kStages) && (it < 2 || wait(taken[buf], it / 2 - 1));
       if (!__all_sync(kAll, ok)) break;
       fence_after();
       if (lane == 0) {
@@ -245,14 +254,16 @@ __global__ void __launch_bounds__(kWindowThreads, HALVES <= 2 ? 2 : 1) window_ke
       }
       __syncwarp();
     }
-    cluster_wait();
-    cluster_arrive();
+    if (C > 1) {
+      cluster_wait();
+      cluster_arrive();
+    }
   } else {
     const uint32_t mine = tmem + (static_cast<uint32_t>(warp) << 21);  // this warp's lanes
     const int32_t* positions = p.c.positions != nullptr ? p.c.positions + bh * p.c.S : nullptr;
     float* weights = p.c.weights + bh * p.c.S;
-    auto position = [&](int64_t s) {  // of a slot; one behind the share is seen by no query
-      return s >= hi ? INT32_MAX : positions != nullptr ? positions[s] : static_cast<int32_t>(s);
+    auto position = [&](int64_t s) {  // of a slot; one outside the share is seen by no query
+      return s < lo || s >= hi ? INT32_MAX : positions != nullptr ? positions[s] : static_cast<int32_t>(s);
     };
     // (A wait that has given up ends no loop here: all lanes meet at every barrier, and
     // the weights are NaN at the end.)
@@ -270,10 +281,15 @@ __global__ void __launch_bounds__(kWindowThreads, HALVES <= 2 ? 2 : 1) window_ke
       wait(made[it & 1], it / 2);
       __syncwarp();
       fence_after();
-#pragma unroll 1
+      uint32_t words[2][32];
+      columns32(mine + (it & 1) * kLanes, words[0]);
+#pragma unroll
       for (int c = 0; c < kLanes; c += 32) {
+        columns_wait(words[c / 32 & 1]);
+        if (c + 32 < kLanes) columns32(mine + (it & 1) * kLanes + c + 32, words[(c / 32 + 1) & 1]);
         float x[32];
-        columns32(mine + (it & 1) * kLanes + c, x);
+#pragma unroll
+        for (int i = 0; i < 32; ++i) x[i] = __uint_as_float(words[c / 32 & 1][i]);
         if (!all) {
           // (no exponential of what is not seen: its place is that of a logit of -inf)
 #pragma unroll
@@ -304,8 +320,10 @@ __global__ void __launch_bounds__(kWindowThreads, HALVES <= 2 ? 2 : 1) window_ke
       arrive(smem_u32(&taken[it & 1]));
     }
     sums[tid] = {top, s2.x + s2.y};
-    cluster_arrive();
-    cluster_wait();
+    if (C > 1) {
+      cluster_arrive();
+      cluster_wait();
+    }
     WindowSum all = {-FLT_MAX, 0.f};
     for (uint32_t c = 0; c < C; ++c) {
       const uint32_t from = map_rank(smem_u32(&sums[tid]), c);
@@ -314,7 +332,7 @@ __global__ void __launch_bounds__(kWindowThreads, HALVES <= 2 ? 2 : 1) window_ke
       all.s = all.s * ex2(all.top - most) + s * ex2(t - most);
       all.top = most;
     }
-    cluster_arrive();  // (the other CTAs may end)
+    if (C > 1) cluster_arrive();  // (the other CTAs may end)
     {
       // rows that see nothing, or scores of -inf alone, add 0; so do those past the last
       float* to = reinterpret_cast<float*>(&row_pairs[tid >> 1]) + (tid & 1);
@@ -324,22 +342,28 @@ __global__ void __launch_bounds__(kWindowThreads, HALVES <= 2 ? 2 : 1) window_ke
     }
     lanes_all(true);
     // The slots' weights.
-    at = position(lo + tid);
+    at = position(lo + static_cast<int64_t>(tiles - 1) * kLanes + tid);
     for (; it < 2 * tiles; ++it) {
-      const int64_t s = lo + static_cast<int64_t>(it - tiles) * kLanes + tid;
+      const int64_t s = lo + static_cast<int64_t>(2 * tiles - 1 - it) * kLanes + tid;
       // rows from here on see this slot
       const int64_t after = at == INT32_MAX ? INT64_MAX : at - first;
       const int least = after <= 0 ? 0 : after >= R ? R : static_cast<int>(min(after * p.G, static_cast<int64_t>(R)));
-      at = it + 1 < 2 * tiles ? position(s + kLanes) : 0;
+      at = it + 1 < 2 * tiles ? position(s - kLanes) : 0;
       wait(made[it & 1], it / 2);
       __syncwarp();
       fence_after();
       const bool all_rows = __all_sync(kAll, least == 0);
       float2 w = both(0.f);
-#pragma unroll 1
-      for (int c = 0; c < columns; c += 32) {
+      uint32_t words[2][32];
+      columns32(mine + (it & 1) * kLanes, words[0]);
+#pragma unroll
+      for (int c = 0; c < kLanes; c += 32) {
+        columns_wait(words[c / 32 & 1]);
+        if (c >= columns) break;
+        if (c + 32 < kLanes && c + 32 < columns) columns32(mine + (it & 1) * kLanes + c + 32, words[(c / 32 + 1) & 1]);
         float x[32];
-        columns32(mine + (it & 1) * kLanes + c, x);
+#pragma unroll
+        for (int i = 0; i < 32; ++i) x[i] = __uint_as_float(words[c / 32 & 1][i]);
         const float2 cc = both(scale);
         if (all_rows && c + 32 <= R) {
 #pragma unroll
@@ -371,7 +395,7 @@ __global__ void __launch_bounds__(kWindowThreads, HALVES <= 2 ? 2 : 1) window_ke
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(static_cast<uint32_t>(kColumns))
                  : "memory");
   }
-  cluster_wait();
+  if (C > 1) cluster_wait();
 }
 
 template <int HALVES>
@@ -383,12 +407,11 @@ cudaError_t launch_window_of(const WeightParams& p, cudaStream_t st) {
   cudaError_t e = cudaFuncSetAttribute(reinterpret_cast<const void*>(fn), cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        static_cast<int>(smem));
   if (e != cudaSuccess) return e;
-  // shares of a thousand slots, so that what all CTAs read again is in L2
+  // As many CTAs as are on the device at once, with two tiles each at least: more,
+  // smaller shares cost merges and do not hide more (8 x 8 kv heads of 16384 slots, 32
+  // queries of 4 heads: 4 CTAs a head 120 us, 8 CTAs 129, 16 CTAs 188, 2 CTAs 176).
   uint32_t C = 1;
-  while (C < kMaxRanks && pairs * 2 * C <= INT32_MAX &&
-         (p.c.S > 1024 * static_cast<int64_t>(C) ||
-          (pairs * 2 * C <= 2 * device_sms() && p.c.S >= kLanes * 2 * static_cast<int64_t>(C))))
-    C *= 2;
+  while (C < kMaxRanks && pairs * 2 * C <= 2 * device_sms() && p.c.S >= kLanes * 2 * static_cast<int64_t>(C)) C *= 2;
   // as many whole queries at a time as there are lanes for
   const int each = kLanes / p.G;
   for (int t = 0; t < p.T; t += each) {
