@@ -142,6 +142,8 @@ def test_weights_of_windows_over_several_tiles(dev):
     check_weights(dev, 12, 1, 2, 8, 40, 5000, 72, "bf16", scale=-0.1)
     check_weights(dev, 13, 2, 1, 4, 9, 3000, 200, "bf16", evicted=True, scale=0.0)
     check_weights(dev, 14, 4, 2, 40, 5, 600, 128, "bf16", special=True)
+    check_weights(dev, 15, 2, 3, 7, 7, 900, 128, "bf16", layout=2)
+    check_weights(dev, 16, 3, 2, 128, 2, 300, 64, "bf16", layout=1)
 
 
 def test_weights_decay_zero_reads_nothing(dev):

@@ -714,7 +714,8 @@ int launch_cache_weights(const WeightParams& p, int dtype, qrita_stream_t stream
   const uint64_t a = static_cast<uint64_t>(reinterpret_cast<uintptr_t>(p.query) | reinterpret_cast<uintptr_t>(p.keys)) |
                      2u * static_cast<uint64_t>(p.q_batch | p.q_token | p.q_head | p.k_batch | p.k_head | p.k_slot);
   if ((a & 15u) == 0u) {
-    if (static_cast<int64_t>(p.G) * p.T > kMaxRowsAtOnce && window_fits(p)) return launch_cache_window(p, stream);
+    int result;
+    if (static_cast<int64_t>(p.G) * p.T > kMaxRowsAtOnce && launch_cache_window(p, stream, &result)) return result;
     switch (p.D) {
       case 32: return static_cast<int>(launch_weights_mma<1>(p, st));
       case 64: return static_cast<int>(launch_weights_mma<2>(p, st));

@@ -56,10 +56,10 @@ struct InsertParams {
   int32_t* out_slots;  // [B, H]
 };
 
-// Whether qrita_cache_window.cu takes a call (bf16 rows of 16-byte units on their
-// boundaries), and its launches.
-bool window_fits(const WeightParams& prm);
-int launch_cache_window(const WeightParams& prm, qrita_stream_t stream);
+// Launches qrita_cache_window.cu's kernel (bf16 rows of 16-byte units on their
+// boundaries; *result is a cudaError_t), or returns false where its sizes and strides
+// are none that it takes.
+bool launch_cache_window(const WeightParams& prm, qrita_stream_t stream, int* result);
 
 // Every launch returns a cudaError_t.
 int launch_cache_weights(const WeightParams& prm, int dtype, qrita_stream_t stream);

@@ -13,14 +13,19 @@
 // bytes). Keys are read again for the second product: a share of a thousand slots is
 // small enough that they come from L2.
 //
-// Warps 0 to 3 are the lanes' threads, warp 4 issues the products, warps 5 and 6 copy.
-// Two accumulators of 128 columns and two stages of keys; CTAs ask for so much shared
-// memory that two at most are on an SM, whose tensor memory holds both: no CTA of
-// these kernels waits for columns that another one holds.
+// A CTA has an SM: two groups of four warps, the lanes' threads of every other tile,
+// a warp that issues the products and one that asks for the tiles (TMA). Four
+// accumulators of 128 columns, all of the tensor memory, and as many stages of keys as
+// shared memory has, so that copies are under way while products and exponentials
+// are. No other CTA of these kernels fits beside one, so none waits for columns that
+// another holds.
 
 #include <cfloat>
+#include <cstring>
 #include <cstddef>
 #include <cstdint>
+
+#include <cuda.h>
 
 #include "qrita_cache.h"
 #include "qrita_rows.cuh"
@@ -29,12 +34,17 @@ namespace qrita {
 namespace {
 
 constexpr float kLog2e = 1.44269504088896340736f;
-constexpr int kLanes = 128;              // threads of the epilogues, slots of a tile, rows at most
-constexpr int kWindowThreads = kLanes + 32 + 64;
-constexpr int kCopyThreads = 64;
-constexpr int kColumns = 2 * kLanes;     // of tensor memory: two accumulators
+constexpr int kLanes = 128;              // threads of a group, slots of a tile, rows at most
+constexpr int kGroups = 2;
+constexpr int kWindowThreads = kGroups * kLanes + 64;
+constexpr int kBuffers = 4;              // accumulators
+constexpr int kColumns = kBuffers * kLanes;
 constexpr int kHalf = kLanes * 128;      // bytes of a tile's 64 dimensions
-constexpr int kStages = 2;
+template <int HALVES>
+constexpr int kStages = HALVES == 1 ? 8 : HALVES == 2 ? 5 : 2;
+template <int HALVES>
+constexpr int kWindowSmem = (1 + kStages<HALVES>) * HALVES * kHalf + 1024;
+static_assert(kWindowSmem<1> > 114 * 1024, "one CTA on an SM");
 constexpr uint64_t kWindowLimitNs = 10ull * 1000 * 1000 * 1000;
 
 // Shared-memory operand: rows of 128 bytes, swizzled, eight rows 1024 bytes.
@@ -68,9 +78,13 @@ __device__ __forceinline__ void arrive(uint32_t bar) {
   asm volatile("mbarrier.arrive.release.cta.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
-// 16 bytes to shared memory, zeros where `some` is false (nothing is read then).
-__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool some) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(some ? 16u : 0u) : "memory");
+// A box of a tensor to shared memory, at bar.
+__device__ __forceinline__ void copy_box(uint32_t dst, const CUtensorMap* map, int x, int y, int z, int w, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], "
+      "[%6];" ::"r"(dst),
+      "l"(map), "r"(x), "r"(y), "r"(z), "r"(w), "r"(bar)
+      : "memory");
 }
 
 // 32 columns of this lane, there after columns_wait.
@@ -93,14 +107,14 @@ __device__ __forceinline__ void columns_wait(uint32_t (&r)[32]) {
   for (int i = 0; i < 32; ++i) asm volatile("" : "+r"(r[i]));
 }
 
-// Whether `yes` holds in all of the epilogues' threads.
-__device__ __forceinline__ bool lanes_all(bool yes) {
+// Whether `yes` holds in all threads of a group.
+__device__ __forceinline__ bool lanes_all(bool yes, int group) {
   uint32_t r;
   asm volatile(
-      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbarrier.cta.red.and.pred q, 1, %2, p;\n\tselp.u32 %0, 1, 0, "
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbarrier.cta.red.and.pred q, %3, %2, p;\n\tselp.u32 %0, 1, 0, "
       "q;\n\t}"
       : "=r"(r)
-      : "r"(yes ? 1u : 0u), "n"(kLanes)
+      : "r"(yes ? 1u : 0u), "n"(kLanes), "r"(group + 1)
       : "memory");
   return r != 0u;
 }
@@ -113,25 +127,51 @@ struct WindowSum {
 struct WindowParams {
   WeightParams w;
   int32_t rows, first;  // this launch's rows, and its first query
+  int32_t queries;      // of a box of Q
 };
 
 template <int HALVES>
-__global__ void __launch_bounds__(kWindowThreads, HALVES <= 2 ? 2 : 1) window_kernel(const WindowParams wp) {
+__global__ void __launch_bounds__(kWindowThreads, 1)
+window_kernel(const WindowParams wp, const __grid_constant__ CUtensorMap query_map, const __grid_constant__ CUtensorMap key_map) {
   const WeightParams& p = wp.w;
+  constexpr int kDepth = kStages<HALVES>;
   extern __shared__ unsigned char raw[];
-  __shared__ __align__(8) uint64_t full[kStages], empty[kStages], made[2], taken[2];
-  __shared__ WindowSum sums[kLanes];
+  __shared__ __align__(8) uint64_t full[kDepth], empty[kDepth], made[kBuffers], taken[kBuffers];
+  __shared__ WindowSum sums[kGroups][kLanes];
   __shared__ float4 row_pairs[kLanes / 2];  // -top of two rows, 1 / S of the two
-  __shared__ int tile_positions[2][kLanes];
+  __shared__ int tile_positions[kGroups][2][kLanes];
   __shared__ uint32_t tmem_at;
   __shared__ volatile int failed;  // a bounded wait gave up
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const uint32_t rank = cluster_rank(), C = gridDim.x / static_cast<uint32_t>(p.c.B * p.c.H);
-  const int64_t bh = cluster_id(), b = bh / p.c.H, h = bh % p.c.H;
   const uint32_t base = (smem_u32(raw) + 1023u) & ~1023u;
   const uint32_t q_at = base, k_at = base + HALVES * kHalf;
+  if (tid == 0) {
+    for (int i = 0; i < kDepth; ++i) {
+      mbar_init(smem_u32(&full[i]), 1);
+      mbar_init(smem_u32(&empty[i]), 1);
+    }
+    for (int i = 0; i < kBuffers; ++i) {
+      mbar_init(smem_u32(&made[i]), 1);
+      mbar_init(smem_u32(&taken[i]), kLanes);
+    }
+    fence_mbar_init();
+    failed = 0;
+  }
+  // (tensor memory only after that: the kernel before may be about to take some)
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if (warp == kGroups * 4) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&tmem_at)),
+                 "r"(static_cast<uint32_t>(kColumns))
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    fence_before();
+  }
+  __syncthreads();
+  fence_after();
+  const uint32_t tmem = tmem_at;
+  const uint32_t rank = cluster_rank(), C = gridDim.x / static_cast<uint32_t>(p.c.B * p.c.H);
+  const int64_t bh = cluster_id(), b = bh / p.c.H, h = bh % p.c.H;
   const int32_t given = p.c.lengths[b];
   const int32_t n = static_cast<int32_t>(min(static_cast<int64_t>(max(given, 0)), p.c.S));
   // (the position of this launch's first query)
@@ -143,28 +183,6 @@ __global__ void __launch_bounds__(kWindowThreads, HALVES <= 2 ? 2 : 1) window_ke
   const int R = wp.rows, columns = (R + 15) / 16 * 16;
   // (above 0, so that what is not seen stays -inf)
   const float scale = fminf(fmaxf(fabsf(p.scale) * kLog2e, 1e-37f), FLT_MAX);
-  if (tid == 0) {
-    for (int i = 0; i < kStages; ++i) {
-      mbar_init(smem_u32(&full[i]), kCopyThreads);
-      mbar_init(smem_u32(&empty[i]), 1);
-    }
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(smem_u32(&made[i]), 1);
-      mbar_init(smem_u32(&taken[i]), kLanes);
-    }
-    fence_mbar_init();
-    failed = 0;
-  }
-  if (warp == 4) {
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&tmem_at)),
-                 "r"(static_cast<uint32_t>(kColumns))
-                 : "memory");
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
-    fence_before();
-  }
-  __syncthreads();
-  fence_after();
-  const uint32_t tmem = tmem_at;
   // every CTA of the cluster runs before its memory is read (in a launch without
   // clusters, threads that arrive at the cluster's barrier ahead of others are held)
   if (C > 1) cluster_sync_all();
@@ -176,70 +194,40 @@ __global__ void __launch_bounds__(kWindowThreads, HALVES <= 2 ? 2 : 1) window_ke
     return true;
   };
 
-  if (warp > 4) {
+  if (warp == kGroups * 4 + 1) {
     // copies: Q once, then the tiles of keys, all of them twice; the second time last ones
     // first, which are the ones that L2 has
     if (C > 1) cluster_arrive();
-    const int ct = tid - (kLanes + 32);
-    const unsigned char* q = static_cast<const unsigned char*>(p.query) + (b * p.q_batch + h * p.G * p.q_head) * 2;
-    const unsigned char* keys = static_cast<const unsigned char*>(p.keys) + (b * p.k_batch + h * p.k_head) * 2;
-    constexpr int kChunks = HALVES * 8;
-    for (int i = ct; i < kLanes * kChunks; i += kCopyThreads) {
-      const int r = i / kChunks, c = i % kChunks;
-      const bool some = r < R && c * 8 < p.D;
-      const int64_t t = wp.first + r / p.G, g = r % p.G;
-      copy16(q_at + (c >> 3) * kHalf + r * 128 + (((c & 7) ^ (r & 7)) << 4),
-             some ? q + (t * p.q_token + g * p.q_head) * 2 + c * 16 : q, some);
-    }
-    // this thread's 16 bytes of a row, and its rows
-    constexpr int kPass = kCopyThreads / kChunks;
-    const int c0 = ct % kChunks, r0 = ct / kChunks;
-    int told = 0;  // tiles that the products know of
-    auto tell = [&]() {
-      fence_proxy_async_smem();
-      arrive(smem_u32(&full[told % kStages]));
-      ++told;
-    };
-    for (int it = 0; it < 2 * tiles; ++it) {
-      const int stage = it % kStages;
-      if (it >= kStages && !mbar_try_wait(smem_u32(&empty[stage]), static_cast<uint32_t>(it / kStages - 1) & 1u)) {
-        // the products still read this stage: meanwhile they may have the last tile
-        if (told < it) {
-          asm volatile("cp.async.wait_all;" ::: "memory");
-          tell();
+    if (lane == 0) {
+      for (int it = 0; it < 2 * tiles; ++it) {
+        const int stage = it % kDepth;
+        if (it >= kDepth && !wait(empty[stage], it / kDepth - 1)) break;
+        const int s0 = static_cast<int>(lo) + (it < tiles ? it : 2 * tiles - 1 - it) * kLanes;
+        const uint32_t to = k_at + stage * (HALVES * kHalf), bar = smem_u32(&full[stage]);
+        const uint32_t q_bytes = it == 0 ? static_cast<uint32_t>(HALVES * 128 * wp.queries * p.G) : 0u;
+        mbar_expect_tx(bar, HALVES * kHalf + q_bytes);
+        if (it == 0) {
+          for (int i = 0; i < HALVES; ++i)
+            copy_box(q_at + i * kHalf, &query_map, i * 64, static_cast<int>(h) * p.G, wp.first, static_cast<int>(b), bar);
         }
-        if (!wait(empty[stage], it / kStages - 1)) break;
-      }
-      const int64_t s0 = lo + static_cast<int64_t>(it < tiles ? it : 2 * tiles - 1 - it) * kLanes;
-      const uint32_t to = k_at + stage * (HALVES * kHalf) + (c0 >> 3) * kHalf;
-      const int some = c0 * 8 < p.D ? static_cast<int>(min(hi - s0, static_cast<int64_t>(kLanes))) : 0;  // slots there are
-      const unsigned char* from = keys + (s0 + r0) * p.k_slot * 2 + c0 * 16;
-#pragma unroll 8
-      for (int r = r0; r < kLanes; r += kPass, from += kPass * p.k_slot * 2)
-        copy16(to + r * 128 + (((c0 ^ r) & 7) << 4), r < some ? from : keys, r < some);
-      asm volatile("cp.async.commit_group;" ::: "memory");
-      if (told < it) {
-        asm volatile("cp.async.wait_group 1;" ::: "memory");
-        tell();
+        for (int i = 0; i < HALVES; ++i)
+          copy_box(to + i * kHalf, &key_map, i * 64, s0, static_cast<int>(h), static_cast<int>(b), bar);
       }
     }
-    asm volatile("cp.async.wait_all;" ::: "memory");
-    if (told < 2 * tiles && failed == 0) tell();
+    __syncwarp();
     if (C > 1) {
       cluster_wait();
       cluster_arrive();
     }
-  } else if (warp == 4) {
+  } else if (warp == kGroups * 4) {
     if (C > 1) cluster_arrive();
     // scores of a negative scale are those of -Q
     const uint32_t minus = p.scale < 0.f ? 1u : 0u;
-    for (int it = 0; it < 2 * tiles; ++it) {
-      const int stage = it % kStages, buf = it & 1;
-      bool ok = true;
-      if (lane == 0) ok = wait(full[stage], it / kStages) && (it < 2 || wait(taken[buf], it / 2 - 1));
-      if (!__all_sync(kAll, ok)) break;
-      fence_after();
-      if (lane == 0) {
+    if (lane == 0) {
+      for (int it = 0; it < 2 * tiles; ++it) {
+        const int stage = it % kDepth, buf = it % kBuffers;
+        if (!wait(full[stage], it / kDepth) || (it >= kBuffers && !wait(taken[buf], it / kBuffers - 1))) break;
+        fence_after();
         const uint32_t k = k_at + stage * (HALVES * kHalf), d = tmem + buf * kLanes;
         const bool rows_first = it < tiles;
         const uint32_t shape = product_shape(rows_first ? kLanes : columns) | minus << (rows_first ? 13 : 14);
@@ -252,14 +240,15 @@ __global__ void __launch_bounds__(kWindowThreads, HALVES <= 2 ? 2 : 1) window_ke
         products_done(smem_u32(&empty[stage]));
         products_done(smem_u32(&made[buf]));
       }
-      __syncwarp();
     }
+    __syncwarp();
     if (C > 1) {
       cluster_wait();
       cluster_arrive();
     }
   } else {
-    const uint32_t mine = tmem + (static_cast<uint32_t>(warp) << 21);  // this warp's lanes
+    const int group = warp >> 2, t = tid & (kLanes - 1);  // this thread's lane
+    const uint32_t mine = tmem + (static_cast<uint32_t>(warp & 3) << 21);
     const int32_t* positions = p.c.positions != nullptr ? p.c.positions + bh * p.c.S : nullptr;
     float* weights = p.c.weights + bh * p.c.S;
     auto position = [&](int64_t s) {  // of a slot; one outside the share is seen by no query
@@ -268,25 +257,26 @@ __global__ void __launch_bounds__(kWindowThreads, HALVES <= 2 ? 2 : 1) window_ke
     // (A wait that has given up ends no loop here: all lanes meet at every barrier, and
     // the weights are NaN at the end.)
     // The rows' sums.
-    const int64_t see = first + tid / p.G;  // the last position this thread's row sees
-    float m = -FLT_MAX, top = -FLT_MAX;     // the largest score, and its exponent
+    const int64_t see = first + t / p.G;  // the last position this thread's row sees
+    float m = -FLT_MAX, top = -FLT_MAX;   // the largest score, and its exponent
     float2 s2 = both(0.f);
-    int32_t at = position(lo + tid);
-    int it = 0;
-    for (; it < tiles; ++it) {
-      const int64_t s0 = lo + static_cast<int64_t>(it) * kLanes;
-      tile_positions[it & 1][tid] = at;
-      const bool all = lanes_all(at <= first);
-      at = it + 1 < tiles ? position(s0 + kLanes + tid) : 0;
-      wait(made[it & 1], it / 2);
+    int32_t at = position(lo + group * kLanes + t);
+    int it = group;
+    for (; it < tiles; it += kGroups) {
+      int* of = tile_positions[group][it / kGroups & 1];
+      of[t] = at;
+      const bool all = lanes_all(at <= first, group);
+      at = position(lo + static_cast<int64_t>(it + kGroups) * kLanes + t);
+      wait(made[it % kBuffers], it / kBuffers);
       __syncwarp();
       fence_after();
+      const uint32_t from = mine + it % kBuffers * kLanes;
       uint32_t words[2][32];
-      columns32(mine + (it & 1) * kLanes, words[0]);
+      columns32(from, words[0]);
 #pragma unroll
       for (int c = 0; c < kLanes; c += 32) {
         columns_wait(words[c / 32 & 1]);
-        if (c + 32 < kLanes) columns32(mine + (it & 1) * kLanes + c + 32, words[(c / 32 + 1) & 1]);
+        if (c + 32 < kLanes) columns32(from + c + 32, words[(c / 32 + 1) & 1]);
         float x[32];
 #pragma unroll
         for (int i = 0; i < 32; ++i) x[i] = __uint_as_float(words[c / 32 & 1][i]);
@@ -294,7 +284,7 @@ __global__ void __launch_bounds__(kWindowThreads, HALVES <= 2 ? 2 : 1) window_ke
           // (no exponential of what is not seen: its place is that of a logit of -inf)
 #pragma unroll
           for (int i = 0; i < 32; ++i)
-            if (tile_positions[it & 1][c + i] > see) x[i] = -INFINITY;
+            if (of[c + i] > see) x[i] = -INFINITY;
         }
         float most = x[0];
 #pragma unroll
@@ -317,50 +307,55 @@ __global__ void __launch_bounds__(kWindowThreads, HALVES <= 2 ? 2 : 1) window_ke
         s2 = add2(s2, part);
       }
       fence_before();
-      arrive(smem_u32(&taken[it & 1]));
+      arrive(smem_u32(&taken[it % kBuffers]));
     }
-    sums[tid] = {top, s2.x + s2.y};
+    sums[group][t] = {top, s2.x + s2.y};
+    auto both_groups = [&]() { asm volatile("bar.sync 3, %0;" ::"n"(kGroups * kLanes) : "memory"); };
     if (C > 1) {
       cluster_arrive();
       cluster_wait();
+    } else {
+      both_groups();
     }
-    WindowSum all = {-FLT_MAX, 0.f};
-    for (uint32_t c = 0; c < C; ++c) {
-      const uint32_t from = map_rank(smem_u32(&sums[tid]), c);
-      const float t = ld_dsmem_f32(from), s = ld_dsmem_f32(from + 4);
-      const float most = fmaxf(all.top, t);
-      all.s = all.s * ex2(all.top - most) + s * ex2(t - most);
-      all.top = most;
-    }
-    if (C > 1) cluster_arrive();  // (the other CTAs may end)
-    {
+    if (group == 0) {
+      WindowSum all = {-FLT_MAX, 0.f};
+      for (uint32_t c = 0; c < C * kGroups; ++c) {
+        const uint32_t at = smem_u32(&sums[c % kGroups][t]), from = C > 1 ? map_rank(at, c / kGroups) : at;
+        const float o = ld_dsmem_f32(from), s = ld_dsmem_f32(from + 4);
+        const float most = fmaxf(all.top, o);
+        all.s = all.s * ex2(all.top - most) + s * ex2(o - most);
+        all.top = most;
+      }
       // rows that see nothing, or scores of -inf alone, add 0; so do those past the last
-      float* to = reinterpret_cast<float*>(&row_pairs[tid >> 1]) + (tid & 1);
-      const bool none = all.s == 0.f || tid >= R;
+      float* to = reinterpret_cast<float*>(&row_pairs[t >> 1]) + (t & 1);
+      const bool none = all.s == 0.f || t >= R;
       to[0] = none ? 0.f : -all.top;
       to[2] = none ? 0.f : 1.f / all.s;
     }
-    lanes_all(true);
+    if (C > 1) cluster_arrive();  // (the other CTAs may end)
+    both_groups();
     // The slots' weights.
-    at = position(lo + static_cast<int64_t>(tiles - 1) * kLanes + tid);
-    for (; it < 2 * tiles; ++it) {
-      const int64_t s = lo + static_cast<int64_t>(2 * tiles - 1 - it) * kLanes + tid;
+    it = tiles + ((tiles ^ group) & 1);
+    at = position(lo + static_cast<int64_t>(2 * tiles - 1 - it) * kLanes + t);
+    for (; it < 2 * tiles; it += kGroups) {
+      const int64_t s = lo + static_cast<int64_t>(2 * tiles - 1 - it) * kLanes + t;
       // rows from here on see this slot
       const int64_t after = at == INT32_MAX ? INT64_MAX : at - first;
       const int least = after <= 0 ? 0 : after >= R ? R : static_cast<int>(min(after * p.G, static_cast<int64_t>(R)));
-      at = it + 1 < 2 * tiles ? position(s - kLanes) : 0;
-      wait(made[it & 1], it / 2);
+      at = position(s - kGroups * kLanes);
+      wait(made[it % kBuffers], it / kBuffers);
       __syncwarp();
       fence_after();
+      const uint32_t from = mine + it % kBuffers * kLanes;
       const bool all_rows = __all_sync(kAll, least == 0);
       float2 w = both(0.f);
       uint32_t words[2][32];
-      columns32(mine + (it & 1) * kLanes, words[0]);
+      columns32(from, words[0]);
 #pragma unroll
       for (int c = 0; c < kLanes; c += 32) {
         columns_wait(words[c / 32 & 1]);
         if (c >= columns) break;
-        if (c + 32 < kLanes && c + 32 < columns) columns32(mine + (it & 1) * kLanes + c + 32, words[(c / 32 + 1) & 1]);
+        if (c + 32 < kLanes && c + 32 < columns) columns32(from + c + 32, words[(c / 32 + 1) & 1]);
         float x[32];
 #pragma unroll
         for (int i = 0; i < 32; ++i) x[i] = __uint_as_float(words[c / 32 & 1][i]);
@@ -383,14 +378,14 @@ __global__ void __launch_bounds__(kWindowThreads, HALVES <= 2 ? 2 : 1) window_ke
         }
       }
       fence_before();
-      arrive(smem_u32(&taken[it & 1]));
+      arrive(smem_u32(&taken[it % kBuffers]));
       if (s < hi) weights[s] = p.decay != 0.f ? fmaf(p.decay, weights[s], w.x + w.y) : w.x + w.y;
     }
     if (failed != 0)
-      for (int64_t s = lo + tid; s < hi; s += kLanes) weights[s] = NAN;
+      for (int64_t s = lo + tid; s < hi; s += kGroups * kLanes) weights[s] = NAN;
   }
   __syncthreads();
-  if (warp == 4) {
+  if (warp == kGroups * 4) {
     fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(static_cast<uint32_t>(kColumns))
                  : "memory");
@@ -398,20 +393,53 @@ __global__ void __launch_bounds__(kWindowThreads, HALVES <= 2 ? 2 : 1) window_ke
   if (C > 1) cluster_wait();
 }
 
+using EncodeTiled = decltype(&cuTensorMapEncodeTiled);
+
+// The driver's encoder of tensor maps (null: there is none).
+EncodeTiled encoder() {
+  static std::atomic<EncodeTiled> known{nullptr};
+  EncodeTiled fn = known.load(std::memory_order_relaxed);
+  if (fn != nullptr) return fn;
+  void* at = nullptr;
+  cudaDriverEntryPointQueryResult found;
+  if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &at, 12000, cudaEnableDefault, &found) != cudaSuccess ||
+      found != cudaDriverEntryPointSuccess)
+    return nullptr;
+  fn = reinterpret_cast<EncodeTiled>(at);
+  known.store(fn, std::memory_order_relaxed);
+  return fn;
+}
+
+// A map of bf16 boxes of 64 columns, swizzled over their 128 bytes, of a tensor of
+// four dimensions; strides in elements. False: it cannot be one (a stride of 0 of more
+// than one row, say).
+bool make_map(CUtensorMap* map, const void* at, const int64_t (&dims)[4], const int64_t (&strides)[3], int rows, int more) {
+  EncodeTiled encode = encoder();
+  if (encode == nullptr) return false;
+  cuuint64_t size[4], step[3];
+  for (int i = 0; i < 4; ++i) size[i] = static_cast<cuuint64_t>(dims[i]);
+  for (int i = 0; i < 3; ++i) {
+    if (dims[i + 1] > 1 && strides[i] == 0) return false;
+    step[i] = dims[i + 1] > 1 ? static_cast<cuuint64_t>(strides[i]) * 2 : static_cast<cuuint64_t>(dims[0] + 7) / 8 * 16;
+  }
+  const cuuint32_t box[4] = {64, static_cast<cuuint32_t>(rows), static_cast<cuuint32_t>(more), 1};
+  const cuuint32_t ones[4] = {1, 1, 1, 1};
+  return encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(at), size, step, box, ones,
+                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 template <int HALVES>
-cudaError_t launch_window_of(const WeightParams& p, cudaStream_t st) {
+cudaError_t launch_window_of(const WeightParams& p, const CUtensorMap& query, const CUtensorMap& key, cudaStream_t st) {
   const int64_t pairs = p.c.B * p.c.H;
-  // (80 KB and more, so that two are on an SM at most)
-  constexpr size_t smem = (1 + kStages) * HALVES * kHalf + 1024 < 80 * 1024 ? 80 * 1024 : (1 + kStages) * HALVES * kHalf + 1024;
+  constexpr size_t smem = kWindowSmem<HALVES>;
   auto* fn = &window_kernel<HALVES>;
   cudaError_t e = cudaFuncSetAttribute(reinterpret_cast<const void*>(fn), cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        static_cast<int>(smem));
   if (e != cudaSuccess) return e;
-  // As many CTAs as are on the device at once, with two tiles each at least: more,
-  // smaller shares cost merges and do not hide more (8 x 8 kv heads of 16384 slots, 32
-  // queries of 4 heads: 4 CTAs a head 120 us, 8 CTAs 129, 16 CTAs 188, 2 CTAs 176).
+  // As many CTAs as are on the device at once, with two tiles each at least.
   uint32_t C = 1;
-  while (C < kMaxRanks && pairs * 2 * C <= 2 * device_sms() && p.c.S >= kLanes * 2 * static_cast<int64_t>(C)) C *= 2;
+  while (C < kMaxRanks && pairs * 2 * C <= device_sms() && p.c.S >= kLanes * 2 * static_cast<int64_t>(C)) C *= 2;
   // as many whole queries at a time as there are lanes for
   const int each = kLanes / p.G;
   for (int t = 0; t < p.T; t += each) {
@@ -419,8 +447,9 @@ cudaError_t launch_window_of(const WeightParams& p, cudaStream_t st) {
     q.w = p;
     q.first = t;
     q.rows = (p.T - t < each ? p.T - t : each) * p.G;
+    q.queries = each;
     if (t > 0) q.w.decay = 1.f;
-    e = launch(fn, static_cast<unsigned>(pairs * C), kWindowThreads, C, st, smem, q);
+    e = launch(fn, static_cast<unsigned>(pairs * C), kWindowThreads, C, st, smem, q, query, key);
     if (e != cudaSuccess) return e;
   }
   return cudaSuccess;
@@ -428,12 +457,17 @@ cudaError_t launch_window_of(const WeightParams& p, cudaStream_t st) {
 
 }  // namespace
 
-bool window_fits(const WeightParams& p) { return p.G <= kLanes && p.D <= 256 && p.D % 8 == 0; }
-
-int launch_cache_window(const WeightParams& p, qrita_stream_t stream) {
+bool launch_cache_window(const WeightParams& p, qrita_stream_t stream, int* result) {
+  if (p.G > kLanes || p.D > 256 || p.c.B > INT32_MAX || p.c.S > INT32_MAX - 2 * kLanes) return false;
+  CUtensorMap query, key;
+  if (!make_map(&query, p.query, {p.D, p.c.H * p.G, p.T, p.c.B}, {p.q_head, p.q_token, p.q_batch}, p.G, kLanes / p.G) ||
+      !make_map(&key, p.keys, {p.D, p.c.S, p.c.H, p.c.B}, {p.k_slot, p.k_head, p.k_batch}, kLanes, 1))
+    return false;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  if (p.D <= 64) return static_cast<int>(launch_window_of<1>(p, st));
-  return static_cast<int>(p.D <= 128 ? launch_window_of<2>(p, st) : launch_window_of<4>(p, st));
+  *result = static_cast<int>(p.D <= 64    ? launch_window_of<1>(p, query, key, st)
+                             : p.D <= 128 ? launch_window_of<2>(p, query, key, st)
+                                          : launch_window_of<4>(p, query, key, st));
+  return true;
 }
 
 }  // namespace qrita
