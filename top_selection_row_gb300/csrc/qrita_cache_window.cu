@@ -13,7 +13,7 @@
 // bytes). Keys are read again for the second product: a share of a thousand slots is
 // small enough that they come from L2.
 //
-// A CTA has an SM: two groups of four warps, the lanes' threads of every other tile,
+// A CTA has an SM: four groups of four warps, the lanes' threads of a tile in turn,
 // a warp that issues the products and one that asks for the tiles (TMA). Four
 // accumulators of 128 columns, all of the tensor memory, and as many stages of keys as
 // shared memory has, so that copies are under way while products and exponentials
@@ -35,7 +35,7 @@ namespace {
 
 constexpr float kLog2e = 1.44269504088896340736f;
 constexpr int kLanes = 128;              // threads of a group, slots of a tile, rows at most
-constexpr int kGroups = 2;
+constexpr int kGroups = 4;
 constexpr int kWindowThreads = kGroups * kLanes + 64;
 constexpr int kBuffers = 4;              // accumulators
 constexpr int kColumns = kBuffers * kLanes;
@@ -263,7 +263,7 @@ window_kernel(const WindowParams wp, const __grid_constant__ CUtensorMap query_m
     int32_t at = position(lo + group * kLanes + t);
     int it = group;
     for (; it < tiles; it += kGroups) {
-      int* of = tile_positions[group][it / kGroups & 1];
+      int* of = tile_positions[group][(it / kGroups) & 1];
       of[t] = at;
       const bool all = lanes_all(at <= first, group);
       at = position(lo + static_cast<int64_t>(it + kGroups) * kLanes + t);
@@ -271,15 +271,14 @@ window_kernel(const WindowParams wp, const __grid_constant__ CUtensorMap query_m
       __syncwarp();
       fence_after();
       const uint32_t from = mine + it % kBuffers * kLanes;
-      uint32_t words[2][32];
-      columns32(from, words[0]);
-#pragma unroll
+#pragma unroll 1
       for (int c = 0; c < kLanes; c += 32) {
-        columns_wait(words[c / 32 & 1]);
-        if (c + 32 < kLanes) columns32(from + c + 32, words[(c / 32 + 1) & 1]);
+        uint32_t words[32];
+        columns32(from + c, words);
+        columns_wait(words);
         float x[32];
 #pragma unroll
-        for (int i = 0; i < 32; ++i) x[i] = __uint_as_float(words[c / 32 & 1][i]);
+        for (int i = 0; i < 32; ++i) x[i] = __uint_as_float(words[i]);
         if (!all) {
           // (no exponential of what is not seen: its place is that of a logit of -inf)
 #pragma unroll
@@ -310,7 +309,7 @@ window_kernel(const WindowParams wp, const __grid_constant__ CUtensorMap query_m
       arrive(smem_u32(&taken[it % kBuffers]));
     }
     sums[group][t] = {top, s2.x + s2.y};
-    auto both_groups = [&]() { asm volatile("bar.sync 3, %0;" ::"n"(kGroups * kLanes) : "memory"); };
+    auto both_groups = [&]() { asm volatile("bar.sync 15, %0;" ::"n"(kGroups * kLanes) : "memory"); };
     if (C > 1) {
       cluster_arrive();
       cluster_wait();
@@ -335,7 +334,7 @@ window_kernel(const WindowParams wp, const __grid_constant__ CUtensorMap query_m
     if (C > 1) cluster_arrive();  // (the other CTAs may end)
     both_groups();
     // The slots' weights.
-    it = tiles + ((tiles ^ group) & 1);
+    it = tiles + (group + kGroups - tiles % kGroups) % kGroups;
     at = position(lo + static_cast<int64_t>(2 * tiles - 1 - it) * kLanes + t);
     for (; it < 2 * tiles; it += kGroups) {
       const int64_t s = lo + static_cast<int64_t>(2 * tiles - 1 - it) * kLanes + t;
@@ -349,16 +348,14 @@ window_kernel(const WindowParams wp, const __grid_constant__ CUtensorMap query_m
       const uint32_t from = mine + it % kBuffers * kLanes;
       const bool all_rows = __all_sync(kAll, least == 0);
       float2 w = both(0.f);
-      uint32_t words[2][32];
-      columns32(from, words[0]);
-#pragma unroll
-      for (int c = 0; c < kLanes; c += 32) {
-        columns_wait(words[c / 32 & 1]);
-        if (c >= columns) break;
-        if (c + 32 < kLanes && c + 32 < columns) columns32(from + c + 32, words[(c / 32 + 1) & 1]);
+#pragma unroll 1
+      for (int c = 0; c < columns; c += 32) {
+        uint32_t words[32];
+        columns32(from + c, words);
+        columns_wait(words);
         float x[32];
 #pragma unroll
-        for (int i = 0; i < 32; ++i) x[i] = __uint_as_float(words[c / 32 & 1][i]);
+        for (int i = 0; i < 32; ++i) x[i] = __uint_as_float(words[i]);
         const float2 cc = both(scale);
         if (all_rows && c + 32 <= R) {
 #pragma unroll
@@ -437,9 +434,12 @@ cudaError_t launch_window_of(const WeightParams& p, const CUtensorMap& query, co
   cudaError_t e = cudaFuncSetAttribute(reinterpret_cast<const void*>(fn), cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        static_cast<int>(smem));
   if (e != cudaSuccess) return e;
-  // As many CTAs as are on the device at once, with two tiles each at least.
+  // As many CTAs as are on the device at once, with two tiles each at least, and
+  // clusters of 8 at most: 16 SMs are rarely free together (8 heads of 32768 slots, 512
+  // rows in four launches: 8 CTAs a head 229 us, 16 CTAs 276; 64 heads of 16384, 128
+  // rows, with two groups: 2 CTAs a head 114, 1 CTA 216, 4 CTAs 122).
   uint32_t C = 1;
-  while (C < kMaxRanks && pairs * 2 * C <= device_sms() && p.c.S >= kLanes * 2 * static_cast<int64_t>(C)) C *= 2;
+  while (C < 8 && pairs * 2 * C <= device_sms() && p.c.S >= kLanes * 2 * static_cast<int64_t>(C)) C *= 2;
   // as many whole queries at a time as there are lanes for
   const int each = kLanes / p.G;
   for (int t = 0; t < p.T; t += each) {
