@@ -741,26 +741,48 @@ def qrita_token_scores_grad(logits, ids, grad_logp=None, grad_entropy=None, mask
 EvictedCache = namedtuple("EvictedCache", "keys values weights positions slots lengths")
 
 _Strides = ctypes.c_int64 * 3
+_strides_made = {}
 
 
-def _cache(t, name, device=None, shape=None):
-    """Strides in bytes and the bytes of a row of a [B, H, S, D] (or [B, H, D])
-    tensor whose rows are contiguous; any type."""
-    if t.dim() not in (3, 4) or not t.is_cuda or (device is not None and t.device != device):
-        raise ValueError(f"{name} must be a CUDA [B, H, S, D] tensor" + (f" on {device}" if device is not None else ""))
-    if shape is not None and t.shape != shape:
+def _strides(values, unit):
+    """Up to three strides of `unit` bytes each, as the library takes them. (Made once
+    for the same numbers: to make an array takes as long as the other checks.)"""
+    got = _strides_made.get((values, unit))
+    if got is None:
+        if len(_strides_made) > 1000:
+            _strides_made.clear()
+        got = _strides_made[values, unit] = _Strides(*(v * unit for v in values))
+    return got
+
+
+def _cache(t, name, device, shape=None, unit=None):
+    """Strides and the bytes of a row of a [B, H, S, D] (or [B, H, D]) tensor whose
+    rows are contiguous, of any type; ``unit``: strides in elements."""
+    size = t.shape
+    if shape is not None and size != shape:
         raise ValueError(f"{name} must be {list(shape)}")
-    e, strides = t.element_size(), t.stride()
-    if t.shape[-1] < 1 or (t.shape[-1] > 1 and strides[-1] != 1):
+    if t.device != device:
+        raise ValueError(f"{name} must be a CUDA tensor on {device}")
+    strides = t.stride()
+    D = size[-1]
+    if D < 1 or (D > 1 and strides[-1] != 1):
         raise ValueError(f"{name}: a row must be contiguous")
-    if t.dim() == 4 and t.shape[2] < 2:
-        strides = (*strides[:2], t.shape[-1], 1)
-    return _Strides(*(v * e for v in strides[:-1])), t.shape[-1] * e
+    strides = strides[:-1]
+    if len(strides) == 3 and size[2] < 2:
+        strides = (*strides[:2], D)
+    e = t.element_size()
+    return _strides(strides, unit or e), D * e
+
+
+def _slots_of(keys):
+    if keys.dim() != 4 or not keys.is_cuda:
+        raise ValueError("keys must be a CUDA [B, H, S, D] tensor")
+    return keys.shape, keys.device
 
 
 def _written(t, name):
     """Refuses tensors that are written where rows share memory (expanded ones)."""
-    if any(n > 1 and s == 0 for n, s in zip(t.shape, t.stride())):
+    if 0 in t.stride() and any(n > 1 and s == 0 for n, s in zip(t.shape, t.stride())):
         raise ValueError(f"{name} is written: its rows must not share memory")
 
 
@@ -790,21 +812,20 @@ def qrita_cache_weights(query, keys, weights, lengths, positions=None, seen=None
     """
     if stream is not None:
         return _on_stream(stream, qrita_cache_weights, query, keys, weights, lengths, positions, seen, scale, decay)
-    if query.dim() != 4 or keys.dim() != 4:
-        raise ValueError("query must be [B, T, H G, D] and keys [B, H, S, D]")
-    B, H, S, D = keys.shape
-    T, heads = query.shape[1:3]
+    (B, H, S, D), dev = _slots_of(keys)
+    if query.dim() != 4:
+        raise ValueError("query must be [B, T, H G, D] for keys of [B, H, S, D]")
+    _, T, heads, _ = query.shape
     if query.shape != (B, T, heads, D) or H < 1 or heads < 1 or heads % H or T < 1:
         raise ValueError("query must be [B, T, H G, D] for keys of [B, H, S, D]")
     if query.dtype != keys.dtype:
         raise TypeError("query and keys must have one type")
-    dev = keys.device
-    _cache(keys, "keys")
-    _cache(query, "query", dev)
+    ks, _ = _cache(keys, "keys", dev, unit=1)
+    qs, _ = _cache(query, "query", dev, unit=1)
     dt = _dtype_code(keys)
     w, n, at, se = _order(weights, lengths, positions, seen, B, H, S, dev)
-    _call(lib().qrita_cache_weights, dev, B, H, S, query.data_ptr(), dt, T, heads // H, D, _Strides(*query.stride()[:3]),
-          keys.data_ptr(), _Strides(*keys.stride()[:3]), D ** -0.5 if scale is None else scale, decay, n, at, se, w)
+    _call(lib().qrita_cache_weights, dev, B, H, S, query.data_ptr(), dt, T, heads // H, D, qs,
+          keys.data_ptr(), ks, D ** -0.5 if scale is None else scale, decay, n, at, se, w)
     _wrote(weights)
     return weights
 
@@ -827,20 +848,18 @@ def qrita_cache_evict(keys, values, weights, lengths, budget, sink=0, recent=0, 
         return _on_stream(stream, qrita_cache_evict, keys, values, weights, lengths, budget, sink, recent, positions, seen,
                           None, out)
     torch = _torch()
-    if keys.dim() != 4:
-        raise ValueError("keys must be [B, H, S, D]")
-    B, H, S, _ = keys.shape
-    dev = keys.device
-    ks, kb = _cache(keys, "keys")
-    vs, vb = _cache(values, "values", dev, (B, H, S, values.shape[-1]))
+    (B, H, S, Dk), dev = _slots_of(keys)
+    Dv = values.shape[-1]
+    ks, kb = _cache(keys, "keys", dev)
+    vs, vb = _cache(values, "values", dev, (B, H, S, Dv))
     w, n, at, se = _order(weights, lengths, positions, seen, B, H, S, dev)
     budget = int(budget)
     if budget < 1 or H < 1 or S < 1:
         raise ValueError("a cache has heads and slots, and a budget of at least one")
     if out is None:
         i32 = torch.int32
-        got = EvictedCache(torch.empty((B, H, budget, keys.shape[3]), dtype=keys.dtype, device=dev),
-                           torch.empty((B, H, budget, values.shape[3]), dtype=values.dtype, device=dev),
+        got = EvictedCache(torch.empty((B, H, budget, Dk), dtype=keys.dtype, device=dev),
+                           torch.empty((B, H, budget, Dv), dtype=values.dtype, device=dev),
                            torch.empty((B, H, budget), dtype=torch.float32, device=dev),
                            torch.empty((B, H, budget), dtype=i32, device=dev),
                            torch.empty((B, H, budget), dtype=i32, device=dev), torch.empty(B, dtype=i32, device=dev))
@@ -858,8 +877,8 @@ def qrita_cache_evict(keys, values, weights, lengths, budget, sink=0, recent=0, 
         _written(got.keys, "out keys")
         _written(got.values, "out values")
     more = got.keys.shape[2]
-    oks, _ = _cache(got.keys, "out keys", dev, (B, H, more, keys.shape[3]))
-    ovs, _ = _cache(got.values, "out values", dev, (B, H, more, values.shape[3]))
+    oks, _ = _cache(got.keys, "out keys", dev, (B, H, more, Dk))
+    ovs, _ = _cache(got.values, "out values", dev, (B, H, more, Dv))
     _call(lib().qrita_cache_evict, dev, B, H, S, n, w, at, se, budget, sink, recent, keys.data_ptr(), kb, ks,
           values.data_ptr(), vb, vs, got.keys.data_ptr(), oks, got.values.data_ptr(), ovs, more, got.weights.data_ptr(),
           got.positions.data_ptr(), got.slots.data_ptr(), got.lengths.data_ptr())
@@ -882,12 +901,10 @@ def qrita_cache_insert(keys, values, weights, positions, lengths, seen, new_keys
         return _on_stream(stream, qrita_cache_insert, keys, values, weights, positions, lengths, seen, new_keys, new_values,
                           budget, sink, recent, None, out)
     torch = _torch()
-    if keys.dim() != 4:
-        raise ValueError("keys must be [B, H, S, D]")
-    B, H, S, _ = keys.shape
-    dev = keys.device
-    ks, kb = _cache(keys, "keys")
-    vs, vb = _cache(values, "values", dev, (B, H, S, values.shape[-1]))
+    (B, H, S, Dk), dev = _slots_of(keys)
+    Dv = values.shape[-1]
+    ks, kb = _cache(keys, "keys", dev)
+    vs, vb = _cache(values, "values", dev, (B, H, S, Dv))
     _written(keys, "keys")
     _written(values, "values")
     if positions is None or seen is None:
@@ -895,8 +912,8 @@ def qrita_cache_insert(keys, values, weights, positions, lengths, seen, new_keys
     w, n, at, se = _order(weights, lengths, positions, seen, B, H, S, dev)
     if new_keys.dtype != keys.dtype or new_values.dtype != values.dtype:
         raise TypeError("new_keys and new_values must have the types of keys and values")
-    nks, _ = _cache(new_keys, "new_keys", dev, (B, H, keys.shape[3]))
-    nvs, _ = _cache(new_values, "new_values", dev, (B, H, values.shape[3]))
+    nks, _ = _cache(new_keys, "new_keys", dev, (B, H, Dk))
+    nvs, _ = _cache(new_values, "new_values", dev, (B, H, Dv))
     if out is None:
         slots = torch.empty((B, H), dtype=torch.int32, device=dev)
     else:

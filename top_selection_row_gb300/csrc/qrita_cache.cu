@@ -370,8 +370,8 @@ cudaError_t launch_weights_of(const WeightParams& p, cudaStream_t st) {
   q.stash = fits(C) ? static_cast<int32_t>(floats(C)) : 0;
   const size_t smem = fixed + static_cast<size_t>(q.stash * R) * 4;
   auto* fn = &weights_kernel<SC, BYTES>;
-  const cudaError_t e = cudaFuncSetAttribute(reinterpret_cast<const void*>(fn), cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             static_cast<int>(kMost));
+  static std::atomic<uint64_t> done{0};
+  const cudaError_t e = allow_smem(fn, kMost, done);
   if (e != cudaSuccess) return e;
   return launch(fn, static_cast<unsigned>(pairs * C), kWThreads, C, st, smem, q);
 }
@@ -387,20 +387,26 @@ cudaError_t launch_weights_mma(const WeightParams& p, cudaStream_t st) {
 // ---------------------------------------------------------------------------
 // Eviction: the kept slots of each (sequence, kv head), then their rows.
 // ---------------------------------------------------------------------------
-constexpr int kSelThreads = 512;
+constexpr int kSelThreads = 1024;
 constexpr int kSelWarps = kSelThreads / 32;
-constexpr int kBins = 256;
+constexpr int kBins = 2048;
+constexpr int kFew = 2048;            // keys of a CTA in the boundary's first bin, where they fit
 constexpr int kMaxShare = 48 * 1024;  // keys a CTA keeps in shared memory
 
-// Selection of the first `keep` slots in order: the keep-th largest key by four
-// histograms of 8 bits (integers: any order of the atomics gives the same), then the
-// slots above it and the first of those equal to it, in slot order.
+// Selection of the first `keep` slots in order: the keep-th largest key by histograms
+// of 11, 11 and 10 bits (integers: any order of the atomics gives the same), then the
+// slots above it and the first of those equal to it, in slot order. The first digit has
+// a weight's exponent and two bits more, so that few of a warp's weights meet in a bin;
+// the last digit needs the keys alone that share it. A row has one CTA while its keys
+// fit in shared memory: a barrier of a cluster costs as much as a thousand keys.
 __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictParams p) {
   extern __shared__ __align__(16) unsigned char dynamic[];
   uint32_t* own = reinterpret_cast<uint32_t*>(dynamic);
+  __shared__ uint32_t few[kFew];
+  __shared__ uint32_t n_few;
   __shared__ uint32_t hist[kBins];
   __shared__ uint32_t all[kBins];
-  __shared__ uint32_t counts[2];           // this CTA's protected slots; chosen bin
+  __shared__ uint32_t counts[1];           // this CTA's protected slots
   __shared__ uint32_t above_of, digit_of;
   __shared__ uint32_t warp_more[kSelWarps], warp_same[kSelWarps];
   __shared__ uint32_t tally[2];            // this CTA's slots above the boundary, and equal to it
@@ -414,42 +420,72 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictPa
   const Guard guard(p.c, b, n);
   const float* weights = p.c.weights + bh * p.c.S;
   const int32_t* positions = p.c.positions != nullptr ? p.c.positions + bh * p.c.S : nullptr;
-  const int64_t row = bh * p.out_slots_of;
   int32_t* slots = p.out_slots + bh * p.c.budget;
-  auto write = [&](int32_t at, int32_t s) {
-    slots[at] = s;
-    p.out_weights[row + at] = weights[s];
-    p.out_positions[row + at] = positions != nullptr ? positions[s] : s;
-  };
   if (rank == 0) {
     if (bh % p.c.H == 0 && tid == 0) p.out_lengths[b] = keep;
-    for (int32_t i = keep + tid; i < p.c.budget; i += kSelThreads) {
-      slots[i] = -1;
-      p.out_weights[row + i] = 0.f;
-      p.out_positions[row + i] = -1;
-    }
+    for (int64_t i = static_cast<int64_t>(keep) + tid; i < p.c.budget; i += kSelThreads) slots[i] = -1;
   }
   if (n <= p.c.budget) {  // (the same in every CTA of the cluster)
-    for (int32_t i = rank * kSelThreads + tid; i < n; i += C * kSelThreads) write(i, i);
+    for (int64_t i = rank * kSelThreads + tid; i < n; i += C * kSelThreads) slots[i] = static_cast<int32_t>(i);
     return;
   }
   if (C > 1) cluster_arrive_relaxed();  // every CTA of the cluster runs before its memory is read
-  const int32_t share = (n + static_cast<int32_t>(C) - 1) / static_cast<int32_t>(C);
-  const int32_t lo = min(n, static_cast<int32_t>(rank) * share), hi = min(n, lo + share);
+  const int64_t share = (static_cast<int64_t>(n) + C - 1) / C;
+  const int32_t lo = static_cast<int32_t>(min(static_cast<int64_t>(n), rank * share));
+  const int32_t hi = static_cast<int32_t>(min(static_cast<int64_t>(n), lo + share));
   const bool kept_here = share <= p.share;
   auto raw = [&](int32_t s, bool& held) {
     held = guard.holds(positions != nullptr ? positions[s] : s);
     return weight_key(weights[s]);
   };
-  if (tid == 0) counts[0] = 0u;
+  if (tid == 0) counts[0] = n_few = 0u;
+  for (int i = tid; i < kBins; i += kSelThreads) hist[i] = 0u;
   __syncthreads();
-  // protected slots: they are kept, or (more than the budget) the choice is theirs
+  // Protected slots: they are kept, or (more than the budget) the choice is theirs. The
+  // keys go to shared memory and, while that is the usual case, to the first histogram.
   uint32_t mine = 0;
-  for (int32_t s = lo + tid; s < hi; s += kSelThreads) {
-    bool held;
-    const uint32_t k = raw(s, held);
-    if (kept_here) own[s - lo] = held ? 0xFFFFFFFFu : k;
+  auto take = [&](int64_t s, float w, int32_t at) {
+    const bool held = guard.holds(at);
+    const uint32_t k = held ? 0xFFFFFFFFu : weight_key(w);
     mine += held;
+    atomicAdd(&hist[k >> 21], 1u);
+    return k;
+  };
+  if (kept_here && ((reinterpret_cast<uintptr_t>(weights + lo) | reinterpret_cast<uintptr_t>(positions)) & 15u) == 0 &&
+      (positions == nullptr || (reinterpret_cast<uintptr_t>(positions + lo) & 15u) == 0)) {
+    constexpr int kFlight = 4;  // 16-byte loads of a thread under way
+    const int n4 = (hi - lo) / 4;
+    for (int i0 = tid; i0 < n4; i0 += kFlight * kSelThreads) {
+      float4 w[kFlight];
+      int4 at[kFlight];
+#pragma unroll
+      for (int i = 0; i < kFlight; ++i) {
+        const int j = i0 + i * kSelThreads;
+        if (j >= n4) continue;
+        w[i] = reinterpret_cast<const float4*>(weights + lo)[j];
+        const int32_t s = lo + 4 * j;
+        at[i] = positions != nullptr ? reinterpret_cast<const int4*>(positions + lo)[j] : make_int4(s, s + 1, s + 2, s + 3);
+      }
+#pragma unroll
+      for (int i = 0; i < kFlight; ++i) {
+        const int j = i0 + i * kSelThreads;
+        if (j >= n4) continue;
+        const int64_t s = lo + 4 * j;
+        uint4 k;
+        k.x = take(s, w[i].x, at[i].x);
+        k.y = take(s + 1, w[i].y, at[i].y);
+        k.z = take(s + 2, w[i].z, at[i].z);
+        k.w = take(s + 3, w[i].w, at[i].w);
+        reinterpret_cast<uint4*>(own)[j] = k;
+      }
+    }
+    const int32_t s = lo + 4 * n4 + tid;
+    if (s < hi) own[s - lo] = take(s, weights[s], positions != nullptr ? positions[s] : s);
+  } else {
+    for (int64_t s = lo + tid; s < hi; s += kSelThreads) {
+      const uint32_t k = take(s, weights[s], positions != nullptr ? positions[s] : static_cast<int32_t>(s));
+      if (kept_here) own[s - lo] = k;
+    }
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(kAll, mine, o);
@@ -457,101 +493,161 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictPa
   if (C > 1) cluster_wait();
   row_sync(C);
   uint32_t held_all = 0;
-  for (uint32_t c = 0; c < C; ++c) held_all += ld_dsmem_u32(map_rank(smem_u32(&counts[0]), c));
+  if (C == 1) held_all = counts[0];
+  for (uint32_t c = 0; C > 1 && c < C; ++c) held_all += ld_dsmem_u32(map_rank(smem_u32(&counts[0]), c));
   const bool crowded = held_all > static_cast<uint32_t>(keep);
   // the key of slot s: of protected ones above all others, or all others below them
-  auto key = [&](int32_t s) {
-    if (!crowded && kept_here) return own[s - lo];
+  auto made = [&](int32_t s) {
     bool held;
     const uint32_t k = raw(s, held);
     return crowded ? (held ? max(k, 1u) : 0u) : (held ? 0xFFFFFFFFu : k);
   };
+  if (crowded && kept_here)
+    for (int64_t s = lo + tid; s < hi; s += kSelThreads) own[s - lo] = made(static_cast<int32_t>(s));
+  auto key = [&](int32_t s) { return kept_here ? own[s - lo] : made(s); };
   uint32_t prefix = 0, left = static_cast<uint32_t>(keep);  // the boundary's digits so far; its rank among those that share them
-  for (int shift = 24; shift >= 0; shift -= 8) {
-    for (int i = tid; i < kBins; i += kSelThreads) hist[i] = 0u;
-    __syncthreads();
-    for (int32_t s = lo + tid; s < hi; s += kSelThreads) {
-      const uint32_t k = key(s);
-      if (shift == 24 || (k >> (shift + 8)) == prefix) atomicAdd(&hist[(k >> shift) & 255u], 1u);
+  for (int round = 0; round < 3; ++round) {
+    const int shift = round == 0 ? 21 : round == 1 ? 10 : 0, bits = round < 2 ? 11 : 10;
+    const bool done = round == 0 && !crowded;  // (by the first pass)
+    if (!done) {
+      for (int i = tid; i < kBins; i += kSelThreads) hist[i] = 0u;
+      __syncthreads();
+    }
+    if (done) {
+    } else if (round == 2 && n_few <= kFew) {
+      for (uint32_t i = tid; i < n_few; i += kSelThreads)
+        if (few[i] >> 10 == prefix) atomicAdd(&hist[few[i] & 1023u], 1u);
+    } else {
+      const int all_of = (hi - lo + 31) / 32 * 32;  // (warps in step, for their ballots)
+#pragma unroll 4
+      for (int i = tid; i < all_of; i += kSelThreads) {
+        const uint32_t k = i < hi - lo ? key(lo + i) : 0u;
+        const bool in = i < hi - lo && (round == 0 || k >> (shift + bits) == prefix);
+        if (in) atomicAdd(&hist[(k >> shift) & ((1u << bits) - 1u)], 1u);
+        const uint32_t which = __ballot_sync(kAll, in);
+        if (round == 1 && which != 0u) {
+          uint32_t at = 0u;
+          if (lane == 0) at = atomicAdd(&n_few, static_cast<uint32_t>(__popc(which)));
+          at = __shfl_sync(kAll, at, 0) + __popc(which & ((1u << lane) - 1u));
+          if (in && at < kFew) few[at] = k;
+        }
+      }
     }
     row_sync(C);
-    for (int i = tid; i < kBins; i += kSelThreads) {
-      uint32_t v = 0;
-      for (uint32_t c = 0; c < C; ++c) v += ld_dsmem_u32(map_rank(smem_u32(&hist[i]), c));
-      all[i] = v;
+    const uint32_t* sums = hist;
+    if (C > 1) {
+      for (int i = tid; i < kBins; i += kSelThreads) {
+        uint32_t v = 0;
+        for (uint32_t c = 0; c < C; ++c) v += ld_dsmem_u32(map_rank(smem_u32(&hist[i]), c));
+        all[i] = v;
+      }
+      row_sync(C);  // (the histograms have been read)
+      sums = all;
+    }
+    // two bins a thread, the largest first
+    constexpr int kEach = kBins / kSelThreads;
+    static_assert(kEach == 2, "two bins a thread");
+    const int top = kBins - 1 - kEach * tid;
+    const uint32_t v0 = sums[top], v1 = sums[top - 1];
+    uint32_t upto = v0 + v1;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint32_t up = __shfl_up_sync(kAll, upto, o);
+      if (lane >= o) upto += up;
+    }
+    if (lane == 31) warp_more[warp] = upto;
+    __syncthreads();
+    const uint32_t ahead = lane < warp ? warp_more[lane] : 0u;
+    const uint32_t before = __reduce_add_sync(kAll, ahead) + upto - (v0 + v1);
+    if (before < left && left <= before + v0) {
+      digit_of = static_cast<uint32_t>(top);
+      above_of = before;
+    } else if (before + v0 < left && left <= before + v0 + v1) {
+      digit_of = static_cast<uint32_t>(top - 1);
+      above_of = before + v0;
     }
     __syncthreads();
-    if (warp == 0) {
-      // 8 bins a lane, the largest first
-      uint32_t v[8], sum = 0;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) sum += v[i] = all[255 - (lane * 8 + i)];
-      uint32_t before = sum;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const uint32_t up = __shfl_up_sync(kAll, before, o);
-        if (lane >= o) before += up;
-      }
-      before -= sum;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        if (before < left && left <= before + v[i]) {
-          digit_of = 255u - static_cast<uint32_t>(lane * 8 + i);
-          above_of = before;
-        }
-        before += v[i];
-      }
-    }
-    __syncthreads();
-    prefix = prefix << 8 | digit_of;
+    prefix = prefix << bits | digit_of;
     left -= above_of;
-    row_sync(C);  // (the histograms have been read)
   }
-  // slots above the boundary and equal to it: counts by warp, each with its own range
-  const int32_t span = ((hi - lo + kSelWarps - 1) / kSelWarps + 31) / 32 * 32;
-  const int32_t w_lo = min(hi, lo + warp * span), w_hi = min(hi, w_lo + span);
+  // Slots above the boundary and equal to it. A warp has a range of its own, 32 slots a
+  // step; a lane keeps the ballots of one step of 32, so that no key is read again
+  // where a range is 1024 slots or fewer.
+  const int64_t span = ((static_cast<int64_t>(hi) - lo + kSelWarps - 1) / kSelWarps + 31) / 32 * 32;
+  const int64_t w_lo = min(static_cast<int64_t>(hi), lo + warp * span), w_hi = min(static_cast<int64_t>(hi), w_lo + span);
+  uint32_t gt = 0u, eq = 0u;  // of the lane's step
+  auto ballots = [&](int64_t from) {
+    gt = eq = 0u;
+    const int steps = static_cast<int>(min((w_hi - from + 31) / 32, static_cast<int64_t>(32)));
+#pragma unroll 4
+    for (int i = 0; i < steps; ++i) {
+      const int64_t s = from + 32 * i + lane;
+      const bool some = s < w_hi;
+      const uint32_t k = some ? key(static_cast<int32_t>(s)) : 0u;
+      const uint32_t g = __ballot_sync(kAll, some && k > prefix), e = __ballot_sync(kAll, some && k == prefix);
+      if (lane == i) {
+        gt = g;
+        eq = e;
+      }
+    }
+    return steps;
+  };
+  constexpr int kSpan = 32 * 32;
   uint32_t more = 0, same = 0;
-  for (int32_t s0 = w_lo; s0 < w_hi; s0 += 32) {
-    const int32_t s = s0 + lane;
-    const uint32_t k = s < w_hi ? key(s) : 0u;
-    more += __popc(__ballot_sync(kAll, s < w_hi && k > prefix));
-    same += __popc(__ballot_sync(kAll, s < w_hi && k == prefix));
+  for (int64_t from = w_lo; from < w_hi; from += kSpan) {
+    ballots(from);
+    more += __reduce_add_sync(kAll, static_cast<uint32_t>(__popc(gt)));
+    same += __reduce_add_sync(kAll, static_cast<uint32_t>(__popc(eq)));
   }
   if (lane == 0) {
     warp_more[warp] = more;
     warp_same[warp] = same;
   }
   __syncthreads();
-  if (tid == 0) {
-    uint32_t m = 0, e = 0;
-    for (int w = 0; w < kSelWarps; ++w) {
-      m += warp_more[w];
-      e += warp_same[w];
+  // those of the warps before this one, and of the CTAs before
+  uint32_t m0 = __reduce_add_sync(kAll, lane < warp ? warp_more[lane] : 0u);
+  uint32_t e0 = __reduce_add_sync(kAll, lane < warp ? warp_same[lane] : 0u);
+  if (C > 1) {
+    if (tid == kSelThreads - 1) {
+      tally[0] = m0 + more;
+      tally[1] = e0 + same;
     }
-    tally[0] = m;
-    tally[1] = e;
+    cluster_sync_all();
+    for (uint32_t c = 0; c < rank; ++c) {
+      m0 += ld_dsmem_u32(map_rank(smem_u32(&tally[0]), c));
+      e0 += ld_dsmem_u32(map_rank(smem_u32(&tally[1]), c));
+    }
+    cluster_arrive();
   }
-  row_sync(C);
-  uint32_t m0 = 0, e0 = 0;
-  for (uint32_t c = 0; c < rank; ++c) {
-    m0 += ld_dsmem_u32(map_rank(smem_u32(&tally[0]), c));
-    e0 += ld_dsmem_u32(map_rank(smem_u32(&tally[1]), c));
-  }
-  if (C > 1) cluster_arrive();
-  for (int w = 0; w < warp; ++w) {
-    m0 += warp_more[w];
-    e0 += warp_same[w];
-  }
-  for (int32_t s0 = w_lo; s0 < w_hi; s0 += 32) {
-    const int32_t s = s0 + lane;
-    const uint32_t k = s < w_hi ? key(s) : 0u;
-    const uint32_t gt = __ballot_sync(kAll, s < w_hi && k > prefix), eq = __ballot_sync(kAll, s < w_hi && k == prefix);
-    const uint32_t below = (1u << lane) - 1u;
-    const uint32_t e = e0 + __popc(eq & below);  // equal ones before this slot
-    const bool kept = (gt >> lane & 1u) != 0u || ((eq >> lane & 1u) != 0u && e < left);
-    if (kept) write(static_cast<int32_t>(m0 + __popc(gt & below) + min(e, left)), s);
-    m0 += __popc(gt);
-    e0 += __popc(eq);
+  for (int64_t from = w_lo; from < w_hi; from += kSpan) {
+    int steps = 32;
+    if (span > kSpan)
+      steps = ballots(from);
+    else
+      steps = static_cast<int>((w_hi - from + 31) / 32);
+    uint32_t m = __popc(gt), e = __popc(eq);
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint32_t um = __shfl_up_sync(kAll, m, o), ue = __shfl_up_sync(kAll, e, o);
+      if (lane >= o) {
+        m += um;
+        e += ue;
+      }
+    }
+    const uint32_t e_before = e0 + e - __popc(eq), m_before = m0 + m - __popc(gt);
+    // of the equal ones, those that there is room for
+    uint32_t kept = eq;
+    const uint32_t room = left > e_before ? left - e_before : 0u;
+    while (static_cast<uint32_t>(__popc(kept)) > room) kept &= ~(0x80000000u >> __clz(kept));
+    kept |= gt;
+    const uint32_t first = m_before + min(e_before, left);
+#pragma unroll 4
+    for (int i = 0; i < steps; ++i) {
+      const uint32_t mask = __shfl_sync(kAll, kept, i), at = __shfl_sync(kAll, first, i);
+      if (mask >> lane & 1u) slots[at + __popc(mask & ((1u << lane) - 1u))] = static_cast<int32_t>(from) + 32 * i + lane;
+    }
+    m0 += __shfl_sync(kAll, m, 31);
+    e0 += __shfl_sync(kAll, e, 31);
   }
   if (C > 1) cluster_wait();
 }
@@ -572,6 +668,22 @@ struct UnitOf<1> {
 };
 
 constexpr int kGatherThreads = 256;
+
+// Weights and positions of `count` kept slots from the first-th on; by N threads.
+template <int N>
+__device__ __forceinline__ void gather_order(const EvictParams& p, int64_t bh, int64_t first, int count) {
+  for (int i = threadIdx.x; i < count; i += N) {
+    const int32_t s = p.out_slots[bh * p.c.budget + first + i];
+    float w = 0.f;
+    int32_t at = -1;
+    if (s >= 0) {
+      w = p.c.weights[bh * p.c.S + s];
+      at = p.c.positions != nullptr ? p.c.positions[bh * p.c.S + s] : s;
+    }
+    p.out_weights[bh * p.out_slots_of + first + i] = w;
+    p.out_positions[bh * p.out_slots_of + first + i] = at;
+  }
+}
 
 // The kept rows: threads take units of rows in turn, several loads in flight.
 template <int UNIT>
@@ -606,6 +718,57 @@ __device__ __forceinline__ uint64_t alignment_of(const CacheRows& r) {
 }
 
 constexpr int kGatherRows = 64;
+constexpr int kBulkThreads = 64;         // and rows of a CTA, at most
+constexpr int kBulkBytes = 16 * 1024;    // of its rows
+constexpr uint64_t kBulkLimitNs = 10ull * 1000 * 1000 * 1000;
+
+// The same for rows of 16-byte units on their boundaries, by bulk copies (TMA): a
+// thread asks for a row each, and the rows leave together where they lie one after
+// another. Thirteen CTAs on an SM have 208 KB on their way.
+__global__ void __launch_bounds__(kBulkThreads) evict_bulk_kernel(const EvictParams p, int per) {
+  __shared__ __align__(128) unsigned char rows[kBulkBytes];
+  __shared__ __align__(8) uint64_t bar;
+  const int tid = threadIdx.x;
+  if (tid == 0) {
+    mbar_init(smem_u32(&bar), 1);
+    fence_mbar_init();
+  }
+  __syncthreads();
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const int64_t parts = (p.c.budget + per - 1) / per;
+  const int64_t bh = blockIdx.x / parts, first = blockIdx.x % parts * per, b = bh / p.c.H, h = bh % p.c.H;
+  const int count = static_cast<int>(min(static_cast<int64_t>(per), p.c.budget - first));
+  const CacheRows& from = blockIdx.y == 0 ? p.key : p.value;
+  const CacheRows& to = blockIdx.y == 0 ? p.out_key : p.out_value;
+  const uint32_t bytes = static_cast<uint32_t>(from.bytes);
+  unsigned char* dst = static_cast<unsigned char*>(to.at) + b * to.batch + h * to.head + first * to.slot;
+  const int32_t s = tid < count ? p.out_slots[bh * p.c.budget + first + tid] : -1;
+  const int some = __syncthreads_count(s >= 0);  // the rest have no token
+  if (some > 0) {
+    if (tid == 0) mbar_expect_tx(smem_u32(&bar), some * bytes);
+    __syncthreads();
+    if (s >= 0)
+      bulk_g2s(smem_u32(rows) + tid * bytes, static_cast<const unsigned char*>(from.at) + b * from.batch + h * from.head + s * from.slot,
+               bytes, smem_u32(&bar));
+    if (blockIdx.y == 0) gather_order<kBulkThreads>(p, bh, first, count);
+    // (a copy that never lands, not expected on a healthy device, leaves its rows unwritten)
+    if (__syncthreads_and(mbar_wait_bounded(smem_u32(&bar), 0, kBulkLimitNs))) {
+      const bool together = to.slot == from.bytes;
+      if (together ? tid == 0 : s >= 0) {
+        asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst + (together ? 0 : tid * to.slot)),
+                     "r"(smem_u32(rows) + (together ? 0u : tid * bytes)), "r"(together ? some * bytes : bytes)
+                     : "memory");
+        asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+      }
+    }
+  }
+  if (some == 0 && blockIdx.y == 0) gather_order<kBulkThreads>(p, bh, first, count);
+  for (int r = some; r < count; ++r)
+    for (uint32_t i = tid * 16u; i < bytes; i += kBulkThreads * 16u)
+      *reinterpret_cast<uint4*>(dst + r * to.slot + i) = make_uint4(0u, 0u, 0u, 0u);
+  asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+}
 
 __global__ void __launch_bounds__(kGatherThreads) evict_gather_kernel(const EvictParams p) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -615,6 +778,7 @@ __global__ void __launch_bounds__(kGatherThreads) evict_gather_kernel(const Evic
   const int64_t count = min(static_cast<int64_t>(kGatherRows), p.c.budget - first);
   const CacheRows& from = blockIdx.y == 0 ? p.key : p.value;
   const CacheRows& to = blockIdx.y == 0 ? p.out_key : p.out_value;
+  if (blockIdx.y == 0) gather_order<kGatherThreads>(p, bh, first, static_cast<int>(count));
   const uint64_t a = alignment_of(from) | alignment_of(to);
   if ((a & 15u) == 0u)
     gather_rows<16>(from, to, p, bh, first, count);
@@ -672,11 +836,24 @@ __global__ void __launch_bounds__(kInsThreads) insert_kernel(const InsertParams 
       if (tid == 0) chosen = n;
     } else {
       unsigned long long low = ~0ull;
-      for (int32_t s = tid; s < n; s += kInsThreads) {
-        const unsigned long long held = guard.holds(p.c.positions[row + s]);
-        const unsigned long long k = held << 63 | static_cast<unsigned long long>(weight_key(p.c.weights[row + s])) << 31 |
-                                     static_cast<unsigned long long>(0x7FFFFFFF - s);
-        low = min(low, k);
+      constexpr int kFlight = 8;  // loads of a thread under way
+      for (int64_t s0 = tid; s0 < n; s0 += kFlight * kInsThreads) {
+        float w[kFlight];
+        int32_t at[kFlight];
+#pragma unroll
+        for (int i = 0; i < kFlight; ++i) {
+          const int64_t s = s0 + i * kInsThreads;
+          w[i] = s < n ? p.c.weights[row + s] : 0.f;
+          at[i] = s < n ? p.c.positions[row + s] : 0;
+        }
+#pragma unroll
+        for (int i = 0; i < kFlight; ++i) {
+          const int64_t s = s0 + i * kInsThreads;
+          const unsigned long long held = guard.holds(at[i]);
+          const unsigned long long k = held << 63 | static_cast<unsigned long long>(weight_key(w[i])) << 31 |
+                                       static_cast<unsigned long long>(0x7FFFFFFF - s);
+          if (s < n) low = min(low, k);
+        }
       }
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) low = min(low, __shfl_xor_sync(kAll, low, o));
@@ -733,27 +910,35 @@ int launch_cache_evict(const EvictParams& p, qrita_stream_t stream) {
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   const int64_t pairs = p.c.B * p.c.H;
   uint32_t C = 1;
-  while (C < kMaxRanks && pairs * 2 * C <= 2 * device_sms() && p.c.S / (2 * C) >= 2 * kSelThreads) C *= 2;
+  while (C < kMaxRanks && p.c.S > static_cast<int64_t>(C) * kMaxShare && pairs * 2 * C <= INT32_MAX) C *= 2;
   EvictParams q = p;
   const int64_t share = (p.c.S + C - 1) / C;
   q.share = share <= kMaxShare ? static_cast<int32_t>(share) : 0;
   const size_t smem = static_cast<size_t>(q.share) * 4;
-  cudaError_t e = cudaFuncSetAttribute(reinterpret_cast<const void*>(&evict_select_kernel),
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxShare * 4);
+  static std::atomic<uint64_t> done{0};
+  cudaError_t e = allow_smem(&evict_select_kernel, kMaxShare * 4, done);
   if (e != cudaSuccess) return static_cast<int>(e);
   e = launch(&evict_select_kernel, static_cast<unsigned>(pairs * C), kSelThreads, C, st, smem, q);
   if (e != cudaSuccess) return static_cast<int>(e);
-  const int64_t parts = (p.c.budget + kGatherRows - 1) / kGatherRows;
+  auto aligned = [](const CacheRows& r) {
+    return ((reinterpret_cast<uintptr_t>(r.at) | static_cast<uint64_t>(r.bytes | r.batch | r.head | r.slot)) & 15u) == 0u &&
+           r.bytes <= kBulkBytes;
+  };
+  const bool bulk = aligned(p.key) && aligned(p.value) && aligned(p.out_key) && aligned(p.out_value);
+  const int64_t widest = p.key.bytes > p.value.bytes ? p.key.bytes : p.value.bytes;
+  const int per = !bulk ? kGatherRows : widest * kBulkThreads <= kBulkBytes ? kBulkThreads : static_cast<int>(kBulkBytes / widest);
+  const int64_t parts = (p.c.budget + per - 1) / per;
+  if (pairs * parts > INT32_MAX) return static_cast<int>(cudaErrorInvalidConfiguration);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(pairs * parts), 2, 1);
-  cfg.blockDim = dim3(kGatherThreads, 1, 1);
+  cfg.blockDim = dim3(bulk ? kBulkThreads : kGatherThreads, 1, 1);
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, &evict_gather_kernel, q);
+  e = bulk ? cudaLaunchKernelEx(&cfg, &evict_bulk_kernel, q, per) : cudaLaunchKernelEx(&cfg, &evict_gather_kernel, q);
   const cudaError_t last = cudaGetLastError();
   return static_cast<int>(e != cudaSuccess ? e : last);
 }

@@ -431,8 +431,8 @@ cudaError_t launch_window_of(const WeightParams& p, const CUtensorMap& query, co
   const int64_t pairs = p.c.B * p.c.H;
   constexpr size_t smem = kWindowSmem<HALVES>;
   auto* fn = &window_kernel<HALVES>;
-  cudaError_t e = cudaFuncSetAttribute(reinterpret_cast<const void*>(fn), cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       static_cast<int>(smem));
+  static std::atomic<uint64_t> done{0};
+  cudaError_t e = allow_smem(fn, smem, done);
   if (e != cudaSuccess) return e;
   // As many CTAs as are on the device at once, with two tiles each at least, and
   // clusters of 8 at most: 16 SMs are rarely free together (8 heads of 32768 slots, 512

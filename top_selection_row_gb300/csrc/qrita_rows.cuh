@@ -540,6 +540,21 @@ inline uint32_t row_ctas(int64_t B, int64_t bytes, bool second_pass, int per_sm)
   return C;
 }
 
+// Lets fn have `bytes` of dynamic shared memory, once a device (`done` is fn's own;
+// a device past the 64th is asked each time).
+template <typename F>
+cudaError_t allow_smem(F* fn, size_t bytes, std::atomic<uint64_t>& done) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = dev >= 0 && dev < 64 ? 1ull << dev : 0ull;
+  if ((done.load(std::memory_order_relaxed) & bit) != 0ull) return cudaSuccess;
+  e = cudaFuncSetAttribute(reinterpret_cast<const void*>(fn), cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           static_cast<int>(bytes));
+  if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+  return e;
+}
+
 template <typename F, typename... Args>
 cudaError_t launch(F* fn, unsigned grid, unsigned block, unsigned cluster, cudaStream_t st, size_t smem, Args... args) {
   if (cluster > 8) {
