@@ -134,6 +134,8 @@ def test_weights_of_long_caches(dev):
     check_weights(dev, 5, 1, 1, 2, 1, 70001, 64, "bf16")
     check_weights(dev, 6, 1, 1, 8, 5, 33000, 64, "bf16", evicted=True)
     check_weights(dev, 7, 20, 9, 1, 2, 500, 32, "bf16")
+    check_weights(dev, 8, 1, 1, 16, 1, 40000, 32, "bf16")  # clusters of 16 with most of an SM's memory each
+    check_weights(dev, 9, 1, 1, 16, 1, 70000, 32, "bf16")  # scores that fit nowhere
 
 
 def test_weights_of_windows_over_several_tiles(dev):

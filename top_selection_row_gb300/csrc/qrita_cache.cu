@@ -57,13 +57,23 @@ __device__ __forceinline__ int32_t length_of(const CacheOrder& c, int64_t b, int
 // wait in shared memory where they fit, so that keys are read once, and are worked
 // out again from keys that are in L2 where they do not.
 // ---------------------------------------------------------------------------
-constexpr int kWThreads = 512;
+constexpr int kWThreads = 256;  // two CTAs on an SM: one's merge beside the other's keys
 constexpr int kWWarps = kWThreads / 32;
 constexpr int kMaxRowsAtOnce = 32;
+// Up to as many rows this kernel takes, which reads keys once; more go to the window's
+// where that can be. (32 rows of 64 dimensions in 8 x 8 x 8192 slots: 95 us here, 38
+// there; 16 rows of 128 in 64 x 8 x 2000: 77 and 102; 8 in 16 x 8 x 16384: 132 and 173.)
+constexpr int kFewRows = 16;
 
-struct RowSum {
+struct alignas(8) RowSum {
   float m, s;
 };
+
+__device__ __forceinline__ unsigned long long ld_dsmem_sum(uint32_t addr) {
+  unsigned long long v;
+  asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(v) : "r"(addr) : "memory");
+  return v;
+}
 
 __device__ __forceinline__ void sum_add(RowSum& a, RowSum b) {
   const float m = fmaxf(a.m, b.m);
@@ -129,15 +139,22 @@ struct MmaScores {
     const unsigned char* at = smem + ((threadIdx.x & 31) >> 2) * kPitch + (threadIdx.x & 3) * 16;
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
-      float c[4] = {0.f, 0.f, 0.f, 0.f};
+      // (few columns: several chains of products, each waits for its last one)
+      constexpr int kChains = NT == 1 ? 4 : NT == 2 ? 2 : 1;
+      float cs[kChains][4] = {};
 #pragma unroll
       for (int i = 0; i < CHUNKS; ++i) {
         const uint4 b = *reinterpret_cast<const uint4*>(at + n * 8 * kPitch + i * 64);
         const uint32_t a0[4] = {k[0][i].x, k[1][i].x, k[0][i].y, k[1][i].y};
         const uint32_t a1[4] = {k[0][i].z, k[1][i].z, k[0][i].w, k[1][i].w};
-        mma_bf16(c, a0, b.x, b.y);
-        mma_bf16(c, a1, b.z, b.w);
+        mma_bf16(cs[2 * i % kChains], a0, b.x, b.y);
+        mma_bf16(cs[(2 * i + 1) % kChains], a1, b.z, b.w);
       }
+      float(&c)[4] = cs[0];
+#pragma unroll
+      for (int j = 1; j < kChains; ++j)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) c[i] += cs[j][i];
       x[0][2 * n] = c[0];
       x[0][2 * n + 1] = c[1];
       x[1][2 * n] = c[2];
@@ -205,7 +222,7 @@ struct FmaScores {
 
 // Scores are kept in natural units, and exponents are formed of their differences.
 template <typename SC, int BYTES>
-__global__ void __launch_bounds__(kWThreads, 1) weights_kernel(const WeightParams p) {
+__global__ void __launch_bounds__(kWThreads, 2) weights_kernel(const WeightParams p) {
   extern __shared__ __align__(16) unsigned char dynamic[];
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -216,9 +233,9 @@ __global__ void __launch_bounds__(kWThreads, 1) weights_kernel(const WeightParam
   // dynamic: sums of a chunk's rows by warp, sums of all rows, query rows, scores
   RowSum* by_warp = reinterpret_cast<RowSum*>(dynamic);
   RowSum* sums = by_warp + kWWarps * kMaxRowsAtOnce;
-  unsigned char* rows = reinterpret_cast<unsigned char*>(sums + 2 * ((R + 1) / 2));
+  RowSum* merged = sums + 2 * ((R + 1) / 2);
+  unsigned char* rows = reinterpret_cast<unsigned char*>(merged + 2 * ((R + 1) / 2));
   if (C > 1) cluster_arrive_relaxed();
-  const bool idle = p.c.lengths[b] < 0;
   const int32_t n = length_of(p.c, b, p.c.S);
   const int64_t last = static_cast<int64_t>(p.c.seen != nullptr ? p.c.seen[b] : n) - p.T;  // the first query's position
   const int64_t per = (static_cast<int64_t>(n) + C - 1) / C;
@@ -241,13 +258,15 @@ __global__ void __launch_bounds__(kWThreads, 1) weights_kernel(const WeightParam
     RowSum run[SC::kQ];
 #pragma unroll
     for (int j = 0; j < SC::kQ; ++j) run[j] = {-INFINITY, 0.f};
+    SC next;  // the tile whose keys are on their way
+    next.load(p, keys, lo + warp * SC::kTile, hi);
     for (int64_t s0 = lo + warp * SC::kTile; s0 < hi; s0 += kWWarps * SC::kTile) {
-      SC sc;
+      const SC sc = next;
       float x[SC::kKeys][SC::kQ];
-      sc.load(p, keys, s0, hi);
       int64_t at[SC::kKeys];
 #pragma unroll
       for (int i = 0; i < SC::kKeys; ++i) at[i] = s0 + SC::key(i) < hi ? position(s0 + SC::key(i)) : INT64_MAX;
+      next.load(p, keys, s0 + kWWarps * SC::kTile, hi);
       sc.scores(p, rows, x);
 #pragma unroll
       for (int j = 0; j < SC::kQ; ++j) {
@@ -289,38 +308,41 @@ __global__ void __launch_bounds__(kWThreads, 1) weights_kernel(const WeightParam
       sums[r0 + tid] = all;
     }
   }
-  // the rows' sums over the cluster, in place after everyone has read them
+  // the rows' sums over the cluster
   if (C > 1) cluster_wait();
   row_sync(C);
-  for (int r0 = 0; r0 < R; r0 += kWThreads) {
-    const int r = r0 + tid;
-    RowSum all = {-INFINITY, 0.f};
-    if (r < R)
-      for (uint32_t c = 0; c < C; ++c) {
-        const uint32_t from = map_rank(smem_u32(&sums[r]), c);
-        RowSum other;
-        other.m = ld_dsmem_f32(from);
-        other.s = ld_dsmem_f32(from + 4);
-        sum_add(all, other);
+  for (int r = tid; r < R; r += kWThreads) {
+    RowSum all = sums[r];
+    if (C > 1) {
+      all = {-INFINITY, 0.f};
+      for (uint32_t c0 = 0; c0 < C; c0 += 4) {  // (four loads under way)
+        unsigned long long v[4];
+#pragma unroll
+        for (uint32_t c = 0; c < 4; ++c) v[c] = ld_dsmem_sum(map_rank(smem_u32(&sums[r]), min(c0 + c, C - 1)));
+#pragma unroll
+        for (uint32_t c = 0; c < 4; ++c)
+          if (c0 + c < C)
+            sum_add(all, {__uint_as_float(static_cast<uint32_t>(v[c])), __uint_as_float(static_cast<uint32_t>(v[c] >> 32))});
       }
-    row_sync(C);
-    // (only this chunk's entries change, which everyone has read)
+    }
     // (a row that sees nothing, or logits of -inf alone, adds 0)
-    if (r < R) sums[r] = {all.s == 0.f ? 0.f : all.m, all.s == 0.f ? 0.f : 1.f / all.s};
+    merged[r] = {all.s == 0.f ? 0.f : all.m, all.s == 0.f ? 0.f : 1.f / all.s};
   }
+  if (C > 1) cluster_arrive();  // (waited for at the end: the others read this CTA's sums)
   __syncthreads();
-  if (idle) return;
   if (stashed) {
     for (int64_t s = lo + tid; s < hi; s += kWThreads) {
       const int64_t at = position(s);
       float w = 0.f;
-      for (int r = 0; r < R; ++r)
-        if (at <= last_of(r)) w += ex2((stash[r * p.stash + static_cast<int>(s - lo)] - sums[r].m) * kLog2e) * sums[r].s;
+      const float* x = stash + static_cast<int>(s - lo);
+      for (int t = 0, r = 0; t < p.T; ++t, r += p.G)
+        if (at <= last + t)
+          for (int g = 0; g < p.G; ++g)
+            w += ex2((x[(r + g) * p.stash] - merged[r + g].m) * kLog2e) * merged[r + g].s;
       weights[s] = p.decay != 0.f ? fmaf(p.decay, weights[s], w) : w;
     }
-    return;
   }
-  for (int c = 0; c < chunks; ++c) {
+  for (int c = 0; !stashed && c < chunks; ++c) {
     const int r0 = c * p.rows, nr = min(p.rows, R - r0);
     __syncthreads();
     SC::put_rows(p, q, r0, nr, rows);
@@ -338,7 +360,7 @@ __global__ void __launch_bounds__(kWThreads, 1) weights_kernel(const WeightParam
 #pragma unroll
         for (int j = 0; j < SC::kQ; ++j) {
           const int r = SC::row(j);
-          if (r < nr && at <= last_of(r0 + r)) w += ex2((x[i][j] * p.scale - sums[r0 + r].m) * kLog2e) * sums[r0 + r].s;
+          if (r < nr && at <= last_of(r0 + r)) w += ex2((x[i][j] * p.scale - merged[r0 + r].m) * kLog2e) * merged[r0 + r].s;
         }
 #pragma unroll
         for (int o = 1; o < SC::kFirstLane; o <<= 1) w += __shfl_xor_sync(kAll, w, o);
@@ -347,6 +369,7 @@ __global__ void __launch_bounds__(kWThreads, 1) weights_kernel(const WeightParam
       }
     }
   }
+  if (C > 1) cluster_wait();
 }
 
 template <typename SC, int BYTES>
@@ -354,20 +377,21 @@ cudaError_t launch_weights_of(const WeightParams& p, cudaStream_t st) {
   WeightParams q = p;
   q.rows = SC::kRows;
   const int64_t R = static_cast<int64_t>(p.G) * p.T, pairs = p.c.B * p.c.H;
-  const size_t fixed = sizeof(RowSum) * (kWWarps * kMaxRowsAtOnce + 2 * ((R + 1) / 2)) + q.rows * (sizeof(float) * (p.D + 16));
-  constexpr size_t kMost = 200 * 1024;
+  const size_t fixed = sizeof(RowSum) * (kWWarps * kMaxRowsAtOnce + 4 * ((R + 1) / 2)) + q.rows * (sizeof(float) * (p.D + 16));
+  constexpr size_t kMost = 200 * 1024, kHalfSm = 110 * 1024;
   if (fixed > kMost) return cudaErrorInvalidValue;
-  // shares of the slots: enough for the device, and of no more scores than fit
+  // shares of the slots: enough for the device, and of no more scores than fit (beside
+  // another CTA's, if that can be)
   uint32_t C = 1;
   auto floats = [&](uint32_t c) {
     const int64_t per = (p.c.S + c - 1) / c, share = (per + SC::kTile - 1) / SC::kTile * SC::kTile;
     return share + (4 - share % 16 + 16) % 16;  // (4 modulo 16: a tile's stores meet no bank twice)
   };
-  auto fits = [&](uint32_t c) { return R <= q.rows && fixed + static_cast<size_t>(floats(c) * R) * 4 <= kMost; };
-  while (C < kMaxRanks && pairs * 2 * C <= INT32_MAX && p.c.S / (2 * C) >= kWWarps * SC::kTile / 2 &&
-         (pairs * 2 * C <= 2 * device_sms() || (R <= q.rows && !fits(C))))
+  auto fits = [&](uint32_t c, size_t most) { return R <= q.rows && fixed + static_cast<size_t>(floats(c) * R) * 4 <= most; };
+  while (C < kMaxRanks && pairs * 2 * C <= INT32_MAX && p.c.S / (2 * C) >= kWWarps * SC::kTile &&
+         (pairs * 2 * C <= 2 * device_sms() || (R <= q.rows && !fits(C, kHalfSm))))
     C *= 2;
-  q.stash = fits(C) ? static_cast<int32_t>(floats(C)) : 0;
+  q.stash = fits(C, kMost) ? static_cast<int32_t>(floats(C)) : 0;
   const size_t smem = fixed + static_cast<size_t>(q.stash * R) * 4;
   auto* fn = &weights_kernel<SC, BYTES>;
   static std::atomic<uint64_t> done{0};
@@ -892,7 +916,7 @@ int launch_cache_weights(const WeightParams& p, int dtype, qrita_stream_t stream
                      2u * static_cast<uint64_t>(p.q_batch | p.q_token | p.q_head | p.k_batch | p.k_head | p.k_slot);
   if ((a & 15u) == 0u) {
     int result;
-    if (static_cast<int64_t>(p.G) * p.T > kMaxRowsAtOnce && launch_cache_window(p, stream, &result)) return result;
+    if (static_cast<int64_t>(p.G) * p.T > kFewRows && launch_cache_window(p, stream, &result)) return result;
     switch (p.D) {
       case 32: return static_cast<int>(launch_weights_mma<1>(p, st));
       case 64: return static_cast<int>(launch_weights_mma<2>(p, st));

@@ -318,12 +318,20 @@ window_kernel(const WindowParams wp, const __grid_constant__ CUtensorMap query_m
     }
     if (group == 0) {
       WindowSum all = {-FLT_MAX, 0.f};
-      for (uint32_t c = 0; c < C * kGroups; ++c) {
-        const uint32_t at = smem_u32(&sums[c % kGroups][t]), from = C > 1 ? map_rank(at, c / kGroups) : at;
-        const float o = ld_dsmem_f32(from), s = ld_dsmem_f32(from + 4);
-        const float most = fmaxf(all.top, o);
-        all.s = all.s * ex2(all.top - most) + s * ex2(o - most);
-        all.top = most;
+      for (uint32_t c = 0; c < C; ++c) {
+        float o[kGroups], s[kGroups];  // (all under way at once)
+#pragma unroll
+        for (int i = 0; i < kGroups; ++i) {
+          const uint32_t at = smem_u32(&sums[i][t]), from = C > 1 ? map_rank(at, c) : at;
+          o[i] = ld_dsmem_f32(from);
+          s[i] = ld_dsmem_f32(from + 4);
+        }
+#pragma unroll
+        for (int i = 0; i < kGroups; ++i) {
+          const float most = fmaxf(all.top, o[i]);
+          all.s = all.s * ex2(all.top - most) + s[i] * ex2(o[i] - most);
+          all.top = most;
+        }
       }
       // rows that see nothing, or scores of -inf alone, add 0; so do those past the last
       float* to = reinterpret_cast<float*>(&row_pairs[t >> 1]) + (t & 1);
