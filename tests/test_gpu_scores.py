@@ -126,6 +126,22 @@ def test_specials_alignment_and_padding(dev, keep):
             check(dev, x[1:], dtype, t[1:], None if mask is None else mask[1:], 8, ld=ld)
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_rows_of_many_logits_of_minus_infinity(dev, dtype):
+    """Whole steps of the sums whose exponents have no finite lowest one."""
+    V = 40003
+    rng, x, tokens, _ = make_rows(13, 4, V, "f32")
+    x[:, rng.random(V) < 0.5] = -np.inf
+    x[1, :20000] = -np.inf
+    x[2, 8:] = -np.inf
+    x[3] = np.where(np.arange(V) % 512 == 5, -3.0e38, x[3])
+    if dtype == "bf16":
+        x = f32_to_bf16_bits(x)
+    t = given(rng, np.clip(tokens, 0, V - 1), V, 3)
+    check(dev, x, dtype, t, None, 16)
+    check(dev, np.tile(x, (160, 1)), dtype, np.tile(t, (160, 1)), None, 16)  # one CTA a row
+
+
 def test_only_some_outputs_and_reuse(dev):
     import torch
 
