@@ -56,6 +56,11 @@ __device__ __forceinline__ int32_t length_of(const CacheOrder& c, int64_t b, int
 // distributed shared memory; then a slot's weight is the sum over its scores, which
 // wait in shared memory where they fit, so that keys are read once, and are worked
 // out again from keys that are in L2 where they do not.
+//
+// HBM bounds it: one query of 4 heads on 16 x 8 x 32768 slots of 128 bf16 200 us (5.4
+// TB/s), on 64 x 8 x 4096 97 us (5.5); 4 x 8 x 1024 6.9 us, of latency. A warp has the
+// next tile on its way while it works on one, in four chains of products (a single
+// chain of 16 dependent ones: 230 us).
 // ---------------------------------------------------------------------------
 constexpr int kWThreads = 256;  // two CTAs on an SM: one's merge beside the other's keys
 constexpr int kWWarps = kWThreads / 32;
@@ -422,7 +427,8 @@ constexpr int kMaxShare = 48 * 1024;  // keys a CTA keeps in shared memory
 // slots above it and the first of those equal to it, in slot order. The first digit has
 // a weight's exponent and two bits more, so that few of a warp's weights meet in a bin;
 // the last digit needs the keys alone that share it. A row has one CTA while its keys
-// fit in shared memory: a barrier of a cluster costs as much as a thousand keys.
+// fit in shared memory: a barrier of a cluster costs as much as a thousand keys. Issue
+// slots bound it: 128 rows of 32768 slots 25 us, of 1500 slots 5.
 __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictParams p) {
   extern __shared__ __align__(16) unsigned char dynamic[];
   uint32_t* own = reinterpret_cast<uint32_t*>(dynamic);
@@ -746,7 +752,8 @@ constexpr int kBulkThreads = 64;         // and rows of a CTA, at most
 constexpr int kBulkBytes = 16 * 1024;    // of its rows
 constexpr uint64_t kBulkLimitNs = 10ull * 1000 * 1000 * 1000;
 
-// The same for rows of 16-byte units on their boundaries, by bulk copies (TMA): a
+// The same for rows of 16-byte units on their boundaries (16 x 8 rows of 32768 slots of
+// 256 bytes cut to 4096: 78 us, 6.9 TB/s; by plain loads 95), by bulk copies (TMA): a
 // thread asks for a row each, and the rows leave together where they lie one after
 // another. Thirteen CTAs on an SM have 208 KB on their way.
 __global__ void __launch_bounds__(kBulkThreads) evict_bulk_kernel(const EvictParams p, int per) {
@@ -837,7 +844,8 @@ __device__ __forceinline__ void put_row(const CacheRows& from, const CacheRows& 
 }
 
 // A cluster takes a sequence, its heads in turn; the sequence's length goes up
-// when every CTA has read it.
+// when every CTA has read it. Latency bounds it: 64 x 8 x 4096 slots 7.6 us, 1 x 8 x
+// 1000 3.3.
 __global__ void __launch_bounds__(kInsThreads) insert_kernel(const InsertParams p) {
   __shared__ unsigned long long least[kInsThreads / 32];
   __shared__ int32_t chosen;

@@ -10,8 +10,8 @@
 //           w = sum_r 2^(c x_r - c m_r) / S_r, c = scale log2 e.
 // Between them the rows' sums merge through distributed shared memory. Both products
 // read the same tiles of shared memory (dimensions contiguous, swizzled over 128
-// bytes). Keys are read again for the second product: a share of a thousand slots is
-// small enough that they come from L2.
+// bytes). Keys are read again for the second product, last tiles first: what L2 still
+// has.
 //
 // A CTA has an SM: four groups of four warps, the lanes' threads of a tile in turn,
 // a warp that issues the products and one that asks for the tiles (TMA). Four
@@ -19,6 +19,12 @@
 // shared memory has, so that copies are under way while products and exponentials
 // are. No other CTA of these kernels fits beside one, so none waits for columns that
 // another holds.
+//
+// Exponentials bound it, two a row and slot at 16 a clock and SM: 32 queries of 4 heads
+// on 8 x 8 x 16384 slots of 128 bf16 97 us, of which they are 69 on the 128 SMs at work;
+// keys are read from HBM 1.7 times, 454 MB. (mma.sync in blocks of 32 rows: 930 us.
+// Keys by 16-byte copies of 64 threads, two CTAs an SM, two stages: 120. Two groups,
+// columns loaded ahead of their use: 114.)
 
 #include <cfloat>
 #include <cstring>
