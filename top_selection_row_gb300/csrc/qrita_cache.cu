@@ -57,8 +57,8 @@ __device__ __forceinline__ int32_t length_of(const CacheOrder& c, int64_t b, int
 // wait in shared memory where they fit, so that keys are read once, and are worked
 // out again from keys that are in L2 where they do not.
 //
-// HBM bounds it: one query of 4 heads on 16 x 8 x 32768 slots of 128 bf16 200 us (5.4
-// TB/s), on 64 x 8 x 4096 97 us (5.5); 4 x 8 x 1024 6.9 us, of latency. A warp has the
+// HBM bounds it: one query of 4 heads on 16 x 8 x 32768 slots of 128 bf16 193 us (5.6
+// TB/s), on 64 x 8 x 4096 93 us (5.8); 4 x 8 x 1024 6.6 us, of latency. A warp has the
 // next tile on its way while it works on one, in four chains of products (a single
 // chain of 16 dependent ones: 230 us).
 // ---------------------------------------------------------------------------
@@ -168,11 +168,11 @@ struct MmaScores {
   }
 };
 
-// In fp32, of any type and size: a slot a lane, 8 query rows that the warp reads
-// together.
-template <int DT>
+// In fp32, of any type and size: a slot a lane, ROWS query rows that the warp
+// reads together.
+template <int DT, int ROWS>
 struct FmaScores {
-  static constexpr int kTile = 32, kRows = 8, kKeys = 1, kQ = 8;
+  static constexpr int kTile = 32, kRows = ROWS, kKeys = 1, kQ = ROWS;
   static constexpr int kFirstLane = 1;
   const unsigned char* at;
   bool live;
@@ -206,22 +206,21 @@ struct FmaScores {
         Elem<DT>::unpack(load_unit(at + d * Elem<DT>::kBytes), v);
 #pragma unroll
         for (int i = 0; i < U / 2; ++i) {
-          step(v[i].x, q + 2 * (d + 2 * i), x[0]);
-          step(v[i].y, q + 2 * (d + 2 * i + 1), x[0]);
+          step(v[i].x, q + ROWS / 4 * (d + 2 * i), x[0]);
+          step(v[i].y, q + ROWS / 4 * (d + 2 * i + 1), x[0]);
         }
       }
-    for (; d < p.D; ++d) step(Elem<DT>::load(at, d), q + 2 * d, x[0]);
+    for (; d < p.D; ++d) step(Elem<DT>::load(at, d), q + ROWS / 4 * d, x[0]);
   }
   __device__ __forceinline__ static void step(float k, const float4* q, float (&x)[kQ]) {
-    const float4 a = q[0], b = q[1];
-    x[0] = fmaf(k, a.x, x[0]);
-    x[1] = fmaf(k, a.y, x[1]);
-    x[2] = fmaf(k, a.z, x[2]);
-    x[3] = fmaf(k, a.w, x[3]);
-    x[4] = fmaf(k, b.x, x[4]);
-    x[5] = fmaf(k, b.y, x[5]);
-    x[6] = fmaf(k, b.z, x[6]);
-    x[7] = fmaf(k, b.w, x[7]);
+#pragma unroll
+    for (int i = 0; i < ROWS / 4; ++i) {
+      const float4 a = q[i];
+      x[4 * i] = fmaf(k, a.x, x[4 * i]);
+      x[4 * i + 1] = fmaf(k, a.y, x[4 * i + 1]);
+      x[4 * i + 2] = fmaf(k, a.z, x[4 * i + 2]);
+      x[4 * i + 3] = fmaf(k, a.w, x[4 * i + 3]);
+    }
   }
 };
 
@@ -252,37 +251,54 @@ __global__ void __launch_bounds__(kWThreads, 2) weights_kernel(const WeightParam
   const int32_t* positions = p.c.positions != nullptr ? p.c.positions + bh * p.c.S : nullptr;
   const bool stashed = p.stash > 0;
   float* stash = reinterpret_cast<float*>(rows + p.rows * (sizeof(float) * (p.D + 16)));
-  auto last_of = [&](int r) { return last + r / p.G; };
-  auto position = [&](int64_t s) { return static_cast<int64_t>(positions != nullptr ? positions[s] : s); };
+  auto position = [&](int64_t s) { return positions != nullptr ? positions[s] : static_cast<int32_t>(s); };
+  // The last position that each of a chunk's rows sees (no row past the last sees any);
+  // a slot outside the share has one that none sees.
+  __shared__ int32_t sees[kMaxRowsAtOnce];
+  constexpr int32_t kNone = INT32_MAX;
+  auto set_rows = [&](int r0, int nr) {
+    __syncthreads();
+    SC::put_rows(p, q, r0, nr, rows);
+    if (tid < SC::kRows) {
+      const int64_t at = last + (r0 + tid) / p.G;
+      sees[tid] = tid < nr && at >= INT32_MIN ? static_cast<int32_t>(min(at, static_cast<int64_t>(kNone) - 1)) : INT32_MIN;
+    }
+    __syncthreads();
+  };
 
   for (int c = 0; c < chunks; ++c) {
     const int r0 = c * p.rows, nr = min(p.rows, R - r0);
-    __syncthreads();
-    SC::put_rows(p, q, r0, nr, rows);
-    __syncthreads();
+    set_rows(r0, nr);
     RowSum run[SC::kQ];
+    constexpr bool kHeld = SC::kQ <= 8;  // what this thread's rows see, in registers
+    int32_t held[kHeld ? SC::kQ : 1];
 #pragma unroll
-    for (int j = 0; j < SC::kQ; ++j) run[j] = {-INFINITY, 0.f};
+    for (int j = 0; j < SC::kQ; ++j) {
+      run[j] = {-INFINITY, 0.f};
+      if (kHeld) held[j] = sees[SC::row(j)];
+    }
     SC next;  // the tile whose keys are on their way
     next.load(p, keys, lo + warp * SC::kTile, hi);
-    for (int64_t s0 = lo + warp * SC::kTile; s0 < hi; s0 += kWWarps * SC::kTile) {
+    float* mine = stash + r0 * p.stash;
+    const int len = static_cast<int>(hi - lo);
+    for (int o = warp * SC::kTile; o < len; o += kWWarps * SC::kTile) {
       const SC sc = next;
       float x[SC::kKeys][SC::kQ];
-      int64_t at[SC::kKeys];
+      int32_t at[SC::kKeys];
 #pragma unroll
-      for (int i = 0; i < SC::kKeys; ++i) at[i] = s0 + SC::key(i) < hi ? position(s0 + SC::key(i)) : INT64_MAX;
-      next.load(p, keys, s0 + kWWarps * SC::kTile, hi);
+      for (int i = 0; i < SC::kKeys; ++i) at[i] = o + SC::key(i) < len ? position(lo + o + SC::key(i)) : kNone;
+      next.load(p, keys, lo + o + kWWarps * SC::kTile, hi);
       sc.scores(p, rows, x);
 #pragma unroll
       for (int j = 0; j < SC::kQ; ++j) {
         const int r = SC::row(j);
-        const int64_t see = r < nr ? last_of(r0 + r) : INT64_MIN;
+        const int32_t see = kHeld ? held[kHeld ? j : 0] : sees[r];
         float top = run[j].m;
 #pragma unroll
         for (int i = 0; i < SC::kKeys; ++i) {
           x[i][j] = at[i] <= see ? x[i][j] * p.scale : -INFINITY;
           top = fmaxf(top, x[i][j]);
-          if (stashed && r < nr && s0 + SC::key(i) < hi) stash[r * p.stash + static_cast<int>(s0 + SC::key(i) - lo)] = x[i][j];
+          if (stashed && r < nr) mine[r * p.stash + o + SC::key(i)] = x[i][j];  // (a tile is whole there)
         }
         if (top > run[j].m) {
           run[j].s *= ex2((run[j].m - top) * kLog2e);
@@ -337,7 +353,7 @@ __global__ void __launch_bounds__(kWThreads, 2) weights_kernel(const WeightParam
   __syncthreads();
   if (stashed) {
     for (int64_t s = lo + tid; s < hi; s += kWThreads) {
-      const int64_t at = position(s);
+      const int32_t at = position(s);
       float w = 0.f;
       const float* x = stash + static_cast<int>(s - lo);
       for (int t = 0, r = 0; t < p.T; ++t, r += p.G)
@@ -349,9 +365,7 @@ __global__ void __launch_bounds__(kWThreads, 2) weights_kernel(const WeightParam
   }
   for (int c = 0; !stashed && c < chunks; ++c) {
     const int r0 = c * p.rows, nr = min(p.rows, R - r0);
-    __syncthreads();
-    SC::put_rows(p, q, r0, nr, rows);
-    __syncthreads();
+    set_rows(r0, nr);
     for (int64_t s0 = lo + warp * SC::kTile; s0 < hi; s0 += kWWarps * SC::kTile) {
       SC sc;
       float x[SC::kKeys][SC::kQ];
@@ -360,12 +374,12 @@ __global__ void __launch_bounds__(kWThreads, 2) weights_kernel(const WeightParam
 #pragma unroll
       for (int i = 0; i < SC::kKeys; ++i) {
         const int64_t s = s0 + SC::key(i);
-        const int64_t at = s < hi ? position(s) : INT64_MAX;
+        const int32_t at = s < hi ? position(s) : kNone;
         float w = 0.f;
 #pragma unroll
         for (int j = 0; j < SC::kQ; ++j) {
           const int r = SC::row(j);
-          if (r < nr && at <= last_of(r0 + r)) w += ex2((x[i][j] * p.scale - merged[r0 + r].m) * kLog2e) * merged[r0 + r].s;
+          if (r < nr && at <= sees[r]) w += ex2((x[i][j] * p.scale - merged[r0 + r].m) * kLog2e) * merged[r0 + r].s;
         }
 #pragma unroll
         for (int o = 1; o < SC::kFirstLane; o <<= 1) w += __shfl_xor_sync(kAll, w, o);
@@ -392,9 +406,9 @@ cudaError_t launch_weights_of(const WeightParams& p, cudaStream_t st) {
     const int64_t per = (p.c.S + c - 1) / c, share = (per + SC::kTile - 1) / SC::kTile * SC::kTile;
     return share + (4 - share % 16 + 16) % 16;  // (4 modulo 16: a tile's stores meet no bank twice)
   };
-  auto fits = [&](uint32_t c, size_t most) { return R <= q.rows && fixed + static_cast<size_t>(floats(c) * R) * 4 <= most; };
+  auto fits = [&](uint32_t c, size_t most) { return R <= kMaxRowsAtOnce && fixed + static_cast<size_t>(floats(c) * R) * 4 <= most; };
   while (C < kMaxRanks && pairs * 2 * C <= INT32_MAX && p.c.S / (2 * C) >= kWWarps * SC::kTile &&
-         (pairs * 2 * C <= 2 * device_sms() || (R <= q.rows && !fits(C, kHalfSm))))
+         (pairs * 2 * C <= 2 * device_sms() || (R <= kMaxRowsAtOnce && !fits(C, kHalfSm))))
     C *= 2;
   q.stash = fits(C, kMost) ? static_cast<int32_t>(floats(C)) : 0;
   const size_t smem = fixed + static_cast<size_t>(q.stash * R) * 4;
@@ -403,6 +417,12 @@ cudaError_t launch_weights_of(const WeightParams& p, cudaStream_t st) {
   const cudaError_t e = allow_smem(fn, kMost, done);
   if (e != cudaSuccess) return e;
   return launch(fn, static_cast<unsigned>(pairs * C), kWThreads, C, st, smem, q);
+}
+
+template <int DT, int BYTES>
+cudaError_t launch_weights_fma(const WeightParams& p, cudaStream_t st) {
+  if (static_cast<int64_t>(p.G) * p.T <= 8) return launch_weights_of<FmaScores<DT, 8>, BYTES>(p, st);
+  return launch_weights_of<FmaScores<DT, 16>, BYTES>(p, st);
 }
 
 template <int CHUNKS>
@@ -918,7 +938,7 @@ __global__ void __launch_bounds__(kInsThreads) insert_kernel(const InsertParams 
 
 int launch_cache_weights(const WeightParams& p, int dtype, qrita_stream_t stream) {
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  if (dtype == QRITA_DTYPE_F32) return static_cast<int>(launch_weights_of<FmaScores<QRITA_DTYPE_F32>, 4>(p, st));
+  if (dtype == QRITA_DTYPE_F32) return static_cast<int>(launch_weights_fma<QRITA_DTYPE_F32, 4>(p, st));
   // rows of 16-byte units on their boundaries, 32 dimensions at a time: the tensor cores
   const uint64_t a = static_cast<uint64_t>(reinterpret_cast<uintptr_t>(p.query) | reinterpret_cast<uintptr_t>(p.keys)) |
                      2u * static_cast<uint64_t>(p.q_batch | p.q_token | p.q_head | p.k_batch | p.k_head | p.k_slot);
@@ -935,7 +955,7 @@ int launch_cache_weights(const WeightParams& p, int dtype, qrita_stream_t stream
       default: break;
     }
   }
-  return static_cast<int>(launch_weights_of<FmaScores<QRITA_DTYPE_BF16>, 2>(p, st));
+  return static_cast<int>(launch_weights_fma<QRITA_DTYPE_BF16, 2>(p, st));
 }
 
 int launch_cache_evict(const EvictParams& p, qrita_stream_t stream) {
