@@ -996,6 +996,13 @@ __global__ void __launch_bounds__(kResThreads, kResBlocks) resident_kernel(const
   __shared__ double many_sums[MANY ? kResThreads / 32 : 1], many_ranks[MANY ? kMaxRanks : 1];
   __shared__ ManyRow many_row;
   bool ignored = false;
+  if constexpr (MANY) {
+    // the first pieces on their way to L2 while the ids and their gradients are read
+    if (tid == 0 && n > 0)
+      asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(sh.unit(sh.u_lo)),
+                   "r"(static_cast<uint32_t>(min(n, kSlots * kPieceUnits)) * 16u)
+                   : "memory");
+  }
   if constexpr (MANY)
     ignored = !many.load(p, row, [&](int i, int64_t id) {
       if (!sh.owns(id)) return -INFINITY;
