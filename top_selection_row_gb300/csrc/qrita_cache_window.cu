@@ -20,11 +20,12 @@
 // are. No other CTA of these kernels fits beside one, so none waits for columns that
 // another holds.
 //
-// Exponentials bound it, two a row and slot at 16 a clock and SM: 32 queries of 4 heads
-// on 8 x 8 x 16384 slots of 128 bf16 97 us, of which they are 69 on the 128 SMs at work;
-// keys are read from HBM 1.7 times, 454 MB. (mma.sync in blocks of 32 rows: 930 us.
+// Keys bound it, read twice: 32 queries of 4 heads on 8 x 8 x 16384 slots of 128 bf16
+// 97 us for 537 MB of tiles (5.6 TB/s; 454 MB of them from HBM, on 128 SMs), 16 queries
+// 92; its exponentials are 69 us of their pipe. (mma.sync in blocks of 32 rows: 930 us.
 // Keys by 16-byte copies of 64 threads, two CTAs an SM, two stages: 120. Two groups,
-// columns loaded ahead of their use: 114.)
+// columns loaded ahead of their use: 114. An eighth of the exponentials by polynomials
+// on the multiply-add pipe: 103, a quarter: 106.)
 
 #include <cfloat>
 #include <cstring>

@@ -262,7 +262,7 @@ __device__ __forceinline__ float grad_one(float x, const RowGrad& g, float c) {
 // logits of its ids (read before a gradient is written over them), on their way while
 // the row is summed; ids and gradients are read again where they are used, and wait
 // for the last step in the sums' shared memory. Sums of g_i are fp64, in one order.
-// (512 x 151936 bf16: one id a row 58 us, 20 61, 64 63, 256 88; 255 x 50021 fp32 with
+// (512 x 151936 bf16: one id a row 57 us, 20 60, 64 62, 256 88; 255 x 50021 fp32 with
 // entropies: 64 ids 23 us, 256 34.)
 struct ManyRow {
   F2 ln_s;
