@@ -70,8 +70,10 @@ def test_scores(dev, B, V, dtype, keep, M, top):
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 def test_long_rows(dev, dtype):
     """One CTA a row with many groups of several steps, and clusters of 16."""
-    rng, x, tokens, _ = make_rows(5, 1, 1_500_007, dtype)
-    check(dev, x, dtype, given(rng, tokens, x.shape[1], 3), None, 100)
+    rng, x, tokens, mask = make_rows(5, 1, 1_500_007, dtype, 40_000)
+    t = given(rng, tokens, x.shape[1], 3)
+    check(dev, x, dtype, t, None, 100)
+    check(dev, x, dtype, t, mask, 128)
     B, V = 640, 33000
     rng, x, tokens, mask = make_rows(6, 2, V, dtype, 9000)
     r = rng.integers(0, 2, B)

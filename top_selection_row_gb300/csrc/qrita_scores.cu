@@ -32,6 +32,7 @@ constexpr int kScoreThreads = kLossThreads;
 constexpr int kGroups = 32;     // of a thread, at most
 constexpr int kListCap = 1024;  // candidates of a CTA
 constexpr int kHits = 512;      // groups read again
+constexpr int kMaskGroups = 4096;  // of a CTA under a mask, at most
 
 // Elements of the kernel's units, and the units a thread sums in one step.
 template <int DT, bool MASKED>
@@ -198,6 +199,9 @@ __global__ void __launch_bounds__(THREADS, kLossThreads * kLossBlocks / THREADS)
   __shared__ float row_of[6];  // m, S (its sign and NaN), ln S as a pair, H
   extern __shared__ __align__(16) unsigned char dynamic[];
   float* gmax = reinterpret_cast<float*>(dynamic);  // [groups][THREADS]
+  uint32_t* group_keys = reinterpret_cast<uint32_t*>(dynamic);  // (under a mask)
+  __shared__ int warp_units[MASKED ? THREADS / 32 : 1][64];
+  __shared__ unsigned short warp_bits[MASKED ? THREADS / 32 : 1][64];
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int tid = threadIdx.x;
@@ -244,6 +248,8 @@ __global__ void __launch_bounds__(THREADS, kLossThreads * kLossBlocks / THREADS)
   uint32_t before = 0u;  // logits that precede the token
   const int steps = (n + THREADS * K - 1) / (THREADS * K);
   int in_group = 0, g = 0;
+  const int each = p.group_steps * (MASKED ? 1 : K);  // units of a group
+  const int n_groups = MASKED && N > 0 ? (n + each - 1) / each : 0;
   auto summed = [&](float t, bool end) {
     group = fmaxf(group, t);
     if (N > 0 && (++in_group == p.group_steps || end)) {
@@ -275,28 +281,67 @@ __global__ void __launch_bounds__(THREADS, kLossThreads * kLossBlocks / THREADS)
   };
   if constexpr (MASKED) {
     const uint8_t* keep = sp.keep + sp.id(sp.u_lo);
-    for (int s = 0; s < steps; ++s) {
-      // the masks of all units first; logits only where a bit is set
-      const int u0 = s * (THREADS * K) + tid;
-      uint4 mw[K];
-#pragma unroll
-      for (int k = 0; k < K; ++k)
-        mw[k] = u0 + k * THREADS < n ? __ldcs(reinterpret_cast<const uint4*>(keep) + u0 + k * THREADS) : make_uint4(0u, 0u, 0u, 0u);
-      float t = -INFINITY;
-#pragma unroll
-      for (int k = 0; k < K; ++k) {
-        const uint32_t b = kept_bits(mw[k]);
-        if (b == 0u) continue;
-        const int u = u0 + k * THREADS;
+    // A warp lists its units with a bit set, in their order, and sums them 32 at a time,
+    // a lane each: a sparse row's would otherwise be one lane's work after another's.
+    // The largest kept logit of each group of neighbouring units is kept as a key.
+    const int warp = tid >> 5, lane = tid & 31;
+    for (int i = tid; N > 0 && i < n_groups; i += THREADS) group_keys[i] = 0u;
+    if (N > 0) __syncthreads();
+    int listed = 0;
+    auto sum_units = [&](int many) {  // of the warp's list, the first `many`
+      if (lane < many) {
+        const int u = warp_units[warp][lane];
+        const uint32_t b = warp_bits[warp][lane];
         uint4 w[W];
         float2 x[U / 2];
         sp.words(sp.u_lo + u, b, w);
         Sp::expand(w, b, x);
         if (counts) count_above(w[0], x, u);
-        t = fmaxf(t, run.add_unit(x, p.c));
+        const float t = run.add_unit(x, p.c);
+        if (N > 0) {
+          top = fmaxf(top, t);
+          atomicMax(&group_keys[u / each], f2key(t));
+        }
       }
-      summed(t, s + 1 == steps);
+    };
+    for (int s = 0; s < steps; ++s) {
+      const int u0 = s * (THREADS * K) + tid;
+      uint4 mw[K];
+#pragma unroll
+      for (int k = 0; k < K; ++k)
+        mw[k] = u0 + k * THREADS < n ? __ldcs(reinterpret_cast<const uint4*>(keep) + u0 + k * THREADS) : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+      for (int k = 0; k < K; ++k) {
+        const uint32_t b = kept_bits(mw[k]);
+        const uint32_t some = __ballot_sync(kAll, b != 0u);
+        if (some == 0u) continue;
+        if (b != 0u) {
+          const int at = listed + __popc(some & ((1u << lane) - 1u));
+          warp_units[warp][at] = u0 + k * THREADS;
+          warp_bits[warp][at] = static_cast<unsigned short>(b);
+        }
+        listed += __popc(some);
+        __syncwarp();
+        if (listed >= 32) {
+          sum_units(32);
+          __syncwarp();
+          listed -= 32;
+          int u = 0;
+          unsigned short rest = 0;
+          if (lane < listed) {
+            u = warp_units[warp][32 + lane];
+            rest = warp_bits[warp][32 + lane];
+          }
+          __syncwarp();
+          if (lane < listed) {
+            warp_units[warp][lane] = u;
+            warp_bits[warp][lane] = rest;
+          }
+          __syncwarp();
+        }
+      }
     }
+    sum_units(listed);
   } else {
     const uint4* units = reinterpret_cast<const uint4*>(sp.x + sp.id(sp.u_lo) * Elem<DT>::kBytes) + tid;
     const int full = n / (THREADS * K);
@@ -307,6 +352,10 @@ __global__ void __launch_bounds__(THREADS, kLossThreads * kLossBlocks / THREADS)
       run.add_exponents(x, p.c);
     };
     for (int s = 0; s < full; ++s, units += THREADS * K) {
+      // (L2 is asked for the next step meanwhile: with entropies, rank and 20 alternatives
+      // 1024 x 262144 bf16 117 us without, 102 with, 106 for the step after that)
+      if (tid == 0 && s + 1 < full)
+        asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(units + THREADS * K), "n"(THREADS * K * 16) : "memory");
       uint4 w[K];
       float2 x[K * U / 2];
 #pragma unroll
@@ -340,7 +389,15 @@ __global__ void __launch_bounds__(THREADS, kLossThreads * kLossBlocks / THREADS)
       summed(t, true);
     }
   }
-  const int groups = g;
+  // (under a mask a group is `each` neighbouring units, and a column of threads has some)
+  const int groups = MASKED ? (n_groups + THREADS - 1) / THREADS : g;
+  auto unit_of = [&](int group, int column, int j) {
+    return MASKED ? (group * THREADS + column) * each + j : (group * each + j) * THREADS + column;
+  };
+  auto group_max = [&](int i) {  // of the i-th, NaN where it has none
+    if (MASKED) return i < n_groups ? key2f(group_keys[i]) : NAN;
+    return gmax[i];
+  };
   // the row's head and tail
   int64_t end_j = -1;
   float end_x = -INFINITY;
@@ -421,21 +478,28 @@ __global__ void __launch_bounds__(THREADS, kLossThreads * kLossBlocks / THREADS)
     least = key2f(bound);
     if (end_j >= 0) push(end_x, end_j);
     // the groups that reach it, then their units, each by a thread
-    for (int i = wt; i < groups * (THREADS / 4); i += kOthers) {
-      const float4 v = reinterpret_cast<const float4*>(gmax)[i];
-      const float m[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-        if (m[j] >= least && m[j] > -INFINITY) {
-          const int at = atomicAdd(&found, 1);
-          if (at < kHits) hits[at] = static_cast<unsigned short>(4 * i + j);
-        }
+    auto hit = [&](float m, int i) {
+      if (m >= least && m > -INFINITY) {
+        const int at = atomicAdd(&found, 1);
+        if (at < kHits) hits[at] = static_cast<unsigned short>(i);
+      }
+    };
+    if (MASKED) {
+      for (int i = wt; i < n_groups; i += kOthers) hit(group_max(i), i);
+    } else {
+      for (int i = wt; i < groups * (THREADS / 4); i += kOthers) {
+        const float4 v = reinterpret_cast<const float4*>(gmax)[i];
+        hit(v.x, 4 * i);
+        hit(v.y, 4 * i + 1);
+        hit(v.z, 4 * i + 2);
+        hit(v.w, 4 * i + 3);
+      }
     }
     others_sync();
-    const int each = p.group_steps * K, tasks = min(found, kHits) * each;
+    const int tasks = min(found, kHits) * each;
     for (int i = wt; i < tasks; i += kOthers) {
-      const int hit = hits[i / each];
-      const int u = ((hit / THREADS) * each + i % each) * THREADS + hit % THREADS;
+      const int group = hits[i / each];
+      const int u = unit_of(group / THREADS, group % THREADS, i % each);
       if (u >= n) continue;
       uint4 w[W];
       float2 x[U / 2];
@@ -479,22 +543,20 @@ __global__ void __launch_bounds__(THREADS, kLossThreads * kLossBlocks / THREADS)
       constexpr int kRoom = kListCap - 2 * THREADS;
       if (end_j >= 0) put(end_x, end_j);
       for (int i = 0; i < groups; ++i) {
-        const int s0 = i * p.group_steps, s1 = min(s0 + p.group_steps, steps);
-        const float m = gmax[i * THREADS + tid];
-        const bool some = m > -INFINITY && order_key(m, sp.id(sp.u_lo + s0 * (THREADS * K) + tid)) > above;
+        const float m = group_max(i * THREADS + tid);
+        const bool some = m > -INFINITY && order_key(m, sp.id(sp.u_lo + unit_of(i, tid, 0))) > above;
         if (!__syncthreads_or(some)) continue;
-        for (int s = s0; s < s1; ++s)
-          for (int k = 0; k < K; ++k) {
-            const int64_t u = sp.u_lo + s * (THREADS * K) + k * THREADS + tid;
-            const bool mine = some && u < sp.u_hi;
-            for (int j = 0; j < U; j += 2) {
-              cut(kRoom);
-              if (mine) {
-                put(sp.value(sp.id(u) + j), sp.id(u) + j);
-                put(sp.value(sp.id(u) + j + 1), sp.id(u) + j + 1);
-              }
+        for (int g = 0; g < each; ++g) {
+          const int u = unit_of(i, tid, g);
+          const bool mine = some && u < n;
+          for (int j = 0; j < U; j += 2) {
+            cut(kRoom);
+            if (mine) {
+              put(sp.value(sp.id(sp.u_lo + u) + j), sp.id(sp.u_lo + u) + j);
+              put(sp.value(sp.id(sp.u_lo + u) + j + 1), sp.id(sp.u_lo + u) + j + 1);
             }
           }
+        }
       }
       __syncthreads();
       c = count;
@@ -604,17 +666,28 @@ cudaError_t launch_scores_of(const ScoreParams& p, cudaStream_t st) {
   q.per = (units + C - 1) / C;
   const int64_t steps = (q.per + threads * K - 1) / (threads * K);
   q.group_steps = steps <= kGroups ? 1 : static_cast<int>((steps + kGroups - 1) / kGroups);
+  if (MASKED) q.group_steps = static_cast<int>((q.per + kMaskGroups - 1) / kMaskGroups > 0 ? (q.per + kMaskGroups - 1) / kMaskGroups : 1);
   size_t smem = 0;
   if (p.N > 0) {
-    smem = static_cast<size_t>((steps + q.group_steps - 1) / q.group_steps) * threads * sizeof(float);
+    smem = static_cast<size_t>(MASKED ? (q.per + q.group_steps - 1) / q.group_steps
+                                      : (steps + q.group_steps - 1) / q.group_steps * threads) * sizeof(float);
     const size_t lists = static_cast<size_t>(C) * p.N * 16u;
     if (C > 1 && lists > smem) smem = lists;
   }
   static_assert(kGroups * kScoreThreads * 4 + 16 * 1024 <= 48 * 1024, "a kernel that does not ask has 48 KB");
+  static_assert(kMaskGroups * 4 <= kMaxRanks * kMaxTop * 16, "groups under a mask fit in what is asked for");
   static_assert(kMaxRanks * kMaxTop * 16 <= kGroups * kScoreThreads * 4, "the lists fit in the groups' place");
   const unsigned grid = static_cast<unsigned>(p.B * C);
-  if (small) return launch(&score_kernel<kScoreThreads / 2, DT, ENT, MASKED>, grid, threads, C, st, smem, q);
-  return launch(&score_kernel<kScoreThreads, DT, ENT, MASKED>, grid, threads, C, st, smem, q);
+  auto go = [&](auto* fn, std::atomic<uint64_t>& done) {
+    if (MASKED) {  // (the warps' lists beside the most that the lists of a cluster take)
+      const cudaError_t e = allow_smem(fn, kMaxRanks * kMaxTop * 16, done);
+      if (e != cudaSuccess) return e;
+    }
+    return launch(fn, grid, threads, C, st, smem, q);
+  };
+  static std::atomic<uint64_t> done[2];
+  return small ? go(&score_kernel<kScoreThreads / 2, DT, ENT, MASKED>, done[0])
+               : go(&score_kernel<kScoreThreads, DT, ENT, MASKED>, done[1]);
 }
 
 template <int DT>
