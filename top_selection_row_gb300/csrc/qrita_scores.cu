@@ -179,11 +179,13 @@ __device__ __forceinline__ unsigned long long ld_dsmem_u64(uint32_t addr) {
   return v;
 }
 
-// One CTA a row, or a cluster for few rows. HBM and issue slots bound it together:
-// 1024 x 262144 bf16 91 us with entropies (5.9 TB/s), 101 with the rank besides, 117
-// with 20 alternatives too, of which 8 us are the end of the wave: its blocks' steps
-// that read nothing (bound, groups read again, order). 4 x 32000 fp32 with 5
-// alternatives 8.6 us, of latency.
+// One CTA a row, or a cluster for few rows. HBM bounds the log-probabilities alone
+// (1024 x 262144 bf16 82 us, 6.6 TB/s), and issue slots with it the rest: 88 with
+// entropies, 90 with the rank besides, 102 with 20 alternatives too, of which 8 are the
+// end of the wave: its blocks' steps that read nothing (bound, groups read again,
+// order). 4 x 32000 fp32 with 5 alternatives 8.7 us, of latency. Under a mask that keeps
+// 256 of 262144 ids 79 us with all of it (268 MB of masks); one that keeps a tenth at
+// random 285 (nearly every unit has a bit, and a warp has one load a lane under way).
 template <int THREADS, int DT, bool ENT, bool MASKED>
 __global__ void __launch_bounds__(THREADS, kLossThreads * kLossBlocks / THREADS) score_kernel(const ScoreParams p) {
   using Sp = Span<DT, MASKED>;
@@ -656,7 +658,7 @@ cudaError_t launch_scores_of(const ScoreParams& p, cudaStream_t st) {
   }
   // Blocks of half the threads where rows are short, and where one row a block takes
   // more than a wave: twice as many are on an SM, and a wave ends in the steps of its
-  // blocks that read nothing (1024 x 262144 bf16 117 us, with 256 threads 122). Not
+  // blocks that read nothing (1024 x 262144 bf16 117 us then, with 256 threads 122). Not
   // for many alternatives: the bound is then that of too few maxima.
   const bool small = C == 1 && (bytes <= kShortRow || (p.N > 0 && p.B > sms * kLossBlocks)) && p.N <= kScoreThreads / 8;
   const int threads = small ? kScoreThreads / 2 : kScoreThreads;
