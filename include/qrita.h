@@ -549,7 +549,10 @@ int qrita_token_scores_grad(const void* logits, int dtype, int64_t B, int64_t V,
  *
  * Scores are fp32 sums of exact products, softmax sums fp32. bf16 heads of 32, 64,
  * 96, 128, 192 or 256 dimensions whose rows are aligned to 16 bytes run on the
- * tensor cores. One kernel on stream. Idle sequences are left as they were.
+ * tensor cores, and windows of more than 16 rows (T G) of up to 256 dimensions. One
+ * kernel on stream, or one for every 128 rows of such a window. Idle sequences are
+ * left as they were. (Where a bounded wait of a kernel gives up, not expected on a
+ * healthy device, a share's weights are NaN.)
  */
 int qrita_cache_weights(int64_t B, int64_t H, int64_t S, const void* query, int dtype, int32_t T, int32_t G, int32_t D,
                         const int64_t* query_strides, const void* keys, const int64_t* key_strides, double scale,

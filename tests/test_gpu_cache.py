@@ -378,3 +378,42 @@ def test_refusals_of_the_binding(dev):
     n.fill_(10)
     a = q.qrita_cache_weights(qq + 1, one.expand(2, 2, 10, 32), w.clone(), n)
     assert torch.equal(a, q.qrita_cache_weights(qq + 1, one.expand(2, 2, 10, 32).contiguous(), w.clone(), n))
+
+
+def test_offsets_past_32_bits(dev):
+    """Heads of a cache, and rows of logits, more than 2^31 elements apart: the same as
+    side by side."""
+    import torch
+
+    import top_selection_row_gb300 as q
+
+    far = 2**31 + 64
+    buf = torch.empty(far + 2**16, dtype=torch.bfloat16, device=dev)
+    gen = torch.Generator(device=dev).manual_seed(4)
+    near = torch.randn(1, 2, 300, 64, generator=gen, device=dev).bfloat16()
+    k = buf.as_strided((1, 2, 300, 64), (2 * far, far, 64, 1))
+    k.copy_(near)
+    n = torch.tensor([290], dtype=torch.int32, device=dev)
+    w = torch.rand(1, 2, 300, generator=gen, device=dev)
+    for T in (1, 40):
+        qq = torch.randn(1, T, 8, 64, generator=gen, device=dev).bfloat16()
+        assert torch.equal(q.qrita_cache_weights(qq, k, w.clone(), n), q.qrita_cache_weights(qq, near, w.clone(), n))
+    assert all(torch.equal(a, b) for a, b in zip(q.qrita_cache_evict(k, k, w, n, 50), q.qrita_cache_evict(near, near, w, n, 50)))
+    out = q.qrita_cache_evict(near, near, w, n, 50)
+    far_out = out._replace(keys=buf.as_strided((1, 2, 50, 64), (2 * far, far, 64, 1)), values=torch.empty_like(out.values))
+    got = q.qrita_cache_evict(near, near, w, n, 50, out=far_out)
+    assert torch.equal(got.keys, q.qrita_cache_evict(near, near, w, n, 50).keys)
+    k.copy_(near)
+    state = [[w.clone(), torch.arange(300, dtype=torch.int32, device=dev).expand(1, 2, 300).contiguous(), n + 10, n + 10] for _ in range(2)]
+    new = torch.randn(1, 2, 64, generator=gen, device=dev).bfloat16()
+    slots = [q.qrita_cache_insert(c, c.clone() if c is near else near.clone(), *s, new, new, 300) for c, s in zip((k, near), state)]
+    assert torch.equal(*slots) and torch.equal(k, near)
+    x = torch.randn(2, 9000, generator=gen, device=dev).bfloat16()
+    rows = buf.as_strided((2, 9000), (far, 1))
+    rows.copy_(x)
+    ids = torch.randint(0, 9000, (2, 4), generator=gen, device=dev, dtype=torch.int32)
+    a, b = (q.qrita_token_scores(v, ids, top=9, entropy=True, rank=True) for v in (rows, x))
+    assert all(torch.equal(u, v) for u, v in zip(a, b))
+    g = torch.randn(2, 4, generator=gen, device=dev)
+    want = q.qrita_token_scores_grad(x, ids, g)
+    assert torch.equal(q.qrita_token_scores_grad(rows, ids, g, out_grad=rows), want)
