@@ -857,12 +857,14 @@ def qrita_cache_evict(keys, values, weights, lengths, budget, sink=0, recent=0, 
     if budget < 1 or H < 1 or S < 1:
         raise ValueError("a cache has heads and slots, and a budget of at least one")
     if out is None:
-        i32 = torch.int32
+        at_out = torch.empty((B, H, budget), dtype=torch.int32, device=dev)
         got = EvictedCache(torch.empty((B, H, budget, Dk), dtype=keys.dtype, device=dev),
                            torch.empty((B, H, budget, Dv), dtype=values.dtype, device=dev),
-                           torch.empty((B, H, budget), dtype=torch.float32, device=dev),
-                           torch.empty((B, H, budget), dtype=i32, device=dev),
-                           torch.empty((B, H, budget), dtype=i32, device=dev), torch.empty(B, dtype=i32, device=dev))
+                           torch.empty((B, H, budget), dtype=torch.float32, device=dev), at_out, torch.empty_like(at_out),
+                           torch.empty_like(lengths))
+        more = budget
+        oks = _strides((H * budget * Dk, budget * Dk, Dk), kb // Dk)
+        ovs = _strides((H * budget * Dv, budget * Dv, Dv), vb // Dv)
     else:
         got = EvictedCache(*out)
         if got.keys.dtype != keys.dtype or got.values.dtype != values.dtype:
@@ -876,9 +878,8 @@ def qrita_cache_evict(keys, values, weights, lengths, budget, sink=0, recent=0, 
         _needed(got.lengths, B, torch.int32, "out lengths", dev)
         _written(got.keys, "out keys")
         _written(got.values, "out values")
-    more = got.keys.shape[2]
-    oks, _ = _cache(got.keys, "out keys", dev, (B, H, more, Dk))
-    ovs, _ = _cache(got.values, "out values", dev, (B, H, more, Dv))
+        oks, _ = _cache(got.keys, "out keys", dev, (B, H, more, Dk))
+        ovs, _ = _cache(got.values, "out values", dev, (B, H, more, Dv))
     _call(lib().qrita_cache_evict, dev, B, H, S, n, w, at, se, budget, sink, recent, keys.data_ptr(), kb, ks,
           values.data_ptr(), vb, vs, got.keys.data_ptr(), oks, got.values.data_ptr(), ovs, more, got.weights.data_ptr(),
           got.positions.data_ptr(), got.slots.data_ptr(), got.lengths.data_ptr())
