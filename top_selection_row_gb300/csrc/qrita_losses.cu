@@ -382,7 +382,8 @@ struct Many {
       if (first != k) continue;
       const float lp = f2_float(logp_of(x[i], r.m, r.ln_s, p.inv_t, p.inv_t_lo)), prob = expf(lp);
       float rest = r.a - G;
-      if (r.h != 0.f) rest = fmaf(r.h, lp + r.H, rest);
+      // (a probability of 0 takes nothing of it, not 0 * inf where log p, or h times it, has left fp32)
+      if (r.h != 0.f && prob != 0.f) rest = fmaf(r.h, lp + r.H, rest);
       Elem<DT>::store(grow, id, p.inv_t * (G * -expm1f(lp) - prob * rest));
     }
   }
