@@ -4,7 +4,9 @@ oracle; tolerances as tests/test_gpu_scores.py unless said."""
 import numpy as np
 import pytest
 
-from test_gpu_losses import REL, dev, make_rows, put  # noqa: F401
+from oracle import scores_grad_row
+from test_gpu_losses import BF16_ROUND, F32_ROUND, dev, make_rows, near, put, widened  # noqa: F401
+from parity_helpers import to_device
 from test_gpu_scores import check_grad, given
 from workloads import f32_to_bf16_bits
 
@@ -41,3 +43,41 @@ def test_gradients_of_tokens_of_the_lowest_value(dev, B, V, keep, dtype, inv_t, 
     g[:, 4] = 0
     h = (size * (1 + rng.random(B))).astype(np.float32)
     check_grad(dev, x, dtype, ids, g, h, mask, inv_t)
+
+
+@pytest.mark.parametrize("B,V,keep", [(3, 4000, 0), (1, 1_200_003, 0), (3, 4000, 100)])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_gradient_of_one_token_listed_often(dev, B, V, keep, dtype):  # noqa: F811
+    """A token of nearly all the probability, listed 250 times with gradients that
+    nearly cancel, beside six others. Its entry is G (1 - p) - p R, G its own
+    gradients' sum and R the others'. Sums are fp64 (256 2^-53 of their magnitudes) and
+    rounded once; log p is off by 2^-22 + 2^-24 (10 + E), E < 1 here, and so are 1 - p and
+    p; each of the two products' four operations rounds by 2^-24, expm1 and exp by two
+    such steps."""
+    import top_selection_row_gb300 as q
+
+    rng = np.random.default_rng(V)
+    x = rng.standard_normal((B, V)).astype(np.float32)
+    x[:, 17] = 10 + np.log(V)
+    mask = None
+    if keep:
+        mask = np.zeros((B, V), np.uint8)
+        mask[:, :keep] = 1
+    ids = np.full((B, 256), 17, np.int32)
+    others = rng.permutation(256)[:6]
+    ids[:, others] = 20 + np.arange(6)
+    g = (rng.choice([-1, 1], ids.shape) * rng.uniform(90, 110, ids.shape)).astype(np.float32)
+    g[:, others] = rng.uniform(-1, 1, (B, 6))
+    own = ids == 17
+    last = np.flatnonzero(own[0])[-1]
+    g[:, last] = 3 - np.where(own, g, 0).astype(np.float64).sum(1) + g[:, last]
+    if dtype == "bf16":
+        x = f32_to_bf16_bits(x)
+    got = q.qrita_token_scores_grad(to_device(x, dtype, dev), put(dev, ids), put(dev, g), mask=put(dev, mask))
+    got = got[:, 17].float().cpu().numpy().astype(np.float64)
+    xs = widened(x, dtype)
+    for r in range(B):
+        want = scores_grad_row(xs[r], None if mask is None else mask[r], ids[r], g[r])[0][17]
+        G, R = (np.where(w, g[r], 0).astype(np.float64).sum() for w in (own[r], ~own[r]))
+        tol = (abs(G) + abs(R)) * (2.0**-22 + 11 * 2.0**-24 + 6 * 2.0**-24) + 256 * 2.0**-53 * np.abs(g[r]).sum()
+        near(got[r], want, tol + (BF16_ROUND if dtype == "bf16" else F32_ROUND) * abs(want), f"row {r}")

@@ -261,12 +261,14 @@ __device__ __forceinline__ float grad_one(float x, const RowGrad& g, float c) {
 // taken as G_j (1 - p_j) - p_j (a - G_j + ...), 1 - p_j by expm1. A thread keeps the
 // logits of its ids (read before a gradient is written over them), on their way while
 // the row is summed; ids and gradients are read again where they are used, and wait
-// for the last step in the sums' shared memory. Sums of g_i are fp64, in one order.
+// for the last step in the sums' shared memory. Sums of g_i, of a row and of an id,
+// are fp64, each in one order: a - G_j is what is left of their difference.
 // (512 x 151936 bf16: one id a row 57 us, 20 60, 64 62, 256 88; 255 x 50021 fp32 with
 // entropies: 64 ids 23 us, 256 34.)
 struct ManyRow {
+  double a;
   F2 ln_s;
-  float m, H, a, h;
+  float m, H, h;
 };
 
 template <int THREADS>
@@ -347,13 +349,13 @@ struct Many {
                                                     const double* ranks, ManyRow& r) {
     double a = 0.0;
     for (uint32_t i = 0; i < p.C; ++i) a += ranks[i];
-    r.a = static_cast<float>(a);
+    if (st.s.hi != st.s.hi) a = st.s.hi;  // (NaN for the whole row)
+    r.a = a;
     r.h = ENT && st.s.hi != 0.f ? p.g_entropy[row] : 0.f;
     r.H = v.H;
     r.m = st.m;
     r.ln_s = st.s.hi != 0.f ? ln_pair(sum_of(st)) : f2_make(0.f, 0.f);
-    if (st.s.hi != st.s.hi) r.a = st.s.hi;  // (NaN for the whole row)
-    return row_grad(r.a, r.h, -INFINITY, v.H, v.ln_s, st.m, st.s.hi, p.inv_t);
+    return row_grad(static_cast<float>(a), r.h, -INFINITY, v.H, v.ln_s, st.m, st.s.hi, p.inv_t);
   }
 
   // The entries of this CTA's ids, over what a barrier before this has seen written.
@@ -367,7 +369,7 @@ struct Many {
       const int k = threadIdx.x + i * THREADS;
       if (x[i] == -INFINITY) continue;
       const int id = ids[k];
-      float G = 0.f;
+      double sum = 0.0;
       int first = k;
       for (int j = 0; j < p.K; j += 4) {  // (behind the last id are ids of -1)
         const int4 v = *reinterpret_cast<const int4*>(ids + j);
@@ -376,12 +378,13 @@ struct Many {
         for (int n = 0; n < 4; ++n)
           if (same[n] == id) {
             first = min(first, j + n);
-            G += g[j + n];
+            sum += g[j + n];
           }
       }
       if (first != k) continue;
       const float lp = f2_float(logp_of(x[i], r.m, r.ln_s, p.inv_t, p.inv_t_lo)), prob = expf(lp);
-      float rest = r.a - G;
+      const float G = static_cast<float>(sum);
+      float rest = static_cast<float>(r.a - sum);
       // (a probability of 0 takes nothing of it, not 0 * inf where log p, or h times it, has left fp32)
       if (r.h != 0.f && prob != 0.f) rest = fmaf(r.h, lp + r.H, rest);
       Elem<DT>::store(grow, id, p.inv_t * (G * -expm1f(lp) - prob * rest));
