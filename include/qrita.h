@@ -454,7 +454,8 @@ int qrita_preference_loss(const void* logits, int dtype, int64_t B, int64_t V, i
  *   tokens       int32[B, M]; M from 0 to 8192 (NULL where M is 0).
  *   N            0 to 128.
  *   out_logp     float[B, M]: log p of each token; 0 for padding, -inf where p
- *                is 0 (not kept, or a logit of -inf).
+ *                is 0 (not kept, or a logit of -inf) or log p is below fp32's range
+ *                (the type's lowest value at an inv_temperature above 1).
  *   out_rank     int32[B] or NULL (NULL where M is 0): how many kept tokens
  *                precede tokens[r, 0] in the stable descending order of the row
  *                (0: it is the first); -1 where it is padding or its p is 0.
@@ -480,7 +481,7 @@ int qrita_token_scores(const void* logits, int dtype, int64_t B, int64_t V, int6
  *                    + grad_entropy[r] d H_r / d x_j,
  * the derivatives as in qrita_token_logprobs_grad. The ids are given tokens, top
  * ids, or both in one row; one that is listed twice counts twice, padding and
- * tokens of probability 0 count for nothing.
+ * tokens of probability 0 (not kept, or a logit of -inf) count for nothing.
  *
  *   ids                      int32[B, K]; K from 1 to 256.
  *   grad_logp                float[B, K], grad_entropy float[B]; either may be

@@ -4,7 +4,7 @@ oracle; tolerances as tests/test_gpu_scores.py unless said."""
 import numpy as np
 import pytest
 
-from oracle import scores_grad_row
+from oracle import scores_grad_row, scores_row
 from test_gpu_losses import BF16_ROUND, F32_ROUND, dev, make_rows, near, put, widened  # noqa: F401
 from parity_helpers import to_device
 from test_gpu_scores import check_grad, given
@@ -81,3 +81,23 @@ def test_gradient_of_one_token_listed_often(dev, B, V, keep, dtype):  # noqa: F8
         G, R = (np.where(w, g[r], 0).astype(np.float64).sum() for w in (own[r], ~own[r]))
         tol = (abs(G) + abs(R)) * (2.0**-22 + 11 * 2.0**-24 + 6 * 2.0**-24) + 256 * 2.0**-53 * np.abs(g[r]).sum()
         near(got[r], want, tol + (BF16_ROUND if dtype == "bf16" else F32_ROUND) * abs(want), f"row {r}")
+
+
+@pytest.mark.parametrize("B,V,keep", [(5, 4000, 0), (2, 70001, 0), (700, 3000, 0), (5, 4000, 40)])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_ranks_of_tokens_of_the_lowest_value(dev, B, V, keep, dtype):  # noqa: F811
+    """Log-probabilities beyond fp32 are -inf there; ranks and alternatives are those of
+    the order, which has them."""
+    import top_selection_row_gb300 as q
+
+    _, x, ids, mask = with_lowest(V + keep, min(B, 5), V, dtype, keep)
+    ids = ids[:, 3:]
+    some = np.arange(B) % len(ids)
+    x, ids, mask = x[some], ids[some], None if mask is None else mask[some]
+    got = q.qrita_token_scores(to_device(x, dtype, dev), put(dev, ids), top=60, mask=put(dev, mask), inv_temperature=1.25, rank=True)
+    xs = widened(x, dtype)
+    want = [scores_row(xs[r], None if mask is None else mask[r], ids[r], 1.25, 60) for r in range(min(B, 5))]
+    assert np.array_equal(got.rank.cpu().numpy(), np.array([w[1] for w in want])[some])
+    assert np.array_equal(got.top_ids.cpu().numpy(), np.array([w[3] for w in want])[some])
+    below = np.array([w[0] for w in want])[some] < -3.5e38
+    assert below[:, 0].any() and np.isneginf(got.logp.cpu().numpy()[below]).all()

@@ -616,17 +616,15 @@ __global__ void __launch_bounds__(THREADS, kLossThreads * kLossBlocks / THREADS)
     if (nan) return total;
     return total == 0.f || x == -INFINITY ? -INFINITY : f2_float(logp_of(x, m, ln_s, p.inv_t, p.inv_t_lo));
   };
-  float lp0 = 0.f;
   for (int i = tid; i < p.M; i += THREADS) {
     const int32_t t = i == tid ? my_token : p.tokens[row * p.M + i];
     float lp = 0.f;
     if (t >= 0 && t < p.V) lp = score(i == tid ? mine : sp.value(t));
     p.logp[row * p.M + i] = lp;
-    if (i == 0) lp0 = lp;
   }
   if (tid == 0) {
-    if (p.rank != nullptr)
-      p.rank[row] = counts && !nan && lp0 > -INFINITY ? static_cast<int32_t>(ranked) : -1;
+    // (a finite kept logit has a rank, also where its log p has left fp32)
+    if (p.rank != nullptr) p.rank[row] = counts && !nan ? static_cast<int32_t>(ranked) : -1;
     if (ENT) p.entropy[row] = nan ? total : row_of[4];
   }
   if (N > 0) {
