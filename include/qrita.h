@@ -522,7 +522,10 @@ int qrita_token_scores_grad(const void* logits, int dtype, int64_t B, int64_t V,
  *                Both NULL: slot s has position s, and seen is the length.
  *   strides      host int64 arrays, not negative; a slot's key or value is
  *                contiguous. Rows of inputs may share memory (an expanded head);
- *                rows that are written share none, and outputs overlap nothing.
+ *                rows that are written share none, and what is written overlaps
+ *                nothing else: lengths, seen, weights, positions and slots that
+ *                overlap one another where one of them is written are QRITA_EINVAL,
+ *                and so are keys and values written to the same place.
  * Ownership, streams and errors as qrita_select; QRITA_EINVAL also for sizes,
  * strides or scalars outside their stated range. Nothing is allocated or kept.
  * B == 0 launches nothing.

@@ -58,6 +58,34 @@ bool overlap(const CacheRows& a, const CacheRows& b, int64_t B, int64_t H, int64
          static_cast<Wide>(reinterpret_cast<uintptr_t>(b.at)) < end(a, slots_a);
 }
 
+// A contiguous vector's addresses.
+struct Range {
+  const void* at;  // null: there is none
+  int64_t bytes;
+};
+
+bool overlap(const Range& a, const Range& b) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a.at), y = reinterpret_cast<uintptr_t>(b.at);
+  return x != 0 && y != 0 && x < y + static_cast<uint64_t>(b.bytes) && y < x + static_cast<uint64_t>(a.bytes);
+}
+
+// Whether a vector that is written overlaps another one, or one that is read. (A CTA
+// writes its row's while others still read theirs: what they read would be a matter of
+// timing.)
+bool clash(std::initializer_list<Range> written, std::initializer_list<Range> read) {
+  for (const Range* w = written.begin(); w != written.end(); ++w) {
+    for (const Range* v = written.begin(); v != w; ++v)
+      if (overlap(*w, *v)) return true;
+    for (const Range& r : read)
+      if (overlap(*w, r)) return true;
+  }
+  return false;
+}
+
+// Whether two caches that are written have the same first row. (They may lie in one
+// tensor, side by side.)
+bool same_rows(const CacheRows& a, const CacheRows& b) { return overlap(Range{a.at, a.bytes}, Range{b.at, b.bytes}); }
+
 bool budget_ok(int64_t S, int32_t budget, int32_t sink, int32_t recent, CacheOrder* out) {
   out->budget = budget;
   out->sink = sink;
@@ -83,6 +111,8 @@ int qrita_cache_weights(int64_t B, int64_t H, int64_t S, const void* query, int 
   if (!std::isfinite(static_cast<float>(scale)) || !(decay >= 0.0 && decay <= 1.0)) return QRITA_EINVAL;
   if (B == 0) return QRITA_OK;
   if (query == nullptr || keys == nullptr || query_strides == nullptr || key_strides == nullptr) return QRITA_EINVAL;
+  const int64_t order = 4 * B * H * S;
+  if (qrita::clash({{weights, order}}, {{lengths, 4 * B}, {positions, order}, {seen, 4 * B}})) return QRITA_EINVAL;
   const uint64_t eb = dtype == QRITA_DTYPE_F32 ? 4 : 2;
   if (reinterpret_cast<uintptr_t>(query) % eb != 0 || reinterpret_cast<uintptr_t>(keys) % eb != 0) return QRITA_EINVAL;
   for (int i = 0; i < 3; ++i)
@@ -122,8 +152,12 @@ int qrita_cache_evict(int64_t B, int64_t H, int64_t S, const int32_t* lengths, c
     return QRITA_EINVAL;
   for (const qrita::CacheRows* to : {&prm.out_key, &prm.out_value})
     if (qrita::overlap(prm.key, *to, B, H, S, budget) || qrita::overlap(prm.value, *to, B, H, S, budget)) return QRITA_EINVAL;
-  if (out_weights == weights || (positions != nullptr && out_positions == positions)) return QRITA_EINVAL;
   if (out_weights == nullptr || out_positions == nullptr || out_slots == nullptr || out_lengths == nullptr) return QRITA_EINVAL;
+  const int64_t order = 4 * B * H * S, out_order = 4 * B * H * out_S;
+  if (qrita::same_rows(prm.out_key, prm.out_value) ||
+      qrita::clash({{out_weights, out_order}, {out_positions, out_order}, {out_slots, 4 * B * H * budget}, {out_lengths, 4 * B}},
+                   {{weights, order}, {positions, order}, {lengths, 4 * B}, {seen, 4 * B}}))
+    return QRITA_EINVAL;
   if (B * H > qrita::kMax / ((budget + 63) / 64)) return QRITA_EUNSUPPORTED;
   prm.out_slots_of = out_S;
   prm.out_weights = out_weights;
@@ -148,6 +182,10 @@ int qrita_cache_insert(int64_t B, int64_t H, int64_t S, int32_t* lengths, int32_
       !qrita::rows_ok(values, value_bytes, value_strides, true, &prm.value) ||
       !qrita::rows_ok(new_keys, key_bytes, new_key_strides, false, &prm.new_key) ||
       !qrita::rows_ok(new_values, value_bytes, new_value_strides, false, &prm.new_value))
+    return QRITA_EINVAL;
+  const int64_t order = 4 * B * H * S;
+  if (qrita::same_rows(prm.key, prm.value) ||
+      qrita::clash({{weights, order}, {positions, order}, {lengths, 4 * B}, {seen, 4 * B}, {out_slots, 4 * B * H}}, {}))
     return QRITA_EINVAL;
   prm.out_slots = out_slots;
   return qrita::launch_cache_insert(prm, stream) == 0 ? QRITA_OK : QRITA_ECUDA;
