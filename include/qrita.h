@@ -554,14 +554,25 @@ int qrita_token_scores_grad(const void* logits, int dtype, int64_t B, int64_t V,
  * Scores are fp32 sums of exact products, softmax sums fp32. bf16 heads of 32, 64,
  * 96, 128, 192 or 256 dimensions whose rows are aligned to 16 bytes run on the
  * tensor cores, and windows of more than 16 rows (T G) of up to 256 dimensions. One
- * kernel on stream, or one for every 128 rows of such a window. Idle sequences are
- * left as they were. (Where a bounded wait of a kernel gives up, not expected on a
- * healthy device, a share's weights are NaN.)
+ * kernel on stream, or one for every 128 / G (rounded down) queries of such a window.
+ * Idle sequences are left as they were. (Where a bounded wait of a window's kernel
+ * gives up, not expected on a healthy device, the weights that it leaves without their
+ * scores are NaN: those of a share of a head's slots, or all that a query sees.)
  */
 int qrita_cache_weights(int64_t B, int64_t H, int64_t S, const void* query, int dtype, int32_t T, int32_t G, int32_t D,
                         const int64_t* query_strides, const void* keys, const int64_t* key_strides, double scale,
                         double decay, const int32_t* lengths, const int32_t* positions, const int32_t* seen,
                         float* weights, qrita_stream_t stream);
+
+/* qrita_cache_weights with flags (bitwise or; others are QRITA_EINVAL). */
+#define QRITA_CACHE_FLAG_TEST_GIVE_UP_SUMS 0x1u    /* tests only: in each sequence's first head */
+#define QRITA_CACHE_FLAG_TEST_GIVE_UP_WEIGHTS 0x2u /* a bounded wait of a window's kernel for the */
+                                                   /* scores of its sums, or of its weights, gives */
+                                                   /* up at once: weights of that head are NaN    */
+int qrita_cache_weights_ex(int64_t B, int64_t H, int64_t S, const void* query, int dtype, int32_t T, int32_t G, int32_t D,
+                           const int64_t* query_strides, const void* keys, const int64_t* key_strides, double scale,
+                           double decay, const int32_t* lengths, const int32_t* positions, const int32_t* seen,
+                           float* weights, uint32_t flags, qrita_stream_t stream);
 
 /*
  * qrita_cache_evict: the first min(length, budget) slots in order of each sequence

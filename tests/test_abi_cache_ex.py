@@ -1,0 +1,30 @@
+"""The cache's entry points with flags: the same refusals as without, and unknown flags
+(no GPU here; pointers are never dereferenced, and no call here is a valid one)."""
+
+import ctypes
+
+import pytest
+
+from test_abi_cache import BASE, K, V, strides
+from test_abi_losses import EINVAL, NULL, L  # noqa: F401
+
+
+def weights_ex(L, flags=0, **kw):  # noqa: F811
+    a = {**BASE, "q": V, "dtype": 1, "T": 2, "G": 2, "D": 64, "qs": strides(1024, 512, 64), "keys": K,
+         "ks": strides(25600, 6400, 64), "scale": 0.125, "decay": 1.0, **kw}
+    return L.qrita_cache_weights_ex(a["B"], a["H"], a["S"], a["q"], a["dtype"], a["T"], a["G"], a["D"], a["qs"], a["keys"], a["ks"],
+                                    a["scale"], a["decay"], a["lengths"], a["positions"], a["seen"], a["weights"],
+                                    ctypes.c_uint32(flags), NULL)
+
+
+@pytest.mark.parametrize("call", [weights_ex])
+@pytest.mark.parametrize("flags", [4, 8, 0x1000, 0x80000001])
+def test_unknown_flags(L, call, flags):  # noqa: F811
+    assert call(L, flags) == EINVAL
+
+
+@pytest.mark.parametrize("flags", [0, 1, 2, 3])
+@pytest.mark.parametrize("bad", [dict(dtype=2), dict(T=0), dict(D=1025), dict(q=NULL), dict(keys=NULL), dict(decay=1.1), dict(S=0), dict(lengths=NULL)],
+                         ids=str)
+def test_bad_weights(L, bad, flags):  # noqa: F811
+    assert weights_ex(L, flags, **bad) == EINVAL

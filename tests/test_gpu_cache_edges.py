@@ -59,3 +59,35 @@ def test_keys_and_values_side_by_side(dev):  # noqa: F811
     for c in (a, b):
         q.qrita_cache_insert(*c, *new, 20)
     assert all(torch.equal(x, y) for x, y in zip(a, b))
+
+
+@pytest.mark.parametrize("B,H,G,T,S,D", [(2, 2, 4, 16, 3000, 128), (160, 2, 1, 40, 700, 64), (1, 3, 2, 100, 2500, 200)])
+@pytest.mark.parametrize("late", [False, True])
+def test_a_window_whose_wait_gives_up(dev, B, H, G, T, S, D, late):  # noqa: F811
+    """Sums without their scores make every weight NaN that a query of theirs sees, in
+    every share of the slots; weights without them are NaN by themselves. The other heads,
+    and the calls after, are as ever."""
+    import torch
+
+    import top_selection_row_gb300 as q
+
+    g = torch.Generator(device=dev).manual_seed(B)
+    k = torch.randn(B, H, S, D, generator=g, device=dev).bfloat16()
+    query = torch.randn(B, T, H * G, D, generator=g, device=dev).bfloat16()
+    w = torch.rand(B, H, S, generator=g, device=dev)
+    n = torch.full((B,), S, dtype=torch.int32, device=dev)
+    n[-1] = S // 2
+    want = q.qrita_cache_weights(query, k, w.clone(), n)
+    flag = q.CACHE_FLAG_TEST_GIVE_UP_WEIGHTS if late else q.CACHE_FLAG_TEST_GIVE_UP_SUMS
+    for _ in range(3):
+        got = q.qrita_cache_weights(query, k, w.clone(), n, flags=flag)
+        assert torch.equal(got[:, 1:], want[:, 1:])
+        first, right = got[:, 0], want[:, 0]
+        lost = first.isnan()
+        for b in range(B):
+            m = int(n[b])
+            # the first share of a head: 128 slots, or as many of eight CTAs (all of one's)
+            part = m if not late or B * H > 152 else max(128, (m + 7) // 8)
+            assert bool(lost[b, :part].all()) and not bool(lost[b, m:].any()), b
+        assert torch.equal(first[~lost], right[~lost])
+        assert torch.equal(q.qrita_cache_weights(query, k, w.clone(), n), want)

@@ -31,6 +31,7 @@ FLAG_NO_KEY_HIST = 0x2000
 FLAG_SEARCH_QUATERNARY = 0x4000
 FLAG_SEARCH_BINARY = 0x8000
 LOSS_FLAG_TEST_GIVE_BACK = 0x1
+CACHE_FLAG_TEST_GIVE_UP_SUMS, CACHE_FLAG_TEST_GIVE_UP_WEIGHTS = 0x1, 0x2
 
 
 def flag_cluster(n_ctas: int) -> int:
@@ -798,7 +799,8 @@ def _order(weights, lengths, positions, seen, B, H, S, device):
             _at(positions, B * H * S, torch.int32, "positions", device), _at(seen, B, torch.int32, "seen", device))
 
 
-def qrita_cache_weights(query, keys, weights, lengths, positions=None, seen=None, scale=None, decay=1.0, stream=None):
+def qrita_cache_weights(query, keys, weights, lengths, positions=None, seen=None, scale=None, decay=1.0, stream=None,
+                        flags=0):
     """Adds what the last T queries of each sequence see to their slots' weights.
 
     query: CUDA [B, T, H G, D]; keys: [B, H, S, D], float32 or bfloat16 both, any
@@ -808,10 +810,10 @@ def qrita_cache_weights(query, keys, weights, lengths, positions=None, seen=None
     lengths: int32 [B], a negative one leaves its sequence alone; positions int32
     [B, H, S] and seen int32 [B], or neither (slot s holds position s); scale:
     1 / sqrt(D) where None. Returns weights. include/qrita.h states which slots a
-    query sees.
+    query sees. flags: qrita_cache_weights_ex's.
     """
     if stream is not None:
-        return _on_stream(stream, qrita_cache_weights, query, keys, weights, lengths, positions, seen, scale, decay)
+        return _on_stream(stream, qrita_cache_weights, query, keys, weights, lengths, positions, seen, scale, decay, None, flags)
     (B, H, S, D), dev = _slots_of(keys)
     if query.dim() != 4:
         raise ValueError("query must be [B, T, H G, D] for keys of [B, H, S, D]")
@@ -824,8 +826,9 @@ def qrita_cache_weights(query, keys, weights, lengths, positions=None, seen=None
     qs, _ = _cache(query, "query", dev, unit=1)
     dt = _dtype_code(keys)
     w, n, at, se = _order(weights, lengths, positions, seen, B, H, S, dev)
-    _call(lib().qrita_cache_weights, dev, B, H, S, query.data_ptr(), dt, T, heads // H, D, qs,
-          keys.data_ptr(), ks, D ** -0.5 if scale is None else scale, decay, n, at, se, w)
+    fn, more = (lib().qrita_cache_weights, ()) if flags == 0 else (lib().qrita_cache_weights_ex, (flags,))
+    _call(fn, dev, B, H, S, query.data_ptr(), dt, T, heads // H, D, qs,
+          keys.data_ptr(), ks, D ** -0.5 if scale is None else scale, decay, n, at, se, w, *more)
     _wrote(weights)
     return weights
 

@@ -28,6 +28,7 @@ EXPORTED = (
     "qrita_token_scores",
     "qrita_token_scores_grad",
     "qrita_cache_weights",
+    "qrita_cache_weights_ex",
     "qrita_cache_evict",
     "qrita_cache_insert",
     "qrita_delta_table",
@@ -82,6 +83,8 @@ def lib() -> ctypes.CDLL:
     L.qrita_token_scores_grad.restype = i32
     L.qrita_cache_weights.argtypes = [i64, i64, i64, vp, i32, i32, i32, i32, vp, vp, vp, f64, f64, vp, vp, vp, vp, vp]
     L.qrita_cache_weights.restype = i32
+    L.qrita_cache_weights_ex.argtypes = [*L.qrita_cache_weights.argtypes[:-1], u32, vp]
+    L.qrita_cache_weights_ex.restype = i32
     L.qrita_cache_evict.argtypes = [i64, i64, i64, vp, vp, vp, vp, i32, i32, i32, vp, i64, vp, vp, i64, vp, vp, vp, vp, vp,
                                     i64, vp, vp, vp, vp, vp]
     L.qrita_cache_evict.restype = i32

@@ -35,6 +35,7 @@ struct WeightParams {
   int64_t k_batch, k_head, k_slot;
   int32_t G, T, D;
   float scale, decay;
+  uint32_t flags;    // QRITA_CACHE_FLAG_*
   int32_t rows;      // query rows a CTA has at once
   int32_t stash;     // floats of a row of kept scores (0: scores are worked out twice)
 };

@@ -102,6 +102,15 @@ int qrita_cache_weights(int64_t B, int64_t H, int64_t S, const void* query, int 
                         const int64_t* query_strides, const void* keys, const int64_t* key_strides, double scale,
                         double decay, const int32_t* lengths, const int32_t* positions, const int32_t* seen,
                         float* weights, qrita_stream_t stream) {
+  return qrita_cache_weights_ex(B, H, S, query, dtype, T, G, D, query_strides, keys, key_strides, scale, decay, lengths,
+                                positions, seen, weights, 0u, stream);
+}
+
+int qrita_cache_weights_ex(int64_t B, int64_t H, int64_t S, const void* query, int dtype, int32_t T, int32_t G, int32_t D,
+                           const int64_t* query_strides, const void* keys, const int64_t* key_strides, double scale,
+                           double decay, const int32_t* lengths, const int32_t* positions, const int32_t* seen,
+                           float* weights, uint32_t flags, qrita_stream_t stream) {
+  if ((flags & ~(QRITA_CACHE_FLAG_TEST_GIVE_UP_SUMS | QRITA_CACHE_FLAG_TEST_GIVE_UP_WEIGHTS)) != 0u) return QRITA_EINVAL;
   qrita::WeightParams prm = {};
   const int rc = qrita::order_args(B, H, S, weights, const_cast<int32_t*>(positions), const_cast<int32_t*>(lengths),
                                    const_cast<int32_t*>(seen), qrita::kMax / 16, &prm.c);
@@ -128,6 +137,7 @@ int qrita_cache_weights(int64_t B, int64_t H, int64_t S, const void* query, int 
   prm.G = G;
   prm.T = T;
   prm.D = D;
+  prm.flags = flags;
   prm.scale = static_cast<float>(scale);
   prm.decay = static_cast<float>(decay);
   return qrita::launch_cache_weights(prm, dtype, stream) == 0 ? QRITA_OK : QRITA_ECUDA;

@@ -1,4 +1,4 @@
-// Attention weights of a window of queries: more than 32 rows (queries times the
+// Attention weights of a window of queries: more than 16 rows (queries times the
 // heads that share a kv head) at once, on the fifth-generation tensor cores.
 //
 // The formulas are those of qrita_cache.cu's weights_kernel. A cluster of CTAs takes
@@ -193,13 +193,22 @@ window_kernel(const WindowParams wp, const __grid_constant__ CUtensorMap query_m
   // every CTA of the cluster runs before its memory is read (in a launch without
   // clusters, threads that arrive at the cluster's barrier ahead of others are held)
   if (C > 1) cluster_sync_all();
-  auto wait = [&](uint64_t& bar, int use) {  // for the use-th completion (0, 1, ...)
-    if (failed != 0 || !mbar_wait_bounded(smem_u32(&bar), static_cast<uint32_t>(use) & 1u, kWindowLimitNs)) {
-      failed = 1;
-      return false;
+  // For the use-th completion (0, 1, ...). When a wait has given up (`quit`: at once) all
+  // others do too, and nothing more is asked for or issued.
+  auto wait = [&](uint64_t& bar, int use, bool quit = false) {
+    const uint32_t at = smem_u32(&bar), phase = static_cast<uint32_t>(use) & 1u;
+    if (!quit && failed == 0) {
+      if (mbar_try_wait(at, phase)) return true;
+      const uint64_t t0 = globaltimer_ns();
+      for (uint32_t i = 1; failed == 0 && ((i & 63u) != 0u || globaltimer_ns() - t0 <= kWindowLimitNs); ++i)
+        if (mbar_try_wait(at, phase)) return true;
     }
-    return true;
+    failed = 1;
+    return false;
   };
+  // (tests: the first CTA of a sequence's first head, in its sums or in its weights)
+  const uint32_t quits = rank == 0 && bh % p.c.H == 0 ? p.flags : 0u;
+  int asked = 0;  // tiles that the copying thread has asked for, or whose products are issued
 
   if (warp == kGroups * 4 + 1) {
     // copies: Q once, then the tiles of keys, all of them twice; the second time last ones
@@ -219,6 +228,7 @@ window_kernel(const WindowParams wp, const __grid_constant__ CUtensorMap query_m
         }
         for (int i = 0; i < HALVES; ++i)
           copy_box(to + i * kHalf, &key_map, i * 64, s0, static_cast<int>(h), static_cast<int>(b), bar);
+        asked = it + 1;
       }
     }
     __syncwarp();
@@ -246,6 +256,7 @@ window_kernel(const WindowParams wp, const __grid_constant__ CUtensorMap query_m
         }
         products_done(smem_u32(&empty[stage]));
         products_done(smem_u32(&made[buf]));
+        asked = it + 1;
       }
     }
     __syncwarp();
@@ -261,9 +272,11 @@ window_kernel(const WindowParams wp, const __grid_constant__ CUtensorMap query_m
     auto position = [&](int64_t s) {  // of a slot; one outside the share is seen by no query
       return s < lo || s >= hi ? INT32_MAX : positions != nullptr ? positions[s] : static_cast<int32_t>(s);
     };
-    // (A wait that has given up ends no loop here: all lanes meet at every barrier, and
-    // the weights are NaN at the end.)
+    // (A wait that has given up ends no loop here: all lanes meet at every barrier. What
+    // it leaves without its scores is NaN: a row's sum, with it every weight of a slot that
+    // the row sees, or this CTA's weights, at the end.)
     // The rows' sums.
+    bool summed = true;
     const int64_t see = first + t / p.G;  // the last position this thread's row sees
     float m = -FLT_MAX, top = -FLT_MAX;   // the largest score, and its exponent
     float2 s2 = both(0.f);
@@ -274,7 +287,7 @@ window_kernel(const WindowParams wp, const __grid_constant__ CUtensorMap query_m
       of[t] = at;
       const bool all = lanes_all(at <= first, group);
       at = position(lo + static_cast<int64_t>(it + kGroups) * kLanes + t);
-      wait(made[it % kBuffers], it / kBuffers);
+      summed = wait(made[it % kBuffers], it / kBuffers, (quits & QRITA_CACHE_FLAG_TEST_GIVE_UP_SUMS) != 0u && it == 0) && summed;
       __syncwarp();
       fence_after();
       const uint32_t from = mine + it % kBuffers * kLanes;
@@ -315,7 +328,7 @@ window_kernel(const WindowParams wp, const __grid_constant__ CUtensorMap query_m
       fence_before();
       arrive(smem_u32(&taken[it % kBuffers]));
     }
-    sums[group][t] = {top, s2.x + s2.y};
+    sums[group][t] = {top, summed ? s2.x + s2.y : NAN};
     auto both_groups = [&]() { asm volatile("bar.sync 15, %0;" ::"n"(kGroups * kLanes) : "memory"); };
     if (C > 1) {
       cluster_arrive();
@@ -357,7 +370,7 @@ window_kernel(const WindowParams wp, const __grid_constant__ CUtensorMap query_m
       const int64_t after = at == INT32_MAX ? INT64_MAX : at - first;
       const int least = after <= 0 ? 0 : after >= R ? R : static_cast<int>(min(after * p.G, static_cast<int64_t>(R)));
       at = position(s - kGroups * kLanes);
-      wait(made[it % kBuffers], it / kBuffers);
+      wait(made[it % kBuffers], it / kBuffers, (quits & QRITA_CACHE_FLAG_TEST_GIVE_UP_WEIGHTS) != 0u && it == tiles);
       __syncwarp();
       fence_after();
       const uint32_t from = mine + it % kBuffers * kLanes;
@@ -393,10 +406,18 @@ window_kernel(const WindowParams wp, const __grid_constant__ CUtensorMap query_m
       arrive(smem_u32(&taken[it % kBuffers]));
       if (s < hi) weights[s] = p.decay != 0.f ? fmaf(p.decay, weights[s], w.x + w.y) : w.x + w.y;
     }
-    if (failed != 0)
-      for (int64_t s = lo + tid; s < hi; s += kGroups * kLanes) weights[s] = NAN;
   }
   __syncthreads();
+  if (failed != 0) {
+    // copies and products in flight end (or a limit does) before their memory is given up
+    if (lane == 0 && warp == kGroups * 4 + 1)
+      for (int it = max(0, asked - kDepth); it < asked; ++it)
+        mbar_wait_bounded(smem_u32(&full[it % kDepth]), static_cast<uint32_t>(it / kDepth) & 1u, kWindowLimitNs);
+    if (lane == 0 && warp == kGroups * 4 && asked > 0)
+      mbar_wait_bounded(smem_u32(&made[(asked - 1) % kBuffers]), static_cast<uint32_t>((asked - 1) / kBuffers) & 1u, kWindowLimitNs);
+    for (int64_t s = lo + tid; s < hi; s += kWindowThreads) p.c.weights[bh * p.c.S + s] = NAN;
+    __syncthreads();
+  }
   if (warp == kGroups * 4) {
     fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(static_cast<uint32_t>(kColumns))
