@@ -591,7 +591,8 @@ int qrita_cache_weights_ex(int64_t B, int64_t H, int64_t S, const void* query, i
  *
  * Slots from out_lengths[b] up to the budget get rows and weights of 0 and -1 for
  * position and slot; slots from the budget on are left as they were. Two kernels on
- * stream.
+ * stream. (Where a bounded wait for a bulk copy gives up, not expected on a healthy
+ * device, its rows are moved by plain loads.)
  */
 int qrita_cache_evict(int64_t B, int64_t H, int64_t S, const int32_t* lengths, const float* weights,
                       const int32_t* positions, const int32_t* seen, int32_t budget, int32_t sink, int32_t recent,
@@ -599,6 +600,16 @@ int qrita_cache_evict(int64_t B, int64_t H, int64_t S, const int32_t* lengths, c
                       int64_t value_bytes, const int64_t* value_strides, void* out_keys, const int64_t* out_key_strides,
                       void* out_values, const int64_t* out_value_strides, int64_t out_S, float* out_weights,
                       int32_t* out_positions, int32_t* out_slots, int32_t* out_lengths, qrita_stream_t stream);
+
+/* qrita_cache_evict with flags (bitwise or; others are QRITA_EINVAL). */
+#define QRITA_CACHE_FLAG_TEST_GIVE_UP_ROWS 0x4u /* tests only: the bounded waits for bulk copies give up at once */
+int qrita_cache_evict_ex(int64_t B, int64_t H, int64_t S, const int32_t* lengths, const float* weights,
+                         const int32_t* positions, const int32_t* seen, int32_t budget, int32_t sink, int32_t recent,
+                         const void* keys, int64_t key_bytes, const int64_t* key_strides, const void* values,
+                         int64_t value_bytes, const int64_t* value_strides, void* out_keys, const int64_t* out_key_strides,
+                         void* out_values, const int64_t* out_value_strides, int64_t out_S, float* out_weights,
+                         int32_t* out_positions, int32_t* out_slots, int32_t* out_lengths, uint32_t flags,
+                         qrita_stream_t stream);
 
 /*
  * qrita_cache_insert: one token a sequence, in place. While a sequence holds fewer

@@ -5,7 +5,8 @@ import ctypes
 
 import pytest
 
-from test_abi_cache import BASE, K, V, strides
+from test_abi_cache import BASE, CACHE, K, OK_, OV, V, strides
+from test_abi_cache_overlap import OUT, READ
 from test_abi_losses import EINVAL, NULL, L  # noqa: F401
 
 
@@ -17,10 +18,22 @@ def weights_ex(L, flags=0, **kw):  # noqa: F811
                                     ctypes.c_uint32(flags), NULL)
 
 
-@pytest.mark.parametrize("call", [weights_ex])
-@pytest.mark.parametrize("flags", [4, 8, 0x1000, 0x80000001])
+def evict_ex(L, flags=0, **kw):  # noqa: F811
+    a = {**BASE, **CACHE, **READ, **OUT, "ok": OK_, "oks": strides(5120, 1280, 128), "ov": OV, "ovs": strides(2560, 640, 64), "oS": 10, **kw}
+    return L.qrita_cache_evict_ex(a["B"], a["H"], a["S"], a["lengths"], a["weights"], a["positions"], a["seen"], a["budget"], a["sink"],
+                                  a["recent"], a["keys"], a["kb"], a["ks"], a["values"], a["vb"], a["vs"], a["ok"], a["oks"], a["ov"],
+                                  a["ovs"], a["oS"], a["ow"], a["op"], a["os"], a["ol"], ctypes.c_uint32(flags), NULL)
+
+
+@pytest.mark.parametrize("call,flags", [(weights_ex, 4), (evict_ex, 1), (evict_ex, 2)] + [(c, f) for c in (weights_ex, evict_ex) for f in (8, 0x1000, 0x80000001)])
 def test_unknown_flags(L, call, flags):  # noqa: F811
     assert call(L, flags) == EINVAL
+
+
+@pytest.mark.parametrize("flags", [0, 4])
+@pytest.mark.parametrize("bad", [dict(budget=0), dict(oS=9), dict(ok=NULL), dict(ok=K), dict(ol=READ["lengths"]), dict(S=0)], ids=str)
+def test_bad_evictions(L, bad, flags):  # noqa: F811
+    assert evict_ex(L, flags, **bad) == EINVAL
 
 
 @pytest.mark.parametrize("flags", [0, 1, 2, 3])

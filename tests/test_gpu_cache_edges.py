@@ -91,3 +91,24 @@ def test_a_window_whose_wait_gives_up(dev, B, H, G, T, S, D, late):  # noqa: F81
             assert bool(lost[b, :part].all()) and not bool(lost[b, m:].any()), b
         assert torch.equal(first[~lost], right[~lost])
         assert torch.equal(q.qrita_cache_weights(query, k, w.clone(), n), want)
+
+
+@pytest.mark.parametrize("D", [(32, 64), (8, 512)])
+@pytest.mark.parametrize("apart", [False, True])
+def test_an_eviction_whose_waits_give_up(dev, D, apart):  # noqa: F811
+    """Rows whose bulk copies are not waited for are moved all the same, together and (in
+    a wider tensor) one by one."""
+    import torch
+
+    import top_selection_row_gb300 as q
+
+    _, _, w, n, at = small_cache(dev, S=500)
+    k, v = (torch.randn(3, 2, 500, d, device=dev).bfloat16() for d in D)
+    want = q.qrita_cache_evict(k, v, w, n, 200, sink=2, recent=9, positions=at, seen=n)
+    z = [torch.full_like(t, 9) for t in want]
+    if apart:
+        z[0] = torch.full((3, 2, 200, D[0] + 8), 9, dtype=k.dtype, device=dev)[..., : D[0]]
+        z[1] = torch.full((3, 200, 2, D[1]), 9, dtype=k.dtype, device=dev).transpose(1, 2)
+    for _ in range(3):
+        got = q.qrita_cache_evict(k, v, w, n, 200, sink=2, recent=9, positions=at, seen=n, out=q.EvictedCache(*z), flags=q.CACHE_FLAG_TEST_GIVE_UP_ROWS)
+        assert all(torch.equal(a, b) for a, b in zip(got, want))

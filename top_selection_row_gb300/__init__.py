@@ -31,7 +31,7 @@ FLAG_NO_KEY_HIST = 0x2000
 FLAG_SEARCH_QUATERNARY = 0x4000
 FLAG_SEARCH_BINARY = 0x8000
 LOSS_FLAG_TEST_GIVE_BACK = 0x1
-CACHE_FLAG_TEST_GIVE_UP_SUMS, CACHE_FLAG_TEST_GIVE_UP_WEIGHTS = 0x1, 0x2
+CACHE_FLAG_TEST_GIVE_UP_SUMS, CACHE_FLAG_TEST_GIVE_UP_WEIGHTS, CACHE_FLAG_TEST_GIVE_UP_ROWS = 0x1, 0x2, 0x4
 
 
 def flag_cluster(n_ctas: int) -> int:
@@ -834,7 +834,7 @@ def qrita_cache_weights(query, keys, weights, lengths, positions=None, seen=None
 
 
 def qrita_cache_evict(keys, values, weights, lengths, budget, sink=0, recent=0, positions=None, seen=None, stream=None,
-                      out=None):
+                      out=None, flags=0):
     """The budget slots of each sequence and head that are first in order, packed
     into another cache in slot order.
 
@@ -845,11 +845,11 @@ def qrita_cache_evict(keys, values, weights, lengths, budget, sink=0, recent=0, 
     [B, H, budget], positions int32 [B, H, budget], slots int32 [B, H, budget],
     lengths int32 [B]); behind a sequence's length rows and weights are 0, positions
     and slots -1. ``out`` = such a tuple writes into its tensors, whose caches may
-    have more slots (left as they were).
+    have more slots (left as they were). flags: qrita_cache_evict_ex's.
     """
     if stream is not None:
         return _on_stream(stream, qrita_cache_evict, keys, values, weights, lengths, budget, sink, recent, positions, seen,
-                          None, out)
+                          None, out, flags)
     torch = _torch()
     (B, H, S, Dk), dev = _slots_of(keys)
     Dv = values.shape[-1]
@@ -883,9 +883,10 @@ def qrita_cache_evict(keys, values, weights, lengths, budget, sink=0, recent=0, 
         _written(got.values, "out values")
         oks, _ = _cache(got.keys, "out keys", dev, (B, H, more, Dk))
         ovs, _ = _cache(got.values, "out values", dev, (B, H, more, Dv))
-    _call(lib().qrita_cache_evict, dev, B, H, S, n, w, at, se, budget, sink, recent, keys.data_ptr(), kb, ks,
+    fn, more_args = (lib().qrita_cache_evict, ()) if flags == 0 else (lib().qrita_cache_evict_ex, (flags,))
+    _call(fn, dev, B, H, S, n, w, at, se, budget, sink, recent, keys.data_ptr(), kb, ks,
           values.data_ptr(), vb, vs, got.keys.data_ptr(), oks, got.values.data_ptr(), ovs, more, got.weights.data_ptr(),
-          got.positions.data_ptr(), got.slots.data_ptr(), got.lengths.data_ptr())
+          got.positions.data_ptr(), got.slots.data_ptr(), got.lengths.data_ptr(), *more_args)
     if out is not None:
         _wrote(*got)
     return got

@@ -30,6 +30,7 @@ EXPORTED = (
     "qrita_cache_weights",
     "qrita_cache_weights_ex",
     "qrita_cache_evict",
+    "qrita_cache_evict_ex",
     "qrita_cache_insert",
     "qrita_delta_table",
     "qrita_strerror",
@@ -88,6 +89,8 @@ def lib() -> ctypes.CDLL:
     L.qrita_cache_evict.argtypes = [i64, i64, i64, vp, vp, vp, vp, i32, i32, i32, vp, i64, vp, vp, i64, vp, vp, vp, vp, vp,
                                     i64, vp, vp, vp, vp, vp]
     L.qrita_cache_evict.restype = i32
+    L.qrita_cache_evict_ex.argtypes = [*L.qrita_cache_evict.argtypes[:-1], u32, vp]
+    L.qrita_cache_evict_ex.restype = i32
     L.qrita_cache_insert.argtypes = [i64, i64, i64, vp, vp, vp, vp, i32, i32, i32, vp, i64, vp, vp, i64, vp, vp, vp, vp,
                                      vp, vp, vp]
     L.qrita_cache_insert.restype = i32

@@ -803,8 +803,8 @@ __global__ void __launch_bounds__(kBulkThreads) evict_bulk_kernel(const EvictPar
       bulk_g2s(smem_u32(rows) + tid * bytes, static_cast<const unsigned char*>(from.at) + b * from.batch + h * from.head + s * from.slot,
                bytes, smem_u32(&bar));
     if (blockIdx.y == 0) gather_order<kBulkThreads>(p, bh, first, count);
-    // (a copy that never lands, not expected on a healthy device, leaves its rows unwritten)
-    if (__syncthreads_and(mbar_wait_bounded(smem_u32(&bar), 0, kBulkLimitNs))) {
+    const bool landed = __syncthreads_and(!p.give_up && mbar_wait_bounded(smem_u32(&bar), 0, kBulkLimitNs));
+    if (landed) {
       const bool together = to.slot == from.bytes;
       if (together ? tid == 0 : s >= 0) {
         asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst + (together ? 0 : tid * to.slot)),
@@ -812,6 +812,16 @@ __global__ void __launch_bounds__(kBulkThreads) evict_bulk_kernel(const EvictPar
                      : "memory");
         asm volatile("cp.async.bulk.commit_group;" ::: "memory");
       }
+    } else {
+      // copies that do not land (not expected on a healthy device): the rows by plain loads;
+      // the copies end, or a limit does, before their memory is given up
+      for (int r = 0; r < some; ++r) {
+        const int32_t at = p.out_slots[bh * p.c.budget + first + r];
+        const unsigned char* src = static_cast<const unsigned char*>(from.at) + b * from.batch + h * from.head + at * from.slot;
+        for (uint32_t i = tid * 16u; i < bytes; i += kBulkThreads * 16u)
+          *reinterpret_cast<uint4*>(dst + r * to.slot + i) = load_unit(src + i);
+      }
+      mbar_wait_bounded(smem_u32(&bar), 0, kBulkLimitNs);
     }
   }
   if (some == 0 && blockIdx.y == 0) gather_order<kBulkThreads>(p, bh, first, count);

@@ -49,6 +49,7 @@ struct EvictParams {
   int32_t* out_slots;    // [B, H, budget]
   int32_t* out_lengths;
   int32_t share;         // weights a CTA of the selection keeps in shared memory (0: none)
+  bool give_up;          // tests: the bounded waits for bulk copies do so at once
 };
 
 struct InsertParams {

@@ -149,7 +149,21 @@ int qrita_cache_evict(int64_t B, int64_t H, int64_t S, const int32_t* lengths, c
                       int64_t value_bytes, const int64_t* value_strides, void* out_keys, const int64_t* out_key_strides,
                       void* out_values, const int64_t* out_value_strides, int64_t out_S, float* out_weights,
                       int32_t* out_positions, int32_t* out_slots, int32_t* out_lengths, qrita_stream_t stream) {
+  return qrita_cache_evict_ex(B, H, S, lengths, weights, positions, seen, budget, sink, recent, keys, key_bytes, key_strides,
+                              values, value_bytes, value_strides, out_keys, out_key_strides, out_values, out_value_strides,
+                              out_S, out_weights, out_positions, out_slots, out_lengths, 0u, stream);
+}
+
+int qrita_cache_evict_ex(int64_t B, int64_t H, int64_t S, const int32_t* lengths, const float* weights,
+                         const int32_t* positions, const int32_t* seen, int32_t budget, int32_t sink, int32_t recent,
+                         const void* keys, int64_t key_bytes, const int64_t* key_strides, const void* values,
+                         int64_t value_bytes, const int64_t* value_strides, void* out_keys, const int64_t* out_key_strides,
+                         void* out_values, const int64_t* out_value_strides, int64_t out_S, float* out_weights,
+                         int32_t* out_positions, int32_t* out_slots, int32_t* out_lengths, uint32_t flags,
+                         qrita_stream_t stream) {
+  if ((flags & ~QRITA_CACHE_FLAG_TEST_GIVE_UP_ROWS) != 0u) return QRITA_EINVAL;
   qrita::EvictParams prm = {};
+  prm.give_up = (flags & QRITA_CACHE_FLAG_TEST_GIVE_UP_ROWS) != 0u;
   const int rc = qrita::order_args(B, H, S, const_cast<float*>(weights), const_cast<int32_t*>(positions),
                                    const_cast<int32_t*>(lengths), const_cast<int32_t*>(seen), qrita::kMax / 16, &prm.c);
   if (rc != QRITA_OK) return rc;
