@@ -50,8 +50,9 @@ def test_gradients_of_tokens_of_the_lowest_value(dev, B, V, keep, dtype, inv_t, 
 def test_gradient_of_one_token_listed_often(dev, B, V, keep, dtype):  # noqa: F811
     """A token of nearly all the probability, listed 250 times with gradients that
     nearly cancel, beside six others. Its entry is G (1 - p) - p R, G its own
-    gradients' sum and R the others'. Sums are fp64 (256 2^-53 of their magnitudes) and
-    rounded once; log p is off by 2^-22 + 2^-24 (10 + E), E < 1 here, and so are 1 - p and
+    gradients' sum and R the others'. Sums are fp64 (256 2^-53 of their magnitudes), an
+    id's own pairs of fp32 (256 roundings of a low part of 2^-20 of the magnitudes: below
+    2^-37 of them, 2e-7 here), and rounded once; log p is off by 2^-22 + 2^-24 (10 + E), E < 1 here, and so are 1 - p and
     p; each of the two products' four operations rounds by 2^-24, expm1 and exp by two
     such steps."""
     import top_selection_row_gb300 as q

@@ -261,13 +261,15 @@ __device__ __forceinline__ float grad_one(float x, const RowGrad& g, float c) {
 // taken as G_j (1 - p_j) - p_j (a - G_j + ...), 1 - p_j by expm1. A thread keeps the
 // logits of its ids (read before a gradient is written over them), on their way while
 // the row is summed; ids and gradients are read again where they are used, and wait
-// for the last step in the sums' shared memory. Sums of g_i, of a row and of an id,
-// are fp64, each in one order: a - G_j is what is left of their difference.
-// (512 x 151936 bf16: one id a row 57 us, 20 60, 64 62, 256 88; 255 x 50021 fp32 with
-// entropies: 64 ids 23 us, 256 34.)
+// for the last step in the sums' shared memory. Sums of g_i are fp64 over a row and
+// pairs of fp32 over an id that is listed more than once, each in one order: a - G_j is
+// what is left of their difference. (An id's places are counted first, two instructions
+// an id: with its sum taken on the way 256 ids of 512 x 151936 87 us in fp32, and 64 ids
+// of 255 x 50021 34 in fp64.)
+// (512 x 151936 bf16: one id a row 56 us, 20 59, 64 61, 256 85, half of them one id 94;
+// 255 x 50021 fp32 with entropies: 64 ids 23 us, 256 33.)
 struct ManyRow {
-  double a;
-  F2 ln_s;
+  F2 a, ln_s;
   float m, H, h;
 };
 
@@ -350,12 +352,13 @@ struct Many {
     double a = 0.0;
     for (uint32_t i = 0; i < p.C; ++i) a += ranks[i];
     if (st.s.hi != st.s.hi) a = st.s.hi;  // (NaN for the whole row)
-    r.a = a;
+    r.a.hi = static_cast<float>(a);
+    r.a.lo = static_cast<float>(a - r.a.hi);
     r.h = ENT && st.s.hi != 0.f ? p.g_entropy[row] : 0.f;
     r.H = v.H;
     r.m = st.m;
     r.ln_s = st.s.hi != 0.f ? ln_pair(sum_of(st)) : f2_make(0.f, 0.f);
-    return row_grad(static_cast<float>(a), r.h, -INFINITY, v.H, v.ln_s, st.m, st.s.hi, p.inv_t);
+    return row_grad(r.a.hi, r.h, -INFINITY, v.H, v.ln_s, st.m, st.s.hi, p.inv_t);
   }
 
   // The entries of this CTA's ids, over what a barrier before this has seen written.
@@ -369,22 +372,25 @@ struct Many {
       const int k = threadIdx.x + i * THREADS;
       if (x[i] == -INFINITY) continue;
       const int id = ids[k];
-      double sum = 0.0;
-      int first = k;
+      int places = 0;
       for (int j = 0; j < p.K; j += 4) {  // (behind the last id are ids of -1)
         const int4 v = *reinterpret_cast<const int4*>(ids + j);
-        const int same[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-        for (int n = 0; n < 4; ++n)
-          if (same[n] == id) {
-            first = min(first, j + n);
-            sum += g[j + n];
-          }
+        places += v.x == id;
+        places += v.y == id;
+        places += v.z == id;
+        places += v.w == id;
       }
-      if (first != k) continue;
+      F2 sum = f2_make(g[k], 0.f);
+      if (places > 1) {  // the first of them writes
+        bool first = true;
+        for (int j = 0; j < k && first; ++j) first = ids[j] != id;
+        if (!first) continue;
+        for (int j = k + 1; j < p.K; ++j)
+          if (ids[j] == id) f2_add(sum, g[j]);
+      }
       const float lp = f2_float(logp_of(x[i], r.m, r.ln_s, p.inv_t, p.inv_t_lo)), prob = expf(lp);
-      const float G = static_cast<float>(sum);
-      float rest = static_cast<float>(r.a - sum);
+      const float G = f2_float(sum);
+      float rest = isfinite(r.a.hi) ? f2_float(f2_sub(r.a, sum)) : r.a.hi - G;
       // (a probability of 0 takes nothing of it, not 0 * inf where log p, or h times it, has left fp32)
       if (r.h != 0.f && prob != 0.f) rest = fmaf(r.h, lp + r.H, rest);
       Elem<DT>::store(grow, id, p.inv_t * (G * -expm1f(lp) - prob * rest));
