@@ -112,3 +112,26 @@ def test_an_eviction_whose_waits_give_up(dev, D, apart):  # noqa: F811
     for _ in range(3):
         got = q.qrita_cache_evict(k, v, w, n, 200, sink=2, recent=9, positions=at, seen=n, out=q.EvictedCache(*z), flags=q.CACHE_FLAG_TEST_GIVE_UP_ROWS)
         assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+def test_the_largest_budget(dev):  # noqa: F811
+    """2^31 - 1 slots for a hundred tokens (28 GB): kept whole, and filled to the end."""
+    import torch
+
+    import top_selection_row_gb300 as q
+
+    budget = 2**31 - 1
+    k, v = (torch.randint(-100, 100, (1, 1, 100, 1), device=dev).to(torch.int8) for _ in range(2))
+    w = torch.rand(1, 1, 100, device=dev)
+    n = torch.tensor([90], dtype=torch.int32, device=dev)
+    got = q.qrita_cache_evict(k, v, w, n, budget)
+    assert torch.equal(got.keys[:, :, :90], k[:, :, :90]) and torch.equal(got.values[:, :, :90], v[:, :, :90])
+    assert torch.equal(got.weights[:, :, :90], w[:, :, :90]) and got.lengths.tolist() == [90]
+    assert torch.equal(got.slots[0, 0, :90], torch.arange(90, dtype=torch.int32, device=dev))
+    for t, fill in ((got.keys, 0), (got.values, 0), (got.weights, 0), (got.positions, -1), (got.slots, -1)):
+        rest = t.flatten()[90:]
+        assert rest.numel() == budget - 90
+        for part in rest.split(2**28):  # (views: no copy of it all)
+            assert bool((part == fill).all())
+    del got
+    torch.cuda.empty_cache()

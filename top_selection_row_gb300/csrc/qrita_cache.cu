@@ -787,7 +787,7 @@ __global__ void __launch_bounds__(kBulkThreads) evict_bulk_kernel(const EvictPar
   __syncthreads();
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  const int64_t parts = (p.c.budget + per - 1) / per;
+  const int64_t parts = (static_cast<int64_t>(p.c.budget) + per - 1) / per;
   const int64_t bh = blockIdx.x / parts, first = blockIdx.x % parts * per, b = bh / p.c.H, h = bh % p.c.H;
   const int count = static_cast<int>(min(static_cast<int64_t>(per), p.c.budget - first));
   const CacheRows& from = blockIdx.y == 0 ? p.key : p.value;
@@ -834,7 +834,7 @@ __global__ void __launch_bounds__(kBulkThreads) evict_bulk_kernel(const EvictPar
 __global__ void __launch_bounds__(kGatherThreads) evict_gather_kernel(const EvictParams p) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  const int64_t parts = (p.c.budget + kGatherRows - 1) / kGatherRows;
+  const int64_t parts = (static_cast<int64_t>(p.c.budget) + kGatherRows - 1) / kGatherRows;
   const int64_t bh = blockIdx.x / parts, first = blockIdx.x % parts * kGatherRows;
   const int64_t count = min(static_cast<int64_t>(kGatherRows), p.c.budget - first);
   const CacheRows& from = blockIdx.y == 0 ? p.key : p.value;
@@ -989,7 +989,7 @@ int launch_cache_evict(const EvictParams& p, qrita_stream_t stream) {
   const bool bulk = aligned(p.key) && aligned(p.value) && aligned(p.out_key) && aligned(p.out_value);
   const int64_t widest = p.key.bytes > p.value.bytes ? p.key.bytes : p.value.bytes;
   const int per = !bulk ? kGatherRows : widest * kBulkThreads <= kBulkBytes ? kBulkThreads : static_cast<int>(kBulkBytes / widest);
-  const int64_t parts = (p.c.budget + per - 1) / per;
+  const int64_t parts = (static_cast<int64_t>(p.c.budget) + per - 1) / per;
   if (pairs * parts > INT32_MAX) return static_cast<int>(cudaErrorInvalidConfiguration);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(pairs * parts), 2, 1);

@@ -182,7 +182,7 @@ int qrita_cache_evict_ex(int64_t B, int64_t H, int64_t S, const int32_t* lengths
       qrita::clash({{out_weights, out_order}, {out_positions, out_order}, {out_slots, 4 * B * H * budget}, {out_lengths, 4 * B}},
                    {{weights, order}, {positions, order}, {lengths, 4 * B}, {seen, 4 * B}}))
     return QRITA_EINVAL;
-  if (B * H > qrita::kMax / ((budget + 63) / 64)) return QRITA_EUNSUPPORTED;
+  if (B * H > qrita::kMax / ((static_cast<int64_t>(budget) + 63) / 64)) return QRITA_EUNSUPPORTED;
   prm.out_slots_of = out_S;
   prm.out_weights = out_weights;
   prm.out_positions = out_positions;
