@@ -135,3 +135,26 @@ def test_the_largest_budget(dev):  # noqa: F811
             assert bool((part == fill).all())
     del got
     torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("bad", [dict(budget=2**32 + 5), dict(budget=2**31), dict(sink=2**32), dict(sink=2**31), dict(recent=2**32 + 1),
+                                 dict(recent=2**40), dict(recent=-(2**32)), dict(sink=1.5)])
+def test_numbers_beyond_32_bits(dev, bad):  # noqa: F811
+    """Refused, not cut to their low 32 bits."""
+    import torch
+
+    import top_selection_row_gb300 as q
+
+    k, v, w, n, at = small_cache(dev)
+    seen, new = n + 5, torch.zeros(3, 2, 32, dtype=torch.bfloat16, device=dev)
+    held = [t.clone() for t in (k, v, w, n, at, seen)]
+    how = dict(budget=20, sink=1, recent=2) | bad
+    out = q.qrita_cache_evict(k, v, w, n, 20, positions=at, seen=seen)
+    for call in (lambda: q.qrita_cache_insert(k, v, w, at, n, seen, new, new, **how),
+                 lambda: q.qrita_cache_evict(k, v, w, n, positions=at, seen=seen, out=out, **how)):
+        with pytest.raises((ValueError, TypeError)):
+            call()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip((k, v, w, n, at, seen), held))
+    one = np.int64(3)  # numpy's whole numbers are taken
+    q.qrita_cache_evict(k, v, w, n, np.int32(20), sink=one, recent=one)

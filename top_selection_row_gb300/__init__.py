@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes
 from collections import namedtuple
+from operator import index
 
 import numpy as np
 
@@ -787,6 +788,14 @@ def _written(t, name):
         raise ValueError(f"{name} is written: its rows must not share memory")
 
 
+def _kept(budget, sink, recent):
+    """The three as the library takes them. (A larger one would be cut to its low 32 bits.)"""
+    got = int(budget), index(sink), index(recent)
+    if max(got) >= 2**31 or min(got) < -(2**31):
+        raise ValueError("budget, sink and recent must fit in 32 bits")
+    return got
+
+
 def _order(weights, lengths, positions, seen, B, H, S, device):
     torch = _torch()
     if weights is None or weights.shape != (B, H, S):
@@ -856,7 +865,7 @@ def qrita_cache_evict(keys, values, weights, lengths, budget, sink=0, recent=0, 
     ks, kb = _cache(keys, "keys", dev)
     vs, vb = _cache(values, "values", dev, (B, H, S, Dv))
     w, n, at, se = _order(weights, lengths, positions, seen, B, H, S, dev)
-    budget = int(budget)
+    budget, sink, recent = _kept(budget, sink, recent)
     if budget < 1 or H < 1 or S < 1:
         raise ValueError("a cache has heads and slots, and a budget of at least one")
     if out is None:
@@ -914,6 +923,7 @@ def qrita_cache_insert(keys, values, weights, positions, lengths, seen, new_keys
     _written(values, "values")
     if positions is None or seen is None:
         raise ValueError("positions and seen are required")
+    budget, sink, recent = _kept(budget, sink, recent)
     w, n, at, se = _order(weights, lengths, positions, seen, B, H, S, dev)
     if new_keys.dtype != keys.dtype or new_values.dtype != values.dtype:
         raise TypeError("new_keys and new_values must have the types of keys and values")
@@ -924,7 +934,7 @@ def qrita_cache_insert(keys, values, weights, positions, lengths, seen, new_keys
     else:
         slots = out
         _needed(slots, B * H, torch.int32, "out", dev)
-    _call(lib().qrita_cache_insert, dev, B, H, S, n, se, w, at, int(budget), sink, recent, keys.data_ptr(), kb, ks,
+    _call(lib().qrita_cache_insert, dev, B, H, S, n, se, w, at, budget, sink, recent, keys.data_ptr(), kb, ks,
           values.data_ptr(), vb, vs, new_keys.data_ptr(), nks, new_values.data_ptr(), nvs, slots.data_ptr())
     _wrote(keys, values, weights, positions, lengths, seen, out)
     return slots
