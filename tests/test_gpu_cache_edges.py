@@ -4,7 +4,9 @@ same call made plainly; tolerances as tests/test_gpu_cache.py unless said."""
 import numpy as np
 import pytest
 
-from test_gpu_losses import dev  # noqa: F401
+from oracle import cache_weights
+from test_gpu_cache import check_weights, rounded, tensor
+from test_gpu_losses import dev, put  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -158,3 +160,72 @@ def test_numbers_beyond_32_bits(dev, bad):  # noqa: F811
     assert all(torch.equal(a, b) for a, b in zip((k, v, w, n, at, seen), held))
     one = np.int64(3)  # numpy's whole numbers are taken
     q.qrita_cache_evict(k, v, w, n, np.int32(20), sink=one, recent=one)
+
+
+@pytest.mark.parametrize("G,T", [(1, 1), (4, 1), (4, 4), (3, 7), (8, 20), (1, 130)])
+@pytest.mark.parametrize("evicted", [False, True])
+def test_weights_of_heads_of_192_dimensions(dev, G, T, evicted):  # noqa: F811
+    check_weights(dev, G * T, 4, 2, G, T, 500, 192, "bf16", evicted)
+    check_weights(dev, G * T + 1, 1, 3, G, T, 1300, 192, "bf16", evicted, layout=2)
+
+
+@pytest.mark.parametrize("D", [32, 64, 96, 128, 192, 256, 72])
+@pytest.mark.parametrize("G,T,S", [(1, 17, 100), (4, 8, 900), (8, 9, 3000), (130, 1, 400), (150, 3, 260)])
+def test_weights_of_many_rows_that_no_window_takes(dev, D, G, T, S):  # noqa: F811
+    """Expanded heads (one cache read by all) have no tensor map, and more than 128
+    heads of a group do not fit its lanes: 32 rows at a time. Tolerances as
+    tests/test_gpu_cache.py's weights."""
+    import torch
+
+    import top_selection_row_gb300 as q
+
+    rng = np.random.default_rng(D + S)
+    B, H, expanded = 2, 2, G < 128
+    k = rng.standard_normal((B, 1 if expanded else H, S, D)).astype(np.float32)
+    qq = (1.5 * rng.standard_normal((B, T, H * G, D))).astype(np.float32)
+    w = rng.random((B, H, S)).astype(np.float32)
+    n = np.array([S, S - 31], np.int32)
+    kd = tensor(dev, k, "bf16").expand(B, H, S, D)
+    got = q.qrita_cache_weights(tensor(dev, qq, "bf16"), kd, put(dev, w), put(dev, n), decay=0.75).cpu().numpy().astype(np.float64)
+    k64, q64 = np.broadcast_to(rounded(k, "bf16"), (B, H, S, D)), rounded(qq, "bf16")
+    for b in range(B):
+        for h in range(H):
+            m, mine = int(n[b]), q64[b, :, h * G : (h + 1) * G]
+            add = cache_weights(mine, k64[b, h], np.arange(S), m, m, D**-0.5)
+            want = w[b, h].astype(np.float64)
+            want[:m] = want[:m] * 0.75 + add
+            A = (np.abs(k64[b, h, :m]) @ np.abs(mine).reshape(T * G, D).T).max() * D**-0.5
+            tol = 2 * (2 * (D * 2.0**-22 + 2.0**-23) * A + 2.0**-21 + S * 2.0**-24) * np.r_[add, np.zeros(S - m)] + 2.0**-22 * want
+            tol[m:] = 0
+            assert (np.abs(got[b, h] - want) <= tol).all(), (b, h)
+
+
+@pytest.mark.parametrize("B,H,G,T,S,D,dtype,size", [(2, 2, 4, 1, 20000, 128, "bf16", 1.0), (2, 2, 4, 32, 20000, 128, "bf16", 1.0),
+                                                     (1, 2, 8, 2, 9000, 64, "bf16", 1.0), (10, 8, 1, 17, 65536, 64, "bf16", 0.01),
+                                                     (160, 2, 4, 1, 16384, 64, "bf16", 0.01), (2, 2, 4, 4, 9000, 128, "f32", 1.0)])
+def test_accuracy_of_weights(dev, B, H, G, T, S, D, dtype, size):  # noqa: F811
+    """The root mean square error of what is added, relative to its own. Scores of normal
+    queries and keys are near 1, and near 2 where the square of their weight is. One is a sum
+    of n steps (16 products a step on the tensor cores, D multiply-adds in fp32), each of
+    which loses 0.58 of 2^-23 (cut off there) or 2^-24 of what is summed, sqrt(n / 3) of
+    them in all; scaled and taken from the maximum it is rounded twice more by 0.58 2^-24
+    of 2; the exponential is off by 6e-8, a row's sum by 1.2e-7 (512 additions by each of 8
+    chains, one row in the window's worst case): 3e-7 on the tensor cores, 5e-7 in fp32.
+    (Scores near 0 leave less.)"""
+    import torch
+
+    import top_selection_row_gb300 as q
+
+    g = torch.Generator(device=dev).manual_seed(S)
+    k = torch.randn(B, H, S, D, generator=g, device=dev)
+    qq = size * torch.randn(B, T, H * G, D, generator=g, device=dev)
+    if dtype == "bf16":
+        k, qq = k.bfloat16(), qq.bfloat16()
+    n = torch.full((B,), S, dtype=torch.int32, device=dev)
+    got = q.qrita_cache_weights(qq, k, torch.zeros(B, H, S, device=dev), n)
+    for b, h in ((0, 0), (B - 1, H - 1)):
+        x = (qq[b, :, h * G : (h + 1) * G].reshape(T * G, D).double() @ k[b, h].double().T) / D**0.5
+        after = torch.arange(S, device=dev) > S - T + torch.arange(T, device=dev).repeat_interleave(G)[:, None]
+        want = x.masked_fill(after, -torch.inf).softmax(dim=1).sum(dim=0)
+        err = float((got[b, h].double() - want).norm() / want.norm())
+        assert err < (5e-7 if dtype == "f32" else 3e-7), (b, h, err)
