@@ -229,3 +229,51 @@ def test_accuracy_of_weights(dev, B, H, G, T, S, D, dtype, size):  # noqa: F811
         want = x.masked_fill(after, -torch.inf).softmax(dim=1).sum(dim=0)
         err = float((got[b, h].double() - want).norm() / want.norm())
         assert err < (5e-7 if dtype == "f32" else 3e-7), (b, h, err)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("G,T", [(1, 1), (4, 2), (4, 30), (1, 40), (150, 1)])
+def test_weights_of_scores_far_from_zero(dev, G, T, dtype):  # noqa: F811
+    """Whole scores times 2^40: each row's largest ones share its weight (sums of at most
+    S equal terms: exact; a quotient and R sums of 2^-23 each), the others have none."""
+    import torch
+
+    import top_selection_row_gb300 as q
+
+    rng = np.random.default_rng(G * T)
+    H, S, D = 2, 700, 64
+    k = rng.integers(-1, 2, (1, H, S, D)).astype(np.float32)
+    qq = rng.integers(-1, 2, (1, T, H * G, D)).astype(np.float32)
+    n = torch.tensor([S], dtype=torch.int32, device=dev)
+    got = q.qrita_cache_weights(tensor(dev, qq, dtype), tensor(dev, k, dtype), torch.zeros(1, H, S, device=dev), n, scale=2.0**40)
+    for h in range(H):
+        want = cache_weights(qq[0, :, h * G : (h + 1) * G], k[0, h], np.arange(S), S, S, 2.0**40)
+        assert (np.abs(got[0, h].cpu().numpy() - want) <= G * T * 2.0**-23 * want).all()
+
+
+@pytest.mark.parametrize("G,T", [(1, 1), (4, 3), (4, 40), (1, 60), (150, 1)])
+def test_weights_of_rows_that_see_the_lowest_value_alone(dev, G, T):  # noqa: F811
+    """Keys of the type's lowest value, as masked slots have: the queries that see
+    nothing else see them alike, the others not at all. The rest as tests/test_gpu_cache.py."""
+    import torch
+
+    import top_selection_row_gb300 as q
+
+    rng = np.random.default_rng(T)
+    H, S, D = 2, 64, 64
+    k = rng.standard_normal((1, H, S, D)).astype(np.float32)
+    few = S if T == 1 else 15
+    k[:, :, :few] = 0
+    k[:, :, :few, 0] = -3.3895313892515355e38
+    qq = rng.standard_normal((1, T, H * G, D)).astype(np.float32)
+    qq[..., 0] = 1
+    n = torch.tensor([S], dtype=torch.int32, device=dev)
+    got = q.qrita_cache_weights(tensor(dev, qq, "bf16"), tensor(dev, k, "bf16"), torch.zeros(1, H, S, device=dev), n).cpu().numpy()
+    k64, q64 = rounded(k, "bf16"), rounded(qq, "bf16")
+    for h in range(H):
+        mine = q64[0, :, h * G : (h + 1) * G]
+        with np.errstate(over="ignore"):
+            want = cache_weights(mine, k64[0, h], np.arange(S), S, S, D**-0.5)
+        A = (np.abs(k64[0, h, few:]) @ np.abs(mine).reshape(T * G, D).T).max(initial=0) * D**-0.5
+        tol = 2 * (2 * (D * 2.0**-22 + 2.0**-23) * A + 2.0**-21 + S * 2.0**-24) * want + 2.0**-22 * want
+        assert (np.abs(got[0, h] - want) <= tol).all(), h

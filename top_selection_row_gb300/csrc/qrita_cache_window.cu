@@ -7,7 +7,7 @@
 //   first   Q K^T, a query row a lane of tensor memory: its thread keeps the row's
 //           running maximum and sum over the slots;
 //   second  K Q^T, a slot a lane: its thread adds up the slot's weights over the rows,
-//           w = sum_r 2^(c x_r - c m_r) / S_r, c = scale log2 e.
+//           w = sum_r 2^(c (x_r - m_r)) / S_r, c = scale log2 e.
 // Between them the rows' sums merge through distributed shared memory. Both products
 // read the same tiles of shared memory (dimensions contiguous, swizzled over 128
 // bytes). Keys are read again for the second product, last tiles first: what L2 still
@@ -126,9 +126,11 @@ __device__ __forceinline__ bool lanes_all(bool yes, int group) {
   return r != 0u;
 }
 
-// A row's largest exponent c x and its sum of 2^(c x - top).
+// A row's largest score and its sum of 2^(c (x - m)). (The difference comes first: c x
+// by itself is rounded by 2^-24 of it, which for scores beyond 2^30 is more than an
+// exponent.)
 struct WindowSum {
-  float top, s;
+  float m, s;
 };
 
 struct WindowParams {
@@ -145,7 +147,7 @@ window_kernel(const WindowParams wp, const __grid_constant__ CUtensorMap query_m
   extern __shared__ unsigned char raw[];
   __shared__ __align__(8) uint64_t full[kDepth], empty[kDepth], made[kBuffers], taken[kBuffers];
   __shared__ WindowSum sums[kGroups][kLanes];
-  __shared__ float4 row_pairs[kLanes / 2];  // -top of two rows, 1 / S of the two
+  __shared__ float4 row_pairs[kLanes / 2];  // -m of two rows, 1 / S of the two
   __shared__ int tile_positions[kGroups][2][kLanes];
   __shared__ uint32_t tmem_at;
   __shared__ volatile int failed;  // a bounded wait gave up
@@ -278,7 +280,7 @@ window_kernel(const WindowParams wp, const __grid_constant__ CUtensorMap query_m
     // The rows' sums.
     bool summed = true;
     const int64_t see = first + t / p.G;  // the last position this thread's row sees
-    float m = -FLT_MAX, top = -FLT_MAX;   // the largest score, and its exponent
+    float m = -FLT_MAX;                   // the largest score
     float2 s2 = both(0.f);
     int32_t at = position(lo + group * kLanes + t);
     int it = group;
@@ -310,17 +312,16 @@ window_kernel(const WindowParams wp, const __grid_constant__ CUtensorMap query_m
         for (int i = 1; i < 31; i += 2) most = fmax3(most, x[i], x[i + 1]);
         most = fmaxf(most, x[31]);
         if (most > m) {
-          m = most;
-          const float next = fmaxf(m * scale, -FLT_MAX), f = ex2(top - next);
+          const float f = ex2((m - most) * scale);
           s2.x *= f;
           s2.y *= f;
-          top = next;
+          m = most;
         }
-        const float2 cc = both(scale), nt = both(-top);
+        const float2 cc = both(scale), nm = both(-m);
         float2 part = both(0.f);
 #pragma unroll
         for (int i = 0; i < 32; i += 2) {
-          const float2 y = fma2(make_float2(x[i], x[i + 1]), cc, nt);
+          const float2 y = mul2(add2(make_float2(x[i], x[i + 1]), nm), cc);
           part = add2(part, make_float2(ex2(y.x), ex2(y.y)));
         }
         s2 = add2(s2, part);
@@ -328,7 +329,7 @@ window_kernel(const WindowParams wp, const __grid_constant__ CUtensorMap query_m
       fence_before();
       arrive(smem_u32(&taken[it % kBuffers]));
     }
-    sums[group][t] = {top, summed ? s2.x + s2.y : NAN};
+    sums[group][t] = {m, summed ? s2.x + s2.y : NAN};
     auto both_groups = [&]() { asm volatile("bar.sync 15, %0;" ::"n"(kGroups * kLanes) : "memory"); };
     if (C > 1) {
       cluster_arrive();
@@ -348,15 +349,15 @@ window_kernel(const WindowParams wp, const __grid_constant__ CUtensorMap query_m
         }
 #pragma unroll
         for (int i = 0; i < kGroups; ++i) {
-          const float most = fmaxf(all.top, o[i]);
-          all.s = all.s * ex2(all.top - most) + s[i] * ex2(o[i] - most);
-          all.top = most;
+          const float most = fmaxf(all.m, o[i]);
+          all.s = all.s * ex2((all.m - most) * scale) + s[i] * ex2((o[i] - most) * scale);
+          all.m = most;
         }
       }
       // rows that see nothing, or scores of -inf alone, add 0; so do those past the last
       float* to = reinterpret_cast<float*>(&row_pairs[t >> 1]) + (t & 1);
       const bool none = all.s == 0.f || t >= R;
-      to[0] = none ? 0.f : -all.top;
+      to[0] = none ? 0.f : -all.m;
       to[2] = none ? 0.f : 1.f / all.s;
     }
     if (C > 1) cluster_arrive();  // (the other CTAs may end)
@@ -389,14 +390,14 @@ window_kernel(const WindowParams wp, const __grid_constant__ CUtensorMap query_m
 #pragma unroll
           for (int i = 0; i < 32; i += 2) {
             const float4 row = row_pairs[(c + i) >> 1];
-            const float2 y = fma2(make_float2(x[i], x[i + 1]), cc, make_float2(row.x, row.y));
+            const float2 y = mul2(add2(make_float2(x[i], x[i + 1]), make_float2(row.x, row.y)), cc);
             w = fma2(make_float2(ex2(y.x), ex2(y.y)), make_float2(row.z, row.w), w);
           }
         } else {  // (columns past the last row hold anything)
 #pragma unroll
           for (int i = 0; i < 32; i += 2) {
             const float4 row = row_pairs[(c + i) >> 1];
-            const float2 y = fma2(make_float2(x[i], x[i + 1]), cc, make_float2(row.x, row.y));
+            const float2 y = mul2(add2(make_float2(x[i], x[i + 1]), make_float2(row.x, row.y)), cc);
             if (c + i >= least && c + i < R) w.x = fmaf(ex2(y.x), row.z, w.x);
             if (c + i + 1 >= least && c + i + 1 < R) w.y = fmaf(ex2(y.y), row.w, w.y);
           }
