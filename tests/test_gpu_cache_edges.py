@@ -277,3 +277,29 @@ def test_weights_of_rows_that_see_the_lowest_value_alone(dev, G, T):  # noqa: F8
         A = (np.abs(k64[0, h, few:]) @ np.abs(mine).reshape(T * G, D).T).max(initial=0) * D**-0.5
         tol = 2 * (2 * (D * 2.0**-22 + 2.0**-23) * A + 2.0**-21 + S * 2.0**-24) * want + 2.0**-22 * want
         assert (np.abs(got[0, h] - want) <= tol).all(), h
+
+
+@pytest.mark.parametrize("scale", [0.0, -0.0, 1e-37, 1.3e-38])
+@pytest.mark.parametrize("G,T", [(1, 1), (4, 40), (1, 60)])
+def test_weights_of_a_scale_of_nothing(dev, G, T, scale):  # noqa: F811
+    """Scores of 0, or of 34 and 4 at most, whatever the keys hold. (A row's sum of S terms
+    and its quotient, the sum of R rows: 2^-23 a term; the rounding of a score of 34, of its
+    difference and of that times log2 e: 2^-18 each; the exponential 2^-21.)"""
+    import torch
+
+    import top_selection_row_gb300 as q
+
+    rng = np.random.default_rng(T)
+    H, S, D = 2, 200, 64
+    k = np.zeros((1, H, S, D), np.float32)
+    k[..., 0] = rng.standard_normal((1, H, S))
+    k[:, :, ::3, 0] = -3.3895313892515355e38
+    qq = rng.standard_normal((1, T, H * G, D)).astype(np.float32)
+    qq[..., 0] = 1
+    n = torch.tensor([S], dtype=torch.int32, device=dev)
+    got = q.qrita_cache_weights(tensor(dev, qq, "bf16"), tensor(dev, k, "bf16"), torch.zeros(1, H, S, device=dev), n, scale=scale).cpu().numpy()
+    k64, q64 = rounded(k, "bf16"), rounded(qq, "bf16")
+    size = np.float64(np.float32(scale))
+    for h in range(H):
+        want = cache_weights(q64[0, :, h * G : (h + 1) * G], k64[0, h], np.arange(S), S, S, size)
+        assert (np.abs(got[0, h] - want) <= ((G * T + S) * 2.0**-23 + 3 * 2.0**-18 + 2.0**-21) * want).all(), h

@@ -28,6 +28,7 @@
 // on the multiply-add pipe: 103, a quarter: 106.)
 
 #include <cfloat>
+#include <cmath>
 #include <cstring>
 #include <cstddef>
 #include <cstdint>
@@ -190,8 +191,7 @@ window_kernel(const WindowParams wp, const __grid_constant__ CUtensorMap query_m
   const int64_t lo = min(static_cast<int64_t>(n), rank * share), hi = min(static_cast<int64_t>(n), lo + share);
   const int tiles = static_cast<int>((hi - lo + kLanes - 1) / kLanes);
   const int R = wp.rows, columns = (R + 15) / 16 * 16;
-  // (above 0, so that what is not seen stays -inf)
-  const float scale = fminf(fmaxf(fabsf(p.scale) * kLog2e, 1e-37f), FLT_MAX);
+  const float scale = fminf(fabsf(p.scale) * kLog2e, FLT_MAX);  // (above 0: what is not seen stays -inf)
   // every CTA of the cluster runs before its memory is read (in a launch without
   // clusters, threads that arrive at the cluster's barrier ahead of others are held)
   if (C > 1) cluster_sync_all();
@@ -496,6 +496,8 @@ cudaError_t launch_window_of(const WeightParams& p, const CUtensorMap& query, co
 
 bool launch_cache_window(const WeightParams& p, qrita_stream_t stream, int* result) {
   if (p.G > kLanes || p.D > 256 || p.c.B > INT32_MAX || p.c.S > INT32_MAX - 2 * kLanes) return false;
+  // (scores of 0 whatever their products: no multiple of the products' differences)
+  if (std::fabs(p.scale) < 1e-37f) return false;
   CUtensorMap query, key;
   if (!make_map(&query, p.query, {p.D, p.c.H * p.G, p.T, p.c.B}, {p.q_head, p.q_token, p.q_batch}, p.G, kLanes / p.G) ||
       !make_map(&key, p.keys, {p.D, p.c.S, p.c.H, p.c.B}, {p.k_slot, p.k_head, p.k_batch}, kLanes, 1))
