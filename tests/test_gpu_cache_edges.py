@@ -303,3 +303,121 @@ def test_weights_of_a_scale_of_nothing(dev, G, T, scale):  # noqa: F811
     for h in range(H):
         want = cache_weights(q64[0, :, h * G : (h + 1) * G], k64[0, h], np.arange(S), S, S, size)
         assert (np.abs(got[0, h] - want) <= ((G * T + S) * 2.0**-23 + 3 * 2.0**-18 + 2.0**-21) * want).all(), h
+
+
+def test_batches_of_nothing(dev):  # noqa: F811
+    import torch
+
+    import top_selection_row_gb300 as q
+
+    k, v, w, n, at = (t[:0] for t in small_cache(dev))
+    new, seen, query = torch.zeros(0, 2, 32, dtype=torch.bfloat16, device=dev), n.clone(), torch.zeros(0, 3, 8, 32, dtype=torch.bfloat16, device=dev)
+    assert q.qrita_cache_weights(query, k, w, n).shape == (0, 2, 60)
+    assert [tuple(t.shape) for t in q.qrita_cache_evict(k, v, w, n, 7)] == [(0, 2, 7, 32)] * 2 + [(0, 2, 7)] * 3 + [(0,)]
+    assert q.qrita_cache_insert(k, v, w, at, n, seen, new, new, 60).shape == (0, 2)
+
+
+@pytest.mark.parametrize("off", [1, 2, 3])
+def test_vectors_and_rows_off_their_boundaries(dev, off):  # noqa: F811
+    """Everything `off` elements behind a boundary: the same as on it (weights: with fp32
+    products by the same kernel, so equal too)."""
+    import torch
+
+    import top_selection_row_gb300 as q
+
+    def shifted(t):
+        buf = torch.zeros(t.numel() + off, dtype=t.dtype, device=dev)
+        buf[off:] = t.flatten()
+        return buf[off:].view(t.shape)
+
+    for S in (60, 5001):
+        k, v, w, n, at = small_cache(dev, S=S)
+        seen = n + 3
+        args = [k, v, w, n]
+        want = q.qrita_cache_evict(*args, 31, sink=1, recent=4, positions=at, seen=seen)
+        out = q.EvictedCache(*(shifted(torch.full_like(t, 7)) for t in want))
+        got = q.qrita_cache_evict(*(shifted(t) for t in args), 31, sink=1, recent=4, positions=shifted(at), seen=shifted(seen), out=out)
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+        new = torch.randn(2, 3, 2, 32, device=dev).bfloat16()
+        a = [t.clone() for t in (k, v, w, at, n, seen)]
+        b = [shifted(t) for t in a]
+        one = q.qrita_cache_insert(*a, *new, S, recent=4)
+        assert torch.equal(q.qrita_cache_insert(*b, *(shifted(t) for t in new), S, recent=4), one)
+        assert all(torch.equal(x, y) for x, y in zip(a, b))
+        query = torch.randn(3, 2, 4, 32, device=dev)
+        x = q.qrita_cache_weights(query, k.float(), w.clone(), n, positions=at, seen=seen)
+        y = q.qrita_cache_weights(shifted(query), shifted(k.float()), shifted(w), shifted(n), positions=shifted(at), seen=shifted(seen))
+        assert torch.allclose(x, y, rtol=2**-18, atol=0)  # (another order of a sum of 32 products)
+
+
+def test_two_streams_at_once(dev):  # noqa: F811
+    """Windows (each takes whole SMs), evictions and insertions of two streams, side by
+    side and replayed: nothing is shared between calls."""
+    import torch
+
+    import top_selection_row_gb300 as q
+
+    g = torch.Generator(device=dev).manual_seed(9)
+    rand = lambda *s: torch.randn(*s, generator=g, device=dev).bfloat16()  # noqa: E731
+    sets = []
+    for S in (3000, 4100):
+        k, v, query, new = rand(3, 4, S, 64), rand(3, 4, S, 64), rand(3, 24, 16, 64), rand(3, 4, 64)
+        n = torch.tensor([S, S // 3, S - 1], dtype=torch.int32, device=dev)
+        w0 = torch.rand(3, 4, S, generator=g, device=dev)
+
+        def run(k=k, v=v, query=query, new=new, n=n, w0=w0):
+            w, seen = w0.clone(), n.clone()
+            q.qrita_cache_weights(query, k, w, n)
+            c = q.qrita_cache_evict(k, v, w, n, 500, sink=2, recent=50)
+            slots = q.qrita_cache_insert(c.keys, c.values, c.weights, c.positions, c.lengths, seen, new, new, 500, recent=50)
+            return [w, *c, seen, slots]
+
+        sets.append((run, [t.clone() for t in run()]))
+    streams = [torch.cuda.Stream() for _ in sets]
+    torch.cuda.synchronize()
+    for _ in range(10):
+        got = []
+        for s, (run, _) in zip(streams, sets):
+            with torch.cuda.stream(s):
+                got.append(run())
+        torch.cuda.synchronize()
+        for held, (_, want) in zip(got, sets):
+            assert all(torch.equal(a, b) for a, b in zip(held, want))
+    graphs = []
+    for run, _ in sets:
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            held = run()
+        graphs.append((graph, held))
+    for _ in range(5):
+        for s, (graph, _) in zip(streams, graphs):
+            with torch.cuda.stream(s):
+                graph.replay()
+        torch.cuda.synchronize()
+        for (_, held), (_, want) in zip(graphs, sets):
+            assert all(torch.equal(a, b) for a, b in zip(held, want))
+
+
+def test_many_short_sequences(dev):  # noqa: F811
+    """More heads than a wave of CTAs by far: each as by itself."""
+    import torch
+
+    import top_selection_row_gb300 as q
+
+    g = torch.Generator(device=dev).manual_seed(1)
+    B, H, S, D = 5000, 3, 20, 32
+    k, w = torch.randn(B, H, S, D, generator=g, device=dev).bfloat16(), torch.rand(B, H, S, generator=g, device=dev)
+    n = torch.randint(-1, S + 1, (B,), generator=g, device=dev, dtype=torch.int32)
+    for T in (1, 9):
+        query = torch.randn(B, T, 2 * H, D, generator=g, device=dev).bfloat16()
+        got = q.qrita_cache_weights(query, k, w.clone(), n)
+        for b in (0, 1234, B - 1):
+            assert torch.allclose(got[b], q.qrita_cache_weights(query[b:b + 1], k[b:b + 1], w[b:b + 1].clone(), n[b:b + 1])[0], rtol=2**-20)
+    cut = q.qrita_cache_evict(k, k, w, n, 6, recent=2)
+    for b in (0, 1234, B - 1):
+        assert all(torch.equal(x[b], y[0]) for x, y in zip(cut, q.qrita_cache_evict(k[b:b + 1], k[b:b + 1], w[b:b + 1], n[b:b + 1], 6, recent=2)))
+    seen, lengths, new = n.clamp(min=0), cut.lengths.clone(), torch.randn(B, H, D, generator=g, device=dev).bfloat16()
+    one = [t[7:8].clone() for t in (cut.keys, cut.values, cut.weights, cut.positions, lengths, seen)]
+    q.qrita_cache_insert(cut.keys, cut.values, cut.weights, cut.positions, lengths, seen, new, new, 6, recent=2)
+    q.qrita_cache_insert(*one, new[7:8], new[7:8], 6, recent=2)
+    assert all(torch.equal(x[7:8], y) for x, y in zip((cut.keys, cut.values, cut.weights, cut.positions, lengths, seen), one))

@@ -5,7 +5,7 @@ import numpy as np
 import pytest
 
 from oracle import scores_grad_row, scores_row
-from test_gpu_losses import BF16_ROUND, F32_ROUND, dev, make_rows, near, put, widened  # noqa: F401
+from test_gpu_losses import ABS, BF16_ROUND, F32_ROUND, dev, make_rows, near, put, widened  # noqa: F401
 from parity_helpers import to_device
 from test_gpu_scores import check_grad, given
 from workloads import f32_to_bf16_bits
@@ -102,3 +102,26 @@ def test_ranks_of_tokens_of_the_lowest_value(dev, B, V, keep, dtype):  # noqa: F
     assert np.array_equal(got.top_ids.cpu().numpy(), np.array([w[3] for w in want])[some])
     below = np.array([w[0] for w in want])[some] < -3.5e38
     assert below[:, 0].any() and np.isneginf(got.logp.cpu().numpy()[below]).all()
+
+
+def test_scores_of_nothing_and_of_as_many_as_there_can_be(dev):  # noqa: F811
+    """No rows; 8192 given tokens with 128 alternatives; more alternatives than logits in
+    more rows than a wave."""
+    import torch
+
+    import top_selection_row_gb300 as q
+
+    x = torch.randn(0, 50, device=dev)
+    none = torch.zeros(0, 3, dtype=torch.int32, device=dev)
+    assert q.qrita_token_scores(x, none, top=4, entropy=True, rank=True).top_logp.shape == (0, 4)
+    assert q.qrita_token_scores_grad(x, none, torch.zeros(0, 3, device=dev)).shape == (0, 50)
+    rng = np.random.default_rng(2)
+    for B, V, M, top in ((2, 30000, 8192, 128), (2, 200_000, 8192, 128), (20000, 100, 3, 128)):
+        xs = rng.standard_normal((min(B, 7), V)).astype(np.float32)
+        t = rng.integers(-1, V + 1, (len(xs), M)).astype(np.int32)
+        some = np.arange(B) % len(xs)
+        got = q.qrita_token_scores(put(dev, xs[some]), put(dev, t[some]), top=top, entropy=True, rank=True)
+        want = [scores_row(xs[r].astype(np.float64), None, t[r], 1.0, top) for r in range(len(xs))]
+        assert np.array_equal(got.top_ids.cpu().numpy(), np.array([w[3] for w in want])[some])
+        assert np.array_equal(got.rank.cpu().numpy(), np.array([w[1] for w in want])[some])
+        near(got.logp.cpu().numpy(), np.array([w[0] for w in want])[some], ABS + F32_ROUND * 30, "logp")
