@@ -524,8 +524,9 @@ int qrita_token_scores_grad(const void* logits, int dtype, int64_t B, int64_t V,
  *                contiguous. Rows of inputs may share memory (an expanded head);
  *                rows that are written share none, and what is written overlaps
  *                nothing else: lengths, seen, weights, positions and slots that
- *                overlap one another where one of them is written are QRITA_EINVAL,
- *                and so are keys and values written to the same place.
+ *                overlap one another where one of them is written are QRITA_EINVAL.
+ *                (A slot's value may be a part of its key, as in a cache of latent
+ *                vectors, where the same is written to both.)
  * Ownership, streams and errors as qrita_select; QRITA_EINVAL also for sizes,
  * strides or scalars outside their stated range. Nothing is allocated or kept.
  * B == 0 launches nothing.

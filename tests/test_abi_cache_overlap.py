@@ -4,7 +4,7 @@ is a valid one)."""
 
 import pytest
 
-from test_abi_cache import K, OK_, V, evict, insert, strides, weights
+from test_abi_cache import K, V, evict, insert, strides, weights
 from test_abi_losses import EINVAL, NULL, VP, L  # noqa: F401
 
 # vectors apart from each other: 2 x 4 x 100 weights and positions of 4 bytes, 2 lengths, 2 x 4 x 10 slots
@@ -21,10 +21,9 @@ CASES = [
     (evict, dict(ol=N)), (evict, dict(ol=SEEN)), (evict, dict(ol=behind(N, 4))), (evict, dict(ol=behind(W, 3196))),
     (evict, dict(ow=W)), (evict, dict(ow=behind(W, 3196))), (evict, dict(ow=AT)), (evict, dict(op=AT)), (evict, dict(op=W)),
     (evict, dict(os=AT)), (evict, dict(os=N)), (evict, dict(os=W)), (evict, dict(os=OAT)), (evict, dict(os=OW)), (evict, dict(ol=OS)),
-    (evict, dict(op=OW)), (evict, dict(ov=OK_)), (evict, dict(ov=behind(OK_, 64))), (evict, dict(ol=N, positions=NULL, seen=NULL)),
+    (evict, dict(op=OW)), (evict, dict(ol=N, positions=NULL, seen=NULL)),
     (insert, dict(seen=N)), (insert, dict(lengths=behind(SEEN, 4))), (insert, dict(weights=AT)), (insert, dict(os=N)),
-    (insert, dict(os=W)), (insert, dict(os=behind(AT, 3196))), (insert, dict(lengths=W)), (insert, dict(values=K)),
-    (insert, dict(keys=behind(V, 60))),
+    (insert, dict(os=W)), (insert, dict(os=behind(AT, 3196))), (insert, dict(lengths=W)),
     (weights, dict(weights=AT)), (weights, dict(weights=N)), (weights, dict(weights=behind(SEEN, 4))),
 ]
 

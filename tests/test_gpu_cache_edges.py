@@ -33,12 +33,11 @@ def test_vectors_that_are_read_and_written(dev):  # noqa: F811
     out = q.qrita_cache_evict(k, v, w, n, 20, positions=at, seen=seen)
     new = torch.zeros(3, 2, 32, dtype=torch.bfloat16, device=dev)
     held = [t.clone() for t in (k, v, w, n, at, seen)]
-    for bad in (dict(lengths=n), dict(lengths=seen), dict(slots=out.positions), dict(values=out.keys)):
+    for bad in (dict(lengths=n), dict(lengths=seen), dict(slots=out.positions)):
         with pytest.raises(q.QritaError):
             q.qrita_cache_evict(k, v, w, n, 20, positions=at, seen=seen, out=out._replace(**bad))
-    for args in ((k, v, w, at, n, n), (k, k, w, at, n, seen)):
-        with pytest.raises(q.QritaError):
-            q.qrita_cache_insert(*args, new, new, 60)
+    with pytest.raises(q.QritaError):
+        q.qrita_cache_insert(k, v, w, at, n, n, new, new, 60)
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for a, b in zip((k, v, w, n, at, seen), held))
 
@@ -61,6 +60,26 @@ def test_keys_and_values_side_by_side(dev):  # noqa: F811
     for c in (a, b):
         q.qrita_cache_insert(*c, *new, 20)
     assert all(torch.equal(x, y) for x, y in zip(a, b))
+
+
+@pytest.mark.parametrize("part", [16, 24, 5])
+def test_values_that_are_a_part_of_the_keys(dev, part):  # noqa: F811
+    """A cache of latent vectors, evicted into another one and put into: as with values
+    of their own."""
+    import torch
+
+    import top_selection_row_gb300 as q
+
+    k, _, w, n, at = small_cache(dev)
+    want = q.qrita_cache_evict(k, k[..., :part].clone(), w, n, 20, recent=3)
+    rows = torch.zeros_like(want.keys)
+    out = want._replace(keys=rows, values=rows[..., :part], **{f: torch.empty_like(getattr(want, f)) for f in want._fields[2:]})
+    got = q.qrita_cache_evict(k, k[..., :part], w, n, 20, recent=3, out=out)
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    new, seen = torch.randn(3, 2, 32, device=dev).bfloat16(), [n.clone(), n.clone()]
+    for c, s in zip((want, got), seen):
+        q.qrita_cache_insert(c.keys, c.values, c.weights, c.positions, c.lengths, s, new, new[..., :part], 20)
+    assert all(torch.equal(a, b) for a, b in zip(got, want)) and torch.equal(*seen)
 
 
 @pytest.mark.parametrize("B,H,G,T,S,D", [(2, 2, 4, 16, 3000, 128), (160, 2, 1, 40, 700, 64), (1, 3, 2, 100, 2500, 200)])

@@ -82,10 +82,6 @@ bool clash(std::initializer_list<Range> written, std::initializer_list<Range> re
   return false;
 }
 
-// Whether two caches that are written have the same first row. (They may lie in one
-// tensor, side by side.)
-bool same_rows(const CacheRows& a, const CacheRows& b) { return overlap(Range{a.at, a.bytes}, Range{b.at, b.bytes}); }
-
 bool budget_ok(int64_t S, int32_t budget, int32_t sink, int32_t recent, CacheOrder* out) {
   out->budget = budget;
   out->sink = sink;
@@ -178,8 +174,7 @@ int qrita_cache_evict_ex(int64_t B, int64_t H, int64_t S, const int32_t* lengths
     if (qrita::overlap(prm.key, *to, B, H, S, budget) || qrita::overlap(prm.value, *to, B, H, S, budget)) return QRITA_EINVAL;
   if (out_weights == nullptr || out_positions == nullptr || out_slots == nullptr || out_lengths == nullptr) return QRITA_EINVAL;
   const int64_t order = 4 * B * H * S, out_order = 4 * B * H * out_S;
-  if (qrita::same_rows(prm.out_key, prm.out_value) ||
-      qrita::clash({{out_weights, out_order}, {out_positions, out_order}, {out_slots, 4 * B * H * budget}, {out_lengths, 4 * B}},
+  if (qrita::clash({{out_weights, out_order}, {out_positions, out_order}, {out_slots, 4 * B * H * budget}, {out_lengths, 4 * B}},
                    {{weights, order}, {positions, order}, {lengths, 4 * B}, {seen, 4 * B}}))
     return QRITA_EINVAL;
   if (B * H > qrita::kMax / ((static_cast<int64_t>(budget) + 63) / 64)) return QRITA_EUNSUPPORTED;
@@ -208,8 +203,7 @@ int qrita_cache_insert(int64_t B, int64_t H, int64_t S, int32_t* lengths, int32_
       !qrita::rows_ok(new_values, value_bytes, new_value_strides, false, &prm.new_value))
     return QRITA_EINVAL;
   const int64_t order = 4 * B * H * S;
-  if (qrita::same_rows(prm.key, prm.value) ||
-      qrita::clash({{weights, order}, {positions, order}, {lengths, 4 * B}, {seen, 4 * B}, {out_slots, 4 * B * H}}, {}))
+  if (qrita::clash({{weights, order}, {positions, order}, {lengths, 4 * B}, {seen, 4 * B}, {out_slots, 4 * B * H}}, {}))
     return QRITA_EINVAL;
   prm.out_slots = out_slots;
   return qrita::launch_cache_insert(prm, stream) == 0 ? QRITA_OK : QRITA_ECUDA;

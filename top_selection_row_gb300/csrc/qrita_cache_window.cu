@@ -330,12 +330,12 @@ window_kernel(const WindowParams wp, const __grid_constant__ CUtensorMap query_m
       arrive(smem_u32(&taken[it % kBuffers]));
     }
     sums[group][t] = {m, summed ? s2.x + s2.y : NAN};
-    auto both_groups = [&]() { asm volatile("bar.sync 15, %0;" ::"n"(kGroups * kLanes) : "memory"); };
+    auto all_groups = [&]() { asm volatile("bar.sync 15, %0;" ::"n"(kGroups * kLanes) : "memory"); };
     if (C > 1) {
       cluster_arrive();
       cluster_wait();
     } else {
-      both_groups();
+      all_groups();
     }
     if (group == 0) {
       WindowSum all = {-FLT_MAX, 0.f};
@@ -361,7 +361,7 @@ window_kernel(const WindowParams wp, const __grid_constant__ CUtensorMap query_m
       to[2] = none ? 0.f : 1.f / all.s;
     }
     if (C > 1) cluster_arrive();  // (the other CTAs may end)
-    both_groups();
+    all_groups();
     // The slots' weights.
     it = tiles + (group + kGroups - tiles % kGroups) % kGroups;
     at = position(lo + static_cast<int64_t>(2 * tiles - 1 - it) * kLanes + t);
