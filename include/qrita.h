@@ -512,10 +512,12 @@ int qrita_token_scores_grad(const void* logits, int dtype, int64_t B, int64_t V,
  * the rest of the order.)
  *
  * Common arguments (device pointers unless said otherwise):
- *   B, H, S      sequences, kv heads and slots; S up to 2^31-1, B H up to 2^27.
+ *   B, H, S      sequences, kv heads and slots; S up to 2^31-1, B H below 2^27
+ *                (more is QRITA_EUNSUPPORTED, and so are B H ceil(budget / 64) parts
+ *                of an eviction beyond 2^31-1).
  *   lengths      int32[B]: slots [0, lengths[b]) hold tokens, in every head (more
- *                than there are slots counts as that many). The slots behind them
- *                are not read. A sequence of negative length is idle.
+ *                than there are slots counts as that many). What the slots behind
+ *                them hold changes nothing. A sequence of negative length is idle.
  *   weights      float[B, H, S].
  *   positions    int32[B, H, S]: the position of each slot's token in its sequence,
  *                not negative; seen int32[B]: positions [0, seen[b]) have been put.
@@ -541,8 +543,8 @@ int qrita_token_scores_grad(const void* logits, int dtype, int64_t B, int64_t V,
  * tokens seen: query t is at position seen - T + t, and sees the slots of positions
  * up to its own (all slots, for one query of the newest token). A query that sees no
  * slot, or only scores of -inf, adds nothing; one whose visible scores hold NaN or
- * +inf adds NaN to all the slots that it sees. What keys hold elsewhere changes
- * nothing.
+ * +inf adds NaN to all the slots that it sees. (A score beyond fp32's range may count
+ * as infinite.) What keys hold elsewhere changes nothing.
  *
  *   query         dtype[B, T, H G, D], strides in elements of the batch, the token
  *                 and the head; T G up to 8192.

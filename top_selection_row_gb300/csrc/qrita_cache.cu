@@ -57,10 +57,11 @@ __device__ __forceinline__ int32_t length_of(const CacheOrder& c, int64_t b, int
 // wait in shared memory where they fit, so that keys are read once, and are worked
 // out again from keys that are in L2 where they do not.
 //
-// HBM bounds it: one query of 4 heads on 16 x 8 x 32768 slots of 128 bf16 193 us (5.6
-// TB/s), on 64 x 8 x 4096 93 us (5.8); 4 x 8 x 1024 6.6 us, of latency. A warp has the
+// HBM bounds it: one query of 4 heads on 16 x 8 x 32768 slots of 128 bf16 196 us (5.5
+// TB/s), on 64 x 8 x 4096 94 us (5.7); 4 x 8 x 1024 6.4 us, of latency. A warp has the
 // next tile on its way while it works on one, in four chains of products (a single
-// chain of 16 dependent ones: 230 us).
+// chain of 16 dependent ones: 230 us). fp32 keys go by plain loads, a slot a lane: 16 x
+// 8 x 8192 slots of 128 211 us (2.5 TB/s).
 // ---------------------------------------------------------------------------
 constexpr int kWThreads = 256;  // two CTAs on an SM: one's merge beside the other's keys
 constexpr int kWWarps = kWThreads / 32;
@@ -874,8 +875,8 @@ __device__ __forceinline__ void put_row(const CacheRows& from, const CacheRows& 
 }
 
 // A cluster takes a sequence, its heads in turn; the sequence's length goes up
-// when every CTA has read it. Latency bounds it: 64 x 8 x 4096 slots 7.6 us, 1 x 8 x
-// 1000 3.3.
+// when every CTA has read it. Latency bounds it: 64 x 8 x 4096 slots 7.5 us, 1 x 8 x
+// 1000 3.1; one CTA walks a head, so 1 x 8 x 65536 takes 47.
 __global__ void __launch_bounds__(kInsThreads) insert_kernel(const InsertParams p) {
   __shared__ unsigned long long least[kInsThreads / 32];
   __shared__ int32_t chosen;

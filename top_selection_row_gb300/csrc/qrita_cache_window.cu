@@ -21,11 +21,16 @@
 // another holds.
 //
 // Keys bound it, read twice: 32 queries of 4 heads on 8 x 8 x 16384 slots of 128 bf16
-// 97 us for 537 MB of tiles (5.6 TB/s; 454 MB of them from HBM, on 128 SMs), 16 queries
-// 92; its exponentials are 69 us of their pipe. (mma.sync in blocks of 32 rows: 930 us.
+// 98 us for 537 MB of tiles (5.5 TB/s; 453 MB of them from HBM, on 128 SMs), 16 queries
+// 94; its exponentials are 69 us of their pipe. (mma.sync in blocks of 32 rows: 930 us.
 // Keys by 16-byte copies of 64 threads, two CTAs an SM, two stages: 120. Two groups,
-// columns loaded ahead of their use: 114. An eighth of the exponentials by polynomials
-// on the multiply-add pipe: 103, a quarter: 106.)
+// columns loaded ahead of their use: 114. With exponents as c x less c m, one
+// multiply-add, it took 96: wrong for large scores. From 97 then, an eighth of the
+// exponentials by polynomials on the multiply-add pipe: 103, a quarter: 106.)
+//
+// A row's sum is taken by its lane's thread in each group: 32 columns are summed first,
+// then added to the running sum, S / (128 C) additions of a thread for S slots on C CTAs
+// (512 for 65536 slots on one), each off by half a unit of the sum.
 
 #include <cfloat>
 #include <cmath>
