@@ -41,3 +41,17 @@ def test_bad_evictions(L, bad, flags):  # noqa: F811
                          ids=str)
 def test_bad_weights(L, bad, flags):  # noqa: F811
     assert weights_ex(L, flags, **bad) == EINVAL
+
+
+def test_flags_match_the_header():
+    import os
+    import re
+
+    import top_selection_row_gb300 as q
+
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    with open(os.path.join(root, "include", "qrita.h")) as f:
+        flags = re.findall(r"#define QRITA_(CACHE_FLAG_\w+) (0x\w+)u", f.read())
+    assert len(flags) == 3
+    for name, value in flags:
+        assert getattr(q, name) == int(value, 16), name
